@@ -7,7 +7,8 @@ fallback: if the library is not built, every call raises.
 
 Entry points (same names as the C ABI):
     csa2_cache_write, csa2_quantize_fp4, csa2_indexer_topk, csa2_reindex, csa2_reindex_f32,
-    csa2_sparse_attn, csa2_workspace_size, csa2_poll_error, csa2_selftest_wait_timeout
+    csa2_sparse_attn, csa2_dense_attn, csa2_linear_fp4, csa2_norm_rope, csa2_workspace_size,
+    csa2_poll_error, csa2_selftest_wait_timeout
 plus ``Cache``, which owns the four cache planes as torch tensors.
 """
 import ctypes
@@ -20,7 +21,9 @@ LIB_PATH = os.path.join(_HERE, "libcsa2.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TIMEOUT = 0, 1, 2, 3, 4, 5
 FULL, REINDEX, REUSE = 0, 1, 2
-OP_INDEXER_TOPK, OP_REINDEX, OP_SPARSE_ATTN = 1, 2, 3
+OP_INDEXER_TOPK, OP_REINDEX, OP_SPARSE_ATTN, OP_DENSE_ATTN = 1, 2, 3, 4
+ROPE_HALVES, ROPE_INVERSE, ROPE_NO_NORM = 1, 2, 4
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 D_LAT = 512
 
 
@@ -37,11 +40,17 @@ class _CacheStruct(ctypes.Structure):
                 ("d_lat", ctypes.c_int32), ("d_idx", ctypes.c_int32), ("ratio", ctypes.c_int32)]
 
 
+class _HeadRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("x_tok", ctypes.c_int64), ("x_head", ctypes.c_int64), ("y_tok", ctypes.c_int64),
+                ("y_head", ctypes.c_int64), ("n_heads", ctypes.c_int32)]
+
+
 _lib = None
 EXPORTS = ("csa2_cache_write", "csa2_quantize_fp4", "csa2_indexer_topk", "csa2_reindex", "csa2_sparse_attn",
            "csa2_workspace_size", "csa2_status_string", "csa2_abi_version", "csa2_launch_count",
            "csa2_reindex_noalloc", "csa2_reindex_f32", "csa2_poll_error", "csa2_selftest_wait_timeout",
-           "csa2_cache_write_projected")
+           "csa2_cache_write_projected", "csa2_linear_fp4", "csa2_norm_rope", "csa2_dense_attn")
 
 
 def load(path=None):
@@ -63,6 +72,10 @@ def load(path=None):
     lib.csa2_reindex.argtypes = [i32, cp, vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp]
     lib.csa2_reindex_f32.argtypes = [cp, vp, vp, i32, i32, vp, i32, i32, vp, vp, sz, vp]
     lib.csa2_sparse_attn.argtypes = [cp, vp, i32, i32, vp, vp, i32, vp, i64, i32, ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.csa2_linear_fp4.argtypes = [vp, i32, i64, i64, i32, i32, i32, i32, vp, vp, ctypes.c_float, vp, i32, i64, i64, vp]
+    hp = ctypes.POINTER(_HeadRows)
+    lib.csa2_norm_rope.argtypes = [hp, hp, i32, i32, i32, i32, i32, vp, vp, ctypes.c_float, i32, vp]
+    lib.csa2_dense_attn.argtypes = [cp, vp, i32, i32, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, sz, vp]
     lib.csa2_reindex_noalloc.argtypes = [cp, vp, vp, vp, i32, i32, vp, i32, i32, vp, vp]
     lib.csa2_reindex_noalloc.restype = ctypes.c_int
     lib.csa2_poll_error.argtypes = [vp, sz, vp]
@@ -76,7 +89,7 @@ def load(path=None):
     lib.csa2_abi_version.restype = i32
     lib.csa2_launch_count.restype = i64
     for name in ("csa2_cache_write", "csa2_quantize_fp4", "csa2_indexer_topk", "csa2_reindex", "csa2_reindex_f32",
-                 "csa2_sparse_attn"):
+                 "csa2_sparse_attn", "csa2_linear_fp4", "csa2_norm_rope", "csa2_dense_attn"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -115,13 +128,26 @@ class Cache:
         self.ikey_codes = torch.zeros((batch, capacity, d_idx // 2), dtype=torch.uint8, device=device)
         self.ikey_scales = torch.zeros((batch, capacity, d_idx // 16), dtype=torch.uint8, device=device)
 
+    @classmethod
+    def of(cls, lat_codes, lat_scales, ikey_codes=None, ikey_scales=None, ratio=2):
+        """a cache over planes that exist already (uint8, contiguous): lat_codes [B, n, 256],
+        lat_scales [B, n, 32] and, for the indexer, ikey_codes [B, n, d_idx/2] and ikey_scales"""
+        c = object.__new__(cls)
+        c.batch, c.capacity = lat_codes.shape[0], lat_codes.shape[1]
+        c.d_idx = 128 if ikey_codes is None else 2 * ikey_codes.shape[-1]
+        c.ratio = ratio
+        c.lat_codes, c.lat_scales, c.ikey_codes, c.ikey_scales = lat_codes, lat_scales, ikey_codes, ikey_scales
+        return c
+
     def struct(self):
-        return _CacheStruct(self.lat_codes.data_ptr(), self.lat_scales.data_ptr(), self.ikey_codes.data_ptr(),
-                            self.ikey_scales.data_ptr(), self.batch, self.capacity, D_LAT, self.d_idx,
+        ik, iks = self.ikey_codes, self.ikey_scales
+        return _CacheStruct(self.lat_codes.data_ptr(), self.lat_scales.data_ptr(), ik.data_ptr() if ik is not None else 0,
+                            iks.data_ptr() if iks is not None else 0, self.batch, self.capacity, D_LAT, self.d_idx,
                             getattr(self, "ratio", 2))
 
     def nbytes(self):
-        return sum(t.numel() for t in (self.lat_codes, self.lat_scales, self.ikey_codes, self.ikey_scales))
+        return sum(t.numel() for t in (self.lat_codes, self.lat_scales, self.ikey_codes, self.ikey_scales)
+                   if t is not None)
 
 
 def csa2_launch_count():
@@ -272,4 +298,111 @@ def csa2_sparse_attn(cache, q, q_pos, idx, swa, swa_pos0, scale=D_LAT ** -0.5, o
                                  int(swa_pos0), int(swa.shape[1]) if swa is not None else 0, float(scale), _ptr(out),
                                  _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "csa2_sparse_attn")
+    return out, lse
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, stream=None):
+    """y = alpha * W x with FP4 weights (csa2_quantize_fp4's format), for every token.
+    x bf16 / fp16 / fp32 [T, n_in] with codes uint8 [n_out, n_in/2] and scales uint8 [n_out, n_in/16], or
+    x [T, G, n_in] with codes [G, n_out, n_in/2] and scales [G, n_out, n_in/16] (a product per group).
+    Rows of x and out are contiguous, their other strides free.  Returns [T, n_out] or [T, G, n_out]
+    of out_dtype (default: that of x)."""
+    n_in, n_out = x.shape[-1], codes.shape[-2]
+    grouped = x.dim() == 3
+    _need(x.dim() in (2, 3) and codes.dim() == x.dim() and scales.dim() == x.dim(), "x, codes and scales: 2 or 3 dims each")
+    G = x.shape[1] if grouped else 1
+    _need(n_in % 16 == 0 and codes.shape[-1] * 2 == n_in and scales.shape[-1] * 16 == n_in
+          and scales.shape[-2] == n_out and (not grouped or (codes.shape[0] == G and scales.shape[0] == G)),
+          "codes [.., n_out, n_in/2] and scales [.., n_out, n_in/16] of x [.., n_in], n_in a multiple of 16")
+    _need(codes.dtype == scales.dtype == torch.uint8 and codes.is_contiguous() and scales.is_contiguous(),
+          "codes and scales: contiguous uint8")
+    if out is None:
+        out = torch.empty(x.shape[:-1] + (n_out,), dtype=out_dtype or x.dtype, device=x.device)
+    _need(out.shape[:-1] == x.shape[:-1] and out.shape[-1] == n_out and (out_dtype is None or out.dtype == out_dtype),
+          "out [.., n_out] with the leading sizes of x")
+    _need(x.dtype in _TYPES and out.dtype in _TYPES, "x and out: bf16, fp16 or fp32")
+    _need((x.stride(-1) == 1 or n_in == 0) and (out.stride(-1) == 1 or n_out <= 1), "rows of x and out: contiguous")
+    st = load().csa2_linear_fp4(x.data_ptr(), _TYPES[x.dtype], x.stride(0), x.stride(1) if grouped else 0, x.shape[0], G,
+                                n_in, n_out, codes.data_ptr(), scales.data_ptr(), alpha, out.data_ptr(),
+                                _TYPES[out.dtype], out.stride(0), out.stride(1) if grouped else 0, _stream(stream))
+    _check(st, "csa2_linear_fp4")
+    return out
+
+
+def _head_rows(x, weight, out, T, d, name):
+    _need(x.dim() == 3 and x.shape[0] == T and x.shape[2] == d and out.shape == x.shape,
+          "%s and its output: [T, heads, d]" % name)
+    _need(x.stride(2) == 1 and out.stride(2) == 1, "rows of %s and its output: contiguous" % name)
+    _need(weight is None or (weight.dtype == torch.float32 and weight.shape == (d,) and weight.is_contiguous()),
+          "%s_weight: contiguous fp32 [d]" % name)
+    return _HeadRows(x.data_ptr(), out.data_ptr(), 0 if weight is None else weight.data_ptr(), x.stride(0), x.stride(1),
+                     out.stride(0), out.stride(1), x.shape[1])
+
+
+def csa2_norm_rope(q, pos, inv_freq, q_weight=None, k=None, k_weight=None, eps=1e-6, norm=True, halves=False,
+                   inverse=False, q_out=None, k_out=None, out_dtype=None, stream=None):
+    """RMS norm of every head row of q [T, Hq, d] (and k [T, Hk, d]) with the rotation of its last
+    2 * len(inv_freq) values by pos int64 [T] * inv_freq fp32; norm=False rotates only, inverse=True
+    turns back, halves=True pairs value i with i + d_rot/2 (default: 2i with 2i+1).  pos and inv_freq
+    may both be None (no rotation).  bf16 / fp16 / fp32, rows contiguous, other strides free; q_out may
+    be q.  Returns (q_out, k_out or None)."""
+    T, d = q.shape[0], q.shape[2]
+    d_rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _need(inv_freq is None or (inv_freq.dtype == torch.float32 and inv_freq.is_contiguous() and pos is not None
+                               and pos.dtype == torch.int64 and pos.shape == (T,) and pos.is_contiguous()),
+          "inv_freq: contiguous fp32; pos: contiguous int64 [T]")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    rows_q = _head_rows(q, q_weight, q_out, T, d, "q")
+    rows_k = None
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=q_out.dtype, device=k.device)
+        _need(k.dtype == q.dtype and k_out.dtype == q_out.dtype, "k has the type of q, k_out that of q_out")
+        rows_k = ctypes.byref(_head_rows(k, k_weight, k_out, T, d, "k"))
+    _need(q.dtype in _TYPES and q_out.dtype in _TYPES and (out_dtype is None or q_out.dtype == out_dtype),
+          "q and q_out: bf16, fp16 or fp32")
+    flags = (ROPE_HALVES if halves else 0) | (ROPE_INVERSE if inverse else 0) | (0 if norm else ROPE_NO_NORM)
+    st = load().csa2_norm_rope(ctypes.byref(rows_q), rows_k, _TYPES[q.dtype], _TYPES[q_out.dtype], T, d, d_rot,
+                               pos.data_ptr() if d_rot else None, inv_freq.data_ptr() if d_rot else None, eps, flags,
+                               _stream(stream))
+    _check(st, "csa2_norm_rope")
+    return q_out, k_out if k is not None else None
+
+
+def csa2_dense_attn(cache, q, q_pos, swa, swa_pos0, scale=D_LAT ** -0.5, out=None, out_dtype=torch.bfloat16, lse=None,
+                    want_lse=False, ws=None, stream=None):
+    """Attention over every visible entry of the cache and the window: q bf16 [B, n_q, H, 512]; q_pos
+    int64 [B, n_q]; swa bf16 [B, swa_len, 512] or None, row r of sequence b at raw position
+    swa_pos0[b] + r (int64 [B] on the device, or None: zeros).  Returns (out [B, n_q, H, 512], lse
+    fp32 [B, n_q, H] or None)."""
+    B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
+    _need(q.dtype == torch.bfloat16 and q.is_contiguous() and q.shape[3] == D_LAT and B == cache.batch,
+          "q: contiguous bf16 [batch, n_q, heads, 512]")
+    _need(q_pos.dtype == torch.int64 and q_pos.shape == (B, n_q) and q_pos.is_contiguous(),
+          "q_pos: contiguous int64 [batch, n_q]")
+    _need(swa is None or (swa.dtype == torch.bfloat16 and swa.is_contiguous() and swa.shape[0] == B
+                          and swa.shape[2] == D_LAT), "swa: contiguous bf16 [batch, swa_len, 512]")
+    _need(swa_pos0 is None or (swa_pos0.dtype == torch.int64 and swa_pos0.shape == (B,) and swa_pos0.is_contiguous()),
+          "swa_pos0: contiguous int64 [batch]")
+    if out is None:
+        out = torch.empty((B, n_q, H, D_LAT), dtype=out_dtype, device=q.device)
+    _need(out.dtype in _TYPES and out.is_contiguous() and out.shape == q.shape, "out: contiguous, the shape of q")
+    if want_lse and lse is None:
+        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=q.device)
+    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == (B, n_q, H) and lse.is_contiguous()),
+          "lse: contiguous fp32 [batch, n_q, heads]")
+    if ws is None:
+        ws = workspace(OP_DENSE_ATTN, B, n_q, H, 0, cache.capacity, q.device)
+    c = cache.struct()
+    st = load().csa2_dense_attn(ctypes.byref(c), q.data_ptr(), n_q, H, q_pos.data_ptr(),
+                                None if swa is None else swa.data_ptr(), None if swa_pos0 is None else swa_pos0.data_ptr(),
+                                0 if swa is None else swa.shape[1], scale, out.data_ptr(), _TYPES[out.dtype],
+                                None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "csa2_dense_attn")
     return out, lse

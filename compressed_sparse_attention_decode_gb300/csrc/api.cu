@@ -26,6 +26,16 @@ cudaError_t launch_sparse_attn(const csa2_cache& c, const uint16_t* q, int n_q, 
 size_t sparse_attn_ws(int batch, int n_q, int H, int k);
 size_t indexer_full_ws(int batch, int n_q, int64_t capacity);
 size_t reindex_ws(int batch, int n_q, int64_t pool_len);
+cudaError_t launch_linear_fp4(const void* x, int x_type, int64_t x_tok, int64_t x_group, int n_tok, int n_groups,
+                              int n_in, int n_out, const uint8_t* codes, const uint8_t* scales, float alpha, void* y,
+                              int y_type, int64_t y_tok, int64_t y_group, cudaStream_t st);
+cudaError_t launch_norm_rope(const csa2_head_rows* q, const csa2_head_rows* k, int x_type, int y_type, int n_tok, int d,
+                             int d_rot, const int64_t* pos, const float* inv_freq, float eps, int flags,
+                             cudaStream_t st);
+cudaError_t launch_dense_attn(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
+                              const uint16_t* swa, const int64_t* swa_pos0, int swa_len, float scale, void* out,
+                              int out_type, float* lse, void* ws, cudaStream_t st);
+size_t dense_attn_ws(int batch, int n_q, int n_heads, int64_t capacity);
 cudaError_t launch_selftest_wait(uint32_t max_polls, int* err, cudaStream_t st);
 }  // namespace csa2
 
@@ -63,6 +73,9 @@ csa2_status check_cache(const csa2_cache* c, bool need_ikey) {
 namespace {
 csa2_status from_cuda(cudaError_t e) { return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA; }
 
+bool known_type(int32_t t) { return t == CSA2_BF16 || t == CSA2_F16 || t == CSA2_F32; }
+size_t type_size(int32_t t) { return t == CSA2_F32 ? 4 : 2; }
+
 }  // namespace
 
 extern "C" {
@@ -89,6 +102,7 @@ size_t csa2_workspace_size(int32_t op, int32_t batch, int32_t n_q, int32_t n_hea
         case CSA2_OP_INDEXER_TOPK: return indexer_full_ws(batch, n_q, capacity);
         case CSA2_OP_REINDEX: return reindex_ws(batch, n_q, capacity);
         case CSA2_OP_SPARSE_ATTN: return sparse_attn_ws(batch, n_q, n_heads, k);
+        case CSA2_OP_DENSE_ATTN: return n_heads < 1 ? 0 : dense_attn_ws(batch, n_q, n_heads, capacity);
     }
     return 0;
 }
@@ -231,6 +245,62 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
     if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return CSA2_ERR_WORKSPACE;
     return from_cuda(launch_sparse_attn(*cache, q, n_q, n_heads, q_pos, idx, k, swa, swa_pos0, swa_len, scale, out,
                                         lse, workspace, ws_bytes, (cudaStream_t)stream));
+}
+
+csa2_status csa2_linear_fp4(const void* x, int32_t x_type, int64_t x_tok, int64_t x_group, int32_t n_tok,
+                            int32_t n_groups, int32_t n_in, int32_t n_out, const uint8_t* codes, const uint8_t* scales,
+                            float alpha, void* y, int32_t y_type, int64_t y_tok, int64_t y_group, void* stream) {
+    if (!known_type(x_type) || !known_type(y_type)) return CSA2_ERR_INVALID_ARG;
+    if (n_tok < 0 || n_groups < 1 || n_groups > 65535 || n_in < 0 || n_in % 16 || n_out < 0) return CSA2_ERR_INVALID_ARG;
+    if (!std::isfinite(alpha)) return CSA2_ERR_INVALID_ARG;
+    if (n_tok == 0 || n_out == 0) return CSA2_OK;
+    if (!y || !aligned(y, type_size(y_type))) return CSA2_ERR_INVALID_ARG;
+    if (n_in > 0 && (!x || !codes || !scales || !aligned(x, type_size(x_type)) || !aligned(codes, 16)))
+        return CSA2_ERR_INVALID_ARG;
+    return from_cuda(launch_linear_fp4(x, x_type, x_tok, x_group, n_tok, n_groups, n_in, n_out, codes, scales, alpha, y,
+                                       y_type, y_tok, y_group, (cudaStream_t)stream));
+}
+
+csa2_status csa2_norm_rope(const csa2_head_rows* q, const csa2_head_rows* k, int32_t x_type, int32_t y_type,
+                           int32_t n_tok, int32_t d, int32_t d_rot, const int64_t* pos, const float* inv_freq, float eps,
+                           int32_t flags, void* stream) {
+    if (!q || !known_type(x_type) || !known_type(y_type) || n_tok < 0) return CSA2_ERR_INVALID_ARG;
+    if (d < 2 || d > 1024 || d % 2 || d_rot < 0 || d_rot > d || d_rot % 2) return CSA2_ERR_INVALID_ARG;
+    if (flags & ~(CSA2_ROPE_HALVES | CSA2_ROPE_INVERSE | CSA2_ROPE_NO_NORM)) return CSA2_ERR_INVALID_ARG;
+    const bool norm = !(flags & CSA2_ROPE_NO_NORM);
+    if (norm && !(std::isfinite(eps) && eps >= 0.0f)) return CSA2_ERR_INVALID_ARG;
+    int64_t heads = 0;
+    const csa2_head_rows* sets[2] = {q, k};
+    for (const csa2_head_rows* r : sets) {
+        if (!r) continue;
+        if (r->n_heads < 0 || (!norm && r->weight) || !aligned(r->weight, 4)) return CSA2_ERR_INVALID_ARG;
+        heads += r->n_heads;
+        if (r->n_heads == 0 || n_tok == 0) continue;
+        if (!r->x || !r->y || !aligned(r->x, type_size(x_type)) || !aligned(r->y, type_size(y_type)))
+            return CSA2_ERR_INVALID_ARG;
+    }
+    if (heads > (1 << 20)) return CSA2_ERR_INVALID_ARG;
+    if (n_tok == 0 || heads == 0) return CSA2_OK;
+    if (d_rot > 0 && (!pos || !inv_freq || !aligned(pos, 8) || !aligned(inv_freq, 4))) return CSA2_ERR_INVALID_ARG;
+    return from_cuda(launch_norm_rope(q, k, x_type, y_type, n_tok, d, d_rot, pos, inv_freq, eps, flags,
+                                      (cudaStream_t)stream));
+}
+
+csa2_status csa2_dense_attn(const csa2_cache* cache, const uint16_t* q, int32_t n_q, int32_t n_heads,
+                            const int64_t* q_pos, const uint16_t* swa, const int64_t* swa_pos0, int32_t swa_len,
+                            float scale, void* out, int32_t out_type, float* lse, void* workspace, size_t ws_bytes,
+                            void* stream) {
+    csa2_status s = check_cache(cache, false);
+    if (s != CSA2_OK) return s;
+    if (!q || !q_pos || !out || !aligned(q, 16) || !aligned(q_pos, 8) || !aligned(out, 16)) return CSA2_ERR_INVALID_ARG;
+    if (n_q < 1 || n_heads < 1 || n_heads > 128 || swa_len < 0 || !known_type(out_type)) return CSA2_ERR_INVALID_ARG;
+    if (swa_len > 0 && (!swa || !aligned(swa, 16))) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(swa_pos0, 8) || !aligned(lse, 4)) return CSA2_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return CSA2_ERR_INVALID_ARG;
+    const size_t need = dense_attn_ws(cache->batch, n_q, n_heads, cache->capacity);
+    if (!workspace || ws_bytes < need || !aligned(workspace, 16)) return CSA2_ERR_WORKSPACE;
+    return from_cuda(launch_dense_attn(*cache, q, n_q, n_heads, q_pos, swa, swa_pos0, swa_len, scale, out, out_type, lse,
+                                       workspace, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -35,10 +35,12 @@
  *     stream still runs, and waits for that kernel's completion before it
  *     reads what the stream produced; it lets its own successor start only
  *     after that wait, so it never overlaps any earlier work.  Before the wait
- *     the attention reads only caller inputs that no kernel of this library
- *     writes (the queries q and their positions q_pos, the window rows swa); a
- *     caller that writes those with a kernel of its own that itself lets its
- *     successor start early must make that kernel complete first.  Kernels not
+ *     the sparse attention reads its queries q, their positions q_pos and the
+ *     window rows swa.  csa2_norm_rope and csa2_linear_fp4, which write such
+ *     rows, never let their successor start early, and their rows are visible
+ *     before their blocks end; a caller that writes them with a kernel of its
+ *     own that itself lets its successor start early must make that kernel
+ *     complete first.  Kernels not
  *     launched this way (any caller kernel by default) are waited for as usual.
  */
 #ifndef CSA2_H
@@ -64,7 +66,10 @@ typedef enum {
 enum { CSA2_FULL = 0, CSA2_REINDEX = 1, CSA2_REUSE = 2 };
 
 /* operations that take a workspace */
-enum { CSA2_OP_INDEXER_TOPK = 1, CSA2_OP_REINDEX = 2, CSA2_OP_SPARSE_ATTN = 3 };
+enum { CSA2_OP_INDEXER_TOPK = 1, CSA2_OP_REINDEX = 2, CSA2_OP_SPARSE_ATTN = 3, CSA2_OP_DENSE_ATTN = 4 };
+
+/* element types of the operators that take more than one */
+enum { CSA2_BF16 = 0, CSA2_F16 = 1, CSA2_F32 = 2 };
 
 /*
  * The global KV cache shared by the layers of one block ("DeepSeek-v4.1 Flash"
@@ -228,6 +233,90 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
                              const int64_t* q_pos, const int32_t* idx, int32_t k, const uint16_t* swa,
                              int64_t swa_pos0, int32_t swa_len, float scale, float* out, float* lse,
                              void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Product with FP4 weights for the projections around the attention (the query
+ * and indexer-query projections, the grouped output projection):
+ *     y[t][g][m] = alpha * sum_k W[g][m][k] x[t][g][k]
+ * W in the cache's format (csa2_quantize_fp4 writes it), never expanded in
+ * memory; sums in fp32, y rounded once.  alpha carries a scale of the whole
+ * matrix: weights far below 1 keep their precision if they are quantised after
+ * a multiplication by 1/alpha (an E4M3 scale below 2^-6 is subnormal).
+ *   x       [n_tok][n_groups][n_in] of x_type, n_in contiguous, the other
+ *           strides in elements; y [n_tok][n_groups][n_out] of y_type likewise
+ *   codes   uint8 [n_groups][n_out][n_in/2], 16-byte aligned
+ *   scales  uint8 [n_groups][n_out][n_in/16]
+ * x_type, y_type: CSA2_BF16, CSA2_F16 or CSA2_F32.  n_in a multiple of 16;
+ * n_tok, n_in and n_out may be 0 (n_in 0 gives zeros), n_groups <= 65535; x and
+ * y aligned to their elements; y overlaps no input.  fp32 x is taken to 2^-22 of
+ * each element (two fp16 parts), fp16 and bf16 x exactly, relative to the
+ * largest of the token's values that a block reads together; a NaN scale byte, an
+ * infinite or a NaN x gives what the formula gives.  No workspace.
+ */
+csa2_status csa2_linear_fp4(const void* x, int32_t x_type, int64_t x_tok, int64_t x_group, int32_t n_tok,
+                            int32_t n_groups, int32_t n_in, int32_t n_out, const uint8_t* codes, const uint8_t* scales,
+                            float alpha, void* y, int32_t y_type, int64_t y_tok, int64_t y_group, void* stream);
+
+/* One set of head rows of csa2_norm_rope: row (t, h) of x starts at element
+ * t * x_tok + h * x_head, that of y likewise; the d values of a row are
+ * contiguous.  weight fp32 [d] or NULL (ones). */
+typedef struct {
+    const void* x;
+    void* y;
+    const float* weight;
+    int64_t x_tok, x_head, y_tok, y_head;
+    int32_t n_heads;
+} csa2_head_rows;
+
+enum { CSA2_ROPE_HALVES = 1, CSA2_ROPE_INVERSE = 2, CSA2_ROPE_NO_NORM = 4 };
+
+/*
+ * Norm of every head row and rotation by its position in one pass, for the
+ * queries and the latent rows that the attention takes pre-rotated, and for
+ * turning the attention's output back by the query's position.  Per row x:
+ *     v_j = x_j * rsqrt(mean_i x_i^2 + eps) * weight_j
+ *     the last d_rot values of v form pairs (a, b) that are turned by the angle
+ *     pos[t] * inv_freq[i]:  a' = a cos - b sin,  b' = a sin + b cos
+ *   q, k     the two row sets (the same types, sizes, positions); k may be NULL
+ *   pos      int64 [n_tok] raw positions;  inv_freq fp32 [d_rot/2] (|f| < 2^24);
+ *            angles are exact to 2^-24 turns at any position below 2^40
+ *   flags    CSA2_ROPE_HALVES: pair i is (v[i], v[i + d_rot/2]) of the rotated
+ *            part, else (v[2i], v[2i+1]); CSA2_ROPE_INVERSE: turn by the negative
+ *            angle; CSA2_ROPE_NO_NORM: v = x (eps and the weights are not taken:
+ *            a weight is an error)
+ * x_type, y_type as in csa2_linear_fp4; d even, 2 <= d <= 1024; d_rot even, 0 <=
+ * d_rot <= d (0: no rotation, pos and inv_freq may be NULL); n_tok and n_heads may
+ * be 0.  Arithmetic in fp32, y rounded once.  y may be x itself (same type and
+ * strides); no other overlap.  Rows whose squares overflow fp32 give zeros.
+ * No workspace.
+ */
+csa2_status csa2_norm_rope(const csa2_head_rows* q, const csa2_head_rows* k, int32_t x_type, int32_t y_type,
+                           int32_t n_tok, int32_t d, int32_t d_rot, const int64_t* pos, const float* inv_freq, float eps,
+                           int32_t flags, void* stream);
+
+/*
+ * Attention over every visible entry of the cache and the sliding window, with
+ * no index list ("DeepSeek-v4.1 Flash" §1.1, §2.3.1): csa2_sparse_attn with J =
+ * {0 .. n_elig(p)-1} U window, n_elig(p) clamped to the capacity.  For short
+ * contexts, layers without an indexer, and as the measure of a selection.
+ *   q        bf16 [batch][n_q][n_heads][d_lat], finite
+ *   q_pos    int64 [batch][n_q] raw positions (device)
+ *   swa      bf16 [batch][swa_len][d_lat], row r of sequence b = raw position
+ *            swa_pos0[b] + r; the window of a query is clipped to the rows present
+ *   swa_pos0 int64 [batch] (device) or NULL (zeros)
+ *   out      [batch][n_q][n_heads][d_lat] of out_type (CSA2_BF16, _F16 or _F32;
+ *            the weights pass the tensor cores in fp16, so an fp32 out is good
+ *            to 2e-3 as csa2_sparse_attn's is)
+ *   lse      fp32 [batch][n_q][n_heads] or NULL
+ * A query that sees nothing gets zeros and lse -inf.  Entries and rows that no
+ * query sees are not read.  1 <= n_heads <= 128.  q, swa and out 16-byte
+ * aligned, q_pos and swa_pos0 8, lse 4.
+ * workspace: csa2_workspace_size(CSA2_OP_DENSE_ATTN, ...) bytes (k not used).
+ */
+csa2_status csa2_dense_attn(const csa2_cache* cache, const uint16_t* q, int32_t n_q, int32_t n_heads,
+                            const int64_t* q_pos, const uint16_t* swa, const int64_t* swa_pos0, int32_t swa_len,
+                            float scale, void* out, int32_t out_type, float* lse, void* workspace, size_t ws_bytes,
+                            void* stream);
 
 /*
  * Reindex without a workspace, for callers that cannot allocate device memory:
