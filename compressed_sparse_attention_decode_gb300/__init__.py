@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libcsa2.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TIMEOUT = 0, 1, 2, 3, 4, 5
 FULL, REINDEX, REUSE = 0, 1, 2
-OP_INDEXER_TOPK, OP_REINDEX, OP_SPARSE_ATTN, OP_DENSE_ATTN = 1, 2, 3, 4
+OP_INDEXER_TOPK, OP_REINDEX, OP_SPARSE_ATTN, OP_DENSE_ATTN, OP_LINEAR_FP4 = 1, 2, 3, 4, 5
 ROPE_HALVES, ROPE_INVERSE, ROPE_NO_NORM = 1, 2, 4
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 D_LAT = 512
@@ -72,7 +72,8 @@ def load(path=None):
     lib.csa2_reindex.argtypes = [i32, cp, vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp]
     lib.csa2_reindex_f32.argtypes = [cp, vp, vp, i32, i32, vp, i32, i32, vp, vp, sz, vp]
     lib.csa2_sparse_attn.argtypes = [cp, vp, i32, i32, vp, vp, i32, vp, i64, i32, ctypes.c_float, vp, vp, vp, sz, vp]
-    lib.csa2_linear_fp4.argtypes = [vp, i32, i64, i64, i32, i32, i32, i32, vp, vp, ctypes.c_float, vp, i32, i64, i64, vp]
+    lib.csa2_linear_fp4.argtypes = [vp, i32, i64, i64, i32, i32, i32, i32, vp, vp, ctypes.c_float, vp, i32, i64,
+                                    i64, vp, sz, vp]
     hp = ctypes.POINTER(_HeadRows)
     lib.csa2_norm_rope.argtypes = [hp, hp, i32, i32, i32, i32, i32, vp, vp, ctypes.c_float, i32, vp]
     lib.csa2_dense_attn.argtypes = [cp, vp, i32, i32, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, sz, vp]
@@ -306,7 +307,7 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, stream=None):
+def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, ws=None, stream=None):
     """y = alpha * W x with FP4 weights (csa2_quantize_fp4's format), for every token.
     x bf16 / fp16 / fp32 [T, n_in] with codes uint8 [n_out, n_in/2] and scales uint8 [n_out, n_in/16], or
     x [T, G, n_in] with codes [G, n_out, n_in/2] and scales [G, n_out, n_in/16] (a product per group).
@@ -327,9 +328,14 @@ def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, strea
           "out [.., n_out] with the leading sizes of x")
     _need(x.dtype in _TYPES and out.dtype in _TYPES, "x and out: bf16, fp16 or fp32")
     _need((x.stride(-1) == 1 or n_in == 0) and (out.stride(-1) == 1 or n_out <= 1), "rows of x and out: contiguous")
-    st = load().csa2_linear_fp4(x.data_ptr(), _TYPES[x.dtype], x.stride(0), x.stride(1) if grouped else 0, x.shape[0], G,
-                                n_in, n_out, codes.data_ptr(), scales.data_ptr(), alpha, out.data_ptr(),
-                                _TYPES[out.dtype], out.stride(0), out.stride(1) if grouped else 0, _stream(stream))
+    lib, T, x_type = load(), x.shape[0], _TYPES[x.dtype]
+    if ws is None:
+        n = lib.csa2_workspace_size(OP_LINEAR_FP4, T, G, x_type, 0, n_in)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    st = lib.csa2_linear_fp4(x.data_ptr(), x_type, x.stride(0), x.stride(1) if grouped else 0, T, G, n_in, n_out,
+                             codes.data_ptr(), scales.data_ptr(), alpha, out.data_ptr(), _TYPES[out.dtype], out.stride(0),
+                             out.stride(1) if grouped else 0, None if ws is None else ws.data_ptr(),
+                             0 if ws is None else ws.numel(), _stream(stream))
     _check(st, "csa2_linear_fp4")
     return out
 

@@ -28,7 +28,8 @@ size_t indexer_full_ws(int batch, int n_q, int64_t capacity);
 size_t reindex_ws(int batch, int n_q, int64_t pool_len);
 cudaError_t launch_linear_fp4(const void* x, int x_type, int64_t x_tok, int64_t x_group, int n_tok, int n_groups,
                               int n_in, int n_out, const uint8_t* codes, const uint8_t* scales, float alpha, void* y,
-                              int y_type, int64_t y_tok, int64_t y_group, cudaStream_t st);
+                              int y_type, int64_t y_tok, int64_t y_group, void* ws, cudaStream_t st);
+size_t linear_fp4_ws(int x_type, int n_tok, int n_groups, int n_in);
 cudaError_t launch_norm_rope(const csa2_head_rows* q, const csa2_head_rows* k, int x_type, int y_type, int n_tok, int d,
                              int d_rot, const int64_t* pos, const float* inv_freq, float eps, int flags,
                              cudaStream_t st);
@@ -103,6 +104,8 @@ size_t csa2_workspace_size(int32_t op, int32_t batch, int32_t n_q, int32_t n_hea
         case CSA2_OP_REINDEX: return reindex_ws(batch, n_q, capacity);
         case CSA2_OP_SPARSE_ATTN: return sparse_attn_ws(batch, n_q, n_heads, k);
         case CSA2_OP_DENSE_ATTN: return n_heads < 1 ? 0 : dense_attn_ws(batch, n_q, n_heads, capacity);
+        case CSA2_OP_LINEAR_FP4:
+            return n_heads < 0 || n_heads > CSA2_F32 || capacity > 0x7fffffff ? 0 : linear_fp4_ws(n_heads, batch, n_q, (int)capacity);
     }
     return 0;
 }
@@ -249,7 +252,8 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
 
 csa2_status csa2_linear_fp4(const void* x, int32_t x_type, int64_t x_tok, int64_t x_group, int32_t n_tok,
                             int32_t n_groups, int32_t n_in, int32_t n_out, const uint8_t* codes, const uint8_t* scales,
-                            float alpha, void* y, int32_t y_type, int64_t y_tok, int64_t y_group, void* stream) {
+                            float alpha, void* y, int32_t y_type, int64_t y_tok, int64_t y_group, void* workspace,
+                            size_t ws_bytes, void* stream) {
     if (!known_type(x_type) || !known_type(y_type)) return CSA2_ERR_INVALID_ARG;
     if (n_tok < 0 || n_groups < 1 || n_groups > 65535 || n_in < 0 || n_in % 16 || n_out < 0) return CSA2_ERR_INVALID_ARG;
     if (!std::isfinite(alpha)) return CSA2_ERR_INVALID_ARG;
@@ -257,8 +261,10 @@ csa2_status csa2_linear_fp4(const void* x, int32_t x_type, int64_t x_tok, int64_
     if (!y || !aligned(y, type_size(y_type))) return CSA2_ERR_INVALID_ARG;
     if (n_in > 0 && (!x || !codes || !scales || !aligned(x, type_size(x_type)) || !aligned(codes, 16)))
         return CSA2_ERR_INVALID_ARG;
+    const size_t need = linear_fp4_ws(x_type, n_tok, n_groups, n_in);
+    if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return CSA2_ERR_WORKSPACE;
     return from_cuda(launch_linear_fp4(x, x_type, x_tok, x_group, n_tok, n_groups, n_in, n_out, codes, scales, alpha, y,
-                                       y_type, y_tok, y_group, (cudaStream_t)stream));
+                                       y_type, y_tok, y_group, workspace, (cudaStream_t)stream));
 }
 
 csa2_status csa2_norm_rope(const csa2_head_rows* q, const csa2_head_rows* k, int32_t x_type, int32_t y_type,

@@ -1,93 +1,629 @@
 // Products with FP4 weights (E2M1 codes, one E4M3 scale per 16 values, the
-// cache's format) for the few tokens of a decode step or a small chunk:
-//     y[t][g][m] = alpha * sum_k W[g][m][k] x[t][g][k]
-// W is never expanded in memory: 9/16 of a byte per weight is read once.
+// cache's format):  y[t][g][m] = alpha * sum_k W[g][m][k] x[t][g][k].
 //
-// One warp per output row and 8 tokens; lane l takes the scale groups l, l+32, ..
-// of the row (8 bytes of codes and one scale byte), fp32 sums per token, joined
-// by shuffles.
+// W is never expanded in memory: 9/16 of a byte per weight is read once per pass
+// over the tokens, and the weights become fp16 in registers.  That is exact: an
+// E2M1 value times an E4M3 scale has at most 6 significant bits and lies in
+// [2^-10, 2688].  x goes to fp16 too, each token (of a group) times the power of
+// two 2^-E that brings its largest magnitude into [2^14, 2^15): fp16 x needs no
+// scale, bf16 x loses only what lies 2^39 below the token's largest value, and
+// fp32 x is split into two fp16 parts (2^-22 of each value).  Products are exact,
+// sums fp32; the epilogue multiplies by alpha and 2^E and rounds once.
+//
+// Two kernels:
+//  - k_linear_few (up to 16 tokens): bound by the weight bytes.  mma.sync
+//    m16n8k16, the weights as the A fragments straight from global memory.  The
+//    order of k within a product is free as long as both operands agree, so a
+//    lane takes 16 consecutive bytes of a row (32 weights, two scale groups) and
+//    feeds them, four at a time, to eight products; x lies in shared memory in
+//    the matching order.  The block's 8 warps share rows and inner chunks.
+//  - k_linear_many: tcgen05, M = 128 rows, N = up to 128 tokens.  Expanded
+//    weights go from registers to TMEM (the A operand), so shared memory carries
+//    the tokens alone: with both operands there, N = 128 would need 192 bytes per
+//    clock of the 128 it gives.  x comes by bulk copies in the layout that
+//    k_linear_x has written to the workspace.  When there are few row tiles a
+//    cluster of blocks splits n_in and adds up through distributed shared memory.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
 #include "elem.cuh"
+#include "fp4_f16.cuh"
+#include "umma.cuh"
 
 namespace csa2 {
 
-constexpr int LF_TOK = 8;
+struct LinArgs {
+    const void* x;
+    int64_t x_tok, x_group;
+    int n_tok, n_groups, n_in, n_out;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    float alpha;
+    void* y;
+    int y_type;
+    int64_t y_tok, y_group;
+};
 
-__device__ __forceinline__ float e2m1_to_f32(uint32_t code) {
-    const uint32_t m = code & 7u;
-    const float v = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-    return (code & 8u) ? -v : v;
-}
-// as e4m3_to_f32, with the format's NaN bytes
-__device__ __forceinline__ float e4m3_to_f32_nan(uint32_t b) {
-    return (b & 127u) == 127u ? __int_as_float(0x7fc00000) : e4m3_to_f32(b);
+__device__ __forceinline__ void lin_store(const LinArgs& a, int t, int g, int m, float v) {
+    const int64_t i = t * a.y_tok + g * a.y_group + m;
+    if (a.y_type == CSA2_BF16)
+        reinterpret_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
+    else if (a.y_type == CSA2_F16)
+        reinterpret_cast<__half*>(a.y)[i] = __float2half_rn(v);
+    else
+        reinterpret_cast<float*>(a.y)[i] = v;
 }
 
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(256) k_linear_fp4_rows(const TX* __restrict__ x, int64_t x_tok, int64_t x_group,
-                                                         int n_tok, int n_in, int n_out,
-                                                         const uint8_t* __restrict__ codes,
-                                                         const uint8_t* __restrict__ scales, float alpha,
-                                                         TY* __restrict__ y, int64_t y_tok, int64_t y_group) {
-    pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m = blockIdx.x * 8 + warp, g = blockIdx.y, t0 = blockIdx.z * LF_TOK;
-    if (m < n_out) {
-        const int64_t row = (int64_t)g * n_out + m;
-        const uint2* cw = reinterpret_cast<const uint2*>(codes + row * (n_in / 2));
-        const uint8_t* sc = scales + row * (n_in / 16);
-        const int nt = min(LF_TOK, n_tok - t0);
-        const TX* xp = x + t0 * x_tok + g * x_group;
-        float acc[LF_TOK] = {};
-        for (int i = lane; i < n_in / 16; i += 32) {
-            const uint2 c = cw[i];
-            const float s = e4m3_to_f32_nan(sc[i]);
-            for (int e = 0; e < 16; ++e) {
-                const float w = e2m1_to_f32(((e < 8 ? c.x : c.y) >> (4 * (e & 7))) & 15u) * s;
+// The exponent E of a token whose largest finite magnitude is mx: mx * 2^-E in [2^14, 2^15)
+__device__ __forceinline__ int lin_exp(float mx) {
+    if (mx == 0.0f) return 0;
+    return max(-126, (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 14);
+}
+template <typename TX>
+__device__ __forceinline__ float lin_absmax(const ElemVec<TX, 8>& v) {
+    float m = 0.0f;
 #pragma unroll
-                for (int t = 0; t < LF_TOK; ++t)
-                    if (t < nt) acc[t] = fmaf(w, to_f32(xp[t * x_tok + i * 16 + e]), acc[t]);
+    for (int e = 0; e < 8; ++e) {
+        const float a = fabsf(v.get(e));
+        if (a < INFINITY) m = fmaxf(m, a);           // infinities and NaN stay what they are in fp16
+    }
+    return m;
+}
+// eight values times d as fp16, and for fp32 what that leaves (0 where it is not finite)
+template <typename TX>
+__device__ __forceinline__ void lin_split(const ElemVec<TX, 8>& v, float d, uint4& hi, uint4& lo) {
+    uint32_t h[4], l[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(TX) == 2 && !std::is_same<TX, __nv_bfloat16>::value) {
+            h[i] = v.w[i];
+        } else {
+            const float a = v.get(2 * i) * d, b = v.get(2 * i + 1) * d;
+            const __half2 p = __floats2half2_rn(a, b);
+            h[i] = *reinterpret_cast<const uint32_t*>(&p);
+            if constexpr (sizeof(TX) == 4) {
+                const float ra = a - __low2float(p), rb = b - __high2float(p);
+                l[i] = f16x2_bits(fabsf(ra) < INFINITY ? ra : 0.0f, fabsf(rb) < INFINITY ? rb : 0.0f);
             }
         }
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// the eight elements at p, by 16-byte loads where the rows allow it
+template <typename TX>
+__device__ __forceinline__ ElemVec<TX, 8> lin_load8(const TX* p, bool vec) {
+    ElemVec<TX, 8> v;
+    if (vec) {
+        v.load(p);
+    } else {
 #pragma unroll
-        for (int t = 0; t < LF_TOK; ++t) {
-            for (int o = 16; o; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-            if (lane == 0 && t < nt) y[(t0 + t) * y_tok + g * y_group + m] = from_f32<TY>(alpha * acc[t]);
+        for (int i = 0; i < ElemVec<TX, 8>::WORDS; ++i) v.w[i] = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (sizeof(TX) == 4)
+                v.w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+            else
+                v.w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
         }
+    }
+    return v;
+}
+
+// ================================================================ up to 16 tokens
+
+constexpr int LF_THREADS = 256, LF_WARPS = 8;
+constexpr int LF_TOK = 16;
+constexpr int LF_SMEM = 200 * 1024;              // the tokens' fp16 parts a block may hold
+
+__device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 32 weights (16 bytes of codes, two scales) of one row from k on; zeros from n_in on
+struct LinSeg {
+    uint4 c;
+    uint32_t s;
+    __device__ __forceinline__ void load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int k,
+                                         int n_in, bool wide) {
+        c = make_uint4(0, 0, 0, 0);
+        s = 0u;
+        if (k >= n_in) return;
+        if (wide) {                              // n_in a multiple of 32: every segment is whole and aligned
+            c = __ldg(reinterpret_cast<const uint4*>(codes + k / 2));
+            s = __ldg(reinterpret_cast<const uint16_t*>(scales + k / 16));
+        } else {
+            const uint2 a = __ldg(reinterpret_cast<const uint2*>(codes + k / 2));
+            c.x = a.x, c.y = a.y;
+            s = __ldg(scales + k / 16);
+            if (k + 16 < n_in) {
+                const uint2 b = __ldg(reinterpret_cast<const uint2*>(codes + k / 2) + 1);
+                c.z = b.x, c.w = b.y;
+                s |= (uint32_t)__ldg(scales + k / 16 + 1) << 8;
+            }
+        }
+    }
+};
+
+// byte offset of the 16-byte unit j (8 values) of segment c (32 values) of token t in chunk ch (128
+// values): the eight lanes of a quarter warp (two tokens, four segments) hit eight different bank groups
+__device__ __forceinline__ uint32_t lf_unit(int ch, int t, int c, int j, int n_tok) {
+    return (uint32_t)(((ch * n_tok + t) * 4 + c) * 64 + ((j ^ ((t & 1) * 2 + (c >> 1))) << 4));
+}
+
+// NT: token tiles of 8; wk: warps that share a row tile (1, 2, 4 or 8), each taking every wk-th chunk
+template <typename TX, int NT>
+__global__ void __launch_bounds__(LF_THREADS) k_linear_few(const LinArgs a, int wk, int x_vec, int wide) {
+    extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ unsigned int tmax[LF_TOK];
+    constexpr bool SPLIT = sizeof(TX) == 4, SCALED = !std::is_same<TX, __half>::value;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int K = a.n_in, T = a.n_tok, g = blockIdx.y;
+    const int chunks = (K + 127) / 128;
+    const int rows_block = 16 * (LF_WARPS / wk);
+    const int row_tile = warp / wk, part = warp % wk;
+    const int m0 = blockIdx.x * rows_block + row_tile * 16;
+    const int r = lane >> 2, c = lane & 3;
+    // rows past the end repeat the last one; their results are not stored
+    const int ra = min(m0 + r, a.n_out - 1), rb = min(m0 + r + 8, a.n_out - 1);
+    const int64_t row0 = (int64_t)g * a.n_out;
+    const uint8_t* ca = a.codes + (row0 + ra) * (K / 2);
+    const uint8_t* cb = a.codes + (row0 + rb) * (K / 2);
+    const uint8_t* sa = a.scales + (row0 + ra) * (K / 16);
+    const uint8_t* sb = a.scales + (row0 + rb) * (K / 16);
+    pdl_wait();                                  // x, and weights just quantised, may come from the preceding kernel
+    constexpr int AHEAD = 2;                     // chunks in flight
+    LinSeg wa[AHEAD], wb[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+        const int k = (part + i * wk) * 128 + c * 32;
+        wa[i].load(ca, sa, k, K, wide);
+        wb[i].load(cb, sb, k, K, wide);
+    }
+
+    // ---- the tokens into shared memory (hi part, then for fp32 the lo part)
+    const TX* x = reinterpret_cast<const TX*>(a.x) + (int64_t)g * a.x_group;
+    const uint32_t plane = (uint32_t)chunks * T * 256;
+    const int segs = (chunks * 128 + 255) / 256;             // 256 values of one token per warp step
+    if (SCALED) {
+        if (tid < LF_TOK) tmax[tid] = 0u;
+        __syncthreads();
+        for (int u = warp; u < T * segs; u += LF_WARPS) {
+            const int t = u / segs, k = (u - t * segs) * 256 + lane * 8;
+            float m = 0.0f;
+            if (k < K) m = lin_absmax(lin_load8(x + t * a.x_tok + k, x_vec));
+            const unsigned int w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+            if (lane == 0 && w) atomicMax(&tmax[t], w);
+        }
+        __syncthreads();
+    }
+    for (int u = warp; u < T * segs; u += LF_WARPS) {
+        const int t = u / segs, k = (u - t * segs) * 256 + lane * 8;
+        if (k < chunks * 128) {
+            uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+            if (k < K)
+                lin_split(lin_load8(x + t * a.x_tok + k, x_vec), SCALED ? pow2f(-lin_exp(__uint_as_float(tmax[t]))) : 1.0f, hi, lo);
+            const uint32_t at = lf_unit(k >> 7, t, (k >> 5) & 3, (k >> 3) & 3, T);
+            *reinterpret_cast<uint4*>(sm + at) = hi;
+            if (SPLIT) *reinterpret_cast<uint4*>(sm + plane + at) = lo;
+        }
+    }
+    __syncthreads();
+
+    float acc[NT][2][4] = {};                    // two sums per tile: consecutive products do not wait for each other
+    for (int ch0 = part; ch0 < chunks; ch0 += AHEAD * wk) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int ch = ch0 + i * wk;
+            if (ch >= chunks) break;
+            const LinSeg va = wa[i], vb = wb[i];
+            {
+                const int k = (ch + AHEAD * wk) * 128 + c * 32;
+                wa[i].load(ca, sa, k, K, wide);
+                wb[i].load(cb, sb, k, K, wide);
+            }
+            const __half2 pa = e4m3x2_to_f16x2(va.s), pb = e4m3x2_to_f16x2(vb.s);
+            const uint32_t xa[4] = {va.c.x, va.c.y, va.c.z, va.c.w}, xb[4] = {vb.c.x, vb.c.y, vb.c.z, vb.c.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint4 fa = e2m1x8_scaled(xa[w], w < 2 ? __low2half2(pa) : __high2half2(pa));
+                const uint4 fb = e2m1x8_scaled(xb[w], w < 2 ? __low2half2(pb) : __high2half2(pb));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int t = n * 8 + r;     // this lane's token of the B fragment
+                    uint4 b = make_uint4(0, 0, 0, 0), bl = b;
+                    if (t < T) {
+                        const uint32_t at = lf_unit(ch, t, c, w, T);
+                        b = *reinterpret_cast<const uint4*>(sm + at);
+                        if (SPLIT) bl = *reinterpret_cast<const uint4*>(sm + plane + at);
+                    }
+                    mma_16816(acc[n][0], fa.x, fb.x, fa.y, fb.y, b.x, b.y);
+                    mma_16816(acc[n][1], fa.z, fb.z, fa.w, fb.w, b.z, b.w);
+                    if (SPLIT) {
+                        mma_16816(acc[n][0], fa.x, fb.x, fa.y, fb.y, bl.x, bl.y);
+                        mma_16816(acc[n][1], fa.z, fb.z, fa.w, fb.w, bl.z, bl.w);
+                    }
+                }
+            }
+        }
+    }
+    // ---- join the warps of a row tile in order, scale, store with the rows along the lanes
+    __syncthreads();                             // the tokens are read no more
+    float* red = reinterpret_cast<float*>(sm);   // [warp][token][16 rows]
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            red[(warp * NT * 8 + n * 8 + 2 * c + (i & 1)) * 16 + r + 8 * (i >> 1)] = acc[n][0][i] + acc[n][1][i];
+    __syncthreads();
+    for (int u = tid; u < T * rows_block; u += LF_THREADS) {
+        const int t = u / rows_block, row = u - t * rows_block, m = blockIdx.x * rows_block + row;
+        if (m >= a.n_out) continue;
+        float v = 0.0f;
+        for (int p = 0; p < wk; ++p) v += red[(((row >> 4) * wk + p) * NT * 8 + t) * 16 + (row & 15)];
+        v *= a.alpha;
+        if (SCALED) v *= pow2f(lin_exp(__uint_as_float(tmax[t])));
+        lin_store(a, t, g, m, v);
     }
     __threadfence();    // the attention may stage these rows as its queries before it waits (see norm_rope.cu)
 }
 
+// ================================================================ more tokens
+
+constexpr int LM_THREADS = 320;                  // 8 expanding / epilogue warps, the x copies, the MMAs
+constexpr int LM_M = 128, LM_K = 64;             // rows of a block, values per stage
+constexpr int LM_STAGES = 4;
+
+struct LinPrep {                                 // the workspace's layout
+    int nb, tiles, chunks, planes;               // tokens per tile, token tiles, 64-value chunks, fp16 parts
+    __host__ __device__ int64_t tile_bytes() const { return (int64_t)nb * 128; }
+    // [group][token tile][chunk][part] tiles of nb rows x 64 values in the MMA's swizzled layout
+    __host__ __device__ int64_t tile(int g, int tt, int ch, int p) const {
+        return ((((int64_t)g * tiles + tt) * chunks + ch) * planes + p) * tile_bytes();
+    }
+    __host__ __device__ int64_t scales_at(int groups) const { return (int64_t)groups * tiles * chunks * planes * tile_bytes(); }
+};
+
+// one block per token and group: its scale, and its values in the layout above
+template <typename TX>
+__global__ void __launch_bounds__(256) k_linear_x(const LinArgs a, LinPrep p, uint8_t* __restrict__ ws, int x_vec) {
+    constexpr bool SPLIT = sizeof(TX) == 4, SCALED = !std::is_same<TX, __half>::value;
+    __shared__ unsigned int tmax;
+    pdl_wait();
+    pdl_launch_next();                           // the product's blocks start expanding weights meanwhile
+    const int t = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
+    const TX* x = reinterpret_cast<const TX*>(a.x) + t * a.x_tok + (int64_t)g * a.x_group;
+    float d = 1.0f;
+    float* scale = reinterpret_cast<float*>(ws + p.scales_at(a.n_groups)) + (int64_t)g * a.n_tok + t;
+    if (SCALED) {
+        if (tid == 0) tmax = 0u;
+        __syncthreads();
+        float m = 0.0f;
+        for (int k = tid * 8; k < a.n_in; k += 2048) m = fmaxf(m, lin_absmax(lin_load8(x + k, x_vec)));
+        const unsigned int w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if ((tid & 31) == 0 && w) atomicMax(&tmax, w);
+        __syncthreads();
+        const int e = lin_exp(__uint_as_float(tmax));
+        d = pow2f(-e);
+        if (tid == 0) *scale = pow2f(e);
+    } else if (tid == 0) {
+        *scale = 1.0f;
+    }
+    const int tt = t / p.nb, r = t - tt * p.nb;
+    for (int k = tid * 8; k < p.chunks * LM_K; k += 2048) {
+        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+        if (k < a.n_in) lin_split(lin_load8(x + k, x_vec), d, hi, lo);
+        const int64_t at = p.tile(g, tt, k >> 6, 0) + r * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(ws + at) = hi;
+        if (SPLIT) *reinterpret_cast<uint4*>(ws + at + p.tile_bytes()) = lo;
+    }
+}
+
+// D[tmem] += A[tmem: 128 rows x 16 fp16, two per column] . B[smem]
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// 64 weights of one row: 32 bytes of codes, four scales
+struct LinSeg64 {
+    uint4 c[2];
+    uint32_t s;
+    __device__ __forceinline__ void load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int k,
+                                         int n_in, int wide) {
+        c[0] = c[1] = make_uint4(0, 0, 0, 0);
+        s = 0u;
+        if (k >= n_in) return;
+        if (wide == 2) {                         // n_in a multiple of 64
+            c[0] = __ldg(reinterpret_cast<const uint4*>(codes + k / 2));
+            c[1] = __ldg(reinterpret_cast<const uint4*>(codes + k / 2) + 1);
+            s = __ldg(reinterpret_cast<const uint32_t*>(scales + k / 16));
+        } else {
+            LinSeg h;
+            h.load(codes, scales, k, n_in, wide == 1);
+            c[0] = h.c, s = h.s;
+            h.load(codes, scales, k + 32, n_in, wide == 1);
+            c[1] = h.c, s |= h.s << 16;
+        }
+    }
+};
+
+// grid (row tiles x splits, token tiles, groups); the splits of a row tile form a cluster
+__global__ void __launch_bounds__(LM_THREADS) k_linear_many(const LinArgs a, LinPrep p, const uint8_t* __restrict__ ws,
+                                                            int* __restrict__ err, int splits, int wide) {
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) unsigned long long b_w[LM_STAGES], b_x[LM_STAGES], b_free[LM_STAGES], b_done;
+    __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tile_m = blockIdx.x / splits, split = blockIdx.x % splits, tt = blockIdx.y, g = blockIdx.z;
+    const int NB = p.nb;
+    const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
+    uint8_t* sm = dyn + (base - raw);
+    const uint32_t stage_bytes = (uint32_t)(p.tile_bytes() * p.planes);
+    const int ch0 = (int)((int64_t)p.chunks * split / splits), ch1 = (int)((int64_t)p.chunks * (split + 1) / splits);
+    constexpr uint32_t cols = 256, t_a = 128;                    // D: up to 128 columns; A: 4 stages x 32
+    auto sa = [&](const void* q) { return umma::smem_u32(q); };
+    if (tid == 0) {
+        for (int i = 0; i < LM_STAGES; ++i) {
+            umma::mbar_init(sa(&b_w[i]), 4);                     // the four lane quarters of the stage's weights
+            umma::mbar_init(sa(&b_x[i]), 1);
+            umma::mbar_init(sa(&b_free[i]), 1);
+        }
+        umma::mbar_init(sa(&b_done), 1);
+        umma::fence_mbar_init();
+    }
+    if (warp == 0) umma::tmem_alloc(sa(&tmem_base), cols);
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    const uint32_t tmem = tmem_base;
+    bool ok = true;
+    const int n = ch1 - ch0;
+
+    if (warp < 8) {
+        // ================= weights: warp w takes rows 32(w%4) .. +31 of the tile, chunks of parity w/4.
+        // Only x and its scales come from the kernel before this one, so nothing waits here.
+        const int q = warp & 3, par = warp >> 2;
+        const int m = min(tile_m * LM_M + q * 32 + lane, a.n_out - 1);
+        const int64_t row = (int64_t)g * a.n_out + m;
+        const uint8_t* cr = a.codes + row * (a.n_in / 2);
+        const uint8_t* sr = a.scales + row * (a.n_in / 16);
+        constexpr int AHEAD = 3;
+        LinSeg64 seg[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int j = par + 2 * i;
+            seg[i].load(cr, sr, j < n ? (ch0 + j) * LM_K : a.n_in, a.n_in, wide);
+        }
+        for (int j0 = par; j0 < n; j0 += 2 * AHEAD) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int j = j0 + 2 * i;
+                if (j >= n) break;
+                const LinSeg64 v = seg[i];
+                {
+                    const int jn = j + 2 * AHEAD;
+                    seg[i].load(cr, sr, jn < n ? (ch0 + jn) * LM_K : a.n_in, a.n_in, wide);
+                }
+                uint32_t o[32];
+                const __half2 s01 = e4m3x2_to_f16x2(v.s & 0xffffu), s23 = e4m3x2_to_f16x2(v.s >> 16);
+                const __half2 sc[4] = {__low2half2(s01), __high2half2(s01), __low2half2(s23), __high2half2(s23)};
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    const uint4& cc = v.c[w >> 2];
+                    const uint32_t word = (w & 3) == 0 ? cc.x : (w & 3) == 1 ? cc.y : (w & 3) == 2 ? cc.z : cc.w;
+                    const uint4 f = e2m1x8_scaled(word, sc[w >> 1]);
+                    o[4 * w] = f.x, o[4 * w + 1] = f.y, o[4 * w + 2] = f.z, o[4 * w + 3] = f.w;
+                }
+                const int st = j % LM_STAGES;
+                if (j >= LM_STAGES) {
+                    ok = ok && umma::mbar_wait_fast(sa(&b_free[st]), (j / LM_STAGES - 1) & 1);
+                    umma::fence_after();
+                }
+                tmem_st32(tmem + ((uint32_t)(q * 32) << 16) + t_a + 32 * st, o);
+                umma::tmem_wait_st();
+                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(sa(&b_w[st]));
+            }
+        }
+    } else if (warp == 8) {
+        // ================= x: bulk copies of the prepared tiles
+        if (lane == 0) {
+            pdl_wait();
+            for (int j = 0; j < n; ++j) {
+                const int st = j % LM_STAGES;
+                if (j >= LM_STAGES) ok = ok && umma::mbar_wait_fast(sa(&b_free[st]), (j / LM_STAGES - 1) & 1);
+                if (!ok) break;
+                umma::mbar_arrive_expect_tx(sa(&b_x[st]), stage_bytes);
+                umma::bulk_g2s(base + st * stage_bytes, ws + p.tile(g, tt, ch0 + j, 0), stage_bytes, sa(&b_x[st]));
+            }
+        }
+    } else if (lane == 0) {
+        // ================= MMAs
+        const uint32_t id = umma::idesc_f16(LM_M, NB, 0, 0);
+        for (int j = 0; j < n; ++j) {
+            const int st = j % LM_STAGES;
+            ok = ok && umma::mbar_wait_fast(sa(&b_w[st]), (j / LM_STAGES) & 1);
+            ok = ok && umma::mbar_wait_fast(sa(&b_x[st]), (j / LM_STAGES) & 1);
+            if (!ok) break;
+            umma::fence_after();
+            for (int pl = 0; pl < p.planes; ++pl) {
+                const uint64_t bd = umma::desc(base + st * stage_bytes + pl * (uint32_t)p.tile_bytes(), 16, 1024, umma::LAYOUT_SW128);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_f16_ta(tmem, tmem + t_a + 32 * st + 8 * ks, bd + (uint64_t)((ks * 32) >> 4), id, j > 0 || pl > 0 || ks > 0);
+            }
+            umma::commit(sa(&b_free[st]));
+        }
+        if (ok) umma::commit(sa(&b_done));
+    }
+
+    // ================= epilogue
+    const float* scale = reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)g * a.n_tok;
+    const int t0 = tt * NB, nt = min(NB, a.n_tok - t0);
+    __syncwarp();                                // warps 8 and 9 ran their loops in one lane
+    pdl_wait();                                  // the scales, and y
+    if (warp < 8) {
+        if (n > 0) ok = ok && umma::mbar_wait_fast(sa(&b_done), 0);
+        umma::fence_after();
+    }
+    const int q = warp & 3, m = tile_m * LM_M + q * 32 + lane;
+    const int c0 = (warp >> 2) * (NB / 2);       // this warp's half of the tokens
+    if (splits == 1) {
+        if (warp < 8)
+            for (int c = c0; c < c0 + NB / 2 && c < nt; c += 16) {
+                float v[16];
+                umma::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+                umma::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < nt && m < a.n_out)
+                        lin_store(a, t0 + c + i, g, m, ok ? (n > 0 ? v[i] : 0.0f) * a.alpha * scale[t0 + c + i] : __int_as_float(0x7fc00000));
+            }
+    } else {
+        // this block's sums as [token][128 rows] in its shared memory (its copies are all done and read);
+        // block r of the cluster adds up, in order, and stores every splits-th token
+        float* mine = reinterpret_cast<float*>(sm);
+        if (warp < 8)
+            for (int c = c0; c < c0 + NB / 2; c += 16) {
+                float v[16];
+                umma::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+                umma::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    mine[(c + i) * LM_M + q * 32 + lane] = ok ? (n > 0 ? v[i] : 0.0f) : __int_as_float(0x7fc00000);
+            }
+        umma::cluster_sync();
+        for (int u = tid; u < ((nt - split + splits - 1) / splits) * LM_M; u += LM_THREADS) {
+            const int c = split + (u / LM_M) * splits, row = u % LM_M;
+            float v = 0.0f;
+            for (int s = 0; s < splits; ++s) {
+                float w;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(umma::mapa(sa(mine + c * LM_M + row), s)));
+                v += w;
+            }
+            const int mm = tile_m * LM_M + row;
+            if (mm < a.n_out) lin_store(a, t0 + c, g, mm, v * a.alpha * scale[t0 + c]);
+        }
+        umma::cluster_sync();                    // no block leaves while another reads its sums
+    }
+    if (!ok) atomicExch(err, 1);
+    __threadfence();
+    umma::fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        umma::fence_after();
+        umma::tmem_dealloc(tmem, cols);
+    }
+}
+
 namespace {
-template <typename TX, typename TY>
-cudaError_t lf_launch(const void* x, int64_t x_tok, int64_t x_group, int n_tok, int n_groups, int n_in, int n_out,
-                      const uint8_t* codes, const uint8_t* scales, float alpha, void* y, int64_t y_tok,
-                      int64_t y_group, cudaStream_t st) {
-    const dim3 grid((n_out + 7) / 8, n_groups, (n_tok + LF_TOK - 1) / LF_TOK);
-    launch_k(k_linear_fp4_rows<TX, TY>, grid, 256, 0, st, reinterpret_cast<const TX*>(x), x_tok, x_group, n_tok, n_in,
-             n_out, codes, scales, alpha, reinterpret_cast<TY*>(y), y_tok, y_group);
+constexpr size_t LM_HEAD = 256;                  // the error word and padding
+
+// how the rows of codes and scales may be read: 2: 64 values at a time, 1: 32, 0: 16
+int lin_wide(const LinArgs& a) {
+    const uintptr_t s = reinterpret_cast<uintptr_t>(a.scales);
+    return a.n_in % 64 == 0 && s % 4 == 0 ? 2 : a.n_in % 32 == 0 && s % 2 == 0 ? 1 : 0;
+}
+int lin_planes(int x_type) { return x_type == CSA2_F32 ? 2 : 1; }
+
+// up to 16 tokens whose fp16 parts fit a block's shared memory
+bool lin_few(int x_type, int n_tok, int n_in) {
+    return n_tok <= LF_TOK && (int64_t)(n_in + 127) / 128 * n_tok * 256 * lin_planes(x_type) <= LF_SMEM;
+}
+LinPrep lin_prep(int x_type, int n_tok, int n_in) {
+    LinPrep p;
+    p.nb = n_tok <= 32 ? 32 : n_tok <= 64 ? 64 : 128;
+    p.tiles = (n_tok + p.nb - 1) / p.nb;
+    p.chunks = (n_in + LM_K - 1) / LM_K;
+    p.planes = lin_planes(x_type);
+    return p;
+}
+
+template <typename TX, int NT>
+cudaError_t lf_launch(const LinArgs& a, int x_vec, cudaStream_t st) {
+    // Warps per row tile: until 24 warps per SM have work
+    const int64_t tiles = (int64_t)((a.n_out + 15) / 16) * a.n_groups;
+    const int chunks = (a.n_in + 127) / 128;
+    int wk = 1;
+    while (wk < LF_WARPS && 2 * wk <= chunks && tiles * wk < (int64_t)152 * 3 * LF_WARPS) wk *= 2;
+    const int rows = 16 * (LF_WARPS / wk);
+    const size_t x_bytes = (size_t)chunks * a.n_tok * 256 * (sizeof(TX) == 4 ? 2 : 1);
+    const size_t smem = std::max<size_t>(x_bytes, (size_t)LF_WARPS * NT * 8 * 16 * 4);
+    cudaError_t e = cudaFuncSetAttribute(k_linear_few<TX, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LF_SMEM);
+    if (e != cudaSuccess) return e;
+    launch_k(k_linear_few<TX, NT>, dim3((a.n_out + rows - 1) / rows, a.n_groups), LF_THREADS, smem, st, a, wk, x_vec,
+             lin_wide(a) >= 1 ? 1 : 0);
     note_launch();
     return cudaGetLastError();
 }
-template <typename TX, typename... A>
-cudaError_t lf_pick_y(int y_type, A... a) {
-    if (y_type == CSA2_BF16) return lf_launch<TX, __nv_bfloat16>(a...);
-    if (y_type == CSA2_F16) return lf_launch<TX, __half>(a...);
-    return lf_launch<TX, float>(a...);
+template <typename TX>
+cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st) {
+    const int x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_tok * (int64_t)sizeof(TX) % 16 == 0 &&
+                      a.x_group * (int64_t)sizeof(TX) % 16 == 0;
+    if (lin_few(x_type, a.n_tok, a.n_in))
+        return a.n_tok <= 8 ? lf_launch<TX, 1>(a, x_vec, st) : lf_launch<TX, 2>(a, x_vec, st);
+    const LinPrep p = lin_prep(x_type, a.n_tok, a.n_in);
+    uint8_t* ws = reinterpret_cast<uint8_t*>(wsp);
+    launch_k(k_linear_x<TX>, dim3(a.n_tok, a.n_groups), 256, 0, st, a, p, ws + LM_HEAD, x_vec);
+    // Splits of n_in: while the row and token tiles leave SMs idle and a split keeps eight chunks
+    const int tiles_m = (a.n_out + LM_M - 1) / LM_M;
+    const int64_t blocks = (int64_t)tiles_m * p.tiles * a.n_groups;
+    int splits = 1;
+    while (splits < 8 && blocks * splits * 2 <= 152 && p.chunks >= splits * 2 * 8) splits *= 2;
+    const size_t smem = std::max<size_t>((size_t)LM_STAGES * p.tile_bytes() * p.planes, splits > 1 ? (size_t)p.nb * LM_M * 4 : 0) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k_linear_many, cudaFuncAttributeMaxDynamicSharedMemorySize, 132 * 1024);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles_m * splits, p.tiles, a.n_groups);
+    cfg.blockDim = dim3(LM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, k_linear_many, a, p, (const uint8_t*)(ws + LM_HEAD), reinterpret_cast<int*>(ws), splits,
+                           lin_wide(a));
+    note_launch(2);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 }  // namespace
 
+size_t linear_fp4_ws(int x_type, int n_tok, int n_groups, int n_in) {
+    if (lin_few(x_type, n_tok, n_in)) return 0;
+    const LinPrep p = lin_prep(x_type, n_tok, n_in);
+    return LM_HEAD + (size_t)p.scales_at(n_groups) + (size_t)n_groups * n_tok * sizeof(float);
+}
+
 cudaError_t launch_linear_fp4(const void* x, int x_type, int64_t x_tok, int64_t x_group, int n_tok, int n_groups,
                               int n_in, int n_out, const uint8_t* codes, const uint8_t* scales, float alpha, void* y,
-                              int y_type, int64_t y_tok, int64_t y_group, cudaStream_t st) {
-    if (x_type == CSA2_BF16)
-        return lf_pick_y<__nv_bfloat16>(y_type, x, x_tok, x_group, n_tok, n_groups, n_in, n_out, codes, scales, alpha, y,
-                                        y_tok, y_group, st);
-    if (x_type == CSA2_F16)
-        return lf_pick_y<__half>(y_type, x, x_tok, x_group, n_tok, n_groups, n_in, n_out, codes, scales, alpha, y, y_tok,
-                                 y_group, st);
-    return lf_pick_y<float>(y_type, x, x_tok, x_group, n_tok, n_groups, n_in, n_out, codes, scales, alpha, y, y_tok,
-                            y_group, st);
+                              int y_type, int64_t y_tok, int64_t y_group, void* ws, cudaStream_t st) {
+    const LinArgs a{x, x_tok, x_group, n_tok, n_groups, n_in, n_out, codes, scales, alpha, y, y_type, y_tok, y_group};
+    if (x_type == CSA2_BF16) return lin_launch<__nv_bfloat16>(a, x_type, ws, st);
+    if (x_type == CSA2_F16) return lin_launch<__half>(a, x_type, ws, st);
+    return lin_launch<float>(a, x_type, ws, st);
 }
 
 }  // namespace csa2

@@ -66,7 +66,8 @@ typedef enum {
 enum { CSA2_FULL = 0, CSA2_REINDEX = 1, CSA2_REUSE = 2 };
 
 /* operations that take a workspace */
-enum { CSA2_OP_INDEXER_TOPK = 1, CSA2_OP_REINDEX = 2, CSA2_OP_SPARSE_ATTN = 3, CSA2_OP_DENSE_ATTN = 4 };
+enum { CSA2_OP_INDEXER_TOPK = 1, CSA2_OP_REINDEX = 2, CSA2_OP_SPARSE_ATTN = 3, CSA2_OP_DENSE_ATTN = 4,
+       CSA2_OP_LINEAR_FP4 = 5 };
 
 /* element types of the operators that take more than one */
 enum { CSA2_BF16 = 0, CSA2_F16 = 1, CSA2_F32 = 2 };
@@ -248,14 +249,17 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
  *   scales  uint8 [n_groups][n_out][n_in/16]
  * x_type, y_type: CSA2_BF16, CSA2_F16 or CSA2_F32.  n_in a multiple of 16;
  * n_tok, n_in and n_out may be 0 (n_in 0 gives zeros), n_groups <= 65535; x and
- * y aligned to their elements; y overlaps no input.  fp32 x is taken to 2^-22 of
- * each element (two fp16 parts), fp16 and bf16 x exactly, relative to the
- * largest of the token's values that a block reads together; a NaN scale byte, an
- * infinite or a NaN x gives what the formula gives.  No workspace.
+ * y aligned to their elements; y overlaps no input.  fp16 x enters exactly, bf16
+ * x to 2^-39 of the largest value of its token and group, fp32 x to that or 2^-22
+ * of the value itself, whichever is more; a NaN scale byte, an infinite or a NaN x
+ * gives what the formula gives.
+ * workspace: csa2_workspace_size(CSA2_OP_LINEAR_FP4, n_tok, n_groups, x_type, 0,
+ * n_in) bytes (0, and may be NULL, for few tokens), 16-byte aligned.
  */
 csa2_status csa2_linear_fp4(const void* x, int32_t x_type, int64_t x_tok, int64_t x_group, int32_t n_tok,
                             int32_t n_groups, int32_t n_in, int32_t n_out, const uint8_t* codes, const uint8_t* scales,
-                            float alpha, void* y, int32_t y_type, int64_t y_tok, int64_t y_group, void* stream);
+                            float alpha, void* y, int32_t y_type, int64_t y_tok, int64_t y_group, void* workspace,
+                            size_t ws_bytes, void* stream);
 
 /* One set of head rows of csa2_norm_rope: row (t, h) of x starts at element
  * t * x_tok + h * x_head, that of y likewise; the d values of a row are

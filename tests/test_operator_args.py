@@ -17,8 +17,10 @@ def csa():
 P = ctypes.c_void_p(256)
 
 
-def linear(lib, x=P, xt=0, n_tok=1, groups=1, n_in=64, n_out=8, codes=P, scales=P, alpha=1.0, y=P, yt=0):
-    return lib.csa2_linear_fp4(x, xt, n_in, n_in, n_tok, groups, n_in, n_out, codes, scales, alpha, y, yt, n_out, n_out, None)
+def linear(lib, x=P, xt=0, n_tok=1, groups=1, n_in=64, n_out=8, codes=P, scales=P, alpha=1.0, y=P, yt=0, ws=None,
+           ws_bytes=0):
+    return lib.csa2_linear_fp4(x, xt, n_in, n_in, n_tok, groups, n_in, n_out, codes, scales, alpha, y, yt, n_out, n_out, ws,
+                               ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(xt=3), dict(yt=-1), dict(n_tok=-1), dict(groups=0), dict(groups=65536),
@@ -28,6 +30,16 @@ def linear(lib, x=P, xt=0, n_tok=1, groups=1, n_in=64, n_out=8, codes=P, scales=
                                 dict(y=ctypes.c_void_p(258), yt=2)])
 def test_linear_refusals(csa, kw):
     assert linear(csa.load(), **kw) == csa.ERR_INVALID_ARG
+
+
+def test_linear_workspace(csa):
+    size = lambda T, K, xt: csa.csa2_workspace_size(csa.OP_LINEAR_FP4, T, 1, xt, 0, K)
+    assert size(1, 4096, 0) == 0 and size(16, 64, 2) == 0
+    for T, K, xt in [(17, 64, 0), (300, 4096, 2), (16, 1 << 20, 1)]:
+        need = size(T, K, xt)
+        assert need > 0
+        for kw in [dict(), dict(ws=P, ws_bytes=need - 1), dict(ws=ctypes.c_void_p(264), ws_bytes=need)]:
+            assert linear(csa.load(), n_tok=T, n_in=K, xt=xt, **kw) == csa.ERR_WORKSPACE
 
 
 def test_empty_calls_enqueue_nothing(csa):
