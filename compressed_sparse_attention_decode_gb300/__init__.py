@@ -109,8 +109,11 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """the cudaStream_t of `stream`, or of PyTorch's current stream (asked for as a plain pointer:
+    building a torch.cuda.Stream takes longer than a launch)"""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(status, fn):

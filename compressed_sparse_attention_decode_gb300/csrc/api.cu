@@ -105,7 +105,7 @@ size_t csa2_workspace_size(int32_t op, int32_t batch, int32_t n_q, int32_t n_hea
         case CSA2_OP_SPARSE_ATTN: return sparse_attn_ws(batch, n_q, n_heads, k);
         case CSA2_OP_DENSE_ATTN: return n_heads < 1 ? 0 : dense_attn_ws(batch, n_q, n_heads, capacity);
         case CSA2_OP_LINEAR_FP4:
-            return n_heads < 0 || n_heads > CSA2_F32 || capacity > 0x7fffffff ? 0 : linear_fp4_ws(n_heads, batch, n_q, (int)capacity);
+            return n_heads < 0 || n_heads > CSA2_F32 || capacity > (1 << 24) ? 0 : linear_fp4_ws(n_heads, batch, n_q, (int)capacity);
     }
     return 0;
 }
@@ -255,7 +255,8 @@ csa2_status csa2_linear_fp4(const void* x, int32_t x_type, int64_t x_tok, int64_
                             float alpha, void* y, int32_t y_type, int64_t y_tok, int64_t y_group, void* workspace,
                             size_t ws_bytes, void* stream) {
     if (!known_type(x_type) || !known_type(y_type)) return CSA2_ERR_INVALID_ARG;
-    if (n_tok < 0 || n_groups < 1 || n_groups > 65535 || n_in < 0 || n_in % 16 || n_out < 0) return CSA2_ERR_INVALID_ARG;
+    if (n_tok < 0 || n_groups < 1 || n_groups > 65535 || n_in < 0 || n_in > (1 << 24) || n_in % 16 || n_out < 0)
+        return CSA2_ERR_INVALID_ARG;
     if (!std::isfinite(alpha)) return CSA2_ERR_INVALID_ARG;
     if (n_tok == 0 || n_out == 0) return CSA2_OK;
     if (!y || !aligned(y, type_size(y_type))) return CSA2_ERR_INVALID_ARG;

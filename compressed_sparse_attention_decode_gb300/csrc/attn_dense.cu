@@ -477,11 +477,10 @@ __global__ void __launch_bounds__(128) k_dense_combine(const float* __restrict__
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const int64_t row = (query0 + ql) * n_heads + head;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= inv;
     ElemVec<TO, 4> v;
-#pragma unroll
-    for (int i = 0; i < ElemVec<TO, 4>::WORDS; ++i) v.w[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v.set(i, o[i] * inv);
+    v.pack(o);
     v.store(out + row * D_LAT + 4 * threadIdx.x);
     if (lse != nullptr && threadIdx.x == 0)
         lse[row] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace csa2 {
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -64,13 +66,25 @@ struct ElemVec {
             return to_f32(*reinterpret_cast<const T*>(&b));
         }
     }
-    __device__ __forceinline__ void set(int i, float v) {
-        if constexpr (sizeof(T) == 4)
-            w[i] = __float_as_uint(v);
-        else {
-            const T e = from_f32<T>(v);
-            const uint32_t b = *reinterpret_cast<const uint16_t*>(&e);
-            w[i >> 1] = (i & 1) ? ((w[i >> 1] & 0xffffu) | (b << 16)) : ((w[i >> 1] & 0xffff0000u) | b);
+    // N fp32 values, rounded
+    __device__ __forceinline__ void pack(const float* v) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __float_as_uint(v[i]);
+        } else if constexpr (N == 1) {
+            const T e = from_f32<T>(v[0]);
+            w[0] = *reinterpret_cast<const uint16_t*>(&e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if constexpr (std::is_same<T, __half>::value) {
+                    const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                } else {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+            }
         }
     }
 };

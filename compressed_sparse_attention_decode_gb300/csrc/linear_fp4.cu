@@ -4,19 +4,19 @@
 // W is never expanded in memory: 9/16 of a byte per weight is read once per pass
 // over the tokens, and the weights become fp16 in registers.  That is exact: an
 // E2M1 value times an E4M3 scale has at most 6 significant bits and lies in
-// [2^-10, 2688].  x goes to fp16 too, each token (of a group) times the power of
-// two 2^-E that brings its largest magnitude into [2^14, 2^15): fp16 x needs no
-// scale, bf16 x loses only what lies 2^39 below the token's largest value, and
-// fp32 x is split into two fp16 parts (2^-22 of each value).  Products are exact,
-// sums fp32; the epilogue multiplies by alpha and 2^E and rounds once.
+// [2^-10, 2688].  x goes to fp16 too, each token (of a group, or of a 128-value
+// chunk) times the power of two 2^-E that brings its largest magnitude into [2^14,
+// 2^15): fp16 x needs no scale, bf16 x loses only what lies 2^39 below the largest
+// value, and fp32 x is split into two fp16 parts (2^-22 of each value).  Products
+// are exact, sums fp32; y is rounded once.
 //
 // Two kernels:
 //  - k_linear_few (up to 16 tokens): bound by the weight bytes.  mma.sync
 //    m16n8k16, the weights as the A fragments straight from global memory.  The
 //    order of k within a product is free as long as both operands agree, so a
 //    lane takes 16 consecutive bytes of a row (32 weights, two scale groups) and
-//    feeds them, four at a time, to eight products; x lies in shared memory in
-//    the matching order.  The block's 8 warps share rows and inner chunks.
+//    feeds them, four at a time, to eight products, and x comes from global memory
+//    in the matching order.
 //  - k_linear_many: tcgen05, M = 128 rows, N = up to 128 tokens.  Expanded
 //    weights go from registers to TMEM (the A operand), so shared memory carries
 //    the tokens alone: with both operands there, N = 128 would need 192 bytes per
@@ -113,9 +113,8 @@ __device__ __forceinline__ ElemVec<TX, 8> lin_load8(const TX* p, bool vec) {
 
 // ================================================================ up to 16 tokens
 
-constexpr int LF_THREADS = 256, LF_WARPS = 8;
 constexpr int LF_TOK = 16;
-constexpr int LF_SMEM = 200 * 1024;              // the tokens' fp16 parts a block may hold
+constexpr int LF_MAXW = 8;                       // warps of a block
 
 __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -149,125 +148,131 @@ struct LinSeg {
     }
 };
 
-// byte offset of the 16-byte unit j (8 values) of segment c (32 values) of token t in chunk ch (128
-// values): the eight lanes of a quarter warp (two tokens, four segments) hit eight different bank groups
-__device__ __forceinline__ uint32_t lf_unit(int ch, int t, int c, int j, int n_tok) {
-    return (uint32_t)(((ch * n_tok + t) * 4 + c) * 64 + ((j ^ ((t & 1) * 2 + (c >> 1))) << 4));
-}
-
-// NT: token tiles of 8; wk: warps that share a row tile (1, 2, 4 or 8), each taking every wk-th chunk
-template <typename TX, int NT>
-__global__ void __launch_bounds__(LF_THREADS) k_linear_few(const LinArgs a, int wk, int x_vec, int wide) {
+// A block takes R tiles of 16 rows; its warps split n_in in chunks of 128, warp w taking chunks w, w +
+// warps, ..; per chunk a warp holds the tokens' fragments in registers and runs all R tiles over them.
+// Nothing is shared until the warps' sums are joined at the end, in order.
+template <typename TX, int NT, int R>
+__global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a, int x_vec, int wide) {
     extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ unsigned int tmax[LF_TOK];
     constexpr bool SPLIT = sizeof(TX) == 4, SCALED = !std::is_same<TX, __half>::value;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     const int K = a.n_in, T = a.n_tok, g = blockIdx.y;
     const int chunks = (K + 127) / 128;
-    const int rows_block = 16 * (LF_WARPS / wk);
-    const int row_tile = warp / wk, part = warp % wk;
-    const int m0 = blockIdx.x * rows_block + row_tile * 16;
+    const int m0 = blockIdx.x * (16 * R);
     const int r = lane >> 2, c = lane & 3;
-    // rows past the end repeat the last one; their results are not stored
-    const int ra = min(m0 + r, a.n_out - 1), rb = min(m0 + r + 8, a.n_out - 1);
-    const int64_t row0 = (int64_t)g * a.n_out;
-    const uint8_t* ca = a.codes + (row0 + ra) * (K / 2);
-    const uint8_t* cb = a.codes + (row0 + rb) * (K / 2);
-    const uint8_t* sa = a.scales + (row0 + ra) * (K / 16);
-    const uint8_t* sb = a.scales + (row0 + rb) * (K / 16);
+    constexpr int RING = NT == 1 && !SPLIT ? 2 : 2;           // row tile x chunk pieces in flight per warp
+    const int mine = warp < chunks ? (chunks - warp + warps - 1) / warps : 0;      // chunks of this warp
+    const int items = mine * R;
+
     pdl_wait();                                  // x, and weights just quantised, may come from the preceding kernel
-    constexpr int AHEAD = 2;                     // chunks in flight
-    LinSeg wa[AHEAD], wb[AHEAD];
+    LinSeg wa[RING], wb[RING];
+    const uint8_t* codes = a.codes + ((int64_t)g * a.n_out + m0) * (K / 2);
+    const uint8_t* scales = a.scales + ((int64_t)g * a.n_out + m0) * (K / 16);
+    const int last = a.n_out - 1 - m0;           // rows past the end repeat the last one; their results are not stored
+    // piece `it` of this warp: row tile it % R of its chunk it / R
+    auto fetch = [&](int slot, int it, int tile) {
+        const int k = it < items ? (warp + it / R * warps) * 128 + c * 32 : K;
+        const int ra = min(tile * 16 + r, last), rb = min(tile * 16 + r + 8, last);
+        // offsets within the block's rows: 64 rows of at most 2^24 values fit 32 bits
+        wa[slot].load(codes + (uint32_t)ra * (uint32_t)(K / 2), scales + (uint32_t)ra * (uint32_t)(K / 16), k, K, wide);
+        wb[slot].load(codes + (uint32_t)rb * (uint32_t)(K / 2), scales + (uint32_t)rb * (uint32_t)(K / 16), k, K, wide);
+    };
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-        const int k = (part + i * wk) * 128 + c * 32;
-        wa[i].load(ca, sa, k, K, wide);
-        wb[i].load(cb, sb, k, K, wide);
-    }
+    for (int i = 0; i < RING; ++i) fetch(i, i, i % R);
 
-    // ---- the tokens into shared memory (hi part, then for fp32 the lo part)
     const TX* x = reinterpret_cast<const TX*>(a.x) + (int64_t)g * a.x_group;
-    const uint32_t plane = (uint32_t)chunks * T * 256;
-    const int segs = (chunks * 128 + 255) / 256;             // 256 values of one token per warp step
-    if (SCALED) {
-        if (tid < LF_TOK) tmax[tid] = 0u;
-        __syncthreads();
-        for (int u = warp; u < T * segs; u += LF_WARPS) {
-            const int t = u / segs, k = (u - t * segs) * 256 + lane * 8;
-            float m = 0.0f;
-            if (k < K) m = lin_absmax(lin_load8(x + t * a.x_tok + k, x_vec));
-            const unsigned int w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-            if (lane == 0 && w) atomicMax(&tmax[t], w);
-        }
-        __syncthreads();
-    }
-    for (int u = warp; u < T * segs; u += LF_WARPS) {
-        const int t = u / segs, k = (u - t * segs) * 256 + lane * 8;
-        if (k < chunks * 128) {
-            uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-            if (k < K)
-                lin_split(lin_load8(x + t * a.x_tok + k, x_vec), SCALED ? pow2f(-lin_exp(__uint_as_float(tmax[t]))) : 1.0f, hi, lo);
-            const uint32_t at = lf_unit(k >> 7, t, (k >> 5) & 3, (k >> 3) & 3, T);
-            *reinterpret_cast<uint4*>(sm + at) = hi;
-            if (SPLIT) *reinterpret_cast<uint4*>(sm + plane + at) = lo;
-        }
-    }
-    __syncthreads();
-
-    float acc[NT][2][4] = {};                    // two sums per tile: consecutive products do not wait for each other
-    for (int ch0 = part; ch0 < chunks; ch0 += AHEAD * wk) {
+    uint4 bh[NT][4], bl[SPLIT ? NT : 1][4];      // 32 values of token n * 8 + r: this lane's B fragments of a chunk
+    float back[NT][2];                           // 2^E of tokens n * 8 + 2c and + 1
+    auto tokens = [&](int ch) {
+        const int k0 = ch * 128 + c * 32;
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int ch = ch0 + i * wk;
-            if (ch >= chunks) break;
-            const LinSeg va = wa[i], vb = wb[i];
-            {
-                const int k = (ch + AHEAD * wk) * 128 + c * 32;
-                wa[i].load(ca, sa, k, K, wide);
-                wb[i].load(cb, sb, k, K, wide);
+        for (int n = 0; n < NT; ++n) {
+            const int t = n * 8 + r;
+            ElemVec<TX, 8> v[4];
+            float m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (t < T && k0 + 8 * j < K)
+                    v[j] = lin_load8(x + t * a.x_tok + k0 + 8 * j, x_vec);
+                else
+#pragma unroll
+                    for (int i = 0; i < ElemVec<TX, 8>::WORDS; ++i) v[j].w[i] = 0u;
             }
+            float d = 1.0f;
+            if (SCALED) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = fmaxf(m, lin_absmax(v[j]));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const int e = lin_exp(m);
+                d = pow2f(-e);
+                const float up = pow2f(e);       // of token r (of 8); this lane's results are of tokens 2c, 2c + 1
+                back[n][0] = __shfl_sync(0xffffffffu, up, 8 * c);
+                back[n][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 lo;
+                lin_split(v[j], d, bh[n][j], lo);
+                if (SPLIT) bl[n][j] = lo;
+            }
+        }
+    };
+
+    float acc[R][NT][4] = {};
+    constexpr int U = R > RING ? R : RING; // pieces per round: a multiple of R and of the ring
+    for (int it0 = 0; it0 < items; it0 += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int it = it0 + u;
+            if (it >= items) break;
+            if (u % R == 0) tokens(warp + it / R * warps);
+            const LinSeg va = wa[u % RING], vb = wb[u % RING];
+            fetch(u % RING, it + RING, (u + RING) % R);
             const __half2 pa = e4m3x2_to_f16x2(va.s), pb = e4m3x2_to_f16x2(vb.s);
             const uint32_t xa[4] = {va.c.x, va.c.y, va.c.z, va.c.w}, xb[4] = {vb.c.x, vb.c.y, vb.c.z, vb.c.w};
+            float d[NT][2][4] = {};              // two sums: consecutive products do not wait for each other
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const uint4 fa = e2m1x8_scaled(xa[w], w < 2 ? __low2half2(pa) : __high2half2(pa));
                 const uint4 fb = e2m1x8_scaled(xb[w], w < 2 ? __low2half2(pb) : __high2half2(pb));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const int t = n * 8 + r;     // this lane's token of the B fragment
-                    uint4 b = make_uint4(0, 0, 0, 0), bl = b;
-                    if (t < T) {
-                        const uint32_t at = lf_unit(ch, t, c, w, T);
-                        b = *reinterpret_cast<const uint4*>(sm + at);
-                        if (SPLIT) bl = *reinterpret_cast<const uint4*>(sm + plane + at);
-                    }
-                    mma_16816(acc[n][0], fa.x, fb.x, fa.y, fb.y, b.x, b.y);
-                    mma_16816(acc[n][1], fa.z, fb.z, fa.w, fb.w, b.z, b.w);
+                    mma_16816(d[n][0], fa.x, fb.x, fa.y, fb.y, bh[n][w].x, bh[n][w].y);
+                    mma_16816(d[n][1], fa.z, fb.z, fa.w, fb.w, bh[n][w].z, bh[n][w].w);
                     if (SPLIT) {
-                        mma_16816(acc[n][0], fa.x, fb.x, fa.y, fb.y, bl.x, bl.y);
-                        mma_16816(acc[n][1], fa.z, fb.z, fa.w, fb.w, bl.z, bl.w);
+                        mma_16816(d[n][0], fa.x, fb.x, fa.y, fb.y, bl[n][w].x, bl[n][w].y);
+                        mma_16816(d[n][1], fa.z, fb.z, fa.w, fb.w, bl[n][w].z, bl[n][w].w);
                     }
                 }
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v = d[n][0][i] + d[n][1][i];
+                    acc[u % R][n][i] = SCALED ? fmaf(v, back[n][i & 1], acc[u % R][n][i]) : acc[u % R][n][i] + v;
+                }
         }
     }
-    // ---- join the warps of a row tile in order, scale, store with the rows along the lanes
-    __syncthreads();                             // the tokens are read no more
-    float* red = reinterpret_cast<float*>(sm);   // [warp][token][16 rows]
+    // ---- join the warps in order and store with the rows along the lanes
+    float* red = reinterpret_cast<float*>(sm);   // [warp][token][R * 16 rows]
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int tile = 0; tile < R; ++tile)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            red[(warp * NT * 8 + n * 8 + 2 * c + (i & 1)) * 16 + r + 8 * (i >> 1)] = acc[n][0][i] + acc[n][1][i];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = n * 8 + 2 * c + (i & 1);
+                if (t < T) red[(warp * T + t) * (R * 16) + tile * 16 + r + 8 * (i >> 1)] = acc[tile][n][i];
+            }
     __syncthreads();
-    for (int u = tid; u < T * rows_block; u += LF_THREADS) {
-        const int t = u / rows_block, row = u - t * rows_block, m = blockIdx.x * rows_block + row;
+    for (int u = tid; u < T * R * 16; u += blockDim.x) {
+        const int t = u / (R * 16), m = m0 + u % (R * 16);
         if (m >= a.n_out) continue;
         float v = 0.0f;
-        for (int p = 0; p < wk; ++p) v += red[(((row >> 4) * wk + p) * NT * 8 + t) * 16 + (row & 15)];
-        v *= a.alpha;
-        if (SCALED) v *= pow2f(lin_exp(__uint_as_float(tmax[t])));
-        lin_store(a, t, g, m, v);
+        for (int w = 0; w < warps; ++w) v += red[w * T * (R * 16) + u];
+        lin_store(a, t, g, m, v * a.alpha);
     }
     __threadfence();    // the attention may stage these rows as its queries before it waits (see norm_rope.cu)
 }
@@ -545,10 +550,8 @@ int lin_wide(const LinArgs& a) {
 }
 int lin_planes(int x_type) { return x_type == CSA2_F32 ? 2 : 1; }
 
-// up to 16 tokens whose fp16 parts fit a block's shared memory
-bool lin_few(int x_type, int n_tok, int n_in) {
-    return n_tok <= LF_TOK && (int64_t)(n_in + 127) / 128 * n_tok * 256 * lin_planes(x_type) <= LF_SMEM;
-}
+// the few-token kernel: up to 16 tokens, 8 where x has two parts
+bool lin_few(int x_type, int n_tok) { return n_tok <= (x_type == CSA2_F32 ? LF_TOK / 2 : LF_TOK); }
 LinPrep lin_prep(int x_type, int n_tok, int n_in) {
     LinPrep p;
     p.nb = n_tok <= 32 ? 32 : n_tok <= 64 ? 64 : 128;
@@ -558,29 +561,42 @@ LinPrep lin_prep(int x_type, int n_tok, int n_in) {
     return p;
 }
 
-template <typename TX, int NT>
-cudaError_t lf_launch(const LinArgs& a, int x_vec, cudaStream_t st) {
-    // Warps per row tile: until 24 warps per SM have work
-    const int64_t tiles = (int64_t)((a.n_out + 15) / 16) * a.n_groups;
-    const int chunks = (a.n_in + 127) / 128;
-    int wk = 1;
-    while (wk < LF_WARPS && 2 * wk <= chunks && tiles * wk < (int64_t)152 * 3 * LF_WARPS) wk *= 2;
-    const int rows = 16 * (LF_WARPS / wk);
-    const size_t x_bytes = (size_t)chunks * a.n_tok * 256 * (sizeof(TX) == 4 ? 2 : 1);
-    const size_t smem = std::max<size_t>(x_bytes, (size_t)LF_WARPS * NT * 8 * 16 * 4);
-    cudaError_t e = cudaFuncSetAttribute(k_linear_few<TX, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LF_SMEM);
+template <typename TX, int NT, int R>
+cudaError_t lf_launch(const LinArgs& a, int x_vec, int warps, cudaStream_t st) {
+    const size_t smem = (size_t)warps * a.n_tok * R * 16 * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(k_linear_few<TX, NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         LF_MAXW * NT * 8 * R * 16 * (int)sizeof(float));
     if (e != cudaSuccess) return e;
-    launch_k(k_linear_few<TX, NT>, dim3((a.n_out + rows - 1) / rows, a.n_groups), LF_THREADS, smem, st, a, wk, x_vec,
+    launch_k(k_linear_few<TX, NT, R>, dim3((a.n_out + 16 * R - 1) / (16 * R), a.n_groups), warps * 32, smem, st, a, x_vec,
              lin_wide(a) >= 1 ? 1 : 0);
     note_launch();
     return cudaGetLastError();
+}
+template <typename TX, int NT>
+cudaError_t lf_pick(const LinArgs& a, int x_vec, cudaStream_t st) {
+    // Warps: as many as divide the chunks most evenly, up to 8
+    const int chunks = std::max(1, (a.n_in + 127) / 128);
+    int warps = 1;
+    double best = 0.0;
+    for (int w = std::min(chunks, 4); w <= LF_MAXW && w <= chunks; ++w) {
+        const double even = (double)chunks / ((double)w * ((chunks + w - 1) / w));
+        if (even > best + 0.02) best = even, warps = w;
+    }
+    // Row tiles per block: four (the tokens' fragments are made once for all) when that still gives
+    // every SM a block, else one
+    const int64_t tiles = (int64_t)((a.n_out + 15) / 16) * a.n_groups;
+    if (tiles >= 152 * 4) return lf_launch<TX, NT, 4>(a, x_vec, warps, st);
+    return lf_launch<TX, NT, 1>(a, x_vec, warps, st);
 }
 template <typename TX>
 cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st) {
     const int x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_tok * (int64_t)sizeof(TX) % 16 == 0 &&
                       a.x_group * (int64_t)sizeof(TX) % 16 == 0;
-    if (lin_few(x_type, a.n_tok, a.n_in))
-        return a.n_tok <= 8 ? lf_launch<TX, 1>(a, x_vec, st) : lf_launch<TX, 2>(a, x_vec, st);
+    if (lin_few(x_type, a.n_tok)) {
+        if constexpr (sizeof(TX) == 2)
+            if (a.n_tok > 8) return lf_pick<TX, 2>(a, x_vec, st);
+        return lf_pick<TX, 1>(a, x_vec, st);
+    }
     const LinPrep p = lin_prep(x_type, a.n_tok, a.n_in);
     uint8_t* ws = reinterpret_cast<uint8_t*>(wsp);
     launch_k(k_linear_x<TX>, dim3(a.n_tok, a.n_groups), 256, 0, st, a, p, ws + LM_HEAD, x_vec);
@@ -612,7 +628,7 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
 }  // namespace
 
 size_t linear_fp4_ws(int x_type, int n_tok, int n_groups, int n_in) {
-    if (lin_few(x_type, n_tok, n_in)) return 0;
+    if (lin_few(x_type, n_tok)) return 0;
     const LinPrep p = lin_prep(x_type, n_tok, n_in);
     return LM_HEAD + (size_t)p.scales_at(n_groups) + (size_t)n_groups * n_tok * sizeof(float);
 }

@@ -247,8 +247,8 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
  *           strides in elements; y [n_tok][n_groups][n_out] of y_type likewise
  *   codes   uint8 [n_groups][n_out][n_in/2], 16-byte aligned
  *   scales  uint8 [n_groups][n_out][n_in/16]
- * x_type, y_type: CSA2_BF16, CSA2_F16 or CSA2_F32.  n_in a multiple of 16;
- * n_tok, n_in and n_out may be 0 (n_in 0 gives zeros), n_groups <= 65535; x and
+ * x_type, y_type: CSA2_BF16, CSA2_F16 or CSA2_F32.  n_in a multiple of 16,
+ * at most 2^24; * n_tok, n_in and n_out may be 0 (n_in 0 gives zeros), n_groups <= 65535; x and
  * y aligned to their elements; y overlaps no input.  fp16 x enters exactly, bf16
  * x to 2^-39 of the largest value of its token and group, fp32 x to that or 2^-22
  * of the value itself, whichever is more; a NaN scale byte, an infinite or a NaN x
