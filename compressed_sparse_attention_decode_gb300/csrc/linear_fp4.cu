@@ -26,6 +26,8 @@
 #include <algorithm>
 #include <type_traits>
 
+#include <cuda.h>
+
 #include "common.cuh"
 #include "elem.cuh"
 #include "fp4_f16.cuh"
@@ -279,36 +281,50 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
 
 // ================================================================ more tokens
 
-constexpr int LM_THREADS = 320;                  // 8 expanding / epilogue warps, the x copies, the MMAs
-constexpr int LM_M = 128, LM_K = 64;             // rows of a block, values per stage
-constexpr int LM_STAGES = 4;
+constexpr int LM_EXPAND = 16, LM_EPI = 4;        // warps 0-15 expand weights, 16-19 store results,
+constexpr int LM_XW = LM_EXPAND + LM_EPI;        // 20 copies x, 21 copies codes, 22 and 23 issue MMAs
+constexpr int LM_THREADS = (LM_XW + 4) * 32;
+constexpr int LM_M = 128, LM_K = 128;            // rows of a block, values per stage
+constexpr int LM_MAXC = 9;                       // code stages, at most
+constexpr int LM_S = 4;                          // stages: x in shared memory, expanded weights in TMEM (64 columns each)
+constexpr int LM_CK = 2 * LM_K;                  // values per code stage: 128 bytes of each row, whole lines
+constexpr uint32_t LM_CODES = LM_M * LM_CK / 2;  // bytes of codes of a stage
 
 struct LinPrep {                                 // the workspace's layout
-    int nb, tiles, chunks, planes;               // tokens per tile, token tiles, 64-value chunks, fp16 parts
-    __host__ __device__ int64_t tile_bytes() const { return (int64_t)nb * 128; }
-    // [group][token tile][chunk][part] tiles of nb rows x 64 values in the MMA's swizzled layout
-    __host__ __device__ int64_t tile(int g, int tt, int ch, int p) const {
-        return ((((int64_t)g * tiles + tt) * chunks + ch) * planes + p) * tile_bytes();
+    int nb, tiles, chunks, planes;               // tokens per tile, token tiles, 128-value chunks, fp16 parts
+    __host__ __device__ int64_t half_bytes() const { return (int64_t)nb * 128; }
+    __host__ __device__ int64_t stage_bytes() const { return half_bytes() * 2 * planes; }
+    // [group][token tile][chunk][part][half chunk] tiles of nb rows x 64 values in the MMA's swizzled layout
+    __host__ __device__ int64_t stage(int g, int tt, int ch) const {
+        return (((int64_t)g * tiles + tt) * chunks + ch) * stage_bytes();
     }
-    __host__ __device__ int64_t scales_at(int groups) const { return (int64_t)groups * tiles * chunks * planes * tile_bytes(); }
+    __host__ __device__ int64_t scales_at(int groups) const { return (int64_t)groups * tiles * chunks * stage_bytes(); }
 };
 
 // one block per token and group: its scale, and its values in the layout above
 template <typename TX>
 __global__ void __launch_bounds__(256) k_linear_x(const LinArgs a, LinPrep p, uint8_t* __restrict__ ws, int x_vec) {
     constexpr bool SPLIT = sizeof(TX) == 4, SCALED = !std::is_same<TX, __half>::value;
+    constexpr int KEEP = SCALED ? 2 : 1;         // pieces of 2,048 values that stay in registers between the passes
     __shared__ unsigned int tmax;
-    pdl_wait();
-    pdl_launch_next();                           // the product's blocks start expanding weights meanwhile
     const int t = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
     const TX* x = reinterpret_cast<const TX*>(a.x) + t * a.x_tok + (int64_t)g * a.x_group;
+    if (SCALED && tid == 0) tmax = 0u;
+    pdl_wait();
+    pdl_launch_next();                           // the product's blocks start expanding weights meanwhile
+    ElemVec<TX, 8> v[KEEP];
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        if (tid * 8 + i * 2048 < a.n_in) v[i] = lin_load8(x + tid * 8 + i * 2048, x_vec);
     float d = 1.0f;
     float* scale = reinterpret_cast<float*>(ws + p.scales_at(a.n_groups)) + (int64_t)g * a.n_tok + t;
     if (SCALED) {
-        if (tid == 0) tmax = 0u;
         __syncthreads();
-        float m = 0.0f;
-        for (int k = tid * 8; k < a.n_in; k += 2048) m = fmaxf(m, lin_absmax(lin_load8(x + k, x_vec)));
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+            if (tid * 8 + i * 2048 < a.n_in) m = fmaxf(m, lin_absmax(v[i]));
+        for (int k = tid * 8 + KEEP * 2048; k < a.n_in; k += 2048) m = fmaxf(m, lin_absmax(lin_load8(x + k, x_vec)));
         const unsigned int w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
         if ((tid & 31) == 0 && w) atomicMax(&tmax, w);
         __syncthreads();
@@ -319,15 +335,25 @@ __global__ void __launch_bounds__(256) k_linear_x(const LinArgs a, LinPrep p, ui
         *scale = 1.0f;
     }
     const int tt = t / p.nb, r = t - tt * p.nb;
-    for (int k = tid * 8; k < p.chunks * LM_K; k += 2048) {
+    auto put = [&](int k, const ElemVec<TX, 8>& e) {
         uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-        if (k < a.n_in) lin_split(lin_load8(x + k, x_vec), d, hi, lo);
-        const int64_t at = p.tile(g, tt, k >> 6, 0) + r * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(ws + at) = hi;
-        if (SPLIT) *reinterpret_cast<uint4*>(ws + at + p.tile_bytes()) = lo;
-    }
+        if (k < a.n_in) lin_split(e, d, hi, lo);
+        uint8_t* at = ws + p.stage(g, tt, k >> 7) + ((k >> 6) & 1) * p.half_bytes() + r * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = hi;
+        if (SPLIT) *reinterpret_cast<uint4*>(at + 2 * p.half_bytes()) = lo;
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        if (tid * 8 + i * 2048 < p.chunks * LM_K) put(tid * 8 + i * 2048, v[i]);
+    for (int k = tid * 8 + KEEP * 2048; k < p.chunks * LM_K; k += 2048)
+        put(k, k < a.n_in ? lin_load8(x + k, x_vec) : v[0]);
 }
 
+__device__ __forceinline__ bool umma_elect() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+    return p != 0;
+}
 // D[tmem] += A[tmem: 128 rows x 16 fp16, two per column] . B[smem]
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -346,187 +372,367 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+// a box of the codes (128 bytes of 128 rows) at byte column x (a multiple of 64) and row y
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(mbar)
+        : "memory");
+}
 
-// 64 weights of one row: 32 bytes of codes, four scales
+// the four scales of 64 weights of one row from k on; zeros from n_in on
+__device__ __forceinline__ uint32_t lin_scales4(const uint8_t* __restrict__ s, int k, int n_in, int wide) {
+    if (k >= n_in) return 0u;
+    if (wide == 2) return __ldg(reinterpret_cast<const uint32_t*>(s + k / 16));
+    uint32_t v = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (k + 16 * i < n_in) v |= (uint32_t)__ldg(s + k / 16 + i) << (8 * i);
+    return v;
+}
+// 64 weights of one row: 32 bytes of codes
 struct LinSeg64 {
     uint4 c[2];
-    uint32_t s;
-    __device__ __forceinline__ void load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int k,
-                                         int n_in, int wide) {
-        c[0] = c[1] = make_uint4(0, 0, 0, 0);
-        s = 0u;
-        if (k >= n_in) return;
-        if (wide == 2) {                         // n_in a multiple of 64
-            c[0] = __ldg(reinterpret_cast<const uint4*>(codes + k / 2));
-            c[1] = __ldg(reinterpret_cast<const uint4*>(codes + k / 2) + 1);
-            s = __ldg(reinterpret_cast<const uint32_t*>(scales + k / 16));
-        } else {
-            LinSeg h;
-            h.load(codes, scales, k, n_in, wide == 1);
-            c[0] = h.c, s = h.s;
-            h.load(codes, scales, k + 32, n_in, wide == 1);
-            c[1] = h.c, s |= h.s << 16;
+    __device__ __forceinline__ void load(const uint8_t* __restrict__ codes, int k, int n_in) {
+        uint2 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = make_uint2(0, 0);
+            if (k + 16 * i < n_in) w[i] = __ldg(reinterpret_cast<const uint2*>(codes + k / 2) + i);
         }
+        c[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+        c[1] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
     }
 };
 
-// grid (row tiles x splits, token tiles, groups); the splits of a row tile form a cluster
-__global__ void __launch_bounds__(LM_THREADS) k_linear_many(const LinArgs a, LinPrep p, const uint8_t* __restrict__ ws,
-                                                            int* __restrict__ err, int splits, int wide) {
+// after a wait that gave up: this thread's copies in flight (the last of `issued` into a ring) land before
+// the block ends
+__device__ __forceinline__ void lin_drain(bool ok, unsigned long long* full, uint32_t stages, uint32_t issued) {
+    if (!ok)
+        for (uint32_t j = issued > stages ? issued - stages : 0; j < issued; ++j)
+            umma::mbar_wait(umma::smem_u32(&full[j % stages]), (j / stages) & 1, 1u << 16);
+}
+
+struct LinRings {
+    int tiles_m, splits, wide, c_stages;
+};
+
+// Tiles (row tile, token tile, group) in that order of change from slow to fast: group, row tile, token
+// tile, so that blocks side by side read the same codes.  Without splits the blocks walk the tiles,
+// the results of one being stored while the next is summed; with splits a cluster takes one tile and
+// its blocks a share of the chunks each.  TMA: the codes come by tensor copies (n_in a multiple of 32:
+// rows a multiple of 16 bytes apart), else by plain loads.
+template <bool TMA>
+__global__ void __launch_bounds__(LM_THREADS, 1)
+    k_linear_many(const __grid_constant__ CUtensorMap tmap, const LinArgs a, LinPrep p, const uint8_t* __restrict__ ws,
+                  int* __restrict__ err, LinRings rg) {
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) unsigned long long b_w[LM_STAGES], b_x[LM_STAGES], b_free[LM_STAGES], b_done;
+    __shared__ __align__(8) unsigned long long b_a[LM_S], b_x[LM_S], b_free[LM_S], b_c[LM_MAXC], b_cfree[LM_MAXC], b_d[2],
+        b_dfree[2];
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tile_m = blockIdx.x / splits, split = blockIdx.x % splits, tt = blockIdx.y, g = blockIdx.z;
-    const int NB = p.nb;
+    const int splits = rg.splits, CS = rg.c_stages, NB = p.nb;
     const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
     uint8_t* sm = dyn + (base - raw);
-    const uint32_t stage_bytes = (uint32_t)(p.tile_bytes() * p.planes);
-    const int ch0 = (int)((int64_t)p.chunks * split / splits), ch1 = (int)((int64_t)p.chunks * (split + 1) / splits);
-    constexpr uint32_t cols = 256, t_a = 128;                    // D: up to 128 columns; A: 4 stages x 32
+    const uint32_t stage_bytes = (uint32_t)p.stage_bytes(), xb = base + (TMA ? CS * LM_CODES : 0u);
+    const int64_t tiles = (int64_t)rg.tiles_m * p.tiles * a.n_groups;
+    const int split = splits > 1 ? blockIdx.x % splits : 0;
+    const int64_t first = blockIdx.x / splits, step = gridDim.x / splits;
+    const int ch0 = (int)((int64_t)p.chunks * split / splits), n = (int)((int64_t)p.chunks * (split + 1) / splits) - ch0;
+    struct Tile {
+        int m, t, g;
+    };
+    auto tile_of = [&](int64_t i) {
+        Tile v;
+        v.t = (int)(i % p.tiles);
+        i /= p.tiles;
+        v.m = (int)(i % rg.tiles_m);
+        v.g = (int)(i / rg.tiles_m);
+        return v;
+    };
+    // TMEM: results in columns 0-255, (buffer, half of K) tiles of NB: two buffers up to 64 tokens, else one;
+    // expanded weights in LM_S x 64 columns from 256 on
+    constexpr uint32_t cols = 512, t_a = 256;
+    const int bufs = NB <= 64 ? 2 : 1;
     auto sa = [&](const void* q) { return umma::smem_u32(q); };
     if (tid == 0) {
-        for (int i = 0; i < LM_STAGES; ++i) {
-            umma::mbar_init(sa(&b_w[i]), 4);                     // the four lane quarters of the stage's weights
+        for (int i = 0; i < LM_S; ++i) {
+            umma::mbar_init(sa(&b_a[i]), 8);                     // four lane quarters x two halves of a chunk
             umma::mbar_init(sa(&b_x[i]), 1);
-            umma::mbar_init(sa(&b_free[i]), 1);
+            umma::mbar_init(sa(&b_free[i]), 2);                  // both MMA issuers
         }
-        umma::mbar_init(sa(&b_done), 1);
+        for (int i = 0; i < LM_MAXC; ++i) {
+            umma::mbar_init(sa(&b_c[i]), 1);
+            umma::mbar_init(sa(&b_cfree[i]), LM_EXPAND);
+        }
+        for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(sa(&b_d[i]), 2);
+            umma::mbar_init(sa(&b_dfree[i]), LM_EPI);
+        }
         umma::fence_mbar_init();
     }
-    if (warp == 0) umma::tmem_alloc(sa(&tmem_base), cols);
-    umma::fence_before();
+    if (TMA && warp == LM_XW + 1 && lane == 0)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
     __syncthreads();
-    umma::fence_after();
-    const uint32_t tmem = tmem_base;
+    // the copies start at once; whoever touches TMEM meets here after its allocation
+    uint32_t tmem = 0;
+    auto tmem_ready = [&]() {
+        umma::fence_before();
+        umma::bar_named(1, LM_THREADS - 64);
+        umma::fence_after();
+        tmem = tmem_base;
+    };
     bool ok = true;
-    const int n = ch1 - ch0;
-
-    if (warp < 8) {
-        // ================= weights: warp w takes rows 32(w%4) .. +31 of the tile, chunks of parity w/4.
-        // Only x and its scales come from the kernel before this one, so nothing waits here.
-        const int q = warp & 3, par = warp >> 2;
-        const int m = min(tile_m * LM_M + q * 32 + lane, a.n_out - 1);
-        const int64_t row = (int64_t)g * a.n_out + m;
-        const uint8_t* cr = a.codes + row * (a.n_in / 2);
-        const uint8_t* sr = a.scales + row * (a.n_in / 16);
-        constexpr int AHEAD = 3;
-        LinSeg64 seg[AHEAD];
+    const int my_tiles = first < tiles ? (int)((tiles - first + step - 1) / step) : 0;
+    // Results of tile ti: this warp's lane quarter (rows along the lanes), token columns 16 (part + i * parts),
+    // both halves of K added.  With splits, to this block's shared memory as [token][128 rows].
+    auto store = [&](int ti, int part, int parts) {
+        const Tile v = tile_of(first + ti * step);
+        const int q = warp & 3, buf = ti % bufs, m = v.m * LM_M + q * 32 + lane, t0 = v.t * NB, nt = min(NB, a.n_tok - t0);
+        const float* scale = reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)v.g * a.n_tok + t0;
+        float* mine = reinterpret_cast<float*>(sm);
+        const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + 2 * buf * NB;
+        float f[16];
+        auto scales = [&](int c) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int j = par + 2 * i;
-            seg[i].load(cr, sr, j < n ? (ch0 + j) * LM_K : a.n_in, a.n_in, wide);
+            for (int i = 0; i < 16; ++i) f[i] = c + i < nt ? scale[c + i] * a.alpha : 0.0f;
+        };
+        if (splits == 1) scales(16 * part);                      // in flight while the sums are waited for
+        if (n > 0) ok = ok && umma::mbar_wait_fast(sa(&b_d[buf]), (ti / bufs) & 1);
+        umma::fence_after();
+        for (int c = 16 * part; c < nt; c += 16 * parts) {
+            float r[16], r1[16];
+            umma::tmem_ld16(d + c, r);
+            umma::tmem_ld16(d + NB + c, r1);
+            umma::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = ok ? (n > 0 ? r[i] + r1[i] : 0.0f) : __int_as_float(0x7fc00000);
+            if (splits > 1) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) mine[(c + i) * LM_M + q * 32 + lane] = r[i];
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] *= f[i];
+            if (c + 16 * parts < nt) scales(c + 16 * parts);
+            if (m < a.n_out) {
+                const int64_t y0 = (int64_t)(t0 + c) * a.y_tok + v.g * a.y_group + m;
+                auto put = [&](auto* y) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < nt) y[y0 + i * a.y_tok] = from_f32<std::remove_pointer_t<decltype(y)>>(r[i]);
+                };
+                if (a.y_type == CSA2_BF16)
+                    put(reinterpret_cast<__nv_bfloat16*>(a.y));
+                else if (a.y_type == CSA2_F16)
+                    put(reinterpret_cast<__half*>(a.y));
+                else
+                    put(reinterpret_cast<float*>(a.y));
+            }
         }
-        for (int j0 = par; j0 < n; j0 += 2 * AHEAD) {
+        umma::fence_before();
+    };
+
+    if (warp < LM_EXPAND) {
+        // ================= weights: warp w takes rows 32(w%4) .. +31 of the tile, half (w/4)%2 of a chunk and
+        // every second chunk.  Only x and its scales come from the kernel before this one: nothing waits here.
+        const int q = warp & 3, hf = (warp >> 2) & 1, par = warp >> 3, rt = q * 32 + lane;
+        const uint8_t *cr = nullptr, *sr = nullptr;
+        const int pairs = (n + 1) / 2;                           // of a tile's chunks; a code stage holds a pair
+        const int total = my_tiles * pairs;
+        constexpr int AHEAD = TMA ? 4 : 2;                       // own chunks whose scales (and plain codes) are in flight
+        LinSeg64 seg[TMA ? 1 : AHEAD];
+        uint32_t sc[AHEAD];
+        int at = 0, ai = 0;                                      // tile and pair to load next
+        auto ahead = [&](int i) {
+            int k = a.n_in;
+            if (at < my_tiles) {
+                if (ai == 0) {
+                    const Tile v = tile_of(first + at * step);
+                    const int64_t row = (int64_t)v.g * a.n_out + min(v.m * LM_M + rt, a.n_out - 1);
+                    cr = a.codes + row * (a.n_in / 2);
+                    sr = a.scales + row * (a.n_in / 16);
+                }
+                if (2 * ai + par < n) k = (ch0 + 2 * ai + par) * LM_K + hf * 64;
+                if (++ai == pairs) ai = 0, ++at;
+            }
+            sc[i] = lin_scales4(sr, k, a.n_in, rg.wide);
+            if constexpr (!TMA) seg[i].load(cr, k, a.n_in);
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (total > 0) ahead(i);
+        uint4 c[2];
+        int cs = 0, cph = 0;                                     // code stage of the pair in c, and its phase
+        auto take = [&](int stage) {
+            const uint8_t* src = sm + stage * LM_CODES + rt * 128;
+            const int u = par * 4 + hf * 2;
+            c[0] = *reinterpret_cast<const uint4*>(src + ((u ^ (rt & 7)) << 4));
+            c[1] = *reinterpret_cast<const uint4*>(src + (((u + 1) ^ (rt & 7)) << 4));
+        };
+        if (TMA && total > 0) {
+            ok = ok && umma::mbar_wait_fast(sa(&b_c[0]), 0);
+            take(0);
+        }
+        tmem_ready();
+        int j = par;                                             // chunk within the tile
+        uint32_t it = par;                                       // and among the block's
+        for (int p0 = 0; p0 < total; p0 += AHEAD) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
-                const int j = j0 + 2 * i;
-                if (j >= n) break;
-                const LinSeg64 v = seg[i];
-                {
-                    const int jn = j + 2 * AHEAD;
-                    seg[i].load(cr, sr, jn < n ? (ch0 + jn) * LM_K : a.n_in, a.n_in, wide);
-                }
+                if (p0 + i >= total) break;
+                // the barriers that this round waits for are asked first, so that their answers (and the next
+                // codes) arrive behind the arithmetic
+                const uint32_t st = it % LM_S;
+                const bool more = TMA && p0 + i + 1 < total;
+                const int ncs = cs + 1 == CS ? 0 : cs + 1, ncph = cph ^ (ncs == 0);
+                const bool c_there = more && umma::mbar_test(sa(&b_c[ncs]), ncph);
+                const bool st_free = it < LM_S || umma::mbar_test(sa(&b_free[st]), (it / LM_S - 1) & 1);
+                const uint32_t s4 = sc[i];
+                if constexpr (!TMA) c[0] = seg[TMA ? 0 : i].c[0], c[1] = seg[TMA ? 0 : i].c[1];
+                ahead(i);
                 uint32_t o[32];
-                const __half2 s01 = e4m3x2_to_f16x2(v.s & 0xffffu), s23 = e4m3x2_to_f16x2(v.s >> 16);
-                const __half2 sc[4] = {__low2half2(s01), __high2half2(s01), __low2half2(s23), __high2half2(s23)};
+                const __half2 s01 = e4m3x2_to_f16x2(s4 & 0xffffu), s23 = e4m3x2_to_f16x2(s4 >> 16);
+                const __half2 f4[4] = {__low2half2(s01), __high2half2(s01), __low2half2(s23), __high2half2(s23)};
 #pragma unroll
                 for (int w = 0; w < 8; ++w) {
-                    const uint4& cc = v.c[w >> 2];
+                    const uint4& cc = c[w >> 2];
                     const uint32_t word = (w & 3) == 0 ? cc.x : (w & 3) == 1 ? cc.y : (w & 3) == 2 ? cc.z : cc.w;
-                    const uint4 f = e2m1x8_scaled(word, sc[w >> 1]);
+                    const uint4 f = e2m1x8_scaled(word, f4[w >> 1]);
                     o[4 * w] = f.x, o[4 * w + 1] = f.y, o[4 * w + 2] = f.z, o[4 * w + 3] = f.w;
                 }
-                const int st = j % LM_STAGES;
-                if (j >= LM_STAGES) {
-                    ok = ok && umma::mbar_wait_fast(sa(&b_free[st]), (j / LM_STAGES - 1) & 1);
-                    umma::fence_after();
+                if constexpr (TMA) {
+                    __syncwarp();                                // every lane has its codes in registers
+                    if (lane == 0) umma::mbar_arrive(sa(&b_cfree[cs]));
+                    if (more) {
+                        if (!c_there) ok = ok && umma::mbar_wait(sa(&b_c[ncs]), ncph);
+                        take(ncs);
+                    }
+                    cs = ncs, cph = ncph;
                 }
-                tmem_st32(tmem + ((uint32_t)(q * 32) << 16) + t_a + 32 * st, o);
-                umma::tmem_wait_st();
-                umma::fence_before();
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive(sa(&b_w[st]));
+                if (j < n) {
+                    if (!st_free) ok = ok && umma::mbar_wait(sa(&b_free[st]), (it / LM_S - 1) & 1);
+                    if (it >= LM_S) umma::fence_after();
+                    tmem_st32(tmem + ((uint32_t)(q * 32) << 16) + t_a + 64 * st + 32 * hf, o);
+                    umma::tmem_wait_st();
+                    umma::fence_before();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(sa(&b_a[st]));
+                }
+                j += 2, it += 2;
+                if (j >= 2 * pairs) j -= 2 * pairs, it -= 2 * pairs - n;
             }
         }
-    } else if (warp == 8) {
-        // ================= x: bulk copies of the prepared tiles
+    } else if (warp < LM_XW) {
+        // ================= results of all tiles but the last, while the next is summed
+        tmem_ready();
+        pdl_wait();                                              // the tokens' scales, and y
+        for (int ti = 0; ti + 1 < my_tiles; ++ti) {
+            store(ti, 0, 1);
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(sa(&b_dfree[ti % bufs]));
+        }
+    } else if (warp == LM_XW) {
+        // ================= x: bulk copies of the prepared stages
         if (lane == 0) {
             pdl_wait();
-            for (int j = 0; j < n; ++j) {
-                const int st = j % LM_STAGES;
-                if (j >= LM_STAGES) ok = ok && umma::mbar_wait_fast(sa(&b_free[st]), (j / LM_STAGES - 1) & 1);
-                if (!ok) break;
-                umma::mbar_arrive_expect_tx(sa(&b_x[st]), stage_bytes);
-                umma::bulk_g2s(base + st * stage_bytes, ws + p.tile(g, tt, ch0 + j, 0), stage_bytes, sa(&b_x[st]));
+            uint32_t it = 0;
+            for (int ti = 0; ti < my_tiles && ok; ++ti) {
+                const Tile v = tile_of(first + ti * step);
+                for (int j = 0; j < n; ++j, ++it) {
+                    const uint32_t st = it % LM_S;
+                    if (it >= LM_S) ok = ok && umma::mbar_wait_fast(sa(&b_free[st]), (it / LM_S - 1) & 1);
+                    if (!ok) break;
+                    umma::mbar_arrive_expect_tx(sa(&b_x[st]), stage_bytes);
+                    umma::bulk_g2s(xb + st * stage_bytes, ws + p.stage(v.g, v.t, ch0 + j), stage_bytes, sa(&b_x[st]));
+                }
             }
+            lin_drain(ok, b_x, LM_S, it);
         }
-    } else if (lane == 0) {
-        // ================= MMAs
-        const uint32_t id = umma::idesc_f16(LM_M, NB, 0, 0);
-        for (int j = 0; j < n; ++j) {
-            const int st = j % LM_STAGES;
-            ok = ok && umma::mbar_wait_fast(sa(&b_w[st]), (j / LM_STAGES) & 1);
-            ok = ok && umma::mbar_wait_fast(sa(&b_x[st]), (j / LM_STAGES) & 1);
-            if (!ok) break;
-            umma::fence_after();
-            for (int pl = 0; pl < p.planes; ++pl) {
-                const uint64_t bd = umma::desc(base + st * stage_bytes + pl * (uint32_t)p.tile_bytes(), 16, 1024, umma::LAYOUT_SW128);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f16_ta(tmem, tmem + t_a + 32 * st + 8 * ks, bd + (uint64_t)((ks * 32) >> 4), id, j > 0 || pl > 0 || ks > 0);
+    } else if (warp == LM_XW + 1) {
+        // ================= codes
+        if (TMA && lane == 0) {
+            int st = 0, ph = 1;                                  // a fresh barrier passes a wait for phase 1
+            uint32_t it = 0;
+            for (int ti = 0; ti < my_tiles && ok; ++ti) {
+                const Tile v = tile_of(first + ti * step);
+                const int y = (int)((int64_t)v.g * a.n_out + v.m * LM_M);
+                for (int j = 0; j < n; j += 2, ++it) {
+                    ok = ok && umma::mbar_wait_fast(sa(&b_cfree[st]), ph);
+                    if (!ok) break;
+                    umma::mbar_arrive_expect_tx(sa(&b_c[st]), LM_CODES);
+                    tma_box(base + st * LM_CODES, &tmap, (ch0 + j) * (LM_K / 2), y, sa(&b_c[st]));
+                    if (++st == CS) st = 0, ph ^= 1;
+                }
             }
-            umma::commit(sa(&b_free[st]));
+            lin_drain(ok, b_c, CS, it);
         }
-        if (ok) umma::commit(sa(&b_done));
-    }
-
-    // ================= epilogue
-    const float* scale = reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)g * a.n_tok;
-    const int t0 = tt * NB, nt = min(NB, a.n_tok - t0);
-    __syncwarp();                                // warps 8 and 9 ran their loops in one lane
-    pdl_wait();                                  // the scales, and y
-    if (warp < 8) {
-        if (n > 0) ok = ok && umma::mbar_wait_fast(sa(&b_done), 0);
-        umma::fence_after();
-    }
-    const int q = warp & 3, m = tile_m * LM_M + q * 32 + lane;
-    const int c0 = (warp >> 2) * (NB / 2);       // this warp's half of the tokens
-    if (splits == 1) {
-        if (warp < 8)
-            for (int c = c0; c < c0 + NB / 2 && c < nt; c += 16) {
-                float v[16];
-                umma::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
-                umma::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c + i < nt && m < a.n_out)
-                        lin_store(a, t0 + c + i, g, m, ok ? (n > 0 ? v[i] : 0.0f) * a.alpha * scale[t0 + c + i] : __int_as_float(0x7fc00000));
-            }
     } else {
-        // this block's sums as [token][128 rows] in its shared memory (its copies are all done and read);
-        // block r of the cluster adds up, in order, and stores every splits-th token
-        float* mine = reinterpret_cast<float*>(sm);
-        if (warp < 8)
-            for (int c = c0; c < c0 + NB / 2; c += 16) {
-                float v[16];
-                umma::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
-                umma::tmem_wait_ld();
+        // ================= MMAs: two issuers, one per half of each chunk (one thread cannot issue fast enough to
+        // fill the tensor cores); a whole warp walks the chunks, so that descriptors and addresses stay in
+        // uniform registers, and one elected lane issues
+        const int hf = warp - (LM_XW + 2);
+        if (hf == 0) umma::tmem_alloc(sa(&tmem_base), cols);
+        tmem_ready();
+        const uint32_t id = umma::idesc_f16(LM_M, NB, 0, 0);
+        const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+        uint32_t it = 0;
+        bool there = false;
+        for (int ti = 0; ti < my_tiles && ok; ++ti) {
+            const int buf = ti % bufs;
+            if (ti >= bufs) ok = ok && umma::mbar_wait_fast(sa(&b_dfree[buf]), (ti / bufs - 1) & 1);
+            for (int j = 0; j < n && ok; ++j, ++it) {
+                const uint32_t st = it % LM_S, ph = (it / LM_S) & 1;
+                if (!there) ok = ok && umma::mbar_wait_fast(sa(&b_x[st]), ph) && umma::mbar_wait_fast(sa(&b_a[st]), ph);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                // asked while this chunk's products are issued
+                const uint32_t nst = (it + 1) % LM_S, nph = ((it + 1) / LM_S) & 1;
+                const bool nx = umma::mbar_test(sa(&b_x[nst]), nph), na = umma::mbar_test(sa(&b_a[nst]), nph);
+                umma::fence_after();
+                if (umma_elect()) {
+                    for (int pl = 0; pl < p.planes; ++pl) {
+                        const uint64_t bd = umma::desc(xb + st * stage_bytes + (2 * pl + hf) * (uint32_t)p.half_bytes(), 16, 1024, umma::LAYOUT_SW128);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    mine[(c + i) * LM_M + q * 32 + lane] = ok ? (n > 0 ? v[i] : 0.0f) : __int_as_float(0x7fc00000);
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16_ta(tm + (2 * buf + hf) * NB, tm + t_a + 64 * st + 32 * hf + 8 * ks, bd + (uint64_t)((ks * 32) >> 4),
+                                       id, j > 0 || pl > 0 || ks > 0);
+                    }
+                    umma::commit(sa(&b_free[st]));
+                    if (j == n - 1) umma::commit(sa(&b_d[buf]));
+                }
+                __syncwarp();
+                there = __all_sync(0xffffffffu, nx && na);
             }
+        }
+    }
+    __syncwarp();                                // two warps ran their loops in one lane
+    // The last tile's results: by twenty warps where the expanding ones cannot take an older phase of its
+    // barrier for this one's: in the barrier's first phase, or when their last chunks waited for products of
+    // this very tile
+    const bool wide = my_tiles <= bufs || n >= LM_S + 2;
+    if (my_tiles > 0 && warp < LM_XW && (wide || warp >= LM_EXPAND)) {
+        pdl_wait();
+        store(my_tiles - 1, wide ? warp >> 2 : 0, wide ? LM_XW / 4 : 1);
+    }
+    if (splits > 1) {
+        // block r of the cluster adds the splits up, in order, and stores every splits-th token
+        pdl_wait();
+        const Tile v = tile_of(first);
+        const int t0 = v.t * NB, nt = min(NB, a.n_tok - t0);
+        const float* mine = reinterpret_cast<const float*>(sm);
+        const float* scale = reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)v.g * a.n_tok + t0;
         umma::cluster_sync();
         for (int u = tid; u < ((nt - split + splits - 1) / splits) * LM_M; u += LM_THREADS) {
             const int c = split + (u / LM_M) * splits, row = u % LM_M;
-            float v = 0.0f;
+            float x = 0.0f;
             for (int s = 0; s < splits; ++s) {
                 float w;
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(umma::mapa(sa(mine + c * LM_M + row), s)));
-                v += w;
+                x += w;
             }
-            const int mm = tile_m * LM_M + row;
-            if (mm < a.n_out) lin_store(a, t0 + c, g, mm, v * a.alpha * scale[t0 + c]);
+            const int m = v.m * LM_M + row;
+            if (m < a.n_out) lin_store(a, t0 + c, v.g, m, x * a.alpha * scale[c]);
         }
         umma::cluster_sync();                    // no block leaves while another reads its sums
     }
@@ -534,10 +740,26 @@ __global__ void __launch_bounds__(LM_THREADS) k_linear_many(const LinArgs a, Lin
     __threadfence();
     umma::fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == LM_XW + 2) {
         umma::fence_after();
         umma::tmem_dealloc(tmem, cols);
     }
+}
+
+// cuTensorMapEncodeTiled from the driver, looked up once through the runtime (no link to libcuda)
+typedef CUresult (*LinEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static LinEncodeFn lin_encode() {
+    static const LinEncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<LinEncodeFn>(p);
+    }();
+    return fn;
 }
 
 namespace {
@@ -554,7 +776,7 @@ int lin_planes(int x_type) { return x_type == CSA2_F32 ? 2 : 1; }
 bool lin_few(int x_type, int n_tok) { return n_tok <= (x_type == CSA2_F32 ? LF_TOK / 2 : LF_TOK); }
 LinPrep lin_prep(int x_type, int n_tok, int n_in) {
     LinPrep p;
-    p.nb = n_tok <= 32 ? 32 : n_tok <= 64 ? 64 : 128;
+    p.nb = n_tok <= 32 ? 32 : n_tok <= 64 || x_type == CSA2_F32 ? 64 : 128;
     p.tiles = (n_tok + p.nb - 1) / p.nb;
     p.chunks = (n_in + LM_K - 1) / LM_K;
     p.planes = lin_planes(x_type);
@@ -600,16 +822,31 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     const LinPrep p = lin_prep(x_type, a.n_tok, a.n_in);
     uint8_t* ws = reinterpret_cast<uint8_t*>(wsp);
     launch_k(k_linear_x<TX>, dim3(a.n_tok, a.n_groups), 256, 0, st, a, p, ws + LM_HEAD, x_vec);
-    // Splits of n_in: while the row and token tiles leave SMs idle and a split keeps eight chunks
+    // Splits of n_in: while the row and token tiles leave SMs idle and a split keeps four chunks
     const int tiles_m = (a.n_out + LM_M - 1) / LM_M;
-    const int64_t blocks = (int64_t)tiles_m * p.tiles * a.n_groups;
-    int splits = 1;
-    while (splits < 8 && blocks * splits * 2 <= 152 && p.chunks >= splits * 2 * 8) splits *= 2;
-    const size_t smem = std::max<size_t>((size_t)LM_STAGES * p.tile_bytes() * p.planes, splits > 1 ? (size_t)p.nb * LM_M * 4 : 0) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(k_linear_many, cudaFuncAttributeMaxDynamicSharedMemorySize, 132 * 1024);
+    const int64_t tiles = (int64_t)tiles_m * p.tiles * a.n_groups;
+    LinRings rg{tiles_m, 1, lin_wide(a), 0};
+    while (rg.splits < 8 && tiles * rg.splits * 2 <= 152 && p.chunks >= rg.splits * 2 * 4) rg.splits *= 2;
+    // code stages: what the token ring leaves (a tensor copy lands about 2 us after its issue)
+    rg.c_stages = (int)std::min<int64_t>(LM_MAXC, (224 * 1024 - LM_S * p.stage_bytes()) / LM_CODES);
+    const bool tma = a.n_in % 32 == 0 && a.n_in > 0 && (int64_t)a.n_groups * a.n_out <= 0x7fffffff && lin_encode() != nullptr;
+    CUtensorMap tm = {};
+    if (tma) {
+        const cuuint64_t dims[2] = {(cuuint64_t)(a.n_in / 2), (cuuint64_t)a.n_groups * (cuuint64_t)a.n_out};
+        const cuuint64_t strides[1] = {(cuuint64_t)(a.n_in / 2)};
+        const cuuint32_t box[2] = {LM_CK / 2, LM_M}, estr[2] = {1, 1};
+        if (lin_encode()(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.codes), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const auto kern = tma ? k_linear_many<true> : k_linear_many<false>;
+    const size_t smem = std::max<size_t>((tma ? rg.c_stages * (size_t)LM_CODES : 0) + (size_t)LM_S * p.stage_bytes(),
+                                         rg.splits > 1 ? (size_t)p.nb * LM_M * 4 : 0) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles_m * splits, p.tiles, a.n_groups);
+    cfg.gridDim = dim3((unsigned)(rg.splits > 1 ? tiles * rg.splits : std::min<int64_t>(tiles, 152)));
     cfg.blockDim = dim3(LM_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -617,11 +854,10 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = splits, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.x = rg.splits, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, k_linear_many, a, p, (const uint8_t*)(ws + LM_HEAD), reinterpret_cast<int*>(ws), splits,
-                           lin_wide(a));
+    e = cudaLaunchKernelEx(&cfg, kern, tm, a, p, (const uint8_t*)(ws + LM_HEAD), reinterpret_cast<int*>(ws), rg);
     note_launch(2);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
