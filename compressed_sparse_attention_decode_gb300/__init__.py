@@ -13,6 +13,7 @@ plus ``Cache``, which owns the four cache planes as torch tensors.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -46,6 +47,10 @@ class _HeadRows(ctypes.Structure):
                 ("y_head", ctypes.c_int64), ("n_heads", ctypes.c_int32)]
 
 
+# the two structures as bytes: a call packs them in a fraction of the time that a ctypes object takes
+_PACK_ROWS = struct.Struct("@PPPqqqqi4x").pack
+_PACK_CACHE = struct.Struct("@PPPPiiiii4x").pack
+
 _lib = None
 EXPORTS = ("csa2_cache_write", "csa2_quantize_fp4", "csa2_indexer_topk", "csa2_reindex", "csa2_sparse_attn",
            "csa2_workspace_size", "csa2_status_string", "csa2_abi_version", "csa2_launch_count",
@@ -74,9 +79,8 @@ def load(path=None):
     lib.csa2_sparse_attn.argtypes = [cp, vp, i32, i32, vp, vp, i32, vp, i64, i32, ctypes.c_float, vp, vp, vp, sz, vp]
     lib.csa2_linear_fp4.argtypes = [vp, i32, i64, i64, i32, i32, i32, i32, vp, vp, ctypes.c_float, vp, i32, i64,
                                     i64, vp, sz, vp]
-    hp = ctypes.POINTER(_HeadRows)
-    lib.csa2_norm_rope.argtypes = [hp, hp, i32, i32, i32, i32, i32, vp, vp, ctypes.c_float, i32, vp]
-    lib.csa2_dense_attn.argtypes = [cp, vp, i32, i32, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, sz, vp]
+    lib.csa2_norm_rope.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, ctypes.c_float, i32, vp]
+    lib.csa2_dense_attn.argtypes = [vp, vp, i32, i32, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, sz, vp]
     lib.csa2_reindex_noalloc.argtypes = [cp, vp, vp, vp, i32, i32, vp, i32, i32, vp, vp]
     lib.csa2_reindex_noalloc.restype = ctypes.c_int
     lib.csa2_poll_error.argtypes = [vp, sz, vp]
@@ -316,41 +320,52 @@ def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, ws=No
     x [T, G, n_in] with codes [G, n_out, n_in/2] and scales [G, n_out, n_in/16] (a product per group).
     Rows of x and out are contiguous, their other strides free.  Returns [T, n_out] or [T, G, n_out]
     of out_dtype (default: that of x)."""
-    n_in, n_out = x.shape[-1], codes.shape[-2]
-    grouped = x.dim() == 3
-    _need(x.dim() in (2, 3) and codes.dim() == x.dim() and scales.dim() == x.dim(), "x, codes and scales: 2 or 3 dims each")
-    G = x.shape[1] if grouped else 1
-    _need(n_in % 16 == 0 and codes.shape[-1] * 2 == n_in and scales.shape[-1] * 16 == n_in
-          and scales.shape[-2] == n_out and (not grouped or (codes.shape[0] == G and scales.shape[0] == G)),
+    xs, ms = x.shape, codes.shape
+    if len(xs) == 2:
+        (T, n_in), G, lead, x_group = xs, 1, 0, 0
+    else:
+        _need(len(xs) == 3, "x: [T, n_in] or [T, G, n_in]")
+        T, G, n_in = xs
+        lead, x_group = 1, x.stride(1)
+    _need(len(ms) == lead + 2, "codes: as many leading dims as x has groups")
+    n_out = ms[-2]
+    _need(n_in % 16 == 0 and ms[-1] * 2 == n_in and scales.shape == ms[:-1] + (n_in // 16,) and (not lead or ms[0] == G),
           "codes [.., n_out, n_in/2] and scales [.., n_out, n_in/16] of x [.., n_in], n_in a multiple of 16")
-    _need(codes.dtype == scales.dtype == torch.uint8 and codes.is_contiguous() and scales.is_contiguous(),
+    _need(codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_contiguous() and scales.is_contiguous(),
           "codes and scales: contiguous uint8")
     if out is None:
-        out = torch.empty(x.shape[:-1] + (n_out,), dtype=out_dtype or x.dtype, device=x.device)
-    _need(out.shape[:-1] == x.shape[:-1] and out.shape[-1] == n_out and (out_dtype is None or out.dtype == out_dtype),
-          "out [.., n_out] with the leading sizes of x")
-    _need(x.dtype in _TYPES and out.dtype in _TYPES, "x and out: bf16, fp16 or fp32")
-    _need((x.stride(-1) == 1 or n_in == 0) and (out.stride(-1) == 1 or n_out <= 1), "rows of x and out: contiguous")
-    lib, T, x_type = load(), x.shape[0], _TYPES[x.dtype]
+        out = torch.empty(xs[:-1] + (n_out,), dtype=out_dtype or x.dtype, device=x.device)
+    else:
+        _need(out.shape == xs[:-1] + (n_out,) and (out_dtype is None or out.dtype is out_dtype),
+              "out [.., n_out] with the leading sizes of x")
+    x_type, y_type = _TYPES.get(x.dtype), _TYPES.get(out.dtype)
+    _need(x_type is not None and y_type is not None, "x and out: bf16, fp16 or fp32")
+    _need((x.stride(-1) == 1 or n_in == 0) and (n_out <= 1 or out.stride(-1) == 1), "rows of x and out: contiguous")
+    lib = load()
     if ws is None:
-        n = lib.csa2_workspace_size(OP_LINEAR_FP4, T, G, x_type, 0, n_in)
+        n = lib.csa2_workspace_size(OP_LINEAR_FP4, T, G, x_type, 0, n_in) if T > 8 else 0     # none for so few tokens
         ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-    st = lib.csa2_linear_fp4(x.data_ptr(), x_type, x.stride(0), x.stride(1) if grouped else 0, T, G, n_in, n_out,
-                             codes.data_ptr(), scales.data_ptr(), alpha, out.data_ptr(), _TYPES[out.dtype], out.stride(0),
-                             out.stride(1) if grouped else 0, None if ws is None else ws.data_ptr(),
-                             0 if ws is None else ws.numel(), _stream(stream))
-    _check(st, "csa2_linear_fp4")
+    st = lib.csa2_linear_fp4(x.data_ptr(), x_type, x.stride(0), x_group, T, G, n_in, n_out, codes.data_ptr(),
+                             scales.data_ptr(), alpha, out.data_ptr(), y_type, out.stride(0), out.stride(1) if lead else 0,
+                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _stream(stream))
+    if st:
+        raise Csa2Error(st, "csa2_linear_fp4")
     return out
 
 
 def _head_rows(x, weight, out, T, d, name):
-    _need(x.dim() == 3 and x.shape[0] == T and x.shape[2] == d and out.shape == x.shape,
-          "%s and its output: [T, heads, d]" % name)
-    _need(x.stride(2) == 1 and out.stride(2) == 1, "rows of %s and its output: contiguous" % name)
-    _need(weight is None or (weight.dtype == torch.float32 and weight.shape == (d,) and weight.is_contiguous()),
-          "%s_weight: contiguous fp32 [d]" % name)
-    return _HeadRows(x.data_ptr(), out.data_ptr(), 0 if weight is None else weight.data_ptr(), x.stride(0), x.stride(1),
-                     out.stride(0), out.stride(1), x.shape[1])
+    xs = x.shape
+    _need(len(xs) == 3 and xs[0] == T and xs[2] == d and out.shape == xs, "%s and its output: [T, heads, d]" % name)
+    x0, x1, x2 = x.stride()
+    y0, y1, y2 = out.stride()
+    _need(x2 == 1 and y2 == 1, "rows of a head set and its output: contiguous")
+    if weight is None:
+        w = 0
+    else:
+        _need(weight.dtype is torch.float32 and weight.shape == (d,) and weight.is_contiguous(),
+              "weights: contiguous fp32 [d]")
+        w = weight.data_ptr()
+    return _PACK_ROWS(x.data_ptr(), out.data_ptr(), w, x0, x1, y0, y1, xs[1])
 
 
 def csa2_norm_rope(q, pos, inv_freq, q_weight=None, k=None, k_weight=None, eps=1e-6, norm=True, halves=False,
@@ -360,11 +375,15 @@ def csa2_norm_rope(q, pos, inv_freq, q_weight=None, k=None, k_weight=None, eps=1
     turns back, halves=True pairs value i with i + d_rot/2 (default: 2i with 2i+1).  pos and inv_freq
     may both be None (no rotation).  bf16 / fp16 / fp32, rows contiguous, other strides free; q_out may
     be q.  Returns (q_out, k_out or None)."""
-    T, d = q.shape[0], q.shape[2]
-    d_rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _need(inv_freq is None or (inv_freq.dtype == torch.float32 and inv_freq.is_contiguous() and pos is not None
-                               and pos.dtype == torch.int64 and pos.shape == (T,) and pos.is_contiguous()),
-          "inv_freq: contiguous fp32; pos: contiguous int64 [T]")
+    T, _, d = q.shape
+    if inv_freq is None:
+        d_rot, p_pos, p_freq = 0, None, None
+    else:
+        d_rot = 2 * inv_freq.numel()
+        _need(inv_freq.dtype is torch.float32 and inv_freq.is_contiguous() and pos is not None
+              and pos.dtype is torch.int64 and pos.shape == (T,) and pos.is_contiguous(),
+              "inv_freq: contiguous fp32; pos: contiguous int64 [T]")
+        p_pos, p_freq = pos.data_ptr(), inv_freq.data_ptr()
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
     rows_q = _head_rows(q, q_weight, q_out, T, d, "q")
@@ -372,15 +391,15 @@ def csa2_norm_rope(q, pos, inv_freq, q_weight=None, k=None, k_weight=None, eps=1
     if k is not None:
         if k_out is None:
             k_out = torch.empty(k.shape, dtype=q_out.dtype, device=k.device)
-        _need(k.dtype == q.dtype and k_out.dtype == q_out.dtype, "k has the type of q, k_out that of q_out")
-        rows_k = ctypes.byref(_head_rows(k, k_weight, k_out, T, d, "k"))
-    _need(q.dtype in _TYPES and q_out.dtype in _TYPES and (out_dtype is None or q_out.dtype == out_dtype),
+        _need(k.dtype is q.dtype and k_out.dtype is q_out.dtype, "k has the type of q, k_out that of q_out")
+        rows_k = _head_rows(k, k_weight, k_out, T, d, "k")
+    x_type, y_type = _TYPES.get(q.dtype), _TYPES.get(q_out.dtype)
+    _need(x_type is not None and y_type is not None and (out_dtype is None or q_out.dtype is out_dtype),
           "q and q_out: bf16, fp16 or fp32")
     flags = (ROPE_HALVES if halves else 0) | (ROPE_INVERSE if inverse else 0) | (0 if norm else ROPE_NO_NORM)
-    st = load().csa2_norm_rope(ctypes.byref(rows_q), rows_k, _TYPES[q.dtype], _TYPES[q_out.dtype], T, d, d_rot,
-                               pos.data_ptr() if d_rot else None, inv_freq.data_ptr() if d_rot else None, eps, flags,
-                               _stream(stream))
-    _check(st, "csa2_norm_rope")
+    st = load().csa2_norm_rope(rows_q, rows_k, x_type, y_type, T, d, d_rot, p_pos, p_freq, eps, flags, _stream(stream))
+    if st:
+        raise Csa2Error(st, "csa2_norm_rope")
     return q_out, k_out if k is not None else None
 
 
@@ -390,28 +409,35 @@ def csa2_dense_attn(cache, q, q_pos, swa, swa_pos0, scale=D_LAT ** -0.5, out=Non
     int64 [B, n_q]; swa bf16 [B, swa_len, 512] or None, row r of sequence b at raw position
     swa_pos0[b] + r (int64 [B] on the device, or None: zeros).  Returns (out [B, n_q, H, 512], lse
     fp32 [B, n_q, H] or None)."""
-    B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
-    _need(q.dtype == torch.bfloat16 and q.is_contiguous() and q.shape[3] == D_LAT and B == cache.batch,
+    B, n_q, H, D = q.shape
+    codes = cache.lat_codes
+    _need(q.dtype is torch.bfloat16 and q.is_contiguous() and D == D_LAT and B == cache.batch,
           "q: contiguous bf16 [batch, n_q, heads, 512]")
-    _need(q_pos.dtype == torch.int64 and q_pos.shape == (B, n_q) and q_pos.is_contiguous(),
+    _need(q_pos.dtype is torch.int64 and q_pos.shape == (B, n_q) and q_pos.is_contiguous(),
           "q_pos: contiguous int64 [batch, n_q]")
-    _need(swa is None or (swa.dtype == torch.bfloat16 and swa.is_contiguous() and swa.shape[0] == B
-                          and swa.shape[2] == D_LAT), "swa: contiguous bf16 [batch, swa_len, 512]")
-    _need(swa_pos0 is None or (swa_pos0.dtype == torch.int64 and swa_pos0.shape == (B,) and swa_pos0.is_contiguous()),
+    if swa is None:
+        p_swa, n_swa = None, 0
+    else:
+        Bs, n_swa, Ds = swa.shape
+        _need(swa.dtype is torch.bfloat16 and swa.is_contiguous() and Bs == B and Ds == D_LAT,
+              "swa: contiguous bf16 [batch, swa_len, 512]")
+        p_swa = swa.data_ptr()
+    _need(swa_pos0 is None or (swa_pos0.dtype is torch.int64 and swa_pos0.shape == (B,) and swa_pos0.is_contiguous()),
           "swa_pos0: contiguous int64 [batch]")
     if out is None:
         out = torch.empty((B, n_q, H, D_LAT), dtype=out_dtype, device=q.device)
-    _need(out.dtype in _TYPES and out.is_contiguous() and out.shape == q.shape, "out: contiguous, the shape of q")
+    o_type = _TYPES.get(out.dtype)
+    _need(o_type is not None and out.is_contiguous() and out.shape == q.shape, "out: contiguous, the shape of q")
     if want_lse and lse is None:
         lse = torch.empty((B, n_q, H), dtype=torch.float32, device=q.device)
-    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == (B, n_q, H) and lse.is_contiguous()),
+    _need(lse is None or (lse.dtype is torch.float32 and lse.shape == (B, n_q, H) and lse.is_contiguous()),
           "lse: contiguous fp32 [batch, n_q, heads]")
     if ws is None:
         ws = workspace(OP_DENSE_ATTN, B, n_q, H, 0, cache.capacity, q.device)
-    c = cache.struct()
-    st = load().csa2_dense_attn(ctypes.byref(c), q.data_ptr(), n_q, H, q_pos.data_ptr(),
-                                None if swa is None else swa.data_ptr(), None if swa_pos0 is None else swa_pos0.data_ptr(),
-                                0 if swa is None else swa.shape[1], scale, out.data_ptr(), _TYPES[out.dtype],
+    c = _PACK_CACHE(codes.data_ptr(), cache.lat_scales.data_ptr(), 0, 0, B, cache.capacity, D_LAT, 128, cache.ratio)
+    st = load().csa2_dense_attn(c, q.data_ptr(), n_q, H, q_pos.data_ptr(), p_swa,
+                                None if swa_pos0 is None else swa_pos0.data_ptr(), n_swa, scale, out.data_ptr(), o_type,
                                 None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
-    _check(st, "csa2_dense_attn")
+    if st:
+        raise Csa2Error(st, "csa2_dense_attn")
     return out, lse

@@ -132,6 +132,37 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
     int* flag = qexp + DA_H;
     unsigned int* wmax = reinterpret_cast<unsigned int*>(flag + 8);
 
+    // FP4 rows: a tile is 64 rows x 16 units of 32 dims (16 bytes of codes, 2 of scales); the first one is
+    // fetched before anything else is set up
+    const int lt = tid - DA_LOADW * 32;
+    const uint8_t* codes = a.codes + ((int64_t)b * a.capacity + row0) * (D_LAT / 2);
+    const uint8_t* scales = a.scales + ((int64_t)b * a.capacity + row0) * (D_LAT / 16);
+    constexpr int NU = DA_TILE * 16 / DA_LOADERS;
+    // unit u: a warp takes 4 rows x 8 units, so that a load touches whole 128-byte lines and the
+    // 8 threads of a quarter warp write different bank groups; units below 512 hold dims 0-255
+    auto unit_rc = [](int u, int& r, int& c) {
+        const int qq = u >> 5, l = u & 31;
+        r = 4 * (qq & 15) + (l & 3);
+        c = 8 * (qq >> 4) + (l >> 2);
+    };
+    uint4 cw[NU];
+    uint32_t sc[NU];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            int r, c;
+            unit_rc(lt + i * DA_LOADERS, r, c);
+            cw[i] = make_uint4(0, 0, 0, 0);      // rows past the end expand to zeros
+            sc[i] = 0u;
+            const int j = t * DA_TILE + r;
+            if (j < rows) {
+                cw[i] = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)j * (D_LAT / 2)) + c);
+                sc[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)j * (D_LAT / 16)) + c);
+            }
+        }
+    };
+    if (warp >= DA_LOADW && !window) fetch(0);
+
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             umma::mbar_init(sa(&b_lhalf[i]), DA_LOADERS / 32);
@@ -146,7 +177,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
         *wmax = 0u;
     }
     if (tid < DA_H) m_run[tid] = -INFINITY;
-    if (warp == 0) umma::tmem_alloc(sa(&tmem_base), DAT_COLS);
+    if (warp == DA_LOADW - 1) umma::tmem_alloc(sa(&tmem_base), DAT_COLS);
     // ---- Q: heads h0 .. h0+63 (zero rows past n_heads), bf16 -> fp16 slabs, by warps 0-11; a head whose
     // largest magnitude lies outside [2^-10, 2^15) is scaled by a power of two on the way
     if (warp < DA_LOADW) {
@@ -187,7 +218,6 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
     bool ok = true;
 
     if (warp >= DA_LOADW) {
-        const int lt = tid - DA_LOADW * 32;
         if (window) {
             // ================= window rows: bf16, one scale for all of them
             const uint4* src = reinterpret_cast<const uint4*>(a.swa + ((int64_t)b * a.swa_len + row0) * D_LAT);
@@ -213,37 +243,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
                 }
             }
         } else {
-            // ================= FP4 rows: 64 rows x 16 units of 32 dims (16 bytes of codes, 2 of scales)
-            const uint8_t* codes = a.codes + ((int64_t)b * a.capacity + row0) * (D_LAT / 2);
-            const uint8_t* scales = a.scales + ((int64_t)b * a.capacity + row0) * (D_LAT / 16);
-            constexpr int NU = DA_TILE * 16 / DA_LOADERS;
-            // unit u: a warp takes 4 rows x 8 units, so that a load touches whole 128-byte lines and the
-            // 8 threads of a quarter warp write different bank groups; units below 512 hold dims 0-255
-            auto unit_rc = [](int u, int& r, int& c) {
-                const int qq = u >> 5, l = u & 31;
-                r = 4 * (qq & 15) + (l & 3);
-                c = 8 * (qq >> 4) + (l >> 2);
-            };
-            uint4 cw[NU];
-            uint32_t sc[NU];
-            auto fetch = [&](int t) {
-#pragma unroll
-                for (int i = 0; i < NU; ++i) {
-                    int r, c;
-                    unit_rc(lt + i * DA_LOADERS, r, c);
-                    cw[i] = make_uint4(0, 0, 0, 0);      // rows past the end expand to zeros
-                    sc[i] = 0u;
-                    const int j = t * DA_TILE + r;
-                    if (j < rows) {
-                        cw[i] = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)j * (D_LAT / 2)) + c);
-                        sc[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)j * (D_LAT / 16)) + c);
-                    }
-                }
-            };
+            // ================= FP4 rows
             for (int t = 0; t < T; ++t) {
                 const int buf = t & 1;
                 uint8_t* L = sm + DA_SL + buf * DA_LBUF;
-                fetch(t);
+                if (t > 0) fetch(t);
                 if (lt < DA_TILE && (t + 1) * DA_TILE + lt < rows) {
                     const int64_t j = (t + 1) * DA_TILE + lt;
                     umma::prefetch_l2(codes + j * (D_LAT / 2));
@@ -446,50 +450,97 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
     if (!ok) atomicExch(a.err, 1);
     umma::fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == DA_LOADW - 1) {
         umma::fence_after();
         umma::tmem_dealloc(tmem, DAT_COLS);
     }
 }
 
-// Joins the splits of one query and head: 128 threads, four dims each.
+// Joins the splits of one query and head: 128 threads, four dims each.  The shares' factors are found by
+// the threads side by side, then the outputs are read eight at a time.
+constexpr int DA_MAX_SPLITS = 152;
+
 template <typename TO>
 __global__ void __launch_bounds__(128) k_dense_combine(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
                                                        int splits, int hgroups, int n_heads, int64_t query0,
                                                        TO* __restrict__ out, float* __restrict__ lse) {
-    pdl_wait();
+    __shared__ float fac[DA_MAX_SPLITS + 1], wm[4], wl[4];
+    __shared__ int live[DA_MAX_SPLITS + 1], n_live;
     const int64_t ql = blockIdx.x / n_heads;                      // query of this pass
     const int head = (int)(blockIdx.x - ql * n_heads);
     const int64_t first = (ql * hgroups + head / DA_H) * (splits + 1) * DA_H + head % DA_H;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    pdl_wait();
+    float2 v[2];
     float m = -INFINITY;
-    for (int s = 0; s <= splits; ++s) {
-        const float2 v = part_ml[first + (int64_t)s * DA_H];
-        if (v.y > 0.0f) m = fmaxf(m, v.x);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = tid + 128 * i;
+        v[i] = s <= splits ? part_ml[first + (int64_t)s * DA_H] : make_float2(-INFINITY, 0.0f);
+        if (v[i].y != 0.0f) m = fmaxf(m, v[i].x);
     }
-    float l = 0.0f, o[4] = {};
-    for (int s = 0; s <= splits; ++s) {
-        const float2 v = part_ml[first + (int64_t)s * DA_H];
-        if (!(v.y > 0.0f)) continue;                              // an empty share holds no output
-        const float f = exp2f(v.x - m);
-        l = fmaf(f, v.y, l);
-        const float4 x = reinterpret_cast<const float4*>(part_o + (first + (int64_t)s * DA_H) * D_LAT)[threadIdx.x];
-        o[0] = fmaf(f, x.x, o[0]), o[1] = fmaf(f, x.y, o[1]), o[2] = fmaf(f, x.z, o[2]), o[3] = fmaf(f, x.w, o[3]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) wm[warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3]));
+    float l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = tid + 128 * i;
+        const float f = v[i].y != 0.0f ? exp2f(v[i].x - m) : 0.0f;
+        if (s <= splits) fac[s] = f;
+        l = fmaf(f, v[i].y, l);
+    }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if ((tid & 31) == 0) wl[warp] = l;
+    __syncthreads();
+    l = (wl[0] + wl[1]) + (wl[2] + wl[3]);
+    if (warp == 0) {                                              // shares that hold an output, in order
+        int n = 0;
+        for (int s0 = 0; s0 <= splits; s0 += 32) {
+            const bool is = s0 + tid <= splits && !(fac[s0 + tid] == 0.0f);
+            const unsigned b = __ballot_sync(0xffffffffu, is);
+            if (is) live[n + __popc(b & ((1u << tid) - 1u))] = s0 + tid;
+            n += __popc(b);
+        }
+        if (tid == 0) n_live = n;
+    }
+    __syncthreads();
+    const int n = n_live;
+    float o[4] = {};
+    const float4* src = reinterpret_cast<const float4*>(part_o + first * D_LAT) + tid;
+    for (int s0 = 0; s0 < n; s0 += 8) {
+        float4 x[8];
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            f[i] = 0.0f;
+            x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (s0 + i < n) {
+                const int s = live[s0 + i];
+                f[i] = fac[s];
+                x[i] = src[(int64_t)s * DA_H * (D_LAT / 4)];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[0] = fmaf(f[i], x[i].x, o[0]), o[1] = fmaf(f[i], x[i].y, o[1]);
+            o[2] = fmaf(f[i], x[i].z, o[2]), o[3] = fmaf(f[i], x[i].w, o[3]);
+        }
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const int64_t row = (query0 + ql) * n_heads + head;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] *= inv;
-    ElemVec<TO, 4> v;
-    v.pack(o);
-    v.store(out + row * D_LAT + 4 * threadIdx.x);
-    if (lse != nullptr && threadIdx.x == 0)
-        lse[row] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    ElemVec<TO, 4> y;
+    y.pack(o);
+    y.store(out + row * D_LAT + 4 * tid);
+    if (lse != nullptr && tid == 0) lse[row] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 namespace {
 constexpr int DA_SMS = 152;
 constexpr size_t DA_HEAD = 256;                                   // the error word and padding
-constexpr int DA_MAX_SPLITS = DA_SMS;
 
 // Splits of each query's entries: the count whose whole waves of blocks finish first, at about 2 us a
 // tile and 5 us a block, plus the combine's reading of the shares.

@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
         for (int w = 0; w < warps; ++w) v += red[w * T * (R * 16) + u];
         lin_store(a, t, g, m, v * a.alpha);
     }
-    __threadfence();    // the attention may stage these rows as its queries before it waits (see norm_rope.cu)
+    __syncthreads();
+    if (tid == 0) __threadfence();               // the attention may stage these rows before it waits (see norm_rope.cu)
 }
 
 // ================================================================ more tokens
@@ -737,9 +738,9 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         umma::cluster_sync();                    // no block leaves while another reads its sums
     }
     if (!ok) atomicExch(err, 1);
-    __threadfence();
     umma::fence_before();
     __syncthreads();
+    if (tid == 0) __threadfence();               // as in k_linear_few
     if (warp == LM_XW + 2) {
         umma::fence_after();
         umma::tmem_dealloc(tmem, cols);

@@ -56,103 +56,142 @@ __device__ __forceinline__ unsigned long long nr_turns(float f) {
     return (b >> 31) ? 0ull - r : r;
 }
 
-// VEC consecutive elements per access, up to NCH accesses per lane and row.  Blocks below `q_blocks`
-// take query rows, the others key rows: a block's rows share their weights.
-template <typename TX, int VEC, int NCH>
-__global__ void __launch_bounds__(NR_THREADS, VEC > 1 && VEC * NCH <= 16 ? 4 : VEC * NCH <= 16 ? 2 : 1)
-    k_norm_rope(NrRows q, NrRows k, int64_t n_tok, unsigned q_blocks, int rows_per_block, int lanes, int d, int d_rot,
-                int table, const int64_t* __restrict__ pos, const float* __restrict__ inv_freq, float eps, int norm,
-                int halves, int inverse, int y_type) {
+// (a0, a1) = (a0 b0, a1 b1) in one packed instruction
+__device__ __forceinline__ void mul2_rn(float& a0, float& a1, float b0, float b1) {
+    asm("{\n .reg .b64 ra, rb;\n mov.b64 ra, {%0, %1};\n mov.b64 rb, {%2, %3};\n mul.rn.f32x2 ra, ra, rb;\n"
+        " mov.b64 {%0, %1}, ra;\n}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+
+struct NrArgs {
+    NrRows set[2];                           // queries, keys
+    int64_t n_tok;
+    unsigned q_blocks;                       // blocks below take query rows, the others key rows
+    int rows_per_block, lanes, d, d_rot, table;
+    const int64_t* pos;
+    const float* inv_freq;
+    float eps, inv_d;
+    int norm, halves, inverse, y_type;
+};
+
+// VEC consecutive elements per access, NCH accesses per lane and row (up to NCH unless FULL).  SWAP: a
+// pair's two values lie in different lanes and meet in a row buffer.  Issue slots are what this kernel
+// runs out of first (a 1 KB row is 45 clocks of its SM's share of HBM), so sizes are compile-time where
+// the common shapes allow and the products go two at a time.
+template <typename TX, int VEC, int NCH, bool SWAP, bool FULL>
+__global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 : SWAP ? 3 : 4)
+    k_norm_rope(const NrArgs g) {
     extern __shared__ float2 cs[];           // [tokens of this block][d_rot / 2] (cos, sin); row buffers
-    const bool isq = blockIdx.x < q_blocks;
-    const NrRows R = isq ? q : k;
-    const int heads = R.heads, half = d_rot / 2, keep = d - d_rot;
-    const int64_t n_rows = n_tok * heads;
-    const int64_t r0 = (int64_t)(isq ? blockIdx.x : blockIdx.x - q_blocks) * rows_per_block;
-    const int nr = (int)min((int64_t)rows_per_block, n_rows - r0);
+    const bool isq = blockIdx.x < g.q_blocks;
+    const NrRows R = g.set[isq ? 0 : 1];
+    const int heads = R.heads, d = g.d, d_rot = g.d_rot, half = d_rot / 2, keep = d - d_rot;
+    const int lanes = FULL && NCH > 1 ? 32 : g.lanes;
+    const int64_t r0 = (int64_t)(isq ? blockIdx.x : blockIdx.x - g.q_blocks) * g.rows_per_block;
+    const int nr = (int)min((int64_t)g.rows_per_block, g.n_tok * heads - r0);
     const int64_t t0 = r0 / heads;
     const int h0 = (int)(r0 - t0 * heads);
     const int nt = (h0 + nr - 1) / heads + 1;
     const int sub = threadIdx.x & (lanes - 1);               // lane within the row
     const int slots = NR_THREADS / lanes, slot = threadIdx.x / lanes;
-    const bool swap = VEC == 1 || halves;                    // a pair's two values lie in different lanes
-    float* buf = reinterpret_cast<float*>(cs + table) + slot * d_rot;
+    float* buf = reinterpret_cast<float*>(cs + g.table) + slot * d_rot;
     constexpr bool WREG = VEC > 1;                           // weights in registers (else read as they are used)
     float w[WREG ? NCH : 1][VEC];
-    if (WREG && R.w != nullptr) {
+    if (WREG) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int j = (sub + c * lanes) * VEC + e;
-                w[c][e] = j < d ? __ldg(R.w + j) : 0.0f;
+                w[c][e] = R.w == nullptr ? 1.0f : FULL || j < d ? __ldg(R.w + j) : 0.0f;
             }
     }
     pdl_wait();                              // x and the positions may come from the preceding kernel
 
-    ElemVec<TX, VEC> v[NCH];                 // this lane's columns of row i of the block
-    auto load = [&](int i) {
-        const int t = (h0 + i) / heads, h = h0 + i - t * heads;
-        const TX* x = reinterpret_cast<const TX*>(R.x) + (t0 + t) * R.x_tok + h * R.x_head;
+    // Row i of the block is head h of its token t.  Slots past the last row repeat it and store nothing.
+    const int last = nr - 1;
+    int i = slot, t = (h0 + min(i, last)) / heads, h = h0 + min(i, last) - t * heads;
+    const int dt = slots / heads, dh = slots - dt * heads;   // a step of `slots` rows
+    const TX* x0 = reinterpret_cast<const TX*>(R.x) + t0 * R.x_tok;
+    ElemVec<TX, VEC> v[NCH];                 // this lane's columns
+    auto load = [&](int t, int h) {
+        const TX* x = x0 + t * R.x_tok + h * R.x_head;
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int j = (sub + c * lanes) * VEC;
-            if (j < d) v[c].load(x + j);
+            if (FULL || j < d)
+                v[c].load(x + j);
+            else
+#pragma unroll
+                for (int k = 0; k < ElemVec<TX, VEC>::WORDS; ++k) v[c].w[k] = 0u;
         }
     };
-    if (slot < nr) load(slot);               // in flight while the angles are computed
-    for (int i = threadIdx.x; i < nt * half; i += NR_THREADS) {
-        const int t = i / half, c = i - t * half;
-        const float f = __ldg(inv_freq + c);
-        const unsigned long long a = nr_turns(f) * (unsigned long long)pos[t0 + t];
+    load(t, h);                              // in flight while the angles are computed
+    for (int k = threadIdx.x; k < nt * half; k += NR_THREADS) {
+        const int tt = k / half, c = k - tt * half;
+        const float f = __ldg(g.inv_freq + c);
+        const unsigned long long a = nr_turns(f) * (unsigned long long)g.pos[t0 + tt];
         float s, co;
         sincospif((float)(long long)a * 0x1p-63f, &s, &co);      // half turns in [-1, 1)
         if (!isfinite(f)) s = co = __int_as_float(0x7fc00000);
-        cs[i] = make_float2(co, inverse ? -s : s);
+        cs[k] = make_float2(co, g.inverse ? -s : s);
     }
     __syncthreads();
 
-    for (int i0 = 0; i0 < nr; i0 += slots) {                 // the same trip count for every lane of a warp
-        const int i = i0 + slot;
-        const bool live = i < nr;
-        float a[NCH][VEC], ss = 0.0f;
+    for (int i0 = 0; i0 < nr; i0 += slots, i += slots) {     // the same trip count for every lane of a warp
+        const bool live = i <= last;
+        const int ct = t, ch = h;
+        float a[NCH][VEC], ss[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int c = 0; c < NCH; ++c)
+        for (int c = 0; c < NCH; ++c) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                a[c][e] = live && (sub + c * lanes) * VEC < d ? v[c].get(e) : 0.0f;
-                ss = fmaf(a[c][e], a[c][e], ss);
-            }
-        const int t = live ? (h0 + i) / heads : 0, h = live ? h0 + i - t * heads : 0;
-        __syncwarp();                                        // every load of a row before its stores: y may be x
-        if (i + slots < nr) load(i + slots);                 // the next row, while this one's sum goes round
-        float r = 1.0f;
-        if (norm) {
-            for (int o = lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            r = rsqrtf(ss / (float)d + eps);
+            for (int e = 0; e < VEC; ++e) a[c][e] = v[c].get(e);
+            if (VEC == 1)
+                ss[0] = fmaf(a[c][0], a[c][0], ss[0]);
+            else
+#pragma unroll
+                for (int e = 0; e + 1 < VEC; e += 2) fma2_rn(ss[0], ss[1], a[c][e], a[c][e + 1], a[c][e], a[c][e + 1]);
         }
-        const float2* tab = cs + t * half;
-        const int64_t y0 = (t0 + t) * R.y_tok + h * R.y_head;
+        __syncwarp();                                        // every load of a row before its stores: y may be x
+        if (i + slots <= last) {                             // the next row, while this one's sum goes round
+            t += dt, h += dh;
+            if (h >= heads) h -= heads, ++t;
+            load(t, h);
+        }
+        float r = 1.0f;
+        if (g.norm) {
+            float sum = ss[0] + ss[1];
+            for (int o = lanes >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            r = rsqrtf(fmaf(sum, g.inv_d, g.eps));
+        }
+        const float2* tab = cs + ct * half;
+        const int64_t y0 = (t0 + ct) * R.y_tok + ch * R.y_head;
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int j = (sub + c * lanes) * VEC;
+            if (VEC == 1) {
+                a[c][0] *= r;
+                if (R.w != nullptr && j < d) a[c][0] *= __ldg(R.w + j);
+            } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                a[c][e] *= r;
-                if (R.w != nullptr) a[c][e] *= WREG ? w[WREG ? c : 0][e] : (j + e < d ? __ldg(R.w + j + e) : 0.0f);
+                for (int e = 0; e + 1 < VEC; e += 2) {
+                    float w0 = w[WREG ? c : 0][e], w1 = w[WREG ? c : 0][VEC > 1 ? e + 1 : e];
+                    mul2_rn(w0, w1, r, r);
+                    mul2_rn(a[c][e], a[c][VEC > 1 ? e + 1 : e], w0, w1);
+                }
             }
-            if (swap && live && j < d && j >= keep)
+            if (SWAP && live && (FULL || j < d) && j >= keep)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) buf[j - keep + e] = a[c][e];
         }
-        if (swap) __syncwarp();
+        if (SWAP) __syncwarp();
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int j = (sub + c * lanes) * VEC;
-            if (!live || j >= d) continue;
+            if (!live || !(FULL || j < d)) continue;
             if (j >= keep) {
                 const int u = j - keep;
-                if (!swap) {
+                if (!SWAP) {
 #pragma unroll
                     for (int e = 0; e + 1 < VEC; e += 2) {
                         const float2 z = tab[(u + e) >> 1];
@@ -164,18 +203,18 @@ __global__ void __launch_bounds__(NR_THREADS, VEC > 1 && VEC * NCH <= 16 ? 4 : V
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         const int ue = u + e;
-                        const bool first = halves ? ue < half : !(ue & 1);
-                        const float p = buf[halves ? (first ? ue + half : ue - half) : (ue ^ 1)];
-                        const float2 z = tab[halves ? (first ? ue : ue - half) : ue >> 1];
+                        const bool first = g.halves ? ue < half : !(ue & 1);
+                        const float p = buf[g.halves ? (first ? ue + half : ue - half) : (ue ^ 1)];
+                        const float2 z = tab[g.halves ? (first ? ue : ue - half) : ue >> 1];
                         a[c][e] = first ? a[c][e] * z.x - p * z.y : p * z.y + a[c][e] * z.x;
                     }
                 }
             }
-            if (y_type == CSA2_BF16) {
+            if (g.y_type == CSA2_BF16) {
                 ElemVec<__nv_bfloat16, VEC> o;
                 o.pack(a[c]);
                 o.store(reinterpret_cast<__nv_bfloat16*>(R.y) + y0 + j);
-            } else if (y_type == CSA2_F16) {
+            } else if (g.y_type == CSA2_F16) {
                 ElemVec<__half, VEC> o;
                 o.pack(a[c]);
                 o.store(reinterpret_cast<__half*>(R.y) + y0 + j);
@@ -185,12 +224,14 @@ __global__ void __launch_bounds__(NR_THREADS, VEC > 1 && VEC * NCH <= 16 ? 4 : V
                 o.store(reinterpret_cast<float*>(R.y) + y0 + j);
             }
         }
-        if (swap) __syncwarp();                              // the row buffer is read before the next row writes it
+        if (SWAP) __syncwarp();                              // the row buffer is read before the next row writes it
     }
     // The attention stages its queries and window rows before it waits for the kernel before it, and
     // this kernel writes those: it never lets its successor start early, and its rows are visible to
-    // the whole GPU before its blocks end.
-    __threadfence();
+    // the whole GPU before its blocks end (one fence for all threads, ordered after their stores by the
+    // block's barrier).
+    __syncthreads();
+    if (threadIdx.x == 0) __threadfence();
 }
 
 namespace {
@@ -212,13 +253,21 @@ cudaError_t nr_launch(const NrRows& q, const NrRows& k, int64_t n_tok, int d, in
     const int64_t qb = (n_tok * q.heads + rpb - 1) / rpb, kb = (n_tok * k.heads + rpb - 1) / rpb;
     if (qb + kb > 0x7fffffff) return cudaErrorInvalidConfiguration;
     // the angles, and one row's rotated values per slot where a pair's values lie in different lanes
-    const size_t smem = table(rounds) * sizeof(float2) + (VEC == 1 || halves ? (size_t)slots * d_rot * sizeof(float) : 0);
+    const bool swap = VEC == 1 || halves, full = VEC == 8 && NCH <= 2 && d == lanes * VEC * NCH;
+    const size_t smem = table(rounds) * sizeof(float2) + (swap ? (size_t)slots * d_rot * sizeof(float) : 0);
+    const NrArgs a{{q, k}, n_tok, (unsigned)qb, rpb, lanes, d, d_rot, table(rounds), pos, inv_freq, eps, 1.0f / (float)d,
+                   norm, halves, inverse, y_type};
+    void (*kern)(NrArgs) = k_norm_rope<TX, VEC, NCH, true, false>;
+    if constexpr (VEC > 1) {
+        constexpr bool F = VEC == 8 && NCH <= 2;
+        kern = swap ? (full ? k_norm_rope<TX, VEC, NCH, true, F> : k_norm_rope<TX, VEC, NCH, true, false>)
+                    : (full ? k_norm_rope<TX, VEC, NCH, false, F> : k_norm_rope<TX, VEC, NCH, false, false>);
+    }
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(k_norm_rope<TX, VEC, NCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    launch_k(k_norm_rope<TX, VEC, NCH>, dim3((unsigned)(qb + kb)), NR_THREADS, smem, st, q, k, n_tok, (unsigned)qb, rpb,
-             lanes, d, d_rot, table(rounds), pos, inv_freq, eps, norm, halves, inverse, y_type);
+    launch_k(kern, dim3((unsigned)(qb + kb)), NR_THREADS, smem, st, a);
     note_launch();
     return cudaGetLastError();
 }
