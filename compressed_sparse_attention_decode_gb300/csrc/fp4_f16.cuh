@@ -70,4 +70,13 @@ __device__ __forceinline__ uint4 e2m1x8_scaled(uint32_t w, __half2 s) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+namespace umma {
+// true in one lane of the (whole) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+    return p != 0;
+}
+}  // namespace umma
+
 }  // namespace csa2

@@ -350,11 +350,6 @@ __global__ void __launch_bounds__(256) k_linear_x(const LinArgs a, LinPrep p, ui
         put(k, k < a.n_in ? lin_load8(x + k, x_vec) : v[0]);
 }
 
-__device__ __forceinline__ bool umma_elect() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
-    return p != 0;
-}
 // D[tmem] += A[tmem: 128 rows x 16 fp16, two per column] . B[smem]
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -691,7 +686,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                 const uint32_t nst = (it + 1) % LM_S, nph = ((it + 1) / LM_S) & 1;
                 const bool nx = umma::mbar_test(sa(&b_x[nst]), nph), na = umma::mbar_test(sa(&b_a[nst]), nph);
                 umma::fence_after();
-                if (umma_elect()) {
+                if (umma::elect_one()) {
                     for (int pl = 0; pl < p.planes; ++pl) {
                         const uint64_t bd = umma::desc(xb + st * stage_bytes + (2 * pl + hf) * (uint32_t)p.half_bytes(), 16, 1024, umma::LAYOUT_SW128);
 #pragma unroll
