@@ -343,7 +343,7 @@ def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, ws=No
     _need((x.stride(-1) == 1 or n_in == 0) and (n_out <= 1 or out.stride(-1) == 1), "rows of x and out: contiguous")
     lib = load()
     if ws is None:
-        n = lib.csa2_workspace_size(OP_LINEAR_FP4, T, G, x_type, 0, n_in) if T > 8 else 0     # none for so few tokens
+        n = lib.csa2_workspace_size(OP_LINEAR_FP4, T, G, x_type, 0, n_in) if T > 8 or n_in > 16384 else 0   # none for few tokens
         ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
     st = lib.csa2_linear_fp4(x.data_ptr(), x_type, x.stride(0), x_group, T, G, n_in, n_out, codes.data_ptr(),
                              scales.data_ptr(), alpha, out.data_ptr(), y_type, out.stride(0), out.stride(1) if lead else 0,

@@ -260,7 +260,8 @@ csa2_status csa2_linear_fp4(const void* x, int32_t x_type, int64_t x_tok, int64_
     if (!std::isfinite(alpha)) return CSA2_ERR_INVALID_ARG;
     if (n_tok == 0 || n_out == 0) return CSA2_OK;
     if (!y || !aligned(y, type_size(y_type))) return CSA2_ERR_INVALID_ARG;
-    if (n_in > 0 && (!x || !codes || !scales || !aligned(x, type_size(x_type)) || !aligned(codes, 16)))
+    if (n_in > 0 && (!x || !codes || !scales || !aligned(x, type_size(x_type)) || !aligned(codes, 16) ||
+                     !aligned(scales, 16)))
         return CSA2_ERR_INVALID_ARG;
     const size_t need = linear_fp4_ws(x_type, n_tok, n_groups, n_in);
     if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return CSA2_ERR_WORKSPACE;

@@ -12,11 +12,11 @@
 //
 // Two kernels:
 //  - k_linear_few (up to 16 tokens): bound by the weight bytes.  mma.sync
-//    m16n8k16, the weights as the A fragments straight from global memory.  The
+//    m16n8k16, the weights as the A fragments.  The
 //    order of k within a product is free as long as both operands agree, so a
 //    lane takes 16 consecutive bytes of a row (32 weights, two scale groups) and
 //    feeds them, four at a time, to eight products, and x comes from global memory
-//    in the matching order.
+//    in the matching order.  The weights come by bulk copies, all at once.
 //  - k_linear_many: tcgen05, M = 128 rows, N = up to 128 tokens.  Expanded
 //    weights go from registers to TMEM (the A operand), so shared memory carries
 //    the tokens alone: with both operands there, N = 128 would need 192 bytes per
@@ -62,15 +62,27 @@ __device__ __forceinline__ int lin_exp(float mx) {
     if (mx == 0.0f) return 0;
     return max(-126, (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 14);
 }
+// the largest finite magnitude of eight values: the largest magnitude as bits and, where that is an infinity or
+// a NaN (which stay what they are in fp16), one by one
 template <typename TX>
 __device__ __forceinline__ float lin_absmax(const ElemVec<TX, 8>& v) {
-    float m = 0.0f;
+    uint32_t m = 0u;
+    if constexpr (sizeof(TX) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v.w[i] & 0x7fff7fffu);
+        m = max(m & 0xffffu, m >> 16) << 16;                 // bf16: the upper half of the fp32 bits
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, v.w[i] & 0x7fffffffu);
+    }
+    if (m < 0x7f800000u) return __uint_as_float(m);
+    float f = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float a = fabsf(v.get(e));
-        if (a < INFINITY) m = fmaxf(m, a);           // infinities and NaN stay what they are in fp16
+        if (a < INFINITY) f = fmaxf(f, a);
     }
-    return m;
+    return f;
 }
 // eight values times d as fp16, and for fp32 what that leaves (0 where it is not finite)
 template <typename TX>
@@ -117,6 +129,7 @@ __device__ __forceinline__ ElemVec<TX, 8> lin_load8(const TX* p, bool vec) {
 
 constexpr int LF_TOK = 16;
 constexpr int LF_MAXW = 8;                       // warps of a block
+constexpr int LF_SMEM = 184 * 1024;              // the weights of a block, at most
 
 __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -125,114 +138,147 @@ __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, ui
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 32 weights (16 bytes of codes, two scales) of one row from k on; zeros from n_in on
-struct LinSeg {
-    uint4 c;
-    uint32_t s;
-    __device__ __forceinline__ void load(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int k,
-                                         int n_in, bool wide) {
-        c = make_uint4(0, 0, 0, 0);
-        s = 0u;
-        if (k >= n_in) return;
-        if (wide) {                              // n_in a multiple of 32: every segment is whole and aligned
-            c = __ldg(reinterpret_cast<const uint4*>(codes + k / 2));
-            s = __ldg(reinterpret_cast<const uint16_t*>(scales + k / 16));
-        } else {
-            const uint2 a = __ldg(reinterpret_cast<const uint2*>(codes + k / 2));
-            c.x = a.x, c.y = a.y;
-            s = __ldg(scales + k / 16);
-            if (k + 16 < n_in) {
-                const uint2 b = __ldg(reinterpret_cast<const uint2*>(codes + k / 2) + 1);
-                c.z = b.x, c.w = b.y;
-                s |= (uint32_t)__ldg(scales + k / 16 + 1) << 8;
-            }
-        }
-    }
-};
+// Bytes [start, start + n) of `src` into shared memory at dst (16-byte aligned), byte i at dst + start % 16 + i:
+// a bulk copy of the whole 16-byte pieces, counted on `bar`, and plain loads of the rest by the calling warp.
+__device__ __forceinline__ uint32_t lf_bulk_bytes(uint64_t start, uint32_t n) {
+    return (uint32_t)(((start + n) & ~15ull) - (start & ~15ull));
+}
+__device__ __forceinline__ void lf_copy(uint8_t* dst, const uint8_t* src, uint64_t start, uint32_t n, uint32_t bar, int lane) {
+    const uint64_t a = start & ~15ull;
+    const uint32_t whole = lf_bulk_bytes(start, n);
+    if (lane == 0 && whole > 0) umma::bulk_g2s(umma::smem_u32(dst), src + a, whole, bar);
+    const uint32_t rest = (uint32_t)(start + n - a) - whole;
+    if (lane < (int)rest) dst[whole + lane] = src[a + whole + lane];
+}
 
-// A block takes R tiles of 16 rows; its warps split n_in in chunks of 128, warp w taking chunks w, w +
-// warps, ..; per chunk a warp holds the tokens' fragments in registers and runs all R tiles over them.
-// Nothing is shared until the warps' sums are joined at the end, in order.
+// A block takes R tiles of 16 rows.  Rows are contiguous, so a tile's codes and scales are one piece of
+// memory each: all of them are requested by bulk copies as the block starts, which keeps more bytes in
+// flight than registers could (one token, 1,536 x 32,768: every block's rows at once), and each tile has a
+// barrier of its own.  The warps split n_in in chunks of 128, warp w taking chunks w, w + warps, ..; per
+// chunk a warp holds the tokens' fragments in registers and runs all R tiles over them.  The warps' sums are
+// joined at the end, in order.
 template <typename TX, int NT, int R>
-__global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a, int x_vec, int wide) {
+__global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a, int x_vec) {
     extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ __align__(8) unsigned long long b_tile[R];
     constexpr bool SPLIT = sizeof(TX) == 4, SCALED = !std::is_same<TX, __half>::value;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     const int K = a.n_in, T = a.n_tok, g = blockIdx.y;
     const int chunks = (K + 127) / 128;
     const int m0 = blockIdx.x * (16 * R);
     const int r = lane >> 2, c = lane & 3;
-    constexpr int RING = NT == 1 && !SPLIT ? 2 : 2;           // row tile x chunk pieces in flight per warp
-    const int mine = warp < chunks ? (chunks - warp + warps - 1) / warps : 0;      // chunks of this warp
-    const int items = mine * R;
-
+    const int rows = min(16 * R, a.n_out - m0);
+    // tile i's codes at sm + i * (8 K + 16), its scales after all codes at i * (K + 16) (both with the source's
+    // offset to 16 bytes)
+    const uint32_t c_tile = 8u * K + 16, s_tile = (uint32_t)K + 16;
+    uint8_t* sm_s = sm + R * c_tile;
+    const uint64_t row0 = (uint64_t)g * a.n_out + m0;
+    const uint64_t c0 = row0 * (uint64_t)(K / 2), s0 = row0 * (uint64_t)(K / 16);
+    if (tid == 0) {
+        for (int i = 0; i < R; ++i) umma::mbar_init(umma::smem_u32(&b_tile[i]), 1);
+        umma::fence_mbar_init();
+    }
     pdl_wait();                                  // x, and weights just quantised, may come from the preceding kernel
-    LinSeg wa[RING], wb[RING];
-    const uint8_t* codes = a.codes + ((int64_t)g * a.n_out + m0) * (K / 2);
-    const uint8_t* scales = a.scales + ((int64_t)g * a.n_out + m0) * (K / 16);
-    const int last = a.n_out - 1 - m0;           // rows past the end repeat the last one; their results are not stored
-    // piece `it` of this warp: row tile it % R of its chunk it / R
-    auto fetch = [&](int slot, int it, int tile) {
-        const int k = it < items ? (warp + it / R * warps) * 128 + c * 32 : K;
-        const int ra = min(tile * 16 + r, last), rb = min(tile * 16 + r + 8, last);
-        // offsets within the block's rows: 64 rows of at most 2^24 values fit 32 bits
-        wa[slot].load(codes + (uint32_t)ra * (uint32_t)(K / 2), scales + (uint32_t)ra * (uint32_t)(K / 16), k, K, wide);
-        wb[slot].load(codes + (uint32_t)rb * (uint32_t)(K / 2), scales + (uint32_t)rb * (uint32_t)(K / 16), k, K, wide);
-    };
-#pragma unroll
-    for (int i = 0; i < RING; ++i) fetch(i, i, i % R);
+    if (warp == 0) {
+        __syncwarp();
+        for (int i = 0; i < R; ++i) {
+            const int n = max(0, min(16, rows - 16 * i));
+            const uint64_t cb = c0 + (uint64_t)i * 8 * K, sb = s0 + (uint64_t)i * K;
+            const uint32_t nc = (uint32_t)n * (K / 2), ns = (uint32_t)n * (K / 16);
+            const uint32_t bar = umma::smem_u32(&b_tile[i]);
+            if (lane == 0) umma::mbar_arrive_expect_tx(bar, n > 0 ? lf_bulk_bytes(cb, nc) + lf_bulk_bytes(sb, ns) : 0u);
+            __syncwarp();
+            if (n > 0) {
+                lf_copy(sm + i * c_tile, a.codes, cb, nc, bar, lane);
+                lf_copy(sm_s + i * s_tile, a.scales, sb, ns, bar, lane);
+            }
+        }
+    }
 
     const TX* x = reinterpret_cast<const TX*>(a.x) + (int64_t)g * a.x_group;
     uint4 bh[NT][4], bl[SPLIT ? NT : 1][4];      // 32 values of token n * 8 + r: this lane's B fragments of a chunk
     float back[NT][2];                           // 2^E of tokens n * 8 + 2c and + 1
-    auto tokens = [&](int ch) {
-        const int k0 = ch * 128 + c * 32;
+    ElemVec<TX, 8> v[4];
+    auto fetch = [&](int ch, int n) {            // chunk ch of token n * 8 + r: this lane's segment
+        const int t = n * 8 + r, k0 = ch * 128 + c * 32;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int t = n * 8 + r;
-            ElemVec<TX, 8> v[4];
-            float m = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            if (t < T && k0 + 8 * j < K)
+                v[j] = lin_load8(x + t * a.x_tok + k0 + 8 * j, x_vec);
+            else
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (t < T && k0 + 8 * j < K)
-                    v[j] = lin_load8(x + t * a.x_tok + k0 + 8 * j, x_vec);
-                else
+                for (int i = 0; i < ElemVec<TX, 8>::WORDS; ++i) v[j].w[i] = 0u;
+        }
+    };
+    auto convert = [&](int n) {
+        float m = 0.0f, d = 1.0f;
+        if (SCALED) {
 #pragma unroll
-                    for (int i = 0; i < ElemVec<TX, 8>::WORDS; ++i) v[j].w[i] = 0u;
-            }
-            float d = 1.0f;
-            if (SCALED) {
+            for (int j = 0; j < 4; ++j) m = fmaxf(m, lin_absmax(v[j]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const int e = lin_exp(m);
+            d = pow2f(-e);
+            const float up = pow2f(e);           // of token r (of 8); this lane's results are of tokens 2c, 2c + 1
+            back[n][0] = __shfl_sync(0xffffffffu, up, 8 * c);
+            back[n][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+        }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m = fmaxf(m, lin_absmax(v[j]));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const int e = lin_exp(m);
-                d = pow2f(-e);
-                const float up = pow2f(e);       // of token r (of 8); this lane's results are of tokens 2c, 2c + 1
-                back[n][0] = __shfl_sync(0xffffffffu, up, 8 * c);
-                back[n][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint4 lo;
-                lin_split(v[j], d, bh[n][j], lo);
-                if (SPLIT) bl[n][j] = lo;
+        for (int j = 0; j < 4; ++j) {
+            uint4 lo;
+            lin_split(v[j], d, bh[n][j], lo);
+            if (SPLIT) bl[n][j] = lo;
+        }
+    };
+    // up to 8 tokens: the loads run a chunk ahead (more would not fit the registers)
+    constexpr bool EARLY = NT == 1 && !(SPLIT && R > 1);
+    if (EARLY && warp < chunks) fetch(warp, 0);  // while the weights arrive
+    __syncthreads();                             // the barriers, and the copies' plain ends
+
+    // one row's 32 weights (16 bytes of codes, two scales) from k on; rows past the end repeat the last one (their
+    // results are not stored), and values from n_in on are zeros
+    const uint32_t co = (uint32_t)(c0 & 15), so = (uint32_t)(s0 & 15);     // of every tile: a tile is a multiple of 16 bytes
+    const bool wide = K % 32 == 0;               // codes 16 bytes apart from a 16-byte boundary, scales in pairs
+    auto segment = [&](int tile, int row, int k, uint4& cw, uint32_t& sw) {
+        const int rr = min(row, rows - 1 - tile * 16);
+        const uint8_t* cp = sm + tile * c_tile + co + (uint32_t)rr * (K / 2) + k / 2;
+        const uint8_t* sp = sm_s + tile * s_tile + so + (uint32_t)rr * (K / 16) + k / 16;
+        cw = make_uint4(0, 0, 0, 0);
+        sw = 0u;
+        if (k >= K) return;
+        if (wide && co == 0) {
+            cw = *reinterpret_cast<const uint4*>(cp);
+            sw = sp[0] | ((uint32_t)sp[1] << 8);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(cp);
+            cw.x = u.x, cw.y = u.y;
+            sw = sp[0];
+            if (k + 16 < K) {
+                const uint2 w = *reinterpret_cast<const uint2*>(cp + 8);
+                cw.z = w.x, cw.w = w.y;
+                sw |= (uint32_t)sp[1] << 8;
             }
         }
     };
-
+    bool ok = true;
     float acc[R][NT][4] = {};
-    constexpr int U = R > RING ? R : RING; // pieces per round: a multiple of R and of the ring
-    for (int it0 = 0; it0 < items; it0 += U) {
+    for (int ch = warp; ch < chunks; ch += warps) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int it = it0 + u;
-            if (it >= items) break;
-            if (u % R == 0) tokens(warp + it / R * warps);
-            const LinSeg va = wa[u % RING], vb = wb[u % RING];
-            fetch(u % RING, it + RING, (u + RING) % R);
-            const __half2 pa = e4m3x2_to_f16x2(va.s), pb = e4m3x2_to_f16x2(vb.s);
-            const uint32_t xa[4] = {va.c.x, va.c.y, va.c.z, va.c.w}, xb[4] = {vb.c.x, vb.c.y, vb.c.z, vb.c.w};
+        for (int n = 0; n < NT; ++n) {
+            if (!EARLY) fetch(ch, n);
+            convert(n);
+        }
+        if (EARLY && ch + warps < chunks) fetch(ch + warps, 0);
+#pragma unroll
+        for (int tile = 0; tile < R; ++tile) {
+            if (tile * 16 >= rows) break;
+            if (ch == warp) ok = ok && umma::mbar_wait_fast(umma::smem_u32(&b_tile[tile]), 0);
+            uint4 va, vb;
+            uint32_t sa, sb;
+            segment(tile, r, ch * 128 + c * 32, va, sa);
+            segment(tile, r + 8, ch * 128 + c * 32, vb, sb);
+            const __half2 pa = e4m3x2_to_f16x2(sa), pb = e4m3x2_to_f16x2(sb);
+            const uint32_t xa[4] = {va.x, va.y, va.z, va.w}, xb[4] = {vb.x, vb.y, vb.z, vb.w};
             float d[NT][2][4] = {};              // two sums: consecutive products do not wait for each other
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -253,12 +299,17 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float v = d[n][0][i] + d[n][1][i];
-                    acc[u % R][n][i] = SCALED ? fmaf(v, back[n][i & 1], acc[u % R][n][i]) : acc[u % R][n][i] + v;
+                    acc[tile][n][i] = SCALED ? fmaf(v, back[n][i & 1], acc[tile][n][i]) : acc[tile][n][i] + v;
                 }
         }
     }
+    // every copy has landed before the block's memory is used again or given up: each tile's barrier is waited
+    // for by warp 0 even where it has no chunk
+    if (warp == 0 && chunks == 0)
+        for (int i = 0; i < R; ++i) ok = ok && umma::mbar_wait_fast(umma::smem_u32(&b_tile[i]), 0);
     // ---- join the warps in order and store with the rows along the lanes
     float* red = reinterpret_cast<float*>(sm);   // [warp][token][R * 16 rows]
+    __syncthreads();                             // the weights are read no more
 #pragma unroll
     for (int tile = 0; tile < R; ++tile)
 #pragma unroll
@@ -266,7 +317,7 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int t = n * 8 + 2 * c + (i & 1);
-                if (t < T) red[(warp * T + t) * (R * 16) + tile * 16 + r + 8 * (i >> 1)] = acc[tile][n][i];
+                if (t < T) red[(warp * T + t) * (R * 16) + tile * 16 + r + 8 * (i >> 1)] = ok ? acc[tile][n][i] : __int_as_float(0x7fc00000);
             }
     __syncthreads();
     for (int u = tid; u < T * R * 16; u += blockDim.x) {
@@ -768,8 +819,10 @@ int lin_wide(const LinArgs& a) {
 }
 int lin_planes(int x_type) { return x_type == CSA2_F32 ? 2 : 1; }
 
-// the few-token kernel: up to 16 tokens, 8 where x has two parts
-bool lin_few(int x_type, int n_tok) { return n_tok <= (x_type == CSA2_F32 ? LF_TOK / 2 : LF_TOK); }
+// the few-token kernel: up to 16 tokens, 8 where x has two parts, of rows that fit a block's shared memory
+bool lin_few(int x_type, int n_tok, int n_in) {
+    return n_tok <= (x_type == CSA2_F32 ? LF_TOK / 2 : LF_TOK) && 9 * (int64_t)n_in + 32 <= LF_SMEM;
+}
 LinPrep lin_prep(int x_type, int n_tok, int n_in) {
     LinPrep p;
     p.nb = n_tok <= 32 ? 32 : n_tok <= 64 || x_type == CSA2_F32 ? 64 : 128;
@@ -781,36 +834,38 @@ LinPrep lin_prep(int x_type, int n_tok, int n_in) {
 
 template <typename TX, int NT, int R>
 cudaError_t lf_launch(const LinArgs& a, int x_vec, int warps, cudaStream_t st) {
-    const size_t smem = (size_t)warps * a.n_tok * R * 16 * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(k_linear_few<TX, NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         LF_MAXW * NT * 8 * R * 16 * (int)sizeof(float));
-    if (e != cudaSuccess) return e;
-    launch_k(k_linear_few<TX, NT, R>, dim3((a.n_out + 16 * R - 1) / (16 * R), a.n_groups), warps * 32, smem, st, a, x_vec,
-             lin_wide(a) >= 1 ? 1 : 0);
+    const size_t smem = std::max<size_t>((size_t)warps * a.n_tok * R * 16 * sizeof(float), R * (9 * (size_t)a.n_in + 32));
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(k_linear_few<TX, NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    launch_k(k_linear_few<TX, NT, R>, dim3((a.n_out + 16 * R - 1) / (16 * R), a.n_groups), warps * 32, smem, st, a, x_vec);
     note_launch();
     return cudaGetLastError();
 }
 template <typename TX, int NT>
 cudaError_t lf_pick(const LinArgs& a, int x_vec, cudaStream_t st) {
-    // Warps: as many as divide the chunks most evenly, up to 8
+    // Row tiles per block: four (the tokens' fragments are made once for all) when that still gives every SM
+    // blocks and two of them fit an SM's shared memory, else one
     const int chunks = std::max(1, (a.n_in + 127) / 128);
+    const int64_t tiles = (int64_t)((a.n_out + 15) / 16) * a.n_groups;
+    const bool four = tiles >= 152 * 4 && 4 * (9 * a.n_in + 32) <= LF_SMEM / 2;
+    // Warps: the most, up to 8, that divide the chunks (nearly) as evenly as any number does; up to 4 with four
+    // row tiles, so that four blocks stay on an SM (1,536 x 32,768, one token: 10.6 us against 13.6 with six)
+    const int most = std::min(chunks, four ? 4 : LF_MAXW);
     int warps = 1;
     double best = 0.0;
-    for (int w = std::min(chunks, 4); w <= LF_MAXW && w <= chunks; ++w) {
+    for (int w = std::min(chunks, 3); w <= most; ++w) {
         const double even = (double)chunks / ((double)w * ((chunks + w - 1) / w));
-        if (even > best + 0.02) best = even, warps = w;
+        if (even >= best - 0.02) best = std::max(best, even), warps = w;
     }
-    // Row tiles per block: four (the tokens' fragments are made once for all) when that still gives
-    // every SM a block, else one
-    const int64_t tiles = (int64_t)((a.n_out + 15) / 16) * a.n_groups;
-    if (tiles >= 152 * 4) return lf_launch<TX, NT, 4>(a, x_vec, warps, st);
-    return lf_launch<TX, NT, 1>(a, x_vec, warps, st);
+    return four ? lf_launch<TX, NT, 4>(a, x_vec, warps, st) : lf_launch<TX, NT, 1>(a, x_vec, warps, st);
 }
 template <typename TX>
 cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st) {
     const int x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_tok * (int64_t)sizeof(TX) % 16 == 0 &&
                       a.x_group * (int64_t)sizeof(TX) % 16 == 0;
-    if (lin_few(x_type, a.n_tok)) {
+    if (lin_few(x_type, a.n_tok, a.n_in)) {
         if constexpr (sizeof(TX) == 2)
             if (a.n_tok > 8) return lf_pick<TX, 2>(a, x_vec, st);
         return lf_pick<TX, 1>(a, x_vec, st);
@@ -860,7 +915,7 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
 }  // namespace
 
 size_t linear_fp4_ws(int x_type, int n_tok, int n_groups, int n_in) {
-    if (lin_few(x_type, n_tok)) return 0;
+    if (lin_few(x_type, n_tok, n_in)) return 0;
     const LinPrep p = lin_prep(x_type, n_tok, n_in);
     return LM_HEAD + (size_t)p.scales_at(n_groups) + (size_t)n_groups * n_tok * sizeof(float);
 }

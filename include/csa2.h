@@ -246,7 +246,7 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
  *   x       [n_tok][n_groups][n_in] of x_type, n_in contiguous, the other
  *           strides in elements; y [n_tok][n_groups][n_out] of y_type likewise
  *   codes   uint8 [n_groups][n_out][n_in/2], 16-byte aligned
- *   scales  uint8 [n_groups][n_out][n_in/16]
+ *   scales  uint8 [n_groups][n_out][n_in/16], 16-byte aligned
  * x_type, y_type: CSA2_BF16, CSA2_F16 or CSA2_F32.  n_in a multiple of 16,
  * at most 2^24; * n_tok, n_in and n_out may be 0 (n_in 0 gives zeros), n_groups <= 65535; x and
  * y aligned to their elements; y overlaps no input.  fp16 x enters exactly, bf16

@@ -104,6 +104,18 @@ def test_linear_inner_sizes(csa, K, T):
     check_linear(csa, T, 1, K, 33, BF, F, seed=K)
 
 
+@pytest.mark.parametrize("M,K", [(1, 20912), (17, 20928), (700, 5120), (20000, 48), (9999, 1040), (3, 32768)])
+def test_linear_few_tokens_of_long_and_short_rows(csa, M, K):
+    check_linear(csa, 3, 1, K, M, BF, F, seed=K)
+
+
+@pytest.mark.parametrize("M,K", [(5, 16), (33, 48), (35, 112), (1003, 1040)])
+@pytest.mark.parametrize("T", [1, 12])
+def test_linear_groups_off_16_byte_boundaries(csa, M, K, T):
+    """groups whose codes and scales start between 16-byte boundaries, up to the last byte of the tensors"""
+    check_linear(csa, T, 3, K, M, BF, F, seed=M)
+
+
 @pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 63, 64, 65, 127, 129, 1003, 5000])
 @pytest.mark.parametrize("T", [1, 40])
 def test_linear_outer_sizes(csa, M, T):

@@ -25,7 +25,7 @@ def linear(lib, x=P, xt=0, n_tok=1, groups=1, n_in=64, n_out=8, codes=P, scales=
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(xt=3), dict(yt=-1), dict(n_tok=-1), dict(groups=0), dict(groups=65536),
                                 dict(n_in=24), dict(n_in=-16), dict(n_in=(1 << 24) + 16), dict(n_out=-1), dict(codes=None), dict(scales=None),
-                                dict(codes=ctypes.c_void_p(264)), dict(alpha=float("nan")), dict(alpha=float("inf")),
+                                dict(codes=ctypes.c_void_p(264)), dict(scales=ctypes.c_void_p(264)), dict(alpha=float("nan")), dict(alpha=float("inf")),
                                 dict(y=None), dict(x=ctypes.c_void_p(257)), dict(x=ctypes.c_void_p(258), xt=2),
                                 dict(y=ctypes.c_void_p(258), yt=2)])
 def test_linear_refusals(csa, kw):
@@ -34,8 +34,8 @@ def test_linear_refusals(csa, kw):
 
 def test_linear_workspace(csa):
     size = lambda T, K, xt: csa.csa2_workspace_size(csa.OP_LINEAR_FP4, T, 1, xt, 0, K)
-    assert size(1, 4096, 0) == 0 and size(16, 1 << 20, 1) == 0
-    for T, K, xt in [(17, 64, 0), (300, 4096, 2), (100, 0, 1)]:
+    assert size(1, 4096, 0) == 0 and size(16, 8192, 1) == 0
+    for T, K, xt in [(17, 64, 0), (300, 4096, 2), (100, 0, 1), (1, 1 << 20, 0)]:
         need = size(T, K, xt)
         assert need > 0
         for kw in [dict(), dict(ws=P, ws_bytes=need - 1), dict(ws=ctypes.c_void_p(264), ws_bytes=need)]:
