@@ -82,7 +82,7 @@ struct NrArgs {
 template <typename TX, int VEC, int NCH, bool SWAP, bool FULL>
 __global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 : SWAP ? 3 : 4)
     k_norm_rope(const NrArgs g) {
-    extern __shared__ float2 cs[];           // [tokens of this block][d_rot / 2] (cos, sin); row buffers
+    extern __shared__ __align__(16) float2 cs[];     // [tokens of this block][d_rot / 2] (cos, sin); row buffers
     const bool isq = blockIdx.x < g.q_blocks;
     const NrRows R = g.set[isq ? 0 : 1];
     const int heads = R.heads, d = g.d, d_rot = g.d_rot, half = d_rot / 2, keep = d - d_rot;
@@ -181,9 +181,14 @@ __global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 
                     mul2_rn(a[c][e], a[c][VEC > 1 ? e + 1 : e], w0, w1);
                 }
             }
-            if (SWAP && live && (FULL || j < d) && j >= keep)
+            if (SWAP && live && (FULL || j < d) && j >= keep) {
+                if constexpr (VEC == 1)
+                    buf[j - keep] = a[c][0];
+                else
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) buf[j - keep + e] = a[c][e];
+                    for (int e = 0; e < VEC; e += 4)
+                        *reinterpret_cast<float4*>(buf + j - keep + e) = make_float4(a[c][e], a[c][e + 1], a[c][e + 2], a[c][e + 3]);
+            }
         }
         if (SWAP) __syncwarp();
 #pragma unroll
@@ -200,14 +205,24 @@ __global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 
                         a[c][e] = p0 * z.x - p1 * z.y;
                         a[c][e + 1] = p0 * z.y + p1 * z.x;
                     }
-                } else {
+                } else if (VEC == 1) {
+                    const bool first = g.halves ? u < half : !(u & 1);
+                    const float p = buf[g.halves ? (first ? u + half : u - half) : (u ^ 1)];
+                    const float2 z = tab[g.halves ? (first ? u : u - half) : u >> 1];
+                    a[c][0] = first ? a[c][0] * z.x - p * z.y : p * z.y + a[c][0] * z.x;
+                } else {                                     // halves: a whole access lies on one side
+                    const bool first = u < half;
+                    const float* p = buf + (first ? u + half : u - half);
+                    const float4* z = reinterpret_cast<const float4*>(tab + (first ? u : u - half));
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const int ue = u + e;
-                        const bool first = g.halves ? ue < half : !(ue & 1);
-                        const float p = buf[g.halves ? (first ? ue + half : ue - half) : (ue ^ 1)];
-                        const float2 z = tab[g.halves ? (first ? ue : ue - half) : ue >> 1];
-                        a[c][e] = first ? a[c][e] * z.x - p * z.y : p * z.y + a[c][e] * z.x;
+                    for (int e = 0; e + 3 < VEC; e += 4) {
+                        const float4 q4 = *reinterpret_cast<const float4*>(p + e);
+                        const float4 z0 = z[e / 2], z1 = z[e / 2 + 1];
+                        const float pp[4] = {q4.x, q4.y, q4.z, q4.w}, cc[4] = {z0.x, z0.z, z1.x, z1.z},
+                                    sn[4] = {z0.y, z0.w, z1.y, z1.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            a[c][e + i] = first ? a[c][e + i] * cc[i] - pp[i] * sn[i] : pp[i] * sn[i] + a[c][e + i] * cc[i];
                     }
                 }
             }
@@ -255,6 +270,7 @@ cudaError_t nr_launch(const NrRows& q, const NrRows& k, int64_t n_tok, int d, in
             rounds[i] *= 2;
         cs = std::max(cs, table(heads[i], rounds[i]));
     }
+    cs = (cs + 1) & ~1;                          // the row buffers start on 16 bytes
     const int rq = rounds[0] * slots, rk = rounds[1] * slots;
     const int64_t qb = (n_tok * q.heads + rq - 1) / rq, kb = (n_tok * k.heads + rk - 1) / rk;
     if (qb + kb > 0x7fffffff) return cudaErrorInvalidConfiguration;
