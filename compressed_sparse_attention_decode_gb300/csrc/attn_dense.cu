@@ -52,7 +52,8 @@ constexpr int DA_MMA1 = 8;                           // warps 8, 9: score MMAs
 constexpr int DA_MMA2 = 10;                          // warps 10, 11: value MMAs
 constexpr int DA_LOADW = 12;                         // warps 12-19: rows
 constexpr int DA_LOADERS = 256;
-constexpr int DA_NL = 2;                             // L buffers
+constexpr int DA_NL = 2;                             // L buffers: a window has at most as many tiles
+static_assert(WINDOW <= DA_NL * DA_TILE && DA_TILE == 64, "the window's tiles have a buffer each");
 constexpr uint32_t DA_QSLAB = DA_H * 128;            // 64 heads x 64 dims fp16, 128-byte swizzle
 constexpr uint32_t DA_LSLAB = DA_TILE * 128;         // 64 keys x 64 dims
 constexpr uint32_t DA_SQ = 0;                        // Q: 8 slabs
@@ -297,31 +298,46 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
 
         if (warp >= DA_LOADW) {
             if (window) {
-                // ================= window rows: bf16, one scale for all of them
+                // ================= window rows: bf16, at most two tiles, so every tile has a buffer.  They are converted
+                // as they are while their largest magnitude is found, and once more where it asks for a scale.
                 const uint4* src = reinterpret_cast<const uint4*>(a.swa + ((int64_t)w.b * a.swa_len + row0) * D_LAT);
+                for (int t = 0; t < T; ++t) {
+                    const uint32_t tg = tb + t;
+                    if (tg >= DA_NL) ok = ok && umma::mbar_wait_fast(sa(&b_lfree[tg % DA_NL]), (tg / DA_NL - 1) & 1);
+                }
                 uint32_t mx = 0u;
-                for (int v = lt; v < rows * 64; v += DA_LOADERS) mx = max(mx, bf16_absmax8(src[v]));
+                auto convert = [&](float d) {
+#pragma unroll 1
+                    for (int v0 = lt; v0 < T * DA_TILE * 64; v0 += 8 * DA_LOADERS) {
+                        uint4 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int v = v0 + i * DA_LOADERS;
+                            x[i] = make_uint4(0, 0, 0, 0);
+                            if (v < rows * 64) x[i] = src[v];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int v = v0 + i * DA_LOADERS, t = v >> 12, r = (v >> 6) & 63, c = v & 63;
+                            mx = max(mx, bf16_absmax8(x[i]));
+                            *reinterpret_cast<uint4*>(sm + DA_SL + ((tb + t) % DA_NL) * DA_LBUF + (c >> 3) * DA_LSLAB + da_swz(r, c & 7)) =
+                                bf16x8_to_f16x8(x[i], d);
+                        }
+                    }
+                };
+                convert(1.0f);
                 mx = __reduce_max_sync(0xffffffffu, mx);
                 if (lane == 0) atomicMax(wmax, mx);
                 umma::bar_named(2, DA_LOADERS);
-                const float d = pow2f(-f16_range_exp(*reinterpret_cast<volatile unsigned int*>(wmax)));
-                for (int t = 0; t < T; ++t) {              // at most two tiles
-                    const uint32_t tg = tb + t, buf = tg % DA_NL;
-                    uint8_t* L = sm + DA_SL + buf * DA_LBUF;
-                    if (tg >= DA_NL) ok = ok && umma::mbar_wait_fast(sa(&b_lfree[buf]), (tg / DA_NL - 1) & 1);
-                    for (int v = lt; v < DA_TILE * 64; v += DA_LOADERS) {
-                        const int r = v >> 6, c = v & 63;
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (t * DA_TILE + r < rows) x = src[t * DA_TILE * 64 + v];
-                        *reinterpret_cast<uint4*>(L + (c >> 3) * DA_LSLAB + da_swz(r, c & 7)) = bf16x8_to_f16x8(x, d);
+                const int e = f16_range_exp(*reinterpret_cast<volatile unsigned int*>(wmax));
+                if (e != 0) convert(pow2f(-e));
+                umma::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0)
+                    for (int t = 0; t < T; ++t) {
+                        umma::mbar_arrive(sa(&b_lhalf[(tb + t) % DA_NL]));
+                        umma::mbar_arrive(sa(&b_lfull[(tb + t) % DA_NL]));
                     }
-                    umma::fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        umma::mbar_arrive(sa(&b_lhalf[buf]));
-                        umma::mbar_arrive(sa(&b_lfull[buf]));
-                    }
-                }
             } else {
                 // ================= FP4 rows
                 for (int t = 0; t < T; ++t) {
