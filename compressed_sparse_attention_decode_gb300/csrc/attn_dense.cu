@@ -120,12 +120,44 @@ __device__ __forceinline__ DenseWork da_work(const DenseArgs& a, int item) {
     return w;
 }
 
-__global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a) {
+// One share of a block, and where the block's units go on after it
+struct DenseShare {
+    int64_t row;                 // its first row: of the FP4 planes, or of the window rows
+    int64_t gq, u, start;        // its query; the next unit, and the first unit of the item that has it
+    int h0, rows, share, item, next_item, window;
+};
+// The next share of the units u .. u1-1, `item` with units from `start` on being the one that has unit u;
+// rows = -1 when there is none.  One thread calls it while the block works on the share before, so that
+// this state lives in shared memory and not in everybody's registers.
+__device__ __noinline__ void da_next(const DenseArgs& a, int64_t u, int64_t u1, int64_t start, int item, DenseShare* out) {
+    while (u < u1) {
+        const DenseWork w = da_work(a, item);
+        const int tiles = w.tiles();
+        const int64_t end = start + tiles + w.win();
+        const bool window = u >= start + tiles;
+        const int rest = window ? 0 : (int)(min(u1, start + tiles) - u);     // tiles of this share
+        const bool run = !window || (u == start + tiles && w.win() > 0);     // not the rest of another block's window
+        const int64_t row0 = window ? w.row0 : (u - start) * DA_TILE;
+        out->row = window ? (int64_t)w.b * a.swa_len + row0 : (int64_t)w.b * a.capacity + row0;
+        out->rows = window ? w.rows : (int)min((int64_t)rest * DA_TILE, w.n - row0);
+        out->share = window ? a.n_items + (int)gridDim.x - 1 + item : item + (int)blockIdx.x;
+        out->gq = w.gq, out->h0 = w.h0, out->item = item, out->window = window;
+        u = window ? end : u + rest;
+        if (u >= end) start = end, ++item;
+        if (run) {
+            out->u = u, out->start = start, out->next_item = item;
+            return;
+        }
+    }
+    out->rows = -1;
+}
+
+__global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_constant__ DenseArgs a) {
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) unsigned long long b_lhalf[DA_NL], b_lfull[DA_NL], b_lfree[DA_NL], b_sfull[2], b_sfree[2],
         b_pfull[2], b_odone[2];
-    __shared__ int64_t wsum[DA_THREADS / 32], first_start;
-    __shared__ int first_item;
+    __shared__ int64_t wsum[DA_THREADS / 32], last_unit;
+    __shared__ DenseShare shares[2];
     __shared__ uint32_t tmem_base;
     const uint32_t raw = umma::smem_u32(dyn);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -191,11 +223,13 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
         for (int k = 0; k < 2; ++k)
             if (k < ni) {
                 const int64_t e = s + tl[k] + wn[k];
-                if (s <= u0 && u0 < e) first_item = i0 + k, first_start = s;
+                if (u0 < u1 && s <= u0 && u0 < e) da_next(a, u0, u1, s, i0 + k, &shares[0]);
                 if (blockIdx.x == 0) a.items[i0 + k] = DenseItem{s, tl[k], wn[k]};
                 s = e;
             }
         if (blockIdx.x == 0 && tid == 0) a.items[a.n_items].start = total;
+        if (tid == 0) last_unit = u1;
+        if (tid == 0 && u0 >= u1) shares[0].rows = -1;
     }
     umma::fence_before();
     __syncthreads();
@@ -203,31 +237,18 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
     const uint32_t tmem = tmem_base;
     bool ok = true;
     const int lt = tid - DA_LOADW * 32;
-    int item = u0 < u1 ? first_item : 0, q_item = -1;        // the item whose queries are staged
-    int64_t start = u0 < u1 ? first_start : 0, u = u0;
+    int q_item = -1;                                         // the item whose queries are staged
     uint32_t tb = 0;                                         // tiles done so far: the rings go on from share to share
 
-    while (u < u1) {
-        const DenseWork w = da_work(a, item);
-        const int tiles = w.tiles();
-        const int64_t end = start + tiles + w.win();
-        const bool window = u >= start + tiles;
-        const int rest = window ? 0 : (int)(min(u1, start + tiles) - u);     // tiles of this share
-        const bool run = window ? u == start + tiles && w.win() > 0 : true;
-        const int64_t row0 = window ? w.row0 : (u - start) * DA_TILE;
-        const int rows = window ? w.rows : (int)min((int64_t)rest * DA_TILE, w.n - row0);
-        const int share = window ? a.n_items + (int)gridDim.x - 1 + item : item + (int)blockIdx.x;
-        const int this_item = item;
-        u = window ? end : u + rest;
-        if (u >= end) start = end, ++item;
-        if (!run) continue;                                  // the rest of another block's window
-        const int T = (rows + DA_TILE - 1) / DA_TILE;
-        const int nh = min(DA_H, a.n_heads - w.h0);
+    for (int cur = 0; shares[cur].rows >= 0; cur ^= 1) {
+        const DenseShare& S = shares[cur];
+        const int rows = S.rows, T = (rows + DA_TILE - 1) / DA_TILE;
+        const bool window = S.window;
 
         // FP4 rows: a tile is 64 rows x 16 units of 32 dims (16 bytes of codes, 2 of scales); the first one is
         // fetched before the block meets
-        const uint8_t* codes = a.codes + ((int64_t)w.b * a.capacity + row0) * (D_LAT / 2);
-        const uint8_t* scales = a.scales + ((int64_t)w.b * a.capacity + row0) * (D_LAT / 16);
+        const uint8_t* codes = a.codes + S.row * (D_LAT / 2);
+        const uint8_t* scales = a.scales + S.row * (D_LAT / 16);
         constexpr int NU = DA_TILE * 16 / DA_LOADERS;
         // unit u: a warp takes 4 rows x 8 units, so that a load touches whole 128-byte lines and the
         // 8 threads of a quarter warp write different bank groups; units below 512 hold dims 0-255
@@ -258,12 +279,16 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
         umma::fence_before();
         __syncthreads();
         umma::fence_after();
-        if (tid == 0) *wmax = 0u;
+        if (tid == 0) {
+            *wmax = 0u;
+            da_next(a, S.u, last_unit, S.start, S.next_item, &shares[cur ^ 1]);
+        }
         if (tid < DA_H) m_run[tid] = -INFINITY;
         // Q: heads h0 .. h0+63 (zero rows past n_heads), bf16 -> fp16 slabs, by warps 0-11; a head whose largest
         // magnitude lies outside [2^-10, 2^15) is scaled by a power of two on the way
-        if (q_item != this_item && warp < DA_LOADW) {
-            const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + (w.gq * a.n_heads + w.h0) * D_LAT);
+        if (q_item != S.item && warp < DA_LOADW) {
+            const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + (S.gq * a.n_heads + S.h0) * D_LAT);
+            const int nh = min(DA_H, a.n_heads - S.h0);
             constexpr int HPW = (DA_H + DA_LOADW - 1) / DA_LOADW;
             uint4 qv[HPW][2];
 #pragma unroll
@@ -293,14 +318,14 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
             }
             umma::fence_proxy_async();
         }
-        q_item = this_item;
+        q_item = S.item;
         __syncthreads();
 
         if (warp >= DA_LOADW) {
             if (window) {
                 // ================= window rows: bf16, at most two tiles, so every tile has a buffer.  They are converted
                 // as they are while their largest magnitude is found, and once more where it asks for a scale.
-                const uint4* src = reinterpret_cast<const uint4*>(a.swa + ((int64_t)w.b * a.swa_len + row0) * D_LAT);
+                const uint4* src = reinterpret_cast<const uint4*>(a.swa + S.row * D_LAT);
                 for (int t = 0; t < T; ++t) {
                     const uint32_t tg = tb + t;
                     if (tg >= DA_NL) ok = ok && umma::mbar_wait_fast(sa(&b_lfree[tg % DA_NL]), (tg / DA_NL - 1) & 1);
@@ -532,15 +557,16 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const DenseArgs a)
             lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
             if (par == 0) red[half * DA_H + h] = lsum;
             umma::bar_named(1, DA_SMT);
-            if (tid < DA_H) a.part_ml[(int64_t)share * DA_H + tid] = make_float2(m_run[tid], red[tid] + red[DA_H + tid]);
+            if (tid < DA_H) a.part_ml[(int64_t)S.share * DA_H + tid] = make_float2(m_run[tid], red[tid] + red[DA_H + tid]);
             // ---- this share's O^T (the window's back on the common scale) to the workspace, [head][dim]
             const uint32_t tl = tb + T - 1;
             ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
             umma::fence_after();
             const float up = window ? pow2f(f16_range_exp(*wmax)) : 1.0f;
+            const int nh = min(DA_H, a.n_heads - S.h0);
 #pragma unroll 1
             for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
-                float* dst = a.part_o + (int64_t)share * DA_H * D_LAT + mt * 128 + qd * 32 + lane;
+                float* dst = a.part_o + (int64_t)S.share * DA_H * D_LAT + mt * 128 + qd * 32 + lane;
 #pragma unroll 1
                 for (int c = 0; c < nh; c += 16) {
                     float v[16];
