@@ -309,6 +309,13 @@ def csa2_sparse_attn(cache, q, q_pos, idx, swa, swa_pos0, scale=D_LAT ** -0.5, o
     return out, lse
 
 
+# Scratch of one call, from PyTorch's allocator but for the stream that the call runs on (a tensor would belong
+# to the current stream, and be given to other work there while this stream still uses it): freed as soon as the
+# call is enqueued, it goes to later work of the same stream alone.
+_scratch_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
+_scratch_free = torch._C._cuda_cudaCachingAllocator_raw_delete
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
@@ -319,7 +326,8 @@ def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, ws=No
     x bf16 / fp16 / fp32 [T, n_in] with codes uint8 [n_out, n_in/2] and scales uint8 [n_out, n_in/16], or
     x [T, G, n_in] with codes [G, n_out, n_in/2] and scales [G, n_out, n_in/16] (a product per group).
     Rows of x and out are contiguous, their other strides free.  Returns [T, n_out] or [T, G, n_out]
-    of out_dtype (default: that of x)."""
+    of out_dtype (default: that of x).  With a stream other than the current one, give `out` (a new one
+    belongs to the current stream); without ws the scratch is taken for the call's own stream."""
     xs, ms = x.shape, codes.shape
     if len(xs) == 2:
         (T, n_in), G, lead, x_group = xs, 1, 0, 0
@@ -341,15 +349,19 @@ def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, ws=No
     x_type, y_type = _TYPES.get(x.dtype), _TYPES.get(out.dtype)
     _need(x_type is not None and y_type is not None, "x and out: bf16, fp16 or fp32")
     _need((x.stride(-1) == 1 or n_in == 0) and (n_out <= 1 or out.stride(-1) == 1), "rows of x and out: contiguous")
-    lib = load()
-    if ws is None:
-        n = lib.csa2_workspace_size(OP_LINEAR_FP4, T, G, x_type, 0, n_in) if T > 8 or n_in > 16384 else 0   # none for few tokens
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-    st = lib.csa2_linear_fp4(x.data_ptr(), x_type, x.stride(0), x_group, T, G, n_in, n_out, codes.data_ptr(),
-                             scales.data_ptr(), alpha, out.data_ptr(), y_type, out.stride(0), out.stride(1) if lead else 0,
-                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _stream(stream))
-    if st:
-        raise Csa2Error(st, "csa2_linear_fp4")
+    lib, st, own = load(), _stream(stream), 0
+    if ws is not None:
+        p_ws, n_ws = ws.data_ptr(), ws.numel()
+    else:
+        n_ws = lib.csa2_workspace_size(OP_LINEAR_FP4, T, G, x_type, 0, n_in) if T > 8 or n_in > 16384 else 0   # none for few tokens
+        p_ws = own = _scratch_alloc(n_ws, st) if n_ws else 0
+    status = lib.csa2_linear_fp4(x.data_ptr(), x_type, x.stride(0), x_group, T, G, n_in, n_out, codes.data_ptr(),
+                                 scales.data_ptr(), alpha, out.data_ptr(), y_type, out.stride(0),
+                                 out.stride(1) if lead else 0, p_ws, n_ws, st)
+    if own:
+        _scratch_free(own)
+    if status:
+        raise Csa2Error(status, "csa2_linear_fp4")
     return out
 
 
@@ -408,7 +420,9 @@ def csa2_dense_attn(cache, q, q_pos, swa, swa_pos0, scale=D_LAT ** -0.5, out=Non
     """Attention over every visible entry of the cache and the window: q bf16 [B, n_q, H, 512]; q_pos
     int64 [B, n_q]; swa bf16 [B, swa_len, 512] or None, row r of sequence b at raw position
     swa_pos0[b] + r (int64 [B] on the device, or None: zeros).  Returns (out [B, n_q, H, 512], lse
-    fp32 [B, n_q, H] or None)."""
+    fp32 [B, n_q, H] or None).  With a stream other than the current one, give out and lse (new ones
+    belong to the current stream); without ws the scratch is taken for the call's own stream, and a
+    bounded wait that gave up cannot be polled."""
     B, n_q, H, D = q.shape
     codes = cache.lat_codes
     _need(q.dtype is torch.bfloat16 and q.is_contiguous() and D == D_LAT and B == cache.batch,
@@ -432,12 +446,18 @@ def csa2_dense_attn(cache, q, q_pos, swa, swa_pos0, scale=D_LAT ** -0.5, out=Non
         lse = torch.empty((B, n_q, H), dtype=torch.float32, device=q.device)
     _need(lse is None or (lse.dtype is torch.float32 and lse.shape == (B, n_q, H) and lse.is_contiguous()),
           "lse: contiguous fp32 [batch, n_q, heads]")
-    if ws is None:
-        ws = workspace(OP_DENSE_ATTN, B, n_q, H, 0, cache.capacity, q.device)
+    lib, st, own = load(), _stream(stream), 0
+    if ws is not None:
+        p_ws, n_ws = ws.data_ptr(), ws.numel()
+    else:
+        n_ws = lib.csa2_workspace_size(OP_DENSE_ATTN, B, n_q, H, 0, cache.capacity)
+        p_ws = own = _scratch_alloc(n_ws, st) if n_ws else 0
     c = _PACK_CACHE(codes.data_ptr(), cache.lat_scales.data_ptr(), 0, 0, B, cache.capacity, D_LAT, 128, cache.ratio)
-    st = load().csa2_dense_attn(c, q.data_ptr(), n_q, H, q_pos.data_ptr(), p_swa,
-                                None if swa_pos0 is None else swa_pos0.data_ptr(), n_swa, scale, out.data_ptr(), o_type,
-                                None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
-    if st:
-        raise Csa2Error(st, "csa2_dense_attn")
+    status = lib.csa2_dense_attn(c, q.data_ptr(), n_q, H, q_pos.data_ptr(), p_swa,
+                                 None if swa_pos0 is None else swa_pos0.data_ptr(), n_swa, scale, out.data_ptr(), o_type,
+                                 None if lse is None else lse.data_ptr(), p_ws, n_ws, st)
+    if own:
+        _scratch_free(own)
+    if status:
+        raise Csa2Error(status, "csa2_dense_attn")
     return out, lse

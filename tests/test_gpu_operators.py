@@ -516,3 +516,30 @@ def test_operators_on_another_stream(csa):
     for u, v in zip(a, b):
         assert torch.equal(u, v)
     assert csa.csa2_poll_error(ws, s) == csa.OK
+
+
+def test_scratch_belongs_to_the_stream_of_the_call(csa):
+    """calls without a workspace on a side stream, while the current stream takes and overwrites whatever memory
+    is free: their scratch is not handed to it"""
+    g = gen(13)
+    s = torch.cuda.Stream()
+    codes, scales = fp4((2048, 2048), g)
+    x = randn((100, 2048), g)
+    want = csa.csa2_linear_fp4(x, codes, scales)
+    lat, _ = fp4((4, 3000, 512), g)
+    cache = csa.Cache.of(lat, torch.full((4, 3000, 32), 0x30, dtype=torch.uint8, device="cuda"), ratio=1)
+    q, pos = randn((4, 1, 64, 512), g, BF), torch.full((4, 1), 3100, dtype=torch.int64, device="cuda")
+    dense = csa.csa2_dense_attn(cache, q, pos, None, None)[0]
+    torch.cuda.synchronize()
+    n = csa.csa2_workspace_size(csa.OP_LINEAR_FP4, 100, 1, 2, 0, 2048)
+    m = csa.csa2_workspace_size(csa.OP_DENSE_ATTN, 4, 1, 64, 0, 3000)
+    outs = [(torch.empty_like(want), torch.empty_like(dense)) for _ in range(20)]
+    torch.cuda.synchronize()
+    for y, o in outs:
+        csa.csa2_linear_fp4(x, codes, scales, out=y, stream=s)
+        csa.csa2_dense_attn(cache, q, pos, None, None, out=o, stream=s)
+        for size in (n, m):
+            torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    torch.cuda.synchronize()
+    for y, o in outs:
+        assert torch.equal(y, want) and torch.equal(o, dense)
