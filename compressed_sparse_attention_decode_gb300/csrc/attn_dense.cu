@@ -487,16 +487,16 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
                 }
                 const float mh = m_run[h];
                 const int left = rows - t * DA_TILE - 32 * half;     // valid keys of this half
-                bool exceed = false;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    x[i] = par + 2 * i < left ? x[i] * mul : -INFINITY;
-                    exceed |= x[i] > mh + DA_LAZY;
-                }
-                if (umma::bar_red_or(1, DA_SMT, exceed)) {
-                    float mx = -INFINITY;
+                for (int i = 0; i < 16; ++i) x[i] *= mul;
+                if (left < 32)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[i]);
+                    for (int i = 0; i < 16; ++i)
+                        if (par + 2 * i >= left) x[i] = -INFINITY;
+                float mx = x[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
+                if (umma::bar_red_or(1, DA_SMT, mx > mh + DA_LAZY)) {
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     if (par == 0) red[half * DA_H + h] = mx;
                     umma::bar_named(1, DA_SMT);
@@ -534,11 +534,13 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
                 }
                 if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_odone[sb]), ((tg >> 1) - 1) & 1);   // P buffer free
                 const float m = m_run[h];
+                float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    x[i] = (x[i] == -INFINITY || m == -INFINITY) ? 0.0f : umma::ex2_ftz(x[i] - m);
-                    lsum += x[i];
+                    x[i] = umma::ex2_ftz(x[i] - m);              // 0 for a masked key; m is finite: a tile has a key
+                    sum[i & 1] += x[i];
                 }
+                lsum += sum[0] + sum[1];
                 // row h of P^T: trade half of the values with the lane of the other parity for 16 consecutive keys
                 float rv[8];
 #pragma unroll
