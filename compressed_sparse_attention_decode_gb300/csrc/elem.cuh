@@ -58,6 +58,32 @@ struct ElemVec {
             *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
         }
     }
+    // the same one element at a time, for rows that the wide accesses' alignment does not hold for
+    __device__ __forceinline__ void load_each(const T* p) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * i;
+                w[i] = q[0] | (N > 1 ? (uint32_t)q[N > 1 ? 1 : 0] << 16 : 0u);
+            }
+        }
+    }
+    __device__ __forceinline__ void store_each(T* p) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                uint16_t* q = reinterpret_cast<uint16_t*>(p) + 2 * i;
+                q[0] = (uint16_t)w[i];
+                if (N > 1) q[N > 1 ? 1 : 0] = (uint16_t)(w[i] >> 16);
+            }
+        }
+    }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4)
             return __uint_as_float(w[i]);

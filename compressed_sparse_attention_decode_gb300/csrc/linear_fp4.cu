@@ -109,19 +109,10 @@ __device__ __forceinline__ void lin_split(const ElemVec<TX, 8>& v, float d, uint
 template <typename TX>
 __device__ __forceinline__ ElemVec<TX, 8> lin_load8(const TX* p, bool vec) {
     ElemVec<TX, 8> v;
-    if (vec) {
+    if (vec)
         v.load(p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < ElemVec<TX, 8>::WORDS; ++i) v.w[i] = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (sizeof(TX) == 4)
-                v.w[e] = reinterpret_cast<const uint32_t*>(p)[e];
-            else
-                v.w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
-        }
-    }
+    else
+        v.load_each(p);
     return v;
 }
 

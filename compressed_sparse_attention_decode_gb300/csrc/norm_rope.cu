@@ -72,11 +72,12 @@ struct NrArgs {
     const int64_t* pos;
     const float* inv_freq;
     float eps, inv_d;
-    int norm, halves, inverse, y_type;
+    int norm, halves, inverse, y_type, x_wide, y_wide;
 };
 
 // VEC consecutive elements per access, NCH accesses per lane and row (up to NCH unless FULL).  SWAP: a
-// pair's two values lie in different lanes and meet in a row buffer.  Issue slots are what this kernel
+// pair's two values lie in different lanes and meet in a row buffer.  Rows whose alignment does not hold for
+// wide accesses are read or written an element at a time (never FULL).  Issue slots are what this kernel
 // runs out of first (a 1 KB row is 45 clocks of its SM's share of HBM), so sizes are compile-time where
 // the common shapes allow and the products go two at a time.
 template <typename TX, int VEC, int NCH, bool SWAP, bool FULL>
@@ -120,8 +121,10 @@ __global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int j = (sub + c * lanes) * VEC;
-            if (FULL || j < d)
+            if (FULL || (j < d && g.x_wide))
                 v[c].load(x + j);
+            else if (j < d)
+                v[c].load_each(x + j);
             else
 #pragma unroll
                 for (int k = 0; k < ElemVec<TX, VEC>::WORDS; ++k) v[c].w[k] = 0u;
@@ -226,18 +229,24 @@ __global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 
                     }
                 }
             }
+            const auto put = [&](const auto& o, auto* p) {
+                if (FULL || g.y_wide)
+                    o.store(p);
+                else
+                    o.store_each(p);
+            };
             if (g.y_type == CSA2_BF16) {
                 ElemVec<__nv_bfloat16, VEC> o;
                 o.pack(a[c]);
-                o.store(reinterpret_cast<__nv_bfloat16*>(R.y) + y0 + j);
+                put(o, reinterpret_cast<__nv_bfloat16*>(R.y) + y0 + j);
             } else if (g.y_type == CSA2_F16) {
                 ElemVec<__half, VEC> o;
                 o.pack(a[c]);
-                o.store(reinterpret_cast<__half*>(R.y) + y0 + j);
+                put(o, reinterpret_cast<__half*>(R.y) + y0 + j);
             } else {
                 ElemVec<float, VEC> o;
                 o.pack(a[c]);
-                o.store(reinterpret_cast<float*>(R.y) + y0 + j);
+                put(o, reinterpret_cast<float*>(R.y) + y0 + j);
             }
         }
         if (SWAP) __syncwarp();                              // the row buffer is read before the next row writes it
@@ -254,7 +263,8 @@ namespace {
 
 template <typename TX, int VEC, int NCH>
 cudaError_t nr_launch(const NrRows& q, const NrRows& k, int64_t n_tok, int d, int d_rot, const int64_t* pos,
-                      const float* inv_freq, float eps, int norm, int halves, int inverse, int y_type, cudaStream_t st) {
+                      const float* inv_freq, float eps, int norm, int halves, int inverse, int y_type, int x_wide, int y_wide,
+                      cudaStream_t st) {
     int lanes = 1;
     while (lanes < 32 && lanes * VEC < d) lanes *= 2;
     const int slots = NR_THREADS / lanes;
@@ -275,10 +285,10 @@ cudaError_t nr_launch(const NrRows& q, const NrRows& k, int64_t n_tok, int d, in
     const int64_t qb = (n_tok * q.heads + rq - 1) / rq, kb = (n_tok * k.heads + rk - 1) / rk;
     if (qb + kb > 0x7fffffff) return cudaErrorInvalidConfiguration;
     // the angles, and one row's rotated values per slot where a pair's values lie in different lanes
-    const bool swap = VEC == 1 || halves, full = VEC == 8 && NCH <= 2 && d == lanes * VEC * NCH;
+    const bool swap = VEC == 1 || halves, full = VEC == 8 && NCH <= 2 && d == lanes * VEC * NCH && x_wide && y_wide;
     const size_t smem = cs * sizeof(float2) + (swap ? (size_t)slots * d_rot * sizeof(float) : 0);
     const NrArgs a{{q, k}, n_tok, (unsigned)qb, {rq, rk}, lanes, d, d_rot, cs, pos, inv_freq, eps, 1.0f / (float)d,
-                   norm, halves, inverse, y_type};
+                   norm, halves, inverse, y_type, x_wide, y_wide};
     void (*kern)(NrArgs) = k_norm_rope<TX, VEC, NCH, true, false>;
     if constexpr (VEC > 1) {
         constexpr bool F = VEC == 8 && NCH <= 2;
@@ -294,11 +304,11 @@ cudaError_t nr_launch(const NrRows& q, const NrRows& k, int64_t n_tok, int d, in
     return cudaGetLastError();
 }
 
-// vec: the widest access that pointers, strides, sizes and the rotation's boundaries allow
+// vec: the widest piece that the sizes and the rotation's boundaries allow
 template <typename TX, typename... A>
 cudaError_t nr_pick(int vec, int d, A... a) {
     if (vec == 8) return d <= 256 ? nr_launch<TX, 8, 1>(a...) : d <= 512 ? nr_launch<TX, 8, 2>(a...) : nr_launch<TX, 8, 4>(a...);
-    if (vec == 4) return d <= 512 ? nr_launch<TX, 4, 4>(a...) : nr_launch<TX, 4, 8>(a...);
+    if (vec == 4) return d <= 128 ? nr_launch<TX, 4, 1>(a...) : d <= 512 ? nr_launch<TX, 4, 4>(a...) : nr_launch<TX, 4, 8>(a...);
     return d <= 128 ? nr_launch<TX, 1, 4>(a...) : d <= 512 ? nr_launch<TX, 1, 16>(a...) : nr_launch<TX, 1, 32>(a...);
 }
 
@@ -311,24 +321,22 @@ cudaError_t launch_norm_rope(const csa2_head_rows* q, const csa2_head_rows* k, i
               inverse = !!(flags & CSA2_ROPE_INVERSE);
     const int xs = x_type == CSA2_F32 ? 4 : 2, ys = y_type == CSA2_F32 ? 4 : 2;
     NrRows rows[2] = {};
-    int vec = 8;
+    int vec = 1, x_wide = 1, y_wide = 1;
+    for (int v = 8; v >= 4 && vec == 1; v /= 2)
+        if (d % v == 0 && d_rot % v == 0 && (!halves || d_rot / 2 % v == 0)) vec = v;
+    // a piece moves min(16, vec * size) aligned bytes at a time
+    const int xb = std::min(16, vec * xs), yb = std::min(16, vec * ys);
     const csa2_head_rows* in[2] = {q, k};
     for (int i = 0; i < 2; ++i) {
         if (!in[i] || in[i]->n_heads == 0) continue;
         const csa2_head_rows& r = *in[i];
         rows[i] = NrRows{r.x, r.y, r.weight, r.x_tok, r.x_head, r.y_tok, r.y_head, r.n_heads};
-        for (int v = 8; v >= 4; v /= 2) {
-            // an access of v elements moves min(16, v * size) aligned bytes at a time
-            const int xb = v * xs < 16 ? v * xs : 16, yb = v * ys < 16 ? v * ys : 16;
-            const bool fits = reinterpret_cast<uintptr_t>(r.x) % xb == 0 && reinterpret_cast<uintptr_t>(r.y) % yb == 0 &&
-                              r.x_tok * xs % xb == 0 && r.x_head * xs % xb == 0 && r.y_tok * ys % yb == 0 &&
-                              r.y_head * ys % yb == 0 && d % v == 0 && d_rot % v == 0 && (!halves || d_rot / 2 % v == 0);
-            if (!fits && vec >= v) vec = v == 8 ? 4 : 1;
-        }
+        x_wide &= reinterpret_cast<uintptr_t>(r.x) % xb == 0 && r.x_tok * xs % xb == 0 && r.x_head * xs % xb == 0;
+        y_wide &= reinterpret_cast<uintptr_t>(r.y) % yb == 0 && r.y_tok * ys % yb == 0 && r.y_head * ys % yb == 0;
     }
     const auto pick = [&](auto tx) {
         return nr_pick<decltype(tx)>(vec, d, rows[0], rows[1], (int64_t)n_tok, d, d_rot, pos, inv_freq, eps, norm, halves,
-                                     inverse, y_type, st);
+                                     inverse, y_type, x_wide, y_wide, st);
     };
     if (x_type == CSA2_BF16) return pick(__nv_bfloat16());
     if (x_type == CSA2_F16) return pick(__half());
