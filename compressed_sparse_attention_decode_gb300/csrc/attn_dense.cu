@@ -592,20 +592,23 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
     }
 }
 
-// Joins the shares of one query and head: four groups of 128 threads take every fourth share, four dims a
-// thread, and are added up in order; the shares' factors are found by the threads side by side.
-template <typename TO>
+// Joins the shares of every query and head, four dims a thread: 128 threads per head (SPREAD 1, four heads
+// per block), or four groups of 128 that take every fourth share and are added up in order (SPREAD 4).  Every
+// warp finds the shares' factors for itself, 32 at a time, so that nothing waits but the groups' sum.
+constexpr int DA_MAXS = DA_SMS + 1;              // shares of one query at most
+
+template <typename TO, int SPREAD>
 __global__ void __launch_bounds__(512) k_dense_combine(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
                                                        const DenseItem* __restrict__ items, int n_items, int blocks,
-                                                       int hgroups, int n_heads, int64_t query0, TO* __restrict__ out,
-                                                       float* __restrict__ lse) {
-    __shared__ float fac[DA_SMS + 1], wm[16], wl[16];
-    __shared__ float4 sums[3][128];
-    const int64_t ql = blockIdx.x / n_heads;                      // query of this pass
-    const int head = (int)(blockIdx.x - ql * n_heads);
-    const int item = (int)ql * hgroups + head / DA_H;
-    const int tid = threadIdx.x, warp = tid >> 5, dim = tid & 127, group = tid >> 7;
+                                                       int hgroups, int n_heads, int64_t query0, int64_t n_rows,
+                                                       TO* __restrict__ out, float* __restrict__ lse) {
+    __shared__ float4 sums[SPREAD > 1 ? 3 : 1][128];
+    const int tid = threadIdx.x, lane = tid & 31, dim = tid & 127, group = SPREAD > 1 ? tid >> 7 : 0;
+    const int64_t row = SPREAD > 1 ? blockIdx.x : (int64_t)blockIdx.x * 4 + (tid >> 7);      // query of this pass, head
     pdl_wait();
+    if (SPREAD == 1 && row >= n_rows) return;
+    const int64_t ql = row / n_heads;
+    const int head = (int)(row - ql * n_heads), item = (int)ql * hgroups + head / DA_H;
     // the block that had unit u: the largest b with total * b / parts <= u
     const DenseItem it = items[item];
     const int64_t total = items[n_items].start, parts = min((int64_t)blocks, total);
@@ -616,44 +619,66 @@ __global__ void __launch_bounds__(512) k_dense_combine(const float* __restrict__
     }
     const int n = n_fp4 + (it.win > 0 ? 1 : 0);
     auto share = [&](int s) { return s < n_fp4 ? (int64_t)item + b0 + s : (int64_t)n_items + blocks - 1 + item; };
-    const float2 v = tid < n ? part_ml[share(tid) * DA_H + head % DA_H] : make_float2(-INFINITY, 0.0f);
-    float m = v.y != 0.0f ? v.x : -INFINITY;
+    constexpr int NK = (DA_MAXS + 31) / 32;
+    float fs[NK], ls[NK], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        fs[k] = -INFINITY, ls[k] = 0.0f;
+        if (32 * k < n) {
+            const int s = 32 * k + lane;
+            if (s < n) {
+                const float2 v = part_ml[share(s) * DA_H + head % DA_H];
+                fs[k] = v.x, ls[k] = v.y;
+                if (v.y != 0.0f) m = fmaxf(m, v.x);
+            }
+        }
+    }
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) wm[warp] = m;
-    __syncthreads();
-    m = wm[0];
-    for (int i = 1; i < 5; ++i) m = fmaxf(m, wm[i]);              // at most 153 shares: the first five warps
-    const float fs = v.y != 0.0f ? exp2f(v.x - m) : 0.0f;
-    if (tid < n) fac[tid] = fs;
-    float l = fs * v.y;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        fs[k] = ls[k] != 0.0f ? exp2f(fs[k] - m) : 0.0f;
+        l = fmaf(fs[k], ls[k], l);
+    }
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if ((tid & 31) == 0) wl[warp] = l;
-    __syncthreads();
-    l = (((wl[0] + wl[1]) + wl[2]) + wl[3]) + wl[4];
     float o[4] = {};
     const float4* src = reinterpret_cast<const float4*>(part_o + (int64_t)(head % DA_H) * D_LAT) + dim;
-#pragma unroll 4
-    for (int s = group; s < n; s += 4) {
-        const float4 x = src[share(s) * DA_H * (D_LAT / 4)];
-        const float f = fac[s];
-        o[0] = fmaf(f, x.x, o[0]), o[1] = fmaf(f, x.y, o[1]);
-        o[2] = fmaf(f, x.z, o[2]), o[3] = fmaf(f, x.w, o[3]);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        const int end = min(n, 32 * k + 32);
+        // several shares' loads in flight at a time (past the end: the last one again, times nothing)
+        constexpr int NB = SPREAD > 1 ? 8 : 4;
+        for (int s0 = 32 * k + group; s0 < end; s0 += NB * SPREAD) {
+            float4 x[NB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) x[i] = src[share(min(s0 + i * SPREAD, end - 1)) * DA_H * (D_LAT / 4)];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int s = s0 + i * SPREAD;
+                float f = __shfl_sync(0xffffffffu, fs[k], s & 31);
+                if (s >= end) f = 0.0f;
+                o[0] = fmaf(f, x[i].x, o[0]), o[1] = fmaf(f, x[i].y, o[1]);
+                o[2] = fmaf(f, x[i].z, o[2]), o[3] = fmaf(f, x[i].w, o[3]);
+            }
+        }
     }
-    if (group > 0) sums[group - 1][dim] = make_float4(o[0], o[1], o[2], o[3]);
-    __syncthreads();
-    if (group > 0) return;
-    for (int i = 0; i < 3; ++i) {
-        const float4 x = sums[i][dim];
-        o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
+    if constexpr (SPREAD > 1) {
+        if (group > 0) sums[group - 1][dim] = make_float4(o[0], o[1], o[2], o[3]);
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const float4 x = sums[i][dim];
+            o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
+        }
     }
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    const int64_t row = (query0 + ql) * n_heads + head;
+    const int64_t at = query0 * n_heads + row;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] *= inv;
     ElemVec<TO, 4> y;
     y.pack(o);
-    y.store(out + row * D_LAT + 4 * tid);
-    if (lse != nullptr && tid == 0) lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    y.store(out + at * D_LAT + 4 * dim);
+    if (lse != nullptr && dim == 0) lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 namespace {
@@ -703,8 +728,12 @@ cudaError_t launch_dense_attn(const csa2_cache& c, const uint16_t* q, int n_q, i
         a.n_items = (int)(nq * p.hgroups);
         launch_k(k_dense_attn, dim3((unsigned)p.blocks), DA_THREADS, DA_DYN, st, a);
         auto join = [&](auto* y) {
-            launch_k(k_dense_combine<std::remove_pointer_t<decltype(y)>>, dim3((unsigned)(nq * n_heads)), 512, 0, st, a.part_o,
-                     a.part_ml, a.items, a.n_items, p.blocks, p.hgroups, n_heads, q0, y, lse);
+            // few items: many shares each, so a block per head; else about (blocks + 2 items) / items of them
+            using TO = std::remove_pointer_t<decltype(y)>;
+            const int64_t rows = nq * n_heads;
+            const bool spread = a.n_items * 8 <= p.blocks;
+            launch_k(spread ? k_dense_combine<TO, 4> : k_dense_combine<TO, 1>, dim3((unsigned)(spread ? rows : (rows + 3) / 4)),
+                     512, 0, st, a.part_o, a.part_ml, a.items, a.n_items, p.blocks, p.hgroups, n_heads, q0, rows, y, lse);
         };
         if (out_type == CSA2_F32)
             join(reinterpret_cast<float*>(out));
