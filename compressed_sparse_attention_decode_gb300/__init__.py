@@ -1,7 +1,8 @@
 """CSA2 sparse-attention decode over an FP4 global KV cache, GB300 (sm_103a).
 
 Thin binding over the C ABI of ``libcsa2.so`` (declared in include/csa2.h):
-argument marshalling only.  Every step runs in the library's CUDA kernels;
+argument marshalling only, by ctypes and, for the operators whose calls are short
+(csa2_linear_fp4, csa2_norm_rope, csa2_dense_attn), by the C++ module ``_native``.  Every step runs in the library's CUDA kernels;
 PyTorch supplies device memory and the current stream.  There is no CPU
 fallback: if the library is not built, every call raises.
 
@@ -12,8 +13,9 @@ Entry points (same names as the C ABI):
 plus ``Cache``, which owns the four cache planes as torch tensors.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -24,7 +26,6 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TIMEOUT = 0, 
 FULL, REINDEX, REUSE = 0, 1, 2
 OP_INDEXER_TOPK, OP_REINDEX, OP_SPARSE_ATTN, OP_DENSE_ATTN, OP_LINEAR_FP4 = 1, 2, 3, 4, 5
 ROPE_HALVES, ROPE_INVERSE, ROPE_NO_NORM = 1, 2, 4
-_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 D_LAT = 512
 
 
@@ -47,10 +48,7 @@ class _HeadRows(ctypes.Structure):
                 ("y_head", ctypes.c_int64), ("n_heads", ctypes.c_int32)]
 
 
-# the two structures as bytes: a call packs them in a fraction of the time that a ctypes object takes
-_PACK_ROWS = struct.Struct("@PPPqqqqi4x").pack
-_PACK_CACHE = struct.Struct("@PPPPiiiii4x").pack
-
+_native = None
 _lib = None
 EXPORTS = ("csa2_cache_write", "csa2_quantize_fp4", "csa2_indexer_topk", "csa2_reindex", "csa2_sparse_attn",
            "csa2_workspace_size", "csa2_status_string", "csa2_abi_version", "csa2_launch_count",
@@ -79,8 +77,9 @@ def load(path=None):
     lib.csa2_sparse_attn.argtypes = [cp, vp, i32, i32, vp, vp, i32, vp, i64, i32, ctypes.c_float, vp, vp, vp, sz, vp]
     lib.csa2_linear_fp4.argtypes = [vp, i32, i64, i64, i32, i32, i32, i32, vp, vp, ctypes.c_float, vp, i32, i64,
                                     i64, vp, sz, vp]
-    lib.csa2_norm_rope.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, ctypes.c_float, i32, vp]
-    lib.csa2_dense_attn.argtypes = [vp, vp, i32, i32, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, sz, vp]
+    hp = ctypes.POINTER(_HeadRows)
+    lib.csa2_norm_rope.argtypes = [hp, hp, i32, i32, i32, i32, i32, vp, vp, ctypes.c_float, i32, vp]
+    lib.csa2_dense_attn.argtypes = [cp, vp, i32, i32, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, sz, vp]
     lib.csa2_reindex_noalloc.argtypes = [cp, vp, vp, vp, i32, i32, vp, i32, i32, vp, vp]
     lib.csa2_reindex_noalloc.restype = ctypes.c_int
     lib.csa2_poll_error.argtypes = [vp, sz, vp]
@@ -97,8 +96,22 @@ def load(path=None):
                  "csa2_sparse_attn", "csa2_linear_fp4", "csa2_norm_rope", "csa2_dense_attn"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
+        _load_native(lib)
         _lib = lib
     return lib
+
+
+def _load_native(lib):
+    """the C++ part of the binding, calling the functions of `lib`"""
+    global _native
+    p = os.path.join(_HERE, "_native.so")
+    if not os.path.exists(p):
+        raise RuntimeError("_native.so is not built (%s); run __graft_entry__.build()" % p)
+    spec = importlib.util.spec_from_file_location("_native", p, loader=importlib.machinery.ExtensionFileLoader("_native", p))
+    _native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_native)
+    _native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                   (lib.csa2_linear_fp4, lib.csa2_norm_rope, lib.csa2_dense_attn, lib.csa2_workspace_size)))
 
 
 def _status_string(s):
@@ -309,18 +322,6 @@ def csa2_sparse_attn(cache, q, q_pos, idx, swa, swa_pos0, scale=D_LAT ** -0.5, o
     return out, lse
 
 
-# Scratch of one call, from PyTorch's allocator but for the stream that the call runs on (a tensor would belong
-# to the current stream, and be given to other work there while this stream still uses it): freed as soon as the
-# call is enqueued, it goes to later work of the same stream alone.
-_scratch_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
-_scratch_free = torch._C._cuda_cudaCachingAllocator_raw_delete
-
-
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
 def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, ws=None, stream=None):
     """y = alpha * W x with FP4 weights (csa2_quantize_fp4's format), for every token.
     x bf16 / fp16 / fp32 [T, n_in] with codes uint8 [n_out, n_in/2] and scales uint8 [n_out, n_in/16], or
@@ -328,56 +329,12 @@ def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, ws=No
     Rows of x and out are contiguous, their other strides free.  Returns [T, n_out] or [T, G, n_out]
     of out_dtype (default: that of x).  With a stream other than the current one, give `out` (a new one
     belongs to the current stream); without ws the scratch is taken for the call's own stream."""
-    xs, ms = x.shape, codes.shape
-    if len(xs) == 2:
-        (T, n_in), G, lead, x_group = xs, 1, 0, 0
-    else:
-        _need(len(xs) == 3, "x: [T, n_in] or [T, G, n_in]")
-        T, G, n_in = xs
-        lead, x_group = 1, x.stride(1)
-    _need(len(ms) == lead + 2, "codes: as many leading dims as x has groups")
-    n_out = ms[-2]
-    _need(n_in % 16 == 0 and ms[-1] * 2 == n_in and scales.shape == ms[:-1] + (n_in // 16,) and (not lead or ms[0] == G),
-          "codes [.., n_out, n_in/2] and scales [.., n_out, n_in/16] of x [.., n_in], n_in a multiple of 16")
-    _need(codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_contiguous() and scales.is_contiguous(),
-          "codes and scales: contiguous uint8")
-    if out is None:
-        out = torch.empty(xs[:-1] + (n_out,), dtype=out_dtype or x.dtype, device=x.device)
-    else:
-        _need(out.shape == xs[:-1] + (n_out,) and (out_dtype is None or out.dtype is out_dtype),
-              "out [.., n_out] with the leading sizes of x")
-    x_type, y_type = _TYPES.get(x.dtype), _TYPES.get(out.dtype)
-    _need(x_type is not None and y_type is not None, "x and out: bf16, fp16 or fp32")
-    _need((x.stride(-1) == 1 or n_in == 0) and (n_out <= 1 or out.stride(-1) == 1), "rows of x and out: contiguous")
-    lib, st, own = load(), _stream(stream), 0
-    if ws is not None:
-        p_ws, n_ws = ws.data_ptr(), ws.numel()
-    else:
-        n_ws = lib.csa2_workspace_size(OP_LINEAR_FP4, T, G, x_type, 0, n_in) if T > 8 or n_in > 16384 else 0   # none for few tokens
-        p_ws = own = _scratch_alloc(n_ws, st) if n_ws else 0
-    status = lib.csa2_linear_fp4(x.data_ptr(), x_type, x.stride(0), x_group, T, G, n_in, n_out, codes.data_ptr(),
-                                 scales.data_ptr(), alpha, out.data_ptr(), y_type, out.stride(0),
-                                 out.stride(1) if lead else 0, p_ws, n_ws, st)
-    if own:
-        _scratch_free(own)
-    if status:
-        raise Csa2Error(status, "csa2_linear_fp4")
-    return out
-
-
-def _head_rows(x, weight, out, T, d, name):
-    xs = x.shape
-    _need(len(xs) == 3 and xs[0] == T and xs[2] == d and out.shape == xs, "%s and its output: [T, heads, d]" % name)
-    x0, x1, x2 = x.stride()
-    y0, y1, y2 = out.stride()
-    _need(x2 == 1 and y2 == 1, "rows of a head set and its output: contiguous")
-    if weight is None:
-        w = 0
-    else:
-        _need(weight.dtype is torch.float32 and weight.shape == (d,) and weight.is_contiguous(),
-              "weights: contiguous fp32 [d]")
-        w = weight.data_ptr()
-    return _PACK_ROWS(x.data_ptr(), out.data_ptr(), w, x0, x1, y0, y1, xs[1])
+    if _native is None:
+        load()
+    r = _native.linear_fp4(x, codes, scales, alpha, out, out_dtype, ws, None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        raise Csa2Error(r, "csa2_linear_fp4")
+    return r
 
 
 def csa2_norm_rope(q, pos, inv_freq, q_weight=None, k=None, k_weight=None, eps=1e-6, norm=True, halves=False,
@@ -387,32 +344,13 @@ def csa2_norm_rope(q, pos, inv_freq, q_weight=None, k=None, k_weight=None, eps=1
     turns back, halves=True pairs value i with i + d_rot/2 (default: 2i with 2i+1).  pos and inv_freq
     may both be None (no rotation).  bf16 / fp16 / fp32, rows contiguous, other strides free; q_out may
     be q.  Returns (q_out, k_out or None)."""
-    T, _, d = q.shape
-    if inv_freq is None:
-        d_rot, p_pos, p_freq = 0, None, None
-    else:
-        d_rot = 2 * inv_freq.numel()
-        _need(inv_freq.dtype is torch.float32 and inv_freq.is_contiguous() and pos is not None
-              and pos.dtype is torch.int64 and pos.shape == (T,) and pos.is_contiguous(),
-              "inv_freq: contiguous fp32; pos: contiguous int64 [T]")
-        p_pos, p_freq = pos.data_ptr(), inv_freq.data_ptr()
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-    rows_q = _head_rows(q, q_weight, q_out, T, d, "q")
-    rows_k = None
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=q_out.dtype, device=k.device)
-        _need(k.dtype is q.dtype and k_out.dtype is q_out.dtype, "k has the type of q, k_out that of q_out")
-        rows_k = _head_rows(k, k_weight, k_out, T, d, "k")
-    x_type, y_type = _TYPES.get(q.dtype), _TYPES.get(q_out.dtype)
-    _need(x_type is not None and y_type is not None and (out_dtype is None or q_out.dtype is out_dtype),
-          "q and q_out: bf16, fp16 or fp32")
-    flags = (ROPE_HALVES if halves else 0) | (ROPE_INVERSE if inverse else 0) | (0 if norm else ROPE_NO_NORM)
-    st = load().csa2_norm_rope(rows_q, rows_k, x_type, y_type, T, d, d_rot, p_pos, p_freq, eps, flags, _stream(stream))
-    if st:
-        raise Csa2Error(st, "csa2_norm_rope")
-    return q_out, k_out if k is not None else None
+    if _native is None:
+        load()
+    r = _native.norm_rope(q, pos, inv_freq, q_weight, k, k_weight, eps, norm, halves, inverse, q_out, k_out, out_dtype,
+                          None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        raise Csa2Error(r, "csa2_norm_rope")
+    return r
 
 
 def csa2_dense_attn(cache, q, q_pos, swa, swa_pos0, scale=D_LAT ** -0.5, out=None, out_dtype=torch.bfloat16, lse=None,
@@ -423,41 +361,10 @@ def csa2_dense_attn(cache, q, q_pos, swa, swa_pos0, scale=D_LAT ** -0.5, out=Non
     fp32 [B, n_q, H] or None).  With a stream other than the current one, give out and lse (new ones
     belong to the current stream); without ws the scratch is taken for the call's own stream, and a
     bounded wait that gave up cannot be polled."""
-    B, n_q, H, D = q.shape
-    codes = cache.lat_codes
-    _need(q.dtype is torch.bfloat16 and q.is_contiguous() and D == D_LAT and B == cache.batch,
-          "q: contiguous bf16 [batch, n_q, heads, 512]")
-    _need(q_pos.dtype is torch.int64 and q_pos.shape == (B, n_q) and q_pos.is_contiguous(),
-          "q_pos: contiguous int64 [batch, n_q]")
-    if swa is None:
-        p_swa, n_swa = None, 0
-    else:
-        Bs, n_swa, Ds = swa.shape
-        _need(swa.dtype is torch.bfloat16 and swa.is_contiguous() and Bs == B and Ds == D_LAT,
-              "swa: contiguous bf16 [batch, swa_len, 512]")
-        p_swa = swa.data_ptr()
-    _need(swa_pos0 is None or (swa_pos0.dtype is torch.int64 and swa_pos0.shape == (B,) and swa_pos0.is_contiguous()),
-          "swa_pos0: contiguous int64 [batch]")
-    if out is None:
-        out = torch.empty((B, n_q, H, D_LAT), dtype=out_dtype, device=q.device)
-    o_type = _TYPES.get(out.dtype)
-    _need(o_type is not None and out.is_contiguous() and out.shape == q.shape, "out: contiguous, the shape of q")
-    if want_lse and lse is None:
-        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=q.device)
-    _need(lse is None or (lse.dtype is torch.float32 and lse.shape == (B, n_q, H) and lse.is_contiguous()),
-          "lse: contiguous fp32 [batch, n_q, heads]")
-    lib, st, own = load(), _stream(stream), 0
-    if ws is not None:
-        p_ws, n_ws = ws.data_ptr(), ws.numel()
-    else:
-        n_ws = lib.csa2_workspace_size(OP_DENSE_ATTN, B, n_q, H, 0, cache.capacity)
-        p_ws = own = _scratch_alloc(n_ws, st) if n_ws else 0
-    c = _PACK_CACHE(codes.data_ptr(), cache.lat_scales.data_ptr(), 0, 0, B, cache.capacity, D_LAT, 128, cache.ratio)
-    status = lib.csa2_dense_attn(c, q.data_ptr(), n_q, H, q_pos.data_ptr(), p_swa,
-                                 None if swa_pos0 is None else swa_pos0.data_ptr(), n_swa, scale, out.data_ptr(), o_type,
-                                 None if lse is None else lse.data_ptr(), p_ws, n_ws, st)
-    if own:
-        _scratch_free(own)
-    if status:
-        raise Csa2Error(status, "csa2_dense_attn")
-    return out, lse
+    if _native is None:
+        load()
+    r = _native.dense_attn(cache.lat_codes, cache.lat_scales, cache.ratio, q, q_pos, swa, swa_pos0, scale, out, out_dtype,
+                           lse, want_lse, ws, None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        raise Csa2Error(r, "csa2_dense_attn")
+    return r
