@@ -10,6 +10,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -34,6 +35,16 @@ const at::Tensor& tensor(PyObject* o, const char* what) {
     return THPVariable_Unpack(o);
 }
 const at::Tensor* tensor_or_none(PyObject* o, const char* what) { return o == Py_None ? nullptr : &tensor(o, what); }
+
+// every given tensor on the current device (the last check: it is the one that needs a GPU)
+template <typename... T>
+void on_device(const T*... t) {
+    const auto one = [](const at::Tensor* v) { return v == nullptr || v->is_cuda(); };
+    need((one(t) && ...), "tensors on the GPU");
+    const auto here = c10::cuda::current_device();
+    const auto same = [&](const at::Tensor* v) { return v == nullptr || v->get_device() == here; };
+    need((same(t) && ...), "tensors on the current device");
+}
 
 int type_of(const at::Tensor& t, const char* what) {
     switch (t.scalar_type()) {
@@ -124,6 +135,7 @@ PyObject* linear(PyObject* const* a) {
     need((x.stride(nd - 1) == 1 || n_in == 0) && (n_out <= 1 || y.stride(nd - 1) == 1), "rows of x and out: contiguous");
     need(T <= INT32_MAX && G <= INT32_MAX && n_in <= INT32_MAX && n_out <= INT32_MAX, "sizes of 31 bits");
     const double alpha = number(a[3]);
+    on_device(&x, &codes, &scales, &y, tensor_or_none(a[6], "ws: a tensor"));
     const cudaStream_t st = stream_of(a[7]);
     Workspace ws;
     if (a[6] != Py_None)
@@ -180,6 +192,7 @@ PyObject* rope(PyObject* const* a) {
     const int flags = (truth(a[8]) ? CSA2_ROPE_HALVES : 0) | (truth(a[9]) ? CSA2_ROPE_INVERSE : 0) |
                       (truth(a[7]) ? 0 : CSA2_ROPE_NO_NORM);
     const double eps = number(a[6]);
+    on_device(&q, pos, freq, qw, k, kw, &qo, k ? (kg ? kg : &km) : nullptr);
     const int status = f_rope(&rq, k ? &rk : nullptr, x_type, y_type, (int32_t)T, (int32_t)d, (int32_t)d_rot,
                               d_rot ? (const int64_t*)pos->data_ptr() : nullptr, d_rot ? (const float*)freq->data_ptr() : nullptr,
                               (float)eps, flags, stream_of(a[13]));
@@ -227,6 +240,7 @@ PyObject* dense(PyObject* const* a) {
     const double scale = number(a[7]);
     const csa2_cache cache{(uint8_t*)codes.data_ptr(), (uint8_t*)scales.data_ptr(), nullptr, nullptr, (int32_t)B, (int32_t)cap,
                            512, 128, (int32_t)whole(a[2])};
+    on_device(&codes, &scales, &q, &pos, swa, pos0, &o, lse, tensor_or_none(a[12], "ws: a tensor"));
     const cudaStream_t st = stream_of(a[13]);
     Workspace ws;
     if (a[12] != Py_None)

@@ -113,24 +113,39 @@ def test_dense_workspace_and_cache_checks(csa):
 def test_binding_checks_shapes_and_types(csa):
     u8 = dict(dtype=torch.uint8)
     x, c, s = torch.zeros(3, 64), torch.zeros(5, 32, **u8), torch.zeros(5, 4, **u8)
+    refused = lambda what: pytest.raises(ValueError, match=what)
+    with refused("GPU"):                       # all is well but for the device
+        csa.csa2_linear_fp4(x, c, s)
+    with refused("GPU"):
+        csa.csa2_linear_fp4(x[:, None].expand(3, 2, 64), c.expand(2, 5, 32).contiguous(), s.expand(2, 5, 4).contiguous())
     for bad in [(x.double(), c, s), (x, c[:, :16], s), (x, c, s[:, :2]), (x, c.int(), s), (x.T.contiguous().T, c, s),
                 (x[:, :40], c, s), (torch.zeros(3, 2, 64), c, s)]:
-        with pytest.raises(ValueError):
+        with refused("n_in|uint8|bf16|contiguous"):
             csa.csa2_linear_fp4(*bad)
-    with pytest.raises(ValueError):
+    with refused("out"):
         csa.csa2_linear_fp4(x, c, s, out=torch.zeros(3, 6))
-    with pytest.raises(ValueError):
+    with refused("out"):
+        csa.csa2_linear_fp4(x, c, s, out=torch.zeros(3, 5), out_dtype=torch.float16)
+    with refused("tensor"):
+        csa.csa2_linear_fp4([1.0], c, s)
+    with pytest.raises(TypeError):
+        csa.csa2_linear_fp4(x, c, s, "alpha")
+    with refused("codes"):
         csa.csa2_linear_fp4(torch.zeros(3, 2, 64), torch.zeros(3, 5, 32, **u8), torch.zeros(3, 5, 4, **u8))
     q, pos, f = torch.zeros(3, 4, 64), torch.zeros(3, dtype=torch.int64), torch.zeros(16)
+    with refused("GPU"):
+        csa.csa2_norm_rope(q, pos, f, k=torch.zeros(3, 1, 64), q_weight=torch.zeros(64))
     for kw in [dict(q=q, pos=pos.int(), inv_freq=f), dict(q=q, pos=pos[:2], inv_freq=f), dict(q=q, pos=None, inv_freq=f),
                dict(q=q, pos=pos, inv_freq=f.double()), dict(q=q.transpose(1, 2), pos=pos, inv_freq=f),
                dict(q=q, pos=pos, inv_freq=f, q_weight=torch.zeros(32)), dict(q=q, pos=pos, inv_freq=f, k=q.half()),
                dict(q=q, pos=pos, inv_freq=f, k=torch.zeros(2, 4, 64)), dict(q=q.double(), pos=pos, inv_freq=f)]:
-        with pytest.raises(ValueError):
+        with refused("contiguous|bf16|k has|a head set"):
             csa.csa2_norm_rope(**kw)
     cache = csa.Cache.of(torch.zeros(2, 8, 256, **u8), torch.zeros(2, 8, 32, **u8))
     bq, p = torch.zeros(2, 1, 4, 512, dtype=torch.bfloat16), torch.zeros(2, 1, dtype=torch.int64)
+    with refused("GPU"):
+        csa.csa2_dense_attn(cache, bq, p, torch.zeros(2, 4, 512, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64))
     for a in [(bq.float(), p, None, None), (bq[:1], p, None, None), (bq, p.int(), None, None), (bq, p[:1], None, None),
               (bq, p, torch.zeros(2, 4, 512), None), (bq, p, None, torch.zeros(2, dtype=torch.int32))]:
-        with pytest.raises(ValueError):
+        with refused("contiguous"):
             csa.csa2_dense_attn(cache, *a)
