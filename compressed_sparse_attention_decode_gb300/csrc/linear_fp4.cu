@@ -11,18 +11,24 @@
 // are exact, sums fp32; y is rounded once.
 //
 // Two kernels:
-//  - k_linear_few (up to 16 tokens): bound by the weight bytes.  mma.sync
-//    m16n8k16, the weights as the A fragments.  The
-//    order of k within a product is free as long as both operands agree, so a
-//    lane takes 16 consecutive bytes of a row (32 weights, two scale groups) and
-//    feeds them, four at a time, to eight products, and x comes from global memory
-//    in the matching order.  The weights come by bulk copies, all at once.
+//  - k_linear_few (up to 16 tokens; 8 of fp32).  The weights' bytes are its floor; what
+//    it runs at is the latency of asking, expanding and joining: one token, 1,536 ->
+//    32,768 (28 MB) takes 10.1 us, 2.8 TB/s, at 42 % of the issue slots.  mma.sync
+//    m16n8k16, the weights as the A fragments.  The order of k within a product is
+//    free as long as both operands agree, so a lane takes 16 consecutive bytes of a
+//    row (32 weights, two scale groups) and feeds them, four at a time, to eight
+//    products, and x comes from global memory in the matching order.  The weights
+//    come by bulk copies, all at once.
 //  - k_linear_many: tcgen05, M = 128 rows, N = up to 128 tokens.  Expanded
 //    weights go from registers to TMEM (the A operand), so shared memory carries
 //    the tokens alone: with both operands there, N = 128 would need 192 bytes per
 //    clock of the 128 it gives.  x comes by bulk copies in the layout that
 //    k_linear_x has written to the workspace.  When there are few row tiles a
 //    cluster of blocks splits n_in and adds up through distributed shared memory.
+//    What bounds it is the chain per 128 weights of every row (wait, expand, issue,
+//    commit): 850 clocks, where the tensor pipe needs 512 at 128 tokens.  64 tokens,
+//    1,536 -> 32,768: 17.5 us; 256 tokens, 4,096 -> 8,192: 21.1 us (814 TFLOP/s);
+//    both with k_linear_x, which overlaps its start.
 #include <algorithm>
 #include <type_traits>
 
