@@ -10,7 +10,7 @@
 // 455 flop per byte, so the tensor cores bound it; with few heads the heads pad the
 // MMA's 64 rows.  Lengths are known on the device alone, so the blocks (one per SM)
 // share the work there: each (query, 64 heads) is as many units as it has 64-key
-// tiles, plus some for its window, and block i takes the i-th even part of all units.
+// tiles, plus some for each tile of its window, and block i takes the i-th even part of all units.
 // A part that covers several queries is worked through one after the other; a query
 // that several blocks share leaves each one's running max, row sum and unnormalised
 // output in the workspace, and k_dense_combine joins them.  The window is always a
@@ -69,7 +69,7 @@ constexpr uint32_t DA_DYN = DA_MISC + 832 + 1024;    // + alignment
 constexpr uint32_t DAT_S = 0, DAT_O = 256, DAT_COLS = 512;   // S^T partial p of buffer b at DAT_S + 64 (2b + p)
 constexpr float DA_LAZY = 8.0f;                      // log2 headroom before the running max is raised
 constexpr int DA_SMS = 152;                          // blocks at most: one per SM
-constexpr int DA_WIN = 5;                            // units of a window share: two tiles, their scale and its own epilogue
+constexpr int DA_WIN = 4;                            // units of a window tile: 64 rows, their scale and the share's epilogue
 
 __device__ __forceinline__ uint32_t da_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
@@ -96,14 +96,35 @@ struct DenseArgs {
     int* err;
 };
 // Shares: block b's part of item i's tiles is number i + b (both only grow along the units, so no two
-// meet), item i's window number n_items + blocks - 1 + i.
+// meet), its part of item i's window n_items + blocks - 1 further.
+
+// a / b for 0 <= a, 0 < b: in 32 bits where that is enough (a 64-bit division takes some 700 clocks)
+__device__ __forceinline__ int64_t da_div(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+// The units' parts: total % parts of them have one unit more than the others, and come first
+struct DenseParts {
+    int64_t each;
+    int parts, more;
+    __device__ __forceinline__ DenseParts(int64_t total, int blocks) {
+        parts = (int)min((int64_t)blocks, total);        // every part has a unit, so a query's shares have no holes
+        each = parts > 0 ? da_div(total, parts) : 0;
+        more = (int)(total - each * parts);
+    }
+    __device__ __forceinline__ int64_t start(int b) const { return each * min(b, parts) + min(b, more); }
+    __device__ __forceinline__ int block_of(int64_t u) const {
+        const int64_t longer = (each + 1) * more;
+        return (int)(u < longer ? da_div(u, each + 1) : more + da_div(u - longer, each));
+    }
+};
 
 // what item i of the pass attends to: FP4 entries 0 .. n-1 and `rows` window rows from `row0` on
 struct DenseWork {
     int64_t gq, row0;
     int b, h0, n, rows;
     __device__ __forceinline__ int tiles() const { return (int)(((unsigned)n + DA_TILE - 1) / DA_TILE); }
-    __device__ __forceinline__ int win() const { return rows > 0 ? DA_WIN : 0; }
+    __device__ __forceinline__ int win() const { return (rows + DA_TILE - 1) / DA_TILE * DA_WIN; }
 };
 __device__ __forceinline__ DenseWork da_work(const DenseArgs& a, int item) {
     DenseWork w;
@@ -134,16 +155,19 @@ __device__ __noinline__ void da_next(const DenseArgs& a, int64_t u, int64_t u1, 
     while (u < u1) {
         const DenseWork w = da_work(a, item);
         const int tiles = w.tiles();
-        const int64_t end = start + tiles + w.win();
-        const bool window = u >= start + tiles;
-        const int rest = window ? 0 : (int)(min(u1, start + tiles) - u);     // tiles of this share
-        const bool run = !window || (u == start + tiles && w.win() > 0);     // not the rest of another block's window
-        const int64_t row0 = window ? w.row0 : (u - start) * DA_TILE;
-        out->row = window ? (int64_t)w.b * a.swa_len + row0 : (int64_t)w.b * a.capacity + row0;
-        out->rows = window ? w.rows : (int)min((int64_t)rest * DA_TILE, w.n - row0);
-        out->share = window ? a.n_items + (int)gridDim.x - 1 + item : item + (int)blockIdx.x;
+        const int64_t ws = start + tiles, end = ws + w.win();
+        const bool window = u >= ws;
+        const int64_t upto = min(u1, window ? end : ws);
+        // of the window the tiles whose first units are among these
+        const int64_t t0 = window ? (u - ws + DA_WIN - 1) / DA_WIN : u - start;
+        const int64_t t1 = window ? (upto - ws + DA_WIN - 1) / DA_WIN : upto - start;
+        const bool run = t1 > t0;
+        const int64_t row0 = (window ? w.row0 : 0) + t0 * DA_TILE;
+        out->row = (int64_t)w.b * (window ? a.swa_len : a.capacity) + row0;
+        out->rows = (int)(min(t1 * DA_TILE, (int64_t)(window ? w.rows : w.n)) - t0 * DA_TILE);
+        out->share = (window ? a.n_items + (int)gridDim.x - 1 : 0) + item + (int)blockIdx.x;
         out->gq = w.gq, out->h0 = w.h0, out->item = item, out->window = window;
-        u = window ? end : u + rest;
+        u = upto;
         if (u >= end) start = end, ++item;
         if (run) {
             out->u = u, out->start = start, out->next_item = item;
@@ -156,7 +180,7 @@ __device__ __noinline__ void da_next(const DenseArgs& a, int64_t u, int64_t u1, 
 __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_constant__ DenseArgs a) {
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) unsigned long long b_lhalf[DA_NL], b_lfull[DA_NL], b_lfree[DA_NL], b_sfull[2], b_sfree[2],
-        b_pfull[2], b_odone[2];
+        b_pfull[2], b_odone[2], b_next;
     __shared__ int64_t wsum[DA_THREADS / 32], last_unit;
     __shared__ DenseShare shares[2];
     __shared__ uint32_t tmem_base;
@@ -170,7 +194,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
     float* fac = m_run + DA_H;
     int* qexp = reinterpret_cast<int*>(fac + DA_H);
     int* flag = qexp + DA_H;
-    unsigned int* wmax = reinterpret_cast<unsigned int*>(flag + 4);
+    unsigned int* wmaxs = reinterpret_cast<unsigned int*>(flag + 4);
     if (tid == 0) {
         for (int i = 0; i < DA_NL; ++i) {
             umma::mbar_init(sa(&b_lhalf[i]), DA_LOADERS / 32);
@@ -183,7 +207,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
             umma::mbar_init(sa(&b_pfull[i]), DA_SMW);
             umma::mbar_init(sa(&b_odone[i]), 2);
         }
+        umma::mbar_init(sa(&b_next), 1);
         umma::fence_mbar_init();
+        wmaxs[0] = wmaxs[1] = 0u;
     }
     if (warp == DA_LOADW - 1) umma::tmem_alloc(sa(&tmem_base), DAT_COLS);
     pdl_wait();                  // q, the positions and the window may come from the preceding kernel
@@ -215,9 +241,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
         if (i < warp) before += v;
         total += v;
     }
-    const int64_t parts = min((int64_t)gridDim.x, total);    // every part has a unit, so a query's shares have no holes
-    const int64_t u0 = blockIdx.x < parts ? total * blockIdx.x / parts : 0;
-    const int64_t u1 = blockIdx.x < parts ? total * (blockIdx.x + 1) / parts : 0;
+    const DenseParts pt(total, (int)gridDim.x);
+    const int64_t u0 = pt.start(blockIdx.x), u1 = pt.start(blockIdx.x + 1);
     {
         int64_t s = before + upto - own;
 #pragma unroll
@@ -241,13 +266,15 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
     int q_item = -1;                                         // the item whose queries are staged
     uint32_t tb = 0;                                         // tiles done so far: the rings go on from share to share
 
-    for (int cur = 0; shares[cur].rows >= 0; cur ^= 1) {
+    // The loaders go from share to share by themselves, held by the buffers alone; the other warps meet.
+    for (uint32_t k = 0; shares[k & 1].rows >= 0; ++k) {
+        const uint32_t cur = k & 1;
         const DenseShare& S = shares[cur];
         const int rows = S.rows, T = (rows + DA_TILE - 1) / DA_TILE;
         const bool window = S.window;
+        unsigned int* wmax = wmaxs + cur;
 
-        // FP4 rows: a tile is 64 rows x 16 units of 32 dims (16 bytes of codes, 2 of scales); the first one is
-        // fetched before the block meets
+        // FP4 rows: a tile is 64 rows x 16 units of 32 dims (16 bytes of codes, 2 of scales)
         const uint8_t* codes = a.codes + S.row * (D_LAT / 2);
         const uint8_t* scales = a.scales + S.row * (D_LAT / 16);
         constexpr int NU = DA_TILE * 16 / DA_LOADERS;
@@ -274,17 +301,14 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
                 }
             }
         };
-        if (warp >= DA_LOADW && !window) fetch(0);
-
-        // ---- the block meets: the share before is done with Q, O and the running max
-        umma::fence_before();
-        __syncthreads();
-        umma::fence_after();
-        if (tid == 0) {
-            *wmax = 0u;
-            da_next(a, S.u, last_unit, S.start, S.next_item, &shares[cur ^ 1]);
+        if (warp < DA_LOADW) {
+            if (k > 0) {             // the share before is done with Q, O and the running max
+                umma::fence_before();
+                umma::bar_named(3, DA_LOADW * 32);
+                umma::fence_after();
+            }
+            if (tid < DA_H) m_run[tid] = -INFINITY;
         }
-        if (tid < DA_H) m_run[tid] = -INFINITY;
         // Q: heads h0 .. h0+63 (zero rows past n_heads), bf16 -> fp16 slabs, by warps 0-11; a head whose largest
         // magnitude lies outside [2^-10, 2^15) is scaled by a power of two on the way
         if (q_item != S.item && warp < DA_LOADW) {
@@ -320,7 +344,13 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
             umma::fence_proxy_async();
         }
         q_item = S.item;
-        __syncthreads();
+        if (warp < DA_LOADW) umma::bar_named(3, DA_LOADW * 32);
+        if (tid == DA_LOADW * 32 - 1) {          // the last warp that has nothing to do yet
+            wmaxs[cur ^ 1] = 0u;
+            da_next(a, S.u, last_unit, S.start, S.next_item, &shares[cur ^ 1]);
+            umma::mbar_arrive(sa(&b_next));
+        }
+        __syncwarp();
 
         if (warp >= DA_LOADW) {
             if (window) {
@@ -369,7 +399,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
                 for (int t = 0; t < T; ++t) {
                     const uint32_t tg = tb + t, buf = tg % DA_NL;
                     uint8_t* L = sm + DA_SL + buf * DA_LBUF;
-                    if (t > 0) fetch(t);
+                    fetch(t);
                     if (lt < DA_TILE && (t + 1) * DA_TILE + lt < rows) {
                         const int64_t j = (t + 1) * DA_TILE + lt;
                         umma::prefetch_l2(codes + j * (D_LAT / 2));
@@ -583,6 +613,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
         }
         tb += T;
         __syncwarp();                                        // the issuers' other lanes
+        ok = umma::mbar_wait_fast(sa(&b_next), k & 1) && ok;
     }
     if (!ok) atomicExch(a.err, 1);
     umma::fence_before();
@@ -596,7 +627,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
 // Joins the shares of every query and head, four dims a thread: 128 threads per head (SPREAD 1, four heads
 // per block), or four groups of 128 that take every fourth share and are added up in order (SPREAD 4).  Every
 // warp finds the shares' factors for itself, 32 at a time, so that nothing waits but the groups' sum.
-constexpr int DA_MAXS = DA_SMS + 1;              // shares of one query at most
+constexpr int DA_MAXS = DA_SMS + 2;              // shares of one query at most
 
 template <typename TO, int SPREAD>
 __global__ void __launch_bounds__(512) k_dense_combine(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
@@ -610,16 +641,19 @@ __global__ void __launch_bounds__(512) k_dense_combine(const float* __restrict__
     if (SPREAD == 1 && row >= n_rows) return;
     const int64_t ql = row / n_heads;
     const int head = (int)(row - ql * n_heads), item = (int)ql * hgroups + head / DA_H;
-    // the block that had unit u: the largest b with total * b / parts <= u
     const DenseItem it = items[item];
-    const int64_t total = items[n_items].start, parts = min((int64_t)blocks, total);
-    int b0 = 0, n_fp4 = 0;
-    if (it.tiles > 0) {
-        b0 = (int)(((it.start + 1) * parts - 1) / total);
-        n_fp4 = (int)(((it.start + it.tiles) * parts - 1) / total) - b0 + 1;
+    const DenseParts pt(items[n_items].start, blocks);
+    const int64_t ws = it.start + it.tiles;
+    int b0 = 0, n_fp4 = 0, n_win = 0, w0 = 0, w1 = 0;
+    if (it.tiles > 0) b0 = pt.block_of(it.start), n_fp4 = pt.block_of(ws - 1) - b0 + 1;
+    if (it.win > 0) {
+        w0 = pt.block_of(ws), n_win = 1;
+        if (it.win > DA_WIN) w1 = pt.block_of(ws + DA_WIN), n_win += w1 != w0;
     }
-    const int n = n_fp4 + (it.win > 0 ? 1 : 0);
-    auto share = [&](int s) { return s < n_fp4 ? (int64_t)item + b0 + s : (int64_t)n_items + blocks - 1 + item; };
+    const int n = n_fp4 + n_win;
+    auto share = [&](int s) {
+        return (int64_t)item + (s < n_fp4 ? b0 + s : n_items + blocks - 1 + (s == n_fp4 ? w0 : w1));
+    };
     constexpr int NK = (DA_MAXS + 31) / 32;
     float fs[NK], ls[NK], m = -INFINITY, l = 0.0f;
 #pragma unroll
@@ -697,8 +731,8 @@ DensePlan dense_plan(int64_t queries, int n_heads, int64_t capacity) {
     p.pass_queries = std::min(queries, DA_PASS / p.hgroups);
     const int64_t items = p.pass_queries * p.hgroups;
     // one block per SM, fewer where even a full cache has fewer units
-    p.blocks = (int)std::min<int64_t>(DA_SMS, items * ((capacity + DA_TILE - 1) / DA_TILE + DA_WIN));
-    const size_t rows = (size_t)(2 * items + p.blocks - 1) * DA_H;
+    p.blocks = (int)std::min<int64_t>(DA_SMS, items * ((capacity + DA_TILE - 1) / DA_TILE + DA_NL * DA_WIN));
+    const size_t rows = (size_t)2 * (items + p.blocks - 1) * DA_H;
     p.items_bytes = ((size_t)(items + 1) * sizeof(DenseItem) + 255) / 256 * 256;
     p.o_bytes = rows * D_LAT * sizeof(float);
     p.ml_bytes = rows * sizeof(float2);
