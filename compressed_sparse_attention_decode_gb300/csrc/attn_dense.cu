@@ -73,9 +73,8 @@ constexpr int DA_WIN = 4;                            // units of a window tile: 
 
 __device__ __forceinline__ uint32_t da_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
-struct DenseItem {               // of one (query, head group), for the combine
-    int64_t start;               // first unit
-    int32_t tiles, win;          // units of FP4 tiles and of the window
+struct DenseItem {               // the shares of an item: blocks b0 .. b0 + n_fp4 - 1; the window's blocks, or -1
+    int b0, n_fp4, w0, w1;
 };
 struct DenseArgs {
     const uint8_t* codes;
@@ -90,7 +89,7 @@ struct DenseArgs {
     float scale_log2e;
     int64_t query0;              // first query of this pass (b * n_q + i)
     int n_items;                 // (query, head group) pairs of this pass
-    DenseItem* items;            // [n_items + 1]: the last one's start is the number of units
+    DenseItem* items;            // [n_items]
     float* part_o;               // [share][64][512]
     float2* part_ml;             // [share][64] running max (log2) and row sum
     int* err;
@@ -98,24 +97,18 @@ struct DenseArgs {
 // Shares: block b's part of item i's tiles is number i + b (both only grow along the units, so no two
 // meet), its part of item i's window n_items + blocks - 1 further.
 
-// a / b for 0 <= a, 0 < b: in 32 bits where that is enough (a 64-bit division takes some 700 clocks)
-__device__ __forceinline__ int64_t da_div(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
-    return a / b;
-}
 // The units' parts: total % parts of them have one unit more than the others, and come first
 struct DenseParts {
-    int64_t each;
-    int parts, more;
-    __device__ __forceinline__ DenseParts(int64_t total, int blocks) {
-        parts = (int)min((int64_t)blocks, total);        // every part has a unit, so a query's shares have no holes
-        each = parts > 0 ? da_div(total, parts) : 0;
-        more = (int)(total - each * parts);
+    int parts, each, more;
+    __device__ __forceinline__ DenseParts(int total, int blocks) {
+        parts = min(blocks, total);                      // every part has a unit, so a query's shares have no holes
+        each = total <= blocks ? 1 : (int)((unsigned)total / (unsigned)blocks);
+        more = total - each * parts;
     }
-    __device__ __forceinline__ int64_t start(int b) const { return each * min(b, parts) + min(b, more); }
-    __device__ __forceinline__ int block_of(int64_t u) const {
-        const int64_t longer = (each + 1) * more;
-        return (int)(u < longer ? da_div(u, each + 1) : more + da_div(u - longer, each));
+    __device__ __forceinline__ int start(int b) const { return each * min(b, parts) + min(b, more); }
+    __device__ __forceinline__ int block_of(int u) const {
+        const int longer = (each + 1) * more;
+        return u < longer ? (unsigned)u / (unsigned)(each + 1) : more + (unsigned)(u - longer) / (unsigned)each;
     }
 };
 
@@ -131,7 +124,7 @@ __device__ __forceinline__ DenseWork da_work(const DenseArgs& a, int item) {
     const int ql = a.hgroups == 1 ? item : item >> 1;                    // at most 128 heads: one or two groups
     w.h0 = a.hgroups == 1 ? 0 : (item & 1) * DA_H;
     w.gq = a.query0 + ql;
-    w.b = (int)(a.query0 == 0 ? (unsigned)ql / (unsigned)a.n_q : w.gq / a.n_q);
+    w.b = (int)(a.n_q == 1 ? w.gq : a.query0 == 0 ? (unsigned)ql / (unsigned)a.n_q : w.gq / a.n_q);
     const int64_t p = a.q_pos[w.gq];
     const int64_t s0 = a.swa_pos0 != nullptr ? a.swa_pos0[w.b] : 0;
     const int64_t v = p >= WINDOW - 1 ? (p - (WINDOW - 1)) >> (a.ratio - 1) : 0;      // ratio 1 or 2
@@ -145,35 +138,35 @@ __device__ __forceinline__ DenseWork da_work(const DenseArgs& a, int item) {
 // One share of a block, and where the block's units go on after it
 struct DenseShare {
     int64_t row;                 // its first row: of the FP4 planes, or of the window rows
-    int64_t gq, u, start;        // its query; the next unit, and the first unit of the item that has it
+    int64_t gq;                  // its query
+    int u, start;                // the next unit, and the first unit of the item that has it
     int h0, rows, share, item, next_item, window;
 };
+// The share that begins at unit u < u1 of item `item` (work w, units from `start` on), if there is one there
+__device__ __forceinline__ bool da_part(const DenseArgs& a, const DenseWork& w, int& u, int u1, int& start, int& item,
+                                        DenseShare* out) {
+    const int ws = start + w.tiles(), end = ws + w.win();
+    const bool window = u >= ws;
+    const int upto = min(u1, window ? end : ws);
+    // of the window the tiles whose first units are among these (none: the rest of another block's tile)
+    const int t0 = window ? (u - ws + DA_WIN - 1) / DA_WIN : u - start;
+    const int t1 = window ? (upto - ws + DA_WIN - 1) / DA_WIN : upto - start;
+    const int row0 = t0 * DA_TILE;
+    out->row = (window ? (int64_t)w.b * a.swa_len + w.row0 : (int64_t)w.b * a.capacity) + row0;
+    out->rows = (int)min((int64_t)(t1 - t0) * DA_TILE, (int64_t)(window ? w.rows : w.n) - row0);
+    out->share = (window ? a.n_items + (int)gridDim.x - 1 : 0) + item + (int)blockIdx.x;
+    out->gq = w.gq, out->h0 = w.h0, out->item = item, out->window = window;
+    u = upto;
+    if (u >= end) start = end, ++item;
+    out->u = u, out->start = start, out->next_item = item;
+    return t1 > t0;
+}
 // The next share of the units u .. u1-1, `item` with units from `start` on being the one that has unit u;
 // rows = -1 when there is none.  One thread calls it while the block works on the share before, so that
 // this state lives in shared memory and not in everybody's registers.
-__device__ __noinline__ void da_next(const DenseArgs& a, int64_t u, int64_t u1, int64_t start, int item, DenseShare* out) {
-    while (u < u1) {
-        const DenseWork w = da_work(a, item);
-        const int tiles = w.tiles();
-        const int64_t ws = start + tiles, end = ws + w.win();
-        const bool window = u >= ws;
-        const int64_t upto = min(u1, window ? end : ws);
-        // of the window the tiles whose first units are among these
-        const int64_t t0 = window ? (u - ws + DA_WIN - 1) / DA_WIN : u - start;
-        const int64_t t1 = window ? (upto - ws + DA_WIN - 1) / DA_WIN : upto - start;
-        const bool run = t1 > t0;
-        const int64_t row0 = (window ? w.row0 : 0) + t0 * DA_TILE;
-        out->row = (int64_t)w.b * (window ? a.swa_len : a.capacity) + row0;
-        out->rows = (int)(min(t1 * DA_TILE, (int64_t)(window ? w.rows : w.n)) - t0 * DA_TILE);
-        out->share = (window ? a.n_items + (int)gridDim.x - 1 : 0) + item + (int)blockIdx.x;
-        out->gq = w.gq, out->h0 = w.h0, out->item = item, out->window = window;
-        u = upto;
-        if (u >= end) start = end, ++item;
-        if (run) {
-            out->u = u, out->start = start, out->next_item = item;
-            return;
-        }
-    }
+__device__ __noinline__ void da_next(const DenseArgs& a, int u, int u1, int start, int item, DenseShare* out) {
+    while (u < u1)
+        if (da_part(a, da_work(a, item), u, u1, start, item, out)) return;
     out->rows = -1;
 }
 
@@ -181,7 +174,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) unsigned long long b_lhalf[DA_NL], b_lfull[DA_NL], b_lfree[DA_NL], b_sfull[2], b_sfree[2],
         b_pfull[2], b_odone[2], b_next;
-    __shared__ int64_t wsum[DA_THREADS / 32], last_unit;
+    __shared__ int wsum[DA_THREADS / 32], last_unit;
     __shared__ DenseShare shares[2];
     __shared__ uint32_t tmem_base;
     const uint32_t raw = umma::smem_u32(dyn);
@@ -218,49 +211,55 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
     // ---- this block's units: a sum over the items' units, each thread taking consecutive items (two at most)
     const int per = (a.n_items + DA_THREADS - 1) / DA_THREADS;
     const int i0 = min(tid * per, a.n_items), ni = min(per, a.n_items - i0);
-    int tl[2] = {0, 0}, wn[2] = {0, 0};
-    int64_t own = 0;
+    DenseWork w[2];
+    int units[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         if (k < ni) {
-            const DenseWork w = da_work(a, i0 + k);
-            tl[k] = w.tiles(), wn[k] = w.win();
-            own += tl[k] + wn[k];
+            w[k] = da_work(a, i0 + k);
+            units[k] = w[k].tiles() + w[k].win();
         }
-    int64_t upto = own;
+    int upto = units[0] + units[1];
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
     }
     if (lane == 31) wsum[warp] = upto;
     __syncthreads();
-    int64_t before = 0, total = 0;
-    const int used = (a.n_items + per * 32 - 1) / (per * 32);            // warps that have items
-    for (int i = 0; i < used; ++i) {
-        const int64_t v = wsum[i];
+    int before = 0, total = 0;
+    for (int i = 0; i * per * 32 < a.n_items; ++i) {                     // warps that have items
+        const int v = wsum[i];
         if (i < warp) before += v;
         total += v;
     }
     const DenseParts pt(total, (int)gridDim.x);
-    const int64_t u0 = pt.start(blockIdx.x), u1 = pt.start(blockIdx.x + 1);
-    {
-        int64_t s = before + upto - own;
+    const int u0 = pt.start(blockIdx.x), u1 = pt.start(blockIdx.x + 1);
+    const int first = before + upto - units[0] - units[1];               // this thread's first unit
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (k < ni) {
-                const int64_t e = s + tl[k] + wn[k];
-                if (u0 < u1 && s <= u0 && u0 < e) da_next(a, u0, u1, s, i0 + k, &shares[0]);
-                if (blockIdx.x == 0) a.items[i0 + k] = DenseItem{s, tl[k], wn[k]};
-                s = e;
-            }
-        if (blockIdx.x == 0 && tid == 0) a.items[a.n_items].start = total;
-        if (tid == 0) last_unit = u1;
-        if (tid == 0 && u0 >= u1) shares[0].rows = -1;
+    for (int k = 0; k < 2; ++k) {
+        int u = u0, s = first + (k > 0 ? units[0] : 0), item = i0 + k;
+        if (k < ni && u0 < u1 && s <= u0 && u0 < s + units[k])
+            if (!da_part(a, w[k], u, u1, s, item, &shares[0])) da_next(a, u, u1, s, item, &shares[0]);
     }
+    if (tid == 0) last_unit = u1;
+    if (tid == 0 && u0 >= u1) shares[0].rows = -1;
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
     const uint32_t tmem = tmem_base;
+    // where the shares of every item are, for the kernel that joins them: the last block, which has least to do
+    if (blockIdx.x == gridDim.x - 1)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (k < ni) {
+                const int s = first + (k > 0 ? units[0] : 0), ws = s + w[k].tiles();
+                DenseItem it{0, 0, -1, -1};
+                if (ws > s) it.b0 = pt.block_of(s), it.n_fp4 = pt.block_of(ws - 1) - it.b0 + 1;
+                if (w[k].win() > 0) it.w0 = pt.block_of(ws);
+                if (w[k].win() > DA_WIN) it.w1 = pt.block_of(ws + DA_WIN);
+                if (it.w1 == it.w0) it.w1 = -1;
+                a.items[i0 + k] = it;
+            }
     bool ok = true;
     const int lt = tid - DA_LOADW * 32;
     int q_item = -1;                                         // the item whose queries are staged
@@ -314,21 +313,22 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
         if (q_item != S.item && warp < DA_LOADW) {
             const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + (S.gq * a.n_heads + S.h0) * D_LAT);
             const int nh = min(DA_H, a.n_heads - S.h0);
-            constexpr int HPW = (DA_H + DA_LOADW - 1) / DA_LOADW;
-            uint4 qv[HPW][2];
+            // (a loop: unrolled over all heads it waits for its own code)
+#pragma unroll 1
+            for (int h0 = warp; h0 < nh; h0 += 2 * DA_LOADW) {
+                uint4 qv[2][2];
 #pragma unroll
-            for (int r = 0; r < HPW; ++r) {
-                const int h = warp + DA_LOADW * r;
-                qv[r][0] = qv[r][1] = make_uint4(0, 0, 0, 0);
-                if (h < nh) {
-                    qv[r][0] = qsrc[h * 64 + lane];
-                    qv[r][1] = qsrc[h * 64 + 32 + lane];
+                for (int r = 0; r < 2; ++r) {
+                    const int h = h0 + DA_LOADW * r;
+                    if (h < nh) {
+                        qv[r][0] = qsrc[h * 64 + lane];
+                        qv[r][1] = qsrc[h * 64 + 32 + lane];
+                    }
                 }
-            }
 #pragma unroll
-            for (int r = 0; r < HPW; ++r) {
-                const int h = warp + DA_LOADW * r;
-                if (h < DA_H) {
+                for (int r = 0; r < 2; ++r) {
+                    const int h = h0 + DA_LOADW * r;
+                    if (h >= nh) break;
                     const uint32_t mx = __reduce_max_sync(0xffffffffu, max(bf16_absmax8(qv[r][0]), bf16_absmax8(qv[r][1])));
                     const int e = f16_range_exp(mx);
                     const float d = pow2f(-e);
@@ -340,6 +340,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
                     }
                     if (lane == 0) qexp[h] = e;
                 }
+            }
+#pragma unroll 1
+            for (int i = nh * 64 + tid; i < DA_H * 64; i += DA_LOADW * 32) {
+                *reinterpret_cast<uint4*>(sm + DA_SQ + ((i & 63) >> 3) * DA_QSLAB + da_swz(i >> 6, i & 7)) = make_uint4(0, 0, 0, 0);
+                qexp[i >> 6] = 0;
             }
             umma::fence_proxy_async();
         }
@@ -630,71 +635,67 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
 constexpr int DA_MAXS = DA_SMS + 2;              // shares of one query at most
 
 template <typename TO, int SPREAD>
-__global__ void __launch_bounds__(512) k_dense_combine(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                                                       const DenseItem* __restrict__ items, int n_items, int blocks,
-                                                       int hgroups, int n_heads, int64_t query0, int64_t n_rows,
-                                                       TO* __restrict__ out, float* __restrict__ lse) {
+__global__ void __launch_bounds__(512) k_dense_combine(const float* part_o, const float2* part_ml,
+                                                       const DenseItem* items, int n_items, int blocks,
+                                                       int hgroups, int n_heads, int64_t query0, int n_rows,
+                                                       TO* out, float* lse) {
+    constexpr int NK = (DA_MAXS + 31) / 32;
     __shared__ float4 sums[SPREAD > 1 ? 3 : 1][128];
+    __shared__ float factors[512 / 32][32 * NK];
     const int tid = threadIdx.x, lane = tid & 31, dim = tid & 127, group = SPREAD > 1 ? tid >> 7 : 0;
-    const int64_t row = SPREAD > 1 ? blockIdx.x : (int64_t)blockIdx.x * 4 + (tid >> 7);      // query of this pass, head
+    const int row = SPREAD > 1 ? (int)blockIdx.x : (int)blockIdx.x * 4 + (tid >> 7);         // query of this pass, head
+    const int ql = (int)((unsigned)row / (unsigned)n_heads);
+    const int head = row - ql * n_heads, item = ql * hgroups + head / DA_H;
+    float* fw = factors[tid >> 5];
     pdl_wait();
     if (SPREAD == 1 && row >= n_rows) return;
-    const int64_t ql = row / n_heads;
-    const int head = (int)(row - ql * n_heads), item = (int)ql * hgroups + head / DA_H;
-    const DenseItem it = items[item];
-    const DenseParts pt(items[n_items].start, blocks);
-    const int64_t ws = it.start + it.tiles;
-    int b0 = 0, n_fp4 = 0, n_win = 0, w0 = 0, w1 = 0;
-    if (it.tiles > 0) b0 = pt.block_of(it.start), n_fp4 = pt.block_of(ws - 1) - b0 + 1;
-    if (it.win > 0) {
-        w0 = pt.block_of(ws), n_win = 1;
-        if (it.win > DA_WIN) w1 = pt.block_of(ws + DA_WIN), n_win += w1 != w0;
-    }
-    const int n = n_fp4 + n_win;
+    const DenseItem it = *(items + item);
+    const int n = it.n_fp4 + (it.w0 >= 0) + (it.w1 >= 0);
     auto share = [&](int s) {
-        return (int64_t)item + (s < n_fp4 ? b0 + s : n_items + blocks - 1 + (s == n_fp4 ? w0 : w1));
+        return (int64_t)item + (s < it.n_fp4 ? it.b0 + s : n_items + blocks - 1 + (s == it.n_fp4 ? it.w0 : it.w1));
     };
-    constexpr int NK = (DA_MAXS + 31) / 32;
+    // several shares' loads in flight at a time (past the end: the last one again, times nothing), the first of
+    // them before the factors are known
+    constexpr int NB = SPREAD > 1 ? 8 : 4;
+    const float4* src = reinterpret_cast<const float4*>(part_o + (int64_t)(head % DA_H) * D_LAT) + dim;
+    float4 x[NB];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) x[i] = src[share(min(s0 + i * SPREAD, n - 1)) * DA_H * (D_LAT / 4)];
+    };
+    if (n > 0) load(group);
     float fs[NK], ls[NK], m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
         fs[k] = -INFINITY, ls[k] = 0.0f;
-        if (32 * k < n) {
-            const int s = 32 * k + lane;
-            if (s < n) {
-                const float2 v = part_ml[share(s) * DA_H + head % DA_H];
-                fs[k] = v.x, ls[k] = v.y;
-                if (v.y != 0.0f) m = fmaxf(m, v.x);
-            }
+        const int s = 32 * k + lane;
+        if (s < n) {
+            const float2 v = part_ml[share(s) * DA_H + head % DA_H];
+            fs[k] = v.x, ls[k] = v.y;
+            if (v.y != 0.0f) m = fmaxf(m, v.x);
         }
     }
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
-        fs[k] = ls[k] != 0.0f ? exp2f(fs[k] - m) : 0.0f;
-        l = fmaf(fs[k], ls[k], l);
-    }
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    float o[4] = {};
-    const float4* src = reinterpret_cast<const float4*>(part_o + (int64_t)(head % DA_H) * D_LAT) + dim;
-#pragma unroll
-    for (int k = 0; k < NK; ++k) {
-        const int end = min(n, 32 * k + 32);
-        // several shares' loads in flight at a time (past the end: the last one again, times nothing)
-        constexpr int NB = SPREAD > 1 ? 8 : 4;
-        for (int s0 = 32 * k + group; s0 < end; s0 += NB * SPREAD) {
-            float4 x[NB];
-#pragma unroll
-            for (int i = 0; i < NB; ++i) x[i] = src[share(min(s0 + i * SPREAD, end - 1)) * DA_H * (D_LAT / 4)];
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int s = s0 + i * SPREAD;
-                float f = __shfl_sync(0xffffffffu, fs[k], s & 31);
-                if (s >= end) f = 0.0f;
-                o[0] = fmaf(f, x[i].x, o[0]), o[1] = fmaf(f, x[i].y, o[1]);
-                o[2] = fmaf(f, x[i].z, o[2]), o[3] = fmaf(f, x[i].w, o[3]);
-            }
+    for (int k = 0; k < NK; ++k)
+        if (32 * k < n) {
+            fs[k] = ls[k] != 0.0f ? exp2f(fs[k] - m) : 0.0f;
+            l = fmaf(fs[k], ls[k], l);
+            fw[32 * k + lane] = fs[k];
         }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    __syncwarp();
+    float o[4] = {};
+    for (int s0 = group; s0 < n;) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int s = s0 + i * SPREAD;
+            const float f = s < n ? fw[s] : 0.0f;
+            o[0] = fmaf(f, x[i].x, o[0]), o[1] = fmaf(f, x[i].y, o[1]);
+            o[2] = fmaf(f, x[i].z, o[2]), o[3] = fmaf(f, x[i].w, o[3]);
+        }
+        s0 += NB * SPREAD;
+        if (s0 < n) load(s0);
     }
     if constexpr (SPREAD > 1) {
         if (group > 0) sums[group - 1][dim] = make_float4(o[0], o[1], o[2], o[3]);
@@ -728,12 +729,13 @@ struct DensePlan {
 DensePlan dense_plan(int64_t queries, int n_heads, int64_t capacity) {
     DensePlan p;
     p.hgroups = (n_heads + DA_H - 1) / DA_H;
-    p.pass_queries = std::min(queries, DA_PASS / p.hgroups);
+    const int64_t units = (capacity + DA_TILE - 1) / DA_TILE + DA_NL * DA_WIN;       // of an item, at most
+    p.pass_queries = std::min(queries, std::min(DA_PASS, 0x7fffffff / units) / p.hgroups);   // units are counted in 32 bits
     const int64_t items = p.pass_queries * p.hgroups;
     // one block per SM, fewer where even a full cache has fewer units
-    p.blocks = (int)std::min<int64_t>(DA_SMS, items * ((capacity + DA_TILE - 1) / DA_TILE + DA_NL * DA_WIN));
+    p.blocks = (int)std::min<int64_t>(DA_SMS, items * units);
     const size_t rows = (size_t)2 * (items + p.blocks - 1) * DA_H;
-    p.items_bytes = ((size_t)(items + 1) * sizeof(DenseItem) + 255) / 256 * 256;
+    p.items_bytes = ((size_t)items * sizeof(DenseItem) + 255) / 256 * 256;
     p.o_bytes = rows * D_LAT * sizeof(float);
     p.ml_bytes = rows * sizeof(float2);
     return p;
@@ -768,7 +770,7 @@ cudaError_t launch_dense_attn(const csa2_cache& c, const uint16_t* q, int n_q, i
             const int64_t rows = nq * n_heads;
             const bool spread = a.n_items * 8 <= p.blocks;
             launch_k(spread ? k_dense_combine<TO, 4> : k_dense_combine<TO, 1>, dim3((unsigned)(spread ? rows : (rows + 3) / 4)),
-                     512, 0, st, a.part_o, a.part_ml, a.items, a.n_items, p.blocks, p.hgroups, n_heads, q0, rows, y, lse);
+                     512, 0, st, a.part_o, a.part_ml, a.items, a.n_items, p.blocks, p.hgroups, n_heads, q0, (int)rows, y, lse);
         };
         if (out_type == CSA2_F32)
             join(reinterpret_cast<float*>(out));
