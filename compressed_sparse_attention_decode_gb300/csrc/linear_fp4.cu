@@ -341,9 +341,10 @@ constexpr uint32_t LM_CODES = LM_M * LM_CK / 2;  // bytes of codes of a stage
 
 struct LinPrep {                                 // the workspace's layout
     int nb, tiles, chunks, planes;               // tokens per tile, token tiles, 128-value chunks, fp16 parts
-    __host__ __device__ int64_t half_bytes() const { return (int64_t)nb * 128; }
-    __host__ __device__ int64_t stage_bytes() const { return half_bytes() * 2 * planes; }
-    // [group][token tile][chunk][part][half chunk] tiles of nb rows x 64 values in the MMA's swizzled layout
+    __host__ __device__ int cols() const { return nb * planes; }         // a product's: the parts of x side by side
+    __host__ __device__ int64_t half_bytes() const { return (int64_t)cols() * 128; }
+    __host__ __device__ int64_t stage_bytes() const { return half_bytes() * 2; }
+    // [group][token tile][chunk][half chunk][part] tiles of nb rows x 64 values in the MMA's swizzled layout
     __host__ __device__ int64_t stage(int g, int tt, int ch) const {
         return (((int64_t)g * tiles + tt) * chunks + ch) * stage_bytes();
     }
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(256) k_linear_x(const LinArgs a, LinPrep p, ui
         if (k < a.n_in) lin_split(e, d, hi, lo);
         uint8_t* at = ws + p.stage(g, tt, k >> 7) + ((k >> 6) & 1) * p.half_bytes() + r * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4);
         *reinterpret_cast<uint4*>(at) = hi;
-        if (SPLIT) *reinterpret_cast<uint4*>(at + 2 * p.half_bytes()) = lo;
+        if (SPLIT) *reinterpret_cast<uint4*>(at + p.nb * 128) = lo;
     };
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
@@ -458,7 +459,7 @@ __device__ __forceinline__ void lin_drain(bool ok, unsigned long long* full, uin
 }
 
 struct LinRings {
-    int tiles_m, splits, wide, c_stages;
+    int tiles_m, log_splits, wide, c_stages;
 };
 
 // Tiles (row tile, token tile, group) in that order of change from slow to fast: group, row tile, token
@@ -475,43 +476,44 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         b_dfree[2];
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int splits = rg.splits, CS = rg.c_stages, NB = p.nb;
+    const int splits = 1 << rg.log_splits, CS = rg.c_stages, NB = p.nb, NC = p.cols();
     const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
     uint8_t* sm = dyn + (base - raw);
     const uint32_t stage_bytes = (uint32_t)p.stage_bytes(), xb = base + (TMA ? CS * LM_CODES : 0u);
-    const int64_t tiles = (int64_t)rg.tiles_m * p.tiles * a.n_groups;
-    const int split = splits > 1 ? blockIdx.x % splits : 0;
-    const int64_t first = blockIdx.x / splits, step = gridDim.x / splits;
-    const int ch0 = (int)((int64_t)p.chunks * split / splits), n = (int)((int64_t)p.chunks * (split + 1) / splits) - ch0;
+    const int tiles = rg.tiles_m * p.tiles * a.n_groups;
+    const int split = blockIdx.x & (splits - 1);                 // (a power of two of them)
+    const int first = blockIdx.x >> rg.log_splits, step = gridDim.x >> rg.log_splits;
+    const int ch0 = (p.chunks * split) >> rg.log_splits, n = ((p.chunks * (split + 1)) >> rg.log_splits) - ch0;
     struct Tile {
         int m, t, g;
     };
-    auto tile_of = [&](int64_t i) {
+    auto tile_of = [&](int i) {                  // (in 32 bits: two 64-bit divisions are 1,500 clocks)
         Tile v;
-        v.t = (int)(i % p.tiles);
-        i /= p.tiles;
-        v.m = (int)(i % rg.tiles_m);
-        v.g = (int)(i / rg.tiles_m);
+        const int j = (unsigned)i / (unsigned)p.tiles;
+        v.t = i - j * p.tiles;
+        v.g = (unsigned)j / (unsigned)rg.tiles_m;
+        v.m = j - v.g * rg.tiles_m;
         return v;
     };
-    // TMEM: results in columns 0-255, (buffer, half of K) tiles of NB: two buffers up to 64 tokens, else one;
+    // TMEM: results in columns 0-255, (buffer, issuer) tiles of NC: two buffers up to 64 columns, else one;
     // expanded weights in LM_S x 64 columns from 256 on
     constexpr uint32_t cols = 512, t_a = 256;
-    const int bufs = NB <= 64 ? 2 : 1;
+    const int bufs = NC <= 64 ? 2 : 1;
     auto sa = [&](const void* q) { return umma::smem_u32(q); };
-    if (tid == 0) {
-        for (int i = 0; i < LM_S; ++i) {
-            umma::mbar_init(sa(&b_a[i]), 8);                     // four lane quarters x two halves of a chunk
-            umma::mbar_init(sa(&b_x[i]), 1);
-            umma::mbar_init(sa(&b_free[i]), 2);                  // both MMA issuers
+    static_assert(LM_S <= 32 && LM_MAXC <= 32, "a lane each");
+    if (warp == 0) {
+        if (lane < LM_S) {
+            umma::mbar_init(sa(&b_a[lane]), 8);                  // four lane quarters x two halves of a chunk
+            umma::mbar_init(sa(&b_x[lane]), 1);
+            umma::mbar_init(sa(&b_free[lane]), 1);
         }
-        for (int i = 0; i < LM_MAXC; ++i) {
-            umma::mbar_init(sa(&b_c[i]), 1);
-            umma::mbar_init(sa(&b_cfree[i]), LM_EXPAND);
+        if (lane < LM_MAXC) {
+            umma::mbar_init(sa(&b_c[lane]), 1);
+            umma::mbar_init(sa(&b_cfree[lane]), LM_EXPAND);
         }
-        for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(sa(&b_d[i]), 2);
-            umma::mbar_init(sa(&b_dfree[i]), LM_EPI);
+        if (lane < 2) {
+            umma::mbar_init(sa(&b_d[lane]), 2);                  // both issuers
+            umma::mbar_init(sa(&b_dfree[lane]), LM_EPI);
         }
         umma::fence_mbar_init();
     }
@@ -527,15 +529,15 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         tmem = tmem_base;
     };
     bool ok = true;
-    const int my_tiles = first < tiles ? (int)((tiles - first + step - 1) / step) : 0;
+    const int my_tiles = first < tiles ? (tiles - 1 - first) / step + 1 : 0;
     // Results of tile ti: this warp's lane quarter (rows along the lanes), token columns 16 (part + i * parts),
-    // both halves of K added.  With splits, to this block's shared memory as [token][128 rows].
+    // both issuers' sums (and of fp32 both parts') added.  With splits, to this block's shared memory as [token][128 rows].
     auto store = [&](int ti, int part, int parts) {
         const Tile v = tile_of(first + ti * step);
         const int q = warp & 3, buf = ti % bufs, m = v.m * LM_M + q * 32 + lane, t0 = v.t * NB, nt = min(NB, a.n_tok - t0);
         const float* scale = reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)v.g * a.n_tok + t0;
         float* mine = reinterpret_cast<float*>(sm);
-        const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + 2 * buf * NB;
+        const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + 2 * buf * NC;
         float f[16];
         auto scales = [&](int c) {
 #pragma unroll
@@ -547,10 +549,20 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         for (int c = 16 * part; c < nt; c += 16 * parts) {
             float r[16], r1[16];
             umma::tmem_ld16(d + c, r);
-            umma::tmem_ld16(d + NB + c, r1);
+            umma::tmem_ld16(d + NC + c, r1);
             umma::tmem_wait_ld();
+            // without a second chunk the second issuer has no products, without a first one nobody has
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = ok ? (n > 0 ? r[i] + r1[i] : 0.0f) : __int_as_float(0x7fc00000);
+            for (int i = 0; i < 16; ++i) r[i] = n > 1 ? r[i] + r1[i] : n > 0 ? r[i] : 0.0f;
+            for (int k = 0; k < (p.planes > 1 ? min(n, 2) : 0); ++k) {
+                umma::tmem_ld16(d + k * NC + NB + c, r1);
+                umma::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] += r1[i];
+            }
+            if (!ok)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] = __int_as_float(0x7fc00000);
             if (splits > 1) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) mine[(c + i) * LM_M + q * 32 + lane] = r[i];
@@ -712,42 +724,41 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             lin_drain(ok, b_c, CS, it);
         }
     } else {
-        // ================= MMAs: two issuers, one per half of each chunk (one thread cannot issue fast enough to
-        // fill the tensor cores); a whole warp walks the chunks, so that descriptors and addresses stay in
-        // uniform registers, and one elected lane issues
+        // ================= MMAs: two issuers, for the even and the odd chunks of a tile (one thread issues an MMA per
+        // 65 clocks and is held 200 by a commit, whatever the sizes; a chunk's halves for one each meant two
+        // commits a chunk, 740-800 clocks); a whole warp walks the chunks, so that descriptors and addresses stay
+        // in uniform registers, and one elected lane issues
         const int hf = warp - (LM_XW + 2);
         if (hf == 0) umma::tmem_alloc(sa(&tmem_base), cols);
         tmem_ready();
-        const uint32_t id = umma::idesc_f16(LM_M, NB, 0, 0);
-        const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
-        uint32_t it = 0;
+        const uint32_t id = umma::idesc_f16(LM_M, NC, 0, 0);
+        const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem), half_bytes = (uint32_t)p.half_bytes();
         bool there = false;
         for (int ti = 0; ti < my_tiles && ok; ++ti) {
             const int buf = ti % bufs;
             if (ti >= bufs) ok = ok && umma::mbar_wait_fast(sa(&b_dfree[buf]), (ti / bufs - 1) & 1);
-            for (int j = 0; j < n && ok; ++j, ++it) {
-                const uint32_t st = it % LM_S, ph = (it / LM_S) & 1;
+            for (int j = hf; j < n && ok; j += 2) {
+                const uint32_t it = (uint32_t)ti * n + j, st = it % LM_S, ph = (it / LM_S) & 1;
                 if (!there) ok = ok && umma::mbar_wait_fast(sa(&b_x[st]), ph) && umma::mbar_wait_fast(sa(&b_a[st]), ph);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 // asked while this chunk's products are issued
-                const uint32_t nst = (it + 1) % LM_S, nph = ((it + 1) / LM_S) & 1;
+                const uint32_t nit = j + 2 < n ? it + 2 : (uint32_t)(ti + 1) * n + hf, nst = nit % LM_S, nph = (nit / LM_S) & 1;
                 const bool nx = umma::mbar_test(sa(&b_x[nst]), nph), na = umma::mbar_test(sa(&b_a[nst]), nph);
                 umma::fence_after();
+                const uint64_t bd = umma::desc(xb + st * stage_bytes, 16, 1024, umma::LAYOUT_SW128);
                 if (umma::elect_one()) {
-                    for (int pl = 0; pl < p.planes; ++pl) {
-                        const uint64_t bd = umma::desc(xb + st * stage_bytes + (2 * pl + hf) * (uint32_t)p.half_bytes(), 16, 1024, umma::LAYOUT_SW128);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ta(tm + (2 * buf + hf) * NB, tm + t_a + 64 * st + 32 * hf + 8 * ks, bd + (uint64_t)((ks * 32) >> 4),
-                                       id, j > 0 || pl > 0 || ks > 0);
-                    }
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_f16_ta(tm + (2 * buf + hf) * NC, tm + t_a + 64 * st + 8 * ks,
+                                   bd + (uint64_t)(((ks >> 2) * half_bytes + (ks & 3) * 32) >> 4), id, j > hf || ks > 0);
                     umma::commit(sa(&b_free[st]));
-                    if (j == n - 1) umma::commit(sa(&b_d[buf]));
                 }
                 __syncwarp();
                 there = __all_sync(0xffffffffu, nx && na);
             }
+            if (ok && umma::elect_one()) umma::commit(sa(&b_d[buf]));
+            __syncwarp();
         }
     }
     __syncwarp();                                // two warps ran their loops in one lane
@@ -869,12 +880,18 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     }
     const LinPrep p = lin_prep(x_type, a.n_tok, a.n_in);
     uint8_t* ws = reinterpret_cast<uint8_t*>(wsp);
+    // the split of L1 and shared memory that the product needs: an SM changes it only when it is idle, and the
+    // product's blocks are to start beside this kernel's
+    cudaError_t e = cudaFuncSetAttribute(k_linear_x<TX>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     launch_k(k_linear_x<TX>, dim3(a.n_tok, a.n_groups), 256, 0, st, a, p, ws + LM_HEAD, x_vec);
     // Splits of n_in: while the row and token tiles leave SMs idle and a split keeps four chunks
     const int tiles_m = (a.n_out + LM_M - 1) / LM_M;
     const int64_t tiles = (int64_t)tiles_m * p.tiles * a.n_groups;
-    LinRings rg{tiles_m, 1, lin_wide(a), 0};
-    while (rg.splits < 8 && tiles * rg.splits * 2 <= 152 && p.chunks >= rg.splits * 2 * 4) rg.splits *= 2;
+    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;        // y alone would be past any memory
+    LinRings rg{tiles_m, 0, lin_wide(a), 0};
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 152 && p.chunks >= splits * 2 * 4) splits *= 2, ++rg.log_splits;
     // code stages: what the token ring leaves (a tensor copy lands about 2 us after its issue)
     rg.c_stages = (int)std::min<int64_t>(LM_MAXC, (224 * 1024 - LM_S * p.stage_bytes()) / LM_CODES);
     const bool tma = a.n_in % 32 == 0 && a.n_in > 0 && (int64_t)a.n_groups * a.n_out <= 0x7fffffff && lin_encode() != nullptr;
@@ -890,11 +907,11 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     }
     const auto kern = tma ? k_linear_many<true> : k_linear_many<false>;
     const size_t smem = std::max<size_t>((tma ? rg.c_stages * (size_t)LM_CODES : 0) + (size_t)LM_S * p.stage_bytes(),
-                                         rg.splits > 1 ? (size_t)p.nb * LM_M * 4 : 0) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+                                         splits > 1 ? (size_t)p.nb * LM_M * 4 : 0) + 1024;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rg.splits > 1 ? tiles * rg.splits : std::min<int64_t>(tiles, 152)));
+    cfg.gridDim = dim3((unsigned)(splits > 1 ? tiles * splits : std::min<int64_t>(tiles, 152)));
     cfg.blockDim = dim3(LM_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -902,9 +919,9 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = rg.splits, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.x = splits, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, tm, a, p, (const uint8_t*)(ws + LM_HEAD), reinterpret_cast<int*>(ws), rg);
     note_launch(2);
     return e != cudaSuccess ? e : cudaGetLastError();
