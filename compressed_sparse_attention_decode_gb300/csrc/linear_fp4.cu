@@ -574,9 +574,10 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             if (m < a.n_out) {
                 const int64_t y0 = (int64_t)(t0 + c) * a.y_tok + v.g * a.y_group + m;
                 auto put = [&](auto* y) {
+                    y += y0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c + i < nt) y[y0 + i * a.y_tok] = from_f32<std::remove_pointer_t<decltype(y)>>(r[i]);
+                    for (int i = 0; i < 16; ++i, y += a.y_tok)
+                        if (i < nt - c) *y = from_f32<std::remove_pointer_t<decltype(y)>>(r[i]);
                 };
                 if (a.y_type == CSA2_BF16)
                     put(reinterpret_cast<__nv_bfloat16*>(a.y));
@@ -880,10 +881,7 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     }
     const LinPrep p = lin_prep(x_type, a.n_tok, a.n_in);
     uint8_t* ws = reinterpret_cast<uint8_t*>(wsp);
-    // the split of L1 and shared memory that the product needs: an SM changes it only when it is idle, and the
-    // product's blocks are to start beside this kernel's
-    cudaError_t e = cudaFuncSetAttribute(k_linear_x<TX>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     launch_k(k_linear_x<TX>, dim3(a.n_tok, a.n_groups), 256, 0, st, a, p, ws + LM_HEAD, x_vec);
     // Splits of n_in: while the row and token tiles leave SMs idle and a split keeps four chunks
     const int tiles_m = (a.n_out + LM_M - 1) / LM_M;
