@@ -81,7 +81,7 @@ __device__ __forceinline__ float lin_absmax(const ElemVec<TX, 8>& v) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, v.w[i] & 0x7fffffffu);
     }
-    if (m < 0x7f800000u) return __uint_as_float(m);
+    if (__builtin_expect(m < 0x7f800000u, 1)) return __uint_as_float(m);
     float f = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -176,19 +176,18 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
         umma::fence_mbar_init();
     }
     pdl_wait();                                  // x, and weights just quantised, may come from the preceding kernel
-    if (warp == 0) {
+    __syncthreads();                             // the barriers
+#pragma unroll 1
+    for (int i = warp; i < R; i += warps) {      // a tile's copies are some 150 instructions: a warp for each
+        const int n = max(0, min(16, rows - 16 * i));
+        const uint64_t cb = c0 + (uint64_t)i * 8 * K, sb = s0 + (uint64_t)i * K;
+        const uint32_t nc = (uint32_t)n * (K / 2), ns = (uint32_t)n * (K / 16);
+        const uint32_t bar = umma::smem_u32(&b_tile[i]);
+        if (lane == 0) umma::mbar_arrive_expect_tx(bar, n > 0 ? lf_bulk_bytes(cb, nc) + lf_bulk_bytes(sb, ns) : 0u);
         __syncwarp();
-        for (int i = 0; i < R; ++i) {
-            const int n = max(0, min(16, rows - 16 * i));
-            const uint64_t cb = c0 + (uint64_t)i * 8 * K, sb = s0 + (uint64_t)i * K;
-            const uint32_t nc = (uint32_t)n * (K / 2), ns = (uint32_t)n * (K / 16);
-            const uint32_t bar = umma::smem_u32(&b_tile[i]);
-            if (lane == 0) umma::mbar_arrive_expect_tx(bar, n > 0 ? lf_bulk_bytes(cb, nc) + lf_bulk_bytes(sb, ns) : 0u);
-            __syncwarp();
-            if (n > 0) {
-                lf_copy(sm + i * c_tile, a.codes, cb, nc, bar, lane);
-                lf_copy(sm_s + i * s_tile, a.scales, sb, ns, bar, lane);
-            }
+        if (n > 0) {
+            lf_copy(sm + i * c_tile, a.codes, cb, nc, bar, lane);
+            lf_copy(sm_s + i * s_tile, a.scales, sb, ns, bar, lane);
         }
     }
 
@@ -236,7 +235,16 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
     // results are not stored), and values from n_in on are zeros
     const uint32_t co = (uint32_t)(c0 & 15), so = (uint32_t)(s0 & 15);     // of every tile: a tile is a multiple of 16 bytes
     const bool wide = K % 32 == 0;               // codes 16 bytes apart from a 16-byte boundary, scales in pairs
-    auto segment = [&](int tile, int row, int k, uint4& cw, uint32_t& sw) {
+    const bool full = rows == 16 * R && K % 128 == 0 && co == 0;         // nothing to check, few addresses to find
+    const uint8_t* cl = sm + (uint32_t)r * (K / 2) + c * 16;
+    const uint8_t* sl = sm_s + so + (uint32_t)r * (K / 16) + c * 2;
+    auto segment = [&](int tile, int hi, int ch, uint4& cw, uint32_t& sw) {
+        if (full) {
+            cw = *reinterpret_cast<const uint4*>(cl + tile * c_tile + hi * (K / 2) + ch * 64);
+            sw = *reinterpret_cast<const uint16_t*>(sl + tile * s_tile + hi * (K / 16) + ch * 8);
+            return;
+        }
+        const int row = r + hi, k = ch * 128 + c * 32;
         const int rr = min(row, rows - 1 - tile * 16);
         const uint8_t* cp = sm + tile * c_tile + co + (uint32_t)rr * (K / 2) + k / 2;
         const uint8_t* sp = sm_s + tile * s_tile + so + (uint32_t)rr * (K / 16) + k / 16;
@@ -272,8 +280,8 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
             if (ch == warp) ok = ok && umma::mbar_wait_fast(umma::smem_u32(&b_tile[tile]), 0);
             uint4 va, vb;
             uint32_t sa, sb;
-            segment(tile, r, ch * 128 + c * 32, va, sa);
-            segment(tile, r + 8, ch * 128 + c * 32, vb, sb);
+            segment(tile, 0, ch, va, sa);
+            segment(tile, 8, ch, vb, sb);
             const __half2 pa = e4m3x2_to_f16x2(sa), pb = e4m3x2_to_f16x2(sb);
             const uint32_t xa[4] = {va.x, va.y, va.z, va.w}, xb[4] = {vb.x, vb.y, vb.z, vb.w};
             float d[NT][2][4] = {};              // two sums: consecutive products do not wait for each other
