@@ -13,7 +13,8 @@
 // Two kernels:
 //  - k_linear_few (up to 16 tokens; 8 of fp32).  The weights' bytes are its floor; what
 //    it runs at is the latency of asking, expanding and joining: one token, 1,536 ->
-//    32,768 (28 MB) takes 10.1 us, 2.8 TB/s, at 42 % of the issue slots.  mma.sync
+//    32,768 (28 MB) takes 8.9 us, 3.2 TB/s, and the SMs' instructions: 190 a warp
+//    for 16 rows of 128 values, after 2.5 us of starting and converting x.  mma.sync
 //    m16n8k16, the weights as the A fragments.  The order of k within a product is
 //    free as long as both operands agree, so a lane takes 16 consecutive bytes of a
 //    row (32 weights, two scale groups) and feeds them, four at a time, to eight
@@ -148,23 +149,23 @@ __device__ __forceinline__ void lf_copy(uint8_t* dst, const uint8_t* src, uint64
     if (lane < (int)rest) dst[whole + lane] = src[a + whole + lane];
 }
 
-// A block takes R tiles of 16 rows.  Rows are contiguous, so a tile's codes and scales are one piece of
+// A block takes up to R tiles of 16 rows: `each`, the first `more` blocks one more.  Rows are contiguous, so a tile's codes and scales are one piece of
 // memory each: all of them are requested by bulk copies as the block starts, which keeps more bytes in
 // flight than registers could (one token, 1,536 x 32,768: every block's rows at once), and each tile has a
 // barrier of its own.  The warps split n_in in chunks of 128, warp w taking chunks w, w + warps, ..; per
 // chunk a warp holds the tokens' fragments in registers and runs all R tiles over them.  The warps' sums are
 // joined at the end, in order.
 template <typename TX, int NT, int R>
-__global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a, int x_vec) {
+__global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a, int x_vec, int each, int more) {
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ __align__(8) unsigned long long b_tile[R];
     constexpr bool SPLIT = sizeof(TX) == 4, SCALED = !std::is_same<TX, __half>::value;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     const int K = a.n_in, T = a.n_tok, g = blockIdx.y;
     const int chunks = (K + 127) / 128;
-    const int m0 = blockIdx.x * (16 * R);
+    const int m0 = 16 * ((int)blockIdx.x * each + min((int)blockIdx.x, more));
     const int r = lane >> 2, c = lane & 3;
-    const int rows = min(16 * R, a.n_out - m0);
+    const int rows = min(16 * (each + ((int)blockIdx.x < more)), a.n_out - m0);
     // tile i's codes at sm + i * (8 K + 16), its scales after all codes at i * (K + 16) (both with the source's
     // offset to 16 bytes)
     const uint32_t c_tile = 8u * K + 16, s_tile = (uint32_t)K + 16;
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
     // results are not stored), and values from n_in on are zeros
     const uint32_t co = (uint32_t)(c0 & 15), so = (uint32_t)(s0 & 15);     // of every tile: a tile is a multiple of 16 bytes
     const bool wide = K % 32 == 0;               // codes 16 bytes apart from a 16-byte boundary, scales in pairs
-    const bool full = rows == 16 * R && K % 128 == 0 && co == 0;         // nothing to check, few addresses to find
+    const bool full = rows % 16 == 0 && K % 128 == 0 && co == 0;         // nothing to check, few addresses to find
     const uint8_t* cl = sm + (uint32_t)r * (K / 2) + c * 16;
     const uint8_t* sl = sm_s + so + (uint32_t)r * (K / 16) + c * 2;
     auto segment = [&](int tile, int hi, int ch, uint4& cw, uint32_t& sw) {
@@ -326,11 +327,11 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
             }
     __syncthreads();
     for (int u = tid; u < T * R * 16; u += blockDim.x) {
-        const int t = u / (R * 16), m = m0 + u % (R * 16);
-        if (m >= a.n_out) continue;
+        const int t = u / (R * 16), m = u % (R * 16);
+        if (m >= rows) continue;
         float v = 0.0f;
         for (int w = 0; w < warps; ++w) v += red[w * T * (R * 16) + u];
-        lin_store(a, t, g, m, v * a.alpha);
+        lin_store(a, t, g, m0 + m, v * a.alpha);
     }
     __syncthreads();
     if (tid == 0) __threadfence();               // the attention may stage these rows before it waits (see norm_rope.cu)
@@ -856,7 +857,13 @@ cudaError_t lf_launch(const LinArgs& a, int x_vec, int warps, cudaStream_t st) {
         cudaError_t e = cudaFuncSetAttribute(k_linear_few<TX, NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    launch_k(k_linear_few<TX, NT, R>, dim3((a.n_out + 16 * R - 1) / (16 * R), a.n_groups), warps * 32, smem, st, a, x_vec);
+    // As many blocks as R tiles each need, and then as many more as there are SMs without one in the last round:
+    // the SMs' shares differ by a tile, not by a block (32,768 rows: 608 blocks of 3 or 4 tiles for 512 of 4,
+    // one token 8.9 us for 9.7)
+    const int tiles = (a.n_out + 15) / 16;
+    const int64_t need = (int64_t)((tiles + R - 1) / R) * a.n_groups;
+    const int blocks = (int)std::min<int64_t>(tiles, (need + 151) / 152 * 152 / a.n_groups);
+    launch_k(k_linear_few<TX, NT, R>, dim3(blocks, a.n_groups), warps * 32, smem, st, a, x_vec, tiles / blocks, tiles % blocks);
     note_launch();
     return cudaGetLastError();
 }
