@@ -869,11 +869,13 @@ cudaError_t lf_launch(const LinArgs& a, int x_vec, int warps, cudaStream_t st) {
 }
 template <typename TX, int NT>
 cudaError_t lf_pick(const LinArgs& a, int x_vec, cudaStream_t st) {
-    // Row tiles per block: four (the tokens' fragments are made once for all) when that still gives every SM
-    // blocks and two of them fit an SM's shared memory, else one
+    // Row tiles per block: four or two (the tokens' fragments are made once for all) when that still gives every
+    // SM blocks and two of them fit an SM's shared memory, else one (one token, 4,096 x 8,192: two tiles 8.1 us,
+    // one 13.2; 1,536 x 32,768: four 9.0, two 16.1)
     const int chunks = std::max(1, (a.n_in + 127) / 128);
     const int64_t tiles = (int64_t)((a.n_out + 15) / 16) * a.n_groups;
-    const bool four = tiles >= 152 * 4 && 4 * (9 * a.n_in + 32) <= LF_SMEM / 2;
+    auto fit = [&](int r) { return tiles >= 152 * r && r * (9 * a.n_in + 32) <= LF_SMEM / 2; };
+    const bool four = fit(4);
     // Warps: the most, up to 8, that divide the chunks (nearly) as evenly as any number does; up to 4 with four
     // row tiles, so that four blocks stay on an SM (1,536 x 32,768, one token: 10.6 us against 13.6 with six)
     const int most = std::min(chunks, four ? 4 : LF_MAXW);
@@ -883,7 +885,9 @@ cudaError_t lf_pick(const LinArgs& a, int x_vec, cudaStream_t st) {
         const double even = (double)chunks / ((double)w * ((chunks + w - 1) / w));
         if (even >= best - 0.02) best = std::max(best, even), warps = w;
     }
-    return four ? lf_launch<TX, NT, 4>(a, x_vec, warps, st) : lf_launch<TX, NT, 1>(a, x_vec, warps, st);
+    return four     ? lf_launch<TX, NT, 4>(a, x_vec, warps, st)
+           : fit(2) ? lf_launch<TX, NT, 2>(a, x_vec, warps, st)
+                    : lf_launch<TX, NT, 1>(a, x_vec, warps, st);
 }
 template <typename TX>
 cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st) {
