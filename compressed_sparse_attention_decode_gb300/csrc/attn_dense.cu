@@ -24,8 +24,8 @@
 //   O^T += L^T . P  (M = 4 x 128 dims, N = 64 heads, K = 64 keys; two issuers)
 // What bounds a tile is shared memory: 64 KB written, 128 KB read by the score MMAs (64
 // of them the query again) and 96 KB by the value MMAs, 2,250 clocks at 128 bytes a
-// clock, against 3,300 measured (64 queries of 64 heads at 32K, 16,320 entries each: 216 us
-// with the join, 639 TFLOP/s).  Three buffers of 48 keys, which take the buffers'
+// clock, against 3,200 measured (64 queries of 64 heads at 32K, 16,320 entries each: 206 us
+// with the join, 670 TFLOP/s).  Three buffers of 48 keys, which take the buffers'
 // round off the critical path, read more per key and were slower (2,700 per 48).
 // Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 load the
 // FP4 rows and expand them to fp16 (exact: an E2M1 value times an E4M3 scale has at

@@ -26,10 +26,11 @@
 //    clock of the 128 it gives.  x comes by bulk copies in the layout that
 //    k_linear_x has written to the workspace.  When there are few row tiles a
 //    cluster of blocks splits n_in and adds up through distributed shared memory.
-//    What bounds it is the chain per 128 weights of every row (wait, expand, issue,
-//    commit): 850 clocks, where the tensor pipe needs 512 at 128 tokens.  64 tokens,
-//    1,536 -> 32,768: 17.5 us; 256 tokens, 4,096 -> 8,192: 21.1 us (814 TFLOP/s);
-//    both with k_linear_x, which overlaps its start.
+//    What bounds it is the tensor pipe with 128 tokens (600 clocks per 128 values of
+//    a row tile; the measured bf16 rate would take 590), and with fewer its pipeline's
+//    start (2.5 us to the first product: codes, expansion, x) and end (1.5 us).  64
+//    tokens, 1,536 -> 32,768: 14.6 us; 256 tokens, 4,096 -> 8,192: 19.3 us (890 TFLOP/s
+//    on 128 of the 152 SMs); both with k_linear_x, which overlaps its start.
 #include <algorithm>
 #include <type_traits>
 
@@ -547,6 +548,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         const float* scale = reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)v.g * a.n_tok + t0;
         float* mine = reinterpret_cast<float*>(sm);
         const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + 2 * buf * NC;
+        const int one = n == 1 ? ti & 1 : 0;                     // the issuer that has a tile's only chunk
         float f[16];
         auto scales = [&](int c) {
 #pragma unroll
@@ -557,14 +559,14 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         umma::fence_after();
         for (int c = 16 * part; c < nt; c += 16 * parts) {
             float r[16], r1[16];
-            umma::tmem_ld16(d + c, r);
+            umma::tmem_ld16(d + one * NC + c, r);
             umma::tmem_ld16(d + NC + c, r1);
             umma::tmem_wait_ld();
-            // without a second chunk the second issuer has no products, without a first one nobody has
+            // with a single chunk one issuer has products, without any none
 #pragma unroll
             for (int i = 0; i < 16; ++i) r[i] = n > 1 ? r[i] + r1[i] : n > 0 ? r[i] : 0.0f;
             for (int k = 0; k < (p.planes > 1 ? min(n, 2) : 0); ++k) {
-                umma::tmem_ld16(d + k * NC + NB + c, r1);
+                umma::tmem_ld16(d + (k + one) * NC + NB + c, r1);
                 umma::tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) r[i] += r1[i];
@@ -601,7 +603,8 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
 
     if (warp < LM_EXPAND) {
         // ================= weights: warp w takes rows 32(w%4) .. +31 of the tile, half (w/4)%2 of a chunk and
-        // every second chunk.  Only x and its scales come from the kernel before this one: nothing waits here.
+        // every second of the block's chunks, as the issuers do (not of a tile's: a stage then has the same warps
+        // each time, which have waited for its phase before, so that no wait can meet a barrier two phases back).  Only x and its scales come from the kernel before this one: nothing waits here.
         const int q = warp & 3, hf = (warp >> 2) & 1, par = warp >> 3, rt = q * 32 + lane;
         const uint8_t *cr = nullptr, *sr = nullptr;
         const int pairs = (n + 1) / 2;                           // of a tile's chunks; a code stage holds a pair
@@ -619,7 +622,8 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     cr = a.codes + row * (a.n_in / 2);
                     sr = a.scales + row * (a.n_in / 16);
                 }
-                if (2 * ai + par < n) k = (ch0 + 2 * ai + par) * LM_K + hf * 64;
+                const int jj = 2 * ai + (par ^ (at & n & 1));    // tile `at` begins with chunk at * n of the block's
+                if (jj < n) k = (ch0 + jj) * LM_K + hf * 64;
                 if (++ai == pairs) ai = 0, ++at;
             }
             sc[i] = lin_scales4(sr, k, a.n_in, rg.wide);
@@ -630,15 +634,15 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             if (total > 0) ahead(i);
         uint4 c[2];
         int cs = 0, cph = 0;                                     // code stage of the pair in c, and its phase
-        auto take = [&](int stage) {
+        auto take = [&](int stage, int odd) {                    // the even or the odd chunk of a stage's pair
             const uint8_t* src = sm + stage * LM_CODES + rt * 128;
-            const int u = par * 4 + hf * 2;
+            const int u = odd * 4 + hf * 2;
             c[0] = *reinterpret_cast<const uint4*>(src + ((u ^ (rt & 7)) << 4));
             c[1] = *reinterpret_cast<const uint4*>(src + (((u + 1) ^ (rt & 7)) << 4));
         };
         if (TMA && total > 0) {
             ok = ok && umma::mbar_wait_fast(sa(&b_c[0]), 0);
-            take(0);
+            take(0, par);
         }
         tmem_ready();
         int j = par;                                             // chunk within the tile
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     if (lane == 0) umma::mbar_arrive(sa(&b_cfree[cs]));
                     if (more) {
                         if (!c_there) ok = ok && umma::mbar_wait(sa(&b_c[ncs]), ncph);
-                        take(ncs);
+                        take(ncs, (j ^ (j + 2 >= 2 * pairs ? n : 0)) & 1);
                     }
                     cs = ncs, cph = ncph;
                 }
@@ -686,7 +690,10 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     if (lane == 0) umma::mbar_arrive(sa(&b_a[st]));
                 }
                 j += 2, it += 2;
-                if (j >= 2 * pairs) j -= 2 * pairs, it -= 2 * pairs - n;
+                if (j >= 2 * pairs) {                            // the next tile, of which it has the other chunks where n is odd
+                    const int nj = (j ^ n) & 1;
+                    it += n + nj - j, j = nj;
+                }
             }
         }
     } else if (warp < LM_XW) {
@@ -734,7 +741,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             lin_drain(ok, b_c, CS, it);
         }
     } else {
-        // ================= MMAs: two issuers, for the even and the odd chunks of a tile (one thread issues an MMA per
+        // ================= MMAs: two issuers, for the even and the odd chunks of the block (one thread issues an MMA per
         // 65 clocks and is held 200 by a commit, whatever the sizes; a chunk's halves for one each meant two
         // commits a chunk, 740-800 clocks); a whole warp walks the chunks, so that descriptors and addresses stay
         // in uniform registers, and one elected lane issues
@@ -747,13 +754,13 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         for (int ti = 0; ti < my_tiles && ok; ++ti) {
             const int buf = ti % bufs;
             if (ti >= bufs) ok = ok && umma::mbar_wait_fast(sa(&b_dfree[buf]), (ti / bufs - 1) & 1);
-            for (int j = hf; j < n && ok; j += 2) {
+            for (int j = (hf ^ (ti & n)) & 1; j < n && ok; j += 2) {
                 const uint32_t it = (uint32_t)ti * n + j, st = it % LM_S, ph = (it / LM_S) & 1;
                 if (!there) ok = ok && umma::mbar_wait_fast(sa(&b_x[st]), ph) && umma::mbar_wait_fast(sa(&b_a[st]), ph);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 // asked while this chunk's products are issued
-                const uint32_t nit = j + 2 < n ? it + 2 : (uint32_t)(ti + 1) * n + hf, nst = nit % LM_S, nph = (nit / LM_S) & 1;
+                const uint32_t nst = (it + 2) % LM_S, nph = ((it + 2) / LM_S) & 1;
                 const bool nx = umma::mbar_test(sa(&b_x[nst]), nph), na = umma::mbar_test(sa(&b_a[nst]), nph);
                 umma::fence_after();
                 const uint64_t bd = umma::desc(xb + st * stage_bytes, 16, 1024, umma::LAYOUT_SW128);
@@ -761,7 +768,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         mma_f16_ta(tm + (2 * buf + hf) * NC, tm + t_a + 64 * st + 8 * ks,
-                                   bd + (uint64_t)(((ks >> 2) * half_bytes + (ks & 3) * 32) >> 4), id, j > hf || ks > 0);
+                                   bd + (uint64_t)(((ks >> 2) * half_bytes + (ks & 3) * 32) >> 4), id, j > 1 || ks > 0);
                     umma::commit(sa(&b_free[st]));
                 }
                 __syncwarp();

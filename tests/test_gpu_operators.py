@@ -122,6 +122,12 @@ def test_linear_outer_sizes(csa, M, T):
     check_linear(csa, T, 1, 320, M, HF, F, seed=M)
 
 
+@pytest.mark.parametrize("K", [112, 128, 384, 640, 1168])        # one and odd numbers of 128-value chunks
+@pytest.mark.parametrize("T,xt", [(20, BF), (20, F), (70, HF), (200, BF)])
+def test_linear_blocks_with_several_tiles(csa, K, T, xt):
+    check_linear(csa, T, 1, K, 60001, xt, BF, seed=K)
+
+
 @pytest.mark.parametrize("T,G,K,M", [(1, 3, 160, 50), (5, 16, 512, 64), (40, 5, 96, 100), (130, 2, 1024, 200)])
 @pytest.mark.parametrize("xt", [BF, HF, F])
 def test_linear_groups(csa, T, G, K, M, xt):
