@@ -10,7 +10,8 @@
 // 455 flop per byte, so the tensor cores bound it; with few heads the heads pad the
 // MMA's 64 rows.  Lengths are known on the device alone, so the blocks (one per SM)
 // share the work there: each (query, 64 heads) is as many units as it has 64-key
-// tiles, plus some for each tile of its window, and block i takes the i-th even part of all units.
+// tiles, plus some for each tile of its window, and block i takes the i-th even part of
+// all units.
 // A part that covers several queries is worked through one after the other; a query
 // that several blocks share leaves each one's running max, row sum and unnormalised
 // output in the workspace, and k_dense_combine joins them.  The window is always a
@@ -33,7 +34,7 @@
 //
 // Roundings: scores and sums fp32; P in fp16 (2^-11 of each weight, the tensor
 // cores' operand type), as in the sparse attention; q exact in fp16 after a
-// power-of-two scale per head, the window rows after one per window.
+// power-of-two scale per head, the window rows after one per share.
 #include <algorithm>
 #include <type_traits>
 
