@@ -26,8 +26,8 @@
 //    clock of the 128 it gives.  x comes by bulk copies in the layout that
 //    k_linear_x has written to the workspace.  When there are few row tiles a
 //    cluster of blocks splits n_in and adds up through distributed shared memory.
-//    What bounds it is the tensor pipe with 128 tokens (600 clocks per 128 values of
-//    a row tile; the measured bf16 rate would take 590), and with fewer its pipeline's
+//    What bounds it is the tensor pipe with 128 tokens (busy 512 of the 600 clocks that
+//    128 values of a row tile take), and with fewer its pipeline's
 //    start (2.5 us to the first product: codes, expansion, x) and end (1.5 us).  64
 //    tokens, 1,536 -> 32,768: 14.6 us; 256 tokens, 4,096 -> 8,192: 19.3 us (890 TFLOP/s
 //    on 128 of the 152 SMs); both with k_linear_x, which overlaps its start.
