@@ -24,13 +24,14 @@
 //    weights go from registers to TMEM (the A operand), so shared memory carries
 //    the tokens alone: with both operands there, N = 128 would need 192 bytes per
 //    clock of the 128 it gives.  x comes by bulk copies in the layout that
-//    k_linear_x has written to the workspace.  When there are few row tiles a
-//    cluster of blocks splits n_in and adds up through distributed shared memory.
+//    k_linear_x has written to the workspace; fp16 tokens by tensor copies from where
+//    they are.  When there are few row tiles a cluster of blocks splits n_in and adds
+//    up through distributed shared memory.
 //    What bounds it is the tensor pipe with 128 tokens (busy 512 of the 600 clocks that
-//    128 values of a row tile take), and with fewer its pipeline's
-//    start (2.5 us to the first product: codes, expansion, x) and end (1.5 us).  64
-//    tokens, 1,536 -> 32,768: 14.6 us; 256 tokens, 4,096 -> 8,192: 19.3 us (890 TFLOP/s
-//    on 128 of the 152 SMs); both with k_linear_x, which overlaps its start.
+//    128 values of a row tile take), and with fewer its pipeline's start (2.5 us to the
+//    first product: codes, expansion, x) and end (1.5 us).  64 bf16 tokens, 1,536 ->
+//    32,768: 14.7 us with k_linear_x, which overlaps its start, and in fp16 13.7 without;
+//    256 fp16 tokens, 4,096 -> 8,192: 17.1 us (1,000 TFLOP/s on 128 of the 152 SMs).
 #include <algorithm>
 #include <type_traits>
 
@@ -435,6 +436,14 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* tm, int
         : "memory");
 }
 
+// a box of the tokens (64 values of p.nb tokens) at value x (a multiple of 64), token y and group z
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(mbar)
+        : "memory");
+}
+
 // the four scales of 64 weights of one row from k on; zeros from n_in on
 __device__ __forceinline__ uint32_t lin_scales4(const uint8_t* __restrict__ s, int k, int n_in, int wide) {
     if (k >= n_in) return 0u;
@@ -476,11 +485,12 @@ struct LinRings {
 // tile, so that blocks side by side read the same codes.  Without splits the blocks walk the tiles,
 // the results of one being stored while the next is summed; with splits a cluster takes one tile and
 // its blocks a share of the chunks each.  TMA: the codes come by tensor copies (n_in a multiple of 32:
-// rows a multiple of 16 bytes apart), else by plain loads.
-template <bool TMA>
+// rows a multiple of 16 bytes apart), else by plain loads.  DIRECT: fp16 tokens are read where they are, with
+// no k_linear_x before this kernel (a variant of its own: as a test at run time it cost the others 4 %).
+template <bool TMA, bool DIRECT>
 __global__ void __launch_bounds__(LM_THREADS, 1)
     k_linear_many(const __grid_constant__ CUtensorMap tmap, const LinArgs a, LinPrep p, const uint8_t* __restrict__ ws,
-                  int* __restrict__ err, LinRings rg) {
+                  int* __restrict__ err, LinRings rg, const __grid_constant__ CUtensorMap xmap) {
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) unsigned long long b_a[LM_S], b_x[LM_S], b_free[LM_S], b_c[LM_MAXC], b_cfree[LM_MAXC], b_d[2],
         b_dfree[2];
@@ -529,6 +539,9 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     }
     if (TMA && warp == LM_XW + 1 && lane == 0)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
+    if (DIRECT && warp == LM_XW && lane == 0)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&xmap)) : "memory");
+    if (DIRECT) pdl_wait();                      // else k_linear_x has waited: the weights may have just been quantised
     __syncthreads();
     // the copies start at once; whoever touches TMEM meets here after its allocation
     uint32_t tmem = 0;
@@ -545,14 +558,14 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     auto store = [&](int ti, int part, int parts) {
         const Tile v = tile_of(first + ti * step);
         const int q = warp & 3, buf = ti % bufs, m = v.m * LM_M + q * 32 + lane, t0 = v.t * NB, nt = min(NB, a.n_tok - t0);
-        const float* scale = reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)v.g * a.n_tok + t0;
+        const float* scale = DIRECT ? nullptr : reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)v.g * a.n_tok + t0;
         float* mine = reinterpret_cast<float*>(sm);
         const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + 2 * buf * NC;
         const int one = n == 1 ? ti & 1 : 0;                     // the issuer that has a tile's only chunk
         float f[16];
         auto scales = [&](int c) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = c + i < nt ? scale[c + i] * a.alpha : 0.0f;
+            for (int i = 0; i < 16; ++i) f[i] = DIRECT ? a.alpha : c + i < nt ? scale[c + i] * a.alpha : 0.0f;
         };
         if (splits == 1) scales(16 * part);                      // in flight while the sums are waited for
         if (n > 0) ok = ok && umma::mbar_wait_fast(sa(&b_d[buf]), (ti / bufs) & 1);
@@ -706,7 +719,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             if (lane == 0) umma::mbar_arrive(sa(&b_dfree[ti % bufs]));
         }
     } else if (warp == LM_XW) {
-        // ================= x: bulk copies of the prepared stages
+        // ================= x: bulk copies of the prepared stages, or the tokens themselves into the same layout
         if (lane == 0) {
             pdl_wait();
             uint32_t it = 0;
@@ -717,7 +730,12 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     if (it >= LM_S) ok = ok && umma::mbar_wait_fast(sa(&b_free[st]), (it / LM_S - 1) & 1);
                     if (!ok) break;
                     umma::mbar_arrive_expect_tx(sa(&b_x[st]), stage_bytes);
-                    umma::bulk_g2s(xb + st * stage_bytes, ws + p.stage(v.g, v.t, ch0 + j), stage_bytes, sa(&b_x[st]));
+                    if constexpr (DIRECT)
+                        for (int h = 0; h < 2; ++h)
+                            tma_box3(xb + st * stage_bytes + h * (uint32_t)p.half_bytes(), &xmap, (ch0 + j) * LM_K + h * 64, v.t * NB,
+                                     v.g, sa(&b_x[st]));
+                    else
+                        umma::bulk_g2s(xb + st * stage_bytes, ws + p.stage(v.g, v.t, ch0 + j), stage_bytes, sa(&b_x[st]));
                 }
             }
             lin_drain(ok, b_x, LM_S, it);
@@ -793,7 +811,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         const Tile v = tile_of(first);
         const int t0 = v.t * NB, nt = min(NB, a.n_tok - t0);
         const float* mine = reinterpret_cast<const float*>(sm);
-        const float* scale = reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)v.g * a.n_tok + t0;
+        const float* scale = DIRECT ? nullptr : reinterpret_cast<const float*>(ws + p.scales_at(a.n_groups)) + (int64_t)v.g * a.n_tok + t0;
         umma::cluster_sync();
         for (int u = tid; u < ((nt - split + splits - 1) / splits) * LM_M; u += LM_THREADS) {
             const int c = split + (u / LM_M) * splits, row = u % LM_M;
@@ -804,7 +822,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                 x += w;
             }
             const int m = v.m * LM_M + row;
-            if (m < a.n_out) lin_store(a, t0 + c, v.g, m, x * a.alpha * scale[c]);
+            if (m < a.n_out) lin_store(a, t0 + c, v.g, m, DIRECT ? x * a.alpha : x * a.alpha * scale[c]);
         }
         umma::cluster_sync();                    // no block leaves while another reads its sums
     }
@@ -908,7 +926,21 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     const LinPrep p = lin_prep(x_type, a.n_tok, a.n_in);
     uint8_t* ws = reinterpret_cast<uint8_t*>(wsp);
     cudaError_t e;
-    launch_k(k_linear_x<TX>, dim3(a.n_tok, a.n_groups), 256, 0, st, a, p, ws + LM_HEAD, x_vec);
+    const bool tma = a.n_in % 32 == 0 && a.n_in > 0 && (int64_t)a.n_groups * a.n_out <= 0x7fffffff && lin_encode() != nullptr;
+    // fp16 tokens need no scale: the product reads them itself where a tensor copy can (256 x 4,096 -> 8,192:
+    // 17.6 us, 18.9 with a copy first)
+    CUtensorMap xm = {};
+    bool direct = false;
+    if constexpr (std::is_same<TX, __half>::value)
+        if (tma && x_vec && a.x_tok > 0 && (a.n_groups == 1 || a.x_group > 0)) {
+            const cuuint64_t dims[3] = {(cuuint64_t)a.n_in, (cuuint64_t)a.n_tok, (cuuint64_t)a.n_groups};
+            const cuuint64_t strides[2] = {(cuuint64_t)a.x_tok * 2, (cuuint64_t)(a.n_groups == 1 ? a.x_tok : a.x_group) * 2};
+            const cuuint32_t box[3] = {64, (cuuint32_t)p.nb, 1}, estr[3] = {1, 1, 1};
+            direct = lin_encode()(&xm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(a.x), dims, strides, box, estr,
+                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        }
+    if (!direct) launch_k(k_linear_x<TX>, dim3(a.n_tok, a.n_groups), 256, 0, st, a, p, ws + LM_HEAD, x_vec);
     // Splits of n_in: while the row and token tiles leave SMs idle and a split keeps four chunks
     const int tiles_m = (a.n_out + LM_M - 1) / LM_M;
     const int64_t tiles = (int64_t)tiles_m * p.tiles * a.n_groups;
@@ -918,7 +950,6 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     while (splits < 8 && tiles * splits * 2 <= 152 && p.chunks >= splits * 2 * 4) splits *= 2, ++rg.log_splits;
     // code stages: what the token ring leaves (a tensor copy lands about 2 us after its issue)
     rg.c_stages = (int)std::min<int64_t>(LM_MAXC, (224 * 1024 - LM_S * p.stage_bytes()) / LM_CODES);
-    const bool tma = a.n_in % 32 == 0 && a.n_in > 0 && (int64_t)a.n_groups * a.n_out <= 0x7fffffff && lin_encode() != nullptr;
     CUtensorMap tm = {};
     if (tma) {
         const cuuint64_t dims[2] = {(cuuint64_t)(a.n_in / 2), (cuuint64_t)a.n_groups * (cuuint64_t)a.n_out};
@@ -929,7 +960,7 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    const auto kern = tma ? k_linear_many<true> : k_linear_many<false>;
+    const auto kern = !tma ? k_linear_many<false, false> : direct ? k_linear_many<true, true> : k_linear_many<true, false>;
     const size_t smem = std::max<size_t>((tma ? rg.c_stages * (size_t)LM_CODES : 0) + (size_t)LM_S * p.stage_bytes(),
                                          splits > 1 ? (size_t)p.nb * LM_M * 4 : 0) + 1024;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
@@ -946,8 +977,8 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
     attr[1].val.clusterDim.x = splits, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tm, a, p, (const uint8_t*)(ws + LM_HEAD), reinterpret_cast<int*>(ws), rg);
-    note_launch(2);
+    e = cudaLaunchKernelEx(&cfg, kern, tm, a, p, (const uint8_t*)(ws + LM_HEAD), reinterpret_cast<int*>(ws), rg, xm);
+    note_launch(direct ? 1 : 2);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 }  // namespace

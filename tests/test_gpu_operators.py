@@ -141,6 +141,19 @@ def test_linear_strided_and_unaligned_rows(csa, pad, xt, yt, T):
     check_linear(csa, T, 2, 272, 37, xt, yt, pad=pad, seed=pad)
 
 
+@pytest.mark.parametrize("pad", [0, 3, 8, 24])
+@pytest.mark.parametrize("T,G,K,M", [(24, 2, 288, 37), (80, 3, 96, 130), (130, 1, 1056, 70), (300, 2, 160, 129)])
+def test_linear_strided_fp16_tokens(csa, pad, T, G, K, M):
+    check_linear(csa, T, G, K, M, HF, F, pad=pad, seed=pad)
+
+
+@pytest.mark.parametrize("T", [5, 24, 80])
+@pytest.mark.parametrize("xt", [BF, HF, F])
+def test_linear_tokens_shared_by_the_groups(csa, T, xt):
+    x = randn((T, 1, 256), gen(T), xt).expand(T, 3, 256)
+    check_linear(csa, T, 3, 256, 50, xt, F, x=x)
+
+
 @pytest.mark.parametrize("T", [2, 20, 70])
 @pytest.mark.parametrize("xt", [BF, F])
 def test_linear_wide_range_of_tokens(csa, T, xt):
