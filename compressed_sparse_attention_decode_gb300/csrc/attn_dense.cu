@@ -22,7 +22,8 @@
 //                    issuers take dims 0-255 and 256-511 into two TMEM partials)
 //   online softmax, one head and 32 keys per thread; the running max is raised, and
 //   O rescaled in TMEM, only when a score rises more than 2^8 above it; row sums in fp32
-//   O^T += L^T . P  (M = 4 x 128 dims, N = 64 heads, K = 64 keys; two issuers)
+//   O^T += L^T . P  (M = 4 x 128 dims, N = the heads in steps of 16 (8 heads, 16 queries of 9K entries: 35.0 us, 36.0
+//                    with N = 64), K = 64 keys; two issuers)
 // What bounds a tile is shared memory: 64 KB written, 128 KB read by the score MMAs (64
 // of them the query again) and 96 KB by the value MMAs, 2,250 clocks at 128 bytes a
 // clock, against 3,200 measured (64 queries of 64 heads at 32K, 16,320 entries each: 206 us
@@ -468,7 +469,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
         } else if (warp == DA_MMA2 || warp == DA_MMA2 + 1) {
             // ================= values of tile t once P is written; completion frees the L and P buffers
             const int half = warp - DA_MMA2;
-            const uint32_t id = umma::idesc_f16(128, DA_H, 1, 0);
+            const int n16 = min(DA_H, (a.n_heads - S.h0 + 15) & ~15);        // heads that are there, in MMA steps
+            const uint32_t id = umma::idesc_f16(128, n16, 1, 0);
             const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
             for (int t = 0; t < T; ++t) {
                 const uint32_t tg = tb + t, lb = tg % DA_NL, sb = tg & 1;
