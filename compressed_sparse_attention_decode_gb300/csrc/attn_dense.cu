@@ -66,7 +66,7 @@ constexpr uint32_t DA_LBUF = 8 * DA_LSLAB;
 constexpr uint32_t DA_SP = DA_SL + DA_NL * DA_LBUF;  // P^T: 2 buffers x 64 heads x 64 keys
 constexpr uint32_t DA_PBUF = DA_H * 128;
 constexpr uint32_t DA_RED = DA_SP + 2 * DA_PBUF;     // [2 key halves][64 heads]
-constexpr uint32_t DA_MISC = DA_RED + 512;           // m_run[64], fac[64], qexp[64], flag[4], wmax
+constexpr uint32_t DA_MISC = DA_RED + 512;           // m_run[64], fac[64], qexp[64], flag[4], wmax[2]
 constexpr uint32_t DA_DYN = DA_MISC + 832 + 1024;    // + alignment
 constexpr uint32_t DAT_S = 0, DAT_O = 256, DAT_COLS = 512;   // S^T partial p of buffer b at DAT_S + 64 (2b + p)
 constexpr float DA_LAZY = 8.0f;                      // log2 headroom before the running max is raised

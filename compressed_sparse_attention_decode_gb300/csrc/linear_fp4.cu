@@ -12,14 +12,13 @@
 //
 // Two kernels:
 //  - k_linear_few (up to 16 tokens; 8 of fp32).  The weights' bytes are its floor; what
-//    it runs at is the latency of asking, expanding and joining: one token, 1,536 ->
-//    32,768 (28 MB) takes 8.9 us, 3.2 TB/s, and the SMs' instructions: 190 a warp
-//    for 16 rows of 128 values, after 2.5 us of starting and converting x.  mma.sync
-//    m16n8k16, the weights as the A fragments.  The order of k within a product is
-//    free as long as both operands agree, so a lane takes 16 consecutive bytes of a
-//    row (32 weights, two scale groups) and feeds them, four at a time, to eight
-//    products, and x comes from global memory in the matching order.  The weights
-//    come by bulk copies, all at once.
+//    takes its time are the SMs' instructions, 190 a warp for 16 rows of 128 values,
+//    after 2.5 us of starting and converting x: one token, 1,536 -> 32,768 (28 MB) takes
+//    8.7 us, 3.3 TB/s.  mma.sync m16n8k16, the weights as the A fragments.  The order of
+//    k within a product is free as long as both operands agree, so a lane takes 16
+//    consecutive bytes of a row (32 weights, two scale groups) and feeds them, four at a
+//    time, to eight products, and x comes from global memory in the matching order.  The
+//    weights come by bulk copies, all at once.
 //  - k_linear_many: tcgen05, M = 128 rows, N = up to 128 tokens.  Expanded
 //    weights go from registers to TMEM (the A operand), so shared memory carries
 //    the tokens alone: with both operands there, N = 128 would need 192 bytes per
@@ -31,7 +30,7 @@
 //    128 values of a row tile take), and with fewer its pipeline's start (2.5 us to the
 //    first product: codes, expansion, x) and end (1.5 us).  64 bf16 tokens, 1,536 ->
 //    32,768: 14.7 us with k_linear_x, which overlaps its start, and in fp16 13.7 without;
-//    256 fp16 tokens, 4,096 -> 8,192: 17.1 us (1,000 TFLOP/s on 128 of the 152 SMs).
+//    256 fp16 tokens, 4,096 -> 8,192: 16.6 us (1,040 TFLOP/s on 128 of the 152 SMs).
 #include <algorithm>
 #include <type_traits>
 
