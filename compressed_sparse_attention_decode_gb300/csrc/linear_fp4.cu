@@ -11,7 +11,8 @@
 // are exact, sums fp32; y is rounded once.
 //
 // Two kernels:
-//  - k_linear_few (up to 16 tokens; 8 of fp32).  The weights' bytes are its floor; what
+//  - k_linear_few (up to 8 tokens, 4 of fp32, and twice as many where the matrix is
+//    small).  The weights' bytes are its floor; what
 //    takes its time are the SMs' instructions, 190 a warp for 16 rows of 128 values,
 //    after 2.5 us of starting and converting x: one token, 1,536 -> 32,768 (28 MB) takes
 //    8.7 us, 3.3 TB/s.  mma.sync m16n8k16, the weights as the A fragments.  The order of
@@ -825,7 +826,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         }
         umma::cluster_sync();                    // no block leaves while another reads its sums
     }
-    if (!ok) atomicExch(err, 1);
+    if (!ok && err != nullptr) atomicExch(err, 1);
     umma::fence_before();
     __syncthreads();
     if (tid == 0) __threadfence();               // as in k_linear_few
@@ -861,10 +862,16 @@ int lin_wide(const LinArgs& a) {
 }
 int lin_planes(int x_type) { return x_type == CSA2_F32 ? 2 : 1; }
 
-// the few-token kernel: up to 16 tokens, 8 where x has two parts, of rows that fit a block's shared memory
+// whether the few-token kernel can take them: up to 16 tokens, 8 where x has two parts, of rows that fit a
+// block's shared memory
 bool lin_few(int x_type, int n_tok, int n_in) {
     return n_tok <= (x_type == CSA2_F32 ? LF_TOK / 2 : LF_TOK) && 9 * (int64_t)n_in + 32 <= LF_SMEM;
 }
+// In the upper half of that range it is the better one for small matrices only: below some 20 million weights
+// (16 bf16 tokens, few-token kernel and the other: 1,536 x 8,192 7.6 and 8.2 us, 4,096 x 8,192 13.3 and 11.6,
+// 1,536 x 32,768 16.1 and 13.3; 8 fp32 tokens, 1,536 x 1,024 5.0 and 7.7, 16 groups of 2,048 x 1,024 13.1 and 11.5)
+bool lin_between(int x_type, int n_tok) { return n_tok > (x_type == CSA2_F32 ? LF_TOK / 4 : LF_TOK / 2); }
+constexpr int64_t LIN_BIG = 20 << 20;
 LinPrep lin_prep(int x_type, int n_tok, int n_in) {
     LinPrep p;
     p.nb = n_tok <= 32 ? 32 : n_tok <= 64 || x_type == CSA2_F32 ? 64 : 128;
@@ -917,21 +924,16 @@ template <typename TX>
 cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st) {
     const int x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_tok * (int64_t)sizeof(TX) % 16 == 0 &&
                       a.x_group * (int64_t)sizeof(TX) % 16 == 0;
-    if (lin_few(x_type, a.n_tok, a.n_in)) {
-        if constexpr (sizeof(TX) == 2)
-            if (a.n_tok > 8) return lf_pick<TX, 2>(a, x_vec, st);
-        return lf_pick<TX, 1>(a, x_vec, st);
-    }
-    const LinPrep p = lin_prep(x_type, a.n_tok, a.n_in);
-    uint8_t* ws = reinterpret_cast<uint8_t*>(wsp);
-    cudaError_t e;
     const bool tma = a.n_in % 32 == 0 && a.n_in > 0 && (int64_t)a.n_groups * a.n_out <= 0x7fffffff && lin_encode() != nullptr;
     // fp16 tokens need no scale: the product reads them itself where a tensor copy can (256 x 4,096 -> 8,192:
-    // 17.6 us, 18.9 with a copy first)
+    // 16.6 us, 18.9 with a copy first)
+    const LinPrep p = lin_prep(x_type, a.n_tok, a.n_in);
     CUtensorMap xm = {};
     bool direct = false;
+    const bool few = lin_few(x_type, a.n_tok, a.n_in);
+    const bool big = lin_between(x_type, a.n_tok) && (int64_t)a.n_groups * a.n_out * a.n_in >= LIN_BIG;
     if constexpr (std::is_same<TX, __half>::value)
-        if (tma && x_vec && a.x_tok > 0 && (a.n_groups == 1 || a.x_group > 0)) {
+        if ((!few || big) && tma && x_vec && a.x_tok > 0 && (a.n_groups == 1 || a.x_group > 0)) {
             const cuuint64_t dims[3] = {(cuuint64_t)a.n_in, (cuuint64_t)a.n_tok, (cuuint64_t)a.n_groups};
             const cuuint64_t strides[2] = {(cuuint64_t)a.x_tok * 2, (cuuint64_t)(a.n_groups == 1 ? a.x_tok : a.x_group) * 2};
             const cuuint32_t box[3] = {64, (cuuint32_t)p.nb, 1}, estr[3] = {1, 1, 1};
@@ -939,6 +941,14 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
                                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
         }
+    // (fp16 tokens come without a workspace up to 16 of them)
+    if (few && !(big && (direct || !std::is_same<TX, __half>::value))) {
+        if constexpr (sizeof(TX) == 2)
+            if (a.n_tok > 8) return lf_pick<TX, 2>(a, x_vec, st);
+        return lf_pick<TX, 1>(a, x_vec, st);
+    }
+    uint8_t* ws = reinterpret_cast<uint8_t*>(wsp);
+    cudaError_t e;
     if (!direct) launch_k(k_linear_x<TX>, dim3(a.n_tok, a.n_groups), 256, 0, st, a, p, ws + LM_HEAD, x_vec);
     // Splits of n_in: while the row and token tiles leave SMs idle and a split keeps four chunks
     const int tiles_m = (a.n_out + LM_M - 1) / LM_M;
@@ -983,7 +993,7 @@ cudaError_t lin_launch(const LinArgs& a, int x_type, void* wsp, cudaStream_t st)
 }  // namespace
 
 size_t linear_fp4_ws(int x_type, int n_tok, int n_groups, int n_in) {
-    if (lin_few(x_type, n_tok, n_in)) return 0;
+    if (lin_few(x_type, n_tok, n_in) && !(lin_between(x_type, n_tok) && x_type != CSA2_F16)) return 0;
     const LinPrep p = lin_prep(x_type, n_tok, n_in);
     return LM_HEAD + (size_t)p.scales_at(n_groups) + (size_t)n_groups * n_tok * sizeof(float);
 }

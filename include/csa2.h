@@ -254,7 +254,8 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
  * of the value itself, whichever is more; a NaN scale byte, an infinite or a NaN x
  * gives what the formula gives.
  * workspace: csa2_workspace_size(CSA2_OP_LINEAR_FP4, n_tok, n_groups, x_type, 0,
- * n_in) bytes (0, and may be NULL, for few tokens), 16-byte aligned.
+ * n_in) bytes (0, and may be NULL, for up to 8 tokens of 2 bytes, 16 of fp16 and 4 of
+ * fp32 whose n_in is at most some 20,000), 16-byte aligned.
  */
 csa2_status csa2_linear_fp4(const void* x, int32_t x_type, int64_t x_tok, int64_t x_group, int32_t n_tok,
                             int32_t n_groups, int32_t n_in, int32_t n_out, const uint8_t* codes, const uint8_t* scales,

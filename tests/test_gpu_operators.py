@@ -147,6 +147,13 @@ def test_linear_strided_fp16_tokens(csa, pad, T, G, K, M):
     check_linear(csa, T, G, K, M, HF, F, pad=pad, seed=pad)
 
 
+@pytest.mark.parametrize("T", [5, 8, 9, 16])
+@pytest.mark.parametrize("xt,pad", [(BF, 0), (HF, 0), (HF, 3), (F, 0)])
+@pytest.mark.parametrize("G,K,M", [(1, 1536, 14001), (3, 1552, 5000)])
+def test_linear_some_tokens_of_a_large_matrix(csa, T, xt, pad, G, K, M):
+    check_linear(csa, T, G, K, M, xt, BF, pad=pad, seed=T)
+
+
 @pytest.mark.parametrize("T", [5, 24, 80])
 @pytest.mark.parametrize("xt", [BF, HF, F])
 def test_linear_tokens_shared_by_the_groups(csa, T, xt):
