@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
             umma::mbar_init(sa(&b_pfull[i]), DA_SMW);
             umma::mbar_init(sa(&b_odone[i]), 2);
         }
-        umma::mbar_init(sa(&b_next), 1);
+        umma::mbar_init(sa(&b_next), 1 + DA_LOADERS / 32);
         umma::fence_mbar_init();
         wmaxs[0] = wmaxs[1] = 0u;
     }
@@ -267,7 +267,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
     int q_item = -1;                                         // the item whose queries are staged
     uint32_t tb = 0;                                         // tiles done so far: the rings go on from share to share
 
-    // The loaders go from share to share by themselves, held by the buffers alone; the other warps meet.
+    // The loaders go from share to share by themselves, held by the buffers alone; the other warps meet.  Phase k of
+    // b_next says that the share after share k is known.  A loader warp arrives on it too, once it has seen phase
+    // k - 1: warps 0-11 could otherwise go through share k + 1's hand-over before a delayed loader has looked, and
+    // its wait, which knows a phase by its parity alone, would meet a barrier two phases on.
+    if (warp >= DA_LOADW && lane == 0) umma::mbar_arrive(sa(&b_next));
     for (uint32_t k = 0; shares[k & 1].rows >= 0; ++k) {
         const uint32_t cur = k & 1;
         const DenseShare& S = shares[cur];
@@ -622,6 +626,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
         tb += T;
         __syncwarp();                                        // the issuers' other lanes
         ok = umma::mbar_wait_fast(sa(&b_next), k & 1) && ok;
+        __syncwarp();
+        if (warp >= DA_LOADW && lane == 0) umma::mbar_arrive(sa(&b_next));
     }
     if (!ok) atomicExch(a.err, 1);
     umma::fence_before();
