@@ -99,18 +99,7 @@ __global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 
     const int sub = threadIdx.x & (lanes - 1);               // lane within the row
     const int slots = NR_THREADS / lanes, slot = threadIdx.x / lanes;
     float* buf = reinterpret_cast<float*>(cs + g.table) + slot * d_rot;
-    constexpr bool WREG = VEC > 1;                           // weights in registers (else read as they are used)
-    float w[WREG ? NCH : 1][VEC];
-    if (WREG) {
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int j = (sub + c * lanes) * VEC + e;
-                w[c][e] = R.w == nullptr ? 1.0f : FULL || j < d ? __ldg(R.w + j) : 0.0f;
-            }
-    }
-    pdl_wait();                              // x and the positions may come from the preceding kernel
+    pdl_wait();                              // x, the weights and the positions may come from the preceding kernel
 
     // Row i of the block is head h of its token t.  Slots past the last row repeat it and store nothing.
     const int last = nr - 1;
@@ -133,9 +122,20 @@ __global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 
         }
     };
     load(t, h);                              // in flight while the angles are computed
+    constexpr bool WREG = VEC > 1;                           // weights in registers (else read as they are used)
+    float w[WREG ? NCH : 1][VEC];
+    if (WREG) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int j = (sub + c * lanes) * VEC + e;
+                w[c][e] = R.w == nullptr ? 1.0f : FULL || j < d ? R.w[j] : 0.0f;
+            }
+    }
     for (int k = threadIdx.x; k < nt * half; k += NR_THREADS) {
         const int tt = k / half, c = k - tt * half;
-        const float f = __ldg(g.inv_freq + c);
+        const float f = g.inv_freq[c];
         const unsigned long long a = nr_turns(f) * (unsigned long long)g.pos[t0 + tt];
         float s, co;
         sincospif((float)(long long)a * 0x1p-63f, &s, &co);      // half turns in [-1, 1)
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(NR_THREADS, VEC * NCH > 16 ? 1 : VEC == 1 ? 2 
             const int j = (sub + c * lanes) * VEC;
             if (VEC == 1) {
                 a[c][0] *= r;
-                if (R.w != nullptr && j < d) a[c][0] *= __ldg(R.w + j);
+                if (R.w != nullptr && j < d) a[c][0] *= R.w[j];
             } else {
 #pragma unroll
                 for (int e = 0; e + 1 < VEC; e += 2) {

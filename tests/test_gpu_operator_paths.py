@@ -8,6 +8,48 @@ from test_gpu_operators import BF, HF, F, U, csa, decode, dense_case, fp4, gen, 
 pytestmark = pytest.mark.gpu
 
 
+# ---------------------------------------------------------------- norm and rotation
+
+@pytest.mark.parametrize("D,R,T", [(512, 64, 1), (512, 64, 300), (80, 40, 40), (36, 12, 40), (1024, 64, 9), (66, 10, 40)])
+@pytest.mark.parametrize("halves", [False, True])
+def test_norm_rope_takes_weights_just_written(csa, D, R, T, halves):
+    """weights, frequencies and positions that the kernel just before the call writes, other ones each time, for
+    the wide and the narrow accesses: as with a wait in between, eagerly and in a graph"""
+    g = gen(D)
+    n = 12
+    x, y = randn((T, 5, D), g, BF), torch.empty((n, T, 5, D), dtype=F, device="cuda")
+    k, z = randn((T, 1, D), g, BF), torch.empty((n, T, 1, D), dtype=F, device="cuda")
+    ws = [[randn((D,), g) for _ in range(n)] for _ in range(2)]
+    fs = [torch.rand((R // 2,), generator=g, device="cuda") for _ in range(n)]
+    ps = [torch.randint(0, 1 << 20, (T,), generator=g, device="cuda") for _ in range(n)]
+    qw, kw, f, p = (torch.empty_like(v[0]) for v in (ws[0], ws[1], fs, ps))
+
+    def steps(sync):
+        for i in range(n):
+            # the one just before the call changes from step to step
+            todo = [(f, fs), (p, ps), (kw, ws[1]), (qw, ws[0])]
+            for dst, src in todo[i % 4:] + todo[:i % 4]:
+                dst.copy_(src[i])
+            if sync:
+                torch.cuda.synchronize()
+            csa.csa2_norm_rope(x, p, f, qw, k, kw, halves=halves, q_out=y[i], k_out=z[i])
+
+    steps(True)
+    torch.cuda.synchronize()
+    want = y.clone(), z.clone()
+    for _ in range(10):
+        y.zero_(), z.zero_()
+        steps(False)
+        assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        steps(False)
+    for _ in range(10):
+        y.zero_(), z.zero_()
+        gr.replay()
+        assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+
+
 # ---------------------------------------------------------------- attention over every visible entry
 
 def test_dense_hands_many_short_shares_over(csa):
