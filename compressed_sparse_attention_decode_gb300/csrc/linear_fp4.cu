@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         float f[16];
         auto scales = [&](int c) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = DIRECT ? a.alpha : c + i < nt ? scale[c + i] * a.alpha : 0.0f;
+            for (int i = 0; i < 16; ++i) f[i] = DIRECT ? 1.0f : c + i < nt ? scale[c + i] : 0.0f;
         };
         if (splits == 1) scales(16 * part);                      // in flight while the sums are waited for
         if (n > 0) ok = ok && umma::mbar_wait_fast(sa(&b_d[buf]), (ti / bufs) & 1);
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                 continue;
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] *= f[i];
+            for (int i = 0; i < 16; ++i) r[i] = r[i] * f[i] * a.alpha;           // (2^E alpha itself may leave fp32's range)
             if (c + 16 * parts < nt) scales(c + 16 * parts);
             if (m < a.n_out) {
                 const int64_t y0 = (int64_t)(t0 + c) * a.y_tok + v.g * a.y_group + m;
@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                 x += w;
             }
             const int m = v.m * LM_M + row;
-            if (m < a.n_out) lin_store(a, t0 + c, v.g, m, DIRECT ? x * a.alpha : x * a.alpha * scale[c]);
+            if (m < a.n_out) lin_store(a, t0 + c, v.g, m, (DIRECT ? x : x * scale[c]) * a.alpha);
         }
         umma::cluster_sync();                    // no block leaves while another reads its sums
     }

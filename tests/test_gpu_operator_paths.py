@@ -1,11 +1,37 @@
 """Calls of the operators around the attention that reach their less trodden paths: many short shares a
 block and several passes of the dense attention, against the same 64-bit forms as test_gpu_operators."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_operators import BF, HF, F, U, csa, decode, dense_case, fp4, gen, randn, within  # noqa: F401
+from test_gpu_operators import BF, HF, F, U, check_linear, csa, decode, dense_case, fp4, gen, randn, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- FP4-weight products
+
+@pytest.mark.parametrize("T", [3, 20, 70])
+@pytest.mark.parametrize("xt", [BF, F])
+@pytest.mark.parametrize("K", [512, 4096])
+def test_linear_small_tokens_with_a_small_alpha(csa, T, xt, K):
+    """a token's power of two times alpha lies below fp32's normal range, the results do not"""
+    x = (randn((T, 1, K), gen(K)) * 2.0 ** -112).to(xt)
+    check_linear(csa, T, 1, K, 40, xt, F, x=x, alpha=1.37 * 2.0 ** -14)
+
+
+@pytest.mark.parametrize("T", [3, 20, 70])
+@pytest.mark.parametrize("K", [512, 4096])
+def test_linear_large_tokens_with_a_large_alpha(csa, T, K):
+    """... or above its range: rows without weights still give zeros, the others the infinity that they round to"""
+    g = gen(K)
+    codes, scales = fp4((40, K), g)
+    scales[::3] = 0
+    y = csa.csa2_linear_fp4(randn((T, K), g) * 2.0 ** 105, codes, scales, 2.0 ** 36)
+    assert not y[:, ::3].any()
+    y[:, ::3] = math.inf
+    assert bool(torch.isinf(y).all())
 
 
 # ---------------------------------------------------------------- norm and rotation
