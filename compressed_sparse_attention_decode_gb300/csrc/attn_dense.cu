@@ -13,15 +13,16 @@
 // tiles, plus some for each tile of its window, and block i takes the i-th even part of
 // all units.
 // A part that covers several queries is worked through one after the other; a query
-// that several blocks share leaves each one's running max, row sum and unnormalised
+// that several blocks share leaves each one's reference (below), row sum and unnormalised
 // output in the workspace, and k_dense_combine joins them.  The window is always a
 // share of its own, since its bf16 rows may need a scale of their own.
 //
 // One share, 64-key tiles, double-buffered (L, S, P):
 //   S^T = Q . L^T   (tcgen05 kind::f16, M = 64 heads, N = 64 keys, K = 512; two
 //                    issuers take dims 0-255 and 256-511 into two TMEM partials)
-//   online softmax, one head and 32 keys per thread; the running max is raised, and
-//   O rescaled in TMEM, only when a score rises more than 2^8 above it; row sums in fp32
+//   online softmax, one head and 32 keys per thread.  Weights are taken against a reference that
+//   is set 7 (in log2) below the running max, so that they use fp16's range; it is raised, and O
+//   rescaled in TMEM, only when a score rises more than 15 above it; row sums in fp32
 //   O^T += L^T . P  (M = 4 x 128 dims, N = the heads in steps of 16 (8 heads, 16 queries of 9K entries: 35.0 us, 36.0
 //                    with N = 64), K = 64 keys; two issuers)
 // What bounds a tile is shared memory: 64 KB written, 128 KB read by the score MMAs (64
@@ -33,8 +34,8 @@
 // FP4 rows and expand them to fp16 (exact: an E2M1 value times an E4M3 scale has at
 // most 6 significant bits and lies in [2^-10, 2688]).
 //
-// Roundings: scores and sums fp32; P in fp16 (2^-11 of each weight, the tensor
-// cores' operand type), as in the sparse attention; q exact in fp16 after a
+// Roundings: scores and sums fp32; P in fp16, the tensor cores' operand type (2^-11 of each
+// weight, or 2^-32 of the head's largest where that is more), as in the sparse attention; q exact in fp16 after a
 // power-of-two scale per head, the window rows after one per share.
 #include <algorithm>
 #include <type_traits>
@@ -69,7 +70,10 @@ constexpr uint32_t DA_RED = DA_SP + 2 * DA_PBUF;     // [2 key halves][64 heads]
 constexpr uint32_t DA_MISC = DA_RED + 512;           // m_run[64], fac[64], qexp[64], flag[4], wmax[2]
 constexpr uint32_t DA_DYN = DA_MISC + 832 + 1024;    // + alignment
 constexpr uint32_t DAT_S = 0, DAT_O = 256, DAT_COLS = 512;   // S^T partial p of buffer b at DAT_S + 64 (2b + p)
-constexpr float DA_LAZY = 8.0f;                      // log2 headroom before the running max is raised
+// A head's weights are 2^(score - m), m set DA_UP below the largest score and raised when one is more than DA_TOP
+// above it: the largest weight lies in [2^7, 2^15], within fp16's range, and what fp16 rounds to zero is below
+// 2^-32 of it.
+constexpr float DA_UP = 7.0f, DA_TOP = 15.0f;
 constexpr int DA_SMS = 152;                          // blocks at most: one per SM
 constexpr int DA_WIN = 4;                            // units of a window tile: 64 rows, their scale and the share's epilogue
 
@@ -93,7 +97,7 @@ struct DenseArgs {
     int n_items;                 // (query, head group) pairs of this pass
     DenseItem* items;            // [n_items]
     float* part_o;               // [share][64][512]
-    float2* part_ml;             // [share][64] running max (log2) and row sum
+    float2* part_ml;             // [share][64] reference (log2) of the weights and their sum
     int* err;
 };
 // Shares: block b's part of item i's tiles is number i + b (both only grow along the units, so no two
@@ -539,17 +543,18 @@ __global__ void __launch_bounds__(DA_THREADS, 1) k_dense_attn(const __grid_const
                 float mx = x[0];
 #pragma unroll
                 for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
-                if (umma::bar_red_or(1, DA_SMT, mx > mh + DA_LAZY)) {
+                if (umma::bar_red_or(1, DA_SMT, mx - mh > DA_TOP)) {
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     if (par == 0) red[half * DA_H + h] = mx;
                     umma::bar_named(1, DA_SMT);
                     if (half == 0) {
                         float f = 1.0f;
                         if (par == 0) {
-                            const float mt = fmaxf(red[h], red[DA_H + h]), mo = m_run[h];
-                            if (mt > -INFINITY && (mo == -INFINITY || mt > mo + DA_LAZY)) {
-                                f = mo == -INFINITY ? 0.0f : umma::ex2(mo - mt);
-                                m_run[h] = mt;
+                            const float mt = fmaxf(red[h], red[DA_H + h]), mo = m_run[h], mn = mt - DA_UP;
+                            // (differences, exact where they matter: a sum with m would round away from it)
+                            if (mt > -INFINITY && (mo == -INFINITY || mt - mo > DA_TOP)) {
+                                f = mo == -INFINITY ? 0.0f : umma::ex2(mo - mn);
+                                m_run[h] = mn;
                             }
                             fac[h] = f;
                         }

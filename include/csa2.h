@@ -309,9 +309,10 @@ csa2_status csa2_norm_rope(const csa2_head_rows* q, const csa2_head_rows* k, int
  *   swa      bf16 [batch][swa_len][d_lat], row r of sequence b = raw position
  *            swa_pos0[b] + r; the window of a query is clipped to the rows present
  *   swa_pos0 int64 [batch] (device) or NULL (zeros)
- *   out      [batch][n_q][n_heads][d_lat] of out_type (CSA2_BF16, _F16 or _F32;
- *            the weights pass the tensor cores in fp16, so an fp32 out is good
- *            to 2e-3 as csa2_sparse_attn's is)
+ *   out      [batch][n_q][n_heads][d_lat] of out_type (CSA2_BF16, _F16 or _F32).
+ *            The softmax weights pass the tensor cores in fp16: 2^-11 of each, or
+ *            2^-32 of the head's largest where that is more.  An fp32 out is good to
+ *            2e-3, as csa2_sparse_attn's is, for up to 2^22 entries
  *   lse      fp32 [batch][n_q][n_heads] or NULL
  * A query that sees nothing gets zeros and lse -inf.  Entries and rows that no
  * query sees are not read.  1 <= n_heads <= 128.  q, swa and out 16-byte

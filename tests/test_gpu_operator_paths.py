@@ -94,3 +94,24 @@ def test_dense_hands_many_short_shares_over(csa):
         again, _ = csa.csa2_dense_attn(cache, q, pos, swa, None, ws=ws)
         assert torch.equal(first, again)
     assert bool(torch.isfinite(first).all()) and csa.csa2_poll_error(ws) == csa.OK
+
+
+@pytest.mark.parametrize("n", [1 << 13, 1 << 17])
+def test_dense_long_even_tail_below_one_entry(csa, n):
+    """one entry 18 nats above n - 1 equal ones, which have dims of their own: 152 queries, so that a block takes a
+    whole one.  Each of the tail's weights is 2^-26 of the largest, its part of the output n times that."""
+    Q = 152
+    codes = torch.zeros((1, n, 256), dtype=torch.uint8, device="cuda")
+    codes[0, 0, :128], codes[0, 1:, 128:] = 0x22, 0x22                # ones in dims 0-255, in dims 256-511
+    scales = torch.full((1, n, 32), 0x38, dtype=torch.uint8, device="cuda")
+    q = torch.zeros((1, Q, 16, 512), device="cuda").to(BF)
+    q[..., :256] = 9.0 / 128
+    pos = torch.full((1, Q), n + 127, dtype=torch.int64, device="cuda")
+    out, lse = csa.csa2_dense_attn(csa.Cache.of(codes, scales, ratio=1), q, pos, None, None, 1.0, out_dtype=F, want_lse=True)
+    tail = (n - 1) * math.exp(-18.0)
+    want = torch.full((512,), 1.0 / (1.0 + tail), dtype=torch.float64, device="cuda")
+    want[256:] = tail / (1.0 + tail)
+    # scores exact (256 equal products), P half a step of fp16 or 2^-25 where the largest is 2^7 or more, fp32 sums
+    tol = want * (2.0 ** -11 + n * U + 2.0 ** -20) + n * 2.0 ** -32
+    within(out, want.expand(out.shape), tol.expand(out.shape))
+    assert float((lse.double() - 18.0 - math.log1p(tail)).abs().max()) <= tail * n * U + 2.0 ** -18
