@@ -40,7 +40,8 @@ class DecodeLayer(_Graphed):
     (the norms' weights); rot: how many of the last values are rotated, with frequencies
     base^(-2i/rot).  The caller fills x [B, r_q] and row [B, 512] (the token's latent row) and pos
     [B], keeps the earlier tokens' rows in win [B, 128, 512] (oldest first; the last is this
-    token's, written by the step), and runs enqueue() (or capture() once and run()).  With idx
+    token's, written by the step, so that the first is of position pos - 127), and runs enqueue()
+    (or capture() once and run()).  With idx
     int32 [B, 1, k] the attention reads those entries (the sequences then share one position, as
     csa2_sparse_attn's window does), else every visible one.  The result is y [B, groups, r_out]."""
 
@@ -60,7 +61,7 @@ class DecodeLayer(_Graphed):
         self.pos = torch.zeros((B,), dtype=torch.int64, device=dev)
         self.win = torch.zeros((B, 128, D_LAT), dtype=bf16, device=dev)
         self.swa_pos0 = swa_pos0                # with idx: the position of the window's first row, of every sequence
-        self.win_pos0 = torch.zeros((B,), dtype=torch.int64, device=dev)     # without: of each sequence's
+        self.win_pos0 = torch.zeros((B,), dtype=torch.int64, device=dev)     # without: of each sequence's, set by the step
         # intermediates and the result
         self.q = torch.empty((B, self.H, D_LAT), dtype=bf16, device=dev)
         self.o = torch.empty((B, 1, self.H, D_LAT), dtype=bf16 if idx is None else torch.float32, device=dev)
@@ -72,6 +73,9 @@ class DecodeLayer(_Graphed):
         self.ws_o = workspace(OP_LINEAR_FP4, B, self.groups, 0, 0, wo.shape[2], dev)
 
     def enqueue(self, stream=None):
+        if self.idx is None:
+            with torch.cuda.stream(stream):      # (None: the current one)
+                torch.sub(self.pos, self.win.shape[1] - 1, out=self.win_pos0)
         codes, scales, alpha = self.wq
         csa2_linear_fp4(self.x, codes, scales, alpha, out=self.q.view(self.B, -1), ws=self.ws_q, stream=stream)
         csa2_norm_rope(self.q, self.pos, self.inv_freq, q_weight=self.q_weight, k=self.row, k_weight=self.k_weight,
