@@ -26,6 +26,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TIMEOUT = 0, 
 FULL, REINDEX, REUSE = 0, 1, 2
 OP_INDEXER_TOPK, OP_REINDEX, OP_SPARSE_ATTN, OP_DENSE_ATTN, OP_LINEAR_FP4 = 1, 2, 3, 4, 5
 ROPE_HALVES, ROPE_INVERSE, ROPE_NO_NORM = 1, 2, 4
+WINDOW_AT_QUERY = -(1 << 63)
 D_LAT = 512
 
 
@@ -304,7 +305,8 @@ def csa2_reindex_noalloc(cache, k, iq_codes, iq_scales, w_head, pool, idx_out=No
 
 def csa2_sparse_attn(cache, q, q_pos, idx, swa, swa_pos0, scale=D_LAT ** -0.5, out=None, lse=None,
                      want_lse=False, ws=None, stream=None):
-    """q bf16 [B, n_q, H, 512]; idx int32 [B, n_q, k]; swa bf16 [B, swa_len, 512].
+    """q bf16 [B, n_q, H, 512]; idx int32 [B, n_q, k]; swa bf16 [B, swa_len, 512], row r at raw position
+    swa_pos0 + r, or with swa_pos0 = WINDOW_AT_QUERY the last row at each sequence's last query.
     Returns (out fp32 [B, n_q, H, 512], lse fp32 [B, n_q, H] or None)."""
     B, n_q, H = q.shape[0], q.shape[1], q.shape[2]
     k = idx.shape[-1] if idx is not None else 0

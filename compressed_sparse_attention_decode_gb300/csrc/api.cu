@@ -238,7 +238,8 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
     csa2_status s = check_cache(cache, false);
     if (s != CSA2_OK) return s;
     if (!q || !q_pos || !out || !aligned(q, 16) || !aligned(q_pos, 8) || !aligned(out, 16)) return CSA2_ERR_INVALID_ARG;
-    if (n_q < 1 || n_heads < 1 || n_heads > 128 || k < 0 || k > MAX_K || swa_len < 0 || swa_pos0 < 0)
+    if (n_q < 1 || n_heads < 1 || n_heads > 128 || k < 0 || k > MAX_K || swa_len < 0 ||
+        (swa_pos0 < 0 && swa_pos0 != CSA2_WINDOW_AT_QUERY))
         return CSA2_ERR_INVALID_ARG;
     if (k > 0 && (!idx || !aligned(idx, 4))) return CSA2_ERR_INVALID_ARG;
     if (swa_len > 0 && (!swa || !aligned(swa, 16))) return CSA2_ERR_INVALID_ARG;

@@ -123,6 +123,9 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// AT_QUERY: the window's position comes from the queries' (a variant of its own: as a test at run time it cost every
+// launch 0.07 us, 0.24 % of a 20-layer step)
+template <bool AT_QUERY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(AP_THREADS, 1) k_sparse_attn_pair(
     const uint8_t* __restrict__ lat_codes, const uint8_t* __restrict__ lat_scales, int capacity,
     const uint16_t* __restrict__ q, int n_q, int q0, const int64_t* __restrict__ q_pos,
@@ -150,6 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(AP_THREADS, 1) k_spa
     // window of this query (clipped to the rows present); this CTA's tiles:
     // FP4 tiles rank, rank+2, .. of the T4 tiles of k entries, then its half of the window
     const int64_t p = q_pos[gq];
+    if constexpr (AT_QUERY) swa_pos0 = window_origin(CSA2_WINDOW_AT_QUERY, swa_len, q_pos, b, n_q);
     int64_t wlo = p - (WINDOW - 1);
     if (wlo < 0) wlo = 0;
     if (wlo < swa_pos0) wlo = swa_pos0;
@@ -685,15 +689,16 @@ size_t attn_pair_ws(int, int) { return 256; }
 cudaError_t launch_sparse_attn_pair(const csa2_cache& c, const uint16_t* q, int n_q, const int64_t* q_pos,
                                     const int32_t* idx, int k, const uint16_t* swa, int64_t swa_pos0, int swa_len,
                                     float scale, float* out, float* lse, void* ws, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(k_sparse_attn_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AP_DYN);
+    const auto kern = swa_pos0 == CSA2_WINDOW_AT_QUERY ? k_sparse_attn_pair<true> : k_sparse_attn_pair<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AP_DYN);
     if (e != cudaSuccess) return e;
     int* err = reinterpret_cast<int*>(ws);
     const float scale_log2e = scale * 1.4426950408889634f;
     for (int q0 = 0; q0 < n_q; q0 += 65535) {
         const int nqc = (n_q - q0) < 65535 ? (n_q - q0) : 65535;
         dim3 grid(2, nqc, c.batch);
-        launch_k(k_sparse_attn_pair, grid, AP_THREADS, AP_DYN, st, c.lat_codes, c.lat_scales, c.capacity, q, n_q, q0, q_pos,
-                                                             idx, k, swa, swa_pos0, swa_len, scale_log2e, out, lse, err);
+        launch_k(kern, grid, AP_THREADS, AP_DYN, st, c.lat_codes, c.lat_scales, c.capacity, q, n_q, q0, q_pos, idx, k, swa,
+                 swa_pos0, swa_len, scale_log2e, out, lse, err);
         note_launch();
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(256) k_sparse_attn_simt(
         qs[i] = hh < H ? bf16_bits_to_f32(q[(gq * H + hh) * D_LAT + i % D_LAT]) : 0.0f;
     }
     const int64_t p = q_pos[gq];
+    swa_pos0 = window_origin(swa_pos0, swa_len, q_pos, b, n_q);
     int64_t wlo;
     int nwin;
     window_range(p, swa_pos0, swa_len, wlo, nwin);

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_sparse_attn_tc(
         const int r = tid & 127, half = tid >> 7;
         const int slot = tile * TC_TILE + r;
         const int64_t p = q_pos[gq];
+        swa_pos0 = window_origin(swa_pos0, swa_len, q_pos, b, n_q);
         int64_t wlo = p - (WINDOW - 1);
         if (wlo < 0) wlo = 0;
         if (wlo < swa_pos0) wlo = swa_pos0;

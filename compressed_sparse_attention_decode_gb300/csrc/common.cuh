@@ -54,6 +54,11 @@ constexpr int WINDOW = 128;
 constexpr int MAX_K = 2048;
 constexpr int MAX_IDX_HEADS = 32;
 
+// the raw position of a sequence's first window row
+__device__ __forceinline__ int64_t window_origin(int64_t swa_pos0, int swa_len, const int64_t* q_pos, int b, int n_q) {
+    return swa_pos0 == CSA2_WINDOW_AT_QUERY ? q_pos[(int64_t)b * n_q + n_q - 1] - swa_len + 1 : swa_pos0;
+}
+
 // ---------------------------------------------------------------- formats
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b16) { return __uint_as_float(b16 << 16); }

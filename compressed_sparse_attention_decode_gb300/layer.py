@@ -18,8 +18,8 @@ caller's are used, held in the cache's FP4 format.
 """
 import torch
 
-from . import (D_LAT, OP_DENSE_ATTN, OP_LINEAR_FP4, OP_SPARSE_ATTN, csa2_dense_attn, csa2_linear_fp4, csa2_norm_rope,
-               csa2_quantize_fp4, csa2_sparse_attn, workspace)
+from . import (D_LAT, OP_DENSE_ATTN, OP_LINEAR_FP4, OP_SPARSE_ATTN, WINDOW_AT_QUERY, csa2_dense_attn, csa2_linear_fp4,
+               csa2_norm_rope, csa2_quantize_fp4, csa2_sparse_attn, workspace)
 from .decode import _Graphed
 
 
@@ -41,11 +41,11 @@ class DecodeLayer(_Graphed):
     base^(-2i/rot).  The caller fills x [B, r_q] and row [B, 512] (the token's latent row) and pos
     [B], keeps the earlier tokens' rows in win [B, 128, 512] (oldest first; the last is this
     token's, written by the step, so that the first is of position pos - 127), and runs enqueue()
-    (or capture() once and run()).  With idx
-    int32 [B, 1, k] the attention reads those entries (the sequences then share one position, as
-    csa2_sparse_attn's window does), else every visible one.  The result is y [B, groups, r_out]."""
+    (or capture() once and run()).  With idx int32 [B, 1, k] the attention reads those entries,
+    else every visible one.  The window lies where pos puts it, at every step and in a graph too
+    (swa_pos0 is taken for callers that pass it and not used).  The result is y [B, groups, r_out]."""
 
-    def __init__(self, cache, wq, wo, q_weight, k_weight, rot=64, base=10000.0, eps=1e-6, idx=None, swa_pos0=0,
+    def __init__(self, cache, wq, wo, q_weight, k_weight, rot=64, base=10000.0, eps=1e-6, idx=None, swa_pos0=None,
                  out_dtype=torch.bfloat16):
         dev, B = cache.lat_codes.device, cache.batch
         bf16 = torch.bfloat16
@@ -60,8 +60,8 @@ class DecodeLayer(_Graphed):
         self.row = torch.zeros((B, 1, D_LAT), dtype=bf16, device=dev)
         self.pos = torch.zeros((B,), dtype=torch.int64, device=dev)
         self.win = torch.zeros((B, 128, D_LAT), dtype=bf16, device=dev)
-        self.swa_pos0 = swa_pos0                # with idx: the position of the window's first row, of every sequence
-        self.win_pos0 = torch.zeros((B,), dtype=torch.int64, device=dev)     # without: of each sequence's, set by the step
+        # without idx: the position of each window's first row, set by the step
+        self.win_pos0 = torch.zeros((B,), dtype=torch.int64, device=dev)
         # intermediates and the result
         self.q = torch.empty((B, self.H, D_LAT), dtype=bf16, device=dev)
         self.o = torch.empty((B, 1, self.H, D_LAT), dtype=bf16 if idx is None else torch.float32, device=dev)
@@ -84,7 +84,8 @@ class DecodeLayer(_Graphed):
         if self.idx is None:
             csa2_dense_attn(self.cache, q, q_pos, self.win, self.win_pos0, out=self.o, ws=self.ws, stream=stream)
         else:
-            csa2_sparse_attn(self.cache, q, q_pos, self.idx, self.win, self.swa_pos0, out=self.o, ws=self.ws, stream=stream)
+            csa2_sparse_attn(self.cache, q, q_pos, self.idx, self.win, WINDOW_AT_QUERY, out=self.o, ws=self.ws,
+                             stream=stream)
         csa2_norm_rope(self.o.view(self.B, self.H, D_LAT), self.pos, self.inv_freq, norm=False, inverse=True,
                        q_out=self.o16, stream=stream)
         codes, scales, alpha = self.wo

@@ -69,6 +69,9 @@ enum { CSA2_FULL = 0, CSA2_REINDEX = 1, CSA2_REUSE = 2 };
 enum { CSA2_OP_INDEXER_TOPK = 1, CSA2_OP_REINDEX = 2, CSA2_OP_SPARSE_ATTN = 3, CSA2_OP_DENSE_ATTN = 4,
        CSA2_OP_LINEAR_FP4 = 5 };
 
+/* csa2_sparse_attn's swa_pos0: the window rows end at each sequence's last query */
+#define CSA2_WINDOW_AT_QUERY INT64_MIN
+
 /* element types of the operators that take more than one */
 enum { CSA2_BF16 = 0, CSA2_F16 = 1, CSA2_F32 = 2 };
 
@@ -223,7 +226,10 @@ csa2_status csa2_reindex_f32(const csa2_cache* cache, const float* iq, const flo
  *   q_pos int64 [batch][n_q] raw positions (device)
  *   idx   int32 [batch][n_q][k]
  *   swa   bf16 [batch][swa_len][d_lat], row r = raw position swa_pos0 + r; the
- *         window of a query is clipped to the rows present
+ *         window of a query is clipped to the rows present.  swa_pos0 >= 0, the same
+ *         for every sequence, or CSA2_WINDOW_AT_QUERY: each sequence's rows end at its
+ *         last query's position, read on the device (swa_pos0 = q_pos[b][n_q-1] -
+ *         swa_len + 1, which may be negative), so that a graph follows its queries
  *   out   fp32 [batch][n_q][n_heads][d_lat]
  *   lse   fp32 [batch][n_q][n_heads] or NULL
  * 1 <= n_heads <= 128, k <= 2048.  q, swa and out 16-byte aligned, q_pos 8, idx

@@ -51,7 +51,7 @@ def positions(B, step):
     return torch.full((B,), p, device="cuda") if step % 2 == 0 else (p + 37 * torch.arange(B, device="cuda")) % 1150
 
 
-@pytest.mark.parametrize("with_indices", [False])
+@pytest.mark.parametrize("with_indices", [False, True])
 @pytest.mark.parametrize("captured", [False, True])
 def test_layer_follows_the_position(csa, with_indices, captured):
     layer, g = make(csa, 5, with_indices)
@@ -61,3 +61,24 @@ def test_layer_follows_the_position(csa, with_indices, captured):
     for step in range(12):
         advance(layer, positions(5, step), g)
         check(layer, layer.run)
+
+
+@pytest.mark.parametrize("H", [3, 32, 64, 128])          # CUDA cores, tiles with a join, the pair of blocks
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_sparse_window_at_the_query(csa, H, n_q):
+    """each sequence's window ends at its own last query: as one call a sequence with that position given"""
+    g = gen(H)
+    B = 6
+    codes, _ = fp4((B, 300, 512), g)
+    scales = torch.randint(0x28, 0x38, (B, 300, 32), generator=g, device="cuda", dtype=torch.uint8)
+    idx = torch.randint(-1, 300, (B, n_q, 64), generator=g, device="cuda", dtype=torch.int32)
+    q, swa = randn((B, n_q, H, 512), g, torch.bfloat16), randn((B, 130, 512), g, torch.bfloat16)
+    last = torch.tensor([2, 60, 127, 129, 131, 1 << 33], device="cuda")
+    pos = last[:, None] + torch.arange(1 - n_q, 1, device="cuda")
+    out, lse = csa.csa2_sparse_attn(csa.Cache.of(codes, scales), q, pos, idx, swa, csa.WINDOW_AT_QUERY, want_lse=True)
+    for b, p in enumerate(last.tolist()):
+        s = slice(b, b + 1)
+        first = max(0, p - 129)                          # rows of negative positions are not there
+        one, l1 = csa.csa2_sparse_attn(csa.Cache.of(codes[s], scales[s]), q[s], pos[s], idx[s],
+                                       swa[s, 129 - (p - first):].contiguous(), first, want_lse=True)
+        assert torch.equal(out[s], one) and torch.equal(lse[s], l1)
