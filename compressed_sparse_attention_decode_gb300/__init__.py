@@ -2,9 +2,9 @@
 
 Thin binding over the C ABI of ``libcsa2.so`` (declared in include/csa2.h):
 argument marshalling only, by ctypes and, for the operators whose calls are short
-(csa2_linear_fp4, csa2_norm_rope, csa2_dense_attn), by the C++ module ``_native``.  Every step runs in the library's CUDA kernels;
-PyTorch supplies device memory and the current stream.  There is no CPU
-fallback: if the library is not built, every call raises.
+(csa2_linear_fp4, csa2_norm_rope, csa2_dense_attn), by the C++ module ``_native``, which is loaded at
+the first of them.  Every step runs in the library's CUDA kernels; PyTorch supplies device memory and
+the current stream.  There is no CPU fallback: if the library is not built, every call raises.
 
 Entry points (same names as the C ABI):
     csa2_cache_write, csa2_quantize_fp4, csa2_indexer_topk, csa2_reindex, csa2_reindex_f32,
@@ -97,22 +97,23 @@ def load(path=None):
                  "csa2_sparse_attn", "csa2_linear_fp4", "csa2_norm_rope", "csa2_dense_attn"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
-        _load_native(lib)
         _lib = lib
     return lib
 
 
-def _load_native(lib):
-    """the C++ part of the binding, calling the functions of `lib`"""
+def _load_native():
+    """the C++ part of the binding, for the operators that go through it (nothing else needs it)"""
     global _native
+    lib = load()
     p = os.path.join(_HERE, "_native.so")
     if not os.path.exists(p):
         raise RuntimeError("_native.so is not built (%s); run __graft_entry__.build()" % p)
     spec = importlib.util.spec_from_file_location("_native", p, loader=importlib.machinery.ExtensionFileLoader("_native", p))
-    _native = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_native)
-    _native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                   (lib.csa2_linear_fp4, lib.csa2_norm_rope, lib.csa2_dense_attn, lib.csa2_workspace_size)))
+    native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(native)
+    native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                  (lib.csa2_linear_fp4, lib.csa2_norm_rope, lib.csa2_dense_attn, lib.csa2_workspace_size)))
+    _native = native
 
 
 def _status_string(s):
@@ -332,7 +333,7 @@ def csa2_linear_fp4(x, codes, scales, alpha=1.0, out=None, out_dtype=None, ws=No
     of out_dtype (default: that of x).  With a stream other than the current one, give `out` (a new one
     belongs to the current stream); without ws the scratch is taken for the call's own stream."""
     if _native is None:
-        load()
+        _load_native()
     r = _native.linear_fp4(x, codes, scales, alpha, out, out_dtype, ws, None if stream is None else stream.cuda_stream)
     if type(r) is int:
         raise Csa2Error(r, "csa2_linear_fp4")
@@ -347,7 +348,7 @@ def csa2_norm_rope(q, pos, inv_freq, q_weight=None, k=None, k_weight=None, eps=1
     may both be None (no rotation).  bf16 / fp16 / fp32, rows contiguous, other strides free; q_out may
     be q.  Returns (q_out, k_out or None)."""
     if _native is None:
-        load()
+        _load_native()
     r = _native.norm_rope(q, pos, inv_freq, q_weight, k, k_weight, eps, norm, halves, inverse, q_out, k_out, out_dtype,
                           None if stream is None else stream.cuda_stream)
     if type(r) is int:
@@ -364,7 +365,7 @@ def csa2_dense_attn(cache, q, q_pos, swa, swa_pos0, scale=D_LAT ** -0.5, out=Non
     belong to the current stream); without ws the scratch is taken for the call's own stream, and a
     bounded wait that gave up cannot be polled."""
     if _native is None:
-        load()
+        _load_native()
     r = _native.dense_attn(cache.lat_codes, cache.lat_scales, cache.ratio, q, q_pos, swa, swa_pos0, scale, out, out_dtype,
                            lse, want_lse, ws, None if stream is None else stream.cuda_stream)
     if type(r) is int:

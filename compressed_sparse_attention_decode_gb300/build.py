@@ -62,11 +62,11 @@ def build(verbose=False):
     with cf.ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         binding = ex.submit(_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + ".%d.tmp" % os.getpid()
         subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    binding.result()                             # its failure is told after the library is there
     return LIB
 
 
