@@ -32,15 +32,26 @@ def _compile(src, verbose):
     return obj
 
 
+def _read(path):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def _binding():
     """the C++ part of the binding: host code only, against PyTorch's and Python's own headers"""
     src = os.path.join(CSRC, "binding.cpp")
     deps = [src] + glob.glob(os.path.join(HERE, "..", "include", "*.h"))
-    if os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= max(os.path.getmtime(d) for d in deps):
-        return NATIVE
     import sysconfig
 
     import torch
+    made_for = "%s %s %s" % (sys.version, torch.__version__, torch.__file__)
+    stamp = os.path.join(BUILD, "native_made_for")
+    if (os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= max(os.path.getmtime(d) for d in deps)
+            and _read(stamp) == made_for):
+        return NATIVE
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
@@ -53,6 +64,8 @@ def _binding():
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
     os.replace(tmp, NATIVE)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return NATIVE
 
 

@@ -33,3 +33,24 @@ def test_library_is_built_where_the_native_module_fails(built, monkeypatch, tmp_
     with pytest.raises(RuntimeError, match="no compiler for it"):
         built.build()
     assert os.path.exists(built.LIB)
+
+
+def test_native_module_is_built_again_for_another_pytorch(built, monkeypatch, tmp_path):
+    """its build is kept while sources, Python and PyTorch stay what they were, and made again for others"""
+    calls = []
+
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+    def compiler(cmd, **kw):
+        calls.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return Done
+
+    monkeypatch.setattr(built, "NATIVE", str(tmp_path / "_native.so"))
+    monkeypatch.setattr(built, "BUILD", str(tmp_path))
+    monkeypatch.setattr(built.subprocess, "run", compiler)
+    for version, made in [("2.9.1", 1), ("2.9.1", 1), ("2.11.0", 2), ("2.11.0", 2), ("2.9.1", 3)]:
+        monkeypatch.setattr(torch, "__version__", version)
+        built._binding()
+        assert len(calls) == made
