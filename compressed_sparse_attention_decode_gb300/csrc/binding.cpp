@@ -8,6 +8,7 @@
 // library refuses or fails, its status as an int.
 #include <Python.h>
 
+#include <ATen/MemoryOverlap.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -44,6 +45,16 @@ void on_device(const T*... t) {
     const auto here = c10::cuda::current_device();
     const auto same = [&](const at::Tensor* v) { return v == nullptr || v->get_device() == here; };
     need((same(t) && ...), "tensors on the current device");
+}
+
+const at::Tensor* ws_or_none(PyObject* o) {
+    const at::Tensor* t = tensor_or_none(o, "ws: a tensor");
+    need(t == nullptr || t->is_contiguous(), "ws: contiguous");
+    return t;
+}
+// an output's rows lie apart (several blocks would write one row)
+void rows_apart(const at::Tensor& t) {
+    need(at::has_internal_overlap(t) != at::MemOverlap::Yes, "an output's rows: apart from each other");
 }
 
 int type_of(const at::Tensor& t, const char* what) {
@@ -89,7 +100,7 @@ struct Workspace {
     void* p = nullptr;
     size_t n = 0;
     bool own = false;
-    void given(const at::Tensor& t) { p = t.data_ptr(), n = (size_t)t.nbytes(); }
+    void given(const at::Tensor& t) { p = t.data_ptr(), n = (size_t)t.nbytes(); }     // (contiguous: all of it is there)
     void scratch(size_t bytes, cudaStream_t st) {
         if (bytes == 0) return;
         p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, st);
@@ -135,11 +146,13 @@ PyObject* linear(PyObject* const* a) {
     need((x.stride(nd - 1) == 1 || n_in == 0) && (n_out <= 1 || y.stride(nd - 1) == 1), "rows of x and out: contiguous");
     need(T <= INT32_MAX && G <= INT32_MAX && n_in <= INT32_MAX && n_out <= INT32_MAX, "sizes of 31 bits");
     const double alpha = number(a[3]);
-    on_device(&x, &codes, &scales, &y, tensor_or_none(a[6], "ws: a tensor"));
+    rows_apart(y);
+    const at::Tensor* given_ws = ws_or_none(a[6]);
+    on_device(&x, &codes, &scales, &y, given_ws);
     const cudaStream_t st = stream_of(a[7]);
     Workspace ws;
-    if (a[6] != Py_None)
-        ws.given(tensor(a[6], "ws: a tensor"));
+    if (given_ws != nullptr)
+        ws.given(*given_ws);
     else
         ws.scratch(f_ws(CSA2_OP_LINEAR_FP4, (int32_t)T, (int32_t)G, x_type, 0, n_in), st);
     const int status = f_linear(x.data_ptr(), x_type, x.stride(0), nd == 3 ? x.stride(1) : 0, (int32_t)T, (int32_t)G,
@@ -152,6 +165,7 @@ PyObject* linear(PyObject* const* a) {
 csa2_head_rows rows_of(const at::Tensor& x, const at::Tensor& y, const at::Tensor* w, int64_t T, int64_t d) {
     need(x.dim() == 3 && x.size(0) == T && x.size(2) == d && y.sizes() == x.sizes(), "a head set and its output: [T, heads, d]");
     need(x.stride(2) == 1 && y.stride(2) == 1, "rows of a head set and its output: contiguous");
+    rows_apart(y);
     need(x.size(1) <= INT32_MAX, "sizes of 31 bits");
     need(w == nullptr || (w->scalar_type() == at::kFloat && w->dim() == 1 && w->size(0) == d && w->is_contiguous()),
          "weights: contiguous fp32 [d]");
@@ -240,11 +254,12 @@ PyObject* dense(PyObject* const* a) {
     const double scale = number(a[7]);
     const csa2_cache cache{(uint8_t*)codes.data_ptr(), (uint8_t*)scales.data_ptr(), nullptr, nullptr, (int32_t)B, (int32_t)cap,
                            512, 128, (int32_t)whole(a[2])};
-    on_device(&codes, &scales, &q, &pos, swa, pos0, &o, lse, tensor_or_none(a[12], "ws: a tensor"));
+    const at::Tensor* given_ws = ws_or_none(a[12]);
+    on_device(&codes, &scales, &q, &pos, swa, pos0, &o, lse, given_ws);
     const cudaStream_t st = stream_of(a[13]);
     Workspace ws;
-    if (a[12] != Py_None)
-        ws.given(tensor(a[12], "ws: a tensor"));
+    if (given_ws != nullptr)
+        ws.given(*given_ws);
     else
         ws.scratch(f_ws(CSA2_OP_DENSE_ATTN, (int32_t)B, (int32_t)Q, (int32_t)H, 0, cap), st);
     const int status = f_dense(&cache, (const uint16_t*)q.data_ptr(), (int32_t)Q, (int32_t)H, (const int64_t*)pos.data_ptr(),

@@ -54,3 +54,29 @@ def test_native_module_is_built_again_for_another_pytorch(built, monkeypatch, tm
         monkeypatch.setattr(torch, "__version__", version)
         built._binding()
         assert len(calls) == made
+
+
+def test_binding_refuses_memory_that_is_not_there_or_shared(built):
+    import compressed_sparse_attention_decode_gb300 as csa
+    u8 = dict(dtype=torch.uint8)
+    x, c, s = torch.zeros(20, 64), torch.zeros(5, 32, **u8), torch.zeros(5, 4, **u8)
+    cache = csa.Cache.of(torch.zeros(2, 8, 256, **u8), torch.zeros(2, 8, 32, **u8))
+    q, p = torch.zeros(2, 1, 4, 512, dtype=torch.bfloat16), torch.zeros(2, 1, dtype=torch.int64)
+    one = torch.zeros(1, **u8)
+    for ws in (one.expand(1 << 24), torch.zeros(64, **u8)[::2]):
+        with pytest.raises(ValueError, match="ws: contiguous"):
+            csa.csa2_linear_fp4(x, c, s, ws=ws)
+        with pytest.raises(ValueError, match="ws: contiguous"):
+            csa.csa2_dense_attn(cache, q, p, None, None, ws=ws)
+    with pytest.raises(ValueError, match="apart"):
+        csa.csa2_linear_fp4(x, c, s, out=torch.zeros(1, 5).expand(20, 5))
+    with pytest.raises(ValueError, match="apart"):
+        csa.csa2_linear_fp4(torch.zeros(3, 2, 64), c.expand(2, 5, 32).contiguous(), s.expand(2, 5, 4).contiguous(),
+                            out=torch.zeros(3, 1, 5).expand(3, 2, 5))
+    h = torch.zeros(3, 4, 64)
+    for kw in (dict(q_out=torch.zeros(3, 1, 64).expand(3, 4, 64)), dict(k=h, k_out=torch.zeros(1, 4, 64).expand(3, 4, 64))):
+        with pytest.raises(ValueError, match="apart"):
+            csa.csa2_norm_rope(h, None, None, **kw)
+    # one row may have any stride
+    with pytest.raises(ValueError, match="GPU"):
+        csa.csa2_linear_fp4(x[:1], c, s, out=torch.zeros(1, 5).expand(1, 5))
