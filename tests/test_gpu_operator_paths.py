@@ -34,6 +34,35 @@ def test_linear_large_tokens_with_a_large_alpha(csa, T, K):
     assert bool(torch.isinf(y).all())
 
 
+@pytest.mark.parametrize("xt", [BF, HF, F])
+@pytest.mark.parametrize("T,G,K,M", [(2048, 1, 1536, 1000), (8192, 1, 272, 520), (2050, 3, 112, 129)])
+def test_linear_prompt_chunks(csa, T, G, K, M, xt):
+    check_linear(csa, T, G, K, M, xt, xt, seed=T)
+
+
+@pytest.mark.parametrize("xt,T", [(BF, 40), (HF, 40), (F, 40), (HF, 16)])
+def test_linear_many_tokens_take_weights_just_quantised(csa, xt, T):
+    """the quantiser and the product of many tokens back to back, new weights each time: as with a wait in between"""
+    g = gen(6)
+    x = randn((T, 1536), g, xt)
+    ws = [randn((15000, 1536), g) for _ in range(4)]
+    codes = torch.empty((15000, 768), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((15000, 96), dtype=torch.uint8, device="cuda")
+    want = []
+    for w in ws:
+        csa.csa2_quantize_fp4(w, codes, scales)
+        torch.cuda.synchronize()
+        want.append(csa.csa2_linear_fp4(x, codes, scales, out_dtype=F))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for w in ws:
+            csa.csa2_quantize_fp4(w, codes, scales)
+            got.append(csa.csa2_linear_fp4(x, codes, scales, out_dtype=F))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- norm and rotation
 
 @pytest.mark.parametrize("D,R,T", [(512, 64, 1), (512, 64, 300), (80, 40, 40), (36, 12, 40), (1024, 64, 9), (66, 10, 40)])
@@ -94,6 +123,16 @@ def test_dense_hands_many_short_shares_over(csa):
         again, _ = csa.csa2_dense_attn(cache, q, pos, swa, None, ws=ws)
         assert torch.equal(first, again)
     assert bool(torch.isfinite(first).all()) and csa.csa2_poll_error(ws) == csa.OK
+
+
+@pytest.mark.parametrize("B,Q,H", [(7, 100, 16),      # more (query, 64 heads) pairs than threads: two a thread
+                                   (1, 1024, 8), (1, 1025, 8),                 # one pass to the last pair, and one pair more
+                                   (3, 700, 16), (2, 390, 100)])               # passes that begin inside a sequence
+def test_dense_many_queries(csa, B, Q, H):
+    pos = torch.arange(Q)[None] // 3 + 61 * torch.arange(B)[:, None]
+    pos[0, :5] = -4                                                            # see nothing
+    pos[-1, Q // 2:] = torch.randint(0, 420, (Q - Q // 2,), generator=torch.Generator().manual_seed(Q))
+    dense_case(csa, B, Q, H, 280, pos, ratio=1, out_dtype=F, seed=Q, swa_len=440)
 
 
 @pytest.mark.parametrize("n", [1 << 13, 1 << 17])
