@@ -35,8 +35,9 @@
 // most 6 significant bits and lies in [2^-10, 2688]).
 //
 // Roundings: scores and sums fp32; P in fp16, the tensor cores' operand type (2^-11 of each
-// weight, or 2^-32 of the head's largest where that is more), as in the sparse attention; q exact in fp16 after a
-// power-of-two scale per head, the window rows after one per share.
+// weight, or 2^-32 of the head's largest where that is more); q and the window rows in fp16,
+// exact from 2^-17 up and to 2^-25 below, after a power-of-two scale per head or share where the
+// largest magnitude lies outside [2^-10, 2^15).
 #include <algorithm>
 #include <type_traits>
 

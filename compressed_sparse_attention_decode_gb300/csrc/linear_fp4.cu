@@ -12,10 +12,11 @@
 //
 // Two kernels:
 //  - k_linear_few (up to 8 tokens, 4 of fp32, and twice as many where the matrix is
-//    small).  The weights' bytes are its floor; what
-//    takes its time are the SMs' instructions, 190 a warp for 16 rows of 128 values,
-//    after 2.5 us of starting and converting x: one token, 1,536 -> 32,768 (28 MB) takes
-//    8.7 us, 3.3 TB/s.  mma.sync m16n8k16, the weights as the A fragments.  The order of
+//    small).  The weights' bytes are its floor: one token, 1,536 -> 32,768 (28 MB) takes
+//    8.7 us, 3.2 TB/s, for a floor of 4.2.  Neither memory (26 % busy) nor the SMs' issue
+//    slots (44 %) bound it: launch, set-up, the weights' first bytes (asked for only after
+//    the wait for the kernel before) and the conversion of x take 2.5 us one after the
+//    other, and a block's few tiles then overlap little.  mma.sync m16n8k16, the weights as the A fragments.  The order of
 //    k within a product is free as long as both operands agree, so a lane takes 16
 //    consecutive bytes of a row (32 weights, two scale groups) and feeds them, four at a
 //    time, to eight products, and x comes from global memory in the matching order.  The
@@ -30,7 +31,7 @@
 //    What bounds it is the tensor pipe with 128 tokens (busy 512 of the 600 clocks that
 //    128 values of a row tile take), and with fewer its pipeline's start (2.5 us to the
 //    first product: codes, expansion, x) and end (1.5 us).  64 bf16 tokens, 1,536 ->
-//    32,768: 14.7 us with k_linear_x, which overlaps its start, and in fp16 13.7 without;
+//    32,768: 14.5 us with k_linear_x, which overlaps its start, and in fp16 13.6 without;
 //    256 fp16 tokens, 4,096 -> 8,192: 16.6 us (1,040 TFLOP/s on 128 of the 152 SMs).
 #include <algorithm>
 #include <type_traits>
@@ -151,9 +152,9 @@ __device__ __forceinline__ void lf_copy(uint8_t* dst, const uint8_t* src, uint64
     if (lane < (int)rest) dst[whole + lane] = src[a + whole + lane];
 }
 
-// A block takes up to R tiles of 16 rows: `each`, the first `more` blocks one more.  Rows are contiguous, so a tile's codes and scales are one piece of
-// memory each: all of them are requested by bulk copies as the block starts, which keeps more bytes in
-// flight than registers could (one token, 1,536 x 32,768: every block's rows at once), and each tile has a
+// A block takes up to R tiles of 16 rows: `each`, the first `more` blocks one more.  Rows are contiguous, so a
+// tile's codes and scales are one piece of memory each: all of them are requested by bulk copies as the block
+// starts, which keeps more bytes in flight than registers could (one token, 1,536 x 32,768: every block's rows at once), and each tile has a
 // barrier of its own.  The warps split n_in in chunks of 128, warp w taking chunks w, w + warps, ..; per
 // chunk a warp holds the tokens' fragments in registers and runs all R tiles over them.  The warps' sums are
 // joined at the end, in order.
@@ -325,7 +326,8 @@ __global__ void __launch_bounds__(LF_MAXW * 32, 2) k_linear_few(const LinArgs a,
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int t = n * 8 + 2 * c + (i & 1);
-                if (t < T) red[(warp * T + t) * (R * 16) + tile * 16 + r + 8 * (i >> 1)] = ok ? acc[tile][n][i] : __int_as_float(0x7fc00000);
+                if (t < T)
+                    red[(warp * T + t) * (R * 16) + tile * 16 + r + 8 * (i >> 1)] = ok ? acc[tile][n][i] : __int_as_float(0x7fc00000);
             }
     __syncthreads();
     for (int u = tid; u < T * R * 16; u += blockDim.x) {
@@ -617,7 +619,8 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
     if (warp < LM_EXPAND) {
         // ================= weights: warp w takes rows 32(w%4) .. +31 of the tile, half (w/4)%2 of a chunk and
         // every second of the block's chunks, as the issuers do (not of a tile's: a stage then has the same warps
-        // each time, which have waited for its phase before, so that no wait can meet a barrier two phases back).  Only x and its scales come from the kernel before this one: nothing waits here.
+        // each time, which have waited for its phase before, so that no wait can meet a barrier two phases back).
+        // Only x and its scales come from the kernel before this one: nothing waits here.
         const int q = warp & 3, hf = (warp >> 2) & 1, par = warp >> 3, rt = q * 32 + lane;
         const uint8_t *cr = nullptr, *sr = nullptr;
         const int pairs = (n + 1) / 2;                           // of a tile's chunks; a code stage holds a pair

@@ -15,12 +15,12 @@
 // the cosines and sines of its tokens once: with 64 heads of 512 and 64 rotated
 // values that is 32 angles for 64 rows.  The next row's loads are issued before
 // this row's sum is complete.  Measured: 4,096 tokens of 64 + 1 rows of 512 in bf16, 90 us,
-// 6.0 TB/s (0.89 of a plain copy); a single token's 65 rows 2.8 us, which is the launch and one
+// 6.0 TB/s (0.90 of a plain copy); a single token's 65 rows 2.8 us, which is the launch and one
 // row's chain of loads.
 //
 // Angles.  p * f in turns, modulo one, as a 64-bit fraction: f / 2pi in units of
 // 2^-64 turns (a 24-bit mantissa times a 64-bit 1/2pi), times p modulo 2^64.  Exact
-// to about |p| 2^-64 turns, so positions past 2^24 lose nothing, and no 64-bit
+// to |p| (1 + |f| / 4) 2^-64 turns, so positions past 2^24 lose nothing, and no 64-bit
 // floating point is used (its rate is low on this GPU).
 #include <algorithm>
 

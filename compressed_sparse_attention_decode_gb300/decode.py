@@ -73,7 +73,7 @@ class DecodeStep(_Graphed):
         self.q = torch.zeros((L, B, n_q, H, 512), dtype=bf16, device=device)
         self.win = torch.zeros((L, B, swa_len, 512), dtype=bf16, device=device)
         self.q_pos = torch.zeros((B, n_q), dtype=torch.int64, device=device)
-        self.swa_pos0 = 0
+        self.swa_pos0 = 0        # WINDOW_AT_QUERY: the window follows q_pos, in a captured step too
         # chunked prefill: hidden states (and raw indexer keys) written in the step
         self.chunk_len = 0
         self.h_chunk = None

@@ -254,8 +254,8 @@ csa2_status csa2_sparse_attn(const csa2_cache* cache, const uint16_t* q, int32_t
  *   codes   uint8 [n_groups][n_out][n_in/2], 16-byte aligned
  *   scales  uint8 [n_groups][n_out][n_in/16], 16-byte aligned
  * x_type, y_type: CSA2_BF16, CSA2_F16 or CSA2_F32.  n_in a multiple of 16,
- * at most 2^24; * n_tok, n_in and n_out may be 0 (n_in 0 gives zeros), n_groups <= 65535; x and
- * y aligned to their elements; y overlaps no input.  fp16 x enters exactly, bf16
+ * at most 2^24; n_tok, n_in and n_out may be 0 (n_in 0 gives zeros), n_groups <=
+ * 65535; x and y aligned to their elements; y overlaps no input.  fp16 x enters exactly, bf16
  * x to 2^-39 of the largest value of its token and group, fp32 x to that or 2^-22
  * of the value itself, whichever is more; a NaN scale byte, an infinite or a NaN x
  * gives what the formula gives.
@@ -290,7 +290,7 @@ enum { CSA2_ROPE_HALVES = 1, CSA2_ROPE_INVERSE = 2, CSA2_ROPE_NO_NORM = 4 };
  *     pos[t] * inv_freq[i]:  a' = a cos - b sin,  b' = a sin + b cos
  *   q, k     the two row sets (the same types, sizes, positions); k may be NULL
  *   pos      int64 [n_tok] raw positions;  inv_freq fp32 [d_rot/2] (|f| < 2^24);
- *            angles are exact to 2^-24 turns at any position below 2^40
+ *            an angle is exact to |pos| (1 + |f| / 4) 2^-64 turns, then rounded to fp32
  *   flags    CSA2_ROPE_HALVES: pair i is (v[i], v[i + d_rot/2]) of the rotated
  *            part, else (v[2i], v[2i+1]); CSA2_ROPE_INVERSE: turn by the negative
  *            angle; CSA2_ROPE_NO_NORM: v = x (eps and the weights are not taken:
@@ -310,7 +310,7 @@ csa2_status csa2_norm_rope(const csa2_head_rows* q, const csa2_head_rows* k, int
  * no index list ("DeepSeek-v4.1 Flash" §1.1, §2.3.1): csa2_sparse_attn with J =
  * {0 .. n_elig(p)-1} U window, n_elig(p) clamped to the capacity.  For short
  * contexts, layers without an indexer, and as the measure of a selection.
- *   q        bf16 [batch][n_q][n_heads][d_lat], finite
+ *   q        bf16 [batch][n_q][n_heads][d_lat]; q and the window rows seen are finite
  *   q_pos    int64 [batch][n_q] raw positions (device)
  *   swa      bf16 [batch][swa_len][d_lat], row r of sequence b = raw position
  *            swa_pos0[b] + r; the window of a query is clipped to the rows present
