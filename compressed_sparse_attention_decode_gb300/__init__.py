@@ -2,14 +2,14 @@
 
 Thin binding over the C ABI of ``libcsa2.so`` (declared in include/csa2.h):
 argument marshalling only, by ctypes and, for the operators whose calls are short
-(csa2_linear_fp4, csa2_norm_rope, csa2_dense_attn), by the C++ module ``_native``, which is loaded at
-the first of them.  Every step runs in the library's CUDA kernels; PyTorch supplies device memory and
+(csa2_linear_fp4, csa2_norm_rope, csa2_dense_attn, csa2_tree_attn, csa2_cache_append, csa2_cache_read),
+by the C++ module ``_native``, which is loaded at the first of them.  Every step runs in the library's CUDA kernels; PyTorch supplies device memory and
 the current stream.  There is no CPU fallback: if the library is not built, every call raises.
 
 Entry points (same names as the C ABI):
     csa2_cache_write, csa2_quantize_fp4, csa2_indexer_topk, csa2_reindex, csa2_reindex_f32,
-    csa2_sparse_attn, csa2_dense_attn, csa2_linear_fp4, csa2_norm_rope, csa2_workspace_size,
-    csa2_poll_error, csa2_selftest_wait_timeout
+    csa2_sparse_attn, csa2_dense_attn, csa2_tree_attn, csa2_linear_fp4, csa2_norm_rope, csa2_cache_append,
+    csa2_cache_read, csa2_workspace_size, csa2_poll_error, csa2_selftest_wait_timeout
 plus ``Cache``, which owns the four cache planes as torch tensors.
 """
 import ctypes
@@ -24,9 +24,11 @@ LIB_PATH = os.path.join(_HERE, "libcsa2.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TIMEOUT = 0, 1, 2, 3, 4, 5
 FULL, REINDEX, REUSE = 0, 1, 2
-OP_INDEXER_TOPK, OP_REINDEX, OP_SPARSE_ATTN, OP_DENSE_ATTN, OP_LINEAR_FP4 = 1, 2, 3, 4, 5
+OP_INDEXER_TOPK, OP_REINDEX, OP_SPARSE_ATTN, OP_DENSE_ATTN, OP_LINEAR_FP4, OP_TREE_ATTN = 1, 2, 3, 4, 5, 6
 ROPE_HALVES, ROPE_INVERSE, ROPE_NO_NORM = 1, 2, 4
 WINDOW_AT_QUERY = -(1 << 63)
+EVERY_ENTRY = -1
+LATENTS, INDEXER_KEYS = 0, 1
 D_LAT = 512
 
 
@@ -54,7 +56,8 @@ _lib = None
 EXPORTS = ("csa2_cache_write", "csa2_quantize_fp4", "csa2_indexer_topk", "csa2_reindex", "csa2_sparse_attn",
            "csa2_workspace_size", "csa2_status_string", "csa2_abi_version", "csa2_launch_count",
            "csa2_reindex_noalloc", "csa2_reindex_f32", "csa2_poll_error", "csa2_selftest_wait_timeout",
-           "csa2_cache_write_projected", "csa2_linear_fp4", "csa2_norm_rope", "csa2_dense_attn")
+           "csa2_cache_write_projected", "csa2_linear_fp4", "csa2_norm_rope", "csa2_dense_attn",
+           "csa2_tree_attn", "csa2_cache_append", "csa2_cache_read")
 
 
 def load(path=None):
@@ -81,6 +84,9 @@ def load(path=None):
     hp = ctypes.POINTER(_HeadRows)
     lib.csa2_norm_rope.argtypes = [hp, hp, i32, i32, i32, i32, i32, vp, vp, ctypes.c_float, i32, vp]
     lib.csa2_dense_attn.argtypes = [cp, vp, i32, i32, vp, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, sz, vp]
+    lib.csa2_tree_attn.argtypes = [cp, vp, i32, i32, vp, vp, vp, vp, i32, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp, sz, vp]
+    lib.csa2_cache_append.argtypes = [cp, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.csa2_cache_read.argtypes = [cp, i32, vp, i64, i64, vp, i32, vp]
     lib.csa2_reindex_noalloc.argtypes = [cp, vp, vp, vp, i32, i32, vp, i32, i32, vp, vp]
     lib.csa2_reindex_noalloc.restype = ctypes.c_int
     lib.csa2_poll_error.argtypes = [vp, sz, vp]
@@ -94,7 +100,8 @@ def load(path=None):
     lib.csa2_abi_version.restype = i32
     lib.csa2_launch_count.restype = i64
     for name in ("csa2_cache_write", "csa2_quantize_fp4", "csa2_indexer_topk", "csa2_reindex", "csa2_reindex_f32",
-                 "csa2_sparse_attn", "csa2_linear_fp4", "csa2_norm_rope", "csa2_dense_attn"):
+                 "csa2_sparse_attn", "csa2_linear_fp4", "csa2_norm_rope", "csa2_dense_attn", "csa2_tree_attn",
+                 "csa2_cache_append", "csa2_cache_read"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -112,7 +119,8 @@ def _load_native():
     native = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(native)
     native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                  (lib.csa2_linear_fp4, lib.csa2_norm_rope, lib.csa2_dense_attn, lib.csa2_workspace_size)))
+                  (lib.csa2_linear_fp4, lib.csa2_norm_rope, lib.csa2_dense_attn, lib.csa2_tree_attn, lib.csa2_cache_append,
+                   lib.csa2_cache_read, lib.csa2_workspace_size)))
     _native = native
 
 
@@ -370,4 +378,50 @@ def csa2_dense_attn(cache, q, q_pos, swa, swa_pos0, scale=D_LAT ** -0.5, out=Non
                            lse, want_lse, ws, None if stream is None else stream.cuda_stream)
     if type(r) is int:
         raise Csa2Error(r, "csa2_dense_attn")
+    return r
+
+
+def csa2_tree_attn(cache, q, q_pos, parent, draft, swa, swa_pos0, idx=None, scale=D_LAT ** -0.5, out=None,
+                   out_dtype=torch.bfloat16, lse=None, want_lse=False, ws=None, stream=None):
+    """Attention of drafted trees: q bf16 [B, n, H, 512] and draft bf16 [B, n, 512] of up to 128 nodes a
+    sequence, q_pos int64 [B, n] their raw positions, parent int32 [B, n] (an earlier node, -1: a child of
+    the last committed token, anything else: not there).  A node sees every visible entry, or with idx int32
+    [B, n, k] those of its list; the committed rows of its window (swa and swa_pos0 as in csa2_dense_attn); its
+    ancestors' and its own draft rows.  Returns (out [B, n, H, 512], lse fp32 [B, n, H] or None), zeros
+    and -inf for nodes that are not there.  Streams, out, lse and ws as in csa2_dense_attn; a workspace is
+    workspace(OP_TREE_ATTN, B, n, H, k, capacity), with k EVERY_ENTRY where there is no idx."""
+    if _native is None:
+        _load_native()
+    r = _native.tree_attn(cache.lat_codes, cache.lat_scales, cache.ratio, q, q_pos, parent, draft, swa, swa_pos0, idx, scale,
+                          out, out_dtype, lse, want_lse, ws, None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        raise Csa2Error(r, "csa2_tree_attn")
+    return r
+
+
+def csa2_cache_append(cache, rows, pos0, path=None, prev=None, prev_out=None, w0=None, w1=None, wik_codes=None,
+                      wik_scales=None, stream=None):
+    """Rows into the cache, each sequence at its own position pos0 int64 [B]: rows bf16 [B, n, 512] in their
+    order, or those that path int32 [B, m] names (up to its first number that is no row).  A ratio-2 cache
+    takes prev bf16 [B, 512], the row of position pos0 - 1, leaves the last one in prev_out (may be prev; None:
+    not wanted) and takes w0, w1 as csa2_cache_write does.  With wik_codes and wik_scales the indexer keys are
+    projected from the entries."""
+    if _native is None:
+        _load_native()
+    r = _native.cache_append(cache.lat_codes, cache.lat_scales, cache.ikey_codes, cache.ikey_scales, cache.ratio, rows, pos0, path,
+                             prev, prev_out, w0, w1, wik_codes, wik_scales, None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        raise Csa2Error(r, "csa2_cache_append")
+
+
+def csa2_cache_read(cache, idx=None, first=0, count=None, keys=False, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Entries as values, bf16, fp16 or fp32: those that idx int32 [B, ..] names (zeros for -1 and for numbers
+    outside the cache), or count of them from `first` on (default: all).  Latents [.., 512], or with
+    keys=True indexer keys [.., d_idx].  With a stream other than the current one, give out."""
+    if _native is None:
+        _load_native()
+    r = _native.cache_read(cache.lat_codes, cache.lat_scales, cache.ikey_codes, cache.ikey_scales, cache.ratio, idx, first, count,
+                           keys, out, out_dtype, None if stream is None else stream.cuda_stream)
+    if type(r) is int:
+        raise Csa2Error(r, "csa2_cache_read")
     return r

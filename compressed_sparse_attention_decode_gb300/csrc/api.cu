@@ -37,6 +37,16 @@ cudaError_t launch_dense_attn(const csa2_cache& c, const uint16_t* q, int n_q, i
                               const uint16_t* swa, const int64_t* swa_pos0, int swa_len, float scale, void* out,
                               int out_type, float* lse, void* ws, cudaStream_t st);
 size_t dense_attn_ws(int batch, int n_q, int n_heads, int64_t capacity);
+cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
+                             const int32_t* parent, const uint16_t* draft, const int32_t* idx, int k, const uint16_t* swa,
+                             const int64_t* swa_pos0, int swa_len, float scale, void* out, int out_type, float* lse, void* ws,
+                             cudaStream_t st);
+size_t tree_attn_ws(int batch, int n_q, int n_heads, int k, int64_t capacity);
+cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n_rows, const int32_t* path, int n_path,
+                                const int64_t* pos0, const uint16_t* prev, uint16_t* prev_out, const float* w0,
+                                const float* w1, const uint8_t* wik_codes, const uint8_t* wik_scales, cudaStream_t st);
+cudaError_t launch_cache_read(const csa2_cache& c, bool keys, const int32_t* idx, int64_t first, int64_t n, void* out,
+                              int out_type, cudaStream_t st);
 cudaError_t launch_selftest_wait(uint32_t max_polls, int* err, cudaStream_t st);
 }  // namespace csa2
 
@@ -106,6 +116,11 @@ size_t csa2_workspace_size(int32_t op, int32_t batch, int32_t n_q, int32_t n_hea
         case CSA2_OP_DENSE_ATTN: return n_heads < 1 ? 0 : dense_attn_ws(batch, n_q, n_heads, capacity);
         case CSA2_OP_LINEAR_FP4:
             return n_heads < 0 || n_heads > CSA2_F32 || capacity > (1 << 24) ? 0 : linear_fp4_ws(n_heads, batch, n_q, (int)capacity);
+        case CSA2_OP_TREE_ATTN:
+            return n_q > TREE_NODES || n_heads < 1 || n_heads > 128 || k < CSA2_EVERY_ENTRY || k > MAX_K || capacity < 1 ||
+                           capacity > INT32_MAX
+                       ? 0
+                       : tree_attn_ws(batch, n_q, n_heads, k, capacity);
     }
     return 0;
 }
@@ -310,6 +325,53 @@ csa2_status csa2_dense_attn(const csa2_cache* cache, const uint16_t* q, int32_t 
     if (!workspace || ws_bytes < need || !aligned(workspace, 16)) return CSA2_ERR_WORKSPACE;
     return from_cuda(launch_dense_attn(*cache, q, n_q, n_heads, q_pos, swa, swa_pos0, swa_len, scale, out, out_type, lse,
                                        workspace, (cudaStream_t)stream));
+}
+
+csa2_status csa2_tree_attn(const csa2_cache* cache, const uint16_t* q, int32_t n_q, int32_t n_heads,
+                           const int64_t* q_pos, const int32_t* parent, const uint16_t* draft, const int32_t* idx,
+                           int32_t k, const uint16_t* swa, const int64_t* swa_pos0, int32_t swa_len, float scale,
+                           void* out, int32_t out_type, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    csa2_status s = check_cache(cache, false);
+    if (s != CSA2_OK) return s;
+    if (n_q < 1 || n_q > TREE_NODES || n_heads < 1 || n_heads > 128 || k < CSA2_EVERY_ENTRY || k > MAX_K || swa_len < 0 ||
+        cache->batch > 65535 || !known_type(out_type) || !std::isfinite(scale))
+        return CSA2_ERR_INVALID_ARG;
+    if (!q || !q_pos || !parent || !draft || !out || (k > 0 && !idx) || (swa_len > 0 && !swa)) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(draft, 16) || !aligned(out, 16) || !aligned(q_pos, 8) || !aligned(parent, 4) ||
+        !aligned(idx, 4) || (swa_len > 0 && !aligned(swa, 16)) || !aligned(swa_pos0, 8) || !aligned(lse, 4))
+        return CSA2_ERR_INVALID_ARG;
+    const size_t need = tree_attn_ws(cache->batch, n_q, n_heads, k, cache->capacity);
+    if (!workspace || ws_bytes < need || !aligned(workspace, 16)) return CSA2_ERR_WORKSPACE;
+    return from_cuda(launch_tree_attn(*cache, q, n_q, n_heads, q_pos, parent, draft, idx, k, swa, swa_pos0, swa_len, scale, out,
+                                      out_type, lse, workspace, (cudaStream_t)stream));
+}
+
+csa2_status csa2_cache_append(const csa2_cache* cache, const uint16_t* rows, int32_t n_rows, const int32_t* path,
+                              int32_t n_path, const int64_t* pos0, const uint16_t* prev, uint16_t* prev_out,
+                              const float* w0, const float* w1, const uint8_t* wik_codes, const uint8_t* wik_scales,
+                              void* stream) {
+    csa2_status s = check_cache(cache, wik_codes != nullptr);
+    if (s != CSA2_OK) return s;
+    if (n_rows < 0 || n_path < 0 || (!path && n_path > n_rows) || cache->batch > 65535) return CSA2_ERR_INVALID_ARG;
+    if ((n_rows > 0 && !rows) || !pos0 || !aligned(rows, 16) || !aligned(path, 4) || !aligned(pos0, 8)) return CSA2_ERR_INVALID_ARG;
+    if (!wik_codes != !wik_scales || !aligned(wik_codes, 16) || !aligned(wik_scales, 4)) return CSA2_ERR_INVALID_ARG;
+    if (cache->ratio == 2 && (!prev || !w0 || !w1 || !aligned(prev, 16) || !aligned(prev_out, 16) || !aligned(w0, 16) ||
+                              !aligned(w1, 16)))
+        return CSA2_ERR_INVALID_ARG;
+    return from_cuda(launch_cache_append(*cache, rows, n_rows, path, n_path, pos0, prev, prev_out, w0, w1, wik_codes, wik_scales,
+                                         (cudaStream_t)stream));
+}
+
+csa2_status csa2_cache_read(const csa2_cache* cache, int32_t what, const int32_t* idx, int64_t first, int64_t n,
+                            void* out, int32_t out_type, void* stream) {
+    if (what != CSA2_LATENTS && what != CSA2_INDEXER_KEYS) return CSA2_ERR_INVALID_ARG;
+    csa2_status s = check_cache(cache, what == CSA2_INDEXER_KEYS);
+    if (s != CSA2_OK) return s;
+    if (!known_type(out_type) || n < 0 || n > (INT64_MAX >> 12) / cache->batch || !aligned(idx, 4)) return CSA2_ERR_INVALID_ARG;
+    if (!idx && (first < 0 || first > cache->capacity || n > cache->capacity - first)) return CSA2_ERR_INVALID_ARG;
+    if (n == 0) return CSA2_OK;
+    if (!out || !aligned(out, 16)) return CSA2_ERR_INVALID_ARG;
+    return from_cuda(launch_cache_read(*cache, what == CSA2_INDEXER_KEYS, idx, first, n, out, out_type, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -9,6 +9,7 @@
 // group, so the merge, the group max, the scale and the 8 code bytes stay in
 // registers.  A warp reads 2 KB of bf16 hidden states and writes 256 + 32
 // bytes, all coalesced.
+#include "cache_entry.cuh"
 #include "common.cuh"
 
 namespace csa2 {
@@ -20,33 +21,11 @@ __device__ __forceinline__ void entry_latent(const uint16_t* __restrict__ h, int
                                              const float* __restrict__ w0, const float* __restrict__ w1, int lane,
                                              float* x) {
     const uint16_t* h0 = h + ((int64_t)b * n_ent * ratio + (int64_t)ratio * i) * D_LAT + lane * 16;
-    uint4 a0 = __ldg(reinterpret_cast<const uint4*>(h0));
-    uint4 a1 = __ldg(reinterpret_cast<const uint4*>(h0) + 1);
-    const uint32_t hw0[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-    if (ratio == 1) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) x[c] = bf16_bits_to_f32((c & 1) ? (hw0[c >> 1] >> 16) : (hw0[c >> 1] & 0xffffu));
-        return;
-    }
-    const uint16_t* h1 = h0 + D_LAT;
-    uint4 c0 = __ldg(reinterpret_cast<const uint4*>(h1));
-    uint4 c1 = __ldg(reinterpret_cast<const uint4*>(h1) + 1);
-    const uint32_t hw1[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        float4 p = __ldg(reinterpret_cast<const float4*>(w0 + lane * 16) + v);
-        float4 q = __ldg(reinterpret_cast<const float4*>(w1 + lane * 16) + v);
-        const float pw[4] = {p.x, p.y, p.z, p.w};
-        const float qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            int c = v * 4 + t;
-            uint32_t b0 = (c & 1) ? (hw0[c >> 1] >> 16) : (hw0[c >> 1] & 0xffffu);
-            uint32_t b1 = (c & 1) ? (hw1[c >> 1] >> 16) : (hw1[c >> 1] & 0xffffu);
-            // e = fmaf(w1, h1, float(w0 * h0)): one rounded product, one fused multiply-add
-            x[c] = __fmaf_rn(qw[t], bf16_bits_to_f32(b1), __fmul_rn(pw[t], bf16_bits_to_f32(b0)));
-        }
-    }
+    row16(h0, x);
+    if (ratio == 1) return;
+    float y[16];
+    row16(h0 + D_LAT, y);
+    merge16(x, y, w0 + lane * 16, w1 + lane * 16);
 }
 
 __global__ void __launch_bounds__(256) k_cache_write(uint8_t* __restrict__ lat_codes, uint8_t* __restrict__ lat_scales,
@@ -82,12 +61,6 @@ __global__ void __launch_bounds__(256) k_cache_write(uint8_t* __restrict__ lat_c
         reinterpret_cast<uint2*>(ik_codes + row * (d_idx / 2))[lane] = make_uint2(q0, q1);
         ik_scales[row * (d_idx / 16) + lane] = (uint8_t)sb;
     }
-}
-
-// E4M3 value times 2^9 (an integer below 2^18: the smallest E4M3 value is 2^-9)
-__device__ __forceinline__ int cw_e4m3_x512(uint32_t b) {
-    const uint32_t e = (b >> 3) & 15u, m = b & 7u;
-    return e ? (int)((8u + m) << (e - 1u)) : (int)m;
 }
 
 // Cache write with the indexer key projected from the entry itself

@@ -52,6 +52,7 @@ __device__ __forceinline__ float sqrt_approx(float x) {
 constexpr int D_LAT = 512;
 constexpr int WINDOW = 128;
 constexpr int MAX_K = 2048;
+constexpr int TREE_NODES = WINDOW;            // of a drafted tree at most: a chain then lies in the window
 constexpr int MAX_IDX_HEADS = 32;
 
 // the raw position of a sequence's first window row

@@ -67,10 +67,13 @@ enum { CSA2_FULL = 0, CSA2_REINDEX = 1, CSA2_REUSE = 2 };
 
 /* operations that take a workspace */
 enum { CSA2_OP_INDEXER_TOPK = 1, CSA2_OP_REINDEX = 2, CSA2_OP_SPARSE_ATTN = 3, CSA2_OP_DENSE_ATTN = 4,
-       CSA2_OP_LINEAR_FP4 = 5 };
+       CSA2_OP_LINEAR_FP4 = 5, CSA2_OP_TREE_ATTN = 6 };
 
 /* csa2_sparse_attn's swa_pos0: the window rows end at each sequence's last query */
 #define CSA2_WINDOW_AT_QUERY INT64_MIN
+
+/* csa2_tree_attn's k: no index lists, every visible entry */
+#define CSA2_EVERY_ENTRY (-1)
 
 /* element types of the operators that take more than one */
 enum { CSA2_BF16 = 0, CSA2_F16 = 1, CSA2_F32 = 2 };
@@ -329,6 +332,77 @@ csa2_status csa2_dense_attn(const csa2_cache* cache, const uint16_t* q, int32_t 
                             const int64_t* q_pos, const uint16_t* swa, const int64_t* swa_pos0, int32_t swa_len,
                             float scale, void* out, int32_t out_type, float* lse, void* workspace, size_t ws_bytes,
                             void* stream);
+
+/*
+ * Attention of a tree of drafted tokens: csa2_dense_attn or csa2_sparse_attn for n_q
+ * nodes whose own rows are not in the cache and the window yet ("DeepSeek-v4.1 Flash"
+ * §1.1, §2.3.1).  A node's chain is the node, its parent, and so on up to a child of
+ * the last committed token; with `len` tokens in it, a node at raw position p attends to
+ *     J = {entries i < n_elig(p)} (k = CSA2_EVERY_ENTRY), or its own list's {idx >= 0}
+ *         U committed window rows of positions max(0, p-127) .. p - len
+ *         U the draft rows of its chain
+ * The window rows from position p - len + 1 on (an earlier step's, say) are not read.
+ *   q        bf16 [batch][n_q][n_heads][d_lat], one row set a node; 1 <= n_q <= 128
+ *   q_pos    int64 [batch][n_q] raw positions (device): a child's is its parent's + 1
+ *   parent   int32 [batch][n_q] (device): a node before it (parent[i] < i), or -1 for a
+ *            child of the last committed token.  Any other value: the node is not there,
+ *            nor is what hangs on it; such nodes get zeros and lse -inf
+ *   draft    bf16 [batch][n_q][d_lat], the nodes' latent rows
+ *   idx      int32 [batch][n_q][k], -1 for an empty slot, or NULL where k <= 0;
+ *            entries outside the cache are empty slots; -1 <= k <= 2048
+ *   swa, swa_pos0, swa_len, out, out_type, lse, n_heads: as in csa2_dense_attn, and its
+ *            roundings.  q and what some node attends to are finite.
+ * Nodes that are not there and rows that no node attends to are not taken into account,
+ * whatever they hold.  q, draft, swa and out 16-byte aligned, q_pos and swa_pos0 8, parent,
+ * idx and lse 4.
+ * workspace: csa2_workspace_size(CSA2_OP_TREE_ATTN, batch, n_q, n_heads, k, capacity)
+ * bytes (with k <= 0 enough for CSA2_EVERY_ENTRY), 16-byte aligned.
+ */
+csa2_status csa2_tree_attn(const csa2_cache* cache, const uint16_t* q, int32_t n_q, int32_t n_heads,
+                           const int64_t* q_pos, const int32_t* parent, const uint16_t* draft, const int32_t* idx,
+                           int32_t k, const uint16_t* swa, const int64_t* swa_pos0, int32_t swa_len, float scale,
+                           void* out, int32_t out_type, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Cache write for sequences that each stand at a position of their own, of chosen
+ * rows: what a step has accepted ("DeepSeek-v4.1 Flash" §1.1, §2.3.1; the arithmetic
+ * of csa2_cache_write and csa2_cache_write_projected, bit for bit).  The rows
+ * path[b][0], path[b][1], .. of sequence b are its raw positions pos0[b], pos0[b] + 1,
+ * ..; the path ends at its first number outside 0 .. n_rows-1.  Written is every entry
+ * inside the cache whose last position is among them: of a ratio-2 cache the pairs that
+ * they complete, with the carried row of position pos0 - 1 where pos0 is odd.  No other
+ * entry is touched.
+ *   rows       bf16 [batch][n_rows][d_lat]
+ *   path       int32 [batch][n_path] (device) or NULL: rows 0 .. n_path-1 (n_path <= n_rows)
+ *   pos0       int64 [batch] (device)
+ *   prev       bf16 [batch][d_lat], the row of position pos0 - 1 (ratio 2; not taken with 1)
+ *   prev_out   bf16 [batch][d_lat] or NULL: the row of the path's last position, or prev's
+ *              where the path is empty; may be prev itself (ratio 2; not written with 1)
+ *   w0, w1     fp32 [d_lat] (ratio 2; not taken with 1)
+ *   wik_codes, wik_scales: the indexer-key projection in FP4, as in
+ *              csa2_cache_write_projected, or both NULL: latents only
+ * rows, prev, prev_out, w0, w1 and wik_codes 16-byte aligned, pos0 8, path and wik_scales 4;
+ * n_rows and n_path may be 0; batch <= 65535; rows that are taken are finite.  No workspace.
+ */
+csa2_status csa2_cache_append(const csa2_cache* cache, const uint16_t* rows, int32_t n_rows, const int32_t* path,
+                              int32_t n_path, const int64_t* pos0, const uint16_t* prev, uint16_t* prev_out,
+                              const float* w0, const float* w1, const uint8_t* wik_codes, const uint8_t* wik_scales,
+                              void* stream);
+
+enum { CSA2_LATENTS = 0, CSA2_INDEXER_KEYS = 1 };
+
+/*
+ * Entries of the cache as values (code times scale; exact in every type), latents or
+ * indexer keys: for checks, for exporting a sequence, and for code that wants the
+ * selected rows themselves.
+ *   what  CSA2_LATENTS (d = d_lat) or CSA2_INDEXER_KEYS (d = d_idx)
+ *   idx   int32 [batch][n] entry numbers (device); zeros for an empty slot (-1) and for a
+ *         number outside the cache.  NULL: entries first .. first + n - 1, all inside
+ *   out   [batch][n][d] of out_type (CSA2_BF16, _F16 or _F32), 16-byte aligned
+ * A NaN scale byte gives NaN.  n may be 0.  No workspace.
+ */
+csa2_status csa2_cache_read(const csa2_cache* cache, int32_t what, const int32_t* idx, int64_t first, int64_t n,
+                            void* out, int32_t out_type, void* stream);
 
 /*
  * Reindex without a workspace, for callers that cannot allocate device memory:
