@@ -7,16 +7,790 @@
 //     the committed window rows of positions max(0, p - 127) .. p - len;
 //     the draft rows of its chain (at most 128, so that they always lie in the window).
 //
-// One block of 8 warps a node and 8 heads, a warp a head: 32 rows at a time as fp32 in shared memory, an online
-// softmax with 16 of the output's dims a lane.
+// Every visible entry: k_tree_prep, k_tree_attn, k_tree_join.  The nodes of a sequence see the same entries but for the
+// last few, so their (node, head) rows are one matrix against the same keys: 4 x 512 flop per row and entry, 2,048
+// per byte of an entry and row.  The tensor cores bound it, and what feeds them is shared memory.
+//
+// Work.  An item is 128 consecutive rows of a sequence, worked on by a pair of CTAs with 64 rows each (tcgen05
+// cta_group::2); its units are its 128-key tiles: the committed window rows and the drafts first (at most 255 rows,
+// two tiles), then the entries.  Pair i takes the i-th even part of all units; an item that several pairs
+// share leaves each one's reference, row sums and unnormalised output in the workspace, and k_tree_join joins
+// them; all others are stored by their pair.
+//
+// One tile, CTA r of the pair:
+//   S = Q . L^T   M = 128 rows (64 from each CTA), N = 128 keys (64 from each CTA), K = 512 dims: a CTA expands its own
+//                 64 keys alone, so a key's fp16 row is made once for 128 rows
+//   softmax       a row has four threads, 32 keys each; weights against a reference that is raised, and O rescaled in
+//                 TMEM, only when a score rises far above it
+//   O += P . V    M = 128 rows, N = 2 x 256 dims, K = 128 keys.  Each CTA brings half of every N: dims 128 r .. + 127 and
+//                 256 + 128 r .. + 127 of all 128 keys.  Half of that are its own keys, where they are; the other CTA's
+//                 keys' dims it expands itself, over those dims of its own keys that only S needed: slab s of 64 dims
+//                 goes to place s ^ 2, which gives both CTAs the same address for the same keys, as the MMA asks.
+// Rows, running maxima, sums and outputs of a row stay in its CTA: the pair shares nothing but the MMAs.
+#include <algorithm>
+#include <type_traits>
+#include <utility>
+
 #include "common.cuh"
 #include "elem.cuh"
+#include "fp4_f16.cuh"
+#include "umma.cuh"
 
 namespace csa2 {
 
+// ---------------------------------------------------------------- every visible entry
+
+constexpr int TR_TILE = 128;                         // keys per tile, 64 of each CTA
+constexpr int TR_ROWS = 128;                         // rows of an item, 64 of each CTA
+constexpr int TR_THREADS = 640;
+constexpr int TR_SMW = 8, TR_SMT = TR_SMW * 32;      // warps 0-7: queries, softmax, epilogue
+constexpr int TR_MMA1 = 8;                           // warps 8, 9 of CTA 0: score MMAs of dims 0-255 and 256-511
+constexpr int TR_MMA2 = 10;                          // warps 10, 11 of CTA 0: value MMAs of dims 0-255 and 256-511
+constexpr int TR_LOADW = 12, TR_LOADERS = 256;       // warps 12-19: rows
+constexpr uint32_t TR_SLAB = 64 * 128;               // 64 rows or keys x 64 fp16, 128-byte swizzle
+constexpr uint32_t TR_SQ = 0;                        // Q: 8 slabs
+constexpr uint32_t TR_SL = 8 * TR_SLAB;              // L: 2 buffers x 8 slabs
+constexpr uint32_t TR_LBUF = 8 * TR_SLAB;
+constexpr uint32_t TR_SP = TR_SL + 2 * TR_LBUF;      // P: 2 buffers x 2 slabs (64 keys each)
+constexpr uint32_t TR_PBUF = 2 * TR_SLAB;
+constexpr uint32_t TR_DYN = TR_SP + 2 * TR_PBUF + 1024;                  // + alignment
+constexpr uint32_t TRT_S = 0, TRT_O = 256, TRT_COLS = 512;               // S partial p of buffer b at TRT_S + 64 (2b + p)
+// weights are 2^(score - m), m set TR_UP below the largest score and raised when one is more than TR_TOP above it: the
+// largest weight lies in [2^7, 2^15], within fp16's range, and what fp16 rounds to zero is below 2^-32 of it
+constexpr float TR_UP = 7.0f, TR_TOP = 15.0f;
+constexpr int TR_PAIRS = 76;                         // pairs of CTAs at most: one CTA per SM
+constexpr int TR_OVER = 1;                           // units of an item beside its tiles: its queries and its epilogue
+
+__device__ __forceinline__ uint32_t tr_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+// what the nodes of a sequence attend to, all together
+struct TreeSeq {
+    int n_vis;                   // entries 0 .. n_vis-1
+    int nw, n_rows;              // committed window rows, and with the drafts up to the last node that is there
+    int row_tiles;               // items
+    int exp;                     // the window rows and drafts go to fp16 after a division by 2^exp
+    int w0;                      // the window row that is the first committed one
+    uint32_t there[4];           // the nodes that are there
+    int pad[2];
+    __device__ __forceinline__ int wtiles() const { return (n_rows + TR_TILE - 1) / TR_TILE; }
+    __device__ __forceinline__ int tiles() const { return wtiles() + (int)(((unsigned)n_vis + TR_TILE - 1) / TR_TILE); }
+};
+// an item that several pairs share: the slot of its first share, and how many there are
+struct TreeHead {
+    int b, rt, slot, n;
+};
+struct TreeArgs {
+    const uint8_t *codes, *scales;
+    int batch, capacity, ratio;
+    const uint16_t* q;
+    int n_q, n_heads;
+    const int64_t* q_pos;
+    const int32_t* parent;
+    const uint16_t* draft;
+    const uint16_t* swa;
+    const int64_t* swa_pos0;
+    int swa_len;
+    float scale_log2e;
+    void* out;
+    float* lse;
+    TreeSeq* seq;                // [batch]
+    int* node_vis;               // [batch][n_q] entries that a node sees
+    uint32_t* node_mask;         // [batch][n_q][8] which of the n_rows rows
+    TreeHead* heads;             // [pairs]
+    float* part_o;               // [2 pairs][128][512]
+    float2* part_ml;             // [2 pairs][128] reference (log2) and row sum
+    int* err;
+};
+
+// One block a sequence (and some that write the rows of nodes that are not there): chains, masks, the rows' scale.
+template <typename TO>
+__global__ void __launch_bounds__(1024) k_tree_prep(const __grid_constant__ TreeArgs a) {
+    __shared__ int parent[TREE_NODES], last_s, vis_s;
+    __shared__ long long hi_s;
+    __shared__ uint32_t there[4], mx_s;
+    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x, N = a.n_q;
+    if (tid == 0) last_s = -1, vis_s = 0, mx_s = 0u, hi_s = -1;
+    if (tid < 4) there[tid] = 0u;
+    pdl_wait();
+    pdl_launch_next();
+    if (tid < N) parent[tid] = a.parent[(int64_t)b * N + tid];
+    __syncthreads();
+    int len = 0;
+    uint32_t anc[4] = {0u, 0u, 0u, 0u};
+    int64_t p = 0;
+    if (tid < N) {
+        p = a.q_pos[(int64_t)b * N + tid];
+        int j = tid;
+        while (j >= 0) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if ((j >> 5) == w) anc[w] |= 1u << (j & 31);
+            ++len;
+            const int up = parent[j];
+            j = up >= -1 && up < j ? up : -2;
+        }
+        if (j != -1) len = 0;
+        if (len > 0) {
+            atomicOr(&there[tid >> 5], 1u << lane);
+            atomicMax(&last_s, tid);
+        }
+    }
+    __syncthreads();
+    const int last = last_s;
+    const int row_tiles = ((last + 1) * a.n_heads + TR_ROWS - 1) / TR_ROWS;
+    if (blockIdx.y > 0) {
+        // rows of items that nobody works on
+        const int64_t r0 = (int64_t)row_tiles * TR_ROWS, r1 = (int64_t)N * a.n_heads, base = (int64_t)b * r1;
+        constexpr int E = 16 / (int)sizeof(TO);
+        uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<TO*>(a.out) + base * D_LAT);
+        const int64_t step = (int64_t)(gridDim.y - 1) * 1024, first = (int64_t)(blockIdx.y - 1) * 1024 + tid;
+        for (int64_t i = r0 * (D_LAT / E) + first; i < r1 * (D_LAT / E); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse != nullptr)
+            for (int64_t i = r0 + first; i < r1; i += step) a.lse[base + i] = -INFINITY;
+        return;
+    }
+    // every child of the last committed token stands at the same position: the one after hi
+    if (len > 0 && parent[tid] == -1) hi_s = p - len;
+    __syncthreads();
+    const int64_t s0 = a.swa_pos0 ? a.swa_pos0[b] : 0, hi0 = hi_s;
+    const int64_t lo = max(max((int64_t)0, hi0 - (WINDOW - 2)), s0), hi = min(hi0, s0 + a.swa_len - 1);
+    const int nw = last >= 0 && hi >= lo ? (int)(hi - lo + 1) : 0;       // at most 127
+    const int n_rows = last >= 0 ? nw + last + 1 : 0;
+    if (tid < N) {
+        int vis = 0;
+        uint32_t m[8] = {};
+        if (len > 0) {
+            vis = (int)min(p >= WINDOW - 1 ? (p - (WINDOW - 1)) >> (a.ratio - 1) : (int64_t)0, (int64_t)a.capacity);
+            atomicMax(&vis_s, vis);
+            const int c0 = (int)max((int64_t)0, min((int64_t)nw, p - (WINDOW - 1) - lo));        // committed rows c0 .. nw-1
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const int f = max(c0 - 32 * w, 0), e = min(nw - 32 * w, 32);
+                if (f < e) m[w] = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & ~((1u << f) - 1u);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {            // drafts: bit j of the chain at row nw + j
+                    const int at = nw + 32 * v - 32 * w;
+                    if (at >= 0 && at < 32) m[w] |= anc[v] << at;
+                    if (at < 0 && at > -32) m[w] |= anc[v] >> -at;
+                }
+            }
+        }
+        a.node_vis[(int64_t)b * N + tid] = vis;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) a.node_mask[((int64_t)b * N + tid) * 8 + w] = m[w];
+    }
+    // the largest magnitude of the rows (at most 255, 64 pieces each): all loads in flight
+    uint32_t mx = 0u;
+    const uint4* win = reinterpret_cast<const uint4*>(a.swa + ((int64_t)b * a.swa_len + (lo - s0)) * D_LAT);
+    const uint4* dr = reinterpret_cast<const uint4*>(a.draft + (int64_t)b * N * D_LAT);
+    uint4 x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int v = tid + i * 1024, r = v >> 6, j = r - nw;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < nw)
+            x[i] = win[v];
+        else if (r < n_rows && ((there[j >> 5] >> (j & 31)) & 1u))
+            x[i] = dr[v - nw * 64];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = max(mx, bf16_absmax8(x[i]));
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (lane == 0) atomicMax(&mx_s, mx);
+    __syncthreads();
+    if (tid == 0) {
+        TreeSeq s{vis_s, nw, n_rows, row_tiles, f16_range_exp(mx_s), (int)(lo - s0), {there[0], there[1], there[2], there[3]}, {0, 0}};
+        a.seq[b] = s;
+    }
+}
+
+// Where a pair stands in its part of all units, and the share that comes next
+struct TreeCursor {
+    int64_t u, u1, off;          // the next unit, the end of the part, the unit's place among its sequence's
+    int b;
+};
+struct TreeShare {
+    TreeSeq s;
+    int b, rt, t0, t1, T;        // tiles t0 .. t1-1 of the item's T
+};
+__device__ __forceinline__ bool tr_next(const TreeArgs& a, TreeCursor& c, TreeShare& h) {
+    while (c.u < c.u1) {
+        h.s = a.seq[c.b];
+        h.T = h.s.tiles();
+        const int per = h.T + TR_OVER;
+        if (c.off >= (int64_t)h.s.row_tiles * per) {
+            ++c.b, c.off = 0;
+            continue;
+        }
+        h.b = c.b;
+        h.rt = (int)(c.off / per);
+        h.t0 = (int)(c.off - (int64_t)h.rt * per);
+        const int n = (int)min((int64_t)(per - h.t0), c.u1 - c.u);
+        h.t1 = min(h.t0 + n, h.T);
+        c.u += n, c.off += n;
+        if (h.t1 > h.t0) return true;
+    }
+    return false;
+}
+
+template <typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tree_attn(const __grid_constant__ TreeArgs a) {
+    extern __shared__ uint8_t dyn[];
+    // in CTA 0, counting warps of both CTAs: dims 0-255 of a tile's keys ready, all of them, the other CTA's keys ready, the
+    // scores read, P written, the queries staged.  In each CTA, arrived on by the MMAs: scores done, values done
+    __shared__ __align__(8) unsigned long long b_half[2], b_full[2], b_for[2], b_sfree[2], b_pfull[2], b_q, b_sfull[2], b_odone[2];
+    __shared__ uint32_t tmem_base;
+    __shared__ float red[4][64];
+    __shared__ int qexp[64];
+    __shared__ int64_t wsum[TR_THREADS / 32], start_off;
+    __shared__ int start_b;
+    const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
+    uint8_t* sm = dyn + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = umma::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    auto sa = [&](const void* x) { return umma::smem_u32(x); };
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(sa(&b_half[i]), 2 * TR_LOADERS / 32);
+            umma::mbar_init(sa(&b_full[i]), 2 * TR_LOADERS / 32);
+            umma::mbar_init(sa(&b_for[i]), 2 * TR_LOADERS / 32);
+            umma::mbar_init(sa(&b_sfree[i]), 2 * TR_SMW);
+            umma::mbar_init(sa(&b_pfull[i]), 2 * TR_SMW);
+            umma::mbar_init(sa(&b_sfull[i]), 2);
+            umma::mbar_init(sa(&b_odone[i]), 2);
+        }
+        umma::mbar_init(sa(&b_q), 2 * TR_SMW);
+        umma::fence_mbar_init();
+        start_b = 0, start_off = 0;
+    }
+    if (warp == TR_LOADW - 1) umma::tmem_alloc_pair(sa(&tmem_base), TRT_COLS);
+    pdl_wait();
+    pdl_launch_next();
+
+    // ---- this pair's part of all units: a sum over the sequences, each thread taking consecutive ones
+    const int per = (a.batch + TR_THREADS - 1) / TR_THREADS;
+    const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+    auto units = [&](int b) {
+        const TreeSeq s = a.seq[b];
+        return (int64_t)s.row_tiles * (s.tiles() + TR_OVER);
+    };
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units(b);
+    int64_t upto = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) wsum[warp] = upto;
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    int64_t total = 0;
+    for (int i = 0; i < TR_THREADS / 32; ++i) {
+        if (i < warp) upto += wsum[i];
+        total += wsum[i];
+    }
+    // total % pairs of the parts have one unit more than the others, and come first
+    const int64_t each = total < 0x7fffffff ? (int64_t)((unsigned)total / (unsigned)pairs) : total / pairs;
+    const int64_t more = total - each * pairs;
+    auto start_of = [&](int i) { return each * i + min((int64_t)i, more); };
+    auto part_of = [&](int64_t u) {                  // the pair that has unit u
+        const int64_t longer = (each + 1) * more;
+        return u < longer ? (int)(u / (each + 1)) : (int)(more + (u - longer) / each);
+    };
+    const int64_t u0 = start_of(pair), u1 = start_of(pair + 1);
+    if (rank == 0 && tid == 0) a.heads[pair] = TreeHead{0, 0, 0, 0};
+    {
+        int64_t s = upto - mine;
+        if (u0 < u1 && s <= u0 && u0 < upto)
+            for (int b = b0; b < b1; ++b) {
+                const int64_t n = units(b);
+                if (u0 < s + n) {
+                    start_b = b, start_off = u0 - s;
+                    break;
+                }
+                s += n;
+            }
+    }
+    __syncthreads();
+    umma::cluster_sync();        // the other CTA's barriers are there
+    const uint32_t tmem = tmem_base;
+    TreeCursor cur{u0, u1, start_off, start_b};
+    TreeShare h;
+    bool ok = true;
+    uint32_t tb = 0;                                 // tiles done so far: the rings go on from share to share
+
+    if (warp >= TR_LOADW) {
+        // ================= rows.  A tile's own keys as soon as its buffer is free, the other CTA's keys' dims once its
+        // scores are done; each warp takes whichever is ready, the latter first.
+        const int lt = tid - TR_LOADW * 32, lw = warp - TR_LOADW;
+        const uint32_t r_half[2] = {umma::mapa(sa(&b_half[0]), 0), umma::mapa(sa(&b_half[1]), 0)};
+        const uint32_t r_full[2] = {umma::mapa(sa(&b_full[0]), 0), umma::mapa(sa(&b_full[1]), 0)};
+        const uint32_t r_for[2] = {umma::mapa(sa(&b_for[0]), 0), umma::mapa(sa(&b_for[1]), 0)};
+        auto arrive = [&](uint32_t bar) {
+            umma::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive_remote(bar);
+        };
+        while (tr_next(a, cur, h)) {
+            const int T = h.t1 - h.t0, wt = h.s.wtiles(), n_vis = h.s.n_vis;
+            const uint8_t* codes = a.codes + (int64_t)h.b * a.capacity * (D_LAT / 2);
+            const uint8_t* scales = a.scales + (int64_t)h.b * a.capacity * (D_LAT / 16);
+            const float down = pow2f(-h.s.exp);
+            // a unit is 32 dims of a key (16 bytes of codes, 2 of scales).  Own keys: a warp takes 4 keys x 8 units, whole
+            // 128-byte lines of codes; units below 512 are dims 0-255.  The other's: 4 keys x the 8 units of this CTA's dims
+            const int kr = lane & 3, ku = lane >> 2;
+            auto own_rc = [&](int i, int& r, int& c) {
+                const int qq = lw + 8 * i;
+                r = 4 * (qq & 15) + kr;
+                c = 8 * (qq >> 4) + ku;
+            };
+            auto for_rc = [&](int i, int& r, int& c) {
+                r = 4 * (lw + 8 * i) + kr;
+                c = 8 * (ku >> 2) + 4 * (int)rank + (ku & 3);
+            };
+            uint4 cw[4], fw[2];
+            uint32_t sc[4], fs[2];
+            auto load = [&](int tile, uint32_t side, int r, int c, uint4& w, uint32_t& s) {
+                const int j = tile * TR_TILE + 64 * (int)side + r;
+                w = make_uint4(0u, 0u, 0u, 0u), s = 0u;          // keys past the end expand to zeros
+                if (j < n_vis) {
+                    w = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)j * (D_LAT / 2)) + c);
+                    s = __ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)j * (D_LAT / 16)) + c);
+                }
+            };
+            auto expand = [&](uint8_t* L, int r, int c, int flip, const uint4& w, uint32_t s) {
+                const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                const __half2 sp = e4m3x2_to_f16x2(s);
+                const __half2 s_lo = __low2half2(sp), s_hi = __high2half2(sp);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int cc = 4 * c + k;
+                    *reinterpret_cast<uint4*>(L + ((cc >> 3) ^ flip) * TR_SLAB + tr_swz(r, cc & 7)) =
+                        e2m1x8_scaled(words[k], (k >> 1) ? s_hi : s_lo);
+                }
+            };
+            // row v of the window rows and drafts, 8 dims at chunk cc
+            auto bf16_row = [&](int v, int cc) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                const int j = v - h.s.nw;
+                if (j < 0)
+                    x = *reinterpret_cast<const uint4*>(a.swa + ((int64_t)h.b * a.swa_len + h.s.w0 + v) * D_LAT + 8 * cc);
+                else if (v < h.s.n_rows && ((h.s.there[j >> 5] >> (j & 31)) & 1u))
+                    x = *reinterpret_cast<const uint4*>(a.draft + ((int64_t)h.b * a.n_q + j) * D_LAT + 8 * cc);
+                return bf16x8_to_f16x8(x, down);
+            };
+            auto fetch_own = [&](int t) {
+                if (t < T && h.t0 + t >= wt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        int r, c;
+                        own_rc(i, r, c);
+                        load(h.t0 + t - wt, rank, r, c, cw[i], sc[i]);
+                    }
+            };
+            auto fetch_for = [&](int t) {
+                if (t < T && h.t0 + t >= wt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        int r, c;
+                        for_rc(i, r, c);
+                        load(h.t0 + t - wt, rank ^ 1u, r, c, fw[i], fs[i]);
+                    }
+            };
+            fetch_own(0);
+            fetch_for(0);
+            int own = 0, fo = 0;
+            uint32_t polls = 0;
+            while (ok && fo < T) {
+                const uint32_t go = tb + own, gf = tb + fo;
+                const bool fready = fo < own && umma::mbar_test(sa(&b_sfull[gf & 1]), (gf >> 1) & 1);
+                const bool oready = !fready && own < T && (go < 2 || umma::mbar_test(sa(&b_odone[go & 1]), ((go >> 1) - 1) & 1));
+                if (__any_sync(0xffffffffu, fready)) {
+                    uint8_t* L = sm + TR_SL + (gf & 1) * TR_LBUF;
+                    if (h.t0 + fo < wt) {
+                        const int v0 = (h.t0 + fo) * TR_TILE + 64 * (int)(rank ^ 1u);
+#pragma unroll 4
+                        for (int i = lt; i < 64 * 32; i += TR_LOADERS) {
+                            const int r = i >> 5, cs = i & 31;       // this CTA's 32 chunks: 16 of dims 128 r .., 16 of 256 + 128 r ..
+                            const int cc = 32 * (cs >> 4) + 16 * (int)rank + (cs & 15);
+                            *reinterpret_cast<uint4*>(L + ((cc >> 3) ^ 2) * TR_SLAB + tr_swz(r, cc & 7)) = bf16_row(v0 + r, cc);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            int r, c;
+                            for_rc(i, r, c);
+                            expand(L, r, c, 2, fw[i], fs[i]);
+                        }
+                    }
+                    arrive(r_for[gf & 1]);
+                    ++fo;
+                    fetch_for(fo);
+                    polls = 0;
+                } else if (__any_sync(0xffffffffu, oready)) {
+                    uint8_t* L = sm + TR_SL + (go & 1) * TR_LBUF;
+                    if (h.t0 + own < wt) {
+                        const int v0 = (h.t0 + own) * TR_TILE + 64 * (int)rank;
+#pragma unroll 4
+                        for (int i = lt; i < 64 * 64; i += TR_LOADERS) {
+                            const int r = i >> 6, cc = i & 63;
+                            *reinterpret_cast<uint4*>(L + (cc >> 3) * TR_SLAB + tr_swz(r, cc & 7)) = bf16_row(v0 + r, cc);
+                        }
+                        arrive(r_half[go & 1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            int r, c;
+                            own_rc(i, r, c);
+                            if (i == 2) arrive(r_half[go & 1]);       // dims 0-255 are done
+                            expand(L, r, c, 0, cw[i], sc[i]);
+                        }
+                    }
+                    arrive(r_full[go & 1]);
+                    ++own;
+                    fetch_own(own);
+                    polls = 0;
+                } else if (++polls > (1u << 24)) {
+                    ok = false;
+                }
+                __syncwarp();
+            }
+            tb += T;
+        }
+    } else if (warp >= TR_MMA1 && rank == 0) {
+        // ================= MMAs of the pair.  The whole warp walks the tiles, so that descriptors and addresses stay in
+        // uniform registers; one elected lane issues.
+        const bool scores = warp < TR_MMA2;
+        const int half = (warp - TR_MMA1) & 1;
+        const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+        const uint32_t id = scores ? umma::idesc_f16(128, 128, 0, 0) : umma::idesc_f16(128, 256, 0, 1);
+        const uint64_t qd = umma::desc(base + TR_SQ, 16, 1024, umma::LAYOUT_SW128);
+        uint32_t k = 0;
+        while (ok && tr_next(a, cur, h)) {
+            const int T = h.t1 - h.t0;
+            if (scores) ok = umma::mbar_wait_cluster(sa(&b_q), k & 1);
+            for (int t = 0; t < T; ++t) {
+                const uint32_t tg = tb + t, buf = tg & 1, ph = (tg >> 1) & 1;
+                if (scores) {
+                    ok = ok && umma::mbar_wait_cluster(sa(half == 0 ? &b_half[buf] : &b_full[buf]), ph);
+                    if (tg >= 2) ok = ok && umma::mbar_wait_cluster(sa(&b_sfree[buf]), ph ^ 1);
+                } else {
+                    ok = ok && umma::mbar_wait_cluster(sa(&b_for[buf]), ph);
+                    ok = ok && umma::mbar_wait_cluster(sa(&b_pfull[buf]), ph);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                umma::fence_after();
+                if (umma::elect_one()) {
+                    if (scores) {
+                        const uint64_t ld = umma::desc(base + TR_SL + buf * TR_LBUF, 16, 1024, umma::LAYOUT_SW128);
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk) {
+                            const int ks = 16 * half + kk;
+                            const uint64_t off = (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4);
+                            umma::mma_f16_pair(tm + TRT_S + 64 * (2 * buf + half), qd + off, ld + off, id, kk > 0);
+                        }
+                        umma::commit_pair(sa(&b_sfull[buf]));
+                    } else {
+                        // keys 0-63 (CTA 0's) in places 4 half, 4 half + 1, keys 64-127 in the two after them
+                        const uint64_t vd = umma::desc(base + TR_SL + buf * TR_LBUF + 4 * half * TR_SLAB, TR_SLAB, 1024, umma::LAYOUT_SW128);
+                        const uint64_t pd = umma::desc(base + TR_SP + buf * TR_PBUF, 16, 1024, umma::LAYOUT_SW128);
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            umma::mma_f16_pair(tm + TRT_O + 128 * half, pd + (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4),
+                                               vd + (uint64_t)((2 * (ks >> 2) * TR_SLAB + (ks & 3) * 2048) >> 4), id,
+                                               (t > 0 || ks > 0) ? 1u : 0u);
+                        umma::commit_pair(sa(&b_odone[buf]));
+                    }
+                }
+                __syncwarp();
+            }
+            tb += T;
+            ++k;
+        }
+    } else if (warp < TR_SMW) {
+        // ================= queries, softmax, outputs: a thread has one row (TMEM lane 32 (warp % 4) + lane: row lane % 64) and,
+        // of the tile's keys, 64 (lane / 64) + 32 (warp / 4) .. + 31; of the row's output, 128 dims
+        const int qd = warp & 3, ch = warp >> 2, kh = qd >> 1, row = 32 * (qd & 1) + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
+        const uint32_t r_q = umma::mapa(sa(&b_q), 0);
+        const uint32_t r_sfree[2] = {umma::mapa(sa(&b_sfree[0]), 0), umma::mapa(sa(&b_sfree[1]), 0)};
+        const uint32_t r_pfull[2] = {umma::mapa(sa(&b_pfull[0]), 0), umma::mapa(sa(&b_pfull[1]), 0)};
+        bool first_share = true;
+        while (tr_next(a, cur, h)) {
+            const int T = h.t1 - h.t0, wt = h.s.wtiles();
+            const int n_rows_q = a.n_q * a.n_heads, q0 = h.rt * TR_ROWS + 64 * (int)rank;
+            // ---- Q: this CTA's 64 rows, bf16 -> fp16 slabs; a row whose largest magnitude lies outside [2^-10, 2^15) is
+            // scaled by a power of two on the way.  (S of the share before is done: its values were.)
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)h.b * n_rows_q + q0) * D_LAT);
+#pragma unroll 1
+                for (int r0 = warp; r0 < 64; r0 += 4 * TR_SMW) {
+                    uint4 x[4][2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + TR_SMW * i;
+                        x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                        if (q0 + r < n_rows_q) x[i][0] = src[r * 64 + lane], x[i][1] = src[r * 64 + 32 + lane];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + TR_SMW * i;
+                        const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
+                        const float d = pow2f(-e);
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const int c = lane + 32 * hh;
+                            *reinterpret_cast<uint4*>(sm + TR_SQ + (c >> 3) * TR_SLAB + tr_swz(r, c & 7)) = bf16x8_to_f16x8(x[i][hh], d);
+                        }
+                        if (lane == 0) qexp[r] = e;
+                    }
+                }
+                umma::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive_remote(r_q);
+                umma::bar_named(1, TR_SMT);
+            }
+            const float mul4 = a.scale_log2e * pow2f(qexp[row]), up = pow2f(h.s.exp);
+            int vis = 0;
+            const uint32_t* mask = nullptr;
+            if (q0 + row < n_rows_q) {
+                const int64_t node = (int64_t)h.b * a.n_q + (int)((unsigned)(q0 + row) / (unsigned)a.n_heads);
+                vis = a.node_vis[node];
+                mask = a.node_mask + node * 8 + 2 * kh + ch;
+            }
+            float m = -INFINITY, lsum = 0.0f;
+            for (int t = 0; t < T; ++t) {
+                const uint32_t tg = tb + t, buf = tg & 1, ph = (tg >> 1) & 1;
+                const int tile = h.t0 + t;
+                const bool window = tile < wt;
+                uint32_t see = 0xffffffffu;          // which of the 32 keys this row attends to
+                if (window)
+                    see = mask != nullptr ? mask[4 * tile] : 0u;
+                else {
+                    const int left = vis - ((tile - wt) * TR_TILE + 64 * kh + 32 * ch);
+                    if (left < 32) see = left <= 0 ? 0u : (1u << left) - 1u;
+                }
+                float x[32];
+                ok = ok && umma::mbar_wait_fast(sa(&b_sfull[buf]), ph);
+                umma::fence_after();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x1[16];
+                    umma::tmem_ld16(lane_base + TRT_S + 64 * (2 * buf) + 32 * ch + 16 * i, x + 16 * i);
+                    umma::tmem_ld16(lane_base + TRT_S + 64 * (2 * buf + 1) + 32 * ch + 16 * i, x1);
+                    umma::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[16 * i + j] += x1[j];
+                }
+                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive_remote(r_sfree[buf]);
+                const float mul = window ? mul4 * up : mul4;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] *= mul;
+                if (see != 0xffffffffu)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((see >> i) & 1u)) x[i] = -INFINITY;
+                float mx = x[0];
+#pragma unroll
+                for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
+                // the window tiles' part of O carries 2^-exp: it is brought to the common scale before the entries' is added
+                const bool rescale_window = !window && tile == wt && t > 0 && h.s.exp != 0;
+                if (umma::bar_red_or(1, TR_SMT, mx - m > TR_TOP || (m == -INFINITY && mx > -INFINITY)) || rescale_window) {
+                    red[2 * kh + ch][row] = mx;
+                    umma::bar_named(1, TR_SMT);
+                    const float mt = fmaxf(fmaxf(red[0][row], red[1][row]), fmaxf(red[2][row], red[3][row]));
+                    float f = 1.0f;
+                    if (mt > -INFINITY && (m == -INFINITY || mt - m > TR_TOP)) {
+                        f = m == -INFINITY ? 0.0f : umma::ex2(m - (mt - TR_UP));
+                        m = mt - TR_UP;
+                    }
+                    lsum *= f;
+                    if (rescale_window) f *= up;
+                    if (t >= 1) {
+                        ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);      // O settled
+                        umma::fence_after();
+                        if (__any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll 1
+                            for (int c = 0; c < 128; c += 16) {
+                                float v[16];
+                                umma::tmem_ld16(lane_base + TRT_O + 128 * ch + c, v);
+                                umma::tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] *= f;
+                                umma::tmem_st16(lane_base + TRT_O + 128 * ch + c, v);
+                            }
+                            umma::tmem_wait_st();
+                        }
+                    }
+                    umma::bar_named(1, TR_SMT);      // red is read
+                }
+                if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf]), ph ^ 1);          // the P buffer is free
+                const float ref = m == -INFINITY ? 0.0f : m;
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    x[i] = umma::ex2_ftz(x[i] - ref);
+                    sum[i & 1] += x[i];
+                }
+                lsum += sum[0] + sum[1];
+                uint8_t* P = sm + TR_SP + buf * TR_PBUF + kh * TR_SLAB;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4*>(P + tr_swz(row, 4 * ch + c)) =
+                        make_uint4(f16x2_bits(x[8 * c], x[8 * c + 1]), f16x2_bits(x[8 * c + 2], x[8 * c + 3]),
+                                   f16x2_bits(x[8 * c + 4], x[8 * c + 5]), f16x2_bits(x[8 * c + 6], x[8 * c + 7]));
+                umma::fence_proxy_async();
+                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive_remote(r_pfull[buf]);
+            }
+            // ---- the share's end: the row's sum over its four threads, then O
+            red[2 * kh + ch][row] = lsum;
+            umma::bar_named(1, TR_SMT);
+            const float l = (red[0][row] + red[1][row]) + (red[2][row] + red[3][row]);
+            const uint32_t tl = tb + T - 1;
+            ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
+            umma::fence_after();
+            const float fin = h.t1 <= wt ? up : 1.0f;
+            const bool whole = T == h.T;
+            const int64_t gr = (int64_t)h.b * n_rows_q + q0 + row;
+            const bool there = q0 + row < n_rows_q;
+            const int slot = 2 * pair + (first_share ? 0 : 1);
+            const int64_t pr = (int64_t)slot * TR_ROWS + 64 * (int)rank + row;
+            const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+            const int d0 = 256 * ch + 128 * kh;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 16) {
+                float v[16];
+                umma::tmem_ld16(lane_base + TRT_O + 128 * ch + c, v);
+                umma::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = ok ? v[i] * fin : __int_as_float(0x7fc00000);
+                if (!whole) {
+                    ElemVec<float, 16> y;
+                    y.pack(v);
+                    y.store(a.part_o + pr * D_LAT + d0 + c);
+                } else if (there) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] *= inv;
+                    ElemVec<TO, 16> y;
+                    y.pack(v);
+                    y.store(reinterpret_cast<TO*>(a.out) + gr * D_LAT + d0 + c);
+                }
+            }
+            if (2 * kh + ch == 0) {
+                if (!whole)
+                    a.part_ml[pr] = make_float2(m, l);
+                else if (there && a.lse != nullptr)
+                    a.lse[gr] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            }
+            // an item that begins here and goes on in other pairs is joined from their shares
+            if (!whole && h.t0 == 0 && rank == 0 && tid == 0)
+                a.heads[pair] = TreeHead{h.b, h.rt, slot, part_of(cur.u - 1 + (h.T - h.t1)) - pair + 1};
+            first_share = false;
+            tb += T;
+            umma::fence_before();
+            umma::bar_named(1, TR_SMT);              // red, qexp and O are read
+            umma::fence_after();
+        }
+    }
+    if (!ok) atomicExch(a.err, 1);
+    umma::fence_before();
+    __syncthreads();
+    umma::cluster_sync();
+    if (warp == TR_LOADW - 1) {
+        umma::fence_after();
+        umma::tmem_dealloc_pair(tmem, TRT_COLS);
+    }
+}
+
+// Joins the shares of an item that several pairs worked on, four dims a thread.  SPREAD 1: block (pair, four rows);
+// SPREAD 4, for few items: block (item, row), four groups of 128 threads that take every fourth share.
+template <typename TO, int SPREAD>
+__global__ void __launch_bounds__(512) k_tree_join(const __grid_constant__ TreeArgs a, int pairs, int row_tiles) {
+    __shared__ float4 sums[SPREAD > 1 ? 3 : 1][128];
+    const int tid = threadIdx.x, dim = tid & 127, group = SPREAD > 1 ? tid >> 7 : 0, lane = tid & 31;
+    pdl_wait();
+    TreeHead hd{0, 0, 0, 0};
+    int row;
+    if (SPREAD == 1) {
+        hd = a.heads[blockIdx.x];
+        row = (int)blockIdx.y * 4 + (tid >> 7);
+    } else {
+        row = (int)blockIdx.y;
+        for (int i = lane; i < pairs; i += 32) {
+            const TreeHead x = a.heads[i];
+            if (x.n > 0 && x.b * row_tiles + x.rt == (int)blockIdx.x) hd = x;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, hd.n > 0);
+        const int src = who ? __ffs(who) - 1 : 0;
+        hd.b = __shfl_sync(0xffffffffu, hd.b, src), hd.rt = __shfl_sync(0xffffffffu, hd.rt, src);
+        hd.slot = __shfl_sync(0xffffffffu, hd.slot, src), hd.n = __shfl_sync(0xffffffffu, hd.n, src);
+    }
+    const int in_seq = hd.rt * TR_ROWS + row;
+    if (hd.n == 0 || in_seq >= a.n_q * a.n_heads) return;
+    // the first share's slot, then the first slots of the pairs after it
+    auto share = [&](int s) { return (int64_t)(s == 0 ? hd.slot : ((hd.slot >> 1) + s) * 2) * TR_ROWS + row; };
+    constexpr int NB = 8;
+    float m = -INFINITY, l = 0.0f;
+    for (int s = lane; s < hd.n; s += 32) {
+        const float2 v = a.part_ml[share(s)];
+        if (v.y != 0.0f) m = fmaxf(m, v.x);
+    }
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float o[4] = {};
+    for (int s0 = group; s0 < hd.n; s0 += NB * SPREAD) {
+        float4 x[NB];
+        float2 v[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int64_t at = share(min(s0 + i * SPREAD, hd.n - 1));
+            x[i] = reinterpret_cast<const float4*>(a.part_o + at * D_LAT)[dim];
+            v[i] = a.part_ml[at];
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            if (s0 + i * SPREAD >= hd.n) continue;
+            const float f = v[i].y != 0.0f ? exp2f(v[i].x - m) : 0.0f;
+            o[0] = fmaf(f, x[i].x, o[0]), o[1] = fmaf(f, x[i].y, o[1]);
+            o[2] = fmaf(f, x[i].z, o[2]), o[3] = fmaf(f, x[i].w, o[3]);
+        }
+    }
+    for (int s = lane; s < hd.n; s += 32) {
+        const float2 v = a.part_ml[share(s)];
+        if (v.y != 0.0f) l = fmaf(exp2f(v.x - m), v.y, l);
+    }
+    for (int o2 = 16; o2; o2 >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
+    if constexpr (SPREAD > 1) {
+        if (group > 0) sums[group - 1][dim] = make_float4(o[0], o[1], o[2], o[3]);
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const float4 x = sums[i][dim];
+            o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
+        }
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    const int64_t gr = (int64_t)hd.b * a.n_q * a.n_heads + in_seq;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= inv;
+    ElemVec<TO, 4> y;
+    y.pack(o);
+    y.store(reinterpret_cast<TO*>(a.out) + gr * D_LAT + 4 * dim);
+    if (a.lse != nullptr && dim == 0) a.lse[gr] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// ---------------------------------------------------------------- index lists
+
 constexpr int TS_TILE = 32, TS_HEADS = 8;
 
-struct TreeArgs {
+struct SimtArgs {
     const uint8_t *codes, *scales;
     int capacity, ratio;
     const uint16_t* q;
@@ -34,7 +808,7 @@ struct TreeArgs {
 };
 
 template <typename TO>
-__global__ void __launch_bounds__(256) k_tree_attn_simt(const __grid_constant__ TreeArgs a, TO* __restrict__ out) {
+__global__ void __launch_bounds__(256) k_tree_attn_simt(const __grid_constant__ SimtArgs a, TO* __restrict__ out) {
     pdl_wait();
     pdl_launch_next();
     extern __shared__ float sm[];
@@ -127,21 +901,81 @@ __global__ void __launch_bounds__(256) k_tree_attn_simt(const __grid_constant__ 
     if (a.lse != nullptr && lane == 0) a.lse[gq * a.n_heads + h] = l == 0.0f ? -INFINITY : m + logf(l);
 }
 
-size_t tree_attn_ws(int, int, int, int, int64_t) { return 256; }
+namespace {
+constexpr size_t TR_HEAD = 256;                      // the error word and padding
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct TreePlan {
+    int row_tiles, pairs;
+    size_t seq, vis, mask, heads, o, ml;             // bytes of the workspace's parts
+    size_t total() const { return TR_HEAD + seq + vis + mask + heads + o + ml; }
+};
+TreePlan tree_plan(int batch, int n_q, int n_heads, int64_t capacity) {
+    TreePlan p;
+    p.row_tiles = (n_q * n_heads + TR_ROWS - 1) / TR_ROWS;
+    // fewer pairs where even a full cache has fewer tiles
+    const int64_t tiles = (capacity + TR_TILE - 1) / TR_TILE + 2;
+    p.pairs = (int)std::min<int64_t>(TR_PAIRS, (int64_t)batch * p.row_tiles * tiles);
+    p.seq = up256((size_t)batch * sizeof(TreeSeq));
+    p.vis = up256((size_t)batch * n_q * sizeof(int));
+    p.mask = up256((size_t)batch * n_q * 8 * sizeof(uint32_t));
+    p.heads = up256((size_t)p.pairs * sizeof(TreeHead));
+    p.o = (size_t)2 * p.pairs * TR_ROWS * D_LAT * sizeof(float);
+    p.ml = (size_t)2 * p.pairs * TR_ROWS * sizeof(float2);
+    return p;
+}
+}  // namespace
+
+size_t tree_attn_ws(int batch, int n_q, int n_heads, int k, int64_t capacity) {
+    return k > 0 ? TR_HEAD : tree_plan(batch, n_q, n_heads, capacity).total();
+}
 
 cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
                              const int32_t* parent, const uint16_t* draft, const int32_t* idx, int k, const uint16_t* swa,
-                             const int64_t* swa_pos0, int swa_len, float scale, void* out, int out_type, float* lse, void*,
+                             const int64_t* swa_pos0, int swa_len, float scale, void* out, int out_type, float* lse, void* ws,
                              cudaStream_t st) {
-    const TreeArgs a{c.lat_codes, c.lat_scales, c.capacity, c.ratio, q, n_q, n_heads, q_pos, parent, draft, idx, k,
-                     swa, swa_pos0, swa_len, scale, lse};
-    const size_t smem = (TS_HEADS + TS_TILE) * D_LAT * sizeof(float);
+    if (k >= 0) {
+        const SimtArgs a{c.lat_codes, c.lat_scales, c.capacity, c.ratio, q, n_q, n_heads, q_pos, parent, draft, idx, k,
+                         swa, swa_pos0, swa_len, scale, lse};
+        const size_t smem = (TS_HEADS + TS_TILE) * D_LAT * sizeof(float);
+        auto go = [&](auto* y) {
+            const auto kern = k_tree_attn_simt<std::remove_pointer_t<decltype(y)>>;
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            launch_k(kern, dim3((n_heads + TS_HEADS - 1) / TS_HEADS, n_q, c.batch), 256, smem, st, a, y);
+            note_launch();
+            return cudaGetLastError();
+        };
+        return out_type == CSA2_F32   ? go(reinterpret_cast<float*>(out))
+               : out_type == CSA2_F16 ? go(reinterpret_cast<__half*>(out))
+                                      : go(reinterpret_cast<__nv_bfloat16*>(out));
+    }
+    const TreePlan p = tree_plan(c.batch, n_q, n_heads, c.capacity);
+    uint8_t* w = reinterpret_cast<uint8_t*>(ws) + TR_HEAD;
+    auto take = [&](size_t n) { return std::exchange(w, w + n); };
+    TreeArgs a{c.lat_codes, c.lat_scales, c.batch, c.capacity, c.ratio, q, n_q, n_heads, q_pos, parent, draft, swa, swa_pos0, swa_len,
+               scale * 1.4426950408889634f, out, lse, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, reinterpret_cast<int*>(ws)};
+    a.seq = reinterpret_cast<TreeSeq*>(take(p.seq));
+    a.node_vis = reinterpret_cast<int*>(take(p.vis));
+    a.node_mask = reinterpret_cast<uint32_t*>(take(p.mask));
+    a.heads = reinterpret_cast<TreeHead*>(take(p.heads));
+    a.part_o = reinterpret_cast<float*>(take(p.o));
+    a.part_ml = reinterpret_cast<float2*>(take(p.ml));
     auto go = [&](auto* y) {
-        const auto kern = k_tree_attn_simt<std::remove_pointer_t<decltype(y)>>;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        using TO = std::remove_pointer_t<decltype(y)>;
+        cudaError_t e = cudaFuncSetAttribute(k_tree_attn<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TR_DYN);
         if (e != cudaSuccess) return e;
-        launch_k(kern, dim3((n_heads + TS_HEADS - 1) / TS_HEADS, n_q, c.batch), 256, smem, st, a, y);
-        note_launch();
+        const int zero = std::min(16, (n_q * n_heads + 511) / 512);      // blocks that write the rows of nodes that are not there
+        launch_k(k_tree_prep<TO>, dim3((unsigned)c.batch, (unsigned)(1 + zero)), 1024, 0, st, a);
+        launch_k(k_tree_attn<TO>, dim3((unsigned)(2 * p.pairs)), TR_THREADS, TR_DYN, st, a);
+        // few items: many shares each, so a block per row
+        const int64_t items = (int64_t)c.batch * p.row_tiles;
+        const int rows = std::min(TR_ROWS, n_q * n_heads);
+        if (items * 8 <= p.pairs)
+            launch_k(k_tree_join<TO, 4>, dim3((unsigned)items, (unsigned)rows), 512, 0, st, a, p.pairs, p.row_tiles);
+        else
+            launch_k(k_tree_join<TO, 1>, dim3((unsigned)p.pairs, (unsigned)((rows + 3) / 4)), 512, 0, st, a, p.pairs, p.row_tiles);
+        note_launch(3);
         return cudaGetLastError();
     };
     return out_type == CSA2_F32   ? go(reinterpret_cast<float*>(out))
