@@ -42,11 +42,12 @@ namespace csa2 {
 
 constexpr int TR_TILE = 128;                         // keys per tile, 64 of each CTA
 constexpr int TR_ROWS = 128;                         // rows of an item, 64 of each CTA
-constexpr int TR_THREADS = 640;
+constexpr int TR_THREADS = 768;
 constexpr int TR_SMW = 8, TR_SMT = TR_SMW * 32;      // warps 0-7: queries, softmax, epilogue
 constexpr int TR_MMA1 = 8;                           // warps 8, 9 of CTA 0: score MMAs of dims 0-255 and 256-511
-constexpr int TR_MMA2 = 10;                          // warps 10, 11 of CTA 0: value MMAs of dims 0-255 and 256-511
-constexpr int TR_LOADW = 12, TR_LOADERS = 256;       // warps 12-19: rows
+constexpr int TR_MMA2 = 10;                          // warp 10 of CTA 0: value MMAs
+constexpr int TR_OWNW = 12, TR_OWN = 256;            // warps 12-19: a CTA's own keys
+constexpr int TR_FORW = 20, TR_FOR = 128;            // warps 20-23: the other CTA's keys, this CTA's dims
 constexpr uint32_t TR_SLAB = 64 * 128;               // 64 rows or keys x 64 fp16, 128-byte swizzle
 constexpr uint32_t TR_SQ = 0;                        // Q: 8 slabs
 constexpr uint32_t TR_SL = 8 * TR_SLAB;              // L: 2 buffers x 8 slabs
@@ -62,6 +63,19 @@ constexpr int TR_PAIRS = 76;                         // pairs of CTAs at most: o
 constexpr int TR_OVER = 1;                           // units of an item beside its tiles: its queries and its epilogue
 
 __device__ __forceinline__ uint32_t tr_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+// (d0, d1) += (a0, a1), one packed instruction
+__device__ __forceinline__ void add2_rn(float& d0, float& d1, float a0, float a1) {
+    asm("{\n .reg .b64 ra, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rd, {%0, %1};\n add.rn.f32x2 rd, rd, ra;\n"
+        " mov.b64 {%0, %1}, rd;\n}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // what the nodes of a sequence attend to, all together
 struct TreeSeq {
@@ -204,30 +218,30 @@ __global__ void __launch_bounds__(1024) k_tree_prep(const __grid_constant__ Tree
     }
 }
 
-// Where a pair stands in its part of all units, and the share that comes next
+// Where a pair stands in its part of all units, and the share that comes next.  (32 bits: a cache that fills the memory has
+// 7.6 million tiles of entries, times 128 items a sequence.)
 struct TreeCursor {
-    int64_t u, u1, off;          // the next unit, the end of the part, the unit's place among its sequence's
-    int b;
+    int left, off, b;            // units left, the next one's place among its sequence's
 };
 struct TreeShare {
-    TreeSeq s;
-    int b, rt, t0, t1, T;        // tiles t0 .. t1-1 of the item's T
+    int b, rt, t0, t1, T, wt;    // tiles t0 .. t1-1 of the item's T, of which the first wt are window rows and drafts
 };
 __device__ __forceinline__ bool tr_next(const TreeArgs& a, TreeCursor& c, TreeShare& h) {
-    while (c.u < c.u1) {
-        h.s = a.seq[c.b];
-        h.T = h.s.tiles();
+    while (c.left > 0) {
+        const TreeSeq* s = a.seq + c.b;
+        h.wt = s->wtiles();
+        h.T = s->tiles();
         const int per = h.T + TR_OVER;
-        if (c.off >= (int64_t)h.s.row_tiles * per) {
+        if (c.off >= s->row_tiles * per) {
             ++c.b, c.off = 0;
             continue;
         }
         h.b = c.b;
-        h.rt = (int)(c.off / per);
-        h.t0 = (int)(c.off - (int64_t)h.rt * per);
-        const int n = (int)min((int64_t)(per - h.t0), c.u1 - c.u);
+        h.rt = (int)((unsigned)c.off / (unsigned)per);
+        h.t0 = c.off - h.rt * per;
+        const int n = min(per - h.t0, c.left);
         h.t1 = min(h.t0 + n, h.T);
-        c.u += n, c.off += n;
+        c.left -= n, c.off += n;
         if (h.t1 > h.t0) return true;
     }
     return false;
@@ -237,13 +251,15 @@ template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tree_attn(const __grid_constant__ TreeArgs a) {
     extern __shared__ uint8_t dyn[];
     // in CTA 0, counting warps of both CTAs: dims 0-255 of a tile's keys ready, all of them, the other CTA's keys ready, the
-    // scores read, P written, the queries staged.  In each CTA, arrived on by the MMAs: scores done, values done
-    __shared__ __align__(8) unsigned long long b_half[2], b_full[2], b_for[2], b_sfree[2], b_pfull[2], b_q, b_sfull[2], b_odone[2];
+    // scores read, P written, the queries staged.  In each CTA, arrived on by the MMAs: scores done, values of dims 0-255
+    // done (their places are free), all values done
+    __shared__ __align__(8) unsigned long long b_half[2], b_full[2], b_for[2], b_sfree[2], b_pfull[2], b_q, b_sfull[2], b_ohalf[2],
+        b_odone[2];
     __shared__ uint32_t tmem_base;
     __shared__ float red[4][64];
     __shared__ int qexp[64];
-    __shared__ int64_t wsum[TR_THREADS / 32], start_off;
-    __shared__ int start_b;
+    __shared__ int64_t wsum[TR_THREADS / 32];
+    __shared__ int start_b, start_off, part_each, part_more;
     const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
     uint8_t* sm = dyn + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -252,19 +268,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
     auto sa = [&](const void* x) { return umma::smem_u32(x); };
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(sa(&b_half[i]), 2 * TR_LOADERS / 32);
-            umma::mbar_init(sa(&b_full[i]), 2 * TR_LOADERS / 32);
-            umma::mbar_init(sa(&b_for[i]), 2 * TR_LOADERS / 32);
+            umma::mbar_init(sa(&b_half[i]), 2 * TR_OWN / 32);
+            umma::mbar_init(sa(&b_full[i]), 2 * TR_OWN / 32);
+            umma::mbar_init(sa(&b_for[i]), 2 * TR_FOR / 32);
             umma::mbar_init(sa(&b_sfree[i]), 2 * TR_SMW);
             umma::mbar_init(sa(&b_pfull[i]), 2 * TR_SMW);
             umma::mbar_init(sa(&b_sfull[i]), 2);
-            umma::mbar_init(sa(&b_odone[i]), 2);
+            umma::mbar_init(sa(&b_ohalf[i]), 1);
+            umma::mbar_init(sa(&b_odone[i]), 1);
         }
         umma::mbar_init(sa(&b_q), 2 * TR_SMW);
         umma::fence_mbar_init();
         start_b = 0, start_off = 0;
     }
-    if (warp == TR_LOADW - 1) umma::tmem_alloc_pair(sa(&tmem_base), TRT_COLS);
+    if (warp == TR_OWNW - 1) umma::tmem_alloc_pair(sa(&tmem_base), TRT_COLS);
     pdl_wait();
     pdl_launch_next();
 
@@ -294,20 +311,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
     // total % pairs of the parts have one unit more than the others, and come first
     const int64_t each = total < 0x7fffffff ? (int64_t)((unsigned)total / (unsigned)pairs) : total / pairs;
     const int64_t more = total - each * pairs;
-    auto start_of = [&](int i) { return each * i + min((int64_t)i, more); };
-    auto part_of = [&](int64_t u) {                  // the pair that has unit u
-        const int64_t longer = (each + 1) * more;
-        return u < longer ? (int)(u / (each + 1)) : (int)(more + (u - longer) / each);
-    };
-    const int64_t u0 = start_of(pair), u1 = start_of(pair + 1);
-    if (rank == 0 && tid == 0) a.heads[pair] = TreeHead{0, 0, 0, 0};
+    const int64_t u0 = each * pair + min((int64_t)pair, more);
+    const int n_units = (int)each + (pair < more ? 1 : 0);
+    if (tid == 0) {
+        part_each = (int)each, part_more = (int)more;
+        if (rank == 0) a.heads[pair] = TreeHead{0, 0, 0, 0};
+    }
     {
         int64_t s = upto - mine;
-        if (u0 < u1 && s <= u0 && u0 < upto)
+        if (n_units > 0 && s <= u0 && u0 < upto)
             for (int b = b0; b < b1; ++b) {
                 const int64_t n = units(b);
                 if (u0 < s + n) {
-                    start_b = b, start_off = u0 - s;
+                    start_b = b, start_off = (int)(u0 - s);
                     break;
                 }
                 s += n;
@@ -316,169 +332,149 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
     __syncthreads();
     umma::cluster_sync();        // the other CTA's barriers are there
     const uint32_t tmem = tmem_base;
-    TreeCursor cur{u0, u1, start_off, start_b};
-    TreeShare h;
+    TreeCursor cur{n_units, start_off, start_b};
+    TreeShare h{};
     bool ok = true;
     uint32_t tb = 0;                                 // tiles done so far: the rings go on from share to share
 
-    if (warp >= TR_LOADW) {
-        // ================= rows.  A tile's own keys as soon as its buffer is free, the other CTA's keys' dims once its
-        // scores are done; each warp takes whichever is ready, the latter first.
-        const int lt = tid - TR_LOADW * 32, lw = warp - TR_LOADW;
-        const uint32_t r_half[2] = {umma::mapa(sa(&b_half[0]), 0), umma::mapa(sa(&b_half[1]), 0)};
-        const uint32_t r_full[2] = {umma::mapa(sa(&b_full[0]), 0), umma::mapa(sa(&b_full[1]), 0)};
-        const uint32_t r_for[2] = {umma::mapa(sa(&b_for[0]), 0), umma::mapa(sa(&b_for[1]), 0)};
-        auto arrive = [&](uint32_t bar) {
+    if (warp >= TR_OWNW) {
+        // ================= rows.  A unit is 32 dims of a key: 16 bytes of codes, 2 of scales.
+        auto load = [&](const uint8_t* codes, const uint8_t* scales, int j, int n, int c, uint4& w, uint32_t& s) {
+            w = make_uint4(0u, 0u, 0u, 0u), s = 0u;              // keys past the end expand to zeros
+            if (j < n) {
+                w = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)j * (D_LAT / 2)) + c);
+                s = __ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)j * (D_LAT / 16)) + c);
+            }
+        };
+        auto expand = [&](uint8_t* L, int r, int c, int flip, const uint4& w, uint32_t s) {
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+            const __half2 sp = e4m3x2_to_f16x2(s);
+            const __half2 s_lo = __low2half2(sp), s_hi = __high2half2(sp);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int cc = 4 * c + k;
+                *reinterpret_cast<uint4*>(L + ((cc >> 3) ^ flip) * TR_SLAB + tr_swz(r, cc & 7)) =
+                    e2m1x8_scaled(words[k], (k >> 1) ? s_hi : s_lo);
+            }
+        };
+        // row v of the window rows and drafts, 8 dims at chunk cc
+        auto bf16_row = [&](int v, int cc) {
+            const TreeSeq* s = a.seq + h.b;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            const int j = v - s->nw;
+            if (j < 0)
+                x = *reinterpret_cast<const uint4*>(a.swa + ((int64_t)h.b * a.swa_len + s->w0 + v) * D_LAT + 8 * cc);
+            else if (v < s->n_rows && ((s->there[j >> 5] >> (j & 31)) & 1u))
+                x = *reinterpret_cast<const uint4*>(a.draft + ((int64_t)h.b * a.n_q + j) * D_LAT + 8 * cc);
+            return bf16x8_to_f16x8(x, pow2f(-s->exp));
+        };
+        // each thread orders its own writes for the tensor core, then one arrival per warp, in CTA 0
+        auto arrive = [&](unsigned long long* bar) {
             umma::fence_proxy_async();
             __syncwarp();
-            if (lane == 0) umma::mbar_arrive_remote(bar);
+            if (lane == 0) umma::mbar_arrive_pair(umma::mapa(sa(bar), 0));
         };
-        while (tr_next(a, cur, h)) {
-            const int T = h.t1 - h.t0, wt = h.s.wtiles(), n_vis = h.s.n_vis;
-            const uint8_t* codes = a.codes + (int64_t)h.b * a.capacity * (D_LAT / 2);
-            const uint8_t* scales = a.scales + (int64_t)h.b * a.capacity * (D_LAT / 16);
-            const float down = pow2f(-h.s.exp);
-            // a unit is 32 dims of a key (16 bytes of codes, 2 of scales).  Own keys: a warp takes 4 keys x 8 units, whole
-            // 128-byte lines of codes; units below 512 are dims 0-255.  The other's: 4 keys x the 8 units of this CTA's dims
-            const int kr = lane & 3, ku = lane >> 2;
-            auto own_rc = [&](int i, int& r, int& c) {
-                const int qq = lw + 8 * i;
-                r = 4 * (qq & 15) + kr;
-                c = 8 * (qq >> 4) + ku;
-            };
-            auto for_rc = [&](int i, int& r, int& c) {
-                r = 4 * (lw + 8 * i) + kr;
-                c = 8 * (ku >> 2) + 4 * (int)rank + (ku & 3);
-            };
-            uint4 cw[4], fw[2];
-            uint32_t sc[4], fs[2];
-            auto load = [&](int tile, uint32_t side, int r, int c, uint4& w, uint32_t& s) {
-                const int j = tile * TR_TILE + 64 * (int)side + r;
-                w = make_uint4(0u, 0u, 0u, 0u), s = 0u;          // keys past the end expand to zeros
-                if (j < n_vis) {
-                    w = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)j * (D_LAT / 2)) + c);
-                    s = __ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)j * (D_LAT / 16)) + c);
-                }
-            };
-            auto expand = [&](uint8_t* L, int r, int c, int flip, const uint4& w, uint32_t s) {
-                const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-                const __half2 sp = e4m3x2_to_f16x2(s);
-                const __half2 s_lo = __low2half2(sp), s_hi = __high2half2(sp);
+        const int kr = lane & 3, ku = lane >> 2;
+        if (warp < TR_FORW) {
+            // ---- this CTA's 64 keys of every tile, dims 0-255 first.  A warp takes 4 keys x 8 units at a time: whole 128-byte
+            // lines of codes, and the 8 threads of a quarter warp write different bank groups
+            const int lt = tid - TR_OWNW * 32, lw = warp - TR_OWNW;
+            while (tr_next(a, cur, h)) {
+                const int T = h.t1 - h.t0, wt = h.wt, n_vis = a.seq[h.b].n_vis;
+                const uint8_t* codes = a.codes + (int64_t)h.b * a.capacity * (D_LAT / 2);
+                const uint8_t* scales = a.scales + (int64_t)h.b * a.capacity * (D_LAT / 16);
+                uint4 cw[4];
+                uint32_t sc[4];
+                auto fetch = [&](int t) {            // units 0, 1: dims 0-255, keys 4 lw .. and 32 + 4 lw ..; units 2, 3: the rest
+                    const int j0 = (h.t0 + t - wt) * TR_TILE + 64 * (int)rank + 4 * lw + kr;
+                    if (t < T && h.t0 + t >= wt)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int cc = 4 * c + k;
-                    *reinterpret_cast<uint4*>(L + ((cc >> 3) ^ flip) * TR_SLAB + tr_swz(r, cc & 7)) =
-                        e2m1x8_scaled(words[k], (k >> 1) ? s_hi : s_lo);
-                }
-            };
-            // row v of the window rows and drafts, 8 dims at chunk cc
-            auto bf16_row = [&](int v, int cc) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                const int j = v - h.s.nw;
-                if (j < 0)
-                    x = *reinterpret_cast<const uint4*>(a.swa + ((int64_t)h.b * a.swa_len + h.s.w0 + v) * D_LAT + 8 * cc);
-                else if (v < h.s.n_rows && ((h.s.there[j >> 5] >> (j & 31)) & 1u))
-                    x = *reinterpret_cast<const uint4*>(a.draft + ((int64_t)h.b * a.n_q + j) * D_LAT + 8 * cc);
-                return bf16x8_to_f16x8(x, down);
-            };
-            auto fetch_own = [&](int t) {
-                if (t < T && h.t0 + t >= wt)
+                        for (int i = 0; i < 4; ++i) load(codes, scales, j0 + 32 * (i & 1), n_vis, 8 * (i >> 1) + ku, cw[i], sc[i]);
+                };
+                fetch(0);
+                for (int t = 0; t < T; ++t) {
+                    const uint32_t tg = tb + t, buf = tg & 1, before = ((tg >> 1) - 1) & 1;
+                    uint8_t* L = sm + TR_SL + buf * TR_LBUF;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        int r, c;
-                        own_rc(i, r, c);
-                        load(h.t0 + t - wt, rank, r, c, cw[i], sc[i]);
-                    }
-            };
-            auto fetch_for = [&](int t) {
-                if (t < T && h.t0 + t >= wt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        int r, c;
-                        for_rc(i, r, c);
-                        load(h.t0 + t - wt, rank ^ 1u, r, c, fw[i], fs[i]);
-                    }
-            };
-            fetch_own(0);
-            fetch_for(0);
-            int own = 0, fo = 0;
-            uint32_t polls = 0;
-            while (ok && fo < T) {
-                const uint32_t go = tb + own, gf = tb + fo;
-                const bool fready = fo < own && umma::mbar_test(sa(&b_sfull[gf & 1]), (gf >> 1) & 1);
-                const bool oready = !fready && own < T && (go < 2 || umma::mbar_test(sa(&b_odone[go & 1]), ((go >> 1) - 1) & 1));
-                if (__any_sync(0xffffffffu, fready)) {
-                    uint8_t* L = sm + TR_SL + (gf & 1) * TR_LBUF;
-                    if (h.t0 + fo < wt) {
-                        const int v0 = (h.t0 + fo) * TR_TILE + 64 * (int)(rank ^ 1u);
+                    for (int half = 0; half < 2; ++half) {
+                        if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(half == 0 ? &b_ohalf[buf] : &b_odone[buf]), before);
+                        if (h.t0 + t < wt) {
+                            const int v0 = (h.t0 + t) * TR_TILE + 64 * (int)rank;
 #pragma unroll 4
-                        for (int i = lt; i < 64 * 32; i += TR_LOADERS) {
+                            for (int i = lt; i < 64 * 32; i += TR_OWN) {
+                                const int r = i >> 5, cc = 32 * half + (i & 31);
+                                *reinterpret_cast<uint4*>(L + (cc >> 3) * TR_SLAB + tr_swz(r, cc & 7)) = bf16_row(v0 + r, cc);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 2 * half; i < 2 * half + 2; ++i)
+                                expand(L, 32 * (i & 1) + 4 * lw + kr, 8 * half + ku, 0, cw[i], sc[i]);
+                        }
+                        arrive(half == 0 ? &b_half[buf] : &b_full[buf]);
+                    }
+                    fetch(t + 1);
+                }
+                tb += T;
+            }
+        } else {
+            // ---- the other CTA's 64 keys, this CTA's 256 dims, over the dims of its own keys that only the scores needed
+            const int lt = tid - TR_FORW * 32, lw = warp - TR_FORW;
+            const int c = 8 * (ku >> 2) + 4 * (int)rank + (ku & 3);
+            while (tr_next(a, cur, h)) {
+                const int T = h.t1 - h.t0, wt = h.wt, n_vis = a.seq[h.b].n_vis;
+                const uint8_t* codes = a.codes + (int64_t)h.b * a.capacity * (D_LAT / 2);
+                const uint8_t* scales = a.scales + (int64_t)h.b * a.capacity * (D_LAT / 16);
+                uint4 cw[4];
+                uint32_t sc[4];
+                auto fetch = [&](int t) {
+                    const int j0 = (h.t0 + t - wt) * TR_TILE + 64 * (int)(rank ^ 1u) + 4 * lw + kr;
+                    if (t < T && h.t0 + t >= wt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) load(codes, scales, j0 + 16 * i, n_vis, c, cw[i], sc[i]);
+                };
+                fetch(0);
+                for (int t = 0; t < T; ++t) {
+                    const uint32_t tg = tb + t, buf = tg & 1;
+                    uint8_t* L = sm + TR_SL + buf * TR_LBUF;
+                    ok = ok && umma::mbar_wait_fast(sa(&b_sfull[buf]), (tg >> 1) & 1);
+                    if (h.t0 + t < wt) {
+                        const int v0 = (h.t0 + t) * TR_TILE + 64 * (int)(rank ^ 1u);
+#pragma unroll 4
+                        for (int i = lt; i < 64 * 32; i += TR_FOR) {
                             const int r = i >> 5, cs = i & 31;       // this CTA's 32 chunks: 16 of dims 128 r .., 16 of 256 + 128 r ..
                             const int cc = 32 * (cs >> 4) + 16 * (int)rank + (cs & 15);
                             *reinterpret_cast<uint4*>(L + ((cc >> 3) ^ 2) * TR_SLAB + tr_swz(r, cc & 7)) = bf16_row(v0 + r, cc);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            int r, c;
-                            for_rc(i, r, c);
-                            expand(L, r, c, 2, fw[i], fs[i]);
-                        }
+                        for (int i = 0; i < 4; ++i) expand(L, 16 * i + 4 * lw + kr, c, 2, cw[i], sc[i]);
                     }
-                    arrive(r_for[gf & 1]);
-                    ++fo;
-                    fetch_for(fo);
-                    polls = 0;
-                } else if (__any_sync(0xffffffffu, oready)) {
-                    uint8_t* L = sm + TR_SL + (go & 1) * TR_LBUF;
-                    if (h.t0 + own < wt) {
-                        const int v0 = (h.t0 + own) * TR_TILE + 64 * (int)rank;
-#pragma unroll 4
-                        for (int i = lt; i < 64 * 64; i += TR_LOADERS) {
-                            const int r = i >> 6, cc = i & 63;
-                            *reinterpret_cast<uint4*>(L + (cc >> 3) * TR_SLAB + tr_swz(r, cc & 7)) = bf16_row(v0 + r, cc);
-                        }
-                        arrive(r_half[go & 1]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            int r, c;
-                            own_rc(i, r, c);
-                            if (i == 2) arrive(r_half[go & 1]);       // dims 0-255 are done
-                            expand(L, r, c, 0, cw[i], sc[i]);
-                        }
-                    }
-                    arrive(r_full[go & 1]);
-                    ++own;
-                    fetch_own(own);
-                    polls = 0;
-                } else if (++polls > (1u << 24)) {
-                    ok = false;
+                    arrive(&b_for[buf]);
+                    fetch(t + 1);
                 }
-                __syncwarp();
+                tb += T;
             }
-            tb += T;
         }
     } else if (warp >= TR_MMA1 && rank == 0) {
         // ================= MMAs of the pair.  The whole warp walks the tiles, so that descriptors and addresses stay in
         // uniform registers; one elected lane issues.
         const bool scores = warp < TR_MMA2;
-        const int half = (warp - TR_MMA1) & 1;
+        const int part = warp - TR_MMA1;             // of the scores' dims
         const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
         const uint32_t id = scores ? umma::idesc_f16(128, 128, 0, 0) : umma::idesc_f16(128, 256, 0, 1);
         const uint64_t qd = umma::desc(base + TR_SQ, 16, 1024, umma::LAYOUT_SW128);
         uint32_t k = 0;
-        while (ok && tr_next(a, cur, h)) {
+        while (ok && warp <= TR_MMA2 && tr_next(a, cur, h)) {
             const int T = h.t1 - h.t0;
-            if (scores) ok = umma::mbar_wait_cluster(sa(&b_q), k & 1);
+            if (scores) ok = umma::mbar_wait_fast(sa(&b_q), k & 1);
             for (int t = 0; t < T; ++t) {
                 const uint32_t tg = tb + t, buf = tg & 1, ph = (tg >> 1) & 1;
                 if (scores) {
-                    ok = ok && umma::mbar_wait_cluster(sa(half == 0 ? &b_half[buf] : &b_full[buf]), ph);
-                    if (tg >= 2) ok = ok && umma::mbar_wait_cluster(sa(&b_sfree[buf]), ph ^ 1);
+                    ok = ok && umma::mbar_wait_fast(sa(part == 0 ? &b_half[buf] : &b_full[buf]), ph);
+                    if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_sfree[buf]), ph ^ 1);
                 } else {
-                    ok = ok && umma::mbar_wait_cluster(sa(&b_for[buf]), ph);
-                    ok = ok && umma::mbar_wait_cluster(sa(&b_pfull[buf]), ph);
+                    ok = ok && umma::mbar_wait_fast(sa(&b_for[buf]), ph);
+                    ok = ok && umma::mbar_wait_fast(sa(&b_pfull[buf]), ph);
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -488,21 +484,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                         const uint64_t ld = umma::desc(base + TR_SL + buf * TR_LBUF, 16, 1024, umma::LAYOUT_SW128);
 #pragma unroll
                         for (int kk = 0; kk < 16; ++kk) {
-                            const int ks = 16 * half + kk;
+                            const int ks = 16 * part + kk;
                             const uint64_t off = (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4);
-                            umma::mma_f16_pair(tm + TRT_S + 64 * (2 * buf + half), qd + off, ld + off, id, kk > 0);
+                            umma::mma_f16_pair(tm + TRT_S + 64 * (2 * buf + part), qd + off, ld + off, id, kk > 0);
                         }
                         umma::commit_pair(sa(&b_sfull[buf]));
                     } else {
-                        // keys 0-63 (CTA 0's) in places 4 half, 4 half + 1, keys 64-127 in the two after them
-                        const uint64_t vd = umma::desc(base + TR_SL + buf * TR_LBUF + 4 * half * TR_SLAB, TR_SLAB, 1024, umma::LAYOUT_SW128);
+                        // dims 0-255 first.  Keys 0-63 (CTA 0's) in places 4 n, 4 n + 1, keys 64-127 in the two after them
                         const uint64_t pd = umma::desc(base + TR_SP + buf * TR_PBUF, 16, 1024, umma::LAYOUT_SW128);
+                        const uint64_t vd = umma::desc(base + TR_SL + buf * TR_LBUF, TR_SLAB, 1024, umma::LAYOUT_SW128);
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            umma::mma_f16_pair(tm + TRT_O + 128 * half, pd + (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4),
-                                               vd + (uint64_t)((2 * (ks >> 2) * TR_SLAB + (ks & 3) * 2048) >> 4), id,
-                                               (t > 0 || ks > 0) ? 1u : 0u);
-                        umma::commit_pair(sa(&b_odone[buf]));
+                        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks)
+                                umma::mma_f16_pair(tm + TRT_O + 128 * n, pd + (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4),
+                                                   vd + (uint64_t)(((4 * n + 2 * (ks >> 2)) * TR_SLAB + (ks & 3) * 2048) >> 4), id,
+                                                   (t > 0 || ks > 0) ? 1u : 0u);
+                            umma::commit_pair(sa(n == 0 ? &b_ohalf[buf] : &b_odone[buf]));
+                        }
                     }
                 }
                 __syncwarp();
@@ -520,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
         const uint32_t r_pfull[2] = {umma::mapa(sa(&b_pfull[0]), 0), umma::mapa(sa(&b_pfull[1]), 0)};
         bool first_share = true;
         while (tr_next(a, cur, h)) {
-            const int T = h.t1 - h.t0, wt = h.s.wtiles();
+            const int T = h.t1 - h.t0, wt = h.wt;
             const int n_rows_q = a.n_q * a.n_heads, q0 = h.rt * TR_ROWS + 64 * (int)rank;
             // ---- Q: this CTA's 64 rows, bf16 -> fp16 slabs; a row whose largest magnitude lies outside [2^-10, 2^15) is
             // scaled by a power of two on the way.  (S of the share before is done: its values were.)
@@ -539,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     for (int i = 0; i < 4; ++i) {
                         const int r = r0 + TR_SMW * i;
                         const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
-                        const float d = pow2f(-e);
+                        const float d = a.scale_log2e < 0.0f ? -pow2f(-e) : pow2f(-e);       // scores are taken times |scale|
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
                             const int c = lane + 32 * hh;
@@ -550,10 +549,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 }
                 umma::fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) umma::mbar_arrive_remote(r_q);
-                umma::bar_named(1, TR_SMT);
+                if (lane == 0) umma::mbar_arrive_pair(r_q);
+                umma::bar_named(3, TR_SMT);
             }
-            const float mul4 = a.scale_log2e * pow2f(qexp[row]), up = pow2f(h.s.exp);
+            // never zero, so that a masked score stays -inf (a score of nearly nothing for a scale of nothing)
+            const float mul4 = fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[row]), 0x1p-100f), up = pow2f(a.seq[h.b].exp);
             int vis = 0;
             const uint32_t* mask = nullptr;
             if (q0 + row < n_rows_q) {
@@ -583,26 +583,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     umma::tmem_ld16(lane_base + TRT_S + 64 * (2 * buf + 1) + 32 * ch + 16 * i, x1);
                     umma::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[16 * i + j] += x1[j];
+                    for (int j = 0; j < 16; j += 2) add2_rn(x[16 * i + j], x[16 * i + j + 1], x1[j], x1[j + 1]);
                 }
                 umma::fence_before();
                 __syncwarp();
-                if (lane == 0) umma::mbar_arrive_remote(r_sfree[buf]);
+                if (lane == 0) umma::mbar_arrive_pair(r_sfree[buf]);
                 const float mul = window ? mul4 * up : mul4;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= mul;
                 if (see != 0xffffffffu)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (!((see >> i) & 1u)) x[i] = -INFINITY;
-                float mx = x[0];
+                float mx = max3(x[0], x[1], x[2]);
 #pragma unroll
-                for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
+                for (int i = 3; i < 31; i += 2) mx = max3(mx, x[i], x[i + 1]);
+                mx = fmaxf(mx, x[31]) * mul;
                 // the window tiles' part of O carries 2^-exp: it is brought to the common scale before the entries' is added
-                const bool rescale_window = !window && tile == wt && t > 0 && h.s.exp != 0;
-                if (umma::bar_red_or(1, TR_SMT, mx - m > TR_TOP || (m == -INFINITY && mx > -INFINITY)) || rescale_window) {
+                const bool rescale_window = !window && tile == wt && t > 0 && up != 1.0f;
+                if (umma::bar_red_or(1 + (qd & 1), TR_SMT / 2, mx - m > TR_TOP) || rescale_window) {
                     red[2 * kh + ch][row] = mx;
-                    umma::bar_named(1, TR_SMT);
+                    umma::bar_named(1 + (qd & 1), TR_SMT / 2);
                     const float mt = fmaxf(fmaxf(red[0][row], red[1][row]), fmaxf(red[2][row], red[3][row]));
                     float f = 1.0f;
                     if (mt > -INFINITY && (m == -INFINITY || mt - m > TR_TOP)) {
@@ -627,31 +626,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                             umma::tmem_wait_st();
                         }
                     }
-                    umma::bar_named(1, TR_SMT);      // red is read
+                    umma::bar_named(1 + (qd & 1), TR_SMT / 2);        // red is read
                 }
                 if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf]), ph ^ 1);          // the P buffer is free
-                const float ref = m == -INFINITY ? 0.0f : m;
-                float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    x[i] = umma::ex2_ftz(x[i] - ref);
-                    sum[i & 1] += x[i];
-                }
-                lsum += sum[0] + sum[1];
+                const float ref = m == -INFINITY ? 0.0f : -m;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 uint8_t* P = sm + TR_SP + buf * TR_PBUF + kh * TR_SLAB;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint4*>(P + tr_swz(row, 4 * ch + c)) =
-                        make_uint4(f16x2_bits(x[8 * c], x[8 * c + 1]), f16x2_bits(x[8 * c + 2], x[8 * c + 3]),
-                                   f16x2_bits(x[8 * c + 4], x[8 * c + 5]), f16x2_bits(x[8 * c + 6], x[8 * c + 7]));
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float d0 = ref, d1 = ref;
+                        fma2_rn(d0, d1, x[8 * c + 2 * i], x[8 * c + 2 * i + 1], mul, mul);
+                        d0 = umma::ex2_ftz(d0), d1 = umma::ex2_ftz(d1);
+                        add2_rn(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], d0, d1);
+                        w[i] = f16x2_bits(d0, d1);
+                    }
+                    *reinterpret_cast<uint4*>(P + tr_swz(row, 4 * ch + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                lsum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 umma::fence_proxy_async();
                 umma::fence_before();
                 __syncwarp();
-                if (lane == 0) umma::mbar_arrive_remote(r_pfull[buf]);
+                if (lane == 0) umma::mbar_arrive_pair(r_pfull[buf]);
             }
             // ---- the share's end: the row's sum over its four threads, then O
             red[2 * kh + ch][row] = lsum;
-            umma::bar_named(1, TR_SMT);
+            umma::bar_named(3, TR_SMT);
             const float l = (red[0][row] + red[1][row]) + (red[2][row] + red[3][row]);
             const uint32_t tl = tb + T - 1;
             ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
@@ -690,12 +692,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     a.lse[gr] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             }
             // an item that begins here and goes on in other pairs is joined from their shares
-            if (!whole && h.t0 == 0 && rank == 0 && tid == 0)
-                a.heads[pair] = TreeHead{h.b, h.rt, slot, part_of(cur.u - 1 + (h.T - h.t1)) - pair + 1};
+            if (!whole && h.t0 == 0 && rank == 0 && tid == 0) {
+                int n = 1;
+                for (int rest = h.T - h.t1; rest > 0; ++n) rest -= part_each + (pair + n < part_more ? 1 : 0);
+                a.heads[pair] = TreeHead{h.b, h.rt, slot, n};
+            }
             first_share = false;
             tb += T;
             umma::fence_before();
-            umma::bar_named(1, TR_SMT);              // red, qexp and O are read
+            umma::bar_named(3, TR_SMT);              // red, qexp and O are read
             umma::fence_after();
         }
     }
@@ -703,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
     umma::fence_before();
     __syncthreads();
     umma::cluster_sync();
-    if (warp == TR_LOADW - 1) {
+    if (warp == TR_OWNW - 1) {
         umma::fence_after();
         umma::tmem_dealloc_pair(tmem, TRT_COLS);
     }

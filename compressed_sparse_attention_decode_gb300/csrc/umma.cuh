@@ -122,6 +122,12 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t remote_mbar) {
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t remote_mbar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_mbar) : "memory");
 }
+// arrive on an mbarrier of the pair's even CTA for shared-memory writes of this CTA that its tensor core is to read: they are
+// ordered by the writers' own proxy fences, so nothing wider than this CTA is waited for (release at cluster scope waits for
+// every access of the thread, and acquire there empties the L1 cache)
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t remote_mbar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(remote_mbar) : "memory");
+}
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
                  : "memory");
