@@ -44,8 +44,7 @@ constexpr int TR_TILE = 128;                         // keys per tile, 64 of eac
 constexpr int TR_ROWS = 128;                         // rows of an item, 64 of each CTA
 constexpr int TR_THREADS = 768;
 constexpr int TR_SMW = 8, TR_SMT = TR_SMW * 32;      // warps 0-7: queries, softmax, epilogue
-constexpr int TR_MMA1 = 8;                           // warps 8, 9 of CTA 0: score MMAs of dims 0-255 and 256-511
-constexpr int TR_MMA2 = 10;                          // warp 10 of CTA 0: value MMAs
+constexpr int TR_MMA1 = 8, TR_MMA2 = 9;              // warps 8 and 9 of CTA 0: score MMAs, value MMAs
 constexpr int TR_OWNW = 12, TR_OWN = 256;            // warps 12-19: a CTA's own keys
 constexpr int TR_FORW = 20, TR_FOR = 128;            // warps 20-23: the other CTA's keys, this CTA's dims
 constexpr uint32_t TR_SLAB = 64 * 128;               // 64 rows or keys x 64 fp16, 128-byte swizzle
@@ -55,7 +54,7 @@ constexpr uint32_t TR_LBUF = 8 * TR_SLAB;
 constexpr uint32_t TR_SP = TR_SL + 2 * TR_LBUF;      // P: 2 buffers x 2 slabs (64 keys each)
 constexpr uint32_t TR_PBUF = 2 * TR_SLAB;
 constexpr uint32_t TR_DYN = TR_SP + 2 * TR_PBUF + 1024;                  // + alignment
-constexpr uint32_t TRT_S = 0, TRT_O = 256, TRT_COLS = 512;               // S partial p of buffer b at TRT_S + 64 (2b + p)
+constexpr uint32_t TRT_S = 0, TRT_O = 256, TRT_COLS = 512;               // S of buffer b at TRT_S + 64 b
 // weights are 2^(score - m), m set TR_UP below the largest score and raised when one is more than TR_TOP above it: the
 // largest weight lies in [2^7, 2^15], within fp16's range, and what fp16 rounds to zero is below 2^-32 of it
 constexpr float TR_UP = 7.0f, TR_TOP = 15.0f;
@@ -250,13 +249,12 @@ __device__ __forceinline__ bool tr_next(const TreeArgs& a, TreeCursor& c, TreeSh
 template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tree_attn(const __grid_constant__ TreeArgs a) {
     extern __shared__ uint8_t dyn[];
-    // in CTA 0, counting warps of both CTAs: dims 0-255 of a tile's keys ready, all of them, the other CTA's keys ready, the
-    // scores read, P written, the queries staged.  In each CTA, arrived on by the MMAs: scores done, values of dims 0-255
+    // in CTA 0, counting warps of both CTAs: dims 0-255 of a tile's keys ready, all of them, the other CTA's keys ready, P
+    // written, the queries staged.  In each CTA, arrived on by the MMAs: scores done, values of dims 0-255
     // done (their places are free), all values done
-    __shared__ __align__(8) unsigned long long b_half[2], b_full[2], b_for[2], b_sfree[2], b_pfull[2], b_q, b_sfull[2], b_ohalf[2],
+    __shared__ __align__(8) unsigned long long b_half[2], b_full[2], b_for[2], b_pfull[2], b_q, b_sfull[2], b_ohalf[2],
         b_odone[2];
     __shared__ uint32_t tmem_base;
-    __shared__ float red[4][64];
     __shared__ int qexp[64];
     __shared__ int64_t wsum[TR_THREADS / 32];
     __shared__ int start_b, start_off, part_each, part_more;
@@ -271,9 +269,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             umma::mbar_init(sa(&b_half[i]), 2 * TR_OWN / 32);
             umma::mbar_init(sa(&b_full[i]), 2 * TR_OWN / 32);
             umma::mbar_init(sa(&b_for[i]), 2 * TR_FOR / 32);
-            umma::mbar_init(sa(&b_sfree[i]), 2 * TR_SMW);
             umma::mbar_init(sa(&b_pfull[i]), 2 * TR_SMW);
-            umma::mbar_init(sa(&b_sfull[i]), 2);
+            umma::mbar_init(sa(&b_sfull[i]), 1);
             umma::mbar_init(sa(&b_ohalf[i]), 1);
             umma::mbar_init(sa(&b_odone[i]), 1);
         }
@@ -458,39 +455,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
     } else if (warp >= TR_MMA1 && rank == 0) {
         // ================= MMAs of the pair.  The whole warp walks the tiles, so that descriptors and addresses stay in
         // uniform registers; one elected lane issues.
-        const bool scores = warp < TR_MMA2;
-        const int part = warp - TR_MMA1;             // of the scores' dims
         const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
-        const uint32_t id = scores ? umma::idesc_f16(128, 128, 0, 0) : umma::idesc_f16(128, 256, 0, 1);
-        const uint64_t qd = umma::desc(base + TR_SQ, 16, 1024, umma::LAYOUT_SW128);
-        uint32_t k = 0;
-        while (ok && warp <= TR_MMA2 && tr_next(a, cur, h)) {
-            const int T = h.t1 - h.t0;
-            if (scores) ok = umma::mbar_wait_fast(sa(&b_q), k & 1);
-            for (int t = 0; t < T; ++t) {
-                const uint32_t tg = tb + t, buf = tg & 1, ph = (tg >> 1) & 1;
-                if (scores) {
-                    ok = ok && umma::mbar_wait_fast(sa(part == 0 ? &b_half[buf] : &b_full[buf]), ph);
-                    if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_sfree[buf]), ph ^ 1);
-                } else {
+        auto both = [&] { return ok = __all_sync(0xffffffffu, ok); };
+        if (warp == TR_MMA1) {
+            // ---- scores of tile t: dims 0-255 as soon as they are expanded and the softmax has read those of tile t-2
+            const uint32_t id = umma::idesc_f16(128, 128, 0, 0);
+            const uint64_t qd = umma::desc(base + TR_SQ, 16, 1024, umma::LAYOUT_SW128);
+            uint32_t k = 0;
+            while (ok && tr_next(a, cur, h)) {
+                ok = umma::mbar_wait_fast(sa(&b_q), k & 1);
+                for (int t = h.t0; t < h.t1; ++t, ++tb) {
+                    const uint32_t buf = tb & 1, ph = (tb >> 1) & 1;
+                    const uint64_t ld = umma::desc(base + TR_SL + buf * TR_LBUF, 16, 1024, umma::LAYOUT_SW128);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && umma::mbar_wait_fast(sa(half == 0 ? &b_half[buf] : &b_full[buf]), ph);
+                        if (!both()) break;
+                        umma::fence_after();
+                        if (umma::elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 16; ++kk) {
+                                const int ks = 16 * half + kk;
+                                const uint64_t off = (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4);
+                                umma::mma_f16_pair(tm + TRT_S + 64 * buf, qd + off, ld + off, id, ks > 0);
+                            }
+                            if (half == 1) umma::commit_pair(sa(&b_sfull[buf]));
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
+                ++k;
+            }
+        } else if (warp == TR_MMA2) {
+            // ---- values of tile t, dims 0-255 first.  Keys 0-63 (CTA 0's) in places 4 n, 4 n + 1, keys 64-127 in the two
+            // after them
+            const uint32_t id = umma::idesc_f16(128, 256, 0, 1);
+            while (ok && tr_next(a, cur, h)) {
+                for (int t = h.t0; t < h.t1; ++t, ++tb) {
+                    const uint32_t buf = tb & 1, ph = (tb >> 1) & 1;
                     ok = ok && umma::mbar_wait_fast(sa(&b_for[buf]), ph);
                     ok = ok && umma::mbar_wait_fast(sa(&b_pfull[buf]), ph);
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                umma::fence_after();
-                if (umma::elect_one()) {
-                    if (scores) {
-                        const uint64_t ld = umma::desc(base + TR_SL + buf * TR_LBUF, 16, 1024, umma::LAYOUT_SW128);
-#pragma unroll
-                        for (int kk = 0; kk < 16; ++kk) {
-                            const int ks = 16 * part + kk;
-                            const uint64_t off = (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4);
-                            umma::mma_f16_pair(tm + TRT_S + 64 * (2 * buf + part), qd + off, ld + off, id, kk > 0);
-                        }
-                        umma::commit_pair(sa(&b_sfull[buf]));
-                    } else {
-                        // dims 0-255 first.  Keys 0-63 (CTA 0's) in places 4 n, 4 n + 1, keys 64-127 in the two after them
+                    if (!both()) break;
+                    umma::fence_after();
+                    if (umma::elect_one()) {
                         const uint64_t pd = umma::desc(base + TR_SP + buf * TR_PBUF, 16, 1024, umma::LAYOUT_SW128);
                         const uint64_t vd = umma::desc(base + TR_SL + buf * TR_LBUF, TR_SLAB, 1024, umma::LAYOUT_SW128);
 #pragma unroll
@@ -499,15 +507,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                             for (int ks = 0; ks < 8; ++ks)
                                 umma::mma_f16_pair(tm + TRT_O + 128 * n, pd + (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4),
                                                    vd + (uint64_t)(((4 * n + 2 * (ks >> 2)) * TR_SLAB + (ks & 3) * 2048) >> 4), id,
-                                                   (t > 0 || ks > 0) ? 1u : 0u);
+                                                   (t > h.t0 || ks > 0) ? 1u : 0u);
                             umma::commit_pair(sa(n == 0 ? &b_ohalf[buf] : &b_odone[buf]));
                         }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-            tb += T;
-            ++k;
         }
     } else if (warp < TR_SMW) {
         // ================= queries, softmax, outputs: a thread has one row (TMEM lane 32 (warp % 4) + lane: row lane % 64) and,
@@ -515,7 +521,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
         const int qd = warp & 3, ch = warp >> 2, kh = qd >> 1, row = 32 * (qd & 1) + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
         const uint32_t r_q = umma::mapa(sa(&b_q), 0);
-        const uint32_t r_sfree[2] = {umma::mapa(sa(&b_sfree[0]), 0), umma::mapa(sa(&b_sfree[1]), 0)};
         const uint32_t r_pfull[2] = {umma::mapa(sa(&b_pfull[0]), 0), umma::mapa(sa(&b_pfull[1]), 0)};
         bool first_share = true;
         while (tr_next(a, cur, h)) {
@@ -576,33 +581,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 float x[32];
                 ok = ok && umma::mbar_wait_fast(sa(&b_sfull[buf]), ph);
                 umma::fence_after();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x1[16];
-                    umma::tmem_ld16(lane_base + TRT_S + 64 * (2 * buf) + 32 * ch + 16 * i, x + 16 * i);
-                    umma::tmem_ld16(lane_base + TRT_S + 64 * (2 * buf + 1) + 32 * ch + 16 * i, x1);
-                    umma::tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) add2_rn(x[16 * i + j], x[16 * i + j + 1], x1[j], x1[j + 1]);
-                }
-                umma::fence_before();
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive_pair(r_sfree[buf]);
+                umma::tmem_ld16(lane_base + TRT_S + 64 * buf + 32 * ch, x);
+                umma::tmem_ld16(lane_base + TRT_S + 64 * buf + 32 * ch + 16, x + 16);
+                umma::tmem_wait_ld();
                 const float mul = window ? mul4 * up : mul4;
                 if (see != 0xffffffffu)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (!((see >> i) & 1u)) x[i] = -INFINITY;
-                float mx = max3(x[0], x[1], x[2]);
+                float m4[4];
 #pragma unroll
-                for (int i = 3; i < 31; i += 2) mx = max3(mx, x[i], x[i + 1]);
-                mx = fmaxf(mx, x[31]) * mul;
+                for (int i = 0; i < 4; ++i)
+                    m4[i] = max3(max3(x[8 * i], x[8 * i + 1], x[8 * i + 2]), max3(x[8 * i + 3], x[8 * i + 4], x[8 * i + 5]),
+                                 fmaxf(x[8 * i + 6], x[8 * i + 7]));
+                const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * mul;
                 // the window tiles' part of O carries 2^-exp: it is brought to the common scale before the entries' is added
                 const bool rescale_window = !window && tile == wt && t > 0 && up != 1.0f;
-                if (umma::bar_red_or(1 + (qd & 1), TR_SMT / 2, mx - m > TR_TOP) || rescale_window) {
-                    red[2 * kh + ch][row] = mx;
+                const bool raise = umma::bar_red_or(1 + (qd & 1), TR_SMT / 2, mx - m > TR_TOP) || rescale_window;
+                // (the P buffer is free: these scores' keys were expanded after the values of the tile before in it; and S is
+                // read before P is handed on, without which its buffer is not written again)
+                if (raise) {
+                    // [4][32] of this half of the rows, where their own P goes afterwards
+                    float* red = reinterpret_cast<float*>(sm + TR_SP + buf * TR_PBUF + 4096 * (qd & 1)) + lane;
+                    red[32 * (2 * kh + ch)] = mx;
                     umma::bar_named(1 + (qd & 1), TR_SMT / 2);
-                    const float mt = fmaxf(fmaxf(red[0][row], red[1][row]), fmaxf(red[2][row], red[3][row]));
+                    float mt = red[0];
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) mt = fmaxf(mt, red[32 * i]);
                     float f = 1.0f;
                     if (mt > -INFINITY && (m == -INFINITY || mt - m > TR_TOP)) {
                         f = m == -INFINITY ? 0.0f : umma::ex2(m - (mt - TR_UP));
@@ -628,7 +633,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     }
                     umma::bar_named(1 + (qd & 1), TR_SMT / 2);        // red is read
                 }
-                if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf]), ph ^ 1);          // the P buffer is free
                 const float ref = m == -INFINITY ? 0.0f : -m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 uint8_t* P = sm + TR_SP + buf * TR_PBUF + kh * TR_SLAB;
@@ -652,12 +656,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 if (lane == 0) umma::mbar_arrive_pair(r_pfull[buf]);
             }
             // ---- the share's end: the row's sum over its four threads, then O
-            red[2 * kh + ch][row] = lsum;
-            umma::bar_named(3, TR_SMT);
-            const float l = (red[0][row] + red[1][row]) + (red[2][row] + red[3][row]);
             const uint32_t tl = tb + T - 1;
             ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
             umma::fence_after();
+            float* red = reinterpret_cast<float*>(sm + TR_SP) + row;      // both P buffers are free
+            red[64 * (2 * kh + ch)] = lsum;
+            umma::bar_named(3, TR_SMT);
+            float l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l += red[64 * i];
             const float fin = h.t1 <= wt ? up : 1.0f;
             const bool whole = T == h.T;
             const int64_t gr = (int64_t)h.b * n_rows_q + q0 + row;
