@@ -1,0 +1,586 @@
+// The nodes of drafted trees over index lists (csa2_tree_attn with k >= 0): what csa2_sparse_attn computes, with a node's
+// window ending in the draft rows of its chain (attn_tree.cu has the definition; "DeepSeek-v4.1 Flash:
+// KVキャッシュ圧縮の限界を押し広げる" §2.3.1).  Lists differ from node to node, so an item is one node and 64 of its heads.
+//
+// Work.  2 x 512 multiply-adds per head and key; 64 heads make 455 flop of a 288-byte entry, so the tensor cores bound it and
+// shared memory feeds them.  An item has two units for its window (at most 128 rows) and one for each 64 slots of its list,
+// known on the host; block i (one per SM) takes the i-th even part of all units.  An item that one block has whole
+// is stored by it, the shares of others are joined.
+//
+// One tile of 64 keys, double-buffered (L, S, P):
+//   S = Q . L^T     (tcgen05 kind::f16, M = 64 heads, N = 64 keys, K = 512; two issuers take dims 0-255 and 256-511 into two
+//                    TMEM partials)
+//   softmax         one head and 16 keys per thread, weights against a reference that is raised, and O rescaled in TMEM, only
+//                   when a score rises far above it
+//   O^T += L^T . P  (M = 4 x 128 dims, N = the heads in steps of 16, K = 64 keys; two issuers)
+// Window rows go to fp16 after a power-of-two scale of their tile where their largest magnitude asks for it; O carries the
+// scale of the tile last added, and is brought to the next one's where they differ.
+// Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 rows.  Nothing waits for a P or S buffer: a tile's
+// keys are expanded only after the values of the tile before it in that buffer, which had read and written both.
+#include <algorithm>
+#include <type_traits>
+
+#include "attn_join.cuh"
+#include "common.cuh"
+#include "elem.cuh"
+#include "fp4_f16.cuh"
+#include "umma.cuh"
+
+namespace csa2 {
+
+constexpr int TL_TILE = 64, TL_H = 64;
+constexpr int TL_THREADS = 640;
+constexpr int TL_SMW = 8, TL_SMT = TL_SMW * 32;
+constexpr int TL_MMA1 = 8, TL_MMA2 = 10, TL_LOADW = 12, TL_LOADERS = 256;
+constexpr uint32_t TL_SLAB = 64 * 128;               // 64 heads or keys x 64 fp16, 128-byte swizzle
+constexpr uint32_t TL_SQ = 0;
+constexpr uint32_t TL_SL = 8 * TL_SLAB, TL_LBUF = 8 * TL_SLAB;
+constexpr uint32_t TL_SP = TL_SL + 2 * TL_LBUF, TL_PBUF = TL_SLAB;
+constexpr uint32_t TL_SLOTS = TL_SP + 2 * TL_PBUF;   // the share's entries, -1 for none
+constexpr uint32_t TL_DYN = TL_SLOTS + MAX_K * 4 + 1024;
+constexpr uint32_t TLT_S = 0, TLT_O = 256, TLT_COLS = 512;       // S partial p of buffer b at TLT_S + 64 (2b + p)
+// weights are 2^(score - m), m set TL_UP below the largest score and raised when one is more than TL_TOP above it: the
+// largest weight lies in [2^7, 2^15], and what fp16 rounds to zero is below 2^-32 of it
+constexpr float TL_UP = 7.0f, TL_TOP = 15.0f;
+constexpr int TL_SMS = 152;
+constexpr int TL_WIN = 2;                            // units of an item's window
+static_assert(WINDOW <= TL_WIN * TL_TILE, "the window's rows have a unit per tile");
+
+__device__ __forceinline__ uint32_t tl_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+struct ListArgs {
+    const uint8_t *codes, *scales;
+    int capacity;
+    const uint16_t* q;
+    int n_q, n_heads, hgroups;
+    const int64_t* q_pos;
+    const int32_t* parent;
+    const uint16_t* draft;
+    const int32_t* idx;
+    int k;
+    const uint16_t* swa;
+    const int64_t* swa_pos0;
+    int swa_len;
+    float scale_log2e;
+    void* out;
+    float* lse;
+    int per;                     // units of an item
+    int each, more;              // the first `more` blocks have each + 1 units, the others `each`
+    float* part_o;               // [2 blocks][64][512]
+    float2* part_ml;             // [2 blocks][64] reference (log2) and sum
+    int* err;
+    __device__ __forceinline__ int start(int b) const { return each * b + min(b, more); }
+    __device__ __forceinline__ int block_of(int u) const {
+        const int longer = (each + 1) * more;
+        return u < longer ? (unsigned)u / (unsigned)(each + 1) : more + (int)((unsigned)(u - longer) / (unsigned)each);
+    }
+};
+
+// Item i: a node, its first head, and its window: nw committed rows from window row `row0` on, then its chain's draft rows
+struct ListItem {
+    int64_t gq, row0;
+    int b, h0, nw, rows;         // rows = 0: the node is not there
+    __device__ __forceinline__ int wtiles() const { return (rows + TL_TILE - 1) / TL_TILE; }
+};
+template <typename F>
+__device__ __forceinline__ ListItem tl_item(const ListArgs& a, int item, F&& chain) {
+    ListItem w;
+    const int64_t g = a.hgroups == 1 ? item : item >> 1;             // at most 128 heads: one or two groups
+    w.h0 = a.hgroups == 1 ? 0 : (item & 1) * TL_H;
+    w.gq = g;
+    w.b = (int)((unsigned)g / (unsigned)a.n_q);
+    const int32_t* parent = a.parent + (int64_t)w.b * a.n_q;
+    int len = 0, j = (int)(g - (int64_t)w.b * a.n_q);
+    while (j >= 0) {
+        chain(len++, j);
+        const int up = parent[j];
+        j = up >= -1 && up < j ? up : -2;
+    }
+    if (j != -1) len = 0;
+    const int64_t p = a.q_pos[g], s0 = a.swa_pos0 != nullptr ? a.swa_pos0[w.b] : 0;
+    const int64_t lo = max(max((int64_t)0, p - (WINDOW - 1)), s0), hi = min(p - len, s0 + a.swa_len - 1);
+    w.nw = len > 0 && hi >= lo ? (int)(hi - lo + 1) : 0;
+    w.rows = w.nw + len;
+    w.row0 = lo - s0;
+    return w;
+}
+
+template <typename TO>
+__global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_constant__ ListArgs a) {
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2];
+    __shared__ float red[2][TL_H], m_run[TL_H], fac[TL_H];
+    __shared__ int qexp[TL_H], wexp[2], any[4];
+    __shared__ unsigned int wmax[2];
+    __shared__ uint32_t slot_ok[2][2], tmem_base;
+    __shared__ uint8_t chain[TREE_NODES];
+    const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
+    uint8_t* sm = dyn + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto sa = [&](const void* x) { return umma::smem_u32(x); };
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(sa(&b_lhalf[i]), TL_LOADERS / 32);
+            umma::mbar_init(sa(&b_lfull[i]), TL_LOADERS / 32);
+            umma::mbar_init(sa(&b_lfree[i]), 2);
+            umma::mbar_init(sa(&b_sfull[i]), 2);
+            umma::mbar_init(sa(&b_pfull[i]), TL_SMW);
+            umma::mbar_init(sa(&b_odone[i]), 2);
+        }
+        umma::fence_mbar_init();
+        wmax[0] = wmax[1] = 0u;
+    }
+    if (warp == TL_LOADW - 1) umma::tmem_alloc(sa(&tmem_base), TLT_COLS);
+    pdl_wait();
+    pdl_launch_next();
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    const uint32_t tmem = tmem_base;
+    bool ok = true;
+    uint32_t tb = 0;                                 // tiles done so far: the rings go on from share to share
+    const int u1 = a.start(blockIdx.x + 1);
+    int u = a.start(blockIdx.x);
+    const int lt = tid - TL_LOADW * 32;
+
+    // every warp goes through the block's shares: units t0 .. t1-1 of an item, units 0 and 1 its window's tiles
+    for (int k = 0; u < u1; ++k) {
+        const int item = (unsigned)u / (unsigned)a.per, t0 = u - item * a.per, t1 = min(a.per, t0 + u1 - u);
+        u += t1 - t0;
+        const bool loader = warp >= TL_LOADW;
+        if (loader) umma::bar_named(2, TL_LOADERS);      // the chain and the slots of the share before are read
+        const ListItem w = tl_item(a, item, [&](int i, int j) {
+            if (lt == 0) chain[i] = (uint8_t)j;
+        });
+        const int wt = w.wtiles();
+        // the tiles that are there, counted on: window tiles first, then the list's
+        const int wa = min(t0, wt), wb = min(t1, wt), la = max(t0, TL_WIN), lb = max(t1, TL_WIN);
+        const int nwt = max(0, min(wb, TL_WIN) - wa), T = w.rows == 0 ? 0 : nwt + (lb - la);
+        const int nh = min(TL_H, a.n_heads - w.h0);
+        if (loader) {
+            // ================= rows
+            const uint8_t* codes = a.codes + (int64_t)w.b * a.capacity * (D_LAT / 2);
+            const uint8_t* scales = a.scales + (int64_t)w.b * a.capacity * (D_LAT / 16);
+            int* slots = reinterpret_cast<int*>(sm + TL_SLOTS);
+            const int s0 = (la - TL_WIN) * TL_TILE;
+            if (T > nwt)
+                for (int j = lt; j < (T - nwt) * TL_TILE; j += TL_LOADERS) {
+                    const int e = s0 + j < a.k ? a.idx[w.gq * a.k + s0 + j] : -1;
+                    slots[j] = (unsigned)e < (unsigned)a.capacity ? e : -1;
+                }
+            umma::bar_named(2, TL_LOADERS);
+            constexpr int NU = TL_TILE * 16 / TL_LOADERS;
+            // unit i of a tile: a warp takes 4 rows x 8 units of 32 dims, whole 128-byte lines of codes; the 8 threads of a
+            // quarter warp write different bank groups; units below NU / 2 are dims 0-255
+            auto unit_rc = [&](int i, int& r, int& c) {
+                const int qq = (lt >> 5) + 8 * i;
+                r = 4 * (qq & 15) + (lane & 3);
+                c = 8 * (qq >> 4) + (lane >> 2);
+            };
+            for (int t = 0; t < T; ++t) {
+                const uint32_t tg = tb + t, buf = tg & 1, before = ((tg >> 1) - 1) & 1;
+                uint8_t* L = sm + TL_SL + buf * TL_LBUF;
+                if (t < nwt) {
+                    // ---- window rows: converted as they are while their largest magnitude is found, and once more where it
+                    // asks for a scale
+                    const int v0 = (wa + t) * TL_TILE;
+                    if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_lfree[buf]), before);
+                    uint32_t mx = 0u;
+                    auto convert = [&](float d) {
+#pragma unroll 1
+                        for (int i0 = lt; i0 < TL_TILE * 64; i0 += 8 * TL_LOADERS) {
+                            uint4 x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int at = i0 + i * TL_LOADERS, v = v0 + (at >> 6), c = at & 63;
+                                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                                if (v < w.nw)
+                                    x[i] = reinterpret_cast<const uint4*>(a.swa + ((int64_t)w.b * a.swa_len + w.row0 + v) * D_LAT)[c];
+                                else if (v < w.rows)
+                                    x[i] = reinterpret_cast<const uint4*>(a.draft + ((int64_t)w.b * a.n_q + chain[v - w.nw]) * D_LAT)[c];
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int at = i0 + i * TL_LOADERS, r = at >> 6, c = at & 63;
+                                mx = max(mx, bf16_absmax8(x[i]));
+                                *reinterpret_cast<uint4*>(L + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)) = bf16x8_to_f16x8(x[i], d);
+                            }
+                        }
+                    };
+                    convert(1.0f);
+                    mx = __reduce_max_sync(0xffffffffu, mx);
+                    if (lane == 0) atomicMax(&wmax[buf], mx);
+                    umma::bar_named(2, TL_LOADERS);
+                    const int e = f16_range_exp(*reinterpret_cast<volatile unsigned int*>(&wmax[buf]));
+                    if (e != 0) convert(pow2f(-e));
+                    umma::bar_named(2, TL_LOADERS);
+                    if (lt == 0) wexp[buf] = e, wmax[buf] = 0u;
+                    umma::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        umma::mbar_arrive(sa(&b_lhalf[buf]));
+                        umma::mbar_arrive(sa(&b_lfull[buf]));
+                    }
+                } else {
+                    // ---- the list's entries
+                    const int* sl = slots + (t - nwt) * TL_TILE;
+                    uint4 cw[NU];
+                    uint32_t sc[NU];
+#pragma unroll
+                    for (int i = 0; i < NU; ++i) {
+                        int r, c;
+                        unit_rc(i, r, c);
+                        cw[i] = make_uint4(0u, 0u, 0u, 0u);          // empty slots expand to zeros
+                        sc[i] = 0u;
+                        const int e = sl[r];
+                        if (e >= 0) {
+                            cw[i] = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)e * (D_LAT / 2)) + c);
+                            sc[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + (int64_t)e * (D_LAT / 16)) + c);
+                        }
+                    }
+                    if (lt < TL_TILE && t + 1 < T) {
+                        const int e = sl[TL_TILE + lt];
+                        if (e >= 0) {
+                            umma::prefetch_l2(codes + (int64_t)e * (D_LAT / 2));
+                            umma::prefetch_l2(codes + (int64_t)e * (D_LAT / 2) + 128);
+                            umma::prefetch_l2(scales + (int64_t)e * (D_LAT / 16));
+                        }
+                    }
+                    if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_lfree[buf]), before);
+                    if (lt < TL_TILE) {
+                        const uint32_t there = __ballot_sync(0xffffffffu, sl[lt] >= 0);
+                        if (lane == 0) slot_ok[buf][lt >> 5] = there;
+                    }
+#pragma unroll
+                    for (int i = 0; i < NU; ++i) {
+                        int r, c;
+                        unit_rc(i, r, c);
+                        if (i == NU / 2) {               // dims 0-255 are done
+                            umma::fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) umma::mbar_arrive(sa(&b_lhalf[buf]));
+                        }
+                        const uint32_t words[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
+                        const __half2 sp = e4m3x2_to_f16x2(sc[i]);
+                        const __half2 s_lo = __low2half2(sp), s_hi = __high2half2(sp);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int cc = c * 4 + j;
+                            *reinterpret_cast<uint4*>(L + (cc >> 3) * TL_SLAB + tl_swz(r, cc & 7)) =
+                                e2m1x8_scaled(words[j], (j >> 1) ? s_hi : s_lo);
+                        }
+                    }
+                    umma::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(sa(&b_lfull[buf]));
+                }
+            }
+        } else {
+            // ================= warps 0-11: Q: heads h0 .. h0+63 (zero rows past n_heads), bf16 -> fp16 slabs; a head whose largest
+            // magnitude lies outside [2^-10, 2^15) is scaled by a power of two on the way
+            umma::fence_before();
+            umma::bar_named(3, TL_LOADW * 32);           // the share before is done with Q, O and what the softmax keeps
+            umma::fence_after();
+            if (T > 0) {
+                const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + (w.gq * a.n_heads + w.h0) * D_LAT);
+#pragma unroll 1
+                for (int r0 = warp; r0 < TL_H; r0 += 2 * TL_LOADW) {
+                    uint4 x[2][2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = r0 + TL_LOADW * i;
+                        x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < nh) x[i][0] = qsrc[r * 64 + lane], x[i][1] = qsrc[r * 64 + 32 + lane];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = r0 + TL_LOADW * i;
+                        if (r >= TL_H) break;
+                        const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
+                        const float d = a.scale_log2e < 0.0f ? -pow2f(-e) : pow2f(-e);       // scores are taken times |scale|
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const int c = lane + 32 * hh;
+                            *reinterpret_cast<uint4*>(sm + TL_SQ + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)) = bf16x8_to_f16x8(x[i][hh], d);
+                        }
+                        if (lane == 0) qexp[r] = e;
+                    }
+                }
+                umma::fence_proxy_async();
+                if (tid < TL_H) m_run[tid] = -INFINITY;
+            }
+            umma::bar_named(3, TL_LOADW * 32);
+            if (warp >= TL_MMA1 && warp < TL_MMA2) {
+                // ================= scores of tile t once its dims are expanded.  The whole warp walks the tiles, so that
+                // descriptors and addresses stay in uniform registers; one elected lane issues.
+                const int half = warp - TL_MMA1;
+                const uint32_t id = umma::idesc_f16(64, TL_TILE, 0, 0);
+                const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+                const uint64_t qd = umma::desc(base + TL_SQ, 16, 1024, umma::LAYOUT_SW128);
+                for (int t = 0; t < T; ++t) {
+                    const uint32_t tg = tb + t, buf = tg & 1;
+                    ok = ok && umma::mbar_wait_fast(sa(half == 0 ? &b_lhalf[buf] : &b_lfull[buf]), (tg >> 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    umma::fence_after();
+                    const uint64_t ld = umma::desc(base + TL_SL + buf * TL_LBUF, 16, 1024, umma::LAYOUT_SW128);
+                    if (umma::elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk) {
+                            const int ks = 16 * half + kk;
+                            const uint64_t off = (uint64_t)(((ks >> 2) * TL_SLAB + (ks & 3) * 32) >> 4);
+                            umma::mma_f16(tm + TLT_S + 64 * (2 * buf + half), qd + off, ld + off, id, kk > 0);
+                        }
+                        umma::commit(sa(&b_sfull[buf]));
+                    }
+                    __syncwarp();
+                }
+            } else if (warp >= TL_MMA2) {
+                // ================= values of tile t once P is written; completion frees the L and P buffers
+                const int half = warp - TL_MMA2;
+                const uint32_t id = umma::idesc_f16(128, (nh + 15) & ~15, 1, 0);     // heads that are there, in MMA steps
+                const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+                for (int t = 0; t < T; ++t) {
+                    const uint32_t tg = tb + t, buf = tg & 1;
+                    ok = ok && umma::mbar_wait_fast(sa(&b_pfull[buf]), (tg >> 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    umma::fence_after();
+                    const uint64_t ld = umma::desc(base + TL_SL + buf * TL_LBUF, TL_SLAB, 1024, umma::LAYOUT_SW128);
+                    const uint64_t pd = umma::desc(base + TL_SP + buf * TL_PBUF, 16, 1024, umma::LAYOUT_SW128);
+                    if (umma::elect_one()) {
+#pragma unroll
+                        for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+                            for (int ks = 0; ks < TL_TILE / 16; ++ks) {
+                                const int mt = 2 * half + m2;
+                                umma::mma_f16(tm + TLT_O + 64 * mt, ld + (uint64_t)((2 * mt * TL_SLAB + ks * 2048) >> 4),
+                                              pd + (uint64_t)((ks * 32) >> 4), id, (t > 0 || ks > 0) ? 1u : 0u);
+                            }
+                        umma::commit(sa(&b_lfree[buf]));
+                        umma::commit(sa(&b_odone[buf]));
+                    }
+                    __syncwarp();
+                }
+            } else if (warp < TL_SMW) {
+                // ================= softmax: lane l of warp w has head 16 (w % 4) + l / 4 + 8 (l % 2) and, of keys 32 (w / 4) .. + 31,
+                // those of parity (l / 2) % 2 (the 16x64b TMEM shape)
+                const int qd = warp & 3, half = warp >> 2;
+                const int h = qd * 16 + (lane >> 2) + 8 * (lane & 1), par = (lane >> 1) & 1;
+                const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
+                // never zero, so that a masked score stays -inf
+                const float mul4 = T > 0 ? fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[h]), 0x1p-100f) : 0.0f;
+                float lsum = 0.0f;
+                int oexp = 0;                        // O is 2^-oexp of what it stands for
+                for (int t = 0; t < T; ++t) {
+                    const uint32_t tg = tb + t, buf = tg & 1, ph = (tg >> 1) & 1;
+                    float x[16];
+                    ok = ok && umma::mbar_wait_fast(sa(&b_sfull[buf]), ph);
+                    ok = ok && umma::mbar_wait_fast(sa(&b_lfull[buf]), ph);          // (the loaders' words too)
+                    umma::fence_after();
+                    {
+                        float x1[16];
+                        umma::tmem_ld16x64b_x16(lane_base + TLT_S + 64 * (2 * buf) + 32 * half, x);
+                        umma::tmem_ld16x64b_x16(lane_base + TLT_S + 64 * (2 * buf + 1) + 32 * half, x1);
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] += x1[i];
+                    }
+                    const bool window = t < nwt;
+                    const int e = window ? *reinterpret_cast<volatile int*>(&wexp[buf]) : 0;
+                    const float mul = fmaxf(mul4 * pow2f(e), 0x1p-126f);
+                    uint32_t see;                    // which of the half's 32 keys are there
+                    if (window) {
+                        const int left = w.rows - (wa + t) * TL_TILE - 32 * half;
+                        see = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+                    } else {
+                        see = *reinterpret_cast<volatile uint32_t*>(&slot_ok[buf][half]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] *= mul;
+                    if (see != 0xffffffffu)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (!((see >> (par + 2 * i)) & 1u)) x[i] = -INFINITY;
+                    const float mh = m_run[h];
+                    float mx = x[0];
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
+                    const bool shift = t > 0 && e != oexp;           // (the same for all)
+                    if (umma::bar_red_or(1, TL_SMT, mx - mh > TL_TOP) || shift) {
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        if (par == 0) red[half][h] = mx;
+                        umma::bar_named(1, TL_SMT);
+                        if (half == 0) {
+                            float f = 1.0f;
+                            if (par == 0) {
+                                const float mt = fmaxf(red[0][h], red[1][h]), mo = m_run[h], mn = mt - TL_UP;
+                                if (mt > -INFINITY && (mo == -INFINITY || mt - mo > TL_TOP)) {
+                                    f = mo == -INFINITY ? 0.0f : umma::ex2(mo - mn);
+                                    m_run[h] = mn;
+                                }
+                                fac[h] = f;
+                            }
+                            const unsigned some = __ballot_sync(0xffffffffu, f != 1.0f);
+                            if (lane == 0) any[qd] = some != 0;
+                        }
+                        if (t >= 1) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);   // O settled
+                        umma::bar_named(1, TL_SMT);
+                        umma::fence_after();
+                        if (t >= 1 && (shift || (any[0] | any[1] | any[2] | any[3]))) {
+                            // the scale's part in two steps: each lies within fp32's range
+                            const float up = shift ? pow2f((oexp - e) / 2) : 1.0f, up2 = shift ? pow2f((oexp - e) - (oexp - e) / 2) : 1.0f;
+#pragma unroll 1
+                            for (int mt = 2 * half; mt < 2 * half + 2; ++mt)
+#pragma unroll 1
+                                for (int c = 0; c < TL_H; c += 16) {
+                                    float v[16];
+                                    umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c, v);
+                                    umma::tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) v[i] = v[i] * fac[c + i] * up * up2;
+                                    umma::tmem_st16(lane_base + TLT_O + 64 * mt + c, v);
+                                }
+                            umma::tmem_wait_st();
+                        }
+                        lsum *= fac[h];
+                    }
+                    oexp = e;
+                    const float mr = m_run[h], m = mr == -INFINITY ? 0.0f : mr;      // (a tile may have no key)
+                    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        x[i] = umma::ex2_ftz(x[i] - m);
+                        sum[i & 1] += x[i];
+                    }
+                    lsum += sum[0] + sum[1];
+                    // row h of P^T: trade half of the values with the lane of the other parity for 16 consecutive keys
+                    float rv[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) rv[i] = __shfl_xor_sync(0xffffffffu, par ? x[i] : x[8 + i], 2);
+                    uint32_t p2[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) p2[j] = par ? f16x2_bits(rv[j], x[8 + j]) : f16x2_bits(x[j], rv[j]);
+                    uint8_t* P = sm + TL_SP + buf * TL_PBUF;
+                    *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                    *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
+                    umma::fence_proxy_async();
+                    umma::fence_before();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(sa(&b_pfull[buf]));
+                }
+                // ---- the share's end: sums, then O^T as [head][dim]
+                lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+                if (par == 0) red[half][h] = lsum;
+                umma::bar_named(1, TL_SMT);
+                const bool whole = t1 - t0 == a.per;
+                const int64_t orow = w.gq * a.n_heads + w.h0, prow = (int64_t)(2 * blockIdx.x + (k == 0 ? 0 : 1)) * TL_H;
+                if (tid < TL_H) {
+                    const float l = T > 0 ? red[0][tid] + red[1][tid] : 0.0f, m = T > 0 ? m_run[tid] : -INFINITY;
+                    if (!whole)
+                        a.part_ml[prow + tid] = make_float2(m, l);
+                    else if (tid < nh && a.lse != nullptr)
+                        a.lse[orow + tid] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    fac[tid] = !whole ? 1.0f : l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                }
+                umma::bar_named(1, TL_SMT);
+                if (T > 0) {
+                    const uint32_t tl = tb + T - 1;
+                    ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
+                    umma::fence_after();
+                    const float up = pow2f(oexp);
+#pragma unroll 1
+                    for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
+                        const int dim = mt * 128 + qd * 32 + lane;
+#pragma unroll 1
+                        for (int c = 0; c < nh; c += 16) {
+                            float v[16];
+                            umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c, v);
+                            umma::tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if (c + i >= nh) break;
+                                const float y = ok ? v[i] * fac[c + i] * up : __int_as_float(0x7fc00000);
+                                if (whole)
+                                    reinterpret_cast<TO*>(a.out)[(orow + c + i) * D_LAT + dim] = from_f32<TO>(y);
+                                else
+                                    a.part_o[(prow + c + i) * D_LAT + dim] = y;
+                            }
+                        }
+                    }
+                } else if (whole) {
+                    for (int i = tid; i < nh * D_LAT; i += TL_SMT) reinterpret_cast<TO*>(a.out)[orow * D_LAT + i] = from_f32<TO>(0.0f);
+                }
+            }
+        }
+        tb += T;
+    }
+    if (!ok) atomicExch(a.err, 1);
+    umma::fence_before();
+    __syncthreads();
+    if (warp == TL_LOADW - 1) {
+        umma::fence_after();
+        umma::tmem_dealloc(tmem, TLT_COLS);
+    }
+}
+
+// Joins the shares of an item that several blocks worked on, four heads a block: block x joins the item whose units begin
+// with block x of k_tree_lists and go on in the next one.
+template <typename TO>
+__global__ void __launch_bounds__(512) k_tree_lists_join(const __grid_constant__ ListArgs a) {
+    pdl_wait();
+    const int blk = blockIdx.x, bound = a.start(blk + 1), item = (unsigned)bound / (unsigned)a.per, first = item * a.per;
+    const int head = (int)blockIdx.y * 4 + ((int)threadIdx.x >> 7);
+    if (bound == first || first < a.start(blk)) return;
+    const int64_t g = a.hgroups == 1 ? item : item >> 1;
+    const int h0 = a.hgroups == 1 ? 0 : (item & 1) * TL_H;
+    if (h0 + head >= a.n_heads || head >= TL_H) return;
+    const int n = a.block_of(first + a.per - 1) - blk + 1, slot = 2 * blk + (first == a.start(blk) ? 0 : 1);
+    auto share = [&](int s) { return (int64_t)(s == 0 ? slot : 2 * (blk + s)) * TL_H + head; };
+    const int64_t row = g * a.n_heads + h0 + head;
+    join_row<TO, 1>(a.part_o, a.part_ml, n, share, reinterpret_cast<TO*>(a.out) + row * D_LAT, a.lse != nullptr ? a.lse + row : nullptr);
+}
+
+namespace {
+constexpr size_t TL_HEAD = 256;                      // the error word and padding
+int lists_blocks(int64_t units) { return (int)std::min<int64_t>(TL_SMS, units); }
+int64_t lists_units(int batch, int n_q, int n_heads, int k) {
+    return (int64_t)batch * n_q * ((n_heads + TL_H - 1) / TL_H) * (TL_WIN + (k + TL_TILE - 1) / TL_TILE);
+}
+}  // namespace
+
+size_t tree_lists_ws(int batch, int n_q, int n_heads, int k) {
+    const size_t rows = (size_t)2 * lists_blocks(lists_units(batch, n_q, n_heads, k)) * TL_H;
+    return TL_HEAD + rows * (D_LAT * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_tree_lists(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
+                              const int32_t* parent, const uint16_t* draft, const int32_t* idx, int k, const uint16_t* swa,
+                              const int64_t* swa_pos0, int swa_len, float scale, void* out, int out_type, float* lse, void* ws,
+                              cudaStream_t st) {
+    const int64_t units = lists_units(c.batch, n_q, n_heads, k);     // below 2^31: at most 65,535 x 128 nodes, 2 groups, 34 units
+    const int blocks = lists_blocks(units);
+    ListArgs a{c.lat_codes, c.lat_scales, c.capacity, q, n_q, n_heads, (n_heads + TL_H - 1) / TL_H, q_pos, parent, draft, idx, k,
+               swa, swa_pos0, swa_len, scale * 1.4426950408889634f, out, lse, TL_WIN + (k + TL_TILE - 1) / TL_TILE,
+               (int)(units / blocks), (int)(units % blocks), nullptr, nullptr, reinterpret_cast<int*>(ws)};
+    uint8_t* w = reinterpret_cast<uint8_t*>(ws) + TL_HEAD;
+    a.part_o = reinterpret_cast<float*>(w);
+    a.part_ml = reinterpret_cast<float2*>(w + (size_t)2 * blocks * TL_H * D_LAT * sizeof(float));
+    auto go = [&](auto* y) {
+        using TO = std::remove_pointer_t<decltype(y)>;
+        const cudaError_t e = cudaFuncSetAttribute(k_tree_lists<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TL_DYN);
+        if (e != cudaSuccess) return e;
+        launch_k(k_tree_lists<TO>, dim3((unsigned)blocks), TL_THREADS, TL_DYN, st, a);
+        note_launch();
+        if (blocks > 1) {
+            launch_k(k_tree_lists_join<TO>, dim3((unsigned)(blocks - 1), (unsigned)((std::min(n_heads, TL_H) + 3) / 4)), 512, 0, st, a);
+            note_launch();
+        }
+        return cudaGetLastError();
+    };
+    return out_type == CSA2_F32   ? go(reinterpret_cast<float*>(out))
+           : out_type == CSA2_F16 ? go(reinterpret_cast<__half*>(out))
+                                  : go(reinterpret_cast<__nv_bfloat16*>(out));
+}
+
+}  // namespace csa2

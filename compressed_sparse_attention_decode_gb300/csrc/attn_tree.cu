@@ -31,6 +31,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "attn_join.cuh"
 #include "common.cuh"
 #include "elem.cuh"
 #include "fp4_f16.cuh"
@@ -584,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 umma::tmem_ld16(lane_base + TRT_S + 64 * buf + 32 * ch, x);
                 umma::tmem_ld16(lane_base + TRT_S + 64 * buf + 32 * ch + 16, x + 16);
                 umma::tmem_wait_ld();
-                const float mul = window ? mul4 * up : mul4;
+                const float mul = window ? fmaxf(mul4 * up, 0x1p-126f) : mul4;
                 if (see != 0xffffffffu)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -725,8 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
 // SPREAD 4, for few items: block (item, row), four groups of 128 threads that take every fourth share.
 template <typename TO, int SPREAD>
 __global__ void __launch_bounds__(512) k_tree_join(const __grid_constant__ TreeArgs a, int pairs, int row_tiles) {
-    __shared__ float4 sums[SPREAD > 1 ? 3 : 1][128];
-    const int tid = threadIdx.x, dim = tid & 127, group = SPREAD > 1 ? tid >> 7 : 0, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
     pdl_wait();
     TreeHead hd{0, 0, 0, 0};
     int row;
@@ -748,170 +748,18 @@ __global__ void __launch_bounds__(512) k_tree_join(const __grid_constant__ TreeA
     if (hd.n == 0 || in_seq >= a.n_q * a.n_heads) return;
     // the first share's slot, then the first slots of the pairs after it
     auto share = [&](int s) { return (int64_t)(s == 0 ? hd.slot : ((hd.slot >> 1) + s) * 2) * TR_ROWS + row; };
-    constexpr int NB = 8;
-    float m = -INFINITY, l = 0.0f;
-    for (int s = lane; s < hd.n; s += 32) {
-        const float2 v = a.part_ml[share(s)];
-        if (v.y != 0.0f) m = fmaxf(m, v.x);
-    }
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float o[4] = {};
-    for (int s0 = group; s0 < hd.n; s0 += NB * SPREAD) {
-        float4 x[NB];
-        float2 v[NB];
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int64_t at = share(min(s0 + i * SPREAD, hd.n - 1));
-            x[i] = reinterpret_cast<const float4*>(a.part_o + at * D_LAT)[dim];
-            v[i] = a.part_ml[at];
-        }
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            if (s0 + i * SPREAD >= hd.n) continue;
-            const float f = v[i].y != 0.0f ? exp2f(v[i].x - m) : 0.0f;
-            o[0] = fmaf(f, x[i].x, o[0]), o[1] = fmaf(f, x[i].y, o[1]);
-            o[2] = fmaf(f, x[i].z, o[2]), o[3] = fmaf(f, x[i].w, o[3]);
-        }
-    }
-    for (int s = lane; s < hd.n; s += 32) {
-        const float2 v = a.part_ml[share(s)];
-        if (v.y != 0.0f) l = fmaf(exp2f(v.x - m), v.y, l);
-    }
-    for (int o2 = 16; o2; o2 >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
-    if constexpr (SPREAD > 1) {
-        if (group > 0) sums[group - 1][dim] = make_float4(o[0], o[1], o[2], o[3]);
-        __syncthreads();
-        if (group > 0) return;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const float4 x = sums[i][dim];
-            o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
-        }
-    }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     const int64_t gr = (int64_t)hd.b * a.n_q * a.n_heads + in_seq;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= inv;
-    ElemVec<TO, 4> y;
-    y.pack(o);
-    y.store(reinterpret_cast<TO*>(a.out) + gr * D_LAT + 4 * dim);
-    if (a.lse != nullptr && dim == 0) a.lse[gr] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    join_row<TO, SPREAD>(a.part_o, a.part_ml, hd.n, share, reinterpret_cast<TO*>(a.out) + gr * D_LAT,
+                         a.lse != nullptr ? a.lse + gr : nullptr);
 }
 
-// ---------------------------------------------------------------- index lists
+// ---------------------------------------------------------------- launches
 
-constexpr int TS_TILE = 32, TS_HEADS = 8;
-
-struct SimtArgs {
-    const uint8_t *codes, *scales;
-    int capacity, ratio;
-    const uint16_t* q;
-    int n_q, n_heads;
-    const int64_t* q_pos;
-    const int32_t* parent;
-    const uint16_t* draft;
-    const int32_t* idx;
-    int k;                       // < 0: every visible entry
-    const uint16_t* swa;
-    const int64_t* swa_pos0;
-    int swa_len;
-    float scale;
-    float* lse;
-};
-
-template <typename TO>
-__global__ void __launch_bounds__(256) k_tree_attn_simt(const __grid_constant__ SimtArgs a, TO* __restrict__ out) {
-    pdl_wait();
-    pdl_launch_next();
-    extern __shared__ float sm[];
-    float* qs = sm;                                  // [8][512]
-    float* tile = qs + TS_HEADS * D_LAT;             // [32][512]
-    __shared__ int chain[128], there[TS_TILE], len_s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h0 = blockIdx.x * TS_HEADS, i = blockIdx.y, b = blockIdx.z, h = h0 + warp;
-    const int64_t gq = (int64_t)b * a.n_q + i;
-    if (tid == 0) {
-        int n = 0, j = i;
-        const int32_t* parent = a.parent + (int64_t)b * a.n_q;
-        while (j >= 0) {
-            chain[n++] = j;
-            const int up = parent[j];
-            j = up >= -1 && up < j ? up : -2;
-        }
-        len_s = j == -1 ? n : 0;
-    }
-    for (int v = tid; v < TS_HEADS * D_LAT; v += 256)
-        qs[v] = h0 + v / D_LAT < a.n_heads ? bf16_bits_to_f32(a.q[(gq * a.n_heads + h0) * D_LAT + v]) : 0.0f;
-    __syncthreads();
-    const int len = len_s;
-    const int64_t p = a.q_pos[gq], s0 = a.swa_pos0 ? a.swa_pos0[b] : 0;
-    const int64_t vis = p >= WINDOW - 1 ? (p - (WINDOW - 1)) >> (a.ratio - 1) : 0;
-    const int n4 = len == 0 ? 0 : a.k >= 0 ? a.k : (int)min(vis, (int64_t)a.capacity);
-    const int64_t lo = max(max((int64_t)0, p - (WINDOW - 1)), s0), hi = min(p - len, s0 + a.swa_len - 1);
-    const int nw = len > 0 && hi >= lo ? (int)(hi - lo + 1) : 0;
-    const int64_t n = (int64_t)n4 + nw + len;
-    float m = -INFINITY, l = 0.0f, o[16] = {};
-    for (int64_t t = 0; t < n; t += TS_TILE) {
-        __syncthreads();
-        const int r = tid >> 3, part = tid & 7;                          // 8 threads a row, 64 dims each
-        const int64_t s = t + r;
-        float* dst = tile + r * D_LAT + part * 64;
-        const uint16_t* src = nullptr;
-        bool ok = false;
-        if (s < n4) {
-            const int64_t j = a.k >= 0 ? (int64_t)a.idx[gq * a.k + s] : s;
-            ok = j >= 0 && j < a.capacity;
-            if (ok) {
-                const int64_t row = (int64_t)b * a.capacity + j;
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t c0 = reinterpret_cast<const uint32_t*>(a.codes + row * (D_LAT / 2) + part * 32)[2 * g];
-                    const uint32_t c1 = reinterpret_cast<const uint32_t*>(a.codes + row * (D_LAT / 2) + part * 32)[2 * g + 1];
-                    const float f = e4m3_to_f32(a.scales[row * (D_LAT / 16) + part * 4 + g]);
-                    for (int e = 0; e < 16; ++e) {
-                        const uint32_t code = ((e < 8 ? c0 : c1) >> (4 * (e & 7))) & 15u, mag = code & 7u;
-                        const float v = mag < 2 ? 0.5f * mag : (float)(1u << ((mag >> 1) - 1)) * ((mag & 1) ? 1.5f : 1.0f);
-                        dst[16 * g + e] = (code & 8u ? -v : v) * f;
-                    }
-                }
-            }
-        } else if (s < n4 + nw) {
-            src = a.swa + ((int64_t)b * a.swa_len + (lo - s0) + (s - n4)) * D_LAT;
-        } else if (s < n) {
-            src = a.draft + ((int64_t)b * a.n_q + chain[s - n4 - nw]) * D_LAT;
-        }
-        if (src != nullptr) {
-            ok = true;
-            for (int e = 0; e < 64; ++e) dst[e] = bf16_bits_to_f32(src[part * 64 + e]);
-        }
-        if (part == 0) there[r] = ok;
-        __syncthreads();
-        if (h < a.n_heads)
-            for (int k = 0; k < TS_TILE; ++k) {
-                if (!there[k]) continue;
-                const float* row = tile + k * D_LAT;
-                float dot = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) dot = fmaf(qs[warp * D_LAT + lane + 32 * e], row[lane + 32 * e], dot);
-                for (int w = 16; w; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
-                const float x = dot * a.scale;
-                if (x > m) {
-                    const float f = expf(m - x);
-                    l *= f, m = x;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] *= f;
-                }
-                const float w = expf(x - m);
-                l += w;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = fmaf(w, row[lane + 32 * e], o[e]);
-            }
-    }
-    if (h >= a.n_heads) return;
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) out[(gq * a.n_heads + h) * D_LAT + lane + 32 * e] = from_f32<TO>(o[e] * inv);
-    if (a.lse != nullptr && lane == 0) a.lse[gq * a.n_heads + h] = l == 0.0f ? -INFINITY : m + logf(l);
-}
+size_t tree_lists_ws(int batch, int n_q, int n_heads, int k);
+cudaError_t launch_tree_lists(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
+                              const int32_t* parent, const uint16_t* draft, const int32_t* idx, int k, const uint16_t* swa,
+                              const int64_t* swa_pos0, int swa_len, float scale, void* out, int out_type, float* lse, void* ws,
+                              cudaStream_t st);
 
 namespace {
 constexpr size_t TR_HEAD = 256;                      // the error word and padding
@@ -939,29 +787,17 @@ TreePlan tree_plan(int batch, int n_q, int n_heads, int64_t capacity) {
 }  // namespace
 
 size_t tree_attn_ws(int batch, int n_q, int n_heads, int k, int64_t capacity) {
-    return k > 0 ? TR_HEAD : tree_plan(batch, n_q, n_heads, capacity).total();
+    const size_t lists = k >= 0 ? tree_lists_ws(batch, n_q, n_heads, k) : 0;
+    return k > 0 ? lists : std::max(lists, tree_plan(batch, n_q, n_heads, capacity).total());
 }
 
 cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
                              const int32_t* parent, const uint16_t* draft, const int32_t* idx, int k, const uint16_t* swa,
                              const int64_t* swa_pos0, int swa_len, float scale, void* out, int out_type, float* lse, void* ws,
                              cudaStream_t st) {
-    if (k >= 0) {
-        const SimtArgs a{c.lat_codes, c.lat_scales, c.capacity, c.ratio, q, n_q, n_heads, q_pos, parent, draft, idx, k,
-                         swa, swa_pos0, swa_len, scale, lse};
-        const size_t smem = (TS_HEADS + TS_TILE) * D_LAT * sizeof(float);
-        auto go = [&](auto* y) {
-            const auto kern = k_tree_attn_simt<std::remove_pointer_t<decltype(y)>>;
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-            launch_k(kern, dim3((n_heads + TS_HEADS - 1) / TS_HEADS, n_q, c.batch), 256, smem, st, a, y);
-            note_launch();
-            return cudaGetLastError();
-        };
-        return out_type == CSA2_F32   ? go(reinterpret_cast<float*>(out))
-               : out_type == CSA2_F16 ? go(reinterpret_cast<__half*>(out))
-                                      : go(reinterpret_cast<__nv_bfloat16*>(out));
-    }
+    if (k >= 0)
+        return launch_tree_lists(c, q, n_q, n_heads, q_pos, parent, draft, idx, k, swa, swa_pos0, swa_len, scale, out, out_type, lse,
+                                 ws, st);
     const TreePlan p = tree_plan(c.batch, n_q, n_heads, c.capacity);
     uint8_t* w = reinterpret_cast<uint8_t*>(ws) + TR_HEAD;
     auto take = [&](size_t n) { return std::exchange(w, w + n); };
