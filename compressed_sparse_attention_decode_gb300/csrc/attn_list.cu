@@ -13,10 +13,11 @@
 //   softmax         one head and 16 keys per thread, weights against a reference that is raised, and O rescaled in TMEM, only
 //                   when a score rises far above it
 //   O^T += L^T . P  (M = 4 x 128 dims, N = the heads in steps of 16, K = 64 keys; two issuers)
-// Window rows go to fp16 after a power-of-two scale of their tile where their largest magnitude asks for it; O carries the
-// scale of the tile last added, and is brought to the next one's where they differ.
-// Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 rows.  Nothing waits for a P or S buffer: a tile's
-// keys are expanded only after the values of the tile before it in that buffer, which had read and written both.
+// The window rows are fp16 values of a power-of-two scale of their own; O carries the scale of the tile last added, and is
+// brought to the entries' after the window where they differ.
+// Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 rows, 20-23 the queries, staged for the next item
+// while this one's last values and outputs are under way.  Nothing waits for a P or S buffer: a tile's keys are expanded
+// only after the values of the tile before it in that buffer, which had read and written both.
 #include <algorithm>
 #include <type_traits>
 
@@ -24,14 +25,15 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "fp4_f16.cuh"
+#include "tree.cuh"
 #include "umma.cuh"
 
 namespace csa2 {
 
 constexpr int TL_TILE = 64, TL_H = 64;
-constexpr int TL_THREADS = 640;
+constexpr int TL_THREADS = 768;
 constexpr int TL_SMW = 8, TL_SMT = TL_SMW * 32;
-constexpr int TL_MMA1 = 8, TL_MMA2 = 10, TL_LOADW = 12, TL_LOADERS = 256;
+constexpr int TL_MMA1 = 8, TL_MMA2 = 10, TL_LOADW = 12, TL_LOADERS = 256, TL_QW = 20, TL_QWARPS = 4;
 constexpr uint32_t TL_SLAB = 64 * 128;               // 64 heads or keys x 64 fp16, 128-byte swizzle
 constexpr uint32_t TL_SQ = 0;
 constexpr uint32_t TL_SL = 8 * TL_SLAB, TL_LBUF = 8 * TL_SLAB;
@@ -53,14 +55,9 @@ struct ListArgs {
     int capacity;
     const uint16_t* q;
     int n_q, n_heads, hgroups;
-    const int64_t* q_pos;
-    const int32_t* parent;
-    const uint16_t* draft;
+    TreeNodes t;
     const int32_t* idx;
     int k;
-    const uint16_t* swa;
-    const int64_t* swa_pos0;
-    int swa_len;
     float scale_log2e;
     void* out;
     float* lse;
@@ -76,44 +73,32 @@ struct ListArgs {
     }
 };
 
-// Item i: a node, its first head, and its window: nw committed rows from window row `row0` on, then its chain's draft rows
+// Item i: a node, its first head, and how many window rows and drafts it attends to
 struct ListItem {
-    int64_t gq, row0;
-    int b, h0, nw, rows;         // rows = 0: the node is not there
+    int64_t gq;
+    int b, h0, rows;             // rows = 0: the node is not there
     __device__ __forceinline__ int wtiles() const { return (rows + TL_TILE - 1) / TL_TILE; }
 };
-template <typename F>
-__device__ __forceinline__ ListItem tl_item(const ListArgs& a, int item, F&& chain) {
+__device__ __forceinline__ ListItem tl_item(const ListArgs& a, int item) {
     ListItem w;
-    const int64_t g = a.hgroups == 1 ? item : item >> 1;             // at most 128 heads: one or two groups
+    const int g = a.hgroups == 1 ? item : item >> 1;                 // at most 128 heads: one or two groups
     w.h0 = a.hgroups == 1 ? 0 : (item & 1) * TL_H;
     w.gq = g;
     w.b = (int)((unsigned)g / (unsigned)a.n_q);
-    const int32_t* parent = a.parent + (int64_t)w.b * a.n_q;
-    int len = 0, j = (int)(g - (int64_t)w.b * a.n_q);
-    while (j >= 0) {
-        chain(len++, j);
-        const int up = parent[j];
-        j = up >= -1 && up < j ? up : -2;
-    }
-    if (j != -1) len = 0;
-    const int64_t p = a.q_pos[g], s0 = a.swa_pos0 != nullptr ? a.swa_pos0[w.b] : 0;
-    const int64_t lo = max(max((int64_t)0, p - (WINDOW - 1)), s0), hi = min(p - len, s0 + a.swa_len - 1);
-    w.nw = len > 0 && hi >= lo ? (int)(hi - lo + 1) : 0;
-    w.rows = w.nw + len;
-    w.row0 = lo - s0;
+    const uint4* m = reinterpret_cast<const uint4*>(a.t.mask + w.gq * 8);
+    const uint4 x = m[0], y = m[1];
+    w.rows = __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w) + __popc(y.x) + __popc(y.y) + __popc(y.z) + __popc(y.w);
     return w;
 }
 
 template <typename TO>
 __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_constant__ ListArgs a) {
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2];
+    __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2], b_q;
     __shared__ float red[2][TL_H], m_run[TL_H], fac[TL_H];
-    __shared__ int qexp[TL_H], wexp[2], any[4];
-    __shared__ unsigned int wmax[2];
+    __shared__ int qexp[2][TL_H], any[4];
     __shared__ uint32_t slot_ok[2][2], tmem_base;
-    __shared__ uint8_t chain[TREE_NODES];
+    __shared__ uint8_t wrow[WINDOW];                         // the rows of rows16 that the share's node attends to
     const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
     uint8_t* sm = dyn + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -127,8 +112,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
             umma::mbar_init(sa(&b_pfull[i]), TL_SMW);
             umma::mbar_init(sa(&b_odone[i]), 2);
         }
+        umma::mbar_init(sa(&b_q), TL_QWARPS);
         umma::fence_mbar_init();
-        wmax[0] = wmax[1] = 0u;
     }
     if (warp == TL_LOADW - 1) umma::tmem_alloc(sa(&tmem_base), TLT_COLS);
     pdl_wait();
@@ -138,7 +123,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
     umma::fence_after();
     const uint32_t tmem = tmem_base;
     bool ok = true;
-    uint32_t tb = 0;                                 // tiles done so far: the rings go on from share to share
+    uint32_t tb = 0, nq = 0;                         // tiles and shares with tiles done so far: the rings go on from share to share
     const int u1 = a.start(blockIdx.x + 1);
     int u = a.start(blockIdx.x);
     const int lt = tid - TL_LOADW * 32;
@@ -147,11 +132,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
     for (int k = 0; u < u1; ++k) {
         const int item = (unsigned)u / (unsigned)a.per, t0 = u - item * a.per, t1 = min(a.per, t0 + u1 - u);
         u += t1 - t0;
-        const bool loader = warp >= TL_LOADW;
-        if (loader) umma::bar_named(2, TL_LOADERS);      // the chain and the slots of the share before are read
-        const ListItem w = tl_item(a, item, [&](int i, int j) {
-            if (lt == 0) chain[i] = (uint8_t)j;
-        });
+        const bool loader = warp >= TL_LOADW && warp < TL_QW;
+        const ListItem w = tl_item(a, item);
         const int wt = w.wtiles();
         // the tiles that are there, counted on: window tiles first, then the list's
         const int wa = min(t0, wt), wb = min(t1, wt), la = max(t0, TL_WIN), lb = max(t1, TL_WIN);
@@ -162,11 +144,25 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
             const uint8_t* codes = a.codes + (int64_t)w.b * a.capacity * (D_LAT / 2);
             const uint8_t* scales = a.scales + (int64_t)w.b * a.capacity * (D_LAT / 16);
             int* slots = reinterpret_cast<int*>(sm + TL_SLOTS);
+            umma::bar_named(2, TL_LOADERS);          // the rows and the slots of the share before are read
+            if (nwt > 0) {
+                // row lt is the node's if its bit is set: as many of its rows come before it as bits lie below
+                const uint32_t* m = a.t.mask + w.gq * 8;
+                const uint32_t mine = m[lt >> 5];
+                int at = __popc(mine & ((1u << lane) - 1u));
+                for (int i = 0; i < (lt >> 5); ++i) at += __popc(m[i]);
+                if ((mine >> lane) & 1u) wrow[at] = (uint8_t)lt;
+            }
             const int s0 = (la - TL_WIN) * TL_TILE;
             if (T > nwt)
                 for (int j = lt; j < (T - nwt) * TL_TILE; j += TL_LOADERS) {
                     const int e = s0 + j < a.k ? a.idx[w.gq * a.k + s0 + j] : -1;
                     slots[j] = (unsigned)e < (unsigned)a.capacity ? e : -1;
+                    if (j < TL_TILE && (unsigned)e < (unsigned)a.capacity) {         // (later tiles: a tile ahead)
+                        umma::prefetch_l2(codes + (int64_t)e * (D_LAT / 2));
+                        umma::prefetch_l2(codes + (int64_t)e * (D_LAT / 2) + 128);
+                        umma::prefetch_l2(scales + (int64_t)e * (D_LAT / 16));
+                    }
                 }
             umma::bar_named(2, TL_LOADERS);
             constexpr int NU = TL_TILE * 16 / TL_LOADERS;
@@ -181,40 +177,17 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                 const uint32_t tg = tb + t, buf = tg & 1, before = ((tg >> 1) - 1) & 1;
                 uint8_t* L = sm + TL_SL + buf * TL_LBUF;
                 if (t < nwt) {
-                    // ---- window rows: converted as they are while their largest magnitude is found, and once more where it
-                    // asks for a scale
+                    // ---- window rows and drafts
                     const int v0 = (wa + t) * TL_TILE;
                     if (tg >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_lfree[buf]), before);
-                    uint32_t mx = 0u;
-                    auto convert = [&](float d) {
-#pragma unroll 1
-                        for (int i0 = lt; i0 < TL_TILE * 64; i0 += 8 * TL_LOADERS) {
-                            uint4 x[8];
+                    const uint16_t* rows16 = a.t.rows16 + (int64_t)w.b * a.t.row_stride * D_LAT;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int at = i0 + i * TL_LOADERS, v = v0 + (at >> 6), c = at & 63;
-                                x[i] = make_uint4(0u, 0u, 0u, 0u);
-                                if (v < w.nw)
-                                    x[i] = reinterpret_cast<const uint4*>(a.swa + ((int64_t)w.b * a.swa_len + w.row0 + v) * D_LAT)[c];
-                                else if (v < w.rows)
-                                    x[i] = reinterpret_cast<const uint4*>(a.draft + ((int64_t)w.b * a.n_q + chain[v - w.nw]) * D_LAT)[c];
-                            }
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int at = i0 + i * TL_LOADERS, r = at >> 6, c = at & 63;
-                                mx = max(mx, bf16_absmax8(x[i]));
-                                *reinterpret_cast<uint4*>(L + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)) = bf16x8_to_f16x8(x[i], d);
-                            }
-                        }
-                    };
-                    convert(1.0f);
-                    mx = __reduce_max_sync(0xffffffffu, mx);
-                    if (lane == 0) atomicMax(&wmax[buf], mx);
-                    umma::bar_named(2, TL_LOADERS);
-                    const int e = f16_range_exp(*reinterpret_cast<volatile unsigned int*>(&wmax[buf]));
-                    if (e != 0) convert(pow2f(-e));
-                    umma::bar_named(2, TL_LOADERS);
-                    if (lt == 0) wexp[buf] = e, wmax[buf] = 0u;
+                    for (int i = 0; i < TL_TILE * 64 / TL_LOADERS; ++i) {
+                        const int r = (lt >> 6) + 4 * i, c = lt & 63;
+                        const bool there = v0 + r < w.rows;
+                        copy16(sa(L + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)), rows16 + (there ? (int)wrow[v0 + r] : 0) * D_LAT + 8 * c, there);
+                    }
+                    copy16_wait();
                     umma::fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
@@ -275,27 +248,25 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     if (lane == 0) umma::mbar_arrive(sa(&b_lfull[buf]));
                 }
             }
-        } else {
-            // ================= warps 0-11: Q: heads h0 .. h0+63 (zero rows past n_heads), bf16 -> fp16 slabs; a head whose largest
-            // magnitude lies outside [2^-10, 2^15) is scaled by a power of two on the way
-            umma::fence_before();
-            umma::bar_named(3, TL_LOADW * 32);           // the share before is done with Q, O and what the softmax keeps
-            umma::fence_after();
-            if (T > 0) {
+        } else if (T > 0 || warp < TL_SMW) {
+            if (warp >= TL_QW) {
+                // ================= Q: heads h0 .. h0+63 (zero rows past n_heads), bf16 -> fp16 slabs, once the softmax of the share
+                // before is done (not its scores alone: of a short share they may be before the softmax has looked at its
+                // queries' exponents); a head whose largest magnitude lies outside [2^-10, 2^15) is scaled by a power of two
                 const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + (w.gq * a.n_heads + w.h0) * D_LAT);
-#pragma unroll 1
-                for (int r0 = warp; r0 < TL_H; r0 += 2 * TL_LOADW) {
-                    uint4 x[2][2];
+                constexpr int NR = 4;                    // rows of a warp in flight
+                for (int r0 = warp - TL_QW; r0 < TL_H; r0 += NR * TL_QWARPS) {
+                    uint4 x[NR][2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = r0 + TL_LOADW * i;
+                    for (int i = 0; i < NR; ++i) {
+                        const int r = r0 + TL_QWARPS * i;
                         x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
                         if (r < nh) x[i][0] = qsrc[r * 64 + lane], x[i][1] = qsrc[r * 64 + 32 + lane];
                     }
+                    if (r0 == warp - TL_QW && tb > 0) ok = ok && umma::mbar_wait_fast(sa(&b_pfull[(tb - 1) & 1]), ((tb - 1) >> 1) & 1);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = r0 + TL_LOADW * i;
-                        if (r >= TL_H) break;
+                    for (int i = 0; i < NR; ++i) {
+                        const int r = r0 + TL_QWARPS * i;
                         const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
                         const float d = a.scale_log2e < 0.0f ? -pow2f(-e) : pow2f(-e);       // scores are taken times |scale|
 #pragma unroll
@@ -303,20 +274,22 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                             const int c = lane + 32 * hh;
                             *reinterpret_cast<uint4*>(sm + TL_SQ + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)) = bf16x8_to_f16x8(x[i][hh], d);
                         }
-                        if (lane == 0) qexp[r] = e;
+                        if (lane == 0) qexp[nq & 1][r] = e;
                     }
                 }
                 umma::fence_proxy_async();
-                if (tid < TL_H) m_run[tid] = -INFINITY;
-            }
-            umma::bar_named(3, TL_LOADW * 32);
-            if (warp >= TL_MMA1 && warp < TL_MMA2) {
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(sa(&b_q));
+                // every phase in turn, the last one at the next share: a wait tells a phase from the next by its parity alone
+                for (int t = 0; t + 1 < T; ++t) ok = ok && umma::mbar_wait_fast(sa(&b_pfull[(tb + t) & 1]), ((tb + t) >> 1) & 1);
+            } else if (warp >= TL_MMA1 && warp < TL_MMA2) {
                 // ================= scores of tile t once its dims are expanded.  The whole warp walks the tiles, so that
                 // descriptors and addresses stay in uniform registers; one elected lane issues.
                 const int half = warp - TL_MMA1;
                 const uint32_t id = umma::idesc_f16(64, TL_TILE, 0, 0);
                 const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
                 const uint64_t qd = umma::desc(base + TL_SQ, 16, 1024, umma::LAYOUT_SW128);
+                ok = ok && umma::mbar_wait_fast(sa(&b_q), nq & 1);
                 for (int t = 0; t < T; ++t) {
                     const uint32_t tg = tb + t, buf = tg & 1;
                     ok = ok && umma::mbar_wait_fast(sa(half == 0 ? &b_lhalf[buf] : &b_lfull[buf]), (tg >> 1) & 1);
@@ -362,14 +335,18 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     }
                     __syncwarp();
                 }
-            } else if (warp < TL_SMW) {
+            } else {
                 // ================= softmax: lane l of warp w has head 16 (w % 4) + l / 4 + 8 (l % 2) and, of keys 32 (w / 4) .. + 31,
                 // those of parity (l / 2) % 2 (the 16x64b TMEM shape)
                 const int qd = warp & 3, half = warp >> 2;
                 const int h = qd * 16 + (lane >> 2) + 8 * (lane & 1), par = (lane >> 1) & 1;
                 const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
+                if (tid < TL_H) m_run[tid] = -INFINITY;
+                if (T > 0) ok = ok && umma::mbar_wait_fast(sa(&b_q), nq & 1);
+                umma::bar_named(1, TL_SMT);
                 // never zero, so that a masked score stays -inf
-                const float mul4 = T > 0 ? fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[h]), 0x1p-100f) : 0.0f;
+                const float mul4 = T > 0 ? fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[nq & 1][h]), 0x1p-100f) : 0.0f;
+                const int wexp = a.t.seq[w.b].exp;
                 float lsum = 0.0f;
                 int oexp = 0;                        // O is 2^-oexp of what it stands for
                 for (int t = 0; t < T; ++t) {
@@ -387,7 +364,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                         for (int i = 0; i < 16; ++i) x[i] += x1[i];
                     }
                     const bool window = t < nwt;
-                    const int e = window ? *reinterpret_cast<volatile int*>(&wexp[buf]) : 0;
+                    const int e = window ? wexp : 0;
                     const float mul = fmaxf(mul4 * pow2f(e), 0x1p-126f);
                     uint32_t see;                    // which of the half's 32 keys are there
                     if (window) {
@@ -489,31 +466,38 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
                     umma::fence_after();
                     const float up = pow2f(oexp);
+                    auto store = [&](auto* dst) {            // row 0's first dim
+                        using TD = std::remove_pointer_t<decltype(dst)>;
 #pragma unroll 1
-                    for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
-                        const int dim = mt * 128 + qd * 32 + lane;
+                        for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
+                            TD* d = dst + mt * 128 + qd * 32 + lane;
 #pragma unroll 1
-                        for (int c = 0; c < nh; c += 16) {
-                            float v[16];
-                            umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c, v);
-                            umma::tmem_wait_ld();
+                            for (int c = 0; c < nh; c += 32) {
+                                float v[32];
+                                umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c, v);
+                                umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c + 16, v + 16);
+                                umma::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                if (c + i >= nh) break;
-                                const float y = ok ? v[i] * fac[c + i] * up : __int_as_float(0x7fc00000);
-                                if (whole)
-                                    reinterpret_cast<TO*>(a.out)[(orow + c + i) * D_LAT + dim] = from_f32<TO>(y);
-                                else
-                                    a.part_o[(prow + c + i) * D_LAT + dim] = y;
+                                for (int i = 0; i < 32; ++i) {
+                                    const float y = ok ? v[i] * fac[c + i] * up : __int_as_float(0x7fc00000);
+                                    if (c + i < nh) d[(c + i) * D_LAT] = from_f32<TD>(y);
+                                }
                             }
                         }
-                    }
+                    };
+                    if (whole)
+                        store(reinterpret_cast<TO*>(a.out) + orow * D_LAT);
+                    else
+                        store(a.part_o + prow * D_LAT);
                 } else if (whole) {
                     for (int i = tid; i < nh * D_LAT; i += TL_SMT) reinterpret_cast<TO*>(a.out)[orow * D_LAT + i] = from_f32<TO>(0.0f);
                 }
+                umma::fence_before();
+                umma::bar_named(1, TL_SMT);              // what the softmax keeps is read
             }
         }
         tb += T;
+        nq += T > 0;
     }
     if (!ok) atomicExch(a.err, 1);
     umma::fence_before();
@@ -550,8 +534,9 @@ int64_t lists_units(int batch, int n_q, int n_heads, int k) {
 }  // namespace
 
 size_t tree_lists_ws(int batch, int n_q, int n_heads, int k) {
+    const size_t nodes = tree_nodes_bytes(batch, n_q);
     const size_t rows = (size_t)2 * lists_blocks(lists_units(batch, n_q, n_heads, k)) * TL_H;
-    return TL_HEAD + rows * (D_LAT * sizeof(float) + sizeof(float2));
+    return TL_HEAD + nodes + rows * (D_LAT * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_tree_lists(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
@@ -560,15 +545,17 @@ cudaError_t launch_tree_lists(const csa2_cache& c, const uint16_t* q, int n_q, i
                               cudaStream_t st) {
     const int64_t units = lists_units(c.batch, n_q, n_heads, k);     // below 2^31: at most 65,535 x 128 nodes, 2 groups, 34 units
     const int blocks = lists_blocks(units);
-    ListArgs a{c.lat_codes, c.lat_scales, c.capacity, q, n_q, n_heads, (n_heads + TL_H - 1) / TL_H, q_pos, parent, draft, idx, k,
-               swa, swa_pos0, swa_len, scale * 1.4426950408889634f, out, lse, TL_WIN + (k + TL_TILE - 1) / TL_TILE,
-               (int)(units / blocks), (int)(units % blocks), nullptr, nullptr, reinterpret_cast<int*>(ws)};
-    uint8_t* w = reinterpret_cast<uint8_t*>(ws) + TL_HEAD;
+    TreeCall call{c.batch, c.capacity, c.ratio, n_q, n_heads, q_pos, parent, draft, swa, swa_pos0, swa_len, {}, nullptr, nullptr, 0};
+    uint8_t* w = tree_nodes_take(call.t, c.batch, n_q, reinterpret_cast<uint8_t*>(ws) + TL_HEAD);
+    ListArgs a{c.lat_codes, c.lat_scales, c.capacity, q, n_q, n_heads, (n_heads + TL_H - 1) / TL_H, call.t, idx, k,
+               scale * 1.4426950408889634f, out, lse, TL_WIN + (k + TL_TILE - 1) / TL_TILE, (int)(units / blocks),
+               (int)(units % blocks), nullptr, nullptr, reinterpret_cast<int*>(ws)};
     a.part_o = reinterpret_cast<float*>(w);
     a.part_ml = reinterpret_cast<float2*>(w + (size_t)2 * blocks * TL_H * D_LAT * sizeof(float));
     auto go = [&](auto* y) {
         using TO = std::remove_pointer_t<decltype(y)>;
-        const cudaError_t e = cudaFuncSetAttribute(k_tree_lists<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TL_DYN);
+        cudaError_t e = cudaFuncSetAttribute(k_tree_lists<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TL_DYN);
+        if (e == cudaSuccess) e = launch_tree_prep(call, st);
         if (e != cudaSuccess) return e;
         launch_k(k_tree_lists<TO>, dim3((unsigned)blocks), TL_THREADS, TL_DYN, st, a);
         note_launch();

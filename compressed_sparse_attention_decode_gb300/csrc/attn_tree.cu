@@ -29,12 +29,12 @@
 // Rows, running maxima, sums and outputs of a row stay in its CTA: the pair shares nothing but the MMAs.
 #include <algorithm>
 #include <type_traits>
-#include <utility>
 
 #include "attn_join.cuh"
 #include "common.cuh"
 #include "elem.cuh"
 #include "fp4_f16.cuh"
+#include "tree.cuh"
 #include "umma.cuh"
 
 namespace csa2 {
@@ -77,145 +77,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// what the nodes of a sequence attend to, all together
-struct TreeSeq {
-    int n_vis;                   // entries 0 .. n_vis-1
-    int nw, n_rows;              // committed window rows, and with the drafts up to the last node that is there
-    int row_tiles;               // items
-    int exp;                     // the window rows and drafts go to fp16 after a division by 2^exp
-    int w0;                      // the window row that is the first committed one
-    uint32_t there[4];           // the nodes that are there
-    int pad[2];
-    __device__ __forceinline__ int wtiles() const { return (n_rows + TR_TILE - 1) / TR_TILE; }
-    __device__ __forceinline__ int tiles() const { return wtiles() + (int)(((unsigned)n_vis + TR_TILE - 1) / TR_TILE); }
-};
 // an item that several pairs share: the slot of its first share, and how many there are
 struct TreeHead {
     int b, rt, slot, n;
 };
 struct TreeArgs {
     const uint8_t *codes, *scales;
-    int batch, capacity, ratio;
+    int batch, capacity;
     const uint16_t* q;
     int n_q, n_heads;
-    const int64_t* q_pos;
-    const int32_t* parent;
-    const uint16_t* draft;
-    const uint16_t* swa;
-    const int64_t* swa_pos0;
-    int swa_len;
     float scale_log2e;
     void* out;
     float* lse;
-    TreeSeq* seq;                // [batch]
-    int* node_vis;               // [batch][n_q] entries that a node sees
-    uint32_t* node_mask;         // [batch][n_q][8] which of the n_rows rows
+    TreeNodes t;
     TreeHead* heads;             // [pairs]
     float* part_o;               // [2 pairs][128][512]
     float2* part_ml;             // [2 pairs][128] reference (log2) and row sum
     int* err;
 };
 
-// One block a sequence (and some that write the rows of nodes that are not there): chains, masks, the rows' scale.
-template <typename TO>
-__global__ void __launch_bounds__(1024) k_tree_prep(const __grid_constant__ TreeArgs a) {
-    __shared__ int parent[TREE_NODES], last_s, vis_s;
-    __shared__ long long hi_s;
-    __shared__ uint32_t there[4], mx_s;
-    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x, N = a.n_q;
-    if (tid == 0) last_s = -1, vis_s = 0, mx_s = 0u, hi_s = -1;
-    if (tid < 4) there[tid] = 0u;
-    pdl_wait();
-    pdl_launch_next();
-    if (tid < N) parent[tid] = a.parent[(int64_t)b * N + tid];
-    __syncthreads();
-    int len = 0;
-    uint32_t anc[4] = {0u, 0u, 0u, 0u};
-    int64_t p = 0;
-    if (tid < N) {
-        p = a.q_pos[(int64_t)b * N + tid];
-        int j = tid;
-        while (j >= 0) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                if ((j >> 5) == w) anc[w] |= 1u << (j & 31);
-            ++len;
-            const int up = parent[j];
-            j = up >= -1 && up < j ? up : -2;
-        }
-        if (j != -1) len = 0;
-        if (len > 0) {
-            atomicOr(&there[tid >> 5], 1u << lane);
-            atomicMax(&last_s, tid);
-        }
-    }
-    __syncthreads();
-    const int last = last_s;
-    const int row_tiles = ((last + 1) * a.n_heads + TR_ROWS - 1) / TR_ROWS;
-    if (blockIdx.y > 0) {
-        // rows of items that nobody works on
-        const int64_t r0 = (int64_t)row_tiles * TR_ROWS, r1 = (int64_t)N * a.n_heads, base = (int64_t)b * r1;
-        constexpr int E = 16 / (int)sizeof(TO);
-        uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<TO*>(a.out) + base * D_LAT);
-        const int64_t step = (int64_t)(gridDim.y - 1) * 1024, first = (int64_t)(blockIdx.y - 1) * 1024 + tid;
-        for (int64_t i = r0 * (D_LAT / E) + first; i < r1 * (D_LAT / E); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.lse != nullptr)
-            for (int64_t i = r0 + first; i < r1; i += step) a.lse[base + i] = -INFINITY;
-        return;
-    }
-    // every child of the last committed token stands at the same position: the one after hi
-    if (len > 0 && parent[tid] == -1) hi_s = p - len;
-    __syncthreads();
-    const int64_t s0 = a.swa_pos0 ? a.swa_pos0[b] : 0, hi0 = hi_s;
-    const int64_t lo = max(max((int64_t)0, hi0 - (WINDOW - 2)), s0), hi = min(hi0, s0 + a.swa_len - 1);
-    const int nw = last >= 0 && hi >= lo ? (int)(hi - lo + 1) : 0;       // at most 127
-    const int n_rows = last >= 0 ? nw + last + 1 : 0;
-    if (tid < N) {
-        int vis = 0;
-        uint32_t m[8] = {};
-        if (len > 0) {
-            vis = (int)min(p >= WINDOW - 1 ? (p - (WINDOW - 1)) >> (a.ratio - 1) : (int64_t)0, (int64_t)a.capacity);
-            atomicMax(&vis_s, vis);
-            const int c0 = (int)max((int64_t)0, min((int64_t)nw, p - (WINDOW - 1) - lo));        // committed rows c0 .. nw-1
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const int f = max(c0 - 32 * w, 0), e = min(nw - 32 * w, 32);
-                if (f < e) m[w] = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & ~((1u << f) - 1u);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {            // drafts: bit j of the chain at row nw + j
-                    const int at = nw + 32 * v - 32 * w;
-                    if (at >= 0 && at < 32) m[w] |= anc[v] << at;
-                    if (at < 0 && at > -32) m[w] |= anc[v] >> -at;
-                }
-            }
-        }
-        a.node_vis[(int64_t)b * N + tid] = vis;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) a.node_mask[((int64_t)b * N + tid) * 8 + w] = m[w];
-    }
-    // the largest magnitude of the rows (at most 255, 64 pieces each): all loads in flight
-    uint32_t mx = 0u;
-    const uint4* win = reinterpret_cast<const uint4*>(a.swa + ((int64_t)b * a.swa_len + (lo - s0)) * D_LAT);
-    const uint4* dr = reinterpret_cast<const uint4*>(a.draft + (int64_t)b * N * D_LAT);
-    uint4 x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int v = tid + i * 1024, r = v >> 6, j = r - nw;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < nw)
-            x[i] = win[v];
-        else if (r < n_rows && ((there[j >> 5] >> (j & 31)) & 1u))
-            x[i] = dr[v - nw * 64];
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) mx = max(mx, bf16_absmax8(x[i]));
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 0) atomicMax(&mx_s, mx);
-    __syncthreads();
-    if (tid == 0) {
-        TreeSeq s{vis_s, nw, n_rows, row_tiles, f16_range_exp(mx_s), (int)(lo - s0), {there[0], there[1], there[2], there[3]}, {0, 0}};
-        a.seq[b] = s;
-    }
+__device__ __forceinline__ int tr_tiles(const TreeSeq& s) {
+    return (s.n_rows + TR_TILE - 1) / TR_TILE + (int)(((unsigned)s.n_vis + TR_TILE - 1) / TR_TILE);
 }
 
 // Where a pair stands in its part of all units, and the share that comes next.  (32 bits: a cache that fills the memory has
@@ -228,9 +110,9 @@ struct TreeShare {
 };
 __device__ __forceinline__ bool tr_next(const TreeArgs& a, TreeCursor& c, TreeShare& h) {
     while (c.left > 0) {
-        const TreeSeq* s = a.seq + c.b;
-        h.wt = s->wtiles();
-        h.T = s->tiles();
+        const TreeSeq* s = a.t.seq + c.b;
+        h.wt = (s->n_rows + TR_TILE - 1) / TR_TILE;
+        h.T = tr_tiles(*s);
         const int per = h.T + TR_OVER;
         if (c.off >= s->row_tiles * per) {
             ++c.b, c.off = 0;
@@ -287,8 +169,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
     const int per = (a.batch + TR_THREADS - 1) / TR_THREADS;
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     auto units = [&](int b) {
-        const TreeSeq s = a.seq[b];
-        return (int64_t)s.row_tiles * (s.tiles() + TR_OVER);
+        const TreeSeq s = a.t.seq[b];
+        return (int64_t)s.row_tiles * (tr_tiles(s) + TR_OVER);
     };
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += units(b);
@@ -355,16 +237,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     e2m1x8_scaled(words[k], (k >> 1) ? s_hi : s_lo);
             }
         };
-        // row v of the window rows and drafts, 8 dims at chunk cc
-        auto bf16_row = [&](int v, int cc) {
-            const TreeSeq* s = a.seq + h.b;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            const int j = v - s->nw;
-            if (j < 0)
-                x = *reinterpret_cast<const uint4*>(a.swa + ((int64_t)h.b * a.swa_len + s->w0 + v) * D_LAT + 8 * cc);
-            else if (v < s->n_rows && ((s->there[j >> 5] >> (j & 31)) & 1u))
-                x = *reinterpret_cast<const uint4*>(a.draft + ((int64_t)h.b * a.n_q + j) * D_LAT + 8 * cc);
-            return bf16x8_to_f16x8(x, pow2f(-s->exp));
+        // row v of the window rows and drafts, 8 dims at chunk cc, to dst
+        auto copy_row = [&](int v, int cc, uint8_t* dst) {
+            const bool there = v < a.t.seq[h.b].n_rows;
+            copy16(sa(dst), a.t.rows16 + ((int64_t)h.b * a.t.row_stride + (there ? v : 0)) * D_LAT + 8 * cc, there);
         };
         // each thread orders its own writes for the tensor core, then one arrival per warp, in CTA 0
         auto arrive = [&](unsigned long long* bar) {
@@ -378,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             // lines of codes, and the 8 threads of a quarter warp write different bank groups
             const int lt = tid - TR_OWNW * 32, lw = warp - TR_OWNW;
             while (tr_next(a, cur, h)) {
-                const int T = h.t1 - h.t0, wt = h.wt, n_vis = a.seq[h.b].n_vis;
+                const int T = h.t1 - h.t0, wt = h.wt, n_vis = a.t.seq[h.b].n_vis;
                 const uint8_t* codes = a.codes + (int64_t)h.b * a.capacity * (D_LAT / 2);
                 const uint8_t* scales = a.scales + (int64_t)h.b * a.capacity * (D_LAT / 16);
                 uint4 cw[4];
@@ -401,8 +277,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
 #pragma unroll 4
                             for (int i = lt; i < 64 * 32; i += TR_OWN) {
                                 const int r = i >> 5, cc = 32 * half + (i & 31);
-                                *reinterpret_cast<uint4*>(L + (cc >> 3) * TR_SLAB + tr_swz(r, cc & 7)) = bf16_row(v0 + r, cc);
+                                copy_row(v0 + r, cc, L + (cc >> 3) * TR_SLAB + tr_swz(r, cc & 7));
                             }
+                            copy16_wait();
                         } else {
 #pragma unroll
                             for (int i = 2 * half; i < 2 * half + 2; ++i)
@@ -419,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             const int lt = tid - TR_FORW * 32, lw = warp - TR_FORW;
             const int c = 8 * (ku >> 2) + 4 * (int)rank + (ku & 3);
             while (tr_next(a, cur, h)) {
-                const int T = h.t1 - h.t0, wt = h.wt, n_vis = a.seq[h.b].n_vis;
+                const int T = h.t1 - h.t0, wt = h.wt, n_vis = a.t.seq[h.b].n_vis;
                 const uint8_t* codes = a.codes + (int64_t)h.b * a.capacity * (D_LAT / 2);
                 const uint8_t* scales = a.scales + (int64_t)h.b * a.capacity * (D_LAT / 16);
                 uint4 cw[4];
@@ -441,8 +318,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                         for (int i = lt; i < 64 * 32; i += TR_FOR) {
                             const int r = i >> 5, cs = i & 31;       // this CTA's 32 chunks: 16 of dims 128 r .., 16 of 256 + 128 r ..
                             const int cc = 32 * (cs >> 4) + 16 * (int)rank + (cs & 15);
-                            *reinterpret_cast<uint4*>(L + ((cc >> 3) ^ 2) * TR_SLAB + tr_swz(r, cc & 7)) = bf16_row(v0 + r, cc);
+                            copy_row(v0 + r, cc, L + ((cc >> 3) ^ 2) * TR_SLAB + tr_swz(r, cc & 7));
                         }
+                        copy16_wait();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) expand(L, 16 * i + 4 * lw + kr, c, 2, cw[i], sc[i]);
@@ -559,13 +437,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 umma::bar_named(3, TR_SMT);
             }
             // never zero, so that a masked score stays -inf (a score of nearly nothing for a scale of nothing)
-            const float mul4 = fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[row]), 0x1p-100f), up = pow2f(a.seq[h.b].exp);
+            const float mul4 = fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[row]), 0x1p-100f), up = pow2f(a.t.seq[h.b].exp);
             int vis = 0;
             const uint32_t* mask = nullptr;
             if (q0 + row < n_rows_q) {
                 const int64_t node = (int64_t)h.b * a.n_q + (int)((unsigned)(q0 + row) / (unsigned)a.n_heads);
-                vis = a.node_vis[node];
-                mask = a.node_mask + node * 8 + 2 * kh + ch;
+                vis = a.t.vis[node];
+                mask = a.t.mask + node * 8 + 2 * kh + ch;
             }
             float m = -INFINITY, lsum = 0.0f;
             for (int t = 0; t < T; ++t) {
@@ -763,12 +641,10 @@ cudaError_t launch_tree_lists(const csa2_cache& c, const uint16_t* q, int n_q, i
 
 namespace {
 constexpr size_t TR_HEAD = 256;                      // the error word and padding
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct TreePlan {
     int row_tiles, pairs;
-    size_t seq, vis, mask, heads, o, ml;             // bytes of the workspace's parts
-    size_t total() const { return TR_HEAD + seq + vis + mask + heads + o + ml; }
+    size_t heads, o, ml;                             // bytes of the workspace's parts after the nodes'
 };
 TreePlan tree_plan(int batch, int n_q, int n_heads, int64_t capacity) {
     TreePlan p;
@@ -776,10 +652,7 @@ TreePlan tree_plan(int batch, int n_q, int n_heads, int64_t capacity) {
     // fewer pairs where even a full cache has fewer tiles
     const int64_t tiles = (capacity + TR_TILE - 1) / TR_TILE + 2;
     p.pairs = (int)std::min<int64_t>(TR_PAIRS, (int64_t)batch * p.row_tiles * tiles);
-    p.seq = up256((size_t)batch * sizeof(TreeSeq));
-    p.vis = up256((size_t)batch * n_q * sizeof(int));
-    p.mask = up256((size_t)batch * n_q * 8 * sizeof(uint32_t));
-    p.heads = up256((size_t)p.pairs * sizeof(TreeHead));
+    p.heads = ((size_t)p.pairs * sizeof(TreeHead) + 255) / 256 * 256;
     p.o = (size_t)2 * p.pairs * TR_ROWS * D_LAT * sizeof(float);
     p.ml = (size_t)2 * p.pairs * TR_ROWS * sizeof(float2);
     return p;
@@ -788,7 +661,9 @@ TreePlan tree_plan(int batch, int n_q, int n_heads, int64_t capacity) {
 
 size_t tree_attn_ws(int batch, int n_q, int n_heads, int k, int64_t capacity) {
     const size_t lists = k >= 0 ? tree_lists_ws(batch, n_q, n_heads, k) : 0;
-    return k > 0 ? lists : std::max(lists, tree_plan(batch, n_q, n_heads, capacity).total());
+    if (k > 0) return lists;
+    const TreePlan p = tree_plan(batch, n_q, n_heads, capacity);
+    return std::max(lists, TR_HEAD + tree_nodes_bytes(batch, n_q) + p.heads + p.o + p.ml);
 }
 
 cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
@@ -799,22 +674,20 @@ cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, in
         return launch_tree_lists(c, q, n_q, n_heads, q_pos, parent, draft, idx, k, swa, swa_pos0, swa_len, scale, out, out_type, lse,
                                  ws, st);
     const TreePlan p = tree_plan(c.batch, n_q, n_heads, c.capacity);
-    uint8_t* w = reinterpret_cast<uint8_t*>(ws) + TR_HEAD;
-    auto take = [&](size_t n) { return std::exchange(w, w + n); };
-    TreeArgs a{c.lat_codes, c.lat_scales, c.batch, c.capacity, c.ratio, q, n_q, n_heads, q_pos, parent, draft, swa, swa_pos0, swa_len,
-               scale * 1.4426950408889634f, out, lse, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, reinterpret_cast<int*>(ws)};
-    a.seq = reinterpret_cast<TreeSeq*>(take(p.seq));
-    a.node_vis = reinterpret_cast<int*>(take(p.vis));
-    a.node_mask = reinterpret_cast<uint32_t*>(take(p.mask));
-    a.heads = reinterpret_cast<TreeHead*>(take(p.heads));
-    a.part_o = reinterpret_cast<float*>(take(p.o));
-    a.part_ml = reinterpret_cast<float2*>(take(p.ml));
+    TreeCall call{c.batch, c.capacity, c.ratio, n_q, n_heads, q_pos, parent, draft, swa, swa_pos0, swa_len, {}, out, lse,
+                  out_type == CSA2_F32 ? 4 : 2};
+    uint8_t* w = tree_nodes_take(call.t, c.batch, n_q, reinterpret_cast<uint8_t*>(ws) + TR_HEAD);
+    TreeArgs a{c.lat_codes, c.lat_scales, c.batch, c.capacity, q, n_q, n_heads, scale * 1.4426950408889634f, out, lse, call.t,
+               nullptr, nullptr, nullptr, reinterpret_cast<int*>(ws)};
+    a.heads = reinterpret_cast<TreeHead*>(w);
+    a.part_o = reinterpret_cast<float*>(w + p.heads);
+    a.part_ml = reinterpret_cast<float2*>(w + p.heads + p.o);
     auto go = [&](auto* y) {
         using TO = std::remove_pointer_t<decltype(y)>;
         cudaError_t e = cudaFuncSetAttribute(k_tree_attn<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TR_DYN);
         if (e != cudaSuccess) return e;
-        const int zero = std::min(16, (n_q * n_heads + 511) / 512);      // blocks that write the rows of nodes that are not there
-        launch_k(k_tree_prep<TO>, dim3((unsigned)c.batch, (unsigned)(1 + zero)), 1024, 0, st, a);
+        e = launch_tree_prep(call, st);
+        if (e != cudaSuccess) return e;
         launch_k(k_tree_attn<TO>, dim3((unsigned)(2 * p.pairs)), TR_THREADS, TR_DYN, st, a);
         // few items: many shares each, so a block per row
         const int64_t items = (int64_t)c.batch * p.row_tiles;
@@ -823,7 +696,7 @@ cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, in
             launch_k(k_tree_join<TO, 4>, dim3((unsigned)items, (unsigned)rows), 512, 0, st, a, p.pairs, p.row_tiles);
         else
             launch_k(k_tree_join<TO, 1>, dim3((unsigned)p.pairs, (unsigned)((rows + 3) / 4)), 512, 0, st, a, p.pairs, p.row_tiles);
-        note_launch(3);
+        note_launch(2);
         return cudaGetLastError();
     };
     return out_type == CSA2_F32   ? go(reinterpret_cast<float*>(out))

@@ -1,0 +1,45 @@
+// What both kernels of drafted trees (attn_tree.cu: every visible entry, attn_list.cu: index lists) take from k_tree_prep.
+#pragma once
+#include "common.cuh"
+
+namespace csa2 {
+
+// what the nodes of a sequence attend to, all together
+struct TreeSeq {
+    int n_vis;                   // entries 0 .. n_vis-1
+    int n_rows;                  // rows of rows16: the committed window rows, then the drafts up to the last node that is there
+    int row_tiles;               // items of attn_tree.cu
+    int exp;                     // rows16 are the rows' values divided by 2^exp
+};
+// A call's parts of the workspace that k_tree_prep writes
+struct TreeNodes {
+    TreeSeq* seq;                // [batch]
+    int* vis;                    // [batch][n_q] entries that a node sees
+    uint32_t* mask;              // [batch][n_q][8] which of the n_rows rows; none for a node that is not there
+    uint16_t* rows16;            // [batch][row_stride][512] fp16: window rows and drafts, zeros for drafts that are not there
+    int row_stride;
+};
+struct TreeCall {
+    int batch, capacity, ratio, n_q, n_heads;
+    const int64_t* q_pos;
+    const int32_t* parent;
+    const uint16_t* draft;
+    const uint16_t* swa;
+    const int64_t* swa_pos0;
+    int swa_len;
+    TreeNodes t;
+    void* out;                   // rows of items that nobody works on are written by k_tree_prep (out_size 0: none)
+    float* lse;
+    int out_size;                // bytes of an element
+};
+size_t tree_nodes_bytes(int batch, int n_q);
+uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, uint8_t* w);       // from a workspace's byte w on; the first byte after it
+cudaError_t launch_tree_prep(const TreeCall& c, cudaStream_t st);
+
+// 16 bytes from global to shared memory, zeros where `there` is false
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+}  // namespace csa2
