@@ -13,35 +13,43 @@ template <typename TO, int SPREAD, typename F>
 __device__ __forceinline__ void join_row(const float* part_o, const float2* part_ml, int n, F&& share, TO* out, float* lse) {
     __shared__ float4 sums[SPREAD > 1 ? 3 : 1][128];
     const int tid = threadIdx.x, dim = tid & 127, group = SPREAD > 1 ? tid >> 7 : 0, lane = tid & 31;
-    constexpr int NB = 8;                            // shares in flight
-    float m = -INFINITY, l = 0.0f;
-    for (int s = lane; s < n; s += 32) {
-        const float2 v = part_ml[share(s)];
-        if (v.y != 0.0f) m = fmaxf(m, v.x);
+    constexpr int NB = SPREAD > 1 ? 8 : 4, NK = 3;   // shares in flight; at most 96 in all
+    float4 x[NB];
+    auto load = [&](int s0) {                        // (past the end: the last one again, times nothing)
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            if (i == 0 || s0 + i * SPREAD < n)
+                x[i] = reinterpret_cast<const float4*>(part_o + (int64_t)share(min(s0 + i * SPREAD, n - 1)) * D_LAT)[dim];
+    };
+    load(group);                                     // before the factors are known
+    float f[NK], m = -INFINITY, l = 0.0f;
+    float2 v[NK];
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        v[k] = make_float2(-INFINITY, 0.0f);
+        if (32 * k + lane < n) v[k] = part_ml[share(32 * k + lane)];
+        if (v[k].y != 0.0f) m = fmaxf(m, v[k].x);
     }
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int s = lane; s < n; s += 32) {
-        const float2 v = part_ml[share(s)];
-        if (v.y != 0.0f) l = fmaf(exp2f(v.x - m), v.y, l);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        f[k] = v[k].y != 0.0f ? exp2f(v[k].x - m) : 0.0f;
+        l = fmaf(f[k], v[k].y, l);
     }
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     float o[4] = {};
-    for (int s0 = group; s0 < n; s0 += NB * SPREAD) {
-        float4 x[NB];
-        float2 v[NB];
+    for (int s0 = group; s0 < n;) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int64_t at = share(min(s0 + i * SPREAD, n - 1));
-            x[i] = reinterpret_cast<const float4*>(part_o + at * D_LAT)[dim];
-            v[i] = part_ml[at];
+            const int s = s0 + i * SPREAD;
+            if (s >= n) break;
+            const float w = __shfl_sync(0xffffffffu, s < 32 ? f[0] : s < 64 ? f[1] : f[2], s & 31);
+            if (w == 0.0f) continue;
+            o[0] = fmaf(w, x[i].x, o[0]), o[1] = fmaf(w, x[i].y, o[1]);
+            o[2] = fmaf(w, x[i].z, o[2]), o[3] = fmaf(w, x[i].w, o[3]);
         }
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            if (s0 + i * SPREAD >= n || v[i].y == 0.0f) continue;
-            const float f = exp2f(v[i].x - m);
-            o[0] = fmaf(f, x[i].x, o[0]), o[1] = fmaf(f, x[i].y, o[1]);
-            o[2] = fmaf(f, x[i].z, o[2]), o[3] = fmaf(f, x[i].w, o[3]);
-        }
+        s0 += NB * SPREAD;
+        if (s0 < n) load(s0);
     }
     if constexpr (SPREAD > 1) {
         if (group > 0) sums[group - 1][dim] = make_float4(o[0], o[1], o[2], o[3]);

@@ -95,7 +95,8 @@ template <typename TO>
 __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_constant__ ListArgs a) {
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2], b_q;
-    __shared__ float red[2][TL_H], m_run[TL_H], fac[TL_H];
+    __shared__ float red[2][TL_H], m_run[TL_H];
+    __shared__ __align__(16) float fac[TL_H];
     __shared__ int qexp[2][TL_H], any[4];
     __shared__ uint32_t slot_ok[2][2], tmem_base;
     __shared__ uint8_t wrow[WINDOW];                         // the rows of rows16 that the share's node attends to
@@ -280,6 +281,14 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                 umma::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(sa(&b_q));
+                // the next share's queries, if it is another item's, on their way while this one runs
+                if (u < u1) {
+                    const int next = (unsigned)u / (unsigned)a.per;
+                    const int64_t g = a.hgroups == 1 ? next : next >> 1;
+                    const int nh0 = a.hgroups == 1 ? 0 : (next & 1) * TL_H;
+                    const char* src = reinterpret_cast<const char*>(a.q + (g * a.n_heads + nh0) * D_LAT);
+                    for (int i = tid - TL_QW * 32; i < min(TL_H, a.n_heads - nh0) * 8; i += TL_QWARPS * 32) umma::prefetch_l2(src + i * 128);
+                }
                 // every phase in turn, the last one at the next share: a wait tells a phase from the next by its parity alone
                 for (int t = 0; t + 1 < T; ++t) ok = ok && umma::mbar_wait_fast(sa(&b_pfull[(tb + t) & 1]), ((tb + t) >> 1) & 1);
             } else if (warp >= TL_MMA1 && warp < TL_MMA2) {
@@ -346,7 +355,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                 umma::bar_named(1, TL_SMT);
                 // never zero, so that a masked score stays -inf
                 const float mul4 = T > 0 ? fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[nq & 1][h]), 0x1p-100f) : 0.0f;
-                const int wexp = a.t.seq[w.b].exp;
+                // the window rows' part of O carries 2^-wexp; a row of another exponent enters with its weight scaled by the difference
+                bool scaled;
+                const int wexp = max(tree_exp(a.t, w.b, a.t.seq[w.b].n_rows, scaled), -100);
                 float lsum = 0.0f;
                 int oexp = 0;                        // O is 2^-oexp of what it stands for
                 for (int t = 0; t < T; ++t) {
@@ -365,7 +376,6 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     }
                     const bool window = t < nwt;
                     const int e = window ? wexp : 0;
-                    const float mul = fmaxf(mul4 * pow2f(e), 0x1p-126f);
                     uint32_t see;                    // which of the half's 32 keys are there
                     if (window) {
                         const int left = w.rows - (wa + t) * TL_TILE - 32 * half;
@@ -374,7 +384,14 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                         see = *reinterpret_cast<volatile uint32_t*>(&slot_ok[buf][half]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] *= mul;
+                    for (int i = 0; i < 16; ++i) x[i] *= mul4;
+                    // exponent of the row that key par + 2i is, 0 for none
+                    auto rexp = [&](int i) {
+                        return (see >> (par + 2 * i)) & 1u ? (int)a.t.exps[w.b * 256 + wrow[(wa + t) * TL_TILE + 32 * half + par + 2 * i]] : 0;
+                    };
+                    if (window && scaled)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] *= pow2f(rexp(i));
                     if (see != 0xffffffffu)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -431,6 +448,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                         sum[i & 1] += x[i];
                     }
                     lsum += sum[0] + sum[1];
+                    if (window && scaled)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] *= pow2f(max(rexp(i) - wexp, -126));
                     // row h of P^T: trade half of the values with the lane of the other parity for 16 consecutive keys
                     float rv[8];
 #pragma unroll
@@ -465,7 +485,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     const uint32_t tl = tb + T - 1;
                     ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
                     umma::fence_after();
-                    const float up = pow2f(oexp);
+                    const float up = ok ? pow2f(oexp) : __int_as_float(0x7fc00000);
                     auto store = [&](auto* dst) {            // row 0's first dim
                         using TD = std::remove_pointer_t<decltype(dst)>;
 #pragma unroll 1
@@ -478,9 +498,12 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                                 umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c + 16, v + 16);
                                 umma::tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const float y = ok ? v[i] * fac[c + i] * up : __int_as_float(0x7fc00000);
-                                    if (c + i < nh) d[(c + i) * D_LAT] = from_f32<TD>(y);
+                                for (int i = 0; i < 32; i += 4) {
+                                    const float4 f = *reinterpret_cast<const float4*>(fac + c + i);
+                                    const float f4[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        if (c + i + j < nh) d[(c + i + j) * D_LAT] = from_f32<TD>(v[i + j] * f4[j] * up);
                                 }
                             }
                         }

@@ -436,8 +436,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 if (lane == 0) umma::mbar_arrive_pair(r_q);
                 umma::bar_named(3, TR_SMT);
             }
+            // the window rows' part of O carries 2^-wexp; a row of another exponent enters with its weight scaled by the difference
+            bool scaled;
+            const int wexp = max(tree_exp(a.t, h.b, a.t.seq[h.b].n_rows, scaled), -100);
             // never zero, so that a masked score stays -inf (a score of nearly nothing for a scale of nothing)
-            const float mul4 = fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[row]), 0x1p-100f), up = pow2f(a.t.seq[h.b].exp);
+            const float mul4 = fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[row]), 0x1p-100f);
             int vis = 0;
             const uint32_t* mask = nullptr;
             if (q0 + row < n_rows_q) {
@@ -446,14 +449,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 mask = a.t.mask + node * 8 + 2 * kh + ch;
             }
             float m = -INFINITY, lsum = 0.0f;
-            for (int t = 0; t < T; ++t) {
+            // this row's O times f
+            auto scale_o = [&](float f) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                    float v[16];
+                    umma::tmem_ld16(lane_base + TRT_O + 128 * ch + c, v);
+                    umma::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] *= f;
+                    umma::tmem_st16(lane_base + TRT_O + 128 * ch + c, v);
+                }
+                umma::tmem_wait_st();
+            };
+            // one tile, of the window or of entries (two copies, so that the entries' carries nothing of the window's)
+            auto step = [&](auto is_window, int t) {
+                constexpr bool window = decltype(is_window)::value;
                 const uint32_t tg = tb + t, buf = tg & 1, ph = (tg >> 1) & 1;
                 const int tile = h.t0 + t;
-                const bool window = tile < wt;
                 uint32_t see = 0xffffffffu;          // which of the 32 keys this row attends to
-                if (window)
+                if constexpr (window) {
                     see = mask != nullptr ? mask[4 * tile] : 0u;
-                else {
+                } else {
                     const int left = vis - ((tile - wt) * TR_TILE + 64 * kh + 32 * ch);
                     if (left < 32) see = left <= 0 ? 0u : (1u << left) - 1u;
                 }
@@ -463,7 +480,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 umma::tmem_ld16(lane_base + TRT_S + 64 * buf + 32 * ch, x);
                 umma::tmem_ld16(lane_base + TRT_S + 64 * buf + 32 * ch + 16, x + 16);
                 umma::tmem_wait_ld();
-                const float mul = window ? fmaxf(mul4 * up, 0x1p-126f) : mul4;
+                float mul = mul4;
+                const bool odd = window && scaled;   // rows of an exponent of their own (in masked places there may be none)
+                if (odd) {
+                    const int8_t* rexp = a.t.exps + h.b * 256 + tile * TR_TILE + 64 * kh + 32 * ch;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = (see >> i) & 1u ? x[i] * mul4 * pow2f(rexp[i]) : 0.0f;
+                    mul = 1.0f;
+                }
                 if (see != 0xffffffffu)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -474,9 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     m4[i] = max3(max3(x[8 * i], x[8 * i + 1], x[8 * i + 2]), max3(x[8 * i + 3], x[8 * i + 4], x[8 * i + 5]),
                                  fmaxf(x[8 * i + 6], x[8 * i + 7]));
                 const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * mul;
-                // the window tiles' part of O carries 2^-exp: it is brought to the common scale before the entries' is added
-                const bool rescale_window = !window && tile == wt && t > 0 && up != 1.0f;
-                const bool raise = umma::bar_red_or(1 + (qd & 1), TR_SMT / 2, mx - m > TR_TOP) || rescale_window;
+                const bool raise = umma::bar_red_or(1 + (qd & 1), TR_SMT / 2, mx - m > TR_TOP);
                 // (the P buffer is free: these scores' keys were expanded after the values of the tile before in it; and S is
                 // read before P is handed on, without which its buffer is not written again)
                 if (raise) {
@@ -493,27 +515,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                         m = mt - TR_UP;
                     }
                     lsum *= f;
-                    if (rescale_window) f *= up;
                     if (t >= 1) {
                         ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);      // O settled
                         umma::fence_after();
-                        if (__any_sync(0xffffffffu, f != 1.0f)) {
-#pragma unroll 1
-                            for (int c = 0; c < 128; c += 16) {
-                                float v[16];
-                                umma::tmem_ld16(lane_base + TRT_O + 128 * ch + c, v);
-                                umma::tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) v[i] *= f;
-                                umma::tmem_st16(lane_base + TRT_O + 128 * ch + c, v);
-                            }
-                            umma::tmem_wait_st();
-                        }
+                        if (__any_sync(0xffffffffu, f != 1.0f)) scale_o(f);
                     }
                     umma::bar_named(1 + (qd & 1), TR_SMT / 2);        // red is read
                 }
                 const float ref = m == -INFINITY ? 0.0f : -m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (odd) {                           // the sum is of the weights as they are, P of what their rows need
+                    const int8_t* rexp = a.t.exps + h.b * 256 + tile * TR_TILE + 64 * kh + 32 * ch;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        lsum += umma::ex2_ftz(x[i] + ref);
+                        if ((see >> i) & 1u) x[i] += (float)(rexp[i] - wexp);
+                    }
+                }
                 uint8_t* P = sm + TR_SP + buf * TR_PBUF + kh * TR_SLAB;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -528,12 +546,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     }
                     *reinterpret_cast<uint4*>(P + tr_swz(row, 4 * ch + c)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                lsum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if (!odd) lsum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 umma::fence_proxy_async();
                 umma::fence_before();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive_pair(r_pfull[buf]);
+            };
+            const int T_win = max(0, min(wt - h.t0, T));
+#pragma unroll 1
+            for (int t = 0; t < T_win; ++t) step(std::true_type{}, t);
+            if (T_win > 0 && T_win < T && wexp != 0) {           // the window's part of O to the entries' scale
+                const uint32_t tl = tb + T_win - 1;
+                ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
+                umma::fence_after();
+                scale_o(pow2f(wexp));
             }
+#pragma unroll 1
+            for (int t = T_win; t < T; ++t) step(std::false_type{}, t);
             // ---- the share's end: the row's sum over its four threads, then O
             const uint32_t tl = tb + T - 1;
             ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
@@ -544,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             float l = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) l += red[64 * i];
-            const float fin = h.t1 <= wt ? up : 1.0f;
+            const float fin = h.t1 <= wt ? pow2f(wexp) : 1.0f;
             const bool whole = T == h.T;
             const int64_t gr = (int64_t)h.b * n_rows_q + q0 + row;
             const bool there = q0 + row < n_rows_q;

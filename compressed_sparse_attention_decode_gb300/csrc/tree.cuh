@@ -9,16 +9,27 @@ struct TreeSeq {
     int n_vis;                   // entries 0 .. n_vis-1
     int n_rows;                  // rows of rows16: the committed window rows, then the drafts up to the last node that is there
     int row_tiles;               // items of attn_tree.cu
-    int exp;                     // rows16 are the rows' values divided by 2^exp
+    int pad;
 };
+constexpr int TREE_GROUPS = 16;  // of 16 rows each: at most 255 rows
 // A call's parts of the workspace that k_tree_prep writes
 struct TreeNodes {
     TreeSeq* seq;                // [batch]
     int* vis;                    // [batch][n_q] entries that a node sees
     uint32_t* mask;              // [batch][n_q][8] which of the n_rows rows; none for a node that is not there
-    uint16_t* rows16;            // [batch][row_stride][512] fp16: window rows and drafts, zeros for drafts that are not there
+    // fp16, row r a 2^-exps[r] of the window row or draft (0 but for rows far off fp16's range), zeros for drafts that are not there
+    uint16_t* rows16;            // [batch][row_stride][512]
+    int8_t* exps;                // [batch][256]
+    int* top;                    // [batch][TREE_GROUPS] the largest exponent of a group of rows, 2^16 more where one is not 0
     int row_stride;
 };
+// The largest exponent of a sequence's rows, and whether any is not 0 (a whole warp calls it)
+__device__ __forceinline__ int tree_exp(const TreeNodes& t, int b, int n_rows, bool& scaled) {
+    const int lane = threadIdx.x & 31;
+    const int v = lane * 16 < n_rows ? t.top[b * TREE_GROUPS + lane] : -1000;
+    scaled = __any_sync(0xffffffffu, v > 1000);
+    return __reduce_max_sync(0xffffffffu, v > 1000 ? v - 65536 : v);
+}
 struct TreeCall {
     int batch, capacity, ratio, n_q, n_heads;
     const int64_t* q_pos;
