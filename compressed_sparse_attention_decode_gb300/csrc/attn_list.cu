@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                 // before is done (not its scores alone: of a short share they may be before the softmax has looked at its
                 // queries' exponents); a head whose largest magnitude lies outside [2^-10, 2^15) is scaled by a power of two
                 const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + (w.gq * a.n_heads + w.h0) * D_LAT);
-                constexpr int NR = 4;                    // rows of a warp in flight
+                constexpr int NR = 8;                    // rows of a warp in flight
                 for (int r0 = warp - TL_QW; r0 < TL_H; r0 += NR * TL_QWARPS) {
                     uint4 x[NR][2];
 #pragma unroll
@@ -269,11 +269,13 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     for (int i = 0; i < NR; ++i) {
                         const int r = r0 + TL_QWARPS * i;
                         const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
+                        const bool plain = e == 0 && a.scale_log2e >= 0.0f;
                         const float d = a.scale_log2e < 0.0f ? -pow2f(-e) : pow2f(-e);       // scores are taken times |scale|
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
                             const int c = lane + 32 * hh;
-                            *reinterpret_cast<uint4*>(sm + TL_SQ + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)) = bf16x8_to_f16x8(x[i][hh], d);
+                            *reinterpret_cast<uint4*>(sm + TL_SQ + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)) =
+                                plain ? bf16x8_to_f16x8(x[i][hh]) : bf16x8_to_f16x8(x[i][hh], d);
                         }
                         if (lane == 0) qexp[nq & 1][r] = e;
                     }
@@ -488,24 +490,31 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     const float up = ok ? pow2f(oexp) : __int_as_float(0x7fc00000);
                     auto store = [&](auto* dst) {            // row 0's first dim
                         using TD = std::remove_pointer_t<decltype(dst)>;
-#pragma unroll 1
-                        for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
-                            TD* d = dst + mt * 128 + qd * 32 + lane;
-#pragma unroll 1
-                            for (int c = 0; c < nh; c += 32) {
-                                float v[32];
-                                umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c, v);
-                                umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c + 16, v + 16);
-                                umma::tmem_wait_ld();
+                        // 16 heads of a dim tile at a time, the next ones' load under way while these are stored
+                        float v[2][16];
+                        const int n = (nh + 15) / 16;            // groups of 16 heads
+                        auto load = [&](int g, float* to) { umma::tmem_ld16(lane_base + TLT_O + 64 * (2 * half + g / n) + 16 * (g % n), to); };
+                        auto put = [&](int g, const float* x) {
+                            TD* d = dst + (2 * half + g / n) * 128 + qd * 32 + lane;
+                            const int c = 16 * (g % n);
 #pragma unroll
-                                for (int i = 0; i < 32; i += 4) {
-                                    const float4 f = *reinterpret_cast<const float4*>(fac + c + i);
-                                    const float f4[4] = {f.x, f.y, f.z, f.w};
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(fac + c + i);
+                                const float f4[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        if (c + i + j < nh) d[(c + i + j) * D_LAT] = from_f32<TD>(v[i + j] * f4[j] * up);
-                                }
+                                for (int j = 0; j < 4; ++j)
+                                    if (c + i + j < nh) d[(c + i + j) * D_LAT] = from_f32<TD>(x[i + j] * f4[j] * up);
                             }
+                        };
+                        load(0, v[0]);
+#pragma unroll 1
+                        for (int g = 0; g < 2 * n; g += 2) {
+                            umma::tmem_wait_ld();
+                            load(g + 1, v[1]);
+                            put(g, v[0]);
+                            umma::tmem_wait_ld();
+                            if (g + 2 < 2 * n) load(g + 2, v[0]);
+                            put(g + 1, v[1]);
                         }
                     };
                     if (whole)

@@ -162,6 +162,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
         start_b = 0, start_off = 0;
     }
     if (warp == TR_OWNW - 1) umma::tmem_alloc_pair(sa(&tmem_base), TRT_COLS);
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    umma::cluster_sync();        // the other CTA's barriers are there
+    const uint32_t tmem = tmem_base;
     pdl_wait();
     pdl_launch_next();
 
@@ -180,11 +185,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
         if (lane >= o) upto += v;
     }
     if (lane == 31) wsum[warp] = upto;
-    umma::fence_before();
     __syncthreads();
-    umma::fence_after();
     int64_t total = 0;
-    for (int i = 0; i < TR_THREADS / 32; ++i) {
+    for (int i = 0; i * per * 32 < a.batch; ++i) {                   // warps that have sequences
         if (i < warp) upto += wsum[i];
         total += wsum[i];
     }
@@ -201,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
         int64_t s = upto - mine;
         if (n_units > 0 && s <= u0 && u0 < upto)
             for (int b = b0; b < b1; ++b) {
-                const int64_t n = units(b);
+                const int64_t n = per == 1 ? mine : units(b);
                 if (u0 < s + n) {
                     start_b = b, start_off = (int)(u0 - s);
                     break;
@@ -210,8 +213,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             }
     }
     __syncthreads();
-    umma::cluster_sync();        // the other CTA's barriers are there
-    const uint32_t tmem = tmem_base;
     TreeCursor cur{n_units, start_off, start_b};
     TreeShare h{};
     bool ok = true;
@@ -410,23 +411,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             {
                 const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)h.b * n_rows_q + q0) * D_LAT);
 #pragma unroll 1
-                for (int r0 = warp; r0 < 64; r0 += 4 * TR_SMW) {
-                    uint4 x[4][2];
+                for (int r0 = warp; r0 < 64; r0 += 8 * TR_SMW) {
+                    uint4 x[8][2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const int r = r0 + TR_SMW * i;
                         x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
                         if (q0 + r < n_rows_q) x[i][0] = src[r * 64 + lane], x[i][1] = src[r * 64 + 32 + lane];
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const int r = r0 + TR_SMW * i;
                         const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
+                        const bool plain = e == 0 && a.scale_log2e >= 0.0f;
                         const float d = a.scale_log2e < 0.0f ? -pow2f(-e) : pow2f(-e);       // scores are taken times |scale|
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
                             const int c = lane + 32 * hh;
-                            *reinterpret_cast<uint4*>(sm + TR_SQ + (c >> 3) * TR_SLAB + tr_swz(r, c & 7)) = bf16x8_to_f16x8(x[i][hh], d);
+                            *reinterpret_cast<uint4*>(sm + TR_SQ + (c >> 3) * TR_SLAB + tr_swz(r, c & 7)) =
+                                plain ? bf16x8_to_f16x8(x[i][hh]) : bf16x8_to_f16x8(x[i][hh], d);
                         }
                         if (lane == 0) qexp[r] = e;
                     }
@@ -581,25 +584,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             const int64_t pr = (int64_t)slot * TR_ROWS + 64 * (int)rank + row;
             const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
             const int d0 = 256 * ch + 128 * kh;
+            // 256 bytes of each of the warp's 32 rows at a time through the queries' place (no longer needed), so that rows are
+            // stored as whole lines: a thread has a row, and rows lie far apart
+            auto store = [&](auto* dst, int rows, float f) {         // dst: the warp's first row, first dim
+                using TD = std::remove_pointer_t<decltype(dst)>;
+                constexpr int E = 16 / (int)sizeof(TD), N = 16 * E;  // elements of a piece, of a round
+                uint8_t* mine = sm + TR_SQ + warp * 8192;
+                f = ok ? f : __int_as_float(0x7fc00000);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-                float v[16];
-                umma::tmem_ld16(lane_base + TRT_O + 128 * ch + c, v);
-                umma::tmem_wait_ld();
+                for (int c0 = 0; c0 < 128; c0 += N) {
+#pragma unroll 1
+                    for (int c = 0; c < N; c += 16) {
+                        float v[16];
+                        umma::tmem_ld16(lane_base + TRT_O + 128 * ch + c0 + c, v);
+                        umma::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = ok ? v[i] * fin : __int_as_float(0x7fc00000);
-                if (!whole) {
-                    ElemVec<float, 16> y;
-                    y.pack(v);
-                    y.store(a.part_o + pr * D_LAT + d0 + c);
-                } else if (there) {
+                        for (int i = 0; i < 16; ++i) v[i] *= f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] *= inv;
-                    ElemVec<TO, 16> y;
-                    y.pack(v);
-                    y.store(reinterpret_cast<TO*>(a.out) + gr * D_LAT + d0 + c);
+                        for (int i = 0; i < 16; i += E) {
+                            ElemVec<TD, E> y;
+                            y.pack(v + i);
+                            y.store(reinterpret_cast<TD*>(mine + lane * 256 + ((((c + i) / E) ^ (lane & 15)) << 4)));
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 2 * i + (lane >> 4), k = lane & 15;
+                        const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 256 + ((k ^ (r & 15)) << 4));
+                        if (r < rows) *reinterpret_cast<uint4*>(dst + (int64_t)r * D_LAT + c0 + k * E) = y;
+                    }
+                    __syncwarp();
                 }
-            }
+            };
+            const int wrow = 32 * (qd & 1);                          // the warp's first row
+            if (!whole)
+                store(a.part_o + (pr - lane) * D_LAT + d0, 32, fin);
+            else
+                store(reinterpret_cast<TO*>(a.out) + (gr - lane) * D_LAT + d0, n_rows_q - q0 - wrow, fin * inv);
             if (2 * kh + ch == 0) {
                 if (!whole)
                     a.part_ml[pr] = make_float2(m, l);

@@ -10,11 +10,9 @@ __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t
 
 // the largest bf16 magnitude (as bits, sign cleared) of the eight values in v
 __device__ __forceinline__ uint32_t bf16_absmax8(const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-    return m;
+    const uint32_t a = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), b = __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+    const uint32_t m = __vmaxu2(a, b);
+    return max(m & 0xffffu, m >> 16);
 }
 
 // The exponent E by which values whose largest magnitude has bf16 bits `mx` are divided
@@ -37,6 +35,15 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(const uint4& v, float d) {
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = f16x2_bits(__uint_as_float(w[i] << 16) * d, __uint_as_float(w[i] & 0xffff0000u) * d);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// eight bf16 values as fp16
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f16x2_bits(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
