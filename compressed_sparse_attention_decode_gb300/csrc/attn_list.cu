@@ -4,8 +4,9 @@
 //
 // Work.  2 x 512 multiply-adds per head and key; 64 heads make 455 flop of a 288-byte entry, so the tensor cores bound it and
 // shared memory feeds them.  An item has two units for its window (at most 128 rows) and one for each 64 slots of its list,
-// known on the host; block i (one per SM) takes the i-th even part of all units.  An item that one block has whole
-// is stored by it, the shares of others are joined.
+// known on the host; block i (one per SM) takes the i-th even part of all units, and the shares of an item that several
+// blocks have are joined.  Where whole items a block are not much longer than even parts, the parts are whole items, stored
+// by their block (16 x 16 nodes of 512 slots: 16.8 units a block or 2 items of 10, and no join).
 //
 // One tile of 64 keys, double-buffered (L, S, P):
 //   S = Q . L^T     (tcgen05 kind::f16, M = 64 heads, N = 64 keys, K = 512; two issuers take dims 0-255 and 256-511 into two
@@ -15,8 +16,9 @@
 //   O^T += L^T . P  (M = 4 x 128 dims, N = the heads in steps of 16, K = 64 keys; two issuers)
 // The window rows are fp16 values of a power-of-two scale of their own; O carries the scale of the tile last added, and is
 // brought to the entries' after the window where they differ.
-// Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 rows, 20-23 the queries, staged for the next item
-// while this one's last values and outputs are under way.  Nothing waits for a P or S buffer: a tile's keys are expanded
+// Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 rows, 20-23 the queries, fetched for the next item
+// while this one's last values and outputs are under way (k_tree_prep has them in fp16: converted here they were 10,000
+// clocks late, mostly for their own code).  Nothing waits for a P or S buffer: a tile's keys are expanded
 // only after the values of the tile before it in that buffer, which had read and written both.
 #include <algorithm>
 #include <type_traits>
@@ -53,7 +55,6 @@ __device__ __forceinline__ uint32_t tl_swz(uint32_t row, uint32_t chunk) { retur
 struct ListArgs {
     const uint8_t *codes, *scales;
     int capacity;
-    const uint16_t* q;
     int n_q, n_heads, hgroups;
     TreeNodes t;
     const int32_t* idx;
@@ -62,12 +63,12 @@ struct ListArgs {
     void* out;
     float* lse;
     int per;                     // units of an item
-    int each, more;              // the first `more` blocks have each + 1 units, the others `each`
+    int grain, each, more;       // the first `more` blocks have each + 1 grains of units, the others `each`
     float* part_o;               // [2 blocks][64][512]
     float2* part_ml;             // [2 blocks][64] reference (log2) and sum
     int* err;
-    __device__ __forceinline__ int start(int b) const { return each * b + min(b, more); }
-    __device__ __forceinline__ int block_of(int u) const {
+    __device__ __forceinline__ int start(int b) const { return grain * (each * b + min(b, more)); }
+    __device__ __forceinline__ int block_of(int u) const {           // (of grains of one unit)
         const int longer = (each + 1) * more;
         return u < longer ? (unsigned)u / (unsigned)(each + 1) : more + (int)((unsigned)(u - longer) / (unsigned)each);
     }
@@ -97,9 +98,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
     __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2], b_q;
     __shared__ float red[2][TL_H], m_run[TL_H];
     __shared__ __align__(16) float fac[TL_H];
-    __shared__ int qexp[2][TL_H], any[4];
+    __shared__ int any[4];
     __shared__ uint32_t slot_ok[2][2], tmem_base;
-    __shared__ uint8_t wrow[WINDOW];                         // the rows of rows16 that the share's node attends to
+    __shared__ uint8_t wrows[2][WINDOW];                     // the rows of rows16 that a share's node attends to
     const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
     uint8_t* sm = dyn + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
         u += t1 - t0;
         const bool loader = warp >= TL_LOADW && warp < TL_QW;
         const ListItem w = tl_item(a, item);
+        uint8_t* wrow = wrows[nq & 1];
         const int wt = w.wtiles();
         // the tiles that are there, counted on: window tiles first, then the list's
         const int wa = min(t0, wt), wb = min(t1, wt), la = max(t0, TL_WIN), lb = max(t1, TL_WIN);
@@ -145,8 +147,10 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
             const uint8_t* codes = a.codes + (int64_t)w.b * a.capacity * (D_LAT / 2);
             const uint8_t* scales = a.scales + (int64_t)w.b * a.capacity * (D_LAT / 16);
             int* slots = reinterpret_cast<int*>(sm + TL_SLOTS);
-            umma::bar_named(2, TL_LOADERS);          // the rows and the slots of the share before are read
-            if (nwt > 0) {
+            umma::bar_named(2, TL_LOADERS);          // the slots of the share before are read
+            if (nwt > 0 && T > 0) {
+                // (once the softmax is done with the share before the last, which had its rows here)
+                if (tb >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_lfree[tb & 1]), ((tb >> 1) - 1) & 1);
                 // row lt is the node's if its bit is set: as many of its rows come before it as bits lie below
                 const uint32_t* m = a.t.mask + w.gq * 8;
                 const uint32_t mine = m[lt >> 5];
@@ -251,45 +255,25 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
             }
         } else if (T > 0 || warp < TL_SMW) {
             if (warp >= TL_QW) {
-                // ================= Q: heads h0 .. h0+63 (zero rows past n_heads), bf16 -> fp16 slabs, once the softmax of the share
-                // before is done (not its scores alone: of a short share they may be before the softmax has looked at its
-                // queries' exponents); a head whose largest magnitude lies outside [2^-10, 2^15) is scaled by a power of two
-                const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + (w.gq * a.n_heads + w.h0) * D_LAT);
-                constexpr int NR = 8;                    // rows of a warp in flight
-                for (int r0 = warp - TL_QW; r0 < TL_H; r0 += NR * TL_QWARPS) {
-                    uint4 x[NR][2];
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        const int r = r0 + TL_QWARPS * i;
-                        x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < nh) x[i][0] = qsrc[r * 64 + lane], x[i][1] = qsrc[r * 64 + 32 + lane];
-                    }
-                    if (r0 == warp - TL_QW && tb > 0) ok = ok && umma::mbar_wait_fast(sa(&b_pfull[(tb - 1) & 1]), ((tb - 1) >> 1) & 1);
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        const int r = r0 + TL_QWARPS * i;
-                        const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
-                        const bool plain = e == 0 && a.scale_log2e >= 0.0f;
-                        const float d = a.scale_log2e < 0.0f ? -pow2f(-e) : pow2f(-e);       // scores are taken times |scale|
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const int c = lane + 32 * hh;
-                            *reinterpret_cast<uint4*>(sm + TL_SQ + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)) =
-                                plain ? bf16x8_to_f16x8(x[i][hh]) : bf16x8_to_f16x8(x[i][hh], d);
-                        }
-                        if (lane == 0) qexp[nq & 1][r] = e;
-                    }
+                // ================= Q: heads h0 .. h0+63 (zero rows past n_heads) once the softmax of the share before is done
+                if (tb > 0) ok = ok && umma::mbar_wait_fast(sa(&b_pfull[(tb - 1) & 1]), ((tb - 1) >> 1) & 1);
+                const uint16_t* src = a.t.q16 + (w.gq * a.n_heads + w.h0) * D_LAT;
+#pragma unroll 4
+                for (int i = tid - TL_QW * 32; i < TL_H * 64; i += TL_QWARPS * 32) {
+                    const int r = i >> 6, c = i & 63;
+                    copy16(sa(sm + TL_SQ + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)), src + (r < nh ? r : 0) * D_LAT + 8 * c, r < nh);
                 }
+                copy16_wait();
                 umma::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(sa(&b_q));
-                // the next share's queries, if it is another item's, on their way while this one runs
+                // the next share's queries, if it is another item's, on their way to L2 while this one runs
                 if (u < u1) {
                     const int next = (unsigned)u / (unsigned)a.per;
                     const int64_t g = a.hgroups == 1 ? next : next >> 1;
                     const int nh0 = a.hgroups == 1 ? 0 : (next & 1) * TL_H;
-                    const char* src = reinterpret_cast<const char*>(a.q + (g * a.n_heads + nh0) * D_LAT);
-                    for (int i = tid - TL_QW * 32; i < min(TL_H, a.n_heads - nh0) * 8; i += TL_QWARPS * 32) umma::prefetch_l2(src + i * 128);
+                    const char* ahead = reinterpret_cast<const char*>(a.t.q16 + (g * a.n_heads + nh0) * D_LAT);
+                    for (int i = tid - TL_QW * 32; i < min(TL_H, a.n_heads - nh0) * 8; i += TL_QWARPS * 32) umma::prefetch_l2(ahead + i * 128);
                 }
                 // every phase in turn, the last one at the next share: a wait tells a phase from the next by its parity alone
                 for (int t = 0; t + 1 < T; ++t) ok = ok && umma::mbar_wait_fast(sa(&b_pfull[(tb + t) & 1]), ((tb + t) >> 1) & 1);
@@ -353,10 +337,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                 const int h = qd * 16 + (lane >> 2) + 8 * (lane & 1), par = (lane >> 1) & 1;
                 const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
                 if (tid < TL_H) m_run[tid] = -INFINITY;
-                if (T > 0) ok = ok && umma::mbar_wait_fast(sa(&b_q), nq & 1);
                 umma::bar_named(1, TL_SMT);
                 // never zero, so that a masked score stays -inf
-                const float mul4 = T > 0 ? fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[nq & 1][h]), 0x1p-100f) : 0.0f;
+                const float mul4 = T > 0 ? fmaxf(fabsf(a.scale_log2e) * pow2f(h < nh ? a.t.q_exps[w.gq * a.n_heads + w.h0 + h] : 0), 0x1p-100f) : 0.0f;
                 // the window rows' part of O carries 2^-wexp; a row of another exponent enters with its weight scaled by the difference
                 bool scaled;
                 const int wexp = max(tree_exp(a.t, w.b, a.t.seq[w.b].n_rows, scaled), -100);
@@ -365,17 +348,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                 for (int t = 0; t < T; ++t) {
                     const uint32_t tg = tb + t, buf = tg & 1, ph = (tg >> 1) & 1;
                     float x[16];
-                    ok = ok && umma::mbar_wait_fast(sa(&b_sfull[buf]), ph);
-                    ok = ok && umma::mbar_wait_fast(sa(&b_lfull[buf]), ph);          // (the loaders' words too)
-                    umma::fence_after();
-                    {
-                        float x1[16];
-                        umma::tmem_ld16x64b_x16(lane_base + TLT_S + 64 * (2 * buf) + 32 * half, x);
-                        umma::tmem_ld16x64b_x16(lane_base + TLT_S + 64 * (2 * buf + 1) + 32 * half, x1);
-                        umma::tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] += x1[i];
-                    }
+                    // what does not need the scores comes first: the loaders' words, the reference
+                    ok = ok && umma::mbar_wait_fast(sa(&b_lfull[buf]), ph);
                     const bool window = t < nwt;
                     const int e = window ? wexp : 0;
                     uint32_t see;                    // which of the half's 32 keys are there
@@ -384,6 +358,17 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                         see = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
                     } else {
                         see = *reinterpret_cast<volatile uint32_t*>(&slot_ok[buf][half]);
+                    }
+                    const float mh = m_run[h];
+                    ok = ok && umma::mbar_wait_fast(sa(&b_sfull[buf]), ph);
+                    umma::fence_after();
+                    {
+                        float x1[16];
+                        umma::tmem_ld16x64b_x16(lane_base + TLT_S + 64 * (2 * buf) + 32 * half, x);
+                        umma::tmem_ld16x64b_x16(lane_base + TLT_S + 64 * (2 * buf + 1) + 32 * half, x1);
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] += x1[i];
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] *= mul4;
@@ -398,10 +383,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (!((see >> (par + 2 * i)) & 1u)) x[i] = -INFINITY;
-                    const float mh = m_run[h];
-                    float mx = x[0];
-#pragma unroll
-                    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
+                    const auto max3 = [](float p, float q, float r) { return fmaxf(p, fmaxf(q, r)); };
+                    float mx = max3(max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), x[6]),
+                                    max3(max3(x[7], x[8], x[9]), max3(x[10], x[11], x[12]), x[13]), fmaxf(x[14], x[15]));
                     const bool shift = t > 0 && e != oexp;           // (the same for all)
                     if (umma::bar_red_or(1, TL_SMT, mx - mh > TL_TOP) || shift) {
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -559,43 +543,67 @@ __global__ void __launch_bounds__(512) k_tree_lists_join(const __grid_constant__
 
 namespace {
 constexpr size_t TL_HEAD = 256;                      // the error word and padding
-int lists_blocks(int64_t units) { return (int)std::min<int64_t>(TL_SMS, units); }
-int64_t lists_units(int batch, int n_q, int n_heads, int k) {
-    return (int64_t)batch * n_q * ((n_heads + TL_H - 1) / TL_H) * (TL_WIN + (k + TL_TILE - 1) / TL_TILE);
-}
+constexpr int64_t TL_PASS = 1 << 16;                 // rows of a pass at most (of one sequence 16,384): their fp16 queries are 64 MB
+
+struct ListPlan {
+    int hgroups, per, blocks, grain, each, more;
+    ListPlan(int batch, int n_q, int n_heads, int k) {
+        hgroups = (n_heads + TL_H - 1) / TL_H;
+        per = TL_WIN + (k + TL_TILE - 1) / TL_TILE;
+        const int items = batch * n_q * hgroups;     // at most 65,536
+        blocks = std::min(TL_SMS, items * per);
+        // whole items a block where that is at most 6 units (20,000 clocks) more than an even part: about what the shares'
+        // stores and the join cost
+        const int whole = (items + blocks - 1) / blocks * per;
+        grain = whole <= items * per / blocks + 6 ? per : 1;
+        const int grains = items * per / grain;
+        blocks = std::min(blocks, grains);
+        each = grains / blocks, more = grains % blocks;
+    }
+};
+// sequences of a pass
+int lists_pass(int batch, int n_q, int n_heads) { return (int)std::min<int64_t>(batch, TL_PASS / ((int64_t)n_q * n_heads)); }
 }  // namespace
 
 size_t tree_lists_ws(int batch, int n_q, int n_heads, int k) {
-    const size_t nodes = tree_nodes_bytes(batch, n_q);
-    const size_t rows = (size_t)2 * lists_blocks(lists_units(batch, n_q, n_heads, k)) * TL_H;
-    return TL_HEAD + nodes + rows * (D_LAT * sizeof(float) + sizeof(float2));
+    const int nb = lists_pass(batch, n_q, n_heads);
+    const size_t rows = (size_t)2 * TL_SMS * TL_H;
+    return TL_HEAD + tree_nodes_bytes(nb, n_q, (int64_t)nb * n_q * n_heads) + rows * (D_LAT * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_tree_lists(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
                               const int32_t* parent, const uint16_t* draft, const int32_t* idx, int k, const uint16_t* swa,
                               const int64_t* swa_pos0, int swa_len, float scale, void* out, int out_type, float* lse, void* ws,
                               cudaStream_t st) {
-    const int64_t units = lists_units(c.batch, n_q, n_heads, k);     // below 2^31: at most 65,535 x 128 nodes, 2 groups, 34 units
-    const int blocks = lists_blocks(units);
-    TreeCall call{c.batch, c.capacity, c.ratio, n_q, n_heads, q_pos, parent, draft, swa, swa_pos0, swa_len, {}, nullptr, nullptr, 0};
-    uint8_t* w = tree_nodes_take(call.t, c.batch, n_q, reinterpret_cast<uint8_t*>(ws) + TL_HEAD);
-    ListArgs a{c.lat_codes, c.lat_scales, c.capacity, q, n_q, n_heads, (n_heads + TL_H - 1) / TL_H, call.t, idx, k,
-               scale * 1.4426950408889634f, out, lse, TL_WIN + (k + TL_TILE - 1) / TL_TILE, (int)(units / blocks),
-               (int)(units % blocks), nullptr, nullptr, reinterpret_cast<int*>(ws)};
-    a.part_o = reinterpret_cast<float*>(w);
-    a.part_ml = reinterpret_cast<float2*>(w + (size_t)2 * blocks * TL_H * D_LAT * sizeof(float));
     auto go = [&](auto* y) {
         using TO = std::remove_pointer_t<decltype(y)>;
         cudaError_t e = cudaFuncSetAttribute(k_tree_lists<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TL_DYN);
-        if (e == cudaSuccess) e = launch_tree_prep(call, st);
-        if (e != cudaSuccess) return e;
-        launch_k(k_tree_lists<TO>, dim3((unsigned)blocks), TL_THREADS, TL_DYN, st, a);
-        note_launch();
-        if (blocks > 1) {
-            launch_k(k_tree_lists_join<TO>, dim3((unsigned)(blocks - 1), (unsigned)((std::min(n_heads, TL_H) + 3) / 4)), 512, 0, st, a);
+        const int pass = lists_pass(c.batch, n_q, n_heads);
+        for (int b0 = 0; b0 < c.batch && e == cudaSuccess; b0 += pass) {
+            const int nb = std::min(pass, c.batch - b0);
+            const int64_t n0 = (int64_t)b0 * n_q, r0 = n0 * n_heads;         // nodes and rows before the pass
+            const ListPlan p(nb, n_q, n_heads, k);
+            TreeCall call{nb, c.capacity, c.ratio, n_q, n_heads, q_pos + n0, parent + n0, draft + n0 * D_LAT,
+                          swa ? swa + (int64_t)b0 * swa_len * D_LAT : nullptr, swa_pos0 ? swa_pos0 + b0 : nullptr, swa_len, {},
+                          q + r0 * D_LAT, scale < 0.0f, nullptr, nullptr, 0};
+            uint8_t* w = tree_nodes_take(call.t, nb, n_q, (int64_t)nb * n_q * n_heads, reinterpret_cast<uint8_t*>(ws) + TL_HEAD);
+            ListArgs a{c.lat_codes + (int64_t)b0 * c.capacity * (D_LAT / 2), c.lat_scales + (int64_t)b0 * c.capacity * (D_LAT / 16),
+                       c.capacity, n_q, n_heads, p.hgroups, call.t, idx ? idx + n0 * k : nullptr, k, scale * 1.4426950408889634f,
+                       y + r0 * D_LAT, lse ? lse + r0 : nullptr, p.per, p.grain, p.each, p.more, nullptr, nullptr,
+                       reinterpret_cast<int*>(ws)};
+            a.part_o = reinterpret_cast<float*>(w);
+            a.part_ml = reinterpret_cast<float2*>(w + (size_t)2 * TL_SMS * TL_H * D_LAT * sizeof(float));
+            e = launch_tree_prep(call, st);
+            if (e != cudaSuccess) break;
+            launch_k(k_tree_lists<TO>, dim3((unsigned)p.blocks), TL_THREADS, TL_DYN, st, a);
             note_launch();
+            if (p.grain == 1 && p.blocks > 1) {
+                launch_k(k_tree_lists_join<TO>, dim3((unsigned)(p.blocks - 1), (unsigned)((std::min(n_heads, TL_H) + 3) / 4)), 512, 0, st, a);
+                note_launch();
+            }
+            e = cudaGetLastError();
         }
-        return cudaGetLastError();
+        return e;
     };
     return out_type == CSA2_F32   ? go(reinterpret_cast<float*>(out))
            : out_type == CSA2_F16 ? go(reinterpret_cast<__half*>(out))

@@ -714,7 +714,7 @@ size_t tree_attn_ws(int batch, int n_q, int n_heads, int k, int64_t capacity) {
     const size_t lists = k >= 0 ? tree_lists_ws(batch, n_q, n_heads, k) : 0;
     if (k > 0) return lists;
     const TreePlan p = tree_plan(batch, n_q, n_heads, capacity);
-    return std::max(lists, TR_HEAD + tree_nodes_bytes(batch, n_q) + p.heads + p.o + p.ml);
+    return std::max(lists, TR_HEAD + tree_nodes_bytes(batch, n_q, 0) + p.heads + p.o + p.ml);
 }
 
 cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
@@ -725,9 +725,9 @@ cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, in
         return launch_tree_lists(c, q, n_q, n_heads, q_pos, parent, draft, idx, k, swa, swa_pos0, swa_len, scale, out, out_type, lse,
                                  ws, st);
     const TreePlan p = tree_plan(c.batch, n_q, n_heads, c.capacity);
-    TreeCall call{c.batch, c.capacity, c.ratio, n_q, n_heads, q_pos, parent, draft, swa, swa_pos0, swa_len, {}, out, lse,
+    TreeCall call{c.batch, c.capacity, c.ratio, n_q, n_heads, q_pos, parent, draft, swa, swa_pos0, swa_len, {}, nullptr, false, out, lse,
                   out_type == CSA2_F32 ? 4 : 2};
-    uint8_t* w = tree_nodes_take(call.t, c.batch, n_q, reinterpret_cast<uint8_t*>(ws) + TR_HEAD);
+    uint8_t* w = tree_nodes_take(call.t, c.batch, n_q, 0, reinterpret_cast<uint8_t*>(ws) + TR_HEAD);
     TreeArgs a{c.lat_codes, c.lat_scales, c.batch, c.capacity, q, n_q, n_heads, scale * 1.4426950408889634f, out, lse, call.t,
                nullptr, nullptr, nullptr, reinterpret_cast<int*>(ws)};
     a.heads = reinterpret_cast<TreeHead*>(w);

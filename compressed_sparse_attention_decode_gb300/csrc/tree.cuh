@@ -22,6 +22,9 @@ struct TreeNodes {
     int8_t* exps;                // [batch][256]
     int* top;                    // [batch][TREE_GROUPS] the largest exponent of a group of rows, 2^16 more where one is not 0
     int row_stride;
+    // attn_list.cu: the queries as fp16, row r a 2^-q_exps[r] of q's (times -1 where neg_q), or NULL
+    uint16_t* q16;               // [batch][n_q][n_heads][512]
+    int8_t* q_exps;              // [batch][n_q][n_heads]
 };
 // The largest exponent of a sequence's rows, and whether any is not 0 (a whole warp calls it)
 __device__ __forceinline__ int tree_exp(const TreeNodes& t, int b, int n_rows, bool& scaled) {
@@ -39,12 +42,15 @@ struct TreeCall {
     const int64_t* swa_pos0;
     int swa_len;
     TreeNodes t;
-    void* out;                   // rows of items that nobody works on are written by k_tree_prep (out_size 0: none)
+    const uint16_t* q;
+    bool neg_q;
+    void* out;                   // without q16: rows of items that nobody works on are written by k_tree_prep
     float* lse;
     int out_size;                // bytes of an element
 };
-size_t tree_nodes_bytes(int batch, int n_q);
-uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, uint8_t* w);       // from a workspace's byte w on; the first byte after it
+// a workspace's bytes for it, and its pointers from byte w on (returns the first byte after it); q_rows: rows of q16
+size_t tree_nodes_bytes(int batch, int n_q, int64_t q_rows);
+uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int64_t q_rows, uint8_t* w);
 cudaError_t launch_tree_prep(const TreeCall& c, cudaStream_t st);
 
 // 16 bytes from global to shared memory, zeros where `there` is false

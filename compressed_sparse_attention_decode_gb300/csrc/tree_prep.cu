@@ -8,8 +8,20 @@
 
 namespace csa2 {
 
-// Blocks (sequence, group of 16 rows), and some more that write the rows of items that nobody works on.  Every block finds
-// the chains for itself (a thread a node), the first one writes the nodes' part; then a warp has two rows.
+// A row of 512 bf16 values, two pieces of 16 bytes a lane, to fp16 after a power-of-two scale where its largest magnitude lies
+// outside [2^-10, 2^15); returns the exponent.
+__device__ __forceinline__ int row_to_f16(const uint4* x, uint4* dst, bool neg) {
+    const int lane = threadIdx.x & 31;
+    const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[0]), bf16_absmax8(x[1]))));
+    const float d = neg ? -pow2f(-e) : pow2f(-e);
+    dst[lane] = bf16x8_to_f16x8(x[0], d);
+    dst[32 + lane] = bf16x8_to_f16x8(x[1], d);
+    return e;
+}
+
+// Blocks (sequence, group of 16 rows), and some more that write the rows of items that nobody works on, or convert the
+// sequence's queries.  Every block finds the chains for itself (a thread a node), the first one writes the nodes' part; then
+// a warp has two rows.
 __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeCall a) {
     __shared__ int parent[TREE_NODES], last_s, vis_s, tops[8], offs[8];
     __shared__ long long hi_s;
@@ -49,6 +61,28 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
     __syncthreads();
     const int last = last_s;
     const int row_tiles = ((last + 1) * a.n_heads + 127) / 128;
+    if (group >= TREE_GROUPS && a.t.q16 != nullptr) {
+        // four rows of the sequence's queries a warp at a time (those of nodes that are not there too: nobody reads them)
+        const int rows = N * a.n_heads, warps = ((int)gridDim.y - TREE_GROUPS) * 8;
+        const int64_t r0 = (int64_t)b * rows;
+        for (int r = (group - TREE_GROUPS) * 8 + warp; r < rows; r += 4 * warps) {
+            uint4 x[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r + i * warps < rows) {
+                    const uint4* src = reinterpret_cast<const uint4*>(a.q + (r0 + r + i * warps) * D_LAT);
+                    x[i][0] = src[lane], x[i][1] = src[32 + lane];
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (r + i * warps >= rows) break;
+                const int64_t at = r0 + r + i * warps;
+                const int e = row_to_f16(x[i], reinterpret_cast<uint4*>(a.t.q16 + at * D_LAT), a.neg_q);
+                if (lane == 0) a.t.q_exps[at] = (int8_t)e;
+            }
+        }
+        return;
+    }
     if (group >= TREE_GROUPS) {
         const int64_t r0 = (int64_t)row_tiles * 128, r1 = (int64_t)N * a.n_heads, base = (int64_t)b * r1;
         const int pieces = D_LAT * a.out_size / 16;
@@ -84,10 +118,7 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
         for (int i = 0; i < 2; ++i) {
             const int r = group * 16 + warp + 8 * i;
             if (r >= n_rows) break;
-            const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
-            uint4* row = reinterpret_cast<uint4*>(a.t.rows16 + ((int64_t)b * a.t.row_stride + r) * D_LAT);
-            row[lane] = bf16x8_to_f16x8(x[i][0], pow2f(-e));
-            row[32 + lane] = bf16x8_to_f16x8(x[i][1], pow2f(-e));
+            const int e = row_to_f16(x[i], reinterpret_cast<uint4*>(a.t.rows16 + ((int64_t)b * a.t.row_stride + r) * D_LAT), false);
             if (lane == 0) a.t.exps[b * 256 + r] = (int8_t)e;
             top = max(top, e);
             off = off || e != 0;
@@ -132,24 +163,26 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
 namespace {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 struct NodeParts {
-    size_t seq, vis, mask, exps, top, rows;
-    NodeParts(int batch, int n_q)
+    size_t seq, vis, mask, exps, top, rows, q, q_exps;
+    NodeParts(int batch, int n_q, int64_t q_rows)
         : seq(up256((size_t)batch * sizeof(TreeSeq))),
           vis(up256((size_t)batch * n_q * sizeof(int))),
           mask(up256((size_t)batch * n_q * 8 * sizeof(uint32_t))),
           exps((size_t)batch * 256),
           top(up256((size_t)batch * TREE_GROUPS * sizeof(int))),
-          rows((size_t)batch * (WINDOW - 1 + n_q) * D_LAT * sizeof(uint16_t)) {}
+          rows((size_t)batch * (WINDOW - 1 + n_q) * D_LAT * sizeof(uint16_t)),
+          q((size_t)q_rows * D_LAT * sizeof(uint16_t)),
+          q_exps(up256((size_t)q_rows)) {}
 };
 }  // namespace
 
-size_t tree_nodes_bytes(int batch, int n_q) {
-    const NodeParts p(batch, n_q);
-    return p.seq + p.vis + p.mask + p.exps + p.top + p.rows;
+size_t tree_nodes_bytes(int batch, int n_q, int64_t q_rows) {
+    const NodeParts p(batch, n_q, q_rows);
+    return p.seq + p.vis + p.mask + p.exps + p.top + p.rows + p.q + p.q_exps;
 }
 
-uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, uint8_t* w) {
-    const NodeParts p(batch, n_q);
+uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int64_t q_rows, uint8_t* w) {
+    const NodeParts p(batch, n_q, q_rows);
     t.seq = reinterpret_cast<TreeSeq*>(w), w += p.seq;
     t.vis = reinterpret_cast<int*>(w), w += p.vis;
     t.mask = reinterpret_cast<uint32_t*>(w), w += p.mask;
@@ -157,12 +190,15 @@ uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, uint8_t* w) {
     t.top = reinterpret_cast<int*>(w), w += p.top;
     t.rows16 = reinterpret_cast<uint16_t*>(w), w += p.rows;
     t.row_stride = WINDOW - 1 + n_q;
+    t.q16 = q_rows > 0 ? reinterpret_cast<uint16_t*>(w) : nullptr, w += p.q;
+    t.q_exps = reinterpret_cast<int8_t*>(w), w += p.q_exps;
     return w;
 }
 
 cudaError_t launch_tree_prep(const TreeCall& c, cudaStream_t st) {
-    const int zero = c.out_size == 0 ? 0 : std::min(16, (c.n_q * c.n_heads + 511) / 512);
-    launch_k(k_tree_prep, dim3((unsigned)c.batch, (unsigned)(TREE_GROUPS + zero)), 256, 0, st, c);
+    const int rows = c.n_q * c.n_heads;
+    const int more = c.t.q16 ? (rows + 31) / 32 : std::min(16, (rows + 511) / 512);
+    launch_k(k_tree_prep, dim3((unsigned)c.batch, (unsigned)(TREE_GROUPS + more)), 256, 0, st, c);
     note_launch();
     return cudaGetLastError();
 }
