@@ -16,162 +16,319 @@
 
 namespace csa2 {
 
-constexpr int CA_WARPS = 8;
-
 struct AppendArgs {
     uint8_t *lat_codes, *lat_scales, *ik_codes, *ik_scales;
-    int capacity, ratio, d_idx;
+    int capacity, ratio;
     const uint16_t* rows;
     int n_rows;
     const int32_t* path;
-    int n_path;
+    int n_path, n_ent;           // entries of a sequence at most
     const int64_t* pos0;
     const uint16_t* prev;
     uint16_t* prev_out;
     const float *w0, *w1;
     const uint8_t *wik_codes, *wik_scales;
-    int per_warp;                // entries a warp takes
 };
 
-// how many of the first `upto` steps of a path are rows that exist, the block together
-__device__ __forceinline__ int ca_length(const int32_t* path, int upto, int n_rows) {
-    if (path == nullptr) return upto;
-    for (int j0 = 0; j0 < upto; j0 += CA_WARPS * 32) {
-        const int j = j0 + (int)threadIdx.x;
-        const bool there = j < upto && (unsigned)path[j] < (unsigned)n_rows;
-        const int n = __syncthreads_count(there);
-        if (n == min(CA_WARPS * 32, upto - j0)) continue;
-        // the first that is not there: a minimum over the block
-        __shared__ int first;
-        if (threadIdx.x == 0) first = upto;
-        __syncthreads();
-        if (!there) atomicMin(&first, min(j, upto));
-        __syncthreads();
-        return first;
+// Sequence b of a call
+struct AppendSeq {
+    int64_t e0;                  // the entry of the first position, outside the cache where that is
+    int odd;                     // the first position completes a pair
+    const int32_t* path;
+    const uint16_t* rows;
+    __device__ __forceinline__ AppendSeq(const AppendArgs& a, int b) {
+        const int64_t pos0 = a.pos0[b];
+        odd = a.ratio == 2 ? (int)(pos0 & 1) : 0;
+        e0 = min(a.ratio == 2 ? (pos0 - odd) / 2 : pos0, (int64_t)a.capacity);
+        path = a.path ? a.path + (int64_t)b * a.n_path : nullptr;
+        rows = a.rows + (int64_t)b * a.n_rows * D_LAT;
     }
-    return upto;
-}
-
-// One warp an entry, lane g owning channels 16g .. 16g+15, one scale group.  KEYS: the indexer keys are projected
-// from the stored entry, W in shared memory as in k_cache_write_proj.
-template <int DI>
-__global__ void __launch_bounds__(CA_WARPS * 32) k_cache_append(const __grid_constant__ AppendArgs a) {
-    extern __shared__ int smw[];
-    constexpr int WS = 129;
-    int* Wq = smw;                                   // [DI][WS] doubled E2M1 values, int8 x4
-    int* Ws = Wq + DI * WS;                          // [DI][33] scales x 2^9
-    int* Lq = Ws + DI * 33;                          // per warp: the entry's 128 words and 32 scales
-    float* Kf = reinterpret_cast<float*>(Lq + CA_WARPS * 160);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
-    pdl_wait();
-    pdl_launch_next();
-    const int64_t pos0 = a.pos0[b];
-    const int odd = a.ratio == 2 ? (int)(pos0 & 1) : 0;
-    const int64_t e0 = min(a.ratio == 2 ? (pos0 - odd) / 2 : pos0, (int64_t)a.capacity);
-    const int32_t* path = a.path ? a.path + (int64_t)b * a.n_path : nullptr;
-    const uint16_t* rows = a.rows + (int64_t)b * a.n_rows * D_LAT;
-    const int i0 = blockIdx.x * CA_WARPS * a.per_warp;
-    const int64_t last = (int64_t)(i0 + CA_WARPS * a.per_warp) * a.ratio;
-    const int length = ca_length(path, blockIdx.x == 0 ? a.n_path : (int)min((int64_t)a.n_path, last), a.n_rows);
-    if (DI > 0) {
-        for (int i = tid; i < DI * 128; i += CA_WARPS * 32)
-            Wq[(i >> 7) * WS + (i & 127)] =
-                (int)unpack4_int8(reinterpret_cast<const uint16_t*>(a.wik_codes + (int64_t)(i >> 7) * (D_LAT / 2))[i & 127]);
-        for (int i = tid; i < DI * 32; i += CA_WARPS * 32) Ws[(i >> 5) * 33 + (i & 31)] = cw_e4m3_x512(a.wik_scales[i]);
-        __syncthreads();
+    // how many of the path's first `upto` steps are rows that exist, a whole warp together
+    __device__ __forceinline__ int length(const AppendArgs& a, int upto) const {
+        if (path == nullptr) return upto;
+        const int lane = threadIdx.x & 31;
+        for (int j0 = 0; j0 < upto; j0 += 32) {
+            const unsigned there = __ballot_sync(0xffffffffu, j0 + lane < upto && (unsigned)path[j0 + lane] < (unsigned)a.n_rows);
+            if (there != 0xffffffffu) return min(upto, j0 + __ffs(~there) - 1);
+        }
+        return upto;
     }
-    auto row_of = [&](int j) { return rows + (int64_t)(path ? path[j] : j) * D_LAT + lane * 16; };
-    for (int n = 0; n < a.per_warp; ++n) {
-        const int i = i0 + warp + n * CA_WARPS;
-        const int j = i * a.ratio - odd;                 // the row of the entry's first position; -1: the carried one
-        const int64_t e = e0 + i;
-        if (j + a.ratio - 1 >= length || e < 0 || e >= a.capacity) continue;         // warp-uniform
-        const int64_t entry = (int64_t)b * a.capacity + e;
+    __device__ __forceinline__ const uint16_t* row(int j) const { return rows + (int64_t)(path ? path[j] : j) * D_LAT; }
+    // the entry's 16 channels of this lane's group, quantised; its first row is step j (-1: the carried row)
+    __device__ __forceinline__ void entry(const AppendArgs& a, int b, int j, uint32_t& q0, uint32_t& q1, uint32_t& sb) const {
+        const int at = (threadIdx.x & 31) * 16;
         float x[16];
-        row16(j < 0 ? a.prev + (int64_t)b * D_LAT + lane * 16 : row_of(j), x);
+        row16((j < 0 ? a.prev + (int64_t)b * D_LAT : row(j)) + at, x);
         if (a.ratio == 2) {
             float y[16];
-            row16(row_of(j + 1), y);
-            merge16(x, y, a.w0 + lane * 16, a.w1 + lane * 16);
+            row16(row(j + 1) + at, y);
+            merge16(x, y, a.w0 + at, a.w1 + at);
         }
-        uint32_t q0, q1, sb;
         quant_group16(x, q0, q1, sb);
-        reinterpret_cast<uint2*>(a.lat_codes + entry * (D_LAT / 2))[lane] = make_uint2(q0, q1);
-        a.lat_scales[entry * (D_LAT / 16) + lane] = (uint8_t)sb;
-        if constexpr (DI > 0) {
-            int* Lw = Lq + warp * 160;
-            float* Kw = Kf + warp * DI;
-            Lw[4 * lane] = (int)unpack4_int8(q0 & 0xffffu);
-            Lw[4 * lane + 1] = (int)unpack4_int8(q0 >> 16);
-            Lw[4 * lane + 2] = (int)unpack4_int8(q1 & 0xffffu);
-            Lw[4 * lane + 3] = (int)unpack4_int8(q1 >> 16);
-            Lw[128 + lane] = cw_e4m3_x512(sb);
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < DI / 32; ++t) {
-                const int d = lane + 32 * t;
-                long long D = 0;
-#pragma unroll 8
-                for (int g = 0; g < 32; ++g) {
-                    const int G4 = group_dot4(Wq + d * WS + 4 * g, reinterpret_cast<const uint32_t*>(Lw + 4 * g));
-                    D += (long long)(G4 * Ws[d * 33 + g]) * Lw[128 + g];
-                }
-                Kw[d] = __ll2float_rn(D) * 0x1p-20f;        // one rounding; the power of two is exact
-            }
-            __syncwarp();
-            if (lane < DI / 16) {
-                float kx[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) kx[c] = Kw[16 * lane + c];
-                quant_group16(kx, q0, q1, sb);
-                reinterpret_cast<uint2*>(a.ik_codes + entry * (DI / 2))[lane] = make_uint2(q0, q1);
-                a.ik_scales[entry * (DI / 16) + lane] = (uint8_t)sb;
-            }
-            __syncwarp();
-        }
     }
-    if (blockIdx.x == 0 && a.prev_out != nullptr) {
-        __syncthreads();                                 // prev_out may be prev: its last reader is this block
-        const uint4* src = reinterpret_cast<const uint4*>(
-            length > 0 ? rows + (int64_t)(path ? path[length - 1] : length - 1) * D_LAT : a.prev + (int64_t)b * D_LAT);
-        if (tid < D_LAT / 8) reinterpret_cast<uint4*>(a.prev_out + (int64_t)b * D_LAT)[tid] = src[tid];
+};
+__device__ __forceinline__ void store_latent(const AppendArgs& a, int64_t entry, uint32_t q0, uint32_t q1, uint32_t sb) {
+    const int lane = threadIdx.x & 31;
+    reinterpret_cast<uint2*>(a.lat_codes + entry * (D_LAT / 2))[lane] = make_uint2(q0, q1);
+    a.lat_scales[entry * (D_LAT / 16) + lane] = (uint8_t)sb;
+}
+// the row of the path's last position, or the carried one, to prev_out (which may be prev: whoever reads it is done)
+__device__ __forceinline__ void carry_on(const AppendArgs& a, const AppendSeq& s, int b, int length) {
+    const int lane = threadIdx.x & 31;
+    const uint4* src = reinterpret_cast<const uint4*>(length > 0 ? s.row(length - 1) : a.prev + (int64_t)b * D_LAT);
+    uint4* dst = reinterpret_cast<uint4*>(a.prev_out + (int64_t)b * D_LAT);
+    const uint4 x = src[lane], y = src[32 + lane];
+    dst[lane] = x, dst[32 + lane] = y;
+}
+
+// Few entries, or no indexer keys.  DI = 0: a warp an entry.  Else a block an entry and a warp a group of 16 key dims (it
+// makes the entry for itself: nothing is handed from warp to warp): lane g multiplies latent group g with 16 rows of W,
+// exactly (k_cache_write_proj has the bounds), the 16 sums over the lanes are halved in turn, and the group is quantised.
+// What bounds it are five loads in a row, position, path, rows, weights' products, stores: 64 entries of 128 keys take 3.6 us.
+template <int DI>
+__global__ void __launch_bounds__(256) k_cache_append(const __grid_constant__ AppendArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
+    pdl_wait();
+    pdl_launch_next();
+    const AppendSeq s(a, b);
+    const int i = DI > 0 ? (int)blockIdx.x : (int)blockIdx.x * 8 + warp;
+    const int j = i * a.ratio - s.odd;                   // the step of the entry's first position; -1: the carried row
+    const bool first = blockIdx.x == 0 && warp == 0 && a.prev_out != nullptr;
+    const int length = s.length(a, first ? a.n_path : min(a.n_path, j + a.ratio));
+    const int64_t e = s.e0 + i;
+    const bool there = i < a.n_ent && j + a.ratio <= length && e >= 0 && e < a.capacity;
+    uint2 wc[16];
+    uint32_t wsc[16], q0 = 0u, q1 = 0u, sb = 0u;
+    if constexpr (DI > 0) {
+        if (there)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int64_t d = warp * 16 + k;
+                wc[k] = reinterpret_cast<const uint2*>(a.wik_codes + d * (D_LAT / 2))[lane];
+                wsc[k] = a.wik_scales[d * (D_LAT / 16) + lane];
+            }
+    }
+    if (there) s.entry(a, b, j, q0, q1, sb);
+    if (DI > 0 && blockIdx.x == 0) __syncthreads();      // every warp (every lane) has read the carried row
+    __syncwarp();
+    if (first) carry_on(a, s, b, length);
+    if (!there) return;
+    const int64_t entry = (int64_t)b * a.capacity + e;
+    if (DI == 0 || warp == 0) store_latent(a, entry, q0, q1, sb);
+    if constexpr (DI > 0) {
+        const uint32_t L[4] = {unpack4_int8(q0 & 0xffffu), unpack4_int8(q0 >> 16), unpack4_int8(q1 & 0xffffu), unpack4_int8(q1 >> 16)};
+        const int sl = cw_e4m3_x512(sb);
+        long long t[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int w[4] = {(int)unpack4_int8(wc[k].x & 0xffffu), (int)unpack4_int8(wc[k].x >> 16),
+                              (int)unpack4_int8(wc[k].y & 0xffffu), (int)unpack4_int8(wc[k].y >> 16)};
+            t[k] = (long long)(group_dot4(w, L) * cw_e4m3_x512(wsc[k])) * sl;
+        }
+        // sums over the lanes: each step a lane keeps half of the dims, and has dim lane / 2 in the end
+        const auto halve = [&](auto left, int o) {
+            constexpr int n = decltype(left)::value;
+            const bool up = lane & o;
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+                const long long give = up ? t[k] : t[k + n], keep = up ? t[k + n] : t[k];
+                t[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+        };
+        halve(std::integral_constant<int, 8>{}, 16);
+        halve(std::integral_constant<int, 4>{}, 8);
+        halve(std::integral_constant<int, 2>{}, 4);
+        halve(std::integral_constant<int, 1>{}, 2);
+        t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
+        const float mine = __ll2float_rn(t[0]) * 0x1p-20f;       // one rounding; the power of two is exact
+        float kx[16];
+#pragma unroll
+        for (int d = 0; d < 16; ++d) kx[d] = __shfl_sync(0xffffffffu, mine, 2 * d);
+        quant_group16(kx, q0, q1, sb);
+        if (lane == 0) {
+            *reinterpret_cast<uint2*>(a.ik_codes + entry * (DI / 2) + warp * 8) = make_uint2(q0, q1);
+            a.ik_scales[entry * (DI / 16) + warp] = (uint8_t)sb;
+        }
     }
 }
 
-// Entries as values: eight a thread (one 4-byte word of codes, its group's scale), exact in every output type: an E2M1
-// value times an E4M3 scale has at most 6 significant bits and lies in [2^-10, 2688].
-template <typename TO>
-__global__ void __launch_bounds__(256) k_cache_read(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                    int capacity, int d, const int32_t* __restrict__ idx, int64_t first,
-                                                    int64_t n, int64_t total, TO* __restrict__ out) {
+// Many entries with their indexer keys.  A key is sum_g G_g sL_g sW_g over 32 groups; G, sixteen products of E2M1 values, has 12
+// bits in quarters, the scales 4 each, so that a group's term has 20 bits and comes exactly out of one m16n8k16 product of the
+// scaled values (fp16 holds them exactly).  The sum has to be exact too, over 53 bits.  It is held in three fp32 sums: the
+// first two start at 1.5 x 2^33 and 1.5 x 2^15 and are never more than 2^32 and 2^14 away from there, so that their last bits
+// stay 2^10 and 2^-8; adding a term to the first leaves a remainder (exact, at most 2^9), which is added to the second; its
+// remainder (at most 2^-9, a multiple of 2^-20) goes into the third.  Seven additions a term, no 64-bit arithmetic: they
+// bound the kernel (4 x 4,096 entries of 128 keys: 14 us of them at the fp32 rate; int8 products and 64-bit sums took 112).
+// A warp keeps eight dims of W for all groups in registers; blocks walk tiles of 32 entries, which all warps quantise.
+constexpr int CM_TILE = 32, CM_WARPS = 16;
+
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* x, uint32_t y0, uint32_t y1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y0), "r"(y1), "f"(0.0f));
+}
+// two codes of a byte (low nibble first) times the scale
+__device__ __forceinline__ uint32_t pair_scaled(uint32_t byte, __half2 s) {
+    uint32_t r;
+    asm("{\n .reg .b8 x, y, z, w;\n mov.b32 {x, y, z, w}, %1;\n cvt.rn.f16x2.e2m1x2 %0, x;\n}" : "=r"(r) : "r"(byte));
+    const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&r), s);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int DI>
+__global__ void __launch_bounds__(CM_WARPS * 32, 1) k_cache_append_many(const __grid_constant__ AppendArgs a, int tiles, int batch) {
+    extern __shared__ __align__(16) uint8_t A[];             // entries x 512 fp16, 16-byte pieces at p ^ (entry & 7)
+    float(*K)[DI + 4] = reinterpret_cast<float(*)[DI + 4]>(A + CM_TILE * 1024);      // the tile's keys
+    __shared__ int64_t entry_at[CM_TILE];                    // -1: not there
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int NT = DI / 8;                               // tiles of eight dims; with 8, half of the warps take every half tile of entries
+    const int nt = warp % NT, half0 = warp / NT;
     pdl_wait();
     pdl_launch_next();
-    const int per_row = d / 8;
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
-        const int64_t row = u / per_row;
-        const int c = (int)(u - row * per_row);
-        const int64_t b = row / n;
-        const int64_t e = idx ? (int64_t)idx[row] : first + (row - b * n);
-        uint32_t w = 0u, s = 0u;
-        if (e >= 0 && e < capacity) {
-            const int64_t at = b * capacity + e;
-            w = reinterpret_cast<const uint32_t*>(codes + at * (d / 2))[c];
-            s = scales[at * (d / 16) + (c >> 1)];
-        }
-        __half2 h[4];
-        e2m1x8_to_f16x8(w, h);
-        const __half2 s2 = __half2half2(__low2half(e4m3x2_to_f16x2(s)));
-        float v[8];
+    // B of group g: rows 2 (lane % 4) + {0, 1} and 8 further, column lane / 4: bytes lane % 4 and 4 + lane % 4 of the dim's eight
+    uint32_t B[32][2];
+    {
+        const int d = nt * 8 + (lane >> 2);
+        const uint2* wc = reinterpret_cast<const uint2*>(a.wik_codes + (int64_t)d * (D_LAT / 2));
+        const uint8_t* wsc = a.wik_scales + (int64_t)d * (D_LAT / 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(__hmul2(h[i], s2));
-            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        for (int g = 0; g < 32; ++g) {
+            const uint2 c = wc[g];
+            const __half2 s = __float2half2_rn((float)cw_e4m3_x512(wsc[g]) * 0x1p-9f);       // (as the exact integers take it)
+            B[g][0] = pair_scaled(c.x >> (8 * (lane & 3)), s);
+            B[g][1] = pair_scaled(c.y >> (8 * (lane & 3)), s);
         }
-        ElemVec<TO, 8> y;
-        y.pack(v);
-        y.store(out + row * d + 8 * c);
+    }
+    const uint32_t abase = (uint32_t)__cvta_generic_to_shared(A);
+    for (int tile = blockIdx.x; tile < tiles * batch; tile += gridDim.x) {
+        const int b = tile / tiles, i0 = (tile - b * tiles) * CM_TILE;
+        const AppendSeq s(a, b);
+        const bool first = i0 == 0 && warp == 0 && a.prev_out != nullptr;
+        const int upto = (int)min((int64_t)a.n_path, (int64_t)(i0 + CM_TILE) * a.ratio);
+        const int length = s.length(a, first ? a.n_path : upto);
+        // ---- the entries, two a warp: lane g has channel group g
+#pragma unroll
+        for (int n = 0; n < CM_TILE / CM_WARPS; ++n) {
+            const int r = warp + n * CM_WARPS, i = i0 + r, j = i * a.ratio - s.odd;
+            const int64_t e = s.e0 + i, entry = (int64_t)b * a.capacity + e;
+            uint32_t q0 = 0u, q1 = 0u, sb = 0u;
+            const bool there = i < a.n_ent && j + a.ratio <= length && e >= 0 && e < a.capacity;
+            if (there) {
+                s.entry(a, b, j, q0, q1, sb);
+                store_latent(a, entry, q0, q1, sb);
+            }
+            const __half2 sc = __half2half2(__low2half(e4m3x2_to_f16x2(sb)));
+            *reinterpret_cast<uint4*>(A + r * 1024 + (((2 * lane) ^ (r & 7)) << 4)) = e2m1x8_scaled(q0, sc);
+            *reinterpret_cast<uint4*>(A + r * 1024 + (((2 * lane + 1) ^ (r & 7)) << 4)) = e2m1x8_scaled(q1, sc);
+            if (lane == 0) entry_at[r] = there ? entry : -1;
+        }
+        __syncthreads();
+        if (first) carry_on(a, s, b, length);                // (the carried row is read)
+        // ---- products, 16 entries x 8 dims a warp at a time
+        for (int m = half0; m < CM_TILE / 16; m += CM_WARPS / NT) {
+            float s1[4], s2[4], s3[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) s1[v] = 0x1.8p33f, s2[v] = 0x1.8p15f, s3[v] = 0.0f;
+            const int r = m * 16 + (lane & 15);
+#pragma unroll
+            for (int g = 0; g < 32; ++g) {
+                uint32_t x[4];
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                             : "r"(abase + r * 1024 + (((2 * g + (lane >> 4)) ^ (r & 7)) << 4)));
+                float t[4];
+                mma16816(t, x, B[g][0], B[g][1]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float n1 = __fadd_rn(s1[v], t[v]), r1 = __fsub_rn(t[v], __fsub_rn(n1, s1[v]));
+                    const float n2 = __fadd_rn(s2[v], r1), r2 = __fsub_rn(r1, __fsub_rn(n2, s2[v]));
+                    s1[v] = n1, s2[v] = n2, s3[v] = __fadd_rn(s3[v], r2);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {                    // the three as one number of 2^-20: exact, then one rounding
+                const long long sum = ((long long)__float2int_rn(__fsub_rn(s1[v], 0x1.8p33f) * 0x1p-10f) << 30) +
+                                      ((long long)__float2int_rn(__fsub_rn(s2[v], 0x1.8p15f) * 0x1p8f) << 12) +
+                                      __float2int_rn(s3[v] * 0x1p20f);
+                K[m * 16 + (lane >> 2) + 8 * (v >> 1)][nt * 8 + 2 * (lane & 3) + (v & 1)] = __ll2float_rn(sum) * 0x1p-20f;
+            }
+        }
+        __syncthreads();
+        for (int u = tid; u < CM_TILE * (DI / 16); u += CM_WARPS * 32) {
+            const int r = u / (DI / 16), g = u % (DI / 16);
+            const int64_t entry = entry_at[r];
+            if (entry < 0) continue;
+            float kx[16];
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(&K[r][16 * g + c]);
+                kx[c] = v.x, kx[c + 1] = v.y, kx[c + 2] = v.z, kx[c + 3] = v.w;
+            }
+            uint32_t q0, q1, sb;
+            quant_group16(kx, q0, q1, sb);
+            *reinterpret_cast<uint2*>(a.ik_codes + entry * (DI / 2) + g * 8) = make_uint2(q0, q1);
+            a.ik_scales[entry * (DI / 16) + g] = (uint8_t)sb;
+        }
+        __syncthreads();                                     // A, K and entry_at are read
     }
 }
+
+// Entries as values: a unit is eight of them (one 4-byte word of codes, its group's scale), exact in every output type: an
+// E2M1 value times an E4M3 scale has at most 6 significant bits and lies in [2^-10, 2688].  HBM bounds it, with eight units of a
+// thread asked for at once (8 x 65,536 latents in fp16: 101 us, 6.8 TB/s; with one 152 us); a call that one unit a thread of
+// all SMs holds has one, which is 2 us shorter.
+template <typename TO, int CR_UNITS>
+__global__ void __launch_bounds__(256) k_cache_read(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                    int capacity, int shift, int batch, const int32_t* __restrict__ idx, int64_t first,
+                                                    int64_t n, TO* __restrict__ out) {
+    pdl_wait();
+    pdl_launch_next();
+    const int d = 8 << shift;
+    const int64_t units = n << shift, u0 = (int64_t)blockIdx.x * (256 * CR_UNITS) + threadIdx.x;
+    for (int b = blockIdx.y; b < batch; b += gridDim.y) {
+        int64_t at[CR_UNITS];
+        uint32_t w[CR_UNITS], s[CR_UNITS];
+#pragma unroll
+        for (int i = 0; i < CR_UNITS; ++i) {
+            const int64_t u = u0 + i * 256, row = u >> shift;
+            at[i] = -1;
+            if (u < units) {
+                const int64_t e = idx ? (int64_t)idx[b * n + row] : first + row;
+                if (e >= 0 && e < capacity) at[i] = (int64_t)b * capacity + e;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CR_UNITS; ++i) {
+            const int c = (int)((u0 + i * 256) & ((1 << shift) - 1));
+            w[i] = s[i] = 0u;
+            if (at[i] >= 0) {
+                w[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + at[i] * (d / 2)) + c);
+                s[i] = __ldg(scales + at[i] * (d / 16) + (c >> 1));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CR_UNITS; ++i) {
+            const int64_t u = u0 + i * 256;
+            if (u >= units) break;
+            __half2 h[4];
+            e2m1x8_to_f16x8(w[i], h);
+            const __half2 s2 = __half2half2(__low2half(e4m3x2_to_f16x2(s[i])));
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(__hmul2(h[k], s2));
+                v[2 * k] = f.x, v[2 * k + 1] = f.y;
+            }
+            ElemVec<TO, 8> y;
+            y.pack(v);
+            y.store(out + (b * units + u) * 8);
+        }
+    }
+}
+
+// Entries of a call from which on the tensor cores make their keys: a block of it has W in registers first (2 us), and below
+// this the warps of k_cache_append have less to do than that costs (2,048 entries: measured below)
+constexpr int64_t CA_MANY = 2048;
 
 cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n_rows, const int32_t* path, int n_path,
                                 const int64_t* pos0, const uint16_t* prev, uint16_t* prev_out, const float* w0,
@@ -180,27 +337,37 @@ cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n
     const bool carry = c.ratio == 2 && prev_out != nullptr;
     if (n_ent == 0 && (!carry || prev_out == prev)) return cudaSuccess;
     const int di = wik_codes ? c.d_idx : 0;
-    AppendArgs a{c.lat_codes, c.lat_scales, c.ikey_codes, c.ikey_scales, c.capacity, c.ratio, c.d_idx, rows, n_rows, path, n_path,
-                 pos0, prev, carry ? prev_out : nullptr, w0, w1, wik_codes, wik_scales, n_ent > 64 ? 8 : 1};
-    const auto kern = di == 128 ? k_cache_append<128> : di == 64 ? k_cache_append<64> : k_cache_append<0>;
-    const size_t smem = di ? ((size_t)di * (129 + 33) + CA_WARPS * 160 + CA_WARPS * di) * sizeof(int) : 0;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const int per = CA_WARPS * a.per_warp;
-    e = launch_k(kern, dim3((unsigned)std::max(1, (n_ent - 1) / per + 1), c.batch), CA_WARPS * 32, smem, st, a);
+    const AppendArgs a{c.lat_codes, c.lat_scales, c.ikey_codes, c.ikey_scales, c.capacity, c.ratio, rows, n_rows, path, n_path, n_ent,
+                       pos0, prev, carry ? prev_out : nullptr, w0, w1, wik_codes, wik_scales};
+    if (di > 0 && (int64_t)n_ent * c.batch >= CA_MANY) {
+        const int tiles = (n_ent - 1) / CM_TILE + 1;
+        const unsigned grid = (unsigned)std::min<int64_t>((int64_t)tiles * c.batch, 152);
+        const auto kern = di == 128 ? k_cache_append_many<128> : k_cache_append_many<64>;
+        const int smem = CM_TILE * (1024 + (di + 4) * (int)sizeof(float));
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        launch_k(kern, dim3(grid), CM_WARPS * 32, (size_t)smem, st, a, tiles, (int)c.batch);
+    } else if (di > 0) {
+        launch_k(di == 128 ? k_cache_append<128> : k_cache_append<64>, dim3((unsigned)std::max(1, n_ent), c.batch), di * 2, 0, st, a);
+    } else {
+        launch_k(k_cache_append<0>, dim3((unsigned)std::max(1, (n_ent + 7) / 8), c.batch), 256, 0, st, a);
+    }
     note_launch();
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const csa2_cache& c, bool keys, const int32_t* idx, int64_t first, int64_t n, void* out,
                               int out_type, cudaStream_t st) {
-    const int d = keys ? c.d_idx : D_LAT;
-    const int64_t total = (int64_t)c.batch * n * (d / 8);
+    const int shift = keys ? (c.d_idx == 128 ? 4 : 3) : 6;           // units of a row: 2^shift
     const uint8_t *codes = keys ? c.ikey_codes : c.lat_codes, *scales = keys ? c.ikey_scales : c.lat_scales;
-    const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 152 * 64);
+    const bool few = ((n << shift) * c.batch) <= 152 * 2048;
+    const int64_t per = 256 * (few ? 1 : 8), blocks = ((n << shift) + per - 1) / per;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks, (unsigned)std::min(c.batch, 65535));
     auto go = [&](auto* y) {
         using TO = std::remove_pointer_t<decltype(y)>;
-        launch_k(k_cache_read<TO>, dim3(grid), 256, 0, st, codes, scales, (int)c.capacity, d, idx, first, n, total, y);
+        launch_k(few ? k_cache_read<TO, 1> : k_cache_read<TO, 8>, grid, 256, 0, st, codes, scales, (int)c.capacity, shift, (int)c.batch,
+                 idx, first, n, y);
     };
     if (out_type == CSA2_F32)
         go(reinterpret_cast<float*>(out));
