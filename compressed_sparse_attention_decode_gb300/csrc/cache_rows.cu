@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "fp4_f16.cuh"
+#include "tree.cuh"
 
 namespace csa2 {
 
@@ -159,8 +160,9 @@ __global__ void __launch_bounds__(256) k_cache_append(const __grid_constant__ Ap
 // stay 2^10 and 2^-8; adding a term to the first leaves a remainder (exact, at most 2^9), which is added to the second; its
 // remainder (at most 2^-9, a multiple of 2^-20) goes into the third.  Seven additions a term, no 64-bit arithmetic: they
 // bound the kernel (4 x 4,096 entries of 128 keys: 14 us of them at the fp32 rate; int8 products and 64-bit sums took 112).
-// A warp keeps eight dims of W for all groups in registers; blocks walk tiles of 32 entries, which all warps quantise.
-constexpr int CM_TILE = 32, CM_WARPS = 16;
+// A warp keeps eight dims of W for all groups in registers; blocks walk tiles of 16 entries, which all warps quantise,
+// the next tile's rows on their way to shared memory meanwhile.
+constexpr int CM_TILE = 16;
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* x, uint32_t y0, uint32_t y1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
@@ -176,19 +178,18 @@ __device__ __forceinline__ uint32_t pair_scaled(uint32_t byte, __half2 s) {
 }
 
 template <int DI>
-__global__ void __launch_bounds__(CM_WARPS * 32, 1) k_cache_append_many(const __grid_constant__ AppendArgs a, int tiles, int batch) {
+__global__ void __launch_bounds__(DI * 4, 128 / DI) k_cache_append_many(const __grid_constant__ AppendArgs a, int tiles, int batch) {
     extern __shared__ __align__(16) uint8_t A[];             // entries x 512 fp16, 16-byte pieces at p ^ (entry & 7)
     float(*K)[DI + 4] = reinterpret_cast<float(*)[DI + 4]>(A + CM_TILE * 1024);      // the tile's keys
     __shared__ int64_t entry_at[CM_TILE];                    // -1: not there
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int NT = DI / 8;                               // tiles of eight dims; with 8, half of the warps take every half tile of entries
-    const int nt = warp % NT, half0 = warp / NT;
+    constexpr int CM_WARPS = DI / 8;                         // one for eight dims
     pdl_wait();
     pdl_launch_next();
     // B of group g: rows 2 (lane % 4) + {0, 1} and 8 further, column lane / 4: bytes lane % 4 and 4 + lane % 4 of the dim's eight
     uint32_t B[32][2];
     {
-        const int d = nt * 8 + (lane >> 2);
+        const int d = warp * 8 + (lane >> 2);
         const uint2* wc = reinterpret_cast<const uint2*>(a.wik_codes + (int64_t)d * (D_LAT / 2));
         const uint8_t* wsc = a.wik_scales + (int64_t)d * (D_LAT / 16);
 #pragma unroll
@@ -200,32 +201,69 @@ __global__ void __launch_bounds__(CM_WARPS * 32, 1) k_cache_append_many(const __
         }
     }
     const uint32_t abase = (uint32_t)__cvta_generic_to_shared(A);
-    for (int tile = blockIdx.x; tile < tiles * batch; tile += gridDim.x) {
+    // a warp has CM_TILE / CM_WARPS entries of a tile, and asks for their rows itself
+    constexpr int NE = CM_TILE / CM_WARPS;
+    uint8_t* raw = A + CM_TILE * (1024 + (DI + 4) * (int)sizeof(float)) + warp * NE * 2048;
+    int64_t entry[NE];                                       // of the tile to come, -1: not there
+    int length = 0;
+    auto fetch = [&](int tile) {
         const int b = tile / tiles, i0 = (tile - b * tiles) * CM_TILE;
         const AppendSeq s(a, b);
         const bool first = i0 == 0 && warp == 0 && a.prev_out != nullptr;
-        const int upto = (int)min((int64_t)a.n_path, (int64_t)(i0 + CM_TILE) * a.ratio);
-        const int length = s.length(a, first ? a.n_path : upto);
-        // ---- the entries, two a warp: lane g has channel group g
+        length = s.length(a, first ? a.n_path : (int)min((int64_t)a.n_path, (int64_t)(i0 + CM_TILE) * a.ratio));
 #pragma unroll
-        for (int n = 0; n < CM_TILE / CM_WARPS; ++n) {
-            const int r = warp + n * CM_WARPS, i = i0 + r, j = i * a.ratio - s.odd;
-            const int64_t e = s.e0 + i, entry = (int64_t)b * a.capacity + e;
-            uint32_t q0 = 0u, q1 = 0u, sb = 0u;
+        for (int n = 0; n < NE; ++n) {
+            const int i = i0 + warp + n * CM_WARPS, j = i * a.ratio - s.odd;
+            const int64_t e = s.e0 + i;
             const bool there = i < a.n_ent && j + a.ratio <= length && e >= 0 && e < a.capacity;
-            if (there) {
-                s.entry(a, b, j, q0, q1, sb);
-                store_latent(a, entry, q0, q1, sb);
+            entry[n] = there ? (int64_t)b * a.capacity + e : -1;
+            if (there)
+                for (int k = 0; k < a.ratio; ++k) {
+                    const uint16_t* src = j + k < 0 ? a.prev + (int64_t)b * D_LAT : s.row(j + k);
+                    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(raw + n * 2048 + k * 1024);
+                    copy16(dst + lane * 16, src + lane * 8, true);
+                    copy16(dst + (32 + lane) * 16, src + (32 + lane) * 8, true);
+                }
+        }
+    };
+    if ((int)blockIdx.x < tiles * batch) fetch(blockIdx.x);
+    for (int tile = blockIdx.x; tile < tiles * batch; tile += gridDim.x) {
+        const int b = tile / tiles;
+        copy16_wait();
+        __syncwarp();
+        if (tile == b * tiles && warp == 0 && a.prev_out != nullptr) carry_on(a, AppendSeq(a, b), b, length);   // (the carried row is here)
+        // ---- the entries: lane g has channel group g
+#pragma unroll
+        for (int n = 0; n < NE; ++n) {
+            const int r = warp + n * CM_WARPS, at = lane * 16;
+            uint32_t q0 = 0u, q1 = 0u, sb = 0u;
+            if (entry[n] >= 0) {
+                float x[16], y[16];
+                auto take = [&](int k, float* v) {           // 32 bytes of a row
+                    const uint4* p = reinterpret_cast<const uint4*>(raw + n * 2048 + k * 1024) + 2 * lane;
+                    const uint4 c = p[0], d = p[1];
+                    const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = bf16_bits_to_f32((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xffffu));
+                };
+                take(0, x);
+                if (a.ratio == 2) {
+                    take(1, y);
+                    merge16(x, y, a.w0 + at, a.w1 + at);
+                }
+                quant_group16(x, q0, q1, sb);
+                store_latent(a, entry[n], q0, q1, sb);
             }
             const __half2 sc = __half2half2(__low2half(e4m3x2_to_f16x2(sb)));
             *reinterpret_cast<uint4*>(A + r * 1024 + (((2 * lane) ^ (r & 7)) << 4)) = e2m1x8_scaled(q0, sc);
             *reinterpret_cast<uint4*>(A + r * 1024 + (((2 * lane + 1) ^ (r & 7)) << 4)) = e2m1x8_scaled(q1, sc);
-            if (lane == 0) entry_at[r] = there ? entry : -1;
+            if (lane == 0) entry_at[r] = entry[n];
         }
         __syncthreads();
-        if (first) carry_on(a, s, b, length);                // (the carried row is read)
-        // ---- products, 16 entries x 8 dims a warp at a time
-        for (int m = half0; m < CM_TILE / 16; m += CM_WARPS / NT) {
+        if (tile + (int)gridDim.x < tiles * batch) fetch(tile + gridDim.x);
+        // ---- products, 16 entries x 8 dims a warp
+        {
+            constexpr int m = 0;
             float s1[4], s2[4], s3[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v) s1[v] = 0x1.8p33f, s2[v] = 0x1.8p15f, s3[v] = 0.0f;
@@ -250,7 +288,7 @@ __global__ void __launch_bounds__(CM_WARPS * 32, 1) k_cache_append_many(const __
                 const long long sum = ((long long)__float2int_rn(__fsub_rn(s1[v], 0x1.8p33f) * 0x1p-10f) << 30) +
                                       ((long long)__float2int_rn(__fsub_rn(s2[v], 0x1.8p15f) * 0x1p8f) << 12) +
                                       __float2int_rn(s3[v] * 0x1p20f);
-                K[m * 16 + (lane >> 2) + 8 * (v >> 1)][nt * 8 + 2 * (lane & 3) + (v & 1)] = __ll2float_rn(sum) * 0x1p-20f;
+                K[m * 16 + (lane >> 2) + 8 * (v >> 1)][warp * 8 + 2 * (lane & 3) + (v & 1)] = __ll2float_rn(sum) * 0x1p-20f;
             }
         }
         __syncthreads();
@@ -341,12 +379,12 @@ cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n
                        pos0, prev, carry ? prev_out : nullptr, w0, w1, wik_codes, wik_scales};
     if (di > 0 && (int64_t)n_ent * c.batch >= CA_MANY) {
         const int tiles = (n_ent - 1) / CM_TILE + 1;
-        const unsigned grid = (unsigned)std::min<int64_t>((int64_t)tiles * c.batch, 152);
+        const unsigned grid = (unsigned)std::min<int64_t>((int64_t)tiles * c.batch, 152 * (128 / di));
         const auto kern = di == 128 ? k_cache_append_many<128> : k_cache_append_many<64>;
-        const int smem = CM_TILE * (1024 + (di + 4) * (int)sizeof(float));
+        const int smem = CM_TILE * (1024 + (di + 4) * (int)sizeof(float) + 2048);
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        launch_k(kern, dim3(grid), CM_WARPS * 32, (size_t)smem, st, a, tiles, (int)c.batch);
+        launch_k(kern, dim3(grid), di * 4, (size_t)smem, st, a, tiles, (int)c.batch);
     } else if (di > 0) {
         launch_k(di == 128 ? k_cache_append<128> : k_cache_append<64>, dim3((unsigned)std::max(1, n_ent), c.batch), di * 2, 0, st, a);
     } else {
