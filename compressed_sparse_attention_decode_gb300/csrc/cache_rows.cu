@@ -158,11 +158,14 @@ __global__ void __launch_bounds__(256) k_cache_append(const __grid_constant__ Ap
 // scaled values (fp16 holds them exactly).  The sum has to be exact too, over 53 bits.  It is held in three fp32 sums: the
 // first two start at 1.5 x 2^33 and 1.5 x 2^15 and are never more than 2^32 and 2^14 away from there, so that their last bits
 // stay 2^10 and 2^-8; adding a term to the first leaves a remainder (exact, at most 2^9), which is added to the second; its
-// remainder (at most 2^-9, a multiple of 2^-20) goes into the third.  Seven additions a term, no 64-bit arithmetic: they
-// bound the kernel (4 x 4,096 entries of 128 keys: 14 us of them at the fp32 rate; int8 products and 64-bit sums took 112).
-// A warp keeps eight dims of W for all groups in registers; blocks walk tiles of 16 entries, which all warps quantise,
-// the next tile's rows on their way to shared memory meanwhile.
-constexpr int CM_TILE = 16;
+// remainder (at most 2^-9, a multiple of 2^-20) goes into the third.  Seven additions a term, no 64-bit arithmetic.  The
+// products bound the kernel: an SM's quarter takes an m16n8k16 every 32 clocks or so, and the additions some of what is left
+// (4 x 4,096 entries of 128 keys: 48 us; int8 products and 64-bit sums took 105).
+// W is expanded to shared memory once a block, in the products' order.  Sixteen warps quantise a tile of 32 entries (two each,
+// whose rows they have asked for a tile ahead) while the other sixteen multiply the tile before; one of those has 16 entries
+// and a key group of 16 dims, which it quantises from its sums (all warps doing one after the other: 60 us).
+constexpr int CM_TILE = 32, CM_MAKERS = 16, CM_THREADS = 1024;
+constexpr int CM_A = CM_TILE * 1024, CM_RAW = CM_MAKERS * 2048;      // bytes of a tile's entries (fp16), of the rows under way
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* x, uint32_t y0, uint32_t y1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
@@ -178,136 +181,162 @@ __device__ __forceinline__ uint32_t pair_scaled(uint32_t byte, __half2 s) {
 }
 
 template <int DI>
-__global__ void __launch_bounds__(DI * 4, 128 / DI) k_cache_append_many(const __grid_constant__ AppendArgs a, int tiles, int batch) {
-    extern __shared__ __align__(16) uint8_t A[];             // entries x 512 fp16, 16-byte pieces at p ^ (entry & 7)
-    float(*K)[DI + 4] = reinterpret_cast<float(*)[DI + 4]>(A + CM_TILE * 1024);      // the tile's keys
-    __shared__ int64_t entry_at[CM_TILE];                    // -1: not there
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int CM_WARPS = DI / 8;                         // one for eight dims
+__global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __grid_constant__ AppendArgs a, int tiles, int batch) {
+    extern __shared__ __align__(16) uint8_t A[];             // two tiles: entries x 512 fp16, 16-byte pieces at p ^ (entry & 7)
+    uint2* W = reinterpret_cast<uint2*>(A + 2 * CM_A + CM_RAW);      // [DI / 8][32 groups][32 lanes] the products' B
+    __shared__ int64_t entry_at[2][CM_TILE];                 // -1: not there
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, all = tiles * batch;
     pdl_wait();
     pdl_launch_next();
-    // B of group g: rows 2 (lane % 4) + {0, 1} and 8 further, column lane / 4: bytes lane % 4 and 4 + lane % 4 of the dim's eight
-    uint32_t B[32][2];
-    {
-        const int d = warp * 8 + (lane >> 2);
-        const uint2* wc = reinterpret_cast<const uint2*>(a.wik_codes + (int64_t)d * (D_LAT / 2));
-        const uint8_t* wsc = a.wik_scales + (int64_t)d * (D_LAT / 16);
-#pragma unroll
-        for (int g = 0; g < 32; ++g) {
-            const uint2 c = wc[g];
-            const __half2 s = __float2half2_rn((float)cw_e4m3_x512(wsc[g]) * 0x1p-9f);       // (as the exact integers take it)
-            B[g][0] = pair_scaled(c.x >> (8 * (lane & 3)), s);
-            B[g][1] = pair_scaled(c.y >> (8 * (lane & 3)), s);
-        }
+    // B of a group: rows 2 (lane % 4) + {0, 1} and 8 further, column lane / 4: bytes lane % 4 and 4 + lane % 4 of the dim's eight
+#pragma unroll 4
+    for (int u = warp; u < DI / 8 * 32; u += CM_THREADS / 32) {
+        const int64_t d = (u >> 5) * 8 + (lane >> 2);
+        const int g = u & 31;
+        const uint2 c = reinterpret_cast<const uint2*>(a.wik_codes + d * (D_LAT / 2))[g];
+        // (the scale as the exact integers take it)
+        const __half2 s = __float2half2_rn((float)cw_e4m3_x512(a.wik_scales[d * (D_LAT / 16) + g]) * 0x1p-9f);
+        W[u * 32 + lane] = make_uint2(pair_scaled(c.x >> (8 * (lane & 3)), s), pair_scaled(c.y >> (8 * (lane & 3)), s));
     }
-    const uint32_t abase = (uint32_t)__cvta_generic_to_shared(A);
-    // a warp has CM_TILE / CM_WARPS entries of a tile, and asks for their rows itself
-    constexpr int NE = CM_TILE / CM_WARPS;
-    uint8_t* raw = A + CM_TILE * (1024 + (DI + 4) * (int)sizeof(float)) + warp * NE * 2048;
-    int64_t entry[NE];                                       // of the tile to come, -1: not there
-    int length = 0;
-    auto fetch = [&](int tile) {
-        const int b = tile / tiles, i0 = (tile - b * tiles) * CM_TILE;
-        const AppendSeq s(a, b);
-        const bool first = i0 == 0 && warp == 0 && a.prev_out != nullptr;
-        length = s.length(a, first ? a.n_path : (int)min((int64_t)a.n_path, (int64_t)(i0 + CM_TILE) * a.ratio));
-#pragma unroll
-        for (int n = 0; n < NE; ++n) {
-            const int i = i0 + warp + n * CM_WARPS, j = i * a.ratio - s.odd;
+    __syncthreads();
+    // named barriers: 1 + buf the tile in buffer buf is made, 3 + buf it is read
+    if (warp < CM_MAKERS) {
+        // ================= entries: warp w makes entries w and 16 + w of a tile, lane g its channel group g
+        uint8_t* raw = A + 2 * CM_A + warp * 2048;
+        int64_t entry = -1;
+        int length = 0;
+        auto fetch = [&](int tile, int r) {                  // entry r's rows, if it is there
+            const int b = tile / tiles, i = (tile - b * tiles) * CM_TILE + r;
+            const AppendSeq s(a, b);
+            const int j = i * a.ratio - s.odd;
+            length = s.length(a, i == 0 && a.prev_out != nullptr ? a.n_path : min(a.n_path, j + a.ratio));
             const int64_t e = s.e0 + i;
             const bool there = i < a.n_ent && j + a.ratio <= length && e >= 0 && e < a.capacity;
-            entry[n] = there ? (int64_t)b * a.capacity + e : -1;
+            entry = there ? (int64_t)b * a.capacity + e : -1;
             if (there)
                 for (int k = 0; k < a.ratio; ++k) {
                     const uint16_t* src = j + k < 0 ? a.prev + (int64_t)b * D_LAT : s.row(j + k);
-                    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(raw + n * 2048 + k * 1024);
+                    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(raw + k * 1024);
                     copy16(dst + lane * 16, src + lane * 8, true);
                     copy16(dst + (32 + lane) * 16, src + (32 + lane) * 8, true);
                 }
-        }
-    };
-    if ((int)blockIdx.x < tiles * batch) fetch(blockIdx.x);
-    for (int tile = blockIdx.x; tile < tiles * batch; tile += gridDim.x) {
-        const int b = tile / tiles;
-        copy16_wait();
-        __syncwarp();
-        if (tile == b * tiles && warp == 0 && a.prev_out != nullptr) carry_on(a, AppendSeq(a, b), b, length);   // (the carried row is here)
-        // ---- the entries: lane g has channel group g
-#pragma unroll
-        for (int n = 0; n < NE; ++n) {
-            const int r = warp + n * CM_WARPS, at = lane * 16;
-            uint32_t q0 = 0u, q1 = 0u, sb = 0u;
-            if (entry[n] >= 0) {
+        };
+        if ((int)blockIdx.x < all) fetch(blockIdx.x, warp);
+        int n = 0;
+        for (int tile = blockIdx.x; tile < all; tile += gridDim.x, ++n) {
+            const int buf = n & 1;
+            if (n >= 2) asm volatile("bar.sync %0, %1;" ::"r"(3 + buf), "r"(CM_THREADS) : "memory");
+#pragma unroll 1
+            for (int r = warp; r < CM_TILE; r += CM_MAKERS) {
+                copy16_wait();
+                __syncwarp();
+                const int b = tile / tiles;
+                if (r == 0 && tile == b * tiles && a.prev_out != nullptr) carry_on(a, AppendSeq(a, b), b, length);     // (it is here)
+                const int64_t at = entry;
                 float x[16], y[16];
                 auto take = [&](int k, float* v) {           // 32 bytes of a row
-                    const uint4* p = reinterpret_cast<const uint4*>(raw + n * 2048 + k * 1024) + 2 * lane;
+                    const uint4* p = reinterpret_cast<const uint4*>(raw + k * 1024) + 2 * lane;
                     const uint4 c = p[0], d = p[1];
                     const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = bf16_bits_to_f32((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xffffu));
                 };
-                take(0, x);
-                if (a.ratio == 2) {
-                    take(1, y);
-                    merge16(x, y, a.w0 + at, a.w1 + at);
+                if (at >= 0) {
+                    take(0, x);
+                    if (a.ratio == 2) take(1, y);
                 }
-                quant_group16(x, q0, q1, sb);
-                store_latent(a, entry[n], q0, q1, sb);
+                __syncwarp();
+                if (r + CM_MAKERS < CM_TILE)
+                    fetch(tile, r + CM_MAKERS);
+                else if (tile + (int)gridDim.x < all)
+                    fetch(tile + gridDim.x, warp);
+                uint32_t q0 = 0u, q1 = 0u, sb = 0u;
+                if (at >= 0) {
+                    if (a.ratio == 2) merge16(x, y, a.w0 + lane * 16, a.w1 + lane * 16);
+                    quant_group16(x, q0, q1, sb);
+                    store_latent(a, at, q0, q1, sb);
+                }
+                const __half2 sc = __half2half2(__low2half(e4m3x2_to_f16x2(sb)));
+                uint8_t* row = A + buf * CM_A + r * 1024;
+                *reinterpret_cast<uint4*>(row + (((2 * lane) ^ (r & 7)) << 4)) = e2m1x8_scaled(q0, sc);
+                *reinterpret_cast<uint4*>(row + (((2 * lane + 1) ^ (r & 7)) << 4)) = e2m1x8_scaled(q1, sc);
+                if (lane == 0) entry_at[buf][r] = at;
             }
-            const __half2 sc = __half2half2(__low2half(e4m3x2_to_f16x2(sb)));
-            *reinterpret_cast<uint4*>(A + r * 1024 + (((2 * lane) ^ (r & 7)) << 4)) = e2m1x8_scaled(q0, sc);
-            *reinterpret_cast<uint4*>(A + r * 1024 + (((2 * lane + 1) ^ (r & 7)) << 4)) = e2m1x8_scaled(q1, sc);
-            if (lane == 0) entry_at[r] = entry[n];
+            __threadfence_block();
+            asm volatile("bar.arrive %0, %1;" ::"r"(1 + buf), "r"(CM_THREADS) : "memory");
         }
-        __syncthreads();
-        if (tile + (int)gridDim.x < tiles * batch) fetch(tile + gridDim.x);
-        // ---- products, 16 entries x 8 dims a warp
-        {
-            constexpr int m = 0;
-            float s1[4], s2[4], s3[4];
+    } else {
+        // ================= products: warp w has entries 16 (w % 2) .. + 15 and key group w / 2 (with 64 dims half of the warps
+        // have none)
+        const int w = warp - CM_MAKERS, m = w & 1, group = w >> 1;
+        const bool busy = group < DI / 16;
+        const uint32_t abase = (uint32_t)__cvta_generic_to_shared(A);
+        const uint2* B = W + group * 2048 + lane;
+        int n = 0;
+        for (int tile = blockIdx.x; tile < all; tile += gridDim.x, ++n) {
+            const int buf = n & 1;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + buf), "r"(CM_THREADS) : "memory");
+            float key[2][4];                                 // rows lane / 4 and 8 further, dims 8 h + 2 (lane % 4) + {0, 1}
+            int64_t at[2] = {-1, -1};
+            if (busy) {
+                const int r = m * 16 + (lane & 15);
+                at[0] = entry_at[buf][m * 16 + (lane >> 2)], at[1] = entry_at[buf][m * 16 + 8 + (lane >> 2)];
+                float s1[2][4], s2[2][4], s3[2][4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) s1[v] = 0x1.8p33f, s2[v] = 0x1.8p15f, s3[v] = 0.0f;
-            const int r = m * 16 + (lane & 15);
+                for (int v = 0; v < 8; ++v) s1[v >> 2][v & 3] = 0x1.8p33f, s2[v >> 2][v & 3] = 0x1.8p15f, s3[v >> 2][v & 3] = 0.0f;
+#pragma unroll 2
+                for (int g = 0; g < 32; ++g) {
+                    uint32_t x[4];
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                 : "r"(abase + buf * CM_A + r * 1024 + (((2 * g + (lane >> 4)) ^ (r & 7)) << 4)));
 #pragma unroll
-            for (int g = 0; g < 32; ++g) {
-                uint32_t x[4];
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                             : "r"(abase + r * 1024 + (((2 * g + (lane >> 4)) ^ (r & 7)) << 4)));
-                float t[4];
-                mma16816(t, x, B[g][0], B[g][1]);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint2 y = B[h * 1024 + g * 32];
+                        float t[4];
+                        mma16816(t, x, y.x, y.y);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const float n1 = __fadd_rn(s1[v], t[v]), r1 = __fsub_rn(t[v], __fsub_rn(n1, s1[v]));
-                    const float n2 = __fadd_rn(s2[v], r1), r2 = __fsub_rn(r1, __fsub_rn(n2, s2[v]));
-                    s1[v] = n1, s2[v] = n2, s3[v] = __fadd_rn(s3[v], r2);
+                        for (int v = 0; v < 4; ++v) {
+                            const float n1 = __fadd_rn(s1[h][v], t[v]), r1 = __fsub_rn(t[v], __fsub_rn(n1, s1[h][v]));
+                            const float n2 = __fadd_rn(s2[h][v], r1), r2 = __fsub_rn(r1, __fsub_rn(n2, s2[h][v]));
+                            s1[h][v] = n1, s2[h][v] = n2, s3[h][v] = __fadd_rn(s3[h][v], r2);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {                // the three as one number of 2^-20: exact, then one rounding
+                    const int h = v >> 2, c = v & 3;
+                    const long long sum = ((long long)__float2int_rn(__fsub_rn(s1[h][c], 0x1.8p33f) * 0x1p-10f) << 30) +
+                                          ((long long)__float2int_rn(__fsub_rn(s2[h][c], 0x1.8p15f) * 0x1p8f) << 12) +
+                                          __float2int_rn(s3[h][c] * 0x1p20f);
+                    key[h][c] = __ll2float_rn(sum) * 0x1p-20f;
                 }
             }
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {                    // the three as one number of 2^-20: exact, then one rounding
-                const long long sum = ((long long)__float2int_rn(__fsub_rn(s1[v], 0x1.8p33f) * 0x1p-10f) << 30) +
-                                      ((long long)__float2int_rn(__fsub_rn(s2[v], 0x1.8p15f) * 0x1p8f) << 12) +
-                                      __float2int_rn(s3[v] * 0x1p20f);
-                K[m * 16 + (lane >> 2) + 8 * (v >> 1)][warp * 8 + 2 * (lane & 3) + (v & 1)] = __ll2float_rn(sum) * 0x1p-20f;
+            if (tile + 2 * (int)gridDim.x < all) {
+                __threadfence_block();
+                asm volatile("bar.arrive %0, %1;" ::"r"(3 + buf), "r"(CM_THREADS) : "memory");
             }
-        }
-        __syncthreads();
-        for (int u = tid; u < CM_TILE * (DI / 16); u += CM_WARPS * 32) {
-            const int r = u / (DI / 16), g = u % (DI / 16);
-            const int64_t entry = entry_at[r];
-            if (entry < 0) continue;
-            float kx[16];
+            // a row's group lies in four lanes, four values each
+            if (busy)
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(&K[r][16 * g + c]);
-                kx[c] = v.x, kx[c + 1] = v.y, kx[c + 2] = v.z, kx[c + 3] = v.w;
-            }
-            uint32_t q0, q1, sb;
-            quant_group16(kx, q0, q1, sb);
-            *reinterpret_cast<uint2*>(a.ik_codes + entry * (DI / 2) + g * 8) = make_uint2(q0, q1);
-            a.ik_scales[entry * (DI / 16) + g] = (uint8_t)sb;
+                for (int i = 0; i < 2; ++i) {
+                    const float v[4] = {key[0][2 * i], key[0][2 * i + 1], key[1][2 * i], key[1][2 * i + 1]};
+                    float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const uint32_t sb = f32_to_e4m3_satfinite(__fdiv_rn(top, 6.0f));
+                    const float s = e4m3_to_f32(sb);
+                    uint32_t c[2] = {0u, 0u};
+                    if (s > 0.0f)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) c[h] = e2m1_code(v[2 * h], s) | (e2m1_code(v[2 * h + 1], s) << 4);
+                    if (at[i] >= 0) {
+                        uint8_t* codes = a.ik_codes + at[i] * (DI / 2) + group * 8 + (lane & 3);
+                        codes[0] = (uint8_t)c[0], codes[4] = (uint8_t)c[1];
+                        if ((lane & 3) == 0) a.ik_scales[at[i] * (DI / 16) + group] = (uint8_t)sb;
+                    }
+                }
         }
-        __syncthreads();                                     // A, K and entry_at are read
     }
 }
 
@@ -364,9 +393,9 @@ __global__ void __launch_bounds__(256) k_cache_read(const uint8_t* __restrict__ 
     }
 }
 
-// Entries of a call from which on the tensor cores make their keys: a block of it has W in registers first (2 us), and below
-// this the warps of k_cache_append have less to do than that costs (2,048 entries: measured below)
-constexpr int64_t CA_MANY = 2048;
+// Entries of a call from which on the tensor cores make their keys (512 entries: 12 us without them, 14 with them; 1,024:
+// 22 and 15)
+constexpr int64_t CA_MANY = 768;
 
 cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n_rows, const int32_t* path, int n_path,
                                 const int64_t* pos0, const uint16_t* prev, uint16_t* prev_out, const float* w0,
@@ -379,12 +408,12 @@ cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n
                        pos0, prev, carry ? prev_out : nullptr, w0, w1, wik_codes, wik_scales};
     if (di > 0 && (int64_t)n_ent * c.batch >= CA_MANY) {
         const int tiles = (n_ent - 1) / CM_TILE + 1;
-        const unsigned grid = (unsigned)std::min<int64_t>((int64_t)tiles * c.batch, 152 * (128 / di));
+        const unsigned grid = (unsigned)std::min<int64_t>((int64_t)tiles * c.batch, 152);
         const auto kern = di == 128 ? k_cache_append_many<128> : k_cache_append_many<64>;
-        const int smem = CM_TILE * (1024 + (di + 4) * (int)sizeof(float) + 2048);
+        const int smem = 2 * CM_A + CM_RAW + di * 1024;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        launch_k(kern, dim3(grid), di * 4, (size_t)smem, st, a, tiles, (int)c.batch);
+        launch_k(kern, dim3(grid), CM_THREADS, (size_t)smem, st, a, tiles, (int)c.batch);
     } else if (di > 0) {
         launch_k(di == 128 ? k_cache_append<128> : k_cache_append<64>, dim3((unsigned)std::max(1, n_ent), c.batch), di * 2, 0, st, a);
     } else {

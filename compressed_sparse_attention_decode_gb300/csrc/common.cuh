@@ -86,6 +86,24 @@ __device__ __forceinline__ uint32_t e2m1_code(float x, float s) {
     return m | ((x < 0.0f && m) ? 8u : 0u);
 }
 
+// E2M1 codes of 8 values for scale s > 0 as e2m1_code gives them, by three
+// comparisons a value, each choosing the next one's midpoint (seven, added up, were
+// half of the quantiser's instructions).
+__device__ __forceinline__ uint32_t e2m1_codes8(const float* x, float s) {
+    const float t1 = 0.25f * s, t3 = 0.75f * s, t5 = 1.25f * s, t7 = 1.75f * s, t10 = 2.5f * s, t14 = 3.5f * s, t20 = 5.0f * s;
+    uint32_t w = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(x[i]);
+        const bool p4 = a >= t7, p2 = a >= (p4 ? t14 : t3), p1 = a > (p4 ? (p2 ? t20 : t10) : (p2 ? t5 : t1));
+        if (p4) w |= 4u << (4 * i);
+        if (p2) w |= 2u << (4 * i);
+        if (p1) w |= 1u << (4 * i);
+        if (x[i] < -t1) w |= 8u << (4 * i);              // (a code of zero has no sign)
+    }
+    return w;
+}
+
 // Quantise 16 floats: scale byte = E4M3(amax/6) (IEEE division), two words of
 // packed codes (element 2i in the low nibble of byte i).
 __device__ __forceinline__ void quant_group16(const float* x, uint32_t& w0, uint32_t& w1, uint32_t& sbyte) {
@@ -97,10 +115,8 @@ __device__ __forceinline__ void quant_group16(const float* x, uint32_t& w0, uint
     w0 = 0u;
     w1 = 0u;
     if (s > 0.0f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w0 |= e2m1_code(x[i], s) << (4 * i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w1 |= e2m1_code(x[8 + i], s) << (4 * i);
+        w0 = e2m1_codes8(x, s);
+        w1 = e2m1_codes8(x + 8, s);
     }
 }
 
