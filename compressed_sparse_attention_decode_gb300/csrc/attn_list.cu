@@ -14,6 +14,8 @@
 //   softmax         one head and 16 keys per thread, weights against a reference that is raised, and O rescaled in TMEM, only
 //                   when a score rises far above it
 //   O^T += L^T . P  (M = 4 x 128 dims, N = the heads in steps of 16, K = 64 keys; two issuers)
+// Weights are fp16 (2^-11 of each) where the output is of 16 bits, and two fp16 parts (2^-22) where it is fp32: the value MMAs
+// double, both parts take the two P buffers, and P waits for the values of the tile before.
 // The window rows are fp16 values of a power-of-two scale of their own; O carries the scale of the tile last added, and is
 // brought to the entries' after the window where they differ.
 // Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 rows, 20-23 the queries, fetched for the next item
@@ -94,6 +96,7 @@ __device__ __forceinline__ ListItem tl_item(const ListArgs& a, int item) {
 
 template <typename TO>
 __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_constant__ ListArgs a) {
+    constexpr bool FINE = std::is_same<TO, float>::value;           // weights in two parts
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2], b_q;
     __shared__ float red[2][TL_H], m_run[TL_H];
@@ -315,15 +318,15 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     if (!ok) break;
                     umma::fence_after();
                     const uint64_t ld = umma::desc(base + TL_SL + buf * TL_LBUF, TL_SLAB, 1024, umma::LAYOUT_SW128);
-                    const uint64_t pd = umma::desc(base + TL_SP + buf * TL_PBUF, 16, 1024, umma::LAYOUT_SW128);
+                    const uint64_t pd = umma::desc(base + TL_SP + (FINE ? 0 : buf) * TL_PBUF, 16, 1024, umma::LAYOUT_SW128);
                     if (umma::elect_one()) {
 #pragma unroll
                         for (int m2 = 0; m2 < 2; ++m2)
 #pragma unroll
-                            for (int ks = 0; ks < TL_TILE / 16; ++ks) {
-                                const int mt = 2 * half + m2;
-                                umma::mma_f16(tm + TLT_O + 64 * mt, ld + (uint64_t)((2 * mt * TL_SLAB + ks * 2048) >> 4),
-                                              pd + (uint64_t)((ks * 32) >> 4), id, (t > 0 || ks > 0) ? 1u : 0u);
+                            for (int ks = 0; ks < (FINE ? 2 : 1) * TL_TILE / 16; ++ks) {
+                                const int mt = 2 * half + m2, k4 = ks & 3;       // (P's second part lies one buffer on)
+                                umma::mma_f16(tm + TLT_O + 64 * mt, ld + (uint64_t)((2 * mt * TL_SLAB + k4 * 2048) >> 4),
+                                              pd + (uint64_t)(((ks >> 2) * TL_PBUF + k4 * 32) >> 4), id, (t > 0 || ks > 0) ? 1u : 0u);
                             }
                         umma::commit(sa(&b_lfree[buf]));
                         umma::commit(sa(&b_odone[buf]));
@@ -444,9 +447,20 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     uint32_t p2[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) p2[j] = par ? f16x2_bits(rv[j], x[8 + j]) : f16x2_bits(x[j], rv[j]);
-                    uint8_t* P = sm + TL_SP + buf * TL_PBUF;
+                    if (FINE && t > 0) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);
+                    uint8_t* P = sm + TL_SP + (FINE ? 0 : buf) * TL_PBUF;
                     *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
                     *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
+                    if constexpr (FINE) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {        // what the first part leaves
+                            const float2 part = __half22float2(*reinterpret_cast<const __half2*>(&p2[j]));
+                            p2[j] = par ? f16x2_bits(rv[j] - part.x, x[8 + j] - part.y) : f16x2_bits(x[j] - part.x, rv[j] - part.y);
+                        }
+                        P += TL_PBUF;
+                        *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                        *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
+                    }
                     umma::fence_proxy_async();
                     umma::fence_before();
                     __syncwarp();

@@ -27,6 +27,10 @@
 //                 keys' dims it expands itself, over those dims of its own keys that only S needed: slab s of 64 dims
 //                 goes to place s ^ 2, which gives both CTAs the same address for the same keys, as the MMA asks.
 // Rows, running maxima, sums and outputs of a row stay in its CTA: the pair shares nothing but the MMAs.
+//
+// Roundings: entries are exact in fp16, window rows and queries to 2^-25 of a row's own scale; scores, sums and outputs fp32.
+// The weights are fp16 (2^-11 of each) where the output is of 16 bits, and two fp16 parts (2^-22) where it is fp32, which
+// doubles the value MMAs; both parts then take the two P buffers, and P waits for the values of the tile before.
 #include <algorithm>
 #include <type_traits>
 
@@ -131,6 +135,7 @@ __device__ __forceinline__ bool tr_next(const TreeArgs& a, TreeCursor& c, TreeSh
 
 template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tree_attn(const __grid_constant__ TreeArgs a) {
+    constexpr bool FINE = std::is_same<TO, float>::value;           // weights in two parts
     extern __shared__ uint8_t dyn[];
     // in CTA 0, counting warps of both CTAs: dims 0-255 of a tile's keys ready, all of them, the other CTA's keys ready, P
     // written, the queries staged.  In each CTA, arrived on by the MMAs: scores done, values of dims 0-255
@@ -379,15 +384,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     if (!both()) break;
                     umma::fence_after();
                     if (umma::elect_one()) {
-                        const uint64_t pd = umma::desc(base + TR_SP + buf * TR_PBUF, 16, 1024, umma::LAYOUT_SW128);
+                        const uint64_t pd = umma::desc(base + TR_SP + (FINE ? 0 : buf) * TR_PBUF, 16, 1024, umma::LAYOUT_SW128);
                         const uint64_t vd = umma::desc(base + TR_SL + buf * TR_LBUF, TR_SLAB, 1024, umma::LAYOUT_SW128);
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
 #pragma unroll
-                            for (int ks = 0; ks < 8; ++ks)
-                                umma::mma_f16_pair(tm + TRT_O + 128 * n, pd + (uint64_t)(((ks >> 2) * TR_SLAB + (ks & 3) * 32) >> 4),
-                                                   vd + (uint64_t)(((4 * n + 2 * (ks >> 2)) * TR_SLAB + (ks & 3) * 2048) >> 4), id,
+                            for (int ks = 0; ks < (FINE ? 16 : 8); ++ks) {
+                                const int k8 = ks & 7;               // (P's second part lies one buffer on)
+                                umma::mma_f16_pair(tm + TRT_O + 128 * n,
+                                                   pd + (uint64_t)(((ks >> 3) * TR_PBUF + (k8 >> 2) * TR_SLAB + (k8 & 3) * 32) >> 4),
+                                                   vd + (uint64_t)(((4 * n + 2 * (k8 >> 2)) * TR_SLAB + (k8 & 3) * 2048) >> 4), id,
                                                    (t > h.t0 || ks > 0) ? 1u : 0u);
+                            }
                             umma::commit_pair(sa(n == 0 ? &b_ohalf[buf] : &b_odone[buf]));
                         }
                     }
@@ -504,9 +512,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 const bool raise = umma::bar_red_or(1 + (qd & 1), TR_SMT / 2, mx - m > TR_TOP);
                 // (the P buffer is free: these scores' keys were expanded after the values of the tile before in it; and S is
                 // read before P is handed on, without which its buffer is not written again)
+                if (FINE && t > 0) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);
+                uint8_t* Pbuf = sm + TR_SP + (FINE ? 0 : buf) * TR_PBUF;
                 if (raise) {
                     // [4][32] of this half of the rows, where their own P goes afterwards
-                    float* red = reinterpret_cast<float*>(sm + TR_SP + buf * TR_PBUF + 4096 * (qd & 1)) + lane;
+                    float* red = reinterpret_cast<float*>(Pbuf + 4096 * (qd & 1)) + lane;
                     red[32 * (2 * kh + ch)] = mx;
                     umma::bar_named(1 + (qd & 1), TR_SMT / 2);
                     float mt = red[0];
@@ -535,10 +545,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                         if ((see >> i) & 1u) x[i] += (float)(rexp[i] - wexp);
                     }
                 }
-                uint8_t* P = sm + TR_SP + buf * TR_PBUF + kh * TR_SLAB;
+                uint8_t* P = Pbuf + kh * TR_SLAB;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t w[4];
+                    [[maybe_unused]] uint32_t low[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float d0 = ref, d1 = ref;
@@ -546,8 +557,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                         d0 = umma::ex2_ftz(d0), d1 = umma::ex2_ftz(d1);
                         add2_rn(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], d0, d1);
                         w[i] = f16x2_bits(d0, d1);
+                        if constexpr (FINE) {
+                            const float2 part = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                            low[i] = f16x2_bits(d0 - part.x, d1 - part.y);
+                        }
                     }
                     *reinterpret_cast<uint4*>(P + tr_swz(row, 4 * ch + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if constexpr (FINE)
+                        *reinterpret_cast<uint4*>(P + TR_PBUF + tr_swz(row, 4 * ch + c)) = make_uint4(low[0], low[1], low[2], low[3]);
                 }
                 if (!odd) lsum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 umma::fence_proxy_async();
