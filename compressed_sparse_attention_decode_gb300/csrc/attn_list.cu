@@ -48,6 +48,7 @@ constexpr uint32_t TLT_S = 0, TLT_O = 256, TLT_COLS = 512;       // S partial p 
 // weights are 2^(score - m), m set TL_UP below the largest score and raised when one is more than TL_TOP above it: the
 // largest weight lies in [2^7, 2^15], and what fp16 rounds to zero is below 2^-32 of it
 constexpr float TL_UP = 7.0f, TL_TOP = 15.0f;
+constexpr int TL_RUN = 6;
 constexpr int TL_SMS = 152;
 constexpr int TL_WIN = 2;                            // units of an item's window
 static_assert(WINDOW <= TL_WIN * TL_TILE, "the window's rows have a unit per tile");
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2], b_q;
     __shared__ float red[2][TL_H], m_run[TL_H];
-    __shared__ __align__(16) float fac[TL_H];
+    __shared__ __align__(16) float fac[TL_H], held[FINE ? TL_H : 4];     // (held: FINE's factor of what lies in part_o)
     __shared__ int any[4];
     __shared__ uint32_t slot_ok[2][2], tmem_base;
     __shared__ uint8_t wrows[2][WINDOW];                     // the rows of rows16 that a share's node attends to
@@ -326,7 +327,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                             for (int ks = 0; ks < (FINE ? 2 : 1) * TL_TILE / 16; ++ks) {
                                 const int mt = 2 * half + m2, k4 = ks & 3;       // (P's second part lies one buffer on)
                                 umma::mma_f16(tm + TLT_O + 64 * mt, ld + (uint64_t)((2 * mt * TL_SLAB + k4 * 2048) >> 4),
-                                              pd + (uint64_t)(((ks >> 2) * TL_PBUF + k4 * 32) >> 4), id, (t > 0 || ks > 0) ? 1u : 0u);
+                                              pd + (uint64_t)(((ks >> 2) * TL_PBUF + k4 * 32) >> 4), id,
+                                              ((FINE ? t % TL_RUN : t) > 0 || ks > 0) ? 1u : 0u);
                             }
                         umma::commit(sa(&b_lfree[buf]));
                         umma::commit(sa(&b_odone[buf]));
@@ -339,7 +341,10 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                 const int qd = warp & 3, half = warp >> 2;
                 const int h = qd * 16 + (lane >> 2) + 8 * (lane & 1), par = (lane >> 1) & 1;
                 const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
-                if (tid < TL_H) m_run[tid] = -INFINITY;
+                if (tid < TL_H) {
+                    m_run[tid] = -INFINITY;
+                    if constexpr (FINE) held[tid] = 1.0f;
+                }
                 umma::bar_named(1, TL_SMT);
                 // never zero, so that a masked score stays -inf
                 const float mul4 = T > 0 ? fmaxf(fabsf(a.scale_log2e) * pow2f(h < nh ? a.t.q_exps[w.gq * a.n_heads + w.h0 + h] : 0), 0x1p-100f) : 0.0f;
@@ -348,8 +353,44 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                 const int wexp = max(tree_exp(a.t, w.b, a.t.seq[w.b].n_rows, scaled), -100);
                 float lsum = 0.0f;
                 int oexp = 0;                        // O is 2^-oexp of what it stands for
+                // FINE: the sums of the runs before this one lie in the share's slot of part_o, in this order of its own
+                float4* runs = reinterpret_cast<float4*>(a.part_o + (int64_t)(2 * blockIdx.x + (k == 0 ? 0 : 1)) * TL_H * D_LAT) + tid;
+                // the run that ends with tile t - 1 is added to them; the share's last one: they to it, back in TMEM
+                auto add_run = [&](int t, bool last) {
+                    const uint32_t tp = tb + t - 1;
+                    ok = ok && umma::mbar_wait_fast(sa(&b_odone[tp & 1]), (tp >> 1) & 1);
+                    umma::fence_after();
+#pragma unroll 1
+                    for (int g = 0; g < 8; ++g) {
+                        const uint32_t at = lane_base + TLT_O + 64 * (2 * half + (g >> 2)) + 16 * (g & 3);
+                        const float* fh = held + 16 * (g & 3);
+                        float v[16];
+                        float4 y[4] = {};
+                        if (last || t > TL_RUN)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) y[i] = runs[(4 * g + i) * TL_SMT];
+                        umma::tmem_ld16(at, v);
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[4 * i] = fmaf(y[i].x, fh[4 * i], v[4 * i]), v[4 * i + 1] = fmaf(y[i].y, fh[4 * i + 1], v[4 * i + 1]);
+                            v[4 * i + 2] = fmaf(y[i].z, fh[4 * i + 2], v[4 * i + 2]), v[4 * i + 3] = fmaf(y[i].w, fh[4 * i + 3], v[4 * i + 3]);
+                        }
+                        if (last) {
+                            umma::tmem_st16(at, v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                runs[(4 * g + i) * TL_SMT] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        }
+                    }
+                    if (last) umma::tmem_wait_st();
+                    umma::bar_named(1, TL_SMT);              // held is read
+                    if (!last && tid < TL_H) held[tid] = 1.0f;
+                };
                 for (int t = 0; t < T; ++t) {
                     const uint32_t tg = tb + t, buf = tg & 1, ph = (tg >> 1) & 1;
+                    if (FINE && t > 0 && t % TL_RUN == 0) add_run(t, false);
                     float x[16];
                     // what does not need the scores comes first: the loaders' words, the reference
                     ok = ok && umma::mbar_wait_fast(sa(&b_lfull[buf]), ph);
@@ -403,6 +444,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                                     m_run[h] = mn;
                                 }
                                 fac[h] = f;
+                                if constexpr (FINE) held[h] *= f;
                             }
                             const unsigned some = __ballot_sync(0xffffffffu, f != 1.0f);
                             if (lane == 0) any[qd] = some != 0;
@@ -467,6 +509,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     if (lane == 0) umma::mbar_arrive(sa(&b_pfull[buf]));
                 }
                 // ---- the share's end: sums, then O^T as [head][dim]
+                if (FINE && T > TL_RUN) add_run(T, true);
                 lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
                 if (par == 0) red[half][h] = lsum;
                 umma::bar_named(1, TL_SMT);

@@ -63,6 +63,7 @@ constexpr uint32_t TRT_S = 0, TRT_O = 256, TRT_COLS = 512;               // S of
 // weights are 2^(score - m), m set TR_UP below the largest score and raised when one is more than TR_TOP above it: the
 // largest weight lies in [2^7, 2^15], within fp16's range, and what fp16 rounds to zero is below 2^-32 of it
 constexpr float TR_UP = 7.0f, TR_TOP = 15.0f;
+constexpr int TR_RUN = 2;
 constexpr int TR_PAIRS = 76;                         // pairs of CTAs at most: one CTA per SM
 constexpr int TR_OVER = 1;                           // units of an item beside its tiles: its queries and its epilogue
 
@@ -394,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                                 umma::mma_f16_pair(tm + TRT_O + 128 * n,
                                                    pd + (uint64_t)(((ks >> 3) * TR_PBUF + (k8 >> 2) * TR_SLAB + (k8 & 3) * 32) >> 4),
                                                    vd + (uint64_t)(((4 * n + 2 * (k8 >> 2)) * TR_SLAB + (k8 & 3) * 2048) >> 4), id,
-                                                   (t > h.t0 || ks > 0) ? 1u : 0u);
+                                                   ((FINE ? (t - h.t0) % TR_RUN : t - h.t0) > 0 || ks > 0) ? 1u : 0u);
                             }
                             umma::commit_pair(sa(n == 0 ? &b_ohalf[buf] : &b_odone[buf]));
                         }
@@ -473,6 +474,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 }
                 umma::tmem_wait_st();
             };
+            // FINE: the sums of the runs before this one lie in the share's slot of part_o, in this order of its own, and count
+            // times `held`.  The run that ends with tile t - 1 is added to them; the share's last one: they to it, back in TMEM.
+            float held = 1.0f;
+            const int slot = 2 * pair + (first_share ? 0 : 1);
+            float4* runs = reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * TR_ROWS + 64 * (int)rank) * D_LAT) + tid;
+            auto add_run = [&](int t, bool last) {
+                const uint32_t tp = tb + t - 1;
+                ok = ok && umma::mbar_wait_fast(sa(&b_odone[tp & 1]), (tp >> 1) & 1);
+                umma::fence_after();
+float4 y[2][4] = {};                     // the next 16 columns' under way
+                const bool more = last || t > TR_RUN;
+                auto load = [&](int g, float4* to) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) to[i] = runs[(4 * g + i) * TR_SMT];
+                };
+                auto add = [&](int g, const float4* y) {
+                    const uint32_t at = lane_base + TRT_O + 128 * ch + 16 * g;
+                    float v[16];
+                    umma::tmem_ld16(at, v);
+                    umma::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[4 * i] = fmaf(y[i].x, held, v[4 * i]), v[4 * i + 1] = fmaf(y[i].y, held, v[4 * i + 1]);
+                        v[4 * i + 2] = fmaf(y[i].z, held, v[4 * i + 2]), v[4 * i + 3] = fmaf(y[i].w, held, v[4 * i + 3]);
+                    }
+                    if (last) {
+                        umma::tmem_st16(at, v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            runs[(4 * g + i) * TR_SMT] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                };
+                if (more) load(0, y[0]);
+#pragma unroll 1
+                for (int g = 0; g < 8; g += 2) {
+                    if (more) load(g + 1, y[1]);
+                    add(g, y[0]);
+                    if (more && g + 2 < 8) load(g + 2, y[0]);
+                    add(g + 1, y[1]);
+                }
+                if (last) umma::tmem_wait_st();
+                held = 1.0f;
+            };
             // one tile, of the window or of entries (two copies, so that the entries' carries nothing of the window's)
             auto step = [&](auto is_window, int t) {
                 constexpr bool window = decltype(is_window)::value;
@@ -485,6 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     const int left = vis - ((tile - wt) * TR_TILE + 64 * kh + 32 * ch);
                     if (left < 32) see = left <= 0 ? 0u : (1u << left) - 1u;
                 }
+                if (FINE && !window && t > 0 && t % TR_RUN == 0) add_run(t, false);
                 float x[32];
                 ok = ok && umma::mbar_wait_fast(sa(&b_sfull[buf]), ph);
                 umma::fence_after();
@@ -528,6 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                         m = mt - TR_UP;
                     }
                     lsum *= f;
+                    if (FINE) held *= f;
                     if (t >= 1) {
                         ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);      // O settled
                         umma::fence_after();
@@ -587,6 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             const uint32_t tl = tb + T - 1;
             ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
             umma::fence_after();
+            if (FINE && T > TR_RUN) add_run(T, true);
             float* red = reinterpret_cast<float*>(sm + TR_SP) + row;      // both P buffers are free
             red[64 * (2 * kh + ch)] = lsum;
             umma::bar_named(3, TR_SMT);
@@ -597,7 +645,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             const bool whole = T == h.T;
             const int64_t gr = (int64_t)h.b * n_rows_q + q0 + row;
             const bool there = q0 + row < n_rows_q;
-            const int slot = 2 * pair + (first_share ? 0 : 1);
             const int64_t pr = (int64_t)slot * TR_ROWS + 64 * (int)rank + row;
             const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
             const int d0 = 256 * ch + 128 * kh;
