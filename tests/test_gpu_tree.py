@@ -356,3 +356,39 @@ def test_tree_on_two_streams(csa):
     for w, o in zip(want, outs):
         for out, lse in o:
             assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+
+
+@pytest.mark.parametrize("entries,k", [(8, None), (40, 8), (3000, 2048), (3_000_000, None)])
+def test_tree_fp32_outputs_keep_their_bits(csa, entries, k):
+    """fp32 outputs, whatever the number of keys.  A score is one product of few bits and at most 1 in size, a value is
+    positive, so that what counts is: weights to 2^-22 each, of exponents off by 2^-23 of some 16 at most; runs of 48
+    tensor-core sums (one step of fp32, 2^-23, each); then fp32 sums (2^-24 each) of a row's tiles of 128, of the 76 pairs'
+    or 152 blocks' shares, twice (outputs and weights); a low part of a weight that underflows, 2^-32 of the largest weight."""
+    g = gen(entries)
+    N, H = (2, 3) if k is None else (128, 128)
+    codes = torch.randint(0, 256, (1, entries, 256), generator=g, device="cuda", dtype=torch.uint8) & 0x77
+    codes[..., 0] = torch.randint(0, 256, (1, entries), generator=g, device="cuda", dtype=torch.uint8)    # dims 0 and 1: any sign
+    scales = torch.full((1, entries, 32), 0x30, device="cuda", dtype=torch.uint8)                         # 0.5: values to 3
+    q = torch.zeros((1, N, H, 512), device="cuda", dtype=BF)
+    q[..., 0] = torch.rand((1, N, H), generator=g, device="cuda").to(BF) / 3
+    draft = torch.rand((1, N, 512), generator=g, device="cuda").to(BF)
+    pos = torch.full((1, N), entries + 127, device="cuda", dtype=torch.int64)
+    parent = torch.full((1, N), -1, device="cuda", dtype=torch.int32)
+    idx = None if k is None else torch.randint(0, entries, (1, N, k), generator=g, device="cuda", dtype=torch.int32)
+    x = dict(codes=codes, scales=scales, q=q, pos=pos, parent=parent, draft=draft, swa=None, swa_pos0=None, idx=idx, ratio=1)
+    out, lse = call(csa, x, scale=1.0, out_dtype=F, want_lse=True)
+    keys = (entries if k is None else k) + 1
+    rel = 2.0 ** -22 + 2 * 16 * 2.0 ** -23 + 48 * 2.0 ** -23 + 2 * (keys / 128 / (76 if k is None else 1) + 152 + 32) * U
+    part = 200_000
+    for i in range(N) if k is None else (0, 77, N - 1):
+        qi, d = q[0, i].double(), draft[0, i].double()
+        w = torch.exp(qi @ d)
+        s, o = w.clone(), w[:, None] * d
+        e = torch.arange(entries, device="cuda") if k is None else idx[0, i].long()
+        for at in range(0, e.numel(), part):
+            L = decode(codes[0, e[at:at + part]], scales[0, e[at:at + part]])
+            w = torch.exp(qi @ L.T)
+            s, o = s + w.sum(1), o + w @ L
+        ref = o / s[:, None]
+        within(out[0, i], ref, rel * ref.abs() + keys * 2.0 ** -32 * 3)
+        within(lse[0, i], s.log(), rel + 2.0 ** -22 * (1 + s.log()))
