@@ -14,8 +14,16 @@
 #include "elem.cuh"
 #include "fp4_f16.cuh"
 #include "tree.cuh"
+#include "umma.cuh"
 
 namespace csa2 {
+
+// 16 bf16 channels as floats
+__device__ __forceinline__ void bf16x16_to_f32(const uint4& c, const uint4& d, float* x) {
+    const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = bf16_bits_to_f32((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xffffu));
+}
 
 struct AppendArgs {
     uint8_t *lat_codes, *lat_scales, *ik_codes, *ik_scales;
@@ -59,11 +67,18 @@ struct AppendSeq {
     __device__ __forceinline__ void entry(const AppendArgs& a, int b, int j, uint32_t& q0, uint32_t& q1, uint32_t& sb) const {
         const int at = (threadIdx.x & 31) * 16;
         float x[16];
-        row16((j < 0 ? a.prev + (int64_t)b * D_LAT : row(j)) + at, x);
+        // (plain loads: the carried row may be written by this kernel)
+        const uint4* src = reinterpret_cast<const uint4*>((j < 0 ? a.prev + (int64_t)b * D_LAT : row(j)) + at);
+        const uint4 c0 = src[0], c1 = src[1];
         if (a.ratio == 2) {
+            src = reinterpret_cast<const uint4*>(row(j + 1) + at);
+            const uint4 d0 = src[0], d1 = src[1];
             float y[16];
-            row16(row(j + 1) + at, y);
+            bf16x16_to_f32(c0, c1, x);
+            bf16x16_to_f32(d0, d1, y);
             merge16(x, y, a.w0 + at, a.w1 + at);
+        } else {
+            bf16x16_to_f32(c0, c1, x);
         }
         quant_group16(x, q0, q1, sb);
     }
@@ -153,190 +168,344 @@ __global__ void __launch_bounds__(256) k_cache_append(const __grid_constant__ Ap
     }
 }
 
-// Many entries with their indexer keys.  A key is sum_g G_g sL_g sW_g over 32 groups; G, sixteen products of E2M1 values, has 12
-// bits in quarters, the scales 4 each, so that a group's term has 20 bits and comes exactly out of one m16n8k16 product of the
-// scaled values (fp16 holds them exactly).  The sum has to be exact too, over 53 bits.  It is held in three fp32 sums: the
-// first two start at 1.5 x 2^33 and 1.5 x 2^15 and are never more than 2^32 and 2^14 away from there, so that their last bits
-// stay 2^10 and 2^-8; adding a term to the first leaves a remainder (exact, at most 2^9), which is added to the second; its
-// remainder (at most 2^-9, a multiple of 2^-20) goes into the third.  Seven additions a term, no 64-bit arithmetic.  The
-// products bound the kernel: an SM's quarter takes an m16n8k16 every 32 clocks or so, and the additions some of what is left
-// (4 x 4,096 entries of 128 keys: 48 us; int8 products and 64-bit sums took 105).
-// W is expanded to shared memory once a block, in the products' order.  Sixteen warps quantise a tile of 32 entries (two each,
-// whose rows they have asked for a tile ahead) while the other sixteen multiply the tile before; one of those has 16 entries
-// and a key group of 16 dims, which it quantises from its sums (all warps doing one after the other: 60 us).
-constexpr int CM_TILE = 32, CM_MAKERS = 16, CM_THREADS = 1024;
-constexpr int CM_A = CM_TILE * 1024, CM_RAW = CM_MAKERS * 2048;      // bytes of a tile's entries (fp16), of the rows under way
+// Many entries with their indexer keys.  A key is the exact sum of W . L over 512 dims, rounded once and quantised: what is
+// kept of it is a scale byte of 16 dims and four bits each.  So the tensor cores sum in fp32, which errs by no more than
+// CM_ERR |W_d| |L| (no product and no partial sum is larger than the two norms' product; 17 terms a step of 16 dims, each cut
+// at 2^-24 of that or better; 32 steps), and a value whose scale and code are the same at both ends of that interval has
+// them; the few others (2 to 3 in a thousand of random rows) are summed again exactly: a term of 16 dims, sixteen products of
+// E2M1 values times two scales, has 20 bits and comes exactly out of fp32 additions, and the 32 terms go into 64 bits.
+// W is expanded to shared memory once a block, 128 dims x 512 in fp16 (with 64 dims the other half is zeros).  A tile is 16
+// entries: sixteen warps make one each (its rows are asked for a tile ahead, and the entry kept as it is stored, in fp16), two
+// warps issue half of its sixteen-dim steps each (one thread issues a product per 65 to 85 clocks, whatever its size), and two
+// sets of four warps take the sums of every second tile: TMEM lane = key dim, turned in shared memory so that a thread
+// has an entry's group of 16 dims.
+constexpr int CM_TILE = 16, CM_MAKERS = 16, CM_MMA = 16, CM_OUT = 18, CM_THREADS = 26 * 32;
+constexpr int CM_BUFS = 4;
+constexpr uint32_t CM_W = 128 * 1024, CM_A = CM_TILE * 1024, CM_TURN = CM_TILE * 36 * 4;     // W, a tile, a warp's sums
+constexpr uint32_t CM_DYN = CM_W + CM_BUFS * CM_A + 8 * CM_TURN + 4096 + 1024;                 // + w0 and w1, alignment
+constexpr float CM_ERR = 0x1.4p-18f;
 
-__device__ __forceinline__ void mma16816(float* d, const uint32_t* x, uint32_t y0, uint32_t y1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y0), "r"(y1), "f"(0.0f));
-}
-// two codes of a byte (low nibble first) times the scale
-__device__ __forceinline__ uint32_t pair_scaled(uint32_t byte, __half2 s) {
-    uint32_t r;
-    asm("{\n .reg .b8 x, y, z, w;\n mov.b32 {x, y, z, w}, %1;\n cvt.rn.f16x2.e2m1x2 %0, x;\n}" : "=r"(r) : "r"(byte));
-    const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&r), s);
-    return *reinterpret_cast<const uint32_t*>(&v);
+// sixteen fp16 values of a row of a 128-byte swizzled slab (rows of 64)
+__device__ __forceinline__ void cm_row16(const uint8_t* slab, int row, int g, uint4* v) {
+    const uint8_t* at = slab + row * 128;
+    v[0] = *reinterpret_cast<const uint4*>(at + (((2 * (g & 3)) ^ (row & 7)) << 4));
+    v[1] = *reinterpret_cast<const uint4*>(at + (((2 * (g & 3) + 1) ^ (row & 7)) << 4));
 }
 
 template <int DI>
 __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __grid_constant__ AppendArgs a, int tiles, int batch) {
-    extern __shared__ __align__(16) uint8_t A[];             // two tiles: entries x 512 fp16, 16-byte pieces at p ^ (entry & 7)
-    uint2* W = reinterpret_cast<uint2*>(A + 2 * CM_A + CM_RAW);      // [DI / 8][32 groups][32 lanes] the products' B
-    __shared__ int64_t entry_at[2][CM_TILE];                 // -1: not there
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) unsigned long long b_w, b_full[CM_BUFS], b_free[CM_BUFS], b_sum[2], b_taken[2];
+    __shared__ int64_t entry_at[CM_BUFS][CM_TILE];           // -1: not there
+    __shared__ float norm_l[CM_BUFS][CM_TILE], norm_w[128];
+    __shared__ uint32_t tmem_base;
+    const uint32_t raw0 = umma::smem_u32(dyn), base = (raw0 + 1023u) & ~1023u;
+    uint8_t* W = dyn + (base - raw0);                        // 8 slabs of 128 rows x 64 dims
+    uint8_t* A = W + CM_W;                                   // buffers of 8 slabs of 16 rows x 64 dims
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, all = tiles * batch;
+    auto sa = [&](const void* x) { return umma::smem_u32(x); };
+    if (tid == 0) {
+        umma::mbar_init(sa(&b_w), CM_THREADS / 32 - CM_MAKERS);
+        for (int i = 0; i < CM_BUFS; ++i) umma::mbar_init(sa(&b_full[i]), CM_MAKERS), umma::mbar_init(sa(&b_free[i]), 4);
+        for (int i = 0; i < 2; ++i) umma::mbar_init(sa(&b_sum[i]), 2), umma::mbar_init(sa(&b_taken[i]), 4);
+        umma::fence_mbar_init();
+    }
+    if (warp == CM_MMA) umma::tmem_alloc(sa(&tmem_base), 256);
+    float4* merge = reinterpret_cast<float4*>(A + CM_BUFS * CM_A + 8 * CM_TURN);     // [w0, w1][4][32 lanes] four of a lane's 16 dims
     pdl_wait();
     pdl_launch_next();
-    // B of a group: rows 2 (lane % 4) + {0, 1} and 8 further, column lane / 4: bytes lane % 4 and 4 + lane % 4 of the dim's eight
-#pragma unroll 4
-    for (int u = warp; u < DI / 8 * 32; u += CM_THREADS / 32) {
-        const int64_t d = (u >> 5) * 8 + (lane >> 2);
-        const int g = u & 31;
-        const uint2 c = reinterpret_cast<const uint2*>(a.wik_codes + d * (D_LAT / 2))[g];
-        // (the scale as the exact integers take it)
-        const __half2 s = __float2half2_rn((float)cw_e4m3_x512(a.wik_scales[d * (D_LAT / 16) + g]) * 0x1p-9f);
-        W[u * 32 + lane] = make_uint2(pair_scaled(c.x >> (8 * (lane & 3)), s), pair_scaled(c.y >> (8 * (lane & 3)), s));
-    }
+    if (a.ratio == 2 && tid < 256)
+        merge[(tid & 128) + ((tid & 3) << 5) + ((tid & 127) >> 2)] = reinterpret_cast<const float4*>(tid < 128 ? a.w0 : a.w1)[tid & 127];
+    umma::fence_before();
     __syncthreads();
-    // named barriers: 1 + buf the tile in buffer buf is made, 3 + buf it is read
+    umma::fence_after();
+    const uint32_t tmem = tmem_base;
+    bool ok = true;
     if (warp < CM_MAKERS) {
-        // ================= entries: warp w makes entries w and 16 + w of a tile, lane g its channel group g
-        uint8_t* raw = A + 2 * CM_A + warp * 2048;
-        int64_t entry = -1;
-        int length = 0;
-        auto fetch = [&](int tile, int r) {                  // entry r's rows, if it is there
-            const int b = tile / tiles, i = (tile - b * tiles) * CM_TILE + r;
+        // ================= entries: a warp makes one of a tile, lane g its channel group g
+        // Two tiles ahead where its rows are, and a request for them to L2; one tile ahead the rows.
+        struct Place {
+            int64_t entry;                                   // -1: not there
+            const uint4 *x, *y;
+            int length;
+        };
+        int fb = (int)blockIdx.x / tiles, ft = (int)blockIdx.x - fb * tiles;         // the tile that is found next
+        auto find = [&]() {
+            Place p{-1, nullptr, nullptr, 0};
+            if (fb >= batch) return p;
+            const int b = fb, i = ft * CM_TILE + warp;
+            for (ft += gridDim.x; ft >= tiles && fb < batch; ft -= tiles) ++fb;
             const AppendSeq s(a, b);
             const int j = i * a.ratio - s.odd;
-            length = s.length(a, i == 0 && a.prev_out != nullptr ? a.n_path : min(a.n_path, j + a.ratio));
+            p.length = s.length(a, i == 0 && a.prev_out != nullptr ? a.n_path : min(a.n_path, j + a.ratio));
             const int64_t e = s.e0 + i;
-            const bool there = i < a.n_ent && j + a.ratio <= length && e >= 0 && e < a.capacity;
-            entry = there ? (int64_t)b * a.capacity + e : -1;
-            if (there)
-                for (int k = 0; k < a.ratio; ++k) {
-                    const uint16_t* src = j + k < 0 ? a.prev + (int64_t)b * D_LAT : s.row(j + k);
-                    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(raw + k * 1024);
-                    copy16(dst + lane * 16, src + lane * 8, true);
-                    copy16(dst + (32 + lane) * 16, src + (32 + lane) * 8, true);
-                }
+            if (i < a.n_ent && j + a.ratio <= p.length && e >= 0 && e < a.capacity) {
+                p.entry = (int64_t)b * a.capacity + e;
+                p.x = reinterpret_cast<const uint4*>(j < 0 ? a.prev + (int64_t)b * D_LAT : s.row(j));
+                p.y = a.ratio == 2 ? reinterpret_cast<const uint4*>(s.row(j + 1)) : p.x;
+                if (lane < 16) umma::prefetch_l2((lane & 8 ? p.y : p.x) + 8 * (lane & 7));      // (lines of 128 bytes)
+            }
+            return p;
         };
-        if ((int)blockIdx.x < all) fetch(blockIdx.x, warp);
+        uint4 raw[4];
+        auto fetch = [&](const Place& p) {
+            if (p.entry < 0) return;
+            raw[0] = p.x[2 * lane], raw[1] = p.x[2 * lane + 1];
+            if (a.ratio == 2) raw[2] = p.y[2 * lane], raw[3] = p.y[2 * lane + 1];
+        };
+        Place now = find();
+        fetch(now);
+        Place next = find();
         int n = 0;
         for (int tile = blockIdx.x; tile < all; tile += gridDim.x, ++n) {
-            const int buf = n & 1;
-            if (n >= 2) asm volatile("bar.sync %0, %1;" ::"r"(3 + buf), "r"(CM_THREADS) : "memory");
-#pragma unroll 1
-            for (int r = warp; r < CM_TILE; r += CM_MAKERS) {
-                copy16_wait();
-                __syncwarp();
-                const int b = tile / tiles;
-                if (r == 0 && tile == b * tiles && a.prev_out != nullptr) carry_on(a, AppendSeq(a, b), b, length);     // (it is here)
-                const int64_t at = entry;
-                float x[16], y[16];
-                auto take = [&](int k, float* v) {           // 32 bytes of a row
-                    const uint4* p = reinterpret_cast<const uint4*>(raw + k * 1024) + 2 * lane;
-                    const uint4 c = p[0], d = p[1];
-                    const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+            const int buf = n % CM_BUFS;
+            const int64_t at = now.entry;
+            float x[16];
+            if (at >= 0) {
+                bf16x16_to_f32(raw[0], raw[1], x);
+                if (a.ratio == 2) {
+                    float y[16];
+                    bf16x16_to_f32(raw[2], raw[3], y);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = bf16_bits_to_f32((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xffffu));
-                };
-                if (at >= 0) {
-                    take(0, x);
-                    if (a.ratio == 2) take(1, y);
+                    for (int k = 0; k < 4; ++k) {            // (merge16, of weights in shared memory)
+                        const float4 f0 = merge[k * 32 + lane], f1 = merge[128 + k * 32 + lane];
+                        const float w0[4] = {f0.x, f0.y, f0.z, f0.w}, w1[4] = {f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[4 * k + i] = __fmaf_rn(w1[i], y[4 * k + i], __fmul_rn(w0[i], x[4 * k + i]));
+                    }
                 }
-                __syncwarp();
-                if (r + CM_MAKERS < CM_TILE)
-                    fetch(tile, r + CM_MAKERS);
-                else if (tile + (int)gridDim.x < all)
-                    fetch(tile + gridDim.x, warp);
-                uint32_t q0 = 0u, q1 = 0u, sb = 0u;
-                if (at >= 0) {
-                    if (a.ratio == 2) merge16(x, y, a.w0 + lane * 16, a.w1 + lane * 16);
-                    quant_group16(x, q0, q1, sb);
-                    store_latent(a, at, q0, q1, sb);
-                }
-                const __half2 sc = __half2half2(__low2half(e4m3x2_to_f16x2(sb)));
-                uint8_t* row = A + buf * CM_A + r * 1024;
-                *reinterpret_cast<uint4*>(row + (((2 * lane) ^ (r & 7)) << 4)) = e2m1x8_scaled(q0, sc);
-                *reinterpret_cast<uint4*>(row + (((2 * lane + 1) ^ (r & 7)) << 4)) = e2m1x8_scaled(q1, sc);
-                if (lane == 0) entry_at[buf][r] = at;
             }
-            __threadfence_block();
-            asm volatile("bar.arrive %0, %1;" ::"r"(1 + buf), "r"(CM_THREADS) : "memory");
+            __syncwarp();
+            if (warp == 0 && tile % tiles == 0 && a.prev_out != nullptr) {   // (its rows are here)
+                const int b = tile / tiles;
+                carry_on(a, AppendSeq(a, b), b, now.length);
+            }
+            now = next;
+            fetch(now);
+            next = find();
+            uint32_t q0 = 0u, q1 = 0u, sb = 0u;
+            if (at >= 0) {
+                quant_group16(x, q0, q1, sb);
+                store_latent(a, at, q0, q1, sb);
+            }
+            const __half2 sc = __half2half2(__low2half(e4m3x2_to_f16x2(sb)));
+            __half2 h[8], sq = __half2half2(__ushort_as_half(0));
+            e2m1x8_to_f16x8(q0, h), e2m1x8_to_f16x8(q1, h + 4);
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sq = __hfma2(h[i], h[i], sq);                // (quarters up to 288: exact)
+                const __half2 v = __hmul2(h[i], sc);
+                o[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            const float s = __low2float(sc);
+            float norm = (__low2float(sq) + __high2float(sq)) * s * s;
+#pragma unroll
+            for (int k = 16; k; k >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, k);
+            if (n >= CM_BUFS) ok = ok && umma::mbar_wait_fast(sa(&b_free[buf]), ((n / CM_BUFS) - 1) & 1);
+            uint8_t* row = A + buf * CM_A + (lane >> 2) * (CM_TILE * 128) + warp * 128;
+            *reinterpret_cast<uint4*>(row + (((2 * (lane & 3)) ^ (warp & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(row + (((2 * (lane & 3) + 1) ^ (warp & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            if (lane == 0) entry_at[buf][warp] = at, norm_l[buf][warp] = sqrtf(norm);
+            umma::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(sa(&b_full[buf]));
         }
     } else {
-        // ================= products: warp w has entries 16 (w % 2) .. + 15 and key group w / 2 (with 64 dims half of the warps
-        // have none)
-        const int w = warp - CM_MAKERS, m = w & 1, group = w >> 1;
-        const bool busy = group < DI / 16;
-        const uint32_t abase = (uint32_t)__cvta_generic_to_shared(A);
-        const uint2* B = W + group * 2048 + lane;
-        int n = 0;
-        for (int tile = blockIdx.x; tile < all; tile += gridDim.x, ++n) {
-            const int buf = n & 1;
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + buf), "r"(CM_THREADS) : "memory");
-            float key[2][4];                                 // rows lane / 4 and 8 further, dims 8 h + 2 (lane % 4) + {0, 1}
-            int64_t at[2] = {-1, -1};
-            if (busy) {
-                const int r = m * 16 + (lane & 15);
-                at[0] = entry_at[buf][m * 16 + (lane >> 2)], at[1] = entry_at[buf][m * 16 + 8 + (lane >> 2)];
-                float s1[2][4], s2[2][4], s3[2][4];
+        // ================= W: a warp makes a row, lane g its dims 16 g .. + 15
+        constexpr int N = (128 + CM_THREADS / 32 - CM_MAKERS - 1) / (CM_THREADS / 32 - CM_MAKERS);
+        uint2 wc[N];
+        float ws[N];
 #pragma unroll
-                for (int v = 0; v < 8; ++v) s1[v >> 2][v & 3] = 0x1.8p33f, s2[v >> 2][v & 3] = 0x1.8p15f, s3[v >> 2][v & 3] = 0.0f;
-#pragma unroll 2
-                for (int g = 0; g < 32; ++g) {
-                    uint32_t x[4];
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                 : "r"(abase + buf * CM_A + r * 1024 + (((2 * g + (lane >> 4)) ^ (r & 7)) << 4)));
+        for (int r = 0; r < N; ++r) {
+            const int d = warp - CM_MAKERS + r * (CM_THREADS / 32 - CM_MAKERS);
+            wc[r] = make_uint2(0u, 0u), ws[r] = 0.0f;
+            if (d < DI) {
+                wc[r] = reinterpret_cast<const uint2*>(a.wik_codes + d * (D_LAT / 2))[lane];
+                ws[r] = (float)cw_e4m3_x512(a.wik_scales[d * (D_LAT / 16) + lane]) * 0x1p-9f;    // (as the exact integers take it)
+            }
+        }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint2 y = B[h * 1024 + g * 32];
-                        float t[4];
-                        mma16816(t, x, y.x, y.y);
+        for (int r = 0; r < N; ++r) {
+            const int d = warp - CM_MAKERS + r * (CM_THREADS / 32 - CM_MAKERS);
+            if (d >= 128) break;
+            const uint2 c = wc[r];
+            const float sw = ws[r];
+            const __half2 sc = __float2half2_rn(sw);
+            __half2 h[8], sq = __half2half2(__ushort_as_half(0));
+            e2m1x8_to_f16x8(c.x, h), e2m1x8_to_f16x8(c.y, h + 4);
+            uint32_t o[8];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const float n1 = __fadd_rn(s1[h][v], t[v]), r1 = __fsub_rn(t[v], __fsub_rn(n1, s1[h][v]));
-                            const float n2 = __fadd_rn(s2[h][v], r1), r2 = __fsub_rn(r1, __fsub_rn(n2, s2[h][v]));
-                            s1[h][v] = n1, s2[h][v] = n2, s3[h][v] = __fadd_rn(s3[h][v], r2);
+            for (int i = 0; i < 8; ++i) {
+                sq = __hfma2(h[i], h[i], sq);
+                const __half2 v = __hmul2(h[i], sc);
+                o[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            float norm = (__low2float(sq) + __high2float(sq)) * sw * sw;
+#pragma unroll
+            for (int k = 16; k; k >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, k);
+            uint8_t* row = W + (lane >> 2) * (128 * 128) + d * 128;
+            *reinterpret_cast<uint4*>(row + (((2 * (lane & 3)) ^ (d & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(row + (((2 * (lane & 3) + 1) ^ (d & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            if (lane == 0) norm_w[d] = sqrtf(norm);
+        }
+        umma::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(sa(&b_w));
+        ok = umma::mbar_wait_fast(sa(&b_w), 0);
+        if (warp < CM_OUT) {
+            // ================= sums: dims 256 half .. + 255 of every tile
+            const int half = warp - CM_MMA;
+            const uint32_t id = umma::idesc_f16(128, CM_TILE, 0, 0);
+            const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+            const uint64_t wd = umma::desc(base, 16, 1024, umma::LAYOUT_SW128);
+            int n = 0;
+            for (int tile = blockIdx.x; tile < all; tile += gridDim.x, ++n) {
+                const int buf = n % CM_BUFS, set = n & 1;
+                ok = ok && umma::mbar_wait_fast(sa(&b_full[buf]), (n / CM_BUFS) & 1);
+                if (n >= 2) ok = ok && umma::mbar_wait_fast(sa(&b_taken[set]), ((n >> 1) - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                umma::fence_after();
+                const uint64_t ad = umma::desc(base + CM_W + buf * CM_A, 16, 1024, umma::LAYOUT_SW128);
+                if (umma::elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 16; ++kk) {
+                        const int ks = 16 * half + kk;
+                        umma::mma_f16(tm + 128 * set + 16 * (ks >> 2), wd + (uint64_t)(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                                      ad + (uint64_t)(((ks >> 2) * (CM_TILE * 128) + (ks & 3) * 32) >> 4), id, (kk & 3) > 0);
+                    }
+                    umma::commit(sa(&b_sum[set]));
+                }
+                __syncwarp();
+            }
+        } else {
+            // ================= keys: set s has tiles s, s + 2, ..; warp q of it (TMEM lanes 32 q .. + 31) key groups 2 q and
+            // 2 q + 1, a thread an entry's group
+            const int qd = warp & 3, set = (warp - CM_OUT) >> 2, e = lane & 15, group = 2 * qd + (lane >> 4);
+            float* turn = reinterpret_cast<float*>(A + CM_BUFS * CM_A + (warp - CM_OUT) * CM_TURN);
+            float nw = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) nw = fmaxf(nw, norm_w[group * 16 + i]);
+            int n = 0;
+            for (int tile = blockIdx.x; tile < all; tile += gridDim.x, ++n) {
+                if ((n & 1) != set) continue;
+                const int buf = n % CM_BUFS;
+                ok = ok && umma::mbar_wait_fast(sa(&b_full[buf]), (n / CM_BUFS) & 1);
+                ok = ok && umma::mbar_wait_fast(sa(&b_sum[set]), (n >> 1) & 1);
+                umma::fence_after();
+                {
+                    const uint32_t at = tmem + ((uint32_t)(qd * 32) << 16) + 128 * set;
+                    float v[16], w[16], x[16];
+                    umma::tmem_ld16(at, v);
+#pragma unroll
+                    for (int k = 1; k < 7; k += 2) {
+                        umma::tmem_ld16(at + 16 * k, w);
+                        umma::tmem_ld16(at + 16 * (k + 1), x);
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] += w[i] + x[i];
+                    }
+                    umma::tmem_ld16(at + 112, w);
+                    umma::tmem_wait_ld();
+                    umma::fence_before();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(sa(&b_taken[set]));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) turn[i * 36 + lane] = v[i] + w[i];
+                }
+                __syncwarp();
+                if (qd < DI / 32) {
+                    float v[16];
+                    auto load = [&]() {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(turn + e * 36 + (group & 1) * 16 + i);
+                            v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+                        }
+                    };
+                    load();
+                    const int64_t at = entry_at[buf][e];
+                    const float err = CM_ERR * nw * norm_l[buf][e];
+                    // the values that `open` names, summed again exactly, one after the other: lane g the term of latent group g
+                    auto settle = [&](uint32_t open) {
+                        const bool mine = open != 0u;
+                        for (unsigned who = __ballot_sync(0xffffffffu, mine); who;) {
+                            const int src = __ffs(who) - 1;
+                            const uint32_t left = __shfl_sync(0xffffffffu, open, src);
+                            const int i = __ffs(left) - 1, es = src & 15, d = (2 * qd + (src >> 4)) * 16 + i;
+                            uint4 l[2], w[2];
+                            cm_row16(A + buf * CM_A + (lane >> 2) * (CM_TILE * 128), es, lane, l);
+                            cm_row16(W + (lane >> 2) * (128 * 128), d, lane, w);
+                            const __half2 *lh = reinterpret_cast<const __half2*>(l), *wh = reinterpret_cast<const __half2*>(w);
+                            float t = 0.0f;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float2 x = __half22float2(lh[k]), y = __half22float2(wh[k]);
+                                t = fmaf(x.y, y.y, fmaf(x.x, y.x, t));
+                            }
+                            long long sum = __float2ll_rn(t * 0x1p20f);
+#pragma unroll
+                            for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+                            if (lane == 0) turn[es * 36 + (src >> 4) * 16 + i] = __ll2float_rn(sum) * 0x1p-20f;
+                            if (lane == src) open &= open - 1u;
+                            if ((left & (left - 1u)) == 0u) who &= who - 1u;
+                        }
+                        __syncwarp();
+                        if (mine) load();
+                    };
+                    auto largest = [&]() {
+                        float top = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(v[i]));
+                        return top;
+                    };
+                    const bool there = at >= 0 && ok;
+                    float top = largest();
+                    uint32_t sb = f32_to_e4m3_satfinite(__fdiv_rn(fmaxf(top - err, 0.0f), 6.0f)), done = 0u;
+                    if (there && sb != f32_to_e4m3_satfinite(__fdiv_rn(top + err, 6.0f)))
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) done |= fabsf(v[i]) >= top - 2.0f * err ? 1u << i : 0u;
+                    if (__any_sync(0xffffffffu, done != 0u)) {       // the scale is open: it takes the largest ones
+                        settle(done);
+                        if (done != 0u) sb = f32_to_e4m3_satfinite(__fdiv_rn(largest(), 6.0f));
+                    }
+                    uint32_t q0 = 0u, q1 = 0u, open = 0u;
+                    if (sb != 0u) {
+                        const float s = e4m3_to_f32(sb);
+                        float lo[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) lo[i] = v[i] - err, v[i] += err;
+                        q0 = e2m1_codes8(lo, s), q1 = e2m1_codes8(lo + 8, s);
+                        const uint32_t d0 = q0 ^ e2m1_codes8(v, s), d1 = q1 ^ e2m1_codes8(v + 8, s);
+                        if (there && (d0 | d1) != 0u)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                open |= (((d0 >> (4 * i)) & 15u) ? 1u << i : 0u) | (((d1 >> (4 * i)) & 15u) ? 256u << i : 0u);
+                    }
+                    if (__any_sync(0xffffffffu, open != 0u)) {
+                        settle(open);
+                        if (open != 0u) {                    // (the other codes are those of their exact sums as they are)
+                            const float s = e4m3_to_f32(sb);
+                            q0 = e2m1_codes8(v, s), q1 = e2m1_codes8(v + 8, s);
                         }
                     }
-                }
-#pragma unroll
-                for (int v = 0; v < 8; ++v) {                // the three as one number of 2^-20: exact, then one rounding
-                    const int h = v >> 2, c = v & 3;
-                    const long long sum = ((long long)__float2int_rn(__fsub_rn(s1[h][c], 0x1.8p33f) * 0x1p-10f) << 30) +
-                                          ((long long)__float2int_rn(__fsub_rn(s2[h][c], 0x1.8p15f) * 0x1p8f) << 12) +
-                                          __float2int_rn(s3[h][c] * 0x1p20f);
-                    key[h][c] = __ll2float_rn(sum) * 0x1p-20f;
-                }
-            }
-            if (tile + 2 * (int)gridDim.x < all) {
-                __threadfence_block();
-                asm volatile("bar.arrive %0, %1;" ::"r"(3 + buf), "r"(CM_THREADS) : "memory");
-            }
-            // a row's group lies in four lanes, four values each
-            if (busy)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float v[4] = {key[0][2 * i], key[0][2 * i + 1], key[1][2 * i], key[1][2 * i + 1]};
-                    float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const uint32_t sb = f32_to_e4m3_satfinite(__fdiv_rn(top, 6.0f));
-                    const float s = e4m3_to_f32(sb);
-                    uint32_t c[2] = {0u, 0u};
-                    if (s > 0.0f)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) c[h] = e2m1_code(v[2 * h], s) | (e2m1_code(v[2 * h + 1], s) << 4);
-                    if (at[i] >= 0) {
-                        uint8_t* codes = a.ik_codes + at[i] * (DI / 2) + group * 8 + (lane & 3);
-                        codes[0] = (uint8_t)c[0], codes[4] = (uint8_t)c[1];
-                        if ((lane & 3) == 0) a.ik_scales[at[i] * (DI / 16) + group] = (uint8_t)sb;
+                    if (!ok) q0 = q1 = 0u, sb = 0x7fu;
+                    if (at >= 0) {
+                        *reinterpret_cast<uint2*>(a.ik_codes + at * (DI / 2) + group * 8) = make_uint2(q0, q1);
+                        a.ik_scales[at * (DI / 16) + group] = (uint8_t)sb;
                     }
                 }
+                __syncwarp();                                // (sums and entries are read)
+                if (lane == 0) umma::mbar_arrive(sa(&b_free[buf]));
+            }
         }
+    }
+    umma::fence_before();
+    __syncthreads();
+    if (warp == CM_MMA) {
+        umma::fence_after();
+        umma::tmem_dealloc(tmem, 256);
     }
 }
 
@@ -410,10 +579,9 @@ cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n
         const int tiles = (n_ent - 1) / CM_TILE + 1;
         const unsigned grid = (unsigned)std::min<int64_t>((int64_t)tiles * c.batch, 152);
         const auto kern = di == 128 ? k_cache_append_many<128> : k_cache_append_many<64>;
-        const int smem = 2 * CM_A + CM_RAW + di * 1024;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CM_DYN);
         if (e != cudaSuccess) return e;
-        launch_k(kern, dim3(grid), CM_THREADS, (size_t)smem, st, a, tiles, (int)c.batch);
+        launch_k(kern, dim3(grid), CM_THREADS, CM_DYN, st, a, tiles, (int)c.batch);
     } else if (di > 0) {
         launch_k(di == 128 ? k_cache_append<128> : k_cache_append<64>, dim3((unsigned)std::max(1, n_ent), c.batch), di * 2, 0, st, a);
     } else {
