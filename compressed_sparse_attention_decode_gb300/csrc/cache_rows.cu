@@ -52,13 +52,20 @@ struct AppendSeq {
         path = a.path ? a.path + (int64_t)b * a.n_path : nullptr;
         rows = a.rows + (int64_t)b * a.n_rows * D_LAT;
     }
-    // how many of the path's first `upto` steps are rows that exist, a whole warp together
-    __device__ __forceinline__ int length(const AppendArgs& a, int upto) const {
+    // how many of the path's first `upto` steps are rows that exist, its first `from` being known to be; a whole warp together
+    __device__ __forceinline__ int length(const AppendArgs& a, int upto, int from = 0) const {
         if (path == nullptr) return upto;
         const int lane = threadIdx.x & 31;
-        for (int j0 = 0; j0 < upto; j0 += 32) {
-            const unsigned there = __ballot_sync(0xffffffffu, j0 + lane < upto && (unsigned)path[j0 + lane] < (unsigned)a.n_rows);
-            if (there != 0xffffffffu) return min(upto, j0 + __ffs(~there) - 1);
+        for (int j0 = from & ~31; j0 < upto; j0 += 128) {
+            unsigned there[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {                    // (four loads under way: 8,192 steps are 64 times their latency)
+                const int j = j0 + 32 * k + lane;
+                there[k] = __ballot_sync(0xffffffffu, j < upto && (unsigned)path[j] < (unsigned)a.n_rows);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (there[k] != 0xffffffffu) return min(upto, j0 + 32 * k + __ffs(~there[k]) - 1);
         }
         return upto;
     }
@@ -230,6 +237,8 @@ __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __gri
             int length;
         };
         int fb = (int)blockIdx.x / tiles, ft = (int)blockIdx.x - fb * tiles;         // the tile that is found next
+        int seen_b = -1, seen = 0;
+        bool ends = false;
         auto find = [&]() {
             Place p{-1, nullptr, nullptr, 0};
             if (fb >= batch) return p;
@@ -237,7 +246,11 @@ __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __gri
             for (ft += gridDim.x; ft >= tiles && fb < batch; ft -= tiles) ++fb;
             const AppendSeq s(a, b);
             const int j = i * a.ratio - s.odd;
-            p.length = s.length(a, i == 0 && a.prev_out != nullptr ? a.n_path : min(a.n_path, j + a.ratio));
+            // (of a path that it goes along the warp looks at each step once)
+            const int upto = i == 0 && a.prev_out != nullptr ? a.n_path : min(a.n_path, j + a.ratio);
+            if (b != seen_b) seen_b = b, seen = 0, ends = false;
+            if (!ends && seen < upto) seen = s.length(a, upto, seen), ends = seen < upto;
+            p.length = min(seen, upto);
             const int64_t e = s.e0 + i;
             if (i < a.n_ent && j + a.ratio <= p.length && e >= 0 && e < a.capacity) {
                 p.entry = (int64_t)b * a.capacity + e;

@@ -255,3 +255,46 @@ def test_append_and_read_in_a_graph(csa):
             assert torch.equal(a, b)
         pos += n
         rows.copy_(randn((B, n, 512), g, BF))
+
+
+@pytest.mark.parametrize("d_idx", [64, 128])
+@pytest.mark.parametrize("ratio", [1, 2])
+def test_append_many_with_keys_along_paths(csa, ratio, d_idx):
+    """as many entries as go through the tensor cores, of paths that end at once, in the middle, or not at all"""
+    g = gen(12)
+    path = torch.randint(0, 90, (4, 1600), generator=g, device="cuda", dtype=torch.int32)
+    path[0, 1599] = -1
+    path[1, 0] = 90
+    path[2, 800:803] = -1
+    append_case(csa, 4, 90, 1600, [7, 30, 1, 0], 1700, ratio=ratio, d_idx=d_idx, path=path, seed=13, alias=ratio == 2)
+
+
+@pytest.mark.parametrize("d_idx", [64, 128])
+def test_append_keys_next_to_their_thresholds(csa, d_idx):
+    """rows and projections of few values, whose sums lie on the quantiser's thresholds or cancel to nothing; scales from
+    the smallest to the largest in one row, whose small terms decide"""
+    g = gen(14)
+    B, R = 2, 1024
+    for kind in range(4):
+        rows = torch.zeros((B, R, 512), device="cuda")
+        if kind == 0:
+            rows += torch.randint(-1, 2, (B, R, 512), generator=g, device="cuda")
+        elif kind == 1:
+            rows[..., 0], rows[..., 16], rows[..., 32] = 448 * 6, 448 * 6, 2.0 ** -9 * torch.randint(1, 4, (B, R), generator=g, device="cuda")
+        elif kind == 2:
+            rows += torch.exp2(torch.randint(-14, 12, (B, R, 32), generator=g, device="cuda").float()).repeat_interleave(16, 2)
+            rows *= torch.randint(0, 2, (B, R, 512), generator=g, device="cuda") * 2 - 1
+        wc, ws = fp4((d_idx, 512), g)
+        if kind == 0:
+            wc, ws = torch.randint(0, 256, wc.shape, generator=g, device="cuda", dtype=torch.uint8) & 0xAA, torch.full_like(ws, 0x38)
+        elif kind == 1:
+            wc, ws = torch.full_like(wc, 0x77), torch.full_like(ws, 0x7E)
+            wc[:, 8:16] = 0xFF                                       # cancels the first group against the second
+        elif kind == 2:
+            ws = torch.randint(0, 0x7F, ws.shape, generator=g, device="cuda", dtype=torch.uint8)
+        rows = rows.to(BF)
+        got, want = caches(csa, B, R, d_idx, 1), caches(csa, B, R, d_idx, 1)
+        csa.csa2_cache_append(got, rows, torch.zeros(B, device="cuda", dtype=torch.int64), wik_codes=wc, wik_scales=ws)
+        csa.csa2_cache_write_projected(want, rows, 0, None, None, wc, ws)
+        for a, w in zip(planes(got), planes(want)):
+            assert torch.equal(a, w)
