@@ -275,7 +275,7 @@ def test_append_keys_next_to_their_thresholds(csa, d_idx):
     the smallest to the largest in one row, whose small terms decide"""
     g = gen(14)
     B, R = 2, 1024
-    for kind in range(4):
+    for kind in range(5):
         rows = torch.zeros((B, R, 512), device="cuda")
         if kind == 0:
             rows += torch.randint(-1, 2, (B, R, 512), generator=g, device="cuda")
@@ -292,6 +292,11 @@ def test_append_keys_next_to_their_thresholds(csa, d_idx):
             wc[:, 8:16] = 0xFF                                       # cancels the first group against the second
         elif kind == 2:
             ws = torch.randint(0, 0x7F, ws.shape, generator=g, device="cuda", dtype=torch.uint8)
+        elif kind == 3:                                              # the small term first, then two large ones that cancel
+            rows[..., 16], rows[..., 32] = 448 * 6, 448 * 6
+            rows[..., :16] = 2.0 ** -6 * torch.randint(-6, 7, (B, R, 16), generator=g, device="cuda")
+            wc[:, 8:16], wc[:, 16:24] = 0x77, 0xFF
+            ws[:, :1], ws[:, 1:] = 0x10, 0x7E
         rows = rows.to(BF)
         got, want = caches(csa, B, R, d_idx, 1), caches(csa, B, R, d_idx, 1)
         csa.csa2_cache_append(got, rows, torch.zeros(B, device="cuda", dtype=torch.int64), wik_codes=wc, wik_scales=ws)
