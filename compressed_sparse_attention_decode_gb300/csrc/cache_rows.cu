@@ -575,10 +575,6 @@ __global__ void __launch_bounds__(256) k_cache_read(const uint8_t* __restrict__ 
     }
 }
 
-// Entries of a call from which on the tensor cores make their keys (512 entries: 12 us without them, 14 with them; 1,024:
-// 22 and 15)
-constexpr int64_t CA_MANY = 768;
-
 cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n_rows, const int32_t* path, int n_path,
                                 const int64_t* pos0, const uint16_t* prev, uint16_t* prev_out, const float* w0,
                                 const float* w1, const uint8_t* wik_codes, const uint8_t* wik_scales, cudaStream_t st) {
@@ -588,8 +584,12 @@ cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n
     const int di = wik_codes ? c.d_idx : 0;
     const AppendArgs a{c.lat_codes, c.lat_scales, c.ikey_codes, c.ikey_scales, c.capacity, c.ratio, rows, n_rows, path, n_path, n_ent,
                        pos0, prev, carry ? prev_out : nullptr, w0, w1, wik_codes, wik_scales};
-    if (di > 0 && (int64_t)n_ent * c.batch >= CA_MANY) {
-        const int tiles = (n_ent - 1) / CM_TILE + 1;
+    // the tensor cores make the keys where that is the faster: about 10 us and 4 more for every further round of tiles, and
+    // 24 ns an entry otherwise (64 sequences' 256 entries: 12.5 us without them and 14 with; 512: 18.7 and 14; one entry of each of
+    // 304 sequences: 12.5 and 18)
+    const int tiles = (n_ent + CM_TILE - 1) / CM_TILE;
+    const int64_t rounds = ((int64_t)tiles * c.batch + 151) / 152;
+    if (di > 0 && (int64_t)n_ent * c.batch >= 160 * (1 + rounds)) {
         const unsigned grid = (unsigned)std::min<int64_t>((int64_t)tiles * c.batch, 152);
         const auto kern = di == 128 ? k_cache_append_many<128> : k_cache_append_many<64>;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CM_DYN);
