@@ -589,7 +589,7 @@ cudaError_t launch_cache_append(const csa2_cache& c, const uint16_t* rows, int n
     // 304 sequences: 12.5 and 18)
     const int tiles = (n_ent + CM_TILE - 1) / CM_TILE;
     const int64_t rounds = ((int64_t)tiles * c.batch + 151) / 152;
-    if (di > 0 && (int64_t)n_ent * c.batch >= 160 * (1 + rounds)) {
+    if (di > 0 && (int64_t)n_ent * c.batch >= 160 * (1 + rounds) && (int64_t)tiles * c.batch <= INT32_MAX) {
         const unsigned grid = (unsigned)std::min<int64_t>((int64_t)tiles * c.batch, 152);
         const auto kern = di == 128 ? k_cache_append_many<128> : k_cache_append_many<64>;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CM_DYN);

@@ -343,15 +343,22 @@ csa2_status csa2_dense_attn(const csa2_cache* cache, const uint16_t* q, int32_t 
  *         U the draft rows of its chain
  * The window rows from position p - len + 1 on (an earlier step's, say) are not read.
  *   q        bf16 [batch][n_q][n_heads][d_lat], one row set a node; 1 <= n_q <= 128
- *   q_pos    int64 [batch][n_q] raw positions (device): a child's is its parent's + 1
+ *   q_pos    int64 [batch][n_q] raw positions (device): a child's is its parent's + 1, and
+ *            the children of the last committed token all stand at the one after it
  *   parent   int32 [batch][n_q] (device): a node before it (parent[i] < i), or -1 for a
  *            child of the last committed token.  Any other value: the node is not there,
  *            nor is what hangs on it; such nodes get zeros and lse -inf
  *   draft    bf16 [batch][n_q][d_lat], the nodes' latent rows
  *   idx      int32 [batch][n_q][k], -1 for an empty slot, or NULL where k <= 0;
- *            entries outside the cache are empty slots; -1 <= k <= 2048
- *   swa, swa_pos0, swa_len, out, out_type, lse, n_heads: as in csa2_dense_attn, and its
- *            roundings.  q and what some node attends to are finite.
+ *            entries outside the cache are empty slots, an entry in two slots counts twice;
+ *            -1 <= k <= 2048
+ *   swa, swa_pos0, swa_len, lse, n_heads: as in csa2_dense_attn
+ *   out      [batch][n_q][n_heads][d_lat] of out_type; overlaps no input.  The weights of a
+ *            bf16 or fp16 out are csa2_dense_attn's (2^-11 of each); those of an fp32 out have
+ *            2^-22, and no tensor-core sum runs over more than 48 steps: its error does not
+ *            grow with the number of keys (measured: 1e-6 of the outputs' norm and less, to a
+ *            million entries)
+ * q and what some node attends to are finite.
  * Nodes that are not there and rows that no node attends to are not taken into account,
  * whatever they hold.  q, draft, swa and out 16-byte aligned, q_pos and swa_pos0 8, parent,
  * idx and lse 4.
@@ -382,7 +389,8 @@ csa2_status csa2_tree_attn(const csa2_cache* cache, const uint16_t* q, int32_t n
  *   wik_codes, wik_scales: the indexer-key projection in FP4, as in
  *              csa2_cache_write_projected, or both NULL: latents only
  * rows, prev, prev_out, w0, w1 and wik_codes 16-byte aligned, pos0 8, path and wik_scales 4;
- * n_rows and n_path may be 0; batch <= 65535; rows that are taken are finite.  No workspace.
+ * n_rows and n_path may be 0; batch <= 65535; rows that are taken are finite; prev_out
+ * overlaps nothing but prev.  No workspace.
  */
 csa2_status csa2_cache_append(const csa2_cache* cache, const uint16_t* rows, int32_t n_rows, const int32_t* path,
                               int32_t n_path, const int64_t* pos0, const uint16_t* prev, uint16_t* prev_out,

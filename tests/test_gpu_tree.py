@@ -392,3 +392,32 @@ def test_tree_fp32_outputs_keep_their_bits(csa, entries, k):
         ref = o / s[:, None]
         within(out[0, i], ref, rel * ref.abs() + keys * 2.0 ** -32 * 3)
         within(lse[0, i], s.log(), rel + 2.0 ** -22 * (1 + s.log()))
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F])
+def test_tree_lists_in_several_passes(csa, out_dtype):
+    """more rows than a pass takes (65,536): the later sequences' results and the earlier ones'"""
+    check(csa, tree_inputs(10, 64, 128, 300, [30 * b for b in range(10)], seed=21, k=20), out_dtype=out_dtype)
+
+
+def test_tree_many_sequences(csa):
+    """more sequences than a block has threads, some of them without a node that is there"""
+    parent = [[-1, 0], [-2, 0], [-1, -1]]
+    B = 1700
+    x = tree_inputs(B, 2, 3, 40, [(7 * b) % 190 for b in range(B)], ratio=1, parent=(parent * B)[:B], seed=22)
+    check(csa, x)
+    x = tree_inputs(B, 2, 3, 40, [(7 * b) % 190 for b in range(B)], ratio=1, parent=(parent * B)[:B], seed=23, k=9)
+    check(csa, x)
+
+
+@pytest.mark.parametrize("k", [None, 50])
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1e-30, -3.0])
+def test_tree_scales(csa, k, scale):
+    """none, negative, next to nothing, large enough for one key to take all"""
+    check(csa, tree_inputs(2, 4, 64, 500, [600, 77], seed=24, k=k), scale=scale)
+
+
+def test_tree_same_entry_twice_counts_twice(csa):
+    x = tree_inputs(1, 2, 16, 300, 500, seed=25, k=30)
+    x["idx"][:, :, 1::2] = x["idx"][:, :, ::2]
+    check(csa, x, out_dtype=F)
