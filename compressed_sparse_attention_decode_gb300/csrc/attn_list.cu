@@ -48,6 +48,8 @@ constexpr uint32_t TLT_S = 0, TLT_O = 256, TLT_COLS = 512;       // S partial p 
 // weights are 2^(score - m), m set TL_UP below the largest score and raised when one is more than TL_TOP above it: the
 // largest weight lies in [2^7, 2^15], and what fp16 rounds to zero is below 2^-32 of it
 constexpr float TL_UP = 7.0f, TL_TOP = 15.0f;
+// Tiles of a run of sums for an fp32 output, as in attn_tree.cu: 48 steps (16 nodes of 16 sequences, 512 entries each, 64 heads: 64 us in
+// one run and 1.3e-6 off, 74 us and 7.6e-7 with runs of six tiles, 81 us with runs of four)
 constexpr int TL_RUN = 6;
 constexpr int TL_SMS = 152;
 constexpr int TL_WIN = 2;                            // units of an item's window

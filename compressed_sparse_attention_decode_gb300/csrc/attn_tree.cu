@@ -30,7 +30,8 @@
 //
 // Roundings: entries are exact in fp16, window rows and queries to 2^-25 of a row's own scale; scores, sums and outputs fp32.
 // The weights are fp16 (2^-11 of each) where the output is of 16 bits, and two fp16 parts (2^-22) where it is fp32, which
-// doubles the value MMAs; both parts then take the two P buffers, and P waits for the values of the tile before.
+// doubles the value MMAs; both parts then take the two P buffers, and P waits for the values of the tile before.  An fp32
+// output's sums are also taken out of the tensor cores every few tiles (TR_RUN).
 #include <algorithm>
 #include <type_traits>
 
@@ -63,7 +64,11 @@ constexpr uint32_t TRT_S = 0, TRT_O = 256, TRT_COLS = 512;               // S of
 // weights are 2^(score - m), m set TR_UP below the largest score and raised when one is more than TR_TOP above it: the
 // largest weight lies in [2^7, 2^15], within fp16's range, and what fp16 rounds to zero is below 2^-32 of it
 constexpr float TR_UP = 7.0f, TR_TOP = 15.0f;
-constexpr int TR_RUN = 2;
+// Tiles of a run of sums for an fp32 output: a tensor-core sum loses some 2^-26 of itself at each 16-key step, always to zero's
+// side (200,000 entries: 5.4e-6 of the output, a million 2.6e-5), so that after 48 steps it is added to fp32 sums in global memory,
+// which stay in L2 (6.6e-7 after 32 steps, 1.1e-6 after 64).  That costs 3 us a run and SM: 16 sequences of 32K positions take
+// 564 us in one run, 921 in runs of two tiles, 744 of four.
+constexpr int TR_RUN = 3;
 constexpr int TR_PAIRS = 76;                         // pairs of CTAs at most: one CTA per SM
 constexpr int TR_OVER = 1;                           // units of an item beside its tiles: its queries and its epilogue
 
