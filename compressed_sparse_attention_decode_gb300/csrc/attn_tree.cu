@@ -70,7 +70,9 @@ constexpr float TR_UP = 7.0f, TR_TOP = 15.0f;
 // 564 us in one run, 921 in runs of two tiles, 744 of four.
 constexpr int TR_RUN = 3;
 constexpr int TR_PAIRS = 76;                         // pairs of CTAs at most: one CTA per SM
-constexpr int TR_OVER = 1;                           // units of an item beside its tiles: its queries and its epilogue
+// Units of an item beside its tiles: its queries and its epilogue, some 12,000 clocks, and a tile 3,800 (ragged-7x21: 55.5 us with one,
+// 50.8 with two, 45.9 with three or four; 20 ragged sequences of up to 3,000 positions 63.9, 52.9, 51.1 and 51.3)
+constexpr int TR_OVER = 3;
 
 __device__ __forceinline__ uint32_t tr_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
@@ -771,7 +773,7 @@ TreePlan tree_plan(int batch, int n_q, int n_heads, int64_t capacity) {
     p.row_tiles = (n_q * n_heads + TR_ROWS - 1) / TR_ROWS;
     // fewer pairs where even a full cache has fewer tiles
     const int64_t tiles = (capacity + TR_TILE - 1) / TR_TILE + 2;
-    p.pairs = (int)std::min<int64_t>(TR_PAIRS, (int64_t)batch * p.row_tiles * tiles);
+    p.pairs = (int)std::min<int64_t>(TR_PAIRS, (int64_t)batch * p.row_tiles * (tiles + TR_OVER));
     p.heads = ((size_t)p.pairs * sizeof(TreeHead) + 255) / 256 * 256;
     p.o = (size_t)2 * p.pairs * TR_ROWS * D_LAT * sizeof(float);
     p.ml = (size_t)2 * p.pairs * TR_ROWS * sizeof(float2);
