@@ -49,8 +49,9 @@ namespace csa2 {
 constexpr int TR_TILE = 128;                         // keys per tile, 64 of each CTA
 constexpr int TR_ROWS = 128;                         // rows of an item, 64 of each CTA
 constexpr int TR_THREADS = 768;
-constexpr int TR_SMW = 8, TR_SMT = TR_SMW * 32;      // warps 0-7: queries, softmax, epilogue
+constexpr int TR_SMW = 8, TR_SMT = TR_SMW * 32;      // warps 0-7: softmax, epilogue
 constexpr int TR_MMA1 = 8, TR_MMA2 = 9;              // warps 8 and 9 of CTA 0: score MMAs, value MMAs
+constexpr int TR_QW = 10, TR_QT = 64;                // warps 10-11: the queries of the next item
 constexpr int TR_OWNW = 12, TR_OWN = 256;            // warps 12-19: a CTA's own keys
 constexpr int TR_FORW = 20, TR_FOR = 128;            // warps 20-23: the other CTA's keys, this CTA's dims
 constexpr uint32_t TR_SLAB = 64 * 128;               // 64 rows or keys x 64 fp16, 128-byte swizzle
@@ -96,7 +97,6 @@ struct TreeHead {
 struct TreeArgs {
     const uint8_t *codes, *scales;
     int batch, capacity;
-    const uint16_t* q;
     int n_q, n_heads;
     float scale_log2e;
     void* out;
@@ -149,9 +149,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
     // written, the queries staged.  In each CTA, arrived on by the MMAs: scores done, values of dims 0-255
     // done (their places are free), all values done
     __shared__ __align__(8) unsigned long long b_half[2], b_full[2], b_for[2], b_pfull[2], b_q, b_sfull[2], b_ohalf[2],
-        b_odone[2];
+        b_odone[2], b_qfree;
     __shared__ uint32_t tmem_base;
-    __shared__ int qexp[64];
+    __shared__ float red_l[256];
     __shared__ int64_t wsum[TR_THREADS / 32];
     __shared__ int start_b, start_off, part_each, part_more;
     const uint32_t raw = umma::smem_u32(dyn), base = (raw + 1023u) & ~1023u;
@@ -170,7 +170,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             umma::mbar_init(sa(&b_ohalf[i]), 1);
             umma::mbar_init(sa(&b_odone[i]), 1);
         }
-        umma::mbar_init(sa(&b_q), 2 * TR_SMW);
+        umma::mbar_init(sa(&b_q), 2 * TR_QT / 32);
+        umma::mbar_init(sa(&b_qfree), 1);
         umma::fence_mbar_init();
         start_b = 0, start_off = 0;
     }
@@ -345,6 +346,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 tb += T;
             }
         }
+    } else if (warp >= TR_QW) {
+        // ================= queries: this CTA's 64 rows of the next item, once the last scores of the one before are done (k_tree_prep
+        // has them in fp16: bf16 rows converted by the softmax warps were 5,000 clocks before an item's first scores)
+        const int qt = tid - TR_QW * 32;
+        const uint32_t r_q = umma::mapa(sa(&b_q), 0);
+        for (uint32_t k = 0; tr_next(a, cur, h); ++k) {
+            if (k > 0) ok = ok && umma::mbar_wait_fast(sa(&b_qfree), (k - 1) & 1);
+            const int n_rows_q = a.n_q * a.n_heads, q0 = h.rt * TR_ROWS + 64 * (int)rank;
+            const uint16_t* src = a.t.q16 + ((int64_t)h.b * n_rows_q + q0) * D_LAT;
+#pragma unroll 4
+            for (int i = qt; i < 64 * 64; i += TR_QT) {
+                const int r = i >> 6, c = i & 63;
+                const bool there = q0 + r < n_rows_q;
+                copy16(sa(sm + TR_SQ + (c >> 3) * TR_SLAB + tr_swz(r, c & 7)), there ? src + r * D_LAT + 8 * c : a.t.q16, there);
+            }
+            copy16_wait();
+            umma::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive_pair(r_q);
+        }
     } else if (warp >= TR_MMA1 && rank == 0) {
         // ================= MMAs of the pair.  The whole warp walks the tiles, so that descriptors and addresses stay in
         // uniform registers; one elected lane issues.
@@ -373,6 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                                 umma::mma_f16_pair(tm + TRT_S + 64 * buf, qd + off, ld + off, id, ks > 0);
                             }
                             if (half == 1) umma::commit_pair(sa(&b_sfull[buf]));
+                            if (half == 1 && t == h.t1 - 1) umma::commit_pair(sa(&b_qfree));
                         }
                         __syncwarp();
                     }
@@ -412,54 +434,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             }
         }
     } else if (warp < TR_SMW) {
-        // ================= queries, softmax, outputs: a thread has one row (TMEM lane 32 (warp % 4) + lane: row lane % 64) and,
+        // ================= softmax, outputs: a thread has one row (TMEM lane 32 (warp % 4) + lane: row lane % 64) and,
         // of the tile's keys, 64 (lane / 64) + 32 (warp / 4) .. + 31; of the row's output, 128 dims
         const int qd = warp & 3, ch = warp >> 2, kh = qd >> 1, row = 32 * (qd & 1) + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
-        const uint32_t r_q = umma::mapa(sa(&b_q), 0);
         const uint32_t r_pfull[2] = {umma::mapa(sa(&b_pfull[0]), 0), umma::mapa(sa(&b_pfull[1]), 0)};
         bool first_share = true;
         while (tr_next(a, cur, h)) {
             const int T = h.t1 - h.t0, wt = h.wt;
             const int n_rows_q = a.n_q * a.n_heads, q0 = h.rt * TR_ROWS + 64 * (int)rank;
-            // ---- Q: this CTA's 64 rows, bf16 -> fp16 slabs; a row whose largest magnitude lies outside [2^-10, 2^15) is
-            // scaled by a power of two on the way.  (S of the share before is done: its values were.)
-            {
-                const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)h.b * n_rows_q + q0) * D_LAT);
-#pragma unroll 1
-                for (int r0 = warp; r0 < 64; r0 += 8 * TR_SMW) {
-                    uint4 x[8][2];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = r0 + TR_SMW * i;
-                        x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
-                        if (q0 + r < n_rows_q) x[i][0] = src[r * 64 + lane], x[i][1] = src[r * 64 + 32 + lane];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = r0 + TR_SMW * i;
-                        const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[i][0]), bf16_absmax8(x[i][1]))));
-                        const bool plain = e == 0 && a.scale_log2e >= 0.0f;
-                        const float d = a.scale_log2e < 0.0f ? -pow2f(-e) : pow2f(-e);       // scores are taken times |scale|
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const int c = lane + 32 * hh;
-                            *reinterpret_cast<uint4*>(sm + TR_SQ + (c >> 3) * TR_SLAB + tr_swz(r, c & 7)) =
-                                plain ? bf16x8_to_f16x8(x[i][hh]) : bf16x8_to_f16x8(x[i][hh], d);
-                        }
-                        if (lane == 0) qexp[r] = e;
-                    }
-                }
-                umma::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive_pair(r_q);
-                umma::bar_named(3, TR_SMT);
-            }
             // the window rows' part of O carries 2^-wexp; a row of another exponent enters with its weight scaled by the difference
             bool scaled;
             const int wexp = max(tree_exp(a.t, h.b, a.t.seq[h.b].n_rows, scaled), -100);
+            const int q_exp = q0 + row < n_rows_q ? a.t.q_exps[(int64_t)h.b * n_rows_q + q0 + row] : 0;
             // never zero, so that a masked score stays -inf (a score of nearly nothing for a scale of nothing)
-            const float mul4 = fmaxf(fabsf(a.scale_log2e) * pow2f(qexp[row]), 0x1p-100f);
+            const float mul4 = fmaxf(fabsf(a.scale_log2e) * pow2f(q_exp), 0x1p-100f);
             int vis = 0;
             const uint32_t* mask = nullptr;
             if (q0 + row < n_rows_q) {
@@ -642,12 +631,11 @@ float4 y[2][4] = {};                     // the next 16 columns' under way
             ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
             umma::fence_after();
             if (FINE && T > TR_RUN) add_run(T, true);
-            float* red = reinterpret_cast<float*>(sm + TR_SP) + row;      // both P buffers are free
-            red[64 * (2 * kh + ch)] = lsum;
+            red_l[64 * (2 * kh + ch) + row] = lsum;
             umma::bar_named(3, TR_SMT);
             float l = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) l += red[64 * i];
+            for (int i = 0; i < 4; ++i) l += red_l[64 * i + row];
             const float fin = h.t1 <= wt ? pow2f(wexp) : 1.0f;
             const bool whole = T == h.T;
             const int64_t gr = (int64_t)h.b * n_rows_q + q0 + row;
@@ -655,12 +643,12 @@ float4 y[2][4] = {};                     // the next 16 columns' under way
             const int64_t pr = (int64_t)slot * TR_ROWS + 64 * (int)rank + row;
             const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
             const int d0 = 256 * ch + 128 * kh;
-            // 256 bytes of each of the warp's 32 rows at a time through the queries' place (no longer needed), so that rows are
-            // stored as whole lines: a thread has a row, and rows lie far apart
+            // 128 bytes of each of the warp's 32 rows at a time through the P buffers (both free), so that rows are stored as whole
+            // lines: a thread has a row, and rows lie far apart
             auto store = [&](auto* dst, int rows, float f) {         // dst: the warp's first row, first dim
                 using TD = std::remove_pointer_t<decltype(dst)>;
-                constexpr int E = 16 / (int)sizeof(TD), N = 16 * E;  // elements of a piece, of a round
-                uint8_t* mine = sm + TR_SQ + warp * 8192;
+                constexpr int E = 16 / (int)sizeof(TD), N = 8 * E;   // elements of a piece, of a round
+                uint8_t* mine = sm + TR_SP + warp * 4096;
                 f = ok ? f : __int_as_float(0x7fc00000);
 #pragma unroll 1
                 for (int c0 = 0; c0 < 128; c0 += N) {
@@ -675,14 +663,14 @@ float4 y[2][4] = {};                     // the next 16 columns' under way
                         for (int i = 0; i < 16; i += E) {
                             ElemVec<TD, E> y;
                             y.pack(v + i);
-                            y.store(reinterpret_cast<TD*>(mine + lane * 256 + ((((c + i) / E) ^ (lane & 15)) << 4)));
+                            y.store(reinterpret_cast<TD*>(mine + lane * 128 + ((((c + i) / E) ^ (lane & 7)) << 4)));
                         }
                     }
                     __syncwarp();
 #pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = 2 * i + (lane >> 4), k = lane & 15;
-                        const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 256 + ((k ^ (r & 15)) << 4));
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3), k = lane & 7;
+                        const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 128 + ((k ^ (r & 7)) << 4));
                         if (r < rows) *reinterpret_cast<uint4*>(dst + (int64_t)r * D_LAT + c0 + k * E) = y;
                     }
                     __syncwarp();
@@ -708,7 +696,7 @@ float4 y[2][4] = {};                     // the next 16 columns' under way
             first_share = false;
             tb += T;
             umma::fence_before();
-            umma::bar_named(3, TR_SMT);              // red, qexp and O are read
+            umma::bar_named(3, TR_SMT);              // sums, pieces and O are read
             umma::fence_after();
         }
     }
@@ -767,25 +755,24 @@ constexpr size_t TR_HEAD = 256;                      // the error word and paddi
 struct TreePlan {
     int row_tiles, pairs;
     size_t heads, o, ml;                             // bytes of the workspace's parts after the nodes'
+    TreePlan(int batch, int n_q, int n_heads, int64_t capacity) {
+        row_tiles = (n_q * n_heads + TR_ROWS - 1) / TR_ROWS;
+        // fewer pairs where even a full cache has fewer tiles
+        const int64_t tiles = (capacity + TR_TILE - 1) / TR_TILE + 2;
+        pairs = (int)std::min<int64_t>(TR_PAIRS, (int64_t)batch * row_tiles * (tiles + TR_OVER));
+        heads = ((size_t)pairs * sizeof(TreeHead) + 255) / 256 * 256;
+        o = (size_t)2 * pairs * TR_ROWS * D_LAT * sizeof(float);
+        ml = (size_t)2 * pairs * TR_ROWS * sizeof(float2);
+    }
 };
-TreePlan tree_plan(int batch, int n_q, int n_heads, int64_t capacity) {
-    TreePlan p;
-    p.row_tiles = (n_q * n_heads + TR_ROWS - 1) / TR_ROWS;
-    // fewer pairs where even a full cache has fewer tiles
-    const int64_t tiles = (capacity + TR_TILE - 1) / TR_TILE + 2;
-    p.pairs = (int)std::min<int64_t>(TR_PAIRS, (int64_t)batch * p.row_tiles * (tiles + TR_OVER));
-    p.heads = ((size_t)p.pairs * sizeof(TreeHead) + 255) / 256 * 256;
-    p.o = (size_t)2 * p.pairs * TR_ROWS * D_LAT * sizeof(float);
-    p.ml = (size_t)2 * p.pairs * TR_ROWS * sizeof(float2);
-    return p;
-}
 }  // namespace
 
 size_t tree_attn_ws(int batch, int n_q, int n_heads, int k, int64_t capacity) {
     const size_t lists = k >= 0 ? tree_lists_ws(batch, n_q, n_heads, k) : 0;
     if (k > 0) return lists;
-    const TreePlan p = tree_plan(batch, n_q, n_heads, capacity);
-    return std::max(lists, TR_HEAD + tree_nodes_bytes(batch, n_q, 0) + p.heads + p.o + p.ml);
+    const int nb = tree_pass(batch, n_q, n_heads);   // (a last pass of fewer sequences has fewer pairs, if any)
+    const TreePlan p(nb, n_q, n_heads, capacity);
+    return std::max(lists, TR_HEAD + tree_nodes_bytes(nb, n_q, n_heads) + p.heads + p.o + p.ml);
 }
 
 cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
@@ -795,31 +782,39 @@ cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, in
     if (k >= 0)
         return launch_tree_lists(c, q, n_q, n_heads, q_pos, parent, draft, idx, k, swa, swa_pos0, swa_len, scale, out, out_type, lse,
                                  ws, st);
-    const TreePlan p = tree_plan(c.batch, n_q, n_heads, c.capacity);
-    TreeCall call{c.batch, c.capacity, c.ratio, n_q, n_heads, q_pos, parent, draft, swa, swa_pos0, swa_len, {}, nullptr, false, out, lse,
-                  out_type == CSA2_F32 ? 4 : 2};
-    uint8_t* w = tree_nodes_take(call.t, c.batch, n_q, 0, reinterpret_cast<uint8_t*>(ws) + TR_HEAD);
-    TreeArgs a{c.lat_codes, c.lat_scales, c.batch, c.capacity, q, n_q, n_heads, scale * 1.4426950408889634f, out, lse, call.t,
-               nullptr, nullptr, nullptr, reinterpret_cast<int*>(ws)};
-    a.heads = reinterpret_cast<TreeHead*>(w);
-    a.part_o = reinterpret_cast<float*>(w + p.heads);
-    a.part_ml = reinterpret_cast<float2*>(w + p.heads + p.o);
     auto go = [&](auto* y) {
         using TO = std::remove_pointer_t<decltype(y)>;
         cudaError_t e = cudaFuncSetAttribute(k_tree_attn<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TR_DYN);
-        if (e != cudaSuccess) return e;
-        e = launch_tree_prep(call, st);
-        if (e != cudaSuccess) return e;
-        launch_k(k_tree_attn<TO>, dim3((unsigned)(2 * p.pairs)), TR_THREADS, TR_DYN, st, a);
-        // few items: many shares each, so a block per row
-        const int64_t items = (int64_t)c.batch * p.row_tiles;
-        const int rows = std::min(TR_ROWS, n_q * n_heads);
-        if (items * 8 <= p.pairs)
-            launch_k(k_tree_join<TO, 4>, dim3((unsigned)items, (unsigned)rows), 512, 0, st, a, p.pairs, p.row_tiles);
-        else
-            launch_k(k_tree_join<TO, 1>, dim3((unsigned)p.pairs, (unsigned)((rows + 3) / 4)), 512, 0, st, a, p.pairs, p.row_tiles);
-        note_launch(2);
-        return cudaGetLastError();
+        const int pass = tree_pass(c.batch, n_q, n_heads), rows = std::min(TR_ROWS, n_q * n_heads);
+        for (int b0 = 0; b0 < c.batch && e == cudaSuccess; b0 += pass) {
+            const int nb = std::min(pass, c.batch - b0);
+            const int64_t n0 = (int64_t)b0 * n_q, r0 = n0 * n_heads;         // nodes and rows before the pass
+            const TreePlan p(nb, n_q, n_heads, c.capacity);
+            TO* o = y + r0 * D_LAT;
+            float* l = lse ? lse + r0 : nullptr;
+            TreeCall call{nb, c.capacity, c.ratio, n_q, n_heads, q_pos + n0, parent + n0, draft + n0 * D_LAT,
+                          swa ? swa + (int64_t)b0 * swa_len * D_LAT : nullptr, swa_pos0 ? swa_pos0 + b0 : nullptr, swa_len, {},
+                          q + r0 * D_LAT, scale < 0.0f, o, l, (int)sizeof(TO)};
+            uint8_t* w = tree_nodes_take(call.t, nb, n_q, n_heads, reinterpret_cast<uint8_t*>(ws) + TR_HEAD);
+            TreeArgs a{c.lat_codes + (int64_t)b0 * c.capacity * (D_LAT / 2), c.lat_scales + (int64_t)b0 * c.capacity * (D_LAT / 16), nb,
+                       c.capacity, n_q, n_heads, scale * 1.4426950408889634f, o, l, call.t, nullptr, nullptr, nullptr,
+                       reinterpret_cast<int*>(ws)};
+            a.heads = reinterpret_cast<TreeHead*>(w);
+            a.part_o = reinterpret_cast<float*>(w + p.heads);
+            a.part_ml = reinterpret_cast<float2*>(w + p.heads + p.o);
+            e = launch_tree_prep(call, st);
+            if (e != cudaSuccess) break;
+            launch_k(k_tree_attn<TO>, dim3((unsigned)(2 * p.pairs)), TR_THREADS, TR_DYN, st, a);
+            // few items: many shares each, so a block per row
+            const int64_t items = (int64_t)nb * p.row_tiles;
+            if (items * 8 <= p.pairs)
+                launch_k(k_tree_join<TO, 4>, dim3((unsigned)items, (unsigned)rows), 512, 0, st, a, p.pairs, p.row_tiles);
+            else
+                launch_k(k_tree_join<TO, 1>, dim3((unsigned)p.pairs, (unsigned)((rows + 3) / 4)), 512, 0, st, a, p.pairs, p.row_tiles);
+            note_launch(2);
+            e = cudaGetLastError();
+        }
+        return e;
     };
     return out_type == CSA2_F32   ? go(reinterpret_cast<float*>(out))
            : out_type == CSA2_F16 ? go(reinterpret_cast<__half*>(out))

@@ -1,5 +1,7 @@
 // What both kernels of drafted trees (attn_tree.cu: every visible entry, attn_list.cu: index lists) take from k_tree_prep.
 #pragma once
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace csa2 {
@@ -22,7 +24,7 @@ struct TreeNodes {
     int8_t* exps;                // [batch][256]
     int* top;                    // [batch][TREE_GROUPS] the largest exponent of a group of rows, 2^16 more where one is not 0
     int row_stride;
-    // attn_list.cu: the queries as fp16, row r a 2^-q_exps[r] of q's (times -1 where neg_q), or NULL
+    // the queries as fp16, row r a 2^-q_exps[r] of q's (times -1 where neg_q)
     uint16_t* q16;               // [batch][n_q][n_heads][512]
     int8_t* q_exps;              // [batch][n_q][n_heads]
 };
@@ -44,13 +46,15 @@ struct TreeCall {
     TreeNodes t;
     const uint16_t* q;
     bool neg_q;
-    void* out;                   // without q16: rows of items that nobody works on are written by k_tree_prep
+    void* out;                   // or NULL: rows of attn_tree.cu's items that nobody works on are written by k_tree_prep
     float* lse;
     int out_size;                // bytes of an element
 };
-// a workspace's bytes for it, and its pointers from byte w on (returns the first byte after it); q_rows: rows of q16
-size_t tree_nodes_bytes(int batch, int n_q, int64_t q_rows);
-uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int64_t q_rows, uint8_t* w);
+// Sequences of a pass: 65,536 rows at most (of one sequence 16,384), whose fp16 queries are 64 MB
+inline int tree_pass(int batch, int n_q, int n_heads) { return (int)std::min<int64_t>(batch, (1 << 16) / ((int64_t)n_q * n_heads)); }
+// a workspace's bytes for a pass, and its pointers from byte w on (returns the first byte after it)
+size_t tree_nodes_bytes(int batch, int n_q, int n_heads);
+uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int n_heads, uint8_t* w);
 cudaError_t launch_tree_prep(const TreeCall& c, cudaStream_t st);
 
 // 16 bytes from global to shared memory, zeros where `there` is false

@@ -19,10 +19,10 @@ __device__ __forceinline__ int row_to_f16(const uint4* x, uint4* dst, bool neg) 
     return e;
 }
 
-// Blocks (sequence, group of 16 rows), and some more that write the rows of items that nobody works on, or convert the
-// sequence's queries.  Every block finds the chains for itself (a thread a node), the first one writes the nodes' part; then
-// a warp has two rows.
-__global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeCall a) {
+// Blocks (sequence, group of 16 rows), `fill` more that write the rows of items that nobody works on, and others that convert
+// the sequence's queries.  All but those find the chains for themselves (a thread a node), the first one writes the nodes'
+// part; then a warp has two rows.
+__global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeCall a, int fill) {
     __shared__ int parent[TREE_NODES], last_s, vis_s, tops[8], offs[8];
     __shared__ long long hi_s;
     __shared__ uint32_t there[4];
@@ -31,6 +31,28 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
     if (tid < 4) there[tid] = 0u;
     pdl_wait();
     pdl_launch_next();
+    if (group >= TREE_GROUPS + fill) {
+        // four rows of the sequence's queries a warp at a time (those of nodes that are not there too: nobody reads them)
+        const int rows = N * a.n_heads, warps = ((int)gridDim.y - TREE_GROUPS - fill) * 8;
+        const int64_t r0 = (int64_t)b * rows;
+        for (int r = (group - TREE_GROUPS - fill) * 8 + warp; r < rows; r += 4 * warps) {
+            uint4 x[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r + i * warps < rows) {
+                    const uint4* src = reinterpret_cast<const uint4*>(a.q + (r0 + r + i * warps) * D_LAT);
+                    x[i][0] = src[lane], x[i][1] = src[32 + lane];
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (r + i * warps >= rows) break;
+                const int64_t at = r0 + r + i * warps;
+                const int e = row_to_f16(x[i], reinterpret_cast<uint4*>(a.t.q16 + at * D_LAT), a.neg_q);
+                if (lane == 0) a.t.q_exps[at] = (int8_t)e;
+            }
+        }
+        return;
+    }
     int64_t p = 0;
     if (tid < N) {
         parent[tid] = a.parent[(int64_t)b * N + tid];
@@ -61,33 +83,11 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
     __syncthreads();
     const int last = last_s;
     const int row_tiles = ((last + 1) * a.n_heads + 127) / 128;
-    if (group >= TREE_GROUPS && a.t.q16 != nullptr) {
-        // four rows of the sequence's queries a warp at a time (those of nodes that are not there too: nobody reads them)
-        const int rows = N * a.n_heads, warps = ((int)gridDim.y - TREE_GROUPS) * 8;
-        const int64_t r0 = (int64_t)b * rows;
-        for (int r = (group - TREE_GROUPS) * 8 + warp; r < rows; r += 4 * warps) {
-            uint4 x[4][2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (r + i * warps < rows) {
-                    const uint4* src = reinterpret_cast<const uint4*>(a.q + (r0 + r + i * warps) * D_LAT);
-                    x[i][0] = src[lane], x[i][1] = src[32 + lane];
-                }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (r + i * warps >= rows) break;
-                const int64_t at = r0 + r + i * warps;
-                const int e = row_to_f16(x[i], reinterpret_cast<uint4*>(a.t.q16 + at * D_LAT), a.neg_q);
-                if (lane == 0) a.t.q_exps[at] = (int8_t)e;
-            }
-        }
-        return;
-    }
     if (group >= TREE_GROUPS) {
         const int64_t r0 = (int64_t)row_tiles * 128, r1 = (int64_t)N * a.n_heads, base = (int64_t)b * r1;
         const int pieces = D_LAT * a.out_size / 16;
         uint4* o = reinterpret_cast<uint4*>(a.out) + base * pieces;
-        const int64_t step = (int64_t)(gridDim.y - TREE_GROUPS) * 256, first = (int64_t)(group - TREE_GROUPS) * 256 + tid;
+        const int64_t step = (int64_t)fill * 256, first = (int64_t)(group - TREE_GROUPS) * 256 + tid;
         for (int64_t i = r0 * pieces + first; i < r1 * pieces; i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
         if (a.lse != nullptr)
             for (int64_t i = r0 + first; i < r1; i += step) a.lse[base + i] = -INFINITY;
@@ -164,25 +164,25 @@ namespace {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 struct NodeParts {
     size_t seq, vis, mask, exps, top, rows, q, q_exps;
-    NodeParts(int batch, int n_q, int64_t q_rows)
+    NodeParts(int batch, int n_q, int n_heads)
         : seq(up256((size_t)batch * sizeof(TreeSeq))),
           vis(up256((size_t)batch * n_q * sizeof(int))),
           mask(up256((size_t)batch * n_q * 8 * sizeof(uint32_t))),
           exps((size_t)batch * 256),
           top(up256((size_t)batch * TREE_GROUPS * sizeof(int))),
           rows((size_t)batch * (WINDOW - 1 + n_q) * D_LAT * sizeof(uint16_t)),
-          q((size_t)q_rows * D_LAT * sizeof(uint16_t)),
-          q_exps(up256((size_t)q_rows)) {}
+          q((size_t)batch * n_q * n_heads * D_LAT * sizeof(uint16_t)),
+          q_exps(up256((size_t)batch * n_q * n_heads)) {}
 };
 }  // namespace
 
-size_t tree_nodes_bytes(int batch, int n_q, int64_t q_rows) {
-    const NodeParts p(batch, n_q, q_rows);
+size_t tree_nodes_bytes(int batch, int n_q, int n_heads) {
+    const NodeParts p(batch, n_q, n_heads);
     return p.seq + p.vis + p.mask + p.exps + p.top + p.rows + p.q + p.q_exps;
 }
 
-uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int64_t q_rows, uint8_t* w) {
-    const NodeParts p(batch, n_q, q_rows);
+uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int n_heads, uint8_t* w) {
+    const NodeParts p(batch, n_q, n_heads);
     t.seq = reinterpret_cast<TreeSeq*>(w), w += p.seq;
     t.vis = reinterpret_cast<int*>(w), w += p.vis;
     t.mask = reinterpret_cast<uint32_t*>(w), w += p.mask;
@@ -190,15 +190,15 @@ uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int64_t q_rows, uint8
     t.top = reinterpret_cast<int*>(w), w += p.top;
     t.rows16 = reinterpret_cast<uint16_t*>(w), w += p.rows;
     t.row_stride = WINDOW - 1 + n_q;
-    t.q16 = q_rows > 0 ? reinterpret_cast<uint16_t*>(w) : nullptr, w += p.q;
+    t.q16 = reinterpret_cast<uint16_t*>(w), w += p.q;
     t.q_exps = reinterpret_cast<int8_t*>(w), w += p.q_exps;
     return w;
 }
 
 cudaError_t launch_tree_prep(const TreeCall& c, cudaStream_t st) {
     const int rows = c.n_q * c.n_heads;
-    const int more = c.t.q16 ? (rows + 31) / 32 : std::min(16, (rows + 511) / 512);
-    launch_k(k_tree_prep, dim3((unsigned)c.batch, (unsigned)(TREE_GROUPS + more)), 256, 0, st, c);
+    const int fill = c.out ? std::min(16, (rows + 511) / 512) : 0;
+    launch_k(k_tree_prep, dim3((unsigned)c.batch, (unsigned)(TREE_GROUPS + fill + (rows + 31) / 32)), 256, 0, st, c, fill);
     note_launch();
     return cudaGetLastError();
 }
