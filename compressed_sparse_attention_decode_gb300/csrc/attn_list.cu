@@ -622,9 +622,9 @@ struct ListPlan {
 }  // namespace
 
 size_t tree_lists_ws(int batch, int n_q, int n_heads, int k) {
-    const int nb = tree_pass(batch, n_q, n_heads);
+    const int nb = tree_pass(batch, n_q * n_heads);
     const size_t rows = (size_t)2 * TL_SMS * TL_H;
-    return TL_HEAD + tree_nodes_bytes(nb, n_q, n_heads) + rows * (D_LAT * sizeof(float) + sizeof(float2));
+    return TL_HEAD + tree_nodes_bytes(nb, n_q, n_q * n_heads) + rows * (D_LAT * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_tree_lists(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
@@ -634,15 +634,15 @@ cudaError_t launch_tree_lists(const csa2_cache& c, const uint16_t* q, int n_q, i
     auto go = [&](auto* y) {
         using TO = std::remove_pointer_t<decltype(y)>;
         cudaError_t e = cudaFuncSetAttribute(k_tree_lists<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TL_DYN);
-        const int pass = tree_pass(c.batch, n_q, n_heads);
+        const int pass = tree_pass(c.batch, n_q * n_heads);
         for (int b0 = 0; b0 < c.batch && e == cudaSuccess; b0 += pass) {
             const int nb = std::min(pass, c.batch - b0);
             const int64_t n0 = (int64_t)b0 * n_q, r0 = n0 * n_heads;         // nodes and rows before the pass
             const ListPlan p(nb, n_q, n_heads, k);
             TreeCall call{nb, c.capacity, c.ratio, n_q, n_heads, q_pos + n0, parent + n0, draft + n0 * D_LAT,
                           swa ? swa + (int64_t)b0 * swa_len * D_LAT : nullptr, swa_pos0 ? swa_pos0 + b0 : nullptr, swa_len, {},
-                          q + r0 * D_LAT, scale < 0.0f, nullptr, nullptr, 0};
-            uint8_t* w = tree_nodes_take(call.t, nb, n_q, n_heads, reinterpret_cast<uint8_t*>(ws) + TL_HEAD);
+                          q + r0 * D_LAT, scale < 0.0f, false, nullptr, nullptr, 0};
+            uint8_t* w = tree_nodes_take(call.t, nb, n_q, n_q * n_heads, reinterpret_cast<uint8_t*>(ws) + TL_HEAD);
             ListArgs a{c.lat_codes + (int64_t)b0 * c.capacity * (D_LAT / 2), c.lat_scales + (int64_t)b0 * c.capacity * (D_LAT / 16),
                        c.capacity, n_q, n_heads, p.hgroups, call.t, idx ? idx + n0 * k : nullptr, k, scale * 1.4426950408889634f,
                        y + r0 * D_LAT, lse ? lse + r0 : nullptr, p.per, p.grain, p.each, p.more, nullptr, nullptr,

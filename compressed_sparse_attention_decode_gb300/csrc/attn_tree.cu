@@ -51,7 +51,7 @@ constexpr int TR_ROWS = 128;                         // rows of an item, 64 of e
 constexpr int TR_THREADS = 768;
 constexpr int TR_SMW = 8, TR_SMT = TR_SMW * 32;      // warps 0-7: softmax, epilogue
 constexpr int TR_MMA1 = 8, TR_MMA2 = 9;              // warps 8 and 9 of CTA 0: score MMAs, value MMAs
-constexpr int TR_QW = 10, TR_QT = 64;                // warps 10-11: the queries of the next item
+constexpr int TR_QW = 10;                            // a thread of warp 10: the queries of the next item
 constexpr int TR_OWNW = 12, TR_OWN = 256;            // warps 12-19: a CTA's own keys
 constexpr int TR_FORW = 20, TR_FOR = 128;            // warps 20-23: the other CTA's keys, this CTA's dims
 constexpr uint32_t TR_SLAB = 64 * 128;               // 64 rows or keys x 64 fp16, 128-byte swizzle
@@ -74,8 +74,6 @@ constexpr int TR_PAIRS = 76;                         // pairs of CTAs at most: o
 // Units of an item beside its tiles: its queries and its epilogue, some 12,000 clocks, and a tile 3,800 (ragged-7x21: 55.5 us with one,
 // 50.8 with two, 45.9 with three or four; 20 ragged sequences of up to 3,000 positions 63.9, 52.9, 51.1 and 51.3)
 constexpr int TR_OVER = 3;
-
-__device__ __forceinline__ uint32_t tr_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
 // (d0, d1) += (a0, a1), one packed instruction
 __device__ __forceinline__ void add2_rn(float& d0, float& d1, float a0, float a1) {
@@ -149,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
     // written, the queries staged.  In each CTA, arrived on by the MMAs: scores done, values of dims 0-255
     // done (their places are free), all values done
     __shared__ __align__(8) unsigned long long b_half[2], b_full[2], b_for[2], b_pfull[2], b_q, b_sfull[2], b_ohalf[2],
-        b_odone[2], b_qfree;
+        b_odone[2], b_qfree, b_qhere;
     __shared__ uint32_t tmem_base;
     __shared__ float red_l[256];
     __shared__ int64_t wsum[TR_THREADS / 32];
@@ -170,8 +168,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             umma::mbar_init(sa(&b_ohalf[i]), 1);
             umma::mbar_init(sa(&b_odone[i]), 1);
         }
-        umma::mbar_init(sa(&b_q), 2 * TR_QT / 32);
+        umma::mbar_init(sa(&b_q), 2);
         umma::mbar_init(sa(&b_qfree), 1);
+        umma::mbar_init(sa(&b_qhere), 1);
         umma::fence_mbar_init();
         start_b = 0, start_off = 0;
     }
@@ -248,7 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int cc = 4 * c + k;
-                *reinterpret_cast<uint4*>(L + ((cc >> 3) ^ flip) * TR_SLAB + tr_swz(r, cc & 7)) =
+                *reinterpret_cast<uint4*>(L + ((cc >> 3) ^ flip) * TR_SLAB + tree_swz(r, cc & 7)) =
                     e2m1x8_scaled(words[k], (k >> 1) ? s_hi : s_lo);
             }
         };
@@ -292,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
 #pragma unroll 4
                             for (int i = lt; i < 64 * 32; i += TR_OWN) {
                                 const int r = i >> 5, cc = 32 * half + (i & 31);
-                                copy_row(v0 + r, cc, L + (cc >> 3) * TR_SLAB + tr_swz(r, cc & 7));
+                                copy_row(v0 + r, cc, L + (cc >> 3) * TR_SLAB + tree_swz(r, cc & 7));
                             }
                             copy16_wait();
                         } else {
@@ -333,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                         for (int i = lt; i < 64 * 32; i += TR_FOR) {
                             const int r = i >> 5, cs = i & 31;       // this CTA's 32 chunks: 16 of dims 128 r .., 16 of 256 + 128 r ..
                             const int cc = 32 * (cs >> 4) + 16 * (int)rank + (cs & 15);
-                            copy_row(v0 + r, cc, L + ((cc >> 3) ^ 2) * TR_SLAB + tr_swz(r, cc & 7));
+                            copy_row(v0 + r, cc, L + ((cc >> 3) ^ 2) * TR_SLAB + tree_swz(r, cc & 7));
                         }
                         copy16_wait();
                     } else {
@@ -347,25 +346,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             }
         }
     } else if (warp >= TR_QW) {
-        // ================= queries: this CTA's 64 rows of the next item, once the last scores of the one before are done (k_tree_prep
-        // has them in fp16: bf16 rows converted by the softmax warps were 5,000 clocks before an item's first scores)
-        const int qt = tid - TR_QW * 32;
-        const uint32_t r_q = umma::mapa(sa(&b_q), 0);
-        for (uint32_t k = 0; tr_next(a, cur, h); ++k) {
-            if (k > 0) ok = ok && umma::mbar_wait_fast(sa(&b_qfree), (k - 1) & 1);
-            const int n_rows_q = a.n_q * a.n_heads, q0 = h.rt * TR_ROWS + 64 * (int)rank;
-            const uint16_t* src = a.t.q16 + ((int64_t)h.b * n_rows_q + q0) * D_LAT;
-#pragma unroll 4
-            for (int i = qt; i < 64 * 64; i += TR_QT) {
-                const int r = i >> 6, c = i & 63;
-                const bool there = q0 + r < n_rows_q;
-                copy16(sa(sm + TR_SQ + (c >> 3) * TR_SLAB + tr_swz(r, c & 7)), there ? src + r * D_LAT + 8 * c : a.t.q16, there);
+        // ================= queries: this CTA's 64 rows of the next item, once the last scores of the one before are done.
+        // k_tree_prep has them as fp16 in this very layout (bf16 rows converted by the softmax warps were 5,000 clocks before an
+        // item's first scores, fp16 rows copied 16 bytes at a time 4,000).  Rows that are not there hold anything: a row's scores
+        // and outputs are its own.
+        if (tid == TR_QW * 32) {
+            const uint32_t r_q = umma::mapa(sa(&b_q), 0);
+            const uint8_t* q16 = reinterpret_cast<const uint8_t*>(a.t.q16);
+            const int tiles = (a.n_q * a.n_heads + TR_ROWS - 1) / TR_ROWS;
+            for (uint32_t k = 0; tr_next(a, cur, h); ++k) {
+                if (k > 0) ok = ok && umma::mbar_wait_fast(sa(&b_qfree), (k - 1) & 1);
+                const uint8_t* src = q16 + (((int64_t)h.b * tiles + h.rt) * 2 + rank) * (8 * TR_SLAB);
+                umma::mbar_arrive_expect_tx(sa(&b_qhere), 8 * TR_SLAB);
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) umma::bulk_g2s(base + TR_SQ + i * TR_SLAB, src + i * TR_SLAB, TR_SLAB, sa(&b_qhere));
+                ok = umma::mbar_wait(sa(&b_qhere), k & 1) && ok;
+                umma::mbar_arrive_pair(r_q);
             }
-            copy16_wait();
-            umma::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive_pair(r_q);
         }
+        __syncwarp();
     } else if (warp >= TR_MMA1 && rank == 0) {
         // ================= MMAs of the pair.  The whole warp walks the tiles, so that descriptors and addresses stay in
         // uniform registers; one elected lane issues.
@@ -605,9 +604,9 @@ float4 y[2][4] = {};                     // the next 16 columns' under way
                             low[i] = f16x2_bits(d0 - part.x, d1 - part.y);
                         }
                     }
-                    *reinterpret_cast<uint4*>(P + tr_swz(row, 4 * ch + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(P + tree_swz(row, 4 * ch + c)) = make_uint4(w[0], w[1], w[2], w[3]);
                     if constexpr (FINE)
-                        *reinterpret_cast<uint4*>(P + TR_PBUF + tr_swz(row, 4 * ch + c)) = make_uint4(low[0], low[1], low[2], low[3]);
+                        *reinterpret_cast<uint4*>(P + TR_PBUF + tree_swz(row, 4 * ch + c)) = make_uint4(low[0], low[1], low[2], low[3]);
                 }
                 if (!odd) lsum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 umma::fence_proxy_async();
@@ -770,9 +769,9 @@ struct TreePlan {
 size_t tree_attn_ws(int batch, int n_q, int n_heads, int k, int64_t capacity) {
     const size_t lists = k >= 0 ? tree_lists_ws(batch, n_q, n_heads, k) : 0;
     if (k > 0) return lists;
-    const int nb = tree_pass(batch, n_q, n_heads);   // (a last pass of fewer sequences has fewer pairs, if any)
+    const int q_rows = tree_q_rows(n_q, n_heads, true), nb = tree_pass(batch, q_rows);      // (a last pass of fewer sequences has fewer pairs, if any)
     const TreePlan p(nb, n_q, n_heads, capacity);
-    return std::max(lists, TR_HEAD + tree_nodes_bytes(nb, n_q, n_heads) + p.heads + p.o + p.ml);
+    return std::max(lists, TR_HEAD + tree_nodes_bytes(nb, n_q, q_rows) + p.heads + p.o + p.ml);
 }
 
 cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, int n_heads, const int64_t* q_pos,
@@ -785,7 +784,7 @@ cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, in
     auto go = [&](auto* y) {
         using TO = std::remove_pointer_t<decltype(y)>;
         cudaError_t e = cudaFuncSetAttribute(k_tree_attn<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TR_DYN);
-        const int pass = tree_pass(c.batch, n_q, n_heads), rows = std::min(TR_ROWS, n_q * n_heads);
+        const int q_rows = tree_q_rows(n_q, n_heads, true), pass = tree_pass(c.batch, q_rows), rows = std::min(TR_ROWS, n_q * n_heads);
         for (int b0 = 0; b0 < c.batch && e == cudaSuccess; b0 += pass) {
             const int nb = std::min(pass, c.batch - b0);
             const int64_t n0 = (int64_t)b0 * n_q, r0 = n0 * n_heads;         // nodes and rows before the pass
@@ -794,8 +793,8 @@ cudaError_t launch_tree_attn(const csa2_cache& c, const uint16_t* q, int n_q, in
             float* l = lse ? lse + r0 : nullptr;
             TreeCall call{nb, c.capacity, c.ratio, n_q, n_heads, q_pos + n0, parent + n0, draft + n0 * D_LAT,
                           swa ? swa + (int64_t)b0 * swa_len * D_LAT : nullptr, swa_pos0 ? swa_pos0 + b0 : nullptr, swa_len, {},
-                          q + r0 * D_LAT, scale < 0.0f, o, l, (int)sizeof(TO)};
-            uint8_t* w = tree_nodes_take(call.t, nb, n_q, n_heads, reinterpret_cast<uint8_t*>(ws) + TR_HEAD);
+                          q + r0 * D_LAT, scale < 0.0f, true, o, l, (int)sizeof(TO)};
+            uint8_t* w = tree_nodes_take(call.t, nb, n_q, q_rows, reinterpret_cast<uint8_t*>(ws) + TR_HEAD);
             TreeArgs a{c.lat_codes + (int64_t)b0 * c.capacity * (D_LAT / 2), c.lat_scales + (int64_t)b0 * c.capacity * (D_LAT / 16), nb,
                        c.capacity, n_q, n_heads, scale * 1.4426950408889634f, o, l, call.t, nullptr, nullptr, nullptr,
                        reinterpret_cast<int*>(ws)};

@@ -25,7 +25,7 @@ struct TreeNodes {
     int* top;                    // [batch][TREE_GROUPS] the largest exponent of a group of rows, 2^16 more where one is not 0
     int row_stride;
     // the queries as fp16, row r a 2^-q_exps[r] of q's (times -1 where neg_q)
-    uint16_t* q16;               // [batch][n_q][n_heads][512]
+    uint16_t* q16;               // [batch][n_q][n_heads][512], or q_tiles: [batch][64 rows][8 slabs of 64 dims][64][64], swizzled
     int8_t* q_exps;              // [batch][n_q][n_heads]
 };
 // The largest exponent of a sequence's rows, and whether any is not 0 (a whole warp calls it)
@@ -45,16 +45,20 @@ struct TreeCall {
     int swa_len;
     TreeNodes t;
     const uint16_t* q;
-    bool neg_q;
+    bool neg_q, q_tiles;
     void* out;                   // or NULL: rows of attn_tree.cu's items that nobody works on are written by k_tree_prep
     float* lse;
     int out_size;                // bytes of an element
 };
+// rows of q16 that a sequence has
+inline int tree_q_rows(int n_q, int n_heads, bool q_tiles) { return q_tiles ? (n_q * n_heads + 127) / 128 * 128 : n_q * n_heads; }
 // Sequences of a pass: 65,536 rows at most (of one sequence 16,384), whose fp16 queries are 64 MB
-inline int tree_pass(int batch, int n_q, int n_heads) { return (int)std::min<int64_t>(batch, (1 << 16) / ((int64_t)n_q * n_heads)); }
+inline int tree_pass(int batch, int q_rows) { return std::min(batch, (1 << 16) / q_rows); }
 // a workspace's bytes for a pass, and its pointers from byte w on (returns the first byte after it)
-size_t tree_nodes_bytes(int batch, int n_q, int n_heads);
-uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int n_heads, uint8_t* w);
+size_t tree_nodes_bytes(int batch, int n_q, int q_rows);
+uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int q_rows, uint8_t* w);
+// byte of 16-byte chunk `chunk` of row `row` of a 128-byte swizzled slab
+__device__ __forceinline__ uint32_t tree_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 cudaError_t launch_tree_prep(const TreeCall& c, cudaStream_t st);
 
 // 16 bytes from global to shared memory, zeros where `there` is false

@@ -10,12 +10,11 @@ namespace csa2 {
 
 // A row of 512 bf16 values, two pieces of 16 bytes a lane, to fp16 after a power-of-two scale where its largest magnitude lies
 // outside [2^-10, 2^15); returns the exponent.
-__device__ __forceinline__ int row_to_f16(const uint4* x, uint4* dst, bool neg) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ int row_to_f16(const uint4* x, uint4* d0, uint4* d1, bool neg) {
     const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[0]), bf16_absmax8(x[1]))));
     const float d = neg ? -pow2f(-e) : pow2f(-e);
-    dst[lane] = bf16x8_to_f16x8(x[0], d);
-    dst[32 + lane] = bf16x8_to_f16x8(x[1], d);
+    *d0 = bf16x8_to_f16x8(x[0], d);
+    *d1 = bf16x8_to_f16x8(x[1], d);
     return e;
 }
 
@@ -47,7 +46,13 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
             for (int i = 0; i < 4; ++i) {
                 if (r + i * warps >= rows) break;
                 const int64_t at = r0 + r + i * warps;
-                const int e = row_to_f16(x[i], reinterpret_cast<uint4*>(a.t.q16 + at * D_LAT), a.neg_q);
+                uint4 *d0 = reinterpret_cast<uint4*>(a.t.q16 + at * D_LAT) + lane, *d1 = d0 + 32;
+                if (a.q_tiles) {                         // slabs lane / 8 and 4 + lane / 8 of the row's tile
+                    const int rr = r + i * warps;
+                    uint8_t* tile = reinterpret_cast<uint8_t*>(a.t.q16) + ((int64_t)b * ((rows + 127) / 128) * 2 + (rr >> 6)) * 65536;
+                    d0 = reinterpret_cast<uint4*>(tile + (lane >> 3) * 8192 + tree_swz(rr & 63, lane & 7)), d1 = d0 + 4 * 8192 / 16;
+                }
+                const int e = row_to_f16(x[i], d0, d1, a.neg_q);
                 if (lane == 0) a.t.q_exps[at] = (int8_t)e;
             }
         }
@@ -118,7 +123,8 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
         for (int i = 0; i < 2; ++i) {
             const int r = group * 16 + warp + 8 * i;
             if (r >= n_rows) break;
-            const int e = row_to_f16(x[i], reinterpret_cast<uint4*>(a.t.rows16 + ((int64_t)b * a.t.row_stride + r) * D_LAT), false);
+            uint4* dst = reinterpret_cast<uint4*>(a.t.rows16 + ((int64_t)b * a.t.row_stride + r) * D_LAT) + lane;
+            const int e = row_to_f16(x[i], dst, dst + 32, false);
             if (lane == 0) a.t.exps[b * 256 + r] = (int8_t)e;
             top = max(top, e);
             off = off || e != 0;
@@ -164,25 +170,25 @@ namespace {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 struct NodeParts {
     size_t seq, vis, mask, exps, top, rows, q, q_exps;
-    NodeParts(int batch, int n_q, int n_heads)
+    NodeParts(int batch, int n_q, int q_rows)
         : seq(up256((size_t)batch * sizeof(TreeSeq))),
           vis(up256((size_t)batch * n_q * sizeof(int))),
           mask(up256((size_t)batch * n_q * 8 * sizeof(uint32_t))),
           exps((size_t)batch * 256),
           top(up256((size_t)batch * TREE_GROUPS * sizeof(int))),
           rows((size_t)batch * (WINDOW - 1 + n_q) * D_LAT * sizeof(uint16_t)),
-          q((size_t)batch * n_q * n_heads * D_LAT * sizeof(uint16_t)),
-          q_exps(up256((size_t)batch * n_q * n_heads)) {}
+          q((size_t)batch * q_rows * D_LAT * sizeof(uint16_t)),
+          q_exps(up256((size_t)batch * q_rows)) {}
 };
 }  // namespace
 
-size_t tree_nodes_bytes(int batch, int n_q, int n_heads) {
-    const NodeParts p(batch, n_q, n_heads);
+size_t tree_nodes_bytes(int batch, int n_q, int q_rows) {
+    const NodeParts p(batch, n_q, q_rows);
     return p.seq + p.vis + p.mask + p.exps + p.top + p.rows + p.q + p.q_exps;
 }
 
-uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int n_heads, uint8_t* w) {
-    const NodeParts p(batch, n_q, n_heads);
+uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int q_rows, uint8_t* w) {
+    const NodeParts p(batch, n_q, q_rows);
     t.seq = reinterpret_cast<TreeSeq*>(w), w += p.seq;
     t.vis = reinterpret_cast<int*>(w), w += p.vis;
     t.mask = reinterpret_cast<uint32_t*>(w), w += p.mask;
