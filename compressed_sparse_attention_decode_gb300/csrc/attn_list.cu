@@ -15,7 +15,7 @@
 //                   when a score rises far above it
 //   O^T += L^T . P  (M = 4 x 128 dims, N = the heads in steps of 16, K = 64 keys; two issuers)
 // Weights are fp16 (2^-11 of each) where the output is of 16 bits, and two fp16 parts (2^-22) where it is fp32: the value MMAs
-// double, both parts take the two P buffers, and P waits for the values of the tile before.
+// double, and the second part, in a P buffer of its own, waits for the values of the tile before.
 // The window rows are fp16 values of a power-of-two scale of their own; O carries the scale of the tile last added, and is
 // brought to the entries' after the window where they differ.
 // Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 rows, 20-23 the queries, fetched for the next item
@@ -41,15 +41,16 @@ constexpr int TL_MMA1 = 8, TL_MMA2 = 10, TL_LOADW = 12, TL_LOADERS = 256, TL_QW 
 constexpr uint32_t TL_SLAB = 64 * 128;               // 64 heads or keys x 64 fp16, 128-byte swizzle
 constexpr uint32_t TL_SQ = 0;
 constexpr uint32_t TL_SL = 8 * TL_SLAB, TL_LBUF = 8 * TL_SLAB;
-constexpr uint32_t TL_SP = TL_SL + 2 * TL_LBUF, TL_PBUF = TL_SLAB;
-constexpr uint32_t TL_SLOTS = TL_SP + 2 * TL_PBUF;   // the share's entries, -1 for none
+constexpr uint32_t TL_SP = TL_SL + 2 * TL_LBUF, TL_PBUF = TL_SLAB;    // P: 2 buffers, and an fp32 output's second parts
+constexpr uint32_t TL_SLOTS = TL_SP + 3 * TL_PBUF;   // the share's entries, -1 for none
 constexpr uint32_t TL_DYN = TL_SLOTS + MAX_K * 4 + 1024;
 constexpr uint32_t TLT_S = 0, TLT_O = 256, TLT_COLS = 512;       // S partial p of buffer b at TLT_S + 64 (2b + p)
 // weights are 2^(score - m), m set TL_UP below the largest score and raised when one is more than TL_TOP above it: the
 // largest weight lies in [2^7, 2^15], and what fp16 rounds to zero is below 2^-32 of it
 constexpr float TL_UP = 7.0f, TL_TOP = 15.0f;
 // Tiles of a run of sums for an fp32 output, as in attn_tree.cu: 48 steps (16 nodes of 16 sequences, 512 entries each, 64 heads: 64 us in
-// one run and 1.3e-6 off, 74 us and 7.6e-7 with runs of six tiles, 81 us with runs of four)
+// one run and 1.3e-6 off, 74 us and 7.6e-7 with runs of six tiles, 81 us with runs of four; 69 us since the weights' second
+// part has a buffer of its own)
 constexpr int TL_RUN = 6;
 constexpr int TL_SMS = 152;
 constexpr int TL_WIN = 2;                            // units of an item's window
@@ -101,7 +102,7 @@ template <typename TO>
 __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_constant__ ListArgs a) {
     constexpr bool FINE = std::is_same<TO, float>::value;           // weights in two parts
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2], b_q;
+    __shared__ __align__(8) unsigned long long b_lhalf[2], b_lfull[2], b_lfree[2], b_sfull[2], b_pfull[2], b_odone[2], b_q, b_plow;
     __shared__ float red[2][TL_H], m_run[TL_H];
     __shared__ __align__(16) float fac[TL_H], held[FINE ? TL_H : 4];     // (held: FINE's factor of what lies in part_o)
     __shared__ int any[4];
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
             umma::mbar_init(sa(&b_odone[i]), 2);
         }
         umma::mbar_init(sa(&b_q), TL_QWARPS);
+        umma::mbar_init(sa(&b_plow), TL_SMW);
         umma::fence_mbar_init();
     }
     if (warp == TL_LOADW - 1) umma::tmem_alloc(sa(&tmem_base), TLT_COLS);
@@ -321,17 +323,28 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     if (!ok) break;
                     umma::fence_after();
                     const uint64_t ld = umma::desc(base + TL_SL + buf * TL_LBUF, TL_SLAB, 1024, umma::LAYOUT_SW128);
-                    const uint64_t pd = umma::desc(base + TL_SP + (FINE ? 0 : buf) * TL_PBUF, 16, 1024, umma::LAYOUT_SW128);
-                    if (umma::elect_one()) {
+                    // part 0 from the tile's own P buffer, FINE's second part from the third
+                    auto part = [&](uint32_t pb, bool first) {
+                        const uint64_t pd = umma::desc(base + TL_SP + pb * TL_PBUF, 16, 1024, umma::LAYOUT_SW128);
 #pragma unroll
                         for (int m2 = 0; m2 < 2; ++m2)
 #pragma unroll
-                            for (int ks = 0; ks < (FINE ? 2 : 1) * TL_TILE / 16; ++ks) {
-                                const int mt = 2 * half + m2, k4 = ks & 3;       // (P's second part lies one buffer on)
-                                umma::mma_f16(tm + TLT_O + 64 * mt, ld + (uint64_t)((2 * mt * TL_SLAB + k4 * 2048) >> 4),
-                                              pd + (uint64_t)(((ks >> 2) * TL_PBUF + k4 * 32) >> 4), id,
-                                              ((FINE ? t % TL_RUN : t) > 0 || ks > 0) ? 1u : 0u);
+                            for (int ks = 0; ks < TL_TILE / 16; ++ks) {
+                                const int mt = 2 * half + m2;
+                                umma::mma_f16(tm + TLT_O + 64 * mt, ld + (uint64_t)((2 * mt * TL_SLAB + ks * 2048) >> 4),
+                                              pd + (uint64_t)((ks * 32) >> 4), id, (!first || ks > 0) ? 1u : 0u);
                             }
+                    };
+                    if (umma::elect_one()) part(buf, (FINE ? t % TL_RUN : t) == 0);
+                    if (FINE) {
+                        __syncwarp();
+                        ok = ok && umma::mbar_wait_fast(sa(&b_plow), tg & 1);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        umma::fence_after();
+                    }
+                    if (umma::elect_one()) {
+                        if (FINE) part(2, false);
                         umma::commit(sa(&b_lfree[buf]));
                         umma::commit(sa(&b_odone[buf]));
                     }
@@ -491,24 +504,26 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     uint32_t p2[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) p2[j] = par ? f16x2_bits(rv[j], x[8 + j]) : f16x2_bits(x[j], rv[j]);
-                    if (FINE && t > 0) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);
-                    uint8_t* P = sm + TL_SP + (FINE ? 0 : buf) * TL_PBUF;
-                    *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                    *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
+                    auto put = [&](uint32_t pb) {
+                        uint8_t* P = sm + TL_SP + pb * TL_PBUF;
+                        *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                        *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
+                        umma::fence_proxy_async();
+                        umma::fence_before();
+                        __syncwarp();
+                    };
+                    put(buf);
+                    if (lane == 0) umma::mbar_arrive(sa(&b_pfull[buf]));
                     if constexpr (FINE) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {        // what the first part leaves
                             const float2 part = __half22float2(*reinterpret_cast<const __half2*>(&p2[j]));
                             p2[j] = par ? f16x2_bits(rv[j] - part.x, x[8 + j] - part.y) : f16x2_bits(x[j] - part.x, rv[j] - part.y);
                         }
-                        P += TL_PBUF;
-                        *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                        *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
+                        if (t > 0) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);
+                        put(2);
+                        if (lane == 0) umma::mbar_arrive(sa(&b_plow));
                     }
-                    umma::fence_proxy_async();
-                    umma::fence_before();
-                    __syncwarp();
-                    if (lane == 0) umma::mbar_arrive(sa(&b_pfull[buf]));
                 }
                 // ---- the share's end: sums, then O^T as [head][dim]
                 if (FINE && T > TL_RUN) add_run(T, true);
