@@ -6,11 +6,14 @@
 namespace csa2 {
 
 // 16 bf16 values as fp32
-__device__ __forceinline__ void row16(const uint16_t* __restrict__ p, float* x) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+__device__ __forceinline__ void bf16x16_to_f32(const uint4& a, const uint4& b, float* x) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int c = 0; c < 16; ++c) x[c] = bf16_bits_to_f32((c & 1) ? (w[c >> 1] >> 16) : (w[c >> 1] & 0xffffu));
+}
+// .. read from memory that the kernel does not write
+__device__ __forceinline__ void row16(const uint16_t* __restrict__ p, float* x) {
+    bf16x16_to_f32(__ldg(reinterpret_cast<const uint4*>(p)), __ldg(reinterpret_cast<const uint4*>(p) + 1), x);
 }
 
 // x <- fmaf(w1, h1, float(w0 * x)), 16 channels: one rounded product, one fused multiply-add

@@ -13,17 +13,9 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "fp4_f16.cuh"
-#include "tree.cuh"
 #include "umma.cuh"
 
 namespace csa2 {
-
-// 16 bf16 channels as floats
-__device__ __forceinline__ void bf16x16_to_f32(const uint4& c, const uint4& d, float* x) {
-    const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = bf16_bits_to_f32((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xffffu));
-}
 
 struct AppendArgs {
     uint8_t *lat_codes, *lat_scales, *ik_codes, *ik_scales;
