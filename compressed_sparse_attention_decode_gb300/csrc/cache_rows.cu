@@ -395,12 +395,13 @@ __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __gri
             float nw = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) nw = fmaxf(nw, norm_w[group * 16 + i]);
+            bool made = true;                                // the entries are (or where they go is not known)
             int n = 0;
             for (int tile = blockIdx.x; tile < all; tile += gridDim.x, ++n) {
                 if ((n & 1) != set) continue;
                 const int buf = n % CM_BUFS;
-                ok = ok && umma::mbar_wait_fast(sa(&b_full[buf]), (n / CM_BUFS) & 1);
-                ok = ok && umma::mbar_wait_fast(sa(&b_sum[set]), (n >> 1) & 1);
+                made = made && umma::mbar_wait_fast(sa(&b_full[buf]), (n / CM_BUFS) & 1);
+                ok = ok && made && umma::mbar_wait_fast(sa(&b_sum[set]), (n >> 1) & 1);
                 umma::fence_after();
                 {
                     const uint32_t at = tmem + ((uint32_t)(qd * 32) << 16) + 128 * set;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __gri
                         }
                     };
                     load();
-                    const int64_t at = entry_at[buf][e];
+                    const int64_t at = made ? entry_at[buf][e] : -1;
                     const float err = CM_ERR * nw * norm_l[buf][e];
                     // the values that `open` names, summed again exactly, one after the other: lane g the term of latent group g
                     auto settle = [&](uint32_t open) {
