@@ -61,14 +61,15 @@ constexpr uint32_t TR_LBUF = 8 * TR_SLAB;
 constexpr uint32_t TR_SP = TR_SL + 2 * TR_LBUF;      // P: 2 buffers x 2 slabs (64 keys each)
 constexpr uint32_t TR_PBUF = 2 * TR_SLAB;
 constexpr uint32_t TR_DYN = TR_SP + 2 * TR_PBUF + 1024;                  // + alignment
-constexpr uint32_t TRT_S = 0, TRT_O = 256, TRT_COLS = 512;               // S of buffer b at TRT_S + 64 b
+constexpr uint32_t TRT_S = 0, TRT_RUN = 128, TRT_O = 256, TRT_COLS = 512;   // S of buffer b at TRT_S + 64 b
 // weights are 2^(score - m), m set TR_UP below the largest score and raised when one is more than TR_TOP above it: the
 // largest weight lies in [2^7, 2^15], within fp16's range, and what fp16 rounds to zero is below 2^-32 of it
 constexpr float TR_UP = 7.0f, TR_TOP = 15.0f;
 // Tiles of a run of sums for an fp32 output: a tensor-core sum loses some 2^-26 of itself at each 16-key step, always to zero's
-// side (200,000 entries: 5.4e-6 of the output, a million 2.6e-5), so that after 48 steps it is added to fp32 sums in global memory,
-// which stay in L2 (6.6e-7 after 32 steps, 1.1e-6 after 64).  That costs 3 us a run and SM: 16 sequences of 32K positions take
-// 564 us in one run, 921 in runs of two tiles, 744 of four.
+// side (200,000 entries: 5.4e-6 of the output, a million 2.6e-5), so that after 48 steps it is added to fp32 sums (6.6e-7 after 32
+// steps, 8.9e-7 after 48, 1.1e-6 after 64), half of them in the columns of TMEM that are free, half in global memory, where they
+// stay in L2.  16 sequences of 32K positions take 564 us in one run and 767 in runs of three tiles; with all sums in global memory
+// 820, 921 in runs of two and 744 of four.
 constexpr int TR_RUN = 3;
 constexpr int TR_PAIRS = 76;                         // pairs of CTAs at most: one CTA per SM
 // Units of an item beside its tiles: its queries and its epilogue, some 12,000 clocks, and a tile 3,800 (ragged-7x21: 55.5 us with one,
@@ -469,8 +470,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 }
                 umma::tmem_wait_st();
             };
-            // FINE: the sums of the runs before this one lie in the share's slot of part_o, in this order of its own, and count
-            // times `held`.  The run that ends with tile t - 1 is added to them; the share's last one: they to it, back in TMEM.
+            // FINE: the sums of the runs before this one, half of a thread's dims in TMEM and half in the share's slot of part_o, in this
+            // order of its own, count times `held`.  The run that ends with tile t - 1 is added to them; the share's last one: they to it, back in TMEM.
             float held = 1.0f;
             const int slot = 2 * pair + (first_share ? 0 : 1);
             float4* runs = reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * TR_ROWS + 64 * (int)rank) * D_LAT) + tid;
@@ -478,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 const uint32_t tp = tb + t - 1;
                 ok = ok && umma::mbar_wait_fast(sa(&b_odone[tp & 1]), (tp >> 1) & 1);
                 umma::fence_after();
-float4 y[2][4] = {};                     // the next 16 columns' under way
+                float4 y[2][4] = {};                 // the next 16 columns' under way
                 const bool more = last || t > TR_RUN;
                 auto load = [&](int g, float4* to) {
 #pragma unroll
@@ -502,15 +503,27 @@ float4 y[2][4] = {};                     // the next 16 columns' under way
                             runs[(4 * g + i) * TR_SMT] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     }
                 };
-                if (more) load(0, y[0]);
+                if (more) load(4, y[0]);
 #pragma unroll 1
-                for (int g = 0; g < 8; g += 2) {
+                for (int g = 0; g < 4; ++g) {
+                    const uint32_t at = lane_base + TRT_O + 128 * ch + 16 * g, sum = lane_base + TRT_RUN + 64 * ch + 16 * g;
+                    float v[16], w[16];
+                    umma::tmem_ld16(at, v);
+                    umma::tmem_ld16(sum, w);
+                    umma::tmem_wait_ld();
+                    if (more)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = fmaf(w[i], held, v[i]);
+                    umma::tmem_st16(last ? at : sum, v);
+                }
+#pragma unroll 1
+                for (int g = 4; g < 8; g += 2) {
                     if (more) load(g + 1, y[1]);
                     add(g, y[0]);
                     if (more && g + 2 < 8) load(g + 2, y[0]);
                     add(g + 1, y[1]);
                 }
-                if (last) umma::tmem_wait_st();
+                umma::tmem_wait_st();
                 held = 1.0f;
             };
             // one tile, of the window or of entries (two copies, so that the entries' carries nothing of the window's)
