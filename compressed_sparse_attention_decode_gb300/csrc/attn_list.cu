@@ -625,10 +625,11 @@ struct ListPlan {
         per = TL_WIN + (k + TL_TILE - 1) / TL_TILE;
         const int items = batch * n_q * hgroups;     // at most 65,536
         blocks = std::min(TL_SMS, items * per);
-        // whole items a block where that is at most 6 units (20,000 clocks) more than an even part: about what the shares'
-        // stores and the join cost
-        const int whole = (items + blocks - 1) / blocks * per;
-        grain = whole <= items * per / blocks + 6 ? per : 1;
+        // Whole items a block where that is at most 6 units (20,000 clocks) more than an even part: about what the shares'
+        // stores and the join cost with all blocks at it.  With fewer units than blocks they cost 2.4 us and 0.03 more a unit, of
+        // which one takes 1.9: 10 items of 4 units 15.6 us whole and 13.2 in parts, 24 of 6 21.6 and 19.0, 38 of 4 18.4 and 19.6.
+        const int units = items * per, whole = (items + blocks - 1) / blocks * per;
+        grain = whole <= units / blocks + 6 && !(units <= TL_SMS && per >= 3 + units / 50) ? per : 1;
         const int grains = items * per / grain;
         blocks = std::min(blocks, grains);
         each = grains / blocks, more = grains % blocks;
