@@ -16,8 +16,8 @@
 //   O^T += L^T . P  (M = 4 x 128 dims, N = the heads in steps of 16, K = 64 keys; two issuers)
 // Weights are fp16 (2^-11 of each) where the output is of 16 bits, and two fp16 parts (2^-22) where it is fp32: the value MMAs
 // double, and the second part, in a P buffer of its own, waits for the values of the tile before.
-// The window rows are fp16 values of a power-of-two scale of their own; O carries the scale of the tile last added, and is
-// brought to the entries' after the window where they differ.
+// Window rows and drafts of another size than most are fp16 values of a power-of-two scale of their own (tree_prep.cu); their weights
+// enter O times that scale, and references are taken from these products.
 // Warps: 0-7 softmax and epilogue, 8-9 score MMAs, 10-11 value MMAs, 12-19 rows, 20-23 the queries, fetched for the next item
 // while this one's last values and outputs are under way (k_tree_prep has them in fp16: converted here they were 10,000
 // clocks late, mostly for their own code).  Nothing waits for a P or S buffer: a tile's keys are expanded
@@ -361,13 +361,11 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     if constexpr (FINE) held[tid] = 1.0f;
                 }
                 umma::bar_named(1, TL_SMT);
-                // never zero, so that a masked score stays -inf
-                const float mul4 = T > 0 ? fmaxf(fabsf(a.scale_log2e) * pow2f(h < nh ? a.t.q_exps[w.gq * a.n_heads + w.h0 + h] : 0), 0x1p-100f) : 0.0f;
-                // the window rows' part of O carries 2^-wexp; a row of another exponent enters with its weight scaled by the difference
-                bool scaled;
-                const int wexp = max(tree_exp(a.t, w.b, a.t.seq[w.b].n_rows, scaled), -100);
+                const int q_exp = T > 0 && h < nh ? a.t.q_exps[w.gq * a.n_heads + w.h0 + h] : 0;
+                // never zero, so that a masked score stays -inf, nor infinite, so that nothing stays nothing
+                const float mul4 = fminf(fmaxf(fabsf(a.scale_log2e) * pow2f(q_exp), 0x1p-100f), 0x1p126f);
+                const bool scaled = tree_scaled(a.t, w.b, a.t.seq[w.b].n_rows);
                 float lsum = 0.0f;
-                int oexp = 0;                        // O is 2^-oexp of what it stands for
                 // FINE: the sums of the runs before this one lie in the share's slot of part_o, in this order of its own
                 float4* runs = reinterpret_cast<float4*>(a.part_o + (int64_t)(2 * blockIdx.x + (k == 0 ? 0 : 1)) * TL_H * D_LAT) + tid;
                 // the run that ends with tile t - 1 is added to them; the share's last one: they to it, back in TMEM
@@ -410,7 +408,6 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     // what does not need the scores comes first: the loaders' words, the reference
                     ok = ok && umma::mbar_wait_fast(sa(&b_lfull[buf]), ph);
                     const bool window = t < nwt;
-                    const int e = window ? wexp : 0;
                     uint32_t see;                    // which of the half's 32 keys are there
                     if (window) {
                         const int left = w.rows - (wa + t) * TL_TILE - 32 * half;
@@ -429,31 +426,38 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
 #pragma unroll
                         for (int i = 0; i < 16; ++i) x[i] += x1[i];
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] *= mul4;
                     // exponent of the row that key par + 2i is, 0 for none
                     auto rexp = [&](int i) {
                         return (see >> (par + 2 * i)) & 1u ? (int)a.t.exps[w.b * 256 + wrow[(wa + t) * TL_TILE + 32 * half + par + 2 * i]] : 0;
                     };
-                    if (window && scaled)
+                    const bool odd = window && scaled;
+                    float mx = -INFINITY;
+                    if (odd) {                       // references are of the weights that O takes: times 2^(the row's exponent)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] *= pow2f(rexp(i));
-                    if (see != 0xffffffffu)
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = rexp(i);
+                            x[i] = (see >> (par + 2 * i)) & 1u ? tree_score(x[i], fabsf(a.scale_log2e), q_exp + e) : -INFINITY;
+                            mx = fmaxf(mx, x[i] + (float)e);
+                        }
+                    } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (!((see >> (par + 2 * i)) & 1u)) x[i] = -INFINITY;
-                    const auto max3 = [](float p, float q, float r) { return fmaxf(p, fmaxf(q, r)); };
-                    float mx = max3(max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), x[6]),
-                                    max3(max3(x[7], x[8], x[9]), max3(x[10], x[11], x[12]), x[13]), fmaxf(x[14], x[15]));
-                    const bool shift = t > 0 && e != oexp;           // (the same for all)
-                    if (umma::bar_red_or(1, TL_SMT, mx - mh > TL_TOP) || shift) {
+                        for (int i = 0; i < 16; ++i) x[i] *= mul4;
+                        if (see != 0xffffffffu)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (!((see >> (par + 2 * i)) & 1u)) x[i] = -INFINITY;
+                        const auto max3 = [](float p, float q, float r) { return fmaxf(p, fmaxf(q, r)); };
+                        mx = max3(max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), x[6]),
+                                  max3(max3(x[7], x[8], x[9]), max3(x[10], x[11], x[12]), x[13]), fmaxf(x[14], x[15]));
+                    }
+                    if (umma::bar_red_or(1, TL_SMT, mx - mh > TL_TOP)) {
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         if (par == 0) red[half][h] = mx;
                         umma::bar_named(1, TL_SMT);
                         if (half == 0) {
                             float f = 1.0f;
                             if (par == 0) {
-                                const float mt = fmaxf(red[0][h], red[1][h]), mo = m_run[h], mn = mt - TL_UP;
+                                const float mt = fmaxf(red[0][h], red[1][h]), mo = m_run[h], mn = floorf(mt) - TL_UP;     // (whole: factors are exact)
                                 if (mt > -INFINITY && (mo == -INFINITY || mt - mo > TL_TOP)) {
                                     f = mo == -INFINITY ? 0.0f : umma::ex2(mo - mn);
                                     m_run[h] = mn;
@@ -467,9 +471,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                         if (t >= 1) ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);   // O settled
                         umma::bar_named(1, TL_SMT);
                         umma::fence_after();
-                        if (t >= 1 && (shift || (any[0] | any[1] | any[2] | any[3]))) {
-                            // the scale's part in two steps: each lies within fp32's range
-                            const float up = shift ? pow2f((oexp - e) / 2) : 1.0f, up2 = shift ? pow2f((oexp - e) - (oexp - e) / 2) : 1.0f;
+                        if (t >= 1 && (any[0] | any[1] | any[2] | any[3])) {
 #pragma unroll 1
                             for (int mt = 2 * half; mt < 2 * half + 2; ++mt)
 #pragma unroll 1
@@ -478,25 +480,30 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                                     umma::tmem_ld16(lane_base + TLT_O + 64 * mt + c, v);
                                     umma::tmem_wait_ld();
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) v[i] = v[i] * fac[c + i] * up * up2;
+                                    for (int i = 0; i < 16; ++i) v[i] *= fac[c + i];
                                     umma::tmem_st16(lane_base + TLT_O + 64 * mt + c, v);
                                 }
                             umma::tmem_wait_st();
                         }
                         lsum *= fac[h];
                     }
-                    oexp = e;
                     const float mr = m_run[h], m = mr == -INFINITY ? 0.0f : mr;      // (a tile may have no key)
                     float sum[2] = {0.0f, 0.0f};
+                    if (odd) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        x[i] = umma::ex2_ftz(x[i] - m);
-                        sum[i & 1] += x[i];
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = rexp(i);
+                            x[i] = umma::ex2_ftz(x[i] + ((float)e - m));
+                            sum[i & 1] = fmaf(x[i], pow2f(-e), sum[i & 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            x[i] = umma::ex2_ftz(x[i] - m);
+                            sum[i & 1] += x[i];
+                        }
                     }
                     lsum += sum[0] + sum[1];
-                    if (window && scaled)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] *= pow2f(max(rexp(i) - wexp, -126));
                     // row h of P^T: trade half of the values with the lane of the other parity for 16 consecutive keys
                     float rv[8];
 #pragma unroll
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     const uint32_t tl = tb + T - 1;
                     ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
                     umma::fence_after();
-                    const float up = ok ? pow2f(oexp) : __int_as_float(0x7fc00000);
+                    const float up = ok ? 1.0f : __int_as_float(0x7fc00000);
                     auto store = [&](auto* dst) {            // row 0's first dim
                         using TD = std::remove_pointer_t<decltype(dst)>;
                         // 16 heads of a dim tile at a time, the next ones' load under way while these are stored

@@ -28,7 +28,8 @@
 //                 goes to place s ^ 2, which gives both CTAs the same address for the same keys, as the MMA asks.
 // Rows, running maxima, sums and outputs of a row stay in its CTA: the pair shares nothing but the MMAs.
 //
-// Roundings: entries are exact in fp16, window rows and queries to 2^-25 of a row's own scale; scores, sums and outputs fp32.
+// Roundings: entries are exact in fp16, window rows and queries to 2^-22 of a row's largest magnitude (tree_prep.cu); scores, sums
+// and outputs fp32.
 // The weights are fp16 (2^-11 of each) where the output is of 16 bits, and two fp16 parts (2^-22) where it is fp32, which
 // doubles the value MMAs; both parts then take the two P buffers, and P waits for the values of the tile before.  An fp32
 // output's sums are also taken out of the tensor cores every few tiles (TR_RUN).
@@ -443,12 +444,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
         while (tr_next(a, cur, h)) {
             const int T = h.t1 - h.t0, wt = h.wt;
             const int n_rows_q = a.n_q * a.n_heads, q0 = h.rt * TR_ROWS + 64 * (int)rank;
-            // the window rows' part of O carries 2^-wexp; a row of another exponent enters with its weight scaled by the difference
-            bool scaled;
-            const int wexp = max(tree_exp(a.t, h.b, a.t.seq[h.b].n_rows, scaled), -100);
+            const bool scaled = tree_scaled(a.t, h.b, a.t.seq[h.b].n_rows);
             const int q_exp = q0 + row < n_rows_q ? a.t.q_exps[(int64_t)h.b * n_rows_q + q0 + row] : 0;
-            // never zero, so that a masked score stays -inf (a score of nearly nothing for a scale of nothing)
-            const float mul4 = fmaxf(fabsf(a.scale_log2e) * pow2f(q_exp), 0x1p-100f);
+            // never zero, so that a masked score stays -inf (a score of nearly nothing for a scale of nothing), nor infinite, so that
+            // nothing stays nothing
+            const float mul4 = fminf(fmaxf(fabsf(a.scale_log2e) * pow2f(q_exp), 0x1p-100f), 0x1p126f);
             int vis = 0;
             const uint32_t* mask = nullptr;
             if (q0 + row < n_rows_q) {
@@ -545,24 +545,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 umma::tmem_ld16(lane_base + TRT_S + 64 * buf + 32 * ch, x);
                 umma::tmem_ld16(lane_base + TRT_S + 64 * buf + 32 * ch + 16, x + 16);
                 umma::tmem_wait_ld();
-                float mul = mul4;
-                const bool odd = window && scaled;   // rows of an exponent of their own (in masked places there may be none)
+                // A row with an exponent e of its own enters O with its weight times 2^e.  The reference is one of these products
+                // then: O stands for itself all the time, the sum takes the weights as they are, and both have their full precision
+                // where rows of any size lie side by side, seen or not.
+                const bool odd = window && scaled;
+                const int8_t* rexp = a.t.exps + h.b * 256 + (window ? tile : 0) * TR_TILE + 64 * kh + 32 * ch;
+                auto exp_of = [&](int i) { return (see >> i) & 1u ? (int)rexp[i] : 0; };     // (in masked places there may be none)
+                const float mul = odd ? 1.0f : mul4;
+                float mx = -INFINITY;
                 if (odd) {
-                    const int8_t* rexp = a.t.exps + h.b * 256 + tile * TR_TILE + 64 * kh + 32 * ch;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = (see >> i) & 1u ? x[i] * mul4 * pow2f(rexp[i]) : 0.0f;
-                    mul = 1.0f;
+                    for (int i = 0; i < 32; ++i) {
+                        const int e = exp_of(i);
+                        x[i] = (see >> i) & 1u ? tree_score(x[i], fabsf(a.scale_log2e), q_exp + e) : -INFINITY;
+                        mx = fmaxf(mx, x[i] + (float)e);
+                    }
+                } else {
+                    if (see != 0xffffffffu)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((see >> i) & 1u)) x[i] = -INFINITY;
+                    float m4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        m4[i] = max3(max3(x[8 * i], x[8 * i + 1], x[8 * i + 2]), max3(x[8 * i + 3], x[8 * i + 4], x[8 * i + 5]),
+                                     fmaxf(x[8 * i + 6], x[8 * i + 7]));
+                    mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * mul;
                 }
-                if (see != 0xffffffffu)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!((see >> i) & 1u)) x[i] = -INFINITY;
-                float m4[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    m4[i] = max3(max3(x[8 * i], x[8 * i + 1], x[8 * i + 2]), max3(x[8 * i + 3], x[8 * i + 4], x[8 * i + 5]),
-                                 fmaxf(x[8 * i + 6], x[8 * i + 7]));
-                const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * mul;
                 const bool raise = umma::bar_red_or(1 + (qd & 1), TR_SMT / 2, mx - m > TR_TOP);
                 // (the P buffer is free: these scores' keys were expanded after the values of the tile before in it; and S is
                 // read before P is handed on, without which its buffer is not written again)
@@ -578,8 +587,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     for (int i = 1; i < 4; ++i) mt = fmaxf(mt, red[32 * i]);
                     float f = 1.0f;
                     if (mt > -INFINITY && (m == -INFINITY || mt - m > TR_TOP)) {
-                        f = m == -INFINITY ? 0.0f : umma::ex2(m - (mt - TR_UP));
-                        m = mt - TR_UP;
+                        const float mn = floorf(mt) - TR_UP;     // (whole, so that exponents and factors of two are exact)
+                        f = m == -INFINITY ? 0.0f : umma::ex2(m - mn);
+                        m = mn;
                     }
                     lsum *= f;
                     if (FINE) held *= f;
@@ -590,15 +600,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     }
                     umma::bar_named(1 + (qd & 1), TR_SMT / 2);        // red is read
                 }
-                const float ref = m == -INFINITY ? 0.0f : -m;
+                float ref = m == -INFINITY ? 0.0f : -m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if (odd) {                           // the sum is of the weights as they are, P of what their rows need
-                    const int8_t* rexp = a.t.exps + h.b * 256 + tile * TR_TILE + 64 * kh + 32 * ch;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        lsum += umma::ex2_ftz(x[i] + ref);
-                        if ((see >> i) & 1u) x[i] += (float)(rexp[i] - wexp);
+                        const int e = exp_of(i);
+                        x[i] += (float)e + ref;
+                        lsum = fmaf(umma::ex2_ftz(x[i]), pow2f(-e), lsum);
                     }
+                    ref = 0.0f;
                 }
                 uint8_t* P = Pbuf + kh * TR_SLAB;
 #pragma unroll
@@ -630,12 +641,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             const int T_win = max(0, min(wt - h.t0, T));
 #pragma unroll 1
             for (int t = 0; t < T_win; ++t) step(std::true_type{}, t);
-            if (T_win > 0 && T_win < T && wexp != 0) {           // the window's part of O to the entries' scale
-                const uint32_t tl = tb + T_win - 1;
-                ok = ok && umma::mbar_wait_fast(sa(&b_odone[tl & 1]), (tl >> 1) & 1);
-                umma::fence_after();
-                scale_o(pow2f(wexp));
-            }
 #pragma unroll 1
             for (int t = T_win; t < T; ++t) step(std::false_type{}, t);
             // ---- the share's end: the row's sum over its four threads, then O
@@ -648,7 +653,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             float l = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) l += red_l[64 * i + row];
-            const float fin = h.t1 <= wt ? pow2f(wexp) : 1.0f;
             const bool whole = T == h.T;
             const int64_t gr = (int64_t)h.b * n_rows_q + q0 + row;
             const bool there = q0 + row < n_rows_q;
@@ -690,9 +694,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
             };
             const int wrow = 32 * (qd & 1);                          // the warp's first row
             if (!whole)
-                store(a.part_o + (pr - lane) * D_LAT + d0, 32, fin);
+                store(a.part_o + (pr - lane) * D_LAT + d0, 32, 1.0f);
             else
-                store(reinterpret_cast<TO*>(a.out) + (gr - lane) * D_LAT + d0, n_rows_q - q0 - wrow, fin * inv);
+                store(reinterpret_cast<TO*>(a.out) + (gr - lane) * D_LAT + d0, n_rows_q - q0 - wrow, inv);
             if (2 * kh + ch == 0) {
                 if (!whole)
                     a.part_ml[pr] = make_float2(m, l);

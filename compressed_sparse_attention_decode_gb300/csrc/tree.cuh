@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "fp4_f16.cuh"
 
 namespace csa2 {
 
@@ -19,21 +20,23 @@ struct TreeNodes {
     TreeSeq* seq;                // [batch]
     int* vis;                    // [batch][n_q] entries that a node sees
     uint32_t* mask;              // [batch][n_q][8] which of the n_rows rows; none for a node that is not there
-    // fp16, row r a 2^-exps[r] of the window row or draft (0 but for rows far off fp16's range), zeros for drafts that are not there
+    // fp16, row r a 2^-exps[r] of the window row or draft (tree_row_exp), zeros for drafts that are not there
     uint16_t* rows16;            // [batch][row_stride][512]
     int8_t* exps;                // [batch][256]
-    int* top;                    // [batch][TREE_GROUPS] the largest exponent of a group of rows, 2^16 more where one is not 0
+    int* off;                    // [batch][TREE_GROUPS] whether a row of the group has another exponent than 0
     int row_stride;
     // the queries as fp16, row r a 2^-q_exps[r] of q's (times -1 where neg_q)
     uint16_t* q16;               // [batch][n_q][n_heads][512], or q_tiles: [batch][64 rows][8 slabs of 64 dims][64][64], swizzled
     int8_t* q_exps;              // [batch][n_q][n_heads]
 };
-// The largest exponent of a sequence's rows, and whether any is not 0 (a whole warp calls it)
-__device__ __forceinline__ int tree_exp(const TreeNodes& t, int b, int n_rows, bool& scaled) {
+// Whether any of a sequence's rows has another exponent than 0 (a whole warp calls it)
+__device__ __forceinline__ bool tree_scaled(const TreeNodes& t, int b, int n_rows) {
     const int lane = threadIdx.x & 31;
-    const int v = lane * 16 < n_rows ? t.top[b * TREE_GROUPS + lane] : -1000;
-    scaled = __any_sync(0xffffffffu, v > 1000);
-    return __reduce_max_sync(0xffffffffu, v > 1000 ? v - 65536 : v);
+    return __any_sync(0xffffffffu, lane * 16 < n_rows && t.off[b * TREE_GROUPS + lane] != 0);
+}
+// |scale| 2^e times a score, -200 <= e <= 252, in steps that leave fp32's range only where the whole does
+__device__ __forceinline__ float tree_score(float x, float scale, int e) {
+    return x * scale * pow2f(e >> 1) * pow2f(e - (e >> 1));
 }
 struct TreeCall {
     int batch, capacity, ratio, n_q, n_heads;

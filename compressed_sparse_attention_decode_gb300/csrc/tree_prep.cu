@@ -8,10 +8,18 @@
 
 namespace csa2 {
 
-// A row of 512 bf16 values, two pieces of 16 bytes a lane, to fp16 after a power-of-two scale where its largest magnitude lies
-// outside [2^-10, 2^15); returns the exponent.
+// The exponent e with which a row goes to fp16 as 2^-e of itself, from the bf16 bits of its largest magnitude: 0 while that lies in
+// [2^-3, 2^5) or is 0, else what brings it into [2^2, 2^3), -100 at least.  So the rows are of one size within 2^8 wherever their
+// exponents are not all the same, what a row loses is 2^-22 of its largest magnitude at most, and a weight times 2^e,
+// which is what the value products take, is small only where the row's part of the output is.
+__device__ __forceinline__ int tree_row_exp(uint32_t mx) {
+    const int e = (int)(mx >> 7) - 127;
+    return mx == 0u || (e >= -3 && e < 5) ? 0 : max(-100, e - 2);
+}
+
+// A row of 512 bf16 values, two pieces of 16 bytes a lane, to fp16; returns its exponent.
 __device__ __forceinline__ int row_to_f16(const uint4* x, uint4* d0, uint4* d1, bool neg) {
-    const int e = f16_range_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[0]), bf16_absmax8(x[1]))));
+    const int e = tree_row_exp(__reduce_max_sync(0xffffffffu, max(bf16_absmax8(x[0]), bf16_absmax8(x[1]))));
     const float d = neg ? -pow2f(-e) : pow2f(-e);
     *d0 = bf16x8_to_f16x8(x[0], d);
     *d1 = bf16x8_to_f16x8(x[1], d);
@@ -22,7 +30,7 @@ __device__ __forceinline__ int row_to_f16(const uint4* x, uint4* d0, uint4* d1, 
 // the sequence's queries.  All but those find the chains for themselves (a thread a node), the first one writes the nodes'
 // part; then a warp has two rows.
 __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeCall a, int fill) {
-    __shared__ int parent[TREE_NODES], last_s, vis_s, tops[8], offs[8];
+    __shared__ int parent[TREE_NODES], last_s, vis_s, offs[8];
     __shared__ long long hi_s;
     __shared__ uint32_t there[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x, group = blockIdx.y, N = a.n_q;
@@ -102,11 +110,9 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
     const int64_t lo = max(max((int64_t)0, hi0 - (WINDOW - 2)), s0), hi = min(hi0, s0 + a.swa_len - 1);
     const int nw = last >= 0 && hi >= lo ? (int)(hi - lo + 1) : 0;       // at most 127
     const int n_rows = last >= 0 ? nw + last + 1 : 0;
-    // ---- rows group * 16 + warp and 8 further: fp16, after a power-of-two scale where their largest magnitude lies outside
-    // [2^-10, 2^15)
+    // ---- rows group * 16 + warp and 8 further as fp16
     if (group * 16 < n_rows) {
         uint4 x[2][2];
-        int top = -1000;
         bool off = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -126,10 +132,9 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
             uint4* dst = reinterpret_cast<uint4*>(a.t.rows16 + ((int64_t)b * a.t.row_stride + r) * D_LAT) + lane;
             const int e = row_to_f16(x[i], dst, dst + 32, false);
             if (lane == 0) a.t.exps[b * 256 + r] = (int8_t)e;
-            top = max(top, e);
             off = off || e != 0;
         }
-        if (lane == 0) tops[warp] = top, offs[warp] = off;
+        if (lane == 0) offs[warp] = off;
     }
     if (group == 0 && tid < N) {
         int vis = 0;
@@ -158,9 +163,9 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
     __syncthreads();
     if (tid == 0) {
         if (group * 16 < n_rows) {
-            int e = -1000, off = 0;
-            for (int i = 0; i < 8; ++i) e = max(e, tops[i]), off |= offs[i];
-            a.t.top[b * TREE_GROUPS + group] = e + (off ? 65536 : 0);
+            int off = 0;
+            for (int i = 0; i < 8; ++i) off |= offs[i];
+            a.t.off[b * TREE_GROUPS + group] = off;
         }
         if (group == 0) a.t.seq[b] = TreeSeq{vis_s, n_rows, row_tiles, 0};
     }
@@ -169,13 +174,13 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
 namespace {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 struct NodeParts {
-    size_t seq, vis, mask, exps, top, rows, q, q_exps;
+    size_t seq, vis, mask, exps, off, rows, q, q_exps;
     NodeParts(int batch, int n_q, int q_rows)
         : seq(up256((size_t)batch * sizeof(TreeSeq))),
           vis(up256((size_t)batch * n_q * sizeof(int))),
           mask(up256((size_t)batch * n_q * 8 * sizeof(uint32_t))),
           exps((size_t)batch * 256),
-          top(up256((size_t)batch * TREE_GROUPS * sizeof(int))),
+          off(up256((size_t)batch * TREE_GROUPS * sizeof(int))),
           rows((size_t)batch * (WINDOW - 1 + n_q) * D_LAT * sizeof(uint16_t)),
           q((size_t)batch * q_rows * D_LAT * sizeof(uint16_t)),
           q_exps(up256((size_t)batch * q_rows)) {}
@@ -184,7 +189,7 @@ struct NodeParts {
 
 size_t tree_nodes_bytes(int batch, int n_q, int q_rows) {
     const NodeParts p(batch, n_q, q_rows);
-    return p.seq + p.vis + p.mask + p.exps + p.top + p.rows + p.q + p.q_exps;
+    return p.seq + p.vis + p.mask + p.exps + p.off + p.rows + p.q + p.q_exps;
 }
 
 uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int q_rows, uint8_t* w) {
@@ -193,7 +198,7 @@ uint8_t* tree_nodes_take(TreeNodes& t, int batch, int n_q, int q_rows, uint8_t* 
     t.vis = reinterpret_cast<int*>(w), w += p.vis;
     t.mask = reinterpret_cast<uint32_t*>(w), w += p.mask;
     t.exps = reinterpret_cast<int8_t*>(w), w += p.exps;
-    t.top = reinterpret_cast<int*>(w), w += p.top;
+    t.off = reinterpret_cast<int*>(w), w += p.off;
     t.rows16 = reinterpret_cast<uint16_t*>(w), w += p.rows;
     t.row_stride = WINDOW - 1 + n_q;
     t.q16 = reinterpret_cast<uint16_t*>(w), w += p.q;

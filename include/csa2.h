@@ -358,7 +358,9 @@ csa2_status csa2_dense_attn(const csa2_cache* cache, const uint16_t* q, int32_t 
  *            2^-22, and no tensor-core sum runs over more than 48 steps: its error does not
  *            grow with the number of keys (measured: 1e-6 of the outputs' norm and less, to a
  *            million entries)
- * q and what some node attends to are finite.
+ * q and what some node attends to are finite, and so are the scores in 32 bits and the outputs
+ * in their type.  A row of q, swa or draft is taken to 2^-22 of its largest magnitude (or
+ * 2^-125 where that is more), whatever rows lie beside it, attended to or not.
  * Nodes that are not there and rows that no node attends to are not taken into account,
  * whatever they hold.  q, draft, swa and out 16-byte aligned, q_pos and swa_pos0 8, parent,
  * idx and lse 4.
