@@ -19,7 +19,7 @@ constexpr int TREE_GROUPS = 16;  // of 16 rows each: at most 255 rows
 struct TreeNodes {
     TreeSeq* seq;                // [batch]
     int* vis;                    // [batch][n_q] entries that a node sees
-    uint32_t* mask;              // [batch][n_q][8] which of the n_rows rows; none for a node that is not there
+    uint32_t* mask;              // [batch][n_q][8] which of the n_rows rows, 128 at most; none for a node that is not there
     // fp16, row r a 2^-exps[r] of the window row or draft (tree_row_exp), zeros for drafts that are not there
     uint16_t* rows16;            // [batch][row_stride][512]
     int8_t* exps;                // [batch][256]

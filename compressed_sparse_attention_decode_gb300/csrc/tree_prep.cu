@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
         if (len > 0) {
             atomicOr(&there[warp], 1u << lane);
             atomicMax(&last_s, tid);
-            // every child of the last committed token stands at the same position: the one after hi
-            if (parent[tid] == -1) hi_s = p - len;
+            // every child of the last committed token stands at the same position: the one after hi (if not, all blocks take the last)
+            if (parent[tid] == -1) atomicMax(&hi_s, (long long)(p - len));
         }
     }
     __syncthreads();
@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(256) k_tree_prep(const __grid_constant__ TreeC
         if (len > 0) {
             vis = (int)min(p >= WINDOW - 1 ? (p - (WINDOW - 1)) >> (a.ratio - 1) : (int64_t)0, (int64_t)a.capacity);
             atomicMax(&vis_s, vis);
-            const int c0 = (int)max((int64_t)0, min((int64_t)nw, p - (WINDOW - 1) - lo));        // committed rows c0 .. nw-1
+            // committed rows c0 .. nw-1; with the chain no more than the window holds, wherever the positions are
+            const int c0 = max((int)max((int64_t)0, min((int64_t)nw, p - (WINDOW - 1) - lo)), nw - (WINDOW - len));
 #pragma unroll
             for (int w = 0; w < 8; ++w) {
                 const int f = max(c0 - 32 * w, 0), e = min(nw - 32 * w, 32);

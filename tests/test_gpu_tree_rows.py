@@ -125,3 +125,26 @@ def test_queries_and_rows_of_opposite_sizes(csa, k):
     """queries of 2^100 against rows of 2^-97, and the other way about: scores near 1 (no entries: theirs are 0)"""
     for size in (-97, 100):
         check(csa, make(100, [-1, 0, -1], 2.0 ** size, 2.0 ** size, k=0 if k else k, seed=3), scale=-1.0)
+
+
+@pytest.mark.parametrize("k", [None, 10])
+def test_positions_that_contradict_the_tree(csa, k):
+    """a chain of 128 whose nodes all claim one position, or positions in reverse, beside a tree that is as it should
+    be: that one's results, and the same bits at every call"""
+    x = make(400, list(range(-1, 127)), 1.0, 1.0, H=8, k=k, seed=9)
+    two = {n: None if v is None else torch.cat((v, v)) for n, v in x.items()}
+    cache = csa.Cache.of(two["codes"], two["scales"], ratio=2)
+
+    def call(pos, parent):
+        return csa.csa2_tree_attn(cache, two["q"], pos, parent, two["draft"], two["swa"], two["swa_pos0"], idx=two["idx"],
+                                  scale=1.0, out_dtype=F, want_lse=True)
+
+    want, wl = call(two["pos"], two["parent"])
+    for pos, parent in ((torch.full_like(x["pos"], 400), x["parent"]), (x["pos"].flip(1), x["parent"]),
+                        (x["pos"].flip(1), torch.full_like(x["parent"], -1)), (x["pos"] * 0 - (1 << 62), x["parent"]),
+                        (x["pos"] * 0 + (1 << 62), x["parent"])):
+        got = [call(torch.cat((pos, x["pos"])), torch.cat((parent, x["parent"]))) for _ in range(3)]
+        for out, lse in got:
+            # (two outputs within 1e-6; the shares of the work are others)
+            assert float((out[1] - want[1]).norm()) <= 2e-6 * float(want[1].norm()) and float((lse[1] - wl[1]).abs().max()) <= 1e-5
+            assert torch.equal(out, got[0][0]) and bool(torch.isfinite(out).all())
