@@ -45,9 +45,11 @@ constexpr uint32_t TL_SP = TL_SL + 2 * TL_LBUF, TL_PBUF = TL_SLAB;    // P: 2 bu
 constexpr uint32_t TL_SLOTS = TL_SP + 3 * TL_PBUF;   // the share's entries, -1 for none
 constexpr uint32_t TL_DYN = TL_SLOTS + MAX_K * 4 + 1024;
 constexpr uint32_t TLT_S = 0, TLT_O = 256, TLT_COLS = 512;       // S partial p of buffer b at TLT_S + 64 (2b + p)
-// weights are 2^(score - m), m set TL_UP below the largest score and raised when one is more than TL_TOP above it: the
-// largest weight lies in [2^7, 2^15], and what fp16 rounds to zero is below 2^-32 of it
-constexpr float TL_UP = 7.0f, TL_TOP = 15.0f;
+// Weights are 2^(score - m), m a whole number TL_UP, or where the output is fp32 TL_UP32, below the largest score's when it was set,
+// and raised when one is more than TL_TOP above it: the largest weight lies in [2^7, 2^16) or [2^10, 2^16), within fp16's range, and
+// fp16's last place (of both parts together, if there are two) is 2^-32 or 2^-35 of it at most.  The higher m is, the more tiles
+// raise it: 16 nodes of 16 sequences, 512 entries each, 64 heads take 69.3 us with 7, 69.6 with 10, 71.1 with 11, 77 with 12.
+constexpr float TL_UP = 7.0f, TL_UP32 = 10.0f, TL_TOP = 15.9f;
 // Tiles of a run of sums for an fp32 output, as in attn_tree.cu: 48 steps (16 nodes of 16 sequences, 512 entries each, 64 heads: 64 us in
 // one run and 1.3e-6 off, 74 us and 7.6e-7 with runs of six tiles, 81 us with runs of four; 69 us since the weights' second
 // part has a buffer of its own)
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                         if (half == 0) {
                             float f = 1.0f;
                             if (par == 0) {
-                                const float mt = fmaxf(red[0][h], red[1][h]), mo = m_run[h], mn = floorf(mt) - TL_UP;     // (whole: factors are exact)
+                                const float mt = fmaxf(red[0][h], red[1][h]), mo = m_run[h], mn = floorf(mt) - (FINE ? TL_UP32 : TL_UP);   // (whole: factors are exact)
                                 if (mt > -INFINITY && (mo == -INFINITY || mt - mo > TL_TOP)) {
                                     f = mo == -INFINITY ? 0.0f : umma::ex2(mo - mn);
                                     m_run[h] = mn;

@@ -63,8 +63,10 @@ constexpr uint32_t TR_SP = TR_SL + 2 * TR_LBUF;      // P: 2 buffers x 2 slabs (
 constexpr uint32_t TR_PBUF = 2 * TR_SLAB;
 constexpr uint32_t TR_DYN = TR_SP + 2 * TR_PBUF + 1024;                  // + alignment
 constexpr uint32_t TRT_S = 0, TRT_RUN = 128, TRT_O = 256, TRT_COLS = 512;   // S of buffer b at TRT_S + 64 b
-// weights are 2^(score - m), m set TR_UP below the largest score and raised when one is more than TR_TOP above it: the
-// largest weight lies in [2^7, 2^15], within fp16's range, and what fp16 rounds to zero is below 2^-32 of it
+// Weights are 2^(score - m), m a whole number TR_UP below the largest score's when it was set, and raised when one is more than
+// TR_TOP above it: the largest weight lies in [2^7, 2^15], within fp16's range, and fp16's last place (of both parts together, if
+// there are two) is 2^-32 of it at most.  Where the output is fp32 a run has an m of its own, so that this counts against the
+// largest weight of 384 keys (against that of all, a million keys 22 nats below one lost their 2e-4 of the output).
 constexpr float TR_UP = 7.0f, TR_TOP = 15.0f;
 // Tiles of a run of sums for an fp32 output: a tensor-core sum loses some 2^-26 of itself at each 16-key step, always to zero's
 // side (200,000 entries: 5.4e-6 of the output, a million 2.6e-5), so that after 48 steps it is added to fp32 sums (6.6e-7 after 32
@@ -470,17 +472,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 }
                 umma::tmem_wait_st();
             };
-            // FINE: the sums of the runs before this one, half of a thread's dims in TMEM and half in the share's slot of part_o, in this
-            // order of its own, count times `held`.  The run that ends with tile t - 1 is added to them; the share's last one: they to it, back in TMEM.
-            float held = 1.0f;
+            // FINE: the sums of the runs before this one: half of a thread's dims in TMEM and half in the share's slot of part_o, in this
+            // order of its own; before them the reference that they were taken against and the sum of the weights in two parts
+            // (thousands of runs may each be less than half of its last place).  The run that ends with tile t - 1 is added to them,
+            // and the next one begins with no reference; the share's last one: they to it, back in TMEM.
             const int slot = 2 * pair + (first_share ? 0 : 1);
             float4* runs = reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * TR_ROWS + 64 * (int)rank) * D_LAT) + tid;
             auto add_run = [&](int t, bool last) {
                 const uint32_t tp = tb + t - 1;
+                const bool more = last || t > TR_RUN;
+                float4 y[2][4] = {};                 // the next 16 columns' under way
+                float4 of = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);    // the sums' reference, the weights' sum, what that rounded off
+                if (more) of = runs[0];
                 ok = ok && umma::mbar_wait_fast(sa(&b_odone[tp & 1]), (tp >> 1) & 1);
                 umma::fence_after();
-                float4 y[2][4] = {};                 // the next 16 columns' under way
-                const bool more = last || t > TR_RUN;
+                const float top = fmaxf(of.x, m);
+                const float held = of.x == -INFINITY ? 0.0f : umma::ex2(of.x - top), run = m == -INFINITY ? 0.0f : umma::ex2(m - top);
+                const float l0 = __fmul_rn(of.y, held), l1 = __fmul_rn(lsum, run), l = __fadd_rn(l0, l1), took = __fsub_rn(l, l0);
+                const float low = fmaf(of.z, held, __fadd_rn(__fsub_rn(l0, __fsub_rn(l, took)), __fsub_rn(l1, took)));
+                if (!last) runs[0] = make_float4(top, l, low, 0.0f);
+                lsum = last ? l + low : 0.0f, m = last ? top : -INFINITY;
                 auto load = [&](int g, float4* to) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) to[i] = runs[(4 * g + i) * TR_SMT];
@@ -492,8 +503,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     umma::tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        v[4 * i] = fmaf(y[i].x, held, v[4 * i]), v[4 * i + 1] = fmaf(y[i].y, held, v[4 * i + 1]);
-                        v[4 * i + 2] = fmaf(y[i].z, held, v[4 * i + 2]), v[4 * i + 3] = fmaf(y[i].w, held, v[4 * i + 3]);
+                        v[4 * i] = fmaf(y[i].x, held, v[4 * i] * run), v[4 * i + 1] = fmaf(y[i].y, held, v[4 * i + 1] * run);
+                        v[4 * i + 2] = fmaf(y[i].z, held, v[4 * i + 2] * run), v[4 * i + 3] = fmaf(y[i].w, held, v[4 * i + 3] * run);
                     }
                     if (last) {
                         umma::tmem_st16(at, v);
@@ -511,9 +522,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     umma::tmem_ld16(at, v);
                     umma::tmem_ld16(sum, w);
                     umma::tmem_wait_ld();
-                    if (more)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = fmaf(w[i], held, v[i]);
+                    for (int i = 0; i < 16; ++i) v[i] = more ? fmaf(w[i], held, v[i] * run) : v[i] * run;
                     umma::tmem_st16(last ? at : sum, v);
                 }
 #pragma unroll 1
@@ -524,7 +534,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     add(g + 1, y[1]);
                 }
                 umma::tmem_wait_st();
-                held = 1.0f;
             };
             // one tile, of the window or of entries (two copies, so that the entries' carries nothing of the window's)
             auto step = [&](auto is_window, int t) {
@@ -538,7 +547,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                     const int left = vis - ((tile - wt) * TR_TILE + 64 * kh + 32 * ch);
                     if (left < 32) see = left <= 0 ? 0u : (1u << left) - 1u;
                 }
-                if (FINE && !window && t > 0 && t % TR_RUN == 0) add_run(t, false);
+                const bool fresh = FINE && !window && t > 0 && t % TR_RUN == 0;      // a run begins: O is of the one before
+                if (fresh) add_run(t, false);
                 float x[32];
                 ok = ok && umma::mbar_wait_fast(sa(&b_sfull[buf]), ph);
                 umma::fence_after();
@@ -592,8 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                         m = mn;
                     }
                     lsum *= f;
-                    if (FINE) held *= f;
-                    if (t >= 1) {
+                    if (t >= 1 && !fresh) {
                         ok = ok && umma::mbar_wait_fast(sa(&b_odone[buf ^ 1]), ((tg - 1) >> 1) & 1);      // O settled
                         umma::fence_after();
                         if (__any_sync(0xffffffffu, f != 1.0f)) scale_o(f);

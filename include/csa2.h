@@ -354,10 +354,12 @@ csa2_status csa2_dense_attn(const csa2_cache* cache, const uint16_t* q, int32_t 
  *            -1 <= k <= 2048
  *   swa, swa_pos0, swa_len, lse, n_heads: as in csa2_dense_attn
  *   out      [batch][n_q][n_heads][d_lat] of out_type; overlaps no input.  The weights of a
- *            bf16 or fp16 out are csa2_dense_attn's (2^-11 of each); those of an fp32 out have
- *            2^-22, and no tensor-core sum runs over more than 48 steps: its error does not
- *            grow with the number of keys (measured: 1e-6 of the outputs' norm and less, to a
- *            million entries)
+ *            bf16 or fp16 out are csa2_dense_attn's (2^-11 of each, or 2^-32 of the row's largest
+ *            where that is more).  Those of an fp32 out have 2^-22, or 2^-32 of the largest
+ *            among 384 keys in a row (with index lists 2^-35 of the row's largest), and no
+ *            tensor-core sum runs over more than 48 steps: its error does not grow with the
+ *            number of keys (at most 3.4e-6 where values have one sign; measured to a million
+ *            entries: 2e-6 of the outputs' norm, 1e-6 with values of both signs)
  * q and what some node attends to are finite, and so are the scores in 32 bits and the outputs
  * in their type.  A row of q, swa or draft is taken to 2^-22 of its largest magnitude (or
  * 2^-125 where that is more), whatever rows lie beside it, attended to or not.
