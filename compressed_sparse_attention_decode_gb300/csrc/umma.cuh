@@ -63,7 +63,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t mbar, uint32_t parity, uint32
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
             : "=r"(done)
-            : "r"(mbar), "r"(parity));
+            : "r"(mbar), "r"(parity)
+            : "memory");
         if (done) return true;
     }
     return false;
