@@ -61,6 +61,13 @@ struct AppendSeq {
         }
         return upto;
     }
+    // the step of entry i's first position; -1: the carried row
+    __device__ __forceinline__ int step(const AppendArgs& a, int i) const { return i * a.ratio - odd; }
+    // where in the cache's planes entry i of the path's goes, -1 where it is not complete within `length` steps or not inside
+    __device__ __forceinline__ int64_t place(const AppendArgs& a, int b, int i, int length) const {
+        const int64_t e = e0 + i;
+        return i < a.n_ent && step(a, i) + a.ratio <= length && e >= 0 && e < a.capacity ? (int64_t)b * a.capacity + e : -1;
+    }
     __device__ __forceinline__ const uint16_t* row(int j) const { return rows + (int64_t)(path ? path[j] : j) * D_LAT; }
     // the entry's 16 channels of this lane's group, quantised; its first row is step j (-1: the carried row)
     __device__ __forceinline__ void entry(const AppendArgs& a, int b, int j, uint32_t& q0, uint32_t& q1, uint32_t& sb) const {
@@ -107,11 +114,11 @@ __global__ void __launch_bounds__(256) k_cache_append(const __grid_constant__ Ap
     pdl_launch_next();
     const AppendSeq s(a, b);
     const int i = DI > 0 ? (int)blockIdx.x : (int)blockIdx.x * 8 + warp;
-    const int j = i * a.ratio - s.odd;                   // the step of the entry's first position; -1: the carried row
+    const int j = s.step(a, i);
     const bool first = blockIdx.x == 0 && warp == 0 && a.prev_out != nullptr;
     const int length = s.length(a, first ? a.n_path : min(a.n_path, j + a.ratio));
-    const int64_t e = s.e0 + i;
-    const bool there = i < a.n_ent && j + a.ratio <= length && e >= 0 && e < a.capacity;
+    const int64_t entry = s.place(a, b, i, length);
+    const bool there = entry >= 0;
     uint2 wc[16];
     uint32_t wsc[16], q0 = 0u, q1 = 0u, sb = 0u;
     if constexpr (DI > 0) {
@@ -128,7 +135,6 @@ __global__ void __launch_bounds__(256) k_cache_append(const __grid_constant__ Ap
     __syncwarp();
     if (first) carry_on(a, s, b, length);
     if (!there) return;
-    const int64_t entry = (int64_t)b * a.capacity + e;
     if (DI == 0 || warp == 0) store_latent(a, entry, q0, q1, sb);
     if constexpr (DI > 0) {
         const uint32_t L[4] = {unpack4_int8(q0 & 0xffffu), unpack4_int8(q0 >> 16), unpack4_int8(q1 & 0xffffu), unpack4_int8(q1 >> 16)};
@@ -187,6 +193,13 @@ constexpr uint32_t CM_W = 128 * 1024, CM_A = CM_TILE * 1024, CM_TURN = CM_TILE *
 constexpr uint32_t CM_DYN = CM_W + CM_BUFS * CM_A + 8 * CM_TURN + 4096 + 1024;                 // + w0 and w1, alignment
 constexpr float CM_ERR = 0x1.4p-18f;
 
+// where entry e (0 .. 15, of each lane) of a tile goes, found out anew; a whole warp together
+__device__ __noinline__ int64_t cm_place(const AppendArgs& a, int tile, int tiles, int e) {
+    const int b = tile / tiles, i = (tile - b * tiles) * CM_TILE + e;
+    const AppendSeq s(a, b);
+    return s.place(a, b, i, s.length(a, a.n_path));
+}
+
 // sixteen fp16 values of a row of a 128-byte swizzled slab (rows of 64)
 __device__ __forceinline__ void cm_row16(const uint8_t* slab, int row, int g, uint4* v) {
     const uint8_t* at = slab + row * 128;
@@ -240,15 +253,14 @@ __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __gri
             const int b = fb, i = ft * CM_TILE + warp;
             for (ft += gridDim.x; ft >= tiles && fb < batch; ft -= tiles) ++fb;
             const AppendSeq s(a, b);
-            const int j = i * a.ratio - s.odd;
+            const int j = s.step(a, i);
             // (of a path that it goes along the warp looks at each step once)
             const int upto = i == 0 && a.prev_out != nullptr ? a.n_path : min(a.n_path, j + a.ratio);
             if (b != seen_b) seen_b = b, seen = 0, ends = false;
             if (!ends && seen < upto) seen = s.length(a, upto, seen), ends = seen < upto;
             p.length = min(seen, upto);
-            const int64_t e = s.e0 + i;
-            if (i < a.n_ent && j + a.ratio <= p.length && e >= 0 && e < a.capacity) {
-                p.entry = (int64_t)b * a.capacity + e;
+            p.entry = s.place(a, b, i, p.length);
+            if (p.entry >= 0) {
                 p.x = reinterpret_cast<const uint4*>(j < 0 ? a.prev + (int64_t)b * D_LAT : s.row(j));
                 p.y = a.ratio == 2 ? reinterpret_cast<const uint4*>(s.row(j + 1)) : p.x;
                 if (lane < 16) umma::prefetch_l2((lane & 8 ? p.y : p.x) + 8 * (lane & 7));      // (lines of 128 bytes)
@@ -395,12 +407,12 @@ __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __gri
             float nw = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) nw = fmaxf(nw, norm_w[group * 16 + i]);
-            bool made = true;                                // the entries are (or where they go is not known)
+            bool made = true;                                // the entries are (if a wait for them ran out, where they go is found out here)
             int n = 0;
             for (int tile = blockIdx.x; tile < all; tile += gridDim.x, ++n) {
                 if ((n & 1) != set) continue;
                 const int buf = n % CM_BUFS;
-                made = made && umma::mbar_wait_fast(sa(&b_full[buf]), (n / CM_BUFS) & 1);
+                made = __all_sync(0xffffffffu, made && umma::mbar_wait_fast(sa(&b_full[buf]), (n / CM_BUFS) & 1));
                 ok = ok && made && umma::mbar_wait_fast(sa(&b_sum[set]), (n >> 1) & 1);
                 umma::fence_after();
                 {
@@ -434,7 +446,7 @@ __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __gri
                         }
                     };
                     load();
-                    const int64_t at = made ? entry_at[buf][e] : -1;
+                    const int64_t at = made ? entry_at[buf][e] : cm_place(a, tile, tiles, e);
                     const float err = CM_ERR * nw * norm_l[buf][e];
                     // the values that `open` names, summed again exactly, one after the other: lane g the term of latent group g
                     auto settle = [&](uint32_t open) {
