@@ -150,17 +150,19 @@ class TreeLayer(_Graphed):
         csa2_linear_fp4(self.o.view(T, self.groups, -1), codes, scales, alpha, out=self.y.view(T, self.groups, -1),
                         ws=self.ws_o, stream=stream)
 
-    def commit(self, path, h=None, prev=None, w0=None, w1=None, wik_codes=None, wik_scales=None):
+    def commit(self, path, h=None, prev=None, w0=None, w1=None, wik_codes=None, wik_scales=None, stream=None):
         """the accepted path int32 [B, m] (node numbers from the root's child on, ended by its first that is no
         node): its draft rows move into the window, and the committed positions on.  With h bf16 [B, n, 512], the
         nodes' rows that the cache is made of, they are appended to it too (prev, w0, w1 and the projection as in
-        csa2_cache_append; prev is carried on in place): once for the layers that share a cache."""
-        if h is not None:
-            csa2_cache_append(self.cache, h, self.committed, path=path, prev=prev, prev_out=prev, w0=w0, w1=w1,
-                              wik_codes=wik_codes, wik_scales=wik_scales)
-        length = ((path >= 0) & (path < self.n)).long().cumprod(1).sum(1)
-        at = path.long().clamp(0, self.n - 1)[..., None].expand(-1, -1, D_LAT)
-        rows = torch.cat((self.win, self.draft.gather(1, at)), 1)
-        keep = torch.arange(128, device=path.device) + length[:, None]
-        self.win.copy_(rows.gather(1, keep[..., None].expand(-1, -1, D_LAT)))
-        self.committed += length
+        csa2_cache_append; prev is carried on in place): once for the layers that share a cache.  It reads what
+        enqueue() wrote and changes what the next one reads: on the same stream, or behind it."""
+        with torch.cuda.stream(stream):          # (None: the current one)
+            if h is not None:
+                csa2_cache_append(self.cache, h, self.committed, path=path, prev=prev, prev_out=prev, w0=w0, w1=w1,
+                                  wik_codes=wik_codes, wik_scales=wik_scales, stream=stream)
+            length = ((path >= 0) & (path < self.n)).long().cumprod(1).sum(1)
+            at = path.long().clamp(0, self.n - 1)[..., None].expand(-1, -1, D_LAT)
+            rows = torch.cat((self.win, self.draft.gather(1, at)), 1)
+            keep = torch.arange(128, device=path.device) + length[:, None]
+            self.win.copy_(rows.gather(1, keep[..., None].expand(-1, -1, D_LAT)))
+            self.committed += length
