@@ -322,14 +322,18 @@ __global__ void __launch_bounds__(CM_THREADS, 1) k_cache_append_many(const __gri
             float norm = (__low2float(sq) + __high2float(sq)) * s * s;
 #pragma unroll
             for (int k = 16; k; k >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, k);
+            // (a buffer that is not known to be free is left alone: the keys' warps then wait for it in vain, and say so)
             if (n >= CM_BUFS) ok = ok && umma::mbar_wait_fast(sa(&b_free[buf]), ((n / CM_BUFS) - 1) & 1);
             uint8_t* row = A + buf * CM_A + (lane >> 2) * (CM_TILE * 128) + warp * 128;
-            *reinterpret_cast<uint4*>(row + (((2 * (lane & 3)) ^ (warp & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(row + (((2 * (lane & 3) + 1) ^ (warp & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-            if (lane == 0) entry_at[buf][warp] = at, norm_l[buf][warp] = sqrtf(norm);
+            if (ok) {
+                *reinterpret_cast<uint4*>(row + (((2 * (lane & 3)) ^ (warp & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(row + (((2 * (lane & 3) + 1) ^ (warp & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                if (lane == 0) entry_at[buf][warp] = at, norm_l[buf][warp] = sqrtf(norm);
+            }
             umma::fence_proxy_async();
+            const bool all = __all_sync(0xffffffffu, ok);
             __syncwarp();
-            if (lane == 0) umma::mbar_arrive(sa(&b_full[buf]));
+            if (all && lane == 0) umma::mbar_arrive(sa(&b_full[buf]));
         }
     } else {
         // ================= W: a warp makes a row, lane g its dims 16 g .. + 15

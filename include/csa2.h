@@ -450,7 +450,8 @@ csa2_status csa2_reindex_noalloc(const csa2_cache* cache, const uint8_t* iq_code
  * the failure in the first 32-bit word of the workspace it was given and
  * returns with its outputs unspecified (the attention writes NaN), so the
  * context stays usable.  No call reports this itself, since calls are
- * asynchronous.
+ * asynchronous.  csa2_cache_append, which takes no workspace, gives the indexer
+ * keys concerned NaN scales (0x7F).
  *
  * csa2_poll_error reads that word of `workspace` (a workspace given to any
  * operation, at least 16 bytes), clears it, and returns CSA2_ERR_TIMEOUT if it
