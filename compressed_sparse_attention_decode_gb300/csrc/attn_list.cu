@@ -58,8 +58,6 @@ constexpr int TL_SMS = 152;
 constexpr int TL_WIN = 2;                            // units of an item's window
 static_assert(WINDOW <= TL_WIN * TL_TILE, "the window's rows have a unit per tile");
 
-__device__ __forceinline__ uint32_t tl_swz(uint32_t row, uint32_t chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
-
 struct ListArgs {
     const uint8_t *codes, *scales;
     int capacity;
@@ -200,7 +198,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     for (int i = 0; i < TL_TILE * 64 / TL_LOADERS; ++i) {
                         const int r = (lt >> 6) + 4 * i, c = lt & 63;
                         const bool there = v0 + r < w.rows;
-                        copy16(sa(L + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)), rows16 + (there ? (int)wrow[v0 + r] : 0) * D_LAT + 8 * c, there);
+                        copy16(sa(L + (c >> 3) * TL_SLAB + tree_swz(r, c & 7)), rows16 + (there ? (int)wrow[v0 + r] : 0) * D_LAT + 8 * c, there);
                     }
                     copy16_wait();
                     umma::fence_proxy_async();
@@ -254,7 +252,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int cc = c * 4 + j;
-                            *reinterpret_cast<uint4*>(L + (cc >> 3) * TL_SLAB + tl_swz(r, cc & 7)) =
+                            *reinterpret_cast<uint4*>(L + (cc >> 3) * TL_SLAB + tree_swz(r, cc & 7)) =
                                 e2m1x8_scaled(words[j], (j >> 1) ? s_hi : s_lo);
                         }
                     }
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
 #pragma unroll 4
                 for (int i = tid - TL_QW * 32; i < TL_H * 64; i += TL_QWARPS * 32) {
                     const int r = i >> 6, c = i & 63;
-                    copy16(sa(sm + TL_SQ + (c >> 3) * TL_SLAB + tl_swz(r, c & 7)), src + (r < nh ? r : 0) * D_LAT + 8 * c, r < nh);
+                    copy16(sa(sm + TL_SQ + (c >> 3) * TL_SLAB + tree_swz(r, c & 7)), src + (r < nh ? r : 0) * D_LAT + 8 * c, r < nh);
                 }
                 copy16_wait();
                 umma::fence_proxy_async();
@@ -515,8 +513,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                     for (int j = 0; j < 8; ++j) p2[j] = par ? f16x2_bits(rv[j], x[8 + j]) : f16x2_bits(x[j], rv[j]);
                     auto put = [&](uint32_t pb) {
                         uint8_t* P = sm + TL_SP + pb * TL_PBUF;
-                        *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                        *reinterpret_cast<uint4*>(P + tl_swz(h, 4 * half + 2 * par + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
+                        *reinterpret_cast<uint4*>(P + tree_swz(h, 4 * half + 2 * par)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                        *reinterpret_cast<uint4*>(P + tree_swz(h, 4 * half + 2 * par + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
                         umma::fence_proxy_async();
                         umma::fence_before();
                         __syncwarp();

@@ -38,15 +38,6 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(const uint4& v, float d) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// eight bf16 values as fp16
-__device__ __forceinline__ uint4 bf16x8_to_f16x8(const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = f16x2_bits(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // two E4M3 bytes (low byte -> low half) to fp16, exactly
 __device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t two) {
     uint32_t r;
