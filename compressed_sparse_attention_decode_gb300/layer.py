@@ -102,8 +102,10 @@ class TreeLayer(_Graphed):
     latent rows), parent [B, n] (an earlier node, -1: a child of the last committed token, -2: not there) and pos
     [B, n] (raw positions), keeps the committed rows in win [B, 128, 512] (the last is of position
     committed[b] - 1, oldest first), and runs enqueue() (or capture() once and run()).  With idx int32 [B, n, k]
-    a node reads the entries of its list, else every visible one.  The result is y [B, n, groups, r_out]; rows of
-    nodes that are not there hold nothing of use.  commit() then takes an accepted path over."""
+    a node reads the entries of its list, else every visible one.  The attention's outputs are held in bf16 with
+    and without lists, with weights of 2^-11 (DecodeLayer's in fp32 with idx: one rounding of 2^-8 less before Wo; for a
+    tree of 16 nodes over 512 entries fp32 would take 70 us where bf16 takes 56).  The result is y [B, n, groups, r_out];
+    rows of nodes that are not there hold nothing of use.  commit() then takes an accepted path over."""
 
     def __init__(self, cache, wq, wo, q_weight, k_weight, nodes, rot=64, base=10000.0, eps=1e-6, idx=None,
                  out_dtype=torch.bfloat16):
