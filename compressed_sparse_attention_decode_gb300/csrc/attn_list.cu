@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
                         if (half == 0) {
                             float f = 1.0f;
                             if (par == 0) {
-                                const float mt = fmaxf(red[0][h], red[1][h]), mo = m_run[h], mn = floorf(mt) - (FINE ? TL_UP32 : TL_UP);   // (whole: factors are exact)
+                                const float mt = fmaxf(red[0][h], red[1][h]), mo = m_run[h], mu = floorf(mt) - (FINE ? TL_UP32 : TL_UP);
+                                const float mn = mt - mu > TL_TOP ? floorf(mt) : mu;     // (whole: factors are exact; beyond 2^27 not every number is there)
                                 if (mt > -INFINITY && (mo == -INFINITY || mt - mo > TL_TOP)) {
                                     f = mo == -INFINITY ? 0.0f : umma::ex2(mo - mn);
                                     m_run[h] = mn;
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) k_tree_lists(const __grid_const
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const int e = rexp(i);
-                            x[i] = umma::ex2_ftz(x[i] + ((float)e - m));
+                            x[i] = umma::ex2_ftz(fminf(x[i] + ((float)e - m), TL_TOP));    // (above it by a rounding at most)
                             sum[i & 1] = fmaf(x[i], pow2f(-e), sum[i & 1]);
                         }
                     } else {

@@ -561,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 const bool odd = window && scaled;
                 const int8_t* rexp = a.t.exps + h.b * 256 + (window ? tile : 0) * TR_TILE + 64 * kh + 32 * ch;
                 auto exp_of = [&](int i) { return (see >> i) & 1u ? (int)rexp[i] : 0; };     // (in masked places there may be none)
-                const float mul = odd ? 1.0f : mul4;
+                float mul = odd ? 1.0f : mul4;
                 float mx = -INFINITY;
                 if (odd) {
 #pragma unroll
@@ -611,11 +611,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TR_THREADS, 1) k_tre
                 }
                 float ref = m == -INFINITY ? 0.0f : -m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (!odd && fabsf(ref) >= 0x1p23f) { // scores rounded as their largest was: half of its last place may be more than 2^15
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] *= mul4;
+                    mul = 1.0f;
+                }
                 if (odd) {                           // the sum is of the weights as they are, P of what their rows need
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const int e = exp_of(i);
-                        x[i] += (float)e + ref;
+                        x[i] = fminf(x[i] + ((float)e + ref), TR_TOP);      // (above it by a rounding at most)
                         lsum = fmaf(umma::ex2_ftz(x[i]), pow2f(-e), lsum);
                     }
                     ref = 0.0f;

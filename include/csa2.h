@@ -361,7 +361,8 @@ csa2_status csa2_dense_attn(const csa2_cache* cache, const uint16_t* q, int32_t 
  *            number of keys (at most 3.4e-6 where values have one sign; measured to a million
  *            entries: 2e-6 of the outputs' norm, 1e-6 with values of both signs)
  * q and what some node attends to are finite, and so are the scores in 32 bits and the outputs
- * in their type.  A row of q, swa or draft is taken to 2^-22 of its largest magnitude (or
+ * in their type; where scores reach 2^22, rows of different magnitude whose scores are the same
+ * may be weighed against each other by a power of two too much.  A row of q, swa or draft is taken to 2^-22 of its largest magnitude (or
  * 2^-125 where that is more), whatever rows lie beside it, attended to or not.
  * Nodes that are not there and rows that no node attends to are not taken into account,
  * whatever they hold.  q, draft, swa and out 16-byte aligned, q_pos and swa_pos0 8, parent,

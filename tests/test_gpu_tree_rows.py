@@ -148,3 +148,13 @@ def test_positions_that_contradict_the_tree(csa, k):
             # (two outputs within 1e-6; the shares of the work are others)
             assert float((out[1] - want[1]).norm()) <= 2e-6 * float(want[1].norm()) and float((lse[1] - wl[1]).abs().max()) <= 1e-5
             assert torch.equal(out, got[0][0]) and bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("k", [None, 0, 40])
+@pytest.mark.parametrize("size,score", [(s, n) for s in (0, 13, -13) for n in range(15, 33 if s == 0 else 22)])
+def test_scores_beyond_the_last_place_of_their_exponents(csa, score, size, k):
+    """scores of 2^score: neighbours in fp32 lie up to 2^9 apart, so that a reference below the largest may be none or far;
+    keys that tie have all the weight (rows of an exponent of their own have their bits below 2^22, as the header says)"""
+    x = make(400, [-1, 0, -1], 2.0 ** size, 2.0 ** size, H=128, k=k, seed=score)
+    x["q"] *= 2.0 ** score
+    check(csa, x)
