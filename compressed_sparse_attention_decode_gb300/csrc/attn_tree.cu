@@ -71,7 +71,7 @@ constexpr float TR_UP = 7.0f, TR_TOP = 15.0f;
 // Tiles of a run of sums for an fp32 output: a tensor-core sum loses some 2^-26 of itself at each 16-key step, always to zero's
 // side (200,000 entries: 5.4e-6 of the output, a million 2.6e-5), so that after 48 steps it is added to fp32 sums (6.6e-7 after 32
 // steps, 8.9e-7 after 48, 1.1e-6 after 64), half of them in the columns of TMEM that are free, half in global memory, where they
-// stay in L2.  16 sequences of 32K positions take 564 us in one run and 775 in runs of three tiles (764 with one reference for all of them);
+// stay in L2.  16 sequences of 32K positions take 564 us in one run and 762 in runs of three tiles;
 // with all sums in global memory 820, 921 in runs of two and 744 of four.
 constexpr int TR_RUN = 3;
 constexpr int TR_PAIRS = 76;                         // pairs of CTAs at most: one CTA per SM
